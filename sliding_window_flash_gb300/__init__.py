@@ -10,6 +10,9 @@ There is no fallback: if libswa.so is missing or the device is not sm_103, the c
     dq, dk, dv = swa_attn_bwd(q, k, v, o, do, lse, window, scale)
     out = SlidingWindowAttention.apply(q, k, v, window, scale)   # autograd wrapper
 
+Serving (cache.py): SwaCache, swa_cache_append, swa_cache_attn, swa_cache_evict and
+swa_attn_key_weights, a paged 8-bit key/value cache with attention over it.
+
 Layout: q, o, do, dq [B, Hq, Lq, D]; k, v, dk, dv [B, Hkv, Lk, D], all contiguous and of one
 dtype (bf16, fp16, or fp32 with bf16 tensor-core operands); lse [B, Hq, Lq] fp32.
 D in {64, 128, 256}; Hq % Hkv == 0; Lq <= Lk (the queries are the last Lq key positions).
@@ -36,7 +39,17 @@ __all__ = [
     "swa_check_device",
     "SlidingWindowAttention",
     "STATUS",
+    "SwaCache",
+    "swa_cache_append",
+    "swa_cache_attn",
+    "swa_cache_attn_workspace_bytes",
+    "swa_cache_evict",
+    "swa_attn_key_weights",
 ]
+
+from . import cache as _cache
+from .cache import (SwaCache, swa_attn_key_weights, swa_cache_append, swa_cache_attn,
+                    swa_cache_attn_workspace_bytes, swa_cache_evict)
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libswa.so"
@@ -51,9 +64,10 @@ STATUS = {
     5: "SWA_ERR_DEVICE_TIMEOUT",
     6: "SWA_ERR_WORKSPACE",
     7: "SWA_ERR_DEVICE_LAYOUT",
+    8: "SWA_ERR_DEVICE_INDEX",
 }
 
-# Every symbol include/swa_attn.h declares, with its ctypes signature.
+# Every symbol include/swa_attn.h and include/swa_cache.h declare, with its ctypes signature.
 _c_int, _c_float, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
 SIGNATURES = {
     "swa_attn_fwd": (_c_int, [_vp] * 5 + [_c_int] * 6 + [_c_float, _vp]),
@@ -99,6 +113,7 @@ SIGNATURES = {
     "swa_check_device": (_c_int, [_vp]),
     "swa_selftest_wait_timeout": (_c_int, [_vp]),
     "swa_version": (_c_int, []),
+    **_cache.SIGNATURES,  # include/swa_cache.h
 }
 
 
@@ -445,7 +460,8 @@ def swa_attn_fwd_bwd_host(q, k, v, do, window: int, scale: Optional[float] = Non
 
 
 def swa_check_device(device=None) -> None:
-    """Synchronize the current stream and raise if a kernel's bounded wait ran out."""
+    """Synchronize the current stream and raise if a kernel's bounded wait ran out, or if a cache
+    call met a page number or length out of range."""
     import torch
 
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device

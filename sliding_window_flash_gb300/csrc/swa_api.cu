@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "swa_attn.h"
+#include "swa_cache_kernels.h"
 #include "swa_kernels.h"
 
 namespace {
@@ -49,6 +50,14 @@ swa_status current_device(unsigned** err) {
   *err = st.err;
   return SWA_OK;
 }
+
+}  // namespace
+
+namespace swa {
+swa_status device_error_word(unsigned** err) { return current_device(err); }
+}  // namespace swa
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -356,6 +365,8 @@ const char* swa_strerror(swa_status status) {
     case SWA_ERR_WORKSPACE: return "SWA_ERR_WORKSPACE: workspace null or too small";
     case SWA_ERR_DEVICE_LAYOUT:
       return "SWA_ERR_DEVICE_LAYOUT: a kernel's shared memory was not 1024-byte aligned";
+    case SWA_ERR_DEVICE_INDEX:
+      return "SWA_ERR_DEVICE_INDEX: a page number or length on the device out of range, skipped";
   }
   return "SWA_ERR_UNKNOWN";
 }
@@ -372,7 +383,8 @@ swa_status swa_check_device(cudaStream_t stream) {
     const unsigned zero = 0;
     if (cudaMemcpyToSymbol(g_swa_error_word, &zero, sizeof(zero)) != cudaSuccess)
       return SWA_ERR_CUDA;
-    return (word & swa::kErrSmemLayout) ? SWA_ERR_DEVICE_LAYOUT : SWA_ERR_DEVICE_TIMEOUT;
+    if (word & swa::kErrSmemLayout) return SWA_ERR_DEVICE_LAYOUT;
+    return (word & swa::kErrWaitTimeout) ? SWA_ERR_DEVICE_TIMEOUT : SWA_ERR_DEVICE_INDEX;
   }
   return SWA_OK;
 }
@@ -384,7 +396,7 @@ swa_status swa_selftest_wait_timeout(cudaStream_t stream) {
   return swa::launch_wait_timeout_selftest(err, stream) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
-int swa_version(void) { return 100; }
+int swa_version(void) { return 101; }
 
 }  // extern "C"
 

@@ -13,6 +13,8 @@ namespace swa {
 constexpr unsigned kErrWaitTimeout = 1u;  // an mbarrier wait ran out
 constexpr unsigned kErrSmemLayout = 2u;   // dynamic shared memory not 1024-byte aligned; the
                                           // kernel returned before any barrier or memory use
+constexpr unsigned kErrIndex = 4u;        // a page number or length read on the device is out of
+                                          // range; what it names was skipped
 
 constexpr int kBlockM = 128;  // query rows per tile
 constexpr int kBlockN = 128;  // key rows per tile

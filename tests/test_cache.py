@@ -1,0 +1,498 @@
+"""The paged 8-bit cache on the GPU against plain 64-bit forms (cache_ref.py): append, attention,
+eviction, key weights, and a run of them together."""
+import math
+
+import pytest
+import torch
+
+import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _cache(swa, g, pages, H, D, page, spread=0, weight=True):
+    """A pool full of codes; block scales differ by up to 2^spread."""
+    def codes():
+        x = torch.randn((pages, H, page, D), generator=g, device="cuda") * 90
+        return x.clamp(-448, 448).to(torch.float8_e4m3fn)
+
+    def scales():
+        e = torch.randint(-8, -7 + spread, (pages, H), generator=g, device="cuda")
+        return torch.exp2(e.float())
+
+    w = torch.exp(torch.randn((pages, H, page), generator=g, device="cuda")) if weight else None
+    return swa.SwaCache(codes(), codes(), scales(), scales(), w)
+
+
+def _table(g, B, width, first=0):
+    order = torch.randperm(B * width, generator=g, device="cuda") + first
+    return order.to(torch.int32).view(B, width).contiguous()
+
+
+def _ints(v):
+    return None if v is None else torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _same_pool(cache, want):
+    got = ref.pool_of(cache)
+    for name, x in want.items():
+        if x is not None:
+            assert torch.equal(torch.nan_to_num(got[name], nan=1e9),
+                               torch.nan_to_num(x, nan=1e9)), name
+
+
+def _near(got, want, tol, what):
+    got = got.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+    fine = torch.isfinite(want)
+    assert torch.equal(got[~fine & ~torch.isnan(want)], want[~fine & ~torch.isnan(want)]), what
+    off = (got - want)[fine].abs()
+    assert (off <= tol[fine]).all(), (what, float((off - tol[fine]).max()),
+                                     float((off / tol[fine].clamp(min=1e-300)).max()))
+
+
+# ---- append ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,H,D,page,T,lens,new,dtype,given", [
+    (1, 1, 64, 32, 1, [0], None, torch.bfloat16, False),
+    (3, 2, 128, 64, 1, [0, 63, 64], None, torch.bfloat16, False),
+    (4, 2, 128, 64, 1, [1, 62, 127, 5], None, torch.float16, True),
+    (2, 3, 128, 64, 200, [0, 37], None, torch.bfloat16, True),
+    (3, 1, 256, 32, 45, [31, 0, 33], [45, 0, 17], torch.float16, False),
+    (2, 2, 64, 128, 129, [127, 1], [129, 1], torch.float32, True),
+    (1, 2, 256, 128, 300, [5], None, torch.float32, False),
+    (2, 1, 128, 32, 33, [0, 31], [33, 32], torch.bfloat16, True),
+])
+def test_append(swa, B, H, D, page, T, lens, new, dtype, given):
+    g = _gen(B * 1000 + T)
+    width = -(-(max(lens) + T) // page)
+    cache = _cache(swa, g, B * width + 2, H, D, page, spread=3)
+    table = _table(g, B, width, first=1)
+    pool = ref.pool_of(cache)
+    # token magnitudes from 2^-6 to 2^6 raise some scales and leave others
+    mag = torch.exp2(torch.randint(-6, 7, (B, H, T, 1), generator=g, device="cuda").float())
+    k = (torch.randn((B, H, T, D), generator=g, device="cuda") * mag).to(dtype)
+    v = (torch.randn((B, H, T, D), generator=g, device="cuda") * mag.flip(2)).to(dtype)
+    w = torch.rand((B, H, T), generator=g, device="cuda") if given else None
+    ref.append(pool, table, lens, k, v, new, w)
+    for _ in range(2):  # again: the same slots, the same codes
+        swa.swa_cache_append(cache, table, _ints(lens), k, v, new=_ints(new), weight=w)
+        swa.swa_check_device()
+        _same_pool(cache, pool)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_append_extreme_values(swa, dtype):
+    """Zeros, values at and above the ends of the scales' range, the borders between two scales,
+    and tokens that are not finite."""
+    g = _gen(5)
+    T, D, page = 96, 64, 32
+    cache = _cache(swa, g, 4, 1, D, page)
+    table = _table(g, 1, 4)
+    k = torch.randn((1, 1, T, D), generator=g, device="cuda")
+    v = torch.randn((1, 1, T, D), generator=g, device="cuda")
+    k[0, 0, :32] = 0.0
+    v[0, 0, :32] = 448.0 * 2.0**-30
+    v[0, 0, 3, 1] = -448.0 * 2.0**-30
+    k[0, 0, 40, 3] = math.nan
+    v[0, 0, 41, 5] = math.inf
+    k[0, 0, 42, 0] = -math.inf
+    v[0, 0, 43, 63] = 1e30
+    k[0, 0, 64:] *= 2.0**-60
+    v[0, 0, 70, 7] = 448.0 * 2.0**40
+    if dtype == torch.float32:
+        k[0, 0, 32, 0] = 448.00003
+    k, v = k.to(dtype), v.to(dtype)
+    pool = ref.pool_of(cache)
+    ref.append(pool, table, [0], k, v)
+    swa.swa_cache_append(cache, table, _ints([0]), k, v)
+    swa.swa_check_device()
+    _same_pool(cache, pool)
+    assert float(pool["k_scale"][int(table[0, 0]), 0]) == 2.0**-48
+    assert torch.isnan(pool["k"][int(table[0, 1]), 0, 8:12]).all()
+
+
+def test_append_without_weights_and_untouched_rows(swa):
+    g = _gen(6)
+    cache = _cache(swa, g, 5, 2, 128, 64, weight=False)
+    before = cache.k.view(torch.uint8).clone()
+    table = _ints([[3, 1], [0, 4]])
+    k = torch.randn((2, 2, 3, 128), generator=g, device="cuda").bfloat16()
+    swa.swa_cache_append(cache, table, _ints([62, 0]), k, k, new=_ints([3, 0]))
+    swa.swa_check_device()
+    now = cache.k.view(torch.uint8)
+    for p in (0, 2, 4):
+        assert torch.equal(now[p], before[p])
+    assert torch.equal(now[1, :, 1:], before[1, :, 1:])
+    assert not torch.equal(now[3, :, 62:], before[3, :, 62:])
+
+
+# ---- attention ---------------------------------------------------------------------------------
+
+ATTN = [
+    # B, Hq, H, D, page, T, lens, window, new, dtype, accumulate
+    (1, 1, 1, 64, 32, 1, [0], 1, None, torch.bfloat16, True),
+    (2, 2, 2, 128, 64, 1, [0, 1], 1000, None, torch.bfloat16, True),
+    (3, 4, 2, 128, 64, 1, [63, 64, 65], 1000, None, torch.bfloat16, True),
+    (3, 4, 2, 128, 64, 1, [700, 300, 5], 100, None, torch.float16, True),
+    (2, 8, 1, 64, 32, 1, [511, 1000], 64, None, torch.bfloat16, False),
+    (2, 6, 2, 256, 128, 1, [400, 129], 5000, None, torch.float16, True),
+    (1, 16, 1, 128, 64, 1, [2500], 5000, None, torch.bfloat16, True),
+    (1, 40, 2, 128, 64, 1, [777], 5000, None, torch.bfloat16, True),
+    (2, 4, 2, 128, 64, 5, [200, 60], 1000, None, torch.bfloat16, True),
+    (3, 4, 2, 128, 32, 7, [200, 60, 0], 33, [7, 0, 3], torch.float16, True),
+    (2, 14, 2, 64, 64, 4, [90, 350], 128, [1, 4], torch.bfloat16, True),
+    (1, 4, 2, 256, 64, 3, [1000], 64, None, torch.bfloat16, True),
+    (1, 4, 1, 128, 64, 64, [300], 5000, None, torch.bfloat16, True),
+    (1, 4, 2, 256, 32, 33, [100], 40, None, torch.float16, True),
+    (2, 2, 2, 64, 128, 16, [0, 5], 1, None, torch.bfloat16, True),
+    (5, 4, 4, 128, 64, 1, [0, 31, 4000, 32, 95], 10000, None, torch.bfloat16, True),
+    (40, 2, 1, 64, 32, 1, [3 * i for i in range(40)], 50, None, torch.float16, True),
+    (1, 2, 1, 128, 64, 1, [20000], 30000, None, torch.bfloat16, True),
+]
+
+
+@pytest.mark.parametrize("B,H_q,H,D,page,T,lens,window,new,dtype,acc", ATTN)
+def test_attn(swa, B, H_q, H, D, page, T, lens, window, new, dtype, acc):
+    g = _gen(B + T + D + lens[0])
+    width = -(-(max(lens) + T) // page) + 1
+    cache = _cache(swa, g, B * width + 1, H, D, page, spread=6)
+    table = _table(g, B, width)
+    # rows behind a sequence's last token hold NaN codes
+    for b in range(B):
+        end = lens[b] + (T if new is None else new[b])
+        for blk in range(end // page, width):
+            row = max(0, end - blk * page)
+            for x in (cache.k, cache.v):
+                x.view(torch.uint8)[int(table[b, blk]), :, row:] = ref.E4M3_NAN
+    q = torch.randn((B, H_q, T, D), generator=g, device="cuda").to(dtype)
+    pool = ref.pool_of(cache)
+    o, lse, to, tl, tw = ref.attn(pool, table, lens, q, window, new=new, accumulate=acc)
+    go, gl = swa.swa_cache_attn(q, cache, table, _ints(lens), window, new=_ints(new),
+                                accumulate=acc)
+    swa.swa_check_device()
+    _near(go, o, to, "o")
+    _near(gl, lse, tl, "lse")
+    if acc:
+        _near(cache.weight, pool["weight"], tw, "weight")
+    # the same bits again, and without touching the weights
+    w = cache.weight.clone()
+    go2, gl2 = swa.swa_cache_attn(q, cache, table, _ints(lens), window, new=_ints(new))
+    assert torch.equal(go, go2) and torch.equal(gl, gl2) and torch.equal(w, cache.weight)
+
+
+def test_attn_reads_nothing_outside_the_window(swa):
+    """Table entries of pages wholly before the window, or behind the last token, may name no page
+    at all, and NaN tokens outside a query's range change nothing for it."""
+    g = _gen(11)
+    cache = _cache(swa, g, 12, 2, 128, 32)
+    table = _table(g, 1, 12)
+    lens, window, T = [200], 64, 2
+    q = torch.randn((1, 4, T, 128), generator=g, device="cuda").bfloat16()
+    pool = ref.pool_of(cache)
+    o, lse, to, tl, _ = ref.attn(pool, table, lens, q, window)
+    # slots 137..201 are seen; slot 136 shares page 4 with them
+    bad = table.clone()
+    bad[0, :4] = -1
+    bad[0, 7:] = 1 << 30
+    cache.k.view(torch.uint8)[int(table[0, 4]), :, :9] = ref.E4M3_NAN
+    cache.v.view(torch.uint8)[int(table[0, 4]), :, :9] = ref.E4M3_NAN
+    go, gl = swa.swa_cache_attn(q, cache, bad, _ints(lens), window)
+    swa.swa_check_device()
+    _near(go, o, to, "o")
+    _near(gl, lse, tl, "lse")
+
+
+def test_attn_nan_token_reaches_only_who_sees_it(swa):
+    g = _gen(12)
+    D, page, T = 64, 32, 4
+    cache = swa.SwaCache.empty(4, 1, D, page)
+    table = _table(g, 1, 4)
+    k = torch.randn((1, 1, 60, D), generator=g, device="cuda").bfloat16()
+    v = torch.randn((1, 1, 60, D), generator=g, device="cuda").bfloat16()
+    k2, v2 = k.clone(), v.clone()
+    v2[0, 0, 58, 3] = math.inf  # the third of the four new tokens
+    q = torch.randn((1, 2, T, D), generator=g, device="cuda").bfloat16()
+    swa.swa_cache_append(cache, table, _ints([0]), k, v)
+    clean, _ = swa.swa_cache_attn(q, cache, table, _ints([56]), 1000)
+    swa.swa_cache_append(cache, table, _ints([0]), k2, v2)
+    o, lse = swa.swa_cache_attn(q, cache, table, _ints([56]), 1000, accumulate=True)
+    swa.swa_check_device()
+    assert torch.isfinite(o[:, :, :2].float()).all() and torch.isfinite(lse[:, :, :2]).all()
+    assert torch.isnan(o[:, :, 2:].float()).all() and torch.isnan(lse[:, :, 2:]).all()
+    _near(o[:, :, :2], clean[:, :, :2].cpu().double(),
+          2.0**-3 * torch.ones((1, 2, 2, D), dtype=torch.float64), "rows before")
+
+
+def test_attn_large_and_small_queries(swa):
+    """Rows of very large and very small queries, and scores far apart."""
+    g = _gen(13)
+    cache = _cache(swa, g, 8, 1, 128, 64)
+    table = _table(g, 1, 8)
+    q = torch.randn((1, 4, 1, 128), generator=g, device="cuda")
+    q[0, 0] *= 1e6
+    q[0, 1] *= 1e-30
+    q[0, 2] = 0
+    q[0, 3, 0, 1:] *= 1e-6
+    q = q.bfloat16()
+    lens = [300]
+    pool = ref.pool_of(cache)
+    o, lse, to, tl, _ = ref.attn(pool, table, lens, q, 1000)
+    go, gl = swa.swa_cache_attn(q, cache, table, _ints(lens), 1000)
+    swa.swa_check_device()
+    _near(go, o, to, "o")
+    _near(gl, lse, tl, "lse")
+
+
+def test_attn_bad_pages_and_lengths(swa):
+    """What the device finds out of range is skipped and reported; other sequences are unharmed."""
+    g = _gen(14)
+    cache = _cache(swa, g, 9, 2, 64, 32)
+    table = _table(g, 3, 3)
+    q = torch.randn((3, 2, 1, 64), generator=g, device="cuda").bfloat16()
+    good, _ = swa.swa_cache_attn(q, cache, table, _ints([40, 50, 60]), 1000)
+    swa.swa_check_device()
+    for lens, page in (([40, -1, 60], None), ([40, 96, 60], None), ([40, 50, 60], -7),
+                       ([40, 50, 60], 9), ([40, 2**31 - 1, 60], None)):
+        t = table.clone()
+        if page is not None:
+            t[1, 0] = page
+        before = cache.weight.clone()
+        o, lse = swa.swa_cache_attn(q, cache, t, _ints(lens), 1000, accumulate=True)
+        with pytest.raises(swa.SwaError, match="INDEX"):
+            swa.swa_check_device()
+        swa.swa_check_device()
+        assert torch.equal(o[0], good[0]) and torch.equal(o[2], good[2])
+        if page is None:
+            assert (o[1] == 0).all() and torch.isinf(lse[1]).all()
+        else:
+            assert torch.isfinite(o[1].float()).all()
+        cache.weight.copy_(before)
+    k = torch.randn((3, 2, 1, 64), generator=g, device="cuda").bfloat16()
+    before = cache.k.view(torch.uint8).clone()
+    t = table.clone()
+    t[:, 1] = -1
+    swa.swa_cache_append(cache, t, _ints([40, 96, -3]), k, k)
+    with pytest.raises(swa.SwaError, match="INDEX"):
+        swa.swa_check_device()
+    assert torch.equal(before, cache.k.view(torch.uint8))
+
+
+# ---- eviction ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("B,H,D,page,lens,budget,recent,ties", [
+    (1, 1, 64, 32, [50], 20, 5, False),
+    (2, 2, 128, 64, [300, 64], 64, 10, False),
+    (3, 2, 128, 64, [64, 65, 0], 64, 64, False),
+    (2, 1, 64, 32, [200, 33], 40, 0, True),
+    (2, 3, 256, 32, [100, 500], 97, 13, True),
+    (1, 2, 64, 128, [3000], 1000, 100, True),
+    (1, 1, 64, 64, [9000], 1, 0, False),
+    (1, 1, 64, 64, [1025], 1024, 1, True),
+    (4, 2, 128, 64, [10, 20, 30, 40], 128, 4, False),
+])
+def test_evict(swa, B, H, D, page, lens, budget, recent, ties):
+    g = _gen(sum(lens) + budget)
+    width = -(-max(lens + [1]) // page)
+    room = -(-budget // page)
+    cache = _cache(swa, g, B * (width + room), H, D, page, spread=12)
+    if ties:
+        cache.weight.copy_(torch.round(cache.weight * 2) / 2)
+    cache.weight[::3, :, 7] = math.nan
+    cache.weight[1::3, :, 9] = -0.0
+    cache.k.view(torch.uint8)[0, 0, 3] = ref.E4M3_NAN
+    order = _table(g, B, width + room)
+    table, dst = order[:, :width].contiguous(), order[:, width:].contiguous()
+    pool = ref.pool_of(cache)
+    kept, out = ref.evict(pool, table, lens, dst, budget, recent)
+    gk, go = swa.swa_cache_evict(cache, table, _ints(lens), dst, budget, recent)
+    swa.swa_check_device()
+    assert torch.equal(go.cpu(), out)
+    assert torch.equal(gk.cpu(), kept)
+    _same_pool(cache, pool)
+
+
+def test_evict_bad_pages_and_lengths(swa):
+    g = _gen(21)
+    cache = _cache(swa, g, 12, 1, 64, 32)
+    order = _table(g, 3, 4)
+    table, dst = order[:, :2].contiguous(), order[:, 2:].contiguous()
+    good = swa.swa_cache_evict(cache, table, _ints([64, 50, 40]), dst, 33, 4)[0].clone()
+    swa.swa_check_device()
+    for lens, where, value in (([64, -1, 40], None, 0), ([64, 65, 40], None, 0),
+                               ([64, 50, 40], "table", 12), ([64, 50, 40], "dst", -1)):
+        t, d = table.clone(), dst.clone()
+        if where:
+            (t if where == "table" else d)[1, 0] = value
+        kept, out = swa.swa_cache_evict(cache, t, _ints(lens), d, 33, 4)
+        with pytest.raises(swa.SwaError, match="INDEX"):
+            swa.swa_check_device()
+        assert torch.equal(kept[0], good[0]) and torch.equal(kept[2], good[2])
+        if where is None:
+            assert int(out[1]) == 0 and (kept[1] == -1).all()
+
+
+# ---- key weights -------------------------------------------------------------------------------
+
+def _ref_lse(q, k, window, causal):
+    B, Hq, Lq, D = q.shape
+    G, Lk = Hq // k.shape[1], k.shape[2]
+    x = q.double().cpu() @ k.double().cpu().repeat_interleave(G, 1).transpose(-1, -2) / math.sqrt(D)
+    d = torch.arange(Lq)[:, None] + (Lk - Lq) - torch.arange(Lk)
+    see = (d < window) & ((d >= 0) if causal else (d > -window))
+    return torch.logsumexp(x.masked_fill(~see, -math.inf), -1).float().cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("B,Hq,H,Lq,Lk,D,window,causal", [
+    (1, 1, 1, 1, 1, 64, 1, True),
+    (2, 4, 2, 255, 255, 64, 64, True),
+    (1, 2, 1, 300, 300, 128, 1, True),
+    (1, 2, 2, 512, 512, 128, 512, True),
+    (1, 6, 2, 130, 1000, 128, 77, True),
+    (1, 4, 1, 700, 700, 256, 200, True),
+    (2, 2, 1, 129, 257, 256, 1000, True),
+    (1, 4, 2, 333, 400, 64, 50, False),
+    (1, 3, 3, 640, 640, 128, 640, False),
+    (1, 2, 1, 1, 513, 128, 100, True),
+    (1, 2, 1, 1500, 1500, 128, 300, True),
+])
+def test_key_weights(swa, B, Hq, H, Lq, Lk, D, window, causal, dtype):
+    g = _gen(Lq + Lk + D)
+    q = torch.randn((B, Hq, Lq, D), generator=g, device="cuda").to(dtype)
+    k = torch.randn((B, H, Lk, D), generator=g, device="cuda").to(dtype)
+    lse = _ref_lse(q, k, window, causal)
+    w, tol = ref.key_weights(q, k, lse, window, causal=causal)
+    got = torch.full((B, H, Lk), math.nan, device="cuda")
+    swa.swa_attn_key_weights(q, k, lse, window, causal=causal, out=got)
+    swa.swa_check_device()
+    _near(got, w, tol, "weights")
+    # every row gives out one, up to the keys' errors together (lse's rounding is among them)
+    total = got.double().cpu().sum(-1)
+    assert ((total - (Hq // H) * Lq).abs() <= tol.sum(-1)).all()
+    again = swa.swa_attn_key_weights(q, k, lse, window, causal=causal)
+    assert torch.equal(again, got)
+
+
+def test_key_weights_nan_stays_inside_the_window(swa):
+    """A NaN query row reaches the keys it sees and no others."""
+    g = _gen(31)
+    q = torch.randn((1, 2, 400, 128), generator=g, device="cuda").bfloat16()
+    k = torch.randn((1, 1, 400, 128), generator=g, device="cuda").bfloat16()
+    lse = _ref_lse(q, k, 50, True)
+    clean = swa.swa_attn_key_weights(q, k, lse, 50)
+    q[0, 1, 200] = math.nan
+    lse[0, 0, 300] = math.nan
+    got = swa.swa_attn_key_weights(q, k, lse, 50)
+    swa.swa_check_device()
+    seen = torch.zeros(400, dtype=torch.bool, device="cuda")
+    seen[151:201] = True
+    seen[251:301] = True
+    assert torch.equal(torch.isnan(got[0, 0]), seen)
+    assert torch.equal(got[0, 0][~seen], clean[0, 0][~seen])
+
+
+# ---- a run of them together --------------------------------------------------------------------
+
+def _serve(swa, prompt, steps, budget, window):
+    """A prompt through the training forward, its tokens and weights into the cache, tokens one by
+    one, an eviction, more tokens: every result against the 64-bit forms on the state the GPU had."""
+    g = _gen(41)
+    B, Hq, H, D, page = 2, 4, 2, 128, 64
+    room = -(-(budget + steps) // page)
+    width = -(-(prompt + steps) // page)
+    cache = swa.SwaCache.empty(B * (width + room), H, D, page)
+    order = _table(g, B, width + room)
+    table, spare = order[:, :width].contiguous(), order[:, width:].contiguous()
+
+    def rand(heads, n):
+        return torch.randn((B, heads, n, D), generator=g, device="cuda").bfloat16()
+
+    q, k, v = rand(Hq, prompt), rand(H, prompt), rand(H, prompt)
+    _, lse = swa.swa_attn_fwd(q, k, v, window)
+    w = swa.swa_attn_key_weights(q, k, lse, window)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    swa.swa_cache_append(cache, table, lens, k, v, weight=w)
+    want, tol = ref.key_weights(q, k, lse, window)
+    stored = torch.stack([torch.stack([
+        torch.cat([cache.weight[int(p), h] for p in table[b]])[:prompt] for h in range(H)])
+        for b in range(B)])
+    _near(stored, want, tol, "prompt weights")
+    lens += prompt
+    for phase in range(2):
+        for _ in range(steps):
+            k1, v1, q1 = rand(H, 1), rand(H, 1), rand(Hq, 1)
+            pool = ref.pool_of(cache)
+            ref.append(pool, table, lens, k1, v1)
+            swa.swa_cache_append(cache, table, lens, k1, v1)
+            _same_pool(cache, pool)
+            o, le, to, tl, tw = ref.attn(pool, table, lens, q1, window, accumulate=True)
+            go, gl = swa.swa_cache_attn(q1, cache, table, lens, window, accumulate=True)
+            _near(go, o, to, "o")
+            _near(gl, le, tl, "lse")
+            _near(cache.weight, pool["weight"], tw, "weight")
+            lens = lens + 1
+        if phase == 0:
+            pool = ref.pool_of(cache)
+            kept, out = ref.evict(pool, table, lens, spare, budget, 8)
+            gk, lens = swa.swa_cache_evict(cache, table, lens, spare, budget, 8)
+            assert torch.equal(gk.cpu(), kept) and torch.equal(lens.cpu(), out)
+            _same_pool(cache, pool)
+            table = spare
+    swa.swa_check_device()
+
+
+def test_serving_full_layer(swa):
+    _serve(swa, prompt=300, steps=4, budget=100, window=1 << 20)
+
+
+def test_serving_sliding_layer(swa):
+    _serve(swa, prompt=170, steps=3, budget=150, window=64)
+
+
+def test_serving_step_in_a_graph(swa):
+    """A captured step (append, attention, lengths) replayed equals eager steps bit for bit, while
+    other lengths than the captured ones hold, on a stream of its own."""
+    g = _gen(51)
+    B, Hq, H, D, page, n = 3, 4, 2, 128, 32, 40
+    width = 6
+
+    def state():
+        gg = _gen(52)
+        c = _cache(swa, gg, B * width, H, D, page)
+        return c, _table(gg, B, width), _ints([0, 31, 100])
+
+    ks = torch.randn((n, B, H, 1, D), generator=g, device="cuda").bfloat16()
+    qs = torch.randn((n, B, Hq, 1, D), generator=g, device="cuda").bfloat16()
+    eager = []
+    cache, table, lens = state()
+    for i in range(n):
+        swa.swa_cache_append(cache, table, lens, ks[i], ks[i])
+        eager.append(swa.swa_cache_attn(qs[i], cache, table, lens, 64, accumulate=True))
+        lens += 1
+    weight = cache.weight.clone()
+    cache, table, lens = state()
+    k, q = ks[0].clone(), qs[0].clone()
+    out = torch.empty_like(q)
+    lse = torch.empty((B, Hq, 1), device="cuda")
+    need = swa.swa_cache_attn_workspace_bytes(B, Hq, H, 1, D, width, page, True)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        swa.swa_cache_append(cache, table, lens, k, k)
+        swa.swa_cache_attn(q, cache, table, lens, 64, accumulate=True, out=out, lse=lse,
+                           workspace=ws)
+        lens += 1
+    for i in range(n):
+        k.copy_(ks[i])
+        q.copy_(qs[i])
+        graph.replay()
+        assert torch.equal(out, eager[i][0]) and torch.equal(lse, eager[i][1]), i
+    assert torch.equal(weight, cache.weight)
+    swa.swa_check_device()
