@@ -1,142 +1,878 @@
 // swa_cache_attn.cu — attention of a few tokens per sequence over the paged e4m3 cache, and the
 // accumulation of the weight each cached token received.
 //
-// First form: one block per (query, head, sequence); its warps take the visible slots in turn with
-// an online softmax each, and join their sums in shared memory.
-#include <cuda_fp8.h>
+// Per (sequence, kv head) the R = G T query rows that share a kv head see the same keys:
+//   x = scale <q, k>,  o = sum p v,  p = exp(x - lse),  lse = ln sum exp(x).
+// Every key and value byte is needed once, 2 D bytes for 4 D R flops, so the memory bounds it and
+// the tensor cores (mma.sync, 16 rows a tile) only have to keep up.  What is built around that:
+//   * The list of all chunks (32 keys, 16 at D = 256: 8 KB of keys and values at D >= 128) of all
+//     items is cut into equal parts, one per team (swa_cache_split.h), so ragged lengths and few
+//     heads fill the SMs alike.  One CTA of 8 warps per SM; a team is MT warps with 16 query rows
+//     each (MT = 1, 2, 4), which share its ring of chunks in shared memory.
+//   * Chunks arrive by TMA, swizzled; 192 KB of ring keep 128 KB in flight per SM.  A lane looks up
+//     the pages and scales of one of the next 32 chunks, so the walk never waits for a table.
+//   * Codes become fp16 exactly (cvt.f16x2.e4m3x2).  S = Q K^T takes keys by ldmatrix, whose 8 x 16
+//     byte matrices give each lane 4 consecutive codes; the order of the contraction is permuted
+//     the same way in Q.  P V takes two values of neighbouring keys from two rows by byte permutes,
+//     which is the transposition that the operand needs; lane group g reads the 16 columns from
+//     16 g on, so a row of o ends up 32 columns to a lane.
+//   * A block's key scale multiplies its scores; its value scale, divided by the walk's reference
+//     scale, multiplies p.  The running maximum and the reference change only when they have to
+//     (a score 4 above, in powers of two; a scale outside [ref, 64 ref]), so o is rarely rescaled.
+// A second kernel joins the items that several teams shared and answers rows that see nothing; with
+// accumulate the first stores its scores, and a third adds exp(x - lse) to the cached tokens' weights.
+#include <climits>
+#include <type_traits>
 
 #include "swa_cache_kernels.h"
+#include "swa_cache_split.h"
 #include "swa_ptx.cuh"
+#include "swa_tmap.h"
 
 namespace swa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxSeqs = 1024;  // sequences per launch; more run as several launches
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
+template <int D>
+struct AttnCfg {
+  static constexpr int CK = D == 256 ? 16 : 32;          // keys of a chunk
+  static constexpr int kCols = D < 128 ? D : 128;        // columns of a TMA box
+  static constexpr int kBoxes = D / kCols;
+  static constexpr int kBoxBytes = CK * kCols;
+  static constexpr int kStageBytes = 2 * CK * D;         // keys, then values
+  static constexpr int kStages = 192 * 1024 / kStageBytes;  // of the CTA, shared out to its teams
+  // D = 256 keeps its Q fragments in shared memory (64 KB), in place of 8 stages.
+  static constexpr int kQBytes = D == 256 ? kWarps * 16 * D * 2 : 0;
+  static constexpr int kRing = kStages - kQBytes / kStageBytes;
+  static constexpr int kOffFirst = kRing * kStageBytes + kQBytes;
+  static constexpr int kOffBar = kOffFirst + (kMaxSeqs + 1) * 8;
+  static constexpr int kOffSums = kOffBar + 2 * kStages * 8 + 16;  // + abort flag
+  static constexpr int kSmemBytes = kOffSums + kWarps * 8;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+};
+
+struct AttnDev {
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;
+  int Hq, G, R;      // query heads, per kv head, rows per kv head (G T)
+  int MT, RT, NRT;   // warps of a team, rows of an item, items per kv head
+  int rows;          // rows an item stores: min(RT, R)
+  int window, parts, f16;
+  float scale_log2;
+  int64_t* first;    // [B + 1] chunks before each sequence
+  float* ml;         // [2 parts][rows][2] partial maxima and sums
+  float* po;         // [2 parts][rows][D] partial outputs
+  float* scores;     // [chunks][rows][CK], or null
+};
+
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&r)[W]) {
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Codes 0, 1 (low half) and 2, 3 (high half) of a word as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+__device__ __forceinline__ uint32_t swizzle_of(int cols, uint32_t row) {
+  return cols == 128 ? (row & 7u) : ((row >> 1) & 3u);
 }
 
-template <int D, bool F16>
-__device__ __forceinline__ float q_value(const void* q, size_t i) {
-  const uint16_t u = static_cast<const uint16_t*>(q)[i];
-  return Elem<F16>::unpack(u).x;
+// Lets the next kernel of the stream be scheduled, and waits for the one before to be complete.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kWarps * 32)
-    swa_cache_attn_kernel(const CacheView c, const CacheAttnArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  const int t = static_cast<int>(blockIdx.x), hq = static_cast<int>(blockIdx.y);
-  const int b = static_cast<int>(blockIdx.z);
-  const int h = hq / (a.Hq / c.Hkv);
+// What a lane holds about one chunk of its team's next 32.
+struct ChunkInfo {
+  int plane;  // page * Hkv + head, or -1: nothing to be seen there
+  int slot;   // first slot
+  int item;
+  float ks, vs;
+};
+
+// The walk's state for one item.
+template <int D>
+struct ItemState {
+  float acc[D / 8][4];  // o in units of vref; tile i of half x: columns 128 x + 16 n + i
+  float m[2], l[2];     // rows g, g + 8: running maximum (base 2) and this lane's part of the sum
+  float vref;
+  float f[2];           // score factors of the two rows without the block's scale
+  int lo[2], hi[2];     // slots the two rows see, inclusive
+  int any_lo, any_hi;   // slots any row sees
+  int all_lo, all_hi;   // slots every real row sees
+};
+
+template <int D, bool kEdge>
+__device__ __forceinline__ void process_chunk(ItemState<D>& st, const uint32_t (*qf)[4],
+                                              uint32_t sq, uint32_t sk, const ChunkInfo& ci,
+                                              float* scores, int rows, int row0) {
+  using C = AttnCfg<D>;
+  constexpr int CK = C::CK;
+  const uint32_t lane = lane_id(), g = lane >> 2, t = lane & 3u;
+  float s[CK / 8][4];
+#pragma unroll
+  for (int j = 0; j < CK / 8; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+#pragma unroll
+  for (int x = 0; x < C::kBoxes; ++x) {
+#pragma unroll
+    for (int cq = 0; cq < C::kCols / 64; ++cq) {
+      uint32_t qa[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int step = x * 8 + cq * 4 + i;
+        if constexpr (D == 256) {
+          lds_words<4>(sq + (step * 32 + lane) * 16, qa[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qa[i][e] = qf[step][e];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < CK / 8; ++j) {
+        const uint32_t row = 8 * j + (lane & 7u);
+        const uint32_t unit = (4 * cq + (lane >> 3)) ^ swizzle_of(C::kCols, row);
+        uint32_t r[4];
+        ldmatrix_x4(sk + x * C::kBoxBytes + row * C::kCols + (unit << 4), r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t b0, b1;
+          e4m3x4_to_f16(r[i], b0, b1);
+          mma16816(s[j], qa[i], b0, b1);
+        }
+      }
+    }
+  }
+  // scores in base 2
+  const float f0 = st.f[0] * ci.ks, f1 = st.f[1] * ci.ks;
+  float mx0 = SWA_NEG_INF, mx1 = SWA_NEG_INF;
+#pragma unroll
+  for (int j = 0; j < CK / 8; ++j) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[j][i] *= f0;
+      s[j][2 + i] *= f1;
+      if (kEdge) {
+        const int slot = ci.slot + 8 * j + 2 * static_cast<int>(t) + i;
+        s[j][i] = slot >= st.lo[0] && slot <= st.hi[0] ? s[j][i] : SWA_NEG_INF;
+        s[j][2 + i] = slot >= st.lo[1] && slot <= st.hi[1] ? s[j][2 + i] : SWA_NEG_INF;
+      }
+      mx0 = fmaxf(mx0, s[j][i]);
+      mx1 = fmaxf(mx1, s[j][2 + i]);
+    }
+  }
+  if (scores != nullptr) {
+#pragma unroll
+    for (int j = 0; j < CK / 8; ++j) {
+      const int r0 = row0 + static_cast<int>(g);
+      if (r0 < rows)
+        *reinterpret_cast<float2*>(scores + r0 * CK + 8 * j + 2 * t) = make_float2(s[j][0], s[j][1]);
+      if (r0 + 8 < rows)
+        *reinterpret_cast<float2*>(scores + (r0 + 8) * CK + 8 * j + 2 * t) =
+            make_float2(s[j][2], s[j][3]);
+    }
+  }
+  mx0 = quad_max(mx0);
+  mx1 = quad_max(mx1);
+  // The maximum and the value reference move only when a probability could reach 2^4, or a scale
+  // leaves [vref, 64 vref]: p vs / vref then stays within fp16 and above its subnormals as far as
+  // p itself is.
+  const bool moves = mx0 > st.m[0] + 4.f || mx1 > st.m[1] + 4.f ||
+                     !(ci.vs >= st.vref && ci.vs <= 64.f * st.vref);
+  if (__any_sync(0xffffffffu, moves)) {
+    const float n0 = fmaxf(st.m[0], mx0), n1 = fmaxf(st.m[1], mx1);
+    const float nref = ci.vs >= st.vref && ci.vs <= 64.f * st.vref ? st.vref : ci.vs * 0.125f;
+    const float a0 = st.m[0] == SWA_NEG_INF ? 0.f : ex2(st.m[0] - n0);
+    const float a1 = st.m[1] == SWA_NEG_INF ? 0.f : ex2(st.m[1] - n1);
+    const float u = nref == st.vref ? 1.f : st.vref / nref;
+    // A sum that is NaN stays so (0 * NaN); before the first visible key everything is zero.
+    st.l[0] *= a0;
+    st.l[1] *= a1;
+    const float w0 = a0 * u, w1 = a1 * u;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      st.acc[i][0] *= w0;
+      st.acc[i][1] *= w0;
+      st.acc[i][2] *= w1;
+      st.acc[i][3] *= w1;
+    }
+    st.m[0] = n0;
+    st.m[1] = n1;
+    st.vref = nref;
+  }
+  const float b0 = st.m[0] == SWA_NEG_INF ? 0.f : st.m[0];
+  const float b1 = st.m[1] == SWA_NEG_INF ? 0.f : st.m[1];
+  const float ratio = ci.vs / st.vref;
+  uint32_t pa[CK / 16][4];
+#pragma unroll
+  for (int j = 0; j < CK / 8; ++j) {
+    float p[4];
+    p[0] = ex2(s[j][0] - b0);
+    p[1] = ex2(s[j][1] - b0);
+    p[2] = ex2(s[j][2] - b1);
+    p[3] = ex2(s[j][3] - b1);
+    st.l[0] += p[0] + p[1];
+    st.l[1] += p[2] + p[3];
+    pa[j / 2][2 * (j & 1)] = pack_f16(p[0] * ratio, p[1] * ratio);
+    pa[j / 2][2 * (j & 1) + 1] = pack_f16(p[2] * ratio, p[3] * ratio);
+  }
+  // o += P V
+  const uint32_t sv = sk + CK * D;
+  constexpr int W = C::kCols / 32;  // words a lane reads of a row: 16 or 8 columns
+#pragma unroll
+  for (int i = 0; i < CK / 16; ++i) {
+#pragma unroll
+    for (int x = 0; x < C::kBoxes; ++x) {
+      uint32_t v[4][W];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t row = 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
+        uint32_t at;
+        if constexpr (W == 4)
+          at = row * 128u + ((g ^ (row & 7u)) << 4);
+        else
+          at = row * 64u + (((g >> 1) ^ ((row >> 1) & 3u)) << 4) + ((g & 1u) << 3);
+        lds_words<W>(sv + x * C::kBoxBytes + at, v[e]);
+        if (kEdge) {
+          const int slot = ci.slot + static_cast<int>(row);
+          if (slot < st.any_lo || slot > st.any_hi) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) v[e][w] = 0u;
+          }
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+        e4m3x4_to_f16(__byte_perm(v[0][w], v[1][w], 0x5140), a0, a1);
+        e4m3x4_to_f16(__byte_perm(v[0][w], v[1][w], 0x7362), a2, a3);
+        e4m3x4_to_f16(__byte_perm(v[2][w], v[3][w], 0x5140), c0, c1);
+        e4m3x4_to_f16(__byte_perm(v[2][w], v[3][w], 0x7362), c2, c3);
+        const int tile = x * (D > 128 ? 16 : 0) + 4 * w;
+        mma16816(st.acc[tile], pa[i], a0, c0);
+        mma16816(st.acc[tile + 1], pa[i], a1, c1);
+        mma16816(st.acc[tile + 2], pa[i], a2, c2);
+        mma16816(st.acc[tile + 3], pa[i], a3, c3);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    swa_cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const CacheView c,
+                          const AttnDev a) {
+  using C = AttnCfg<D>;
+  constexpr int CK = C::CK;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!smem_base_ok(smem, c.err)) return;
+  int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  int& abort_flag = *reinterpret_cast<int*>(bars + 2 * C::kStages);
+  const int tid = static_cast<int>(threadIdx.x);
   const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
-  const size_t row = (static_cast<size_t>(b) * a.Hq + hq) * c.T + t;
-  int len, n;
-  const bool ok = sequence_of(c, b, &len, &n) && t < n;
-  const int hi = ok ? len + t : -1, lo = max(0, hi - a.window + 1);
-  float q[E], o[E] = {}, m = SWA_NEG_INF, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = q_value<D, F16>(a.q, row * D + lane * E + e);
-  for (int s = lo + warp; s <= hi; s += kWarps) {
-    const int page = page_of(c, c.table, b, s / c.page, c.max_pages);
-    if (page < 0) continue;
-    const size_t block = static_cast<size_t>(page) * c.Hkv + h;
-    const size_t at = (block * c.page + s % c.page) * D + lane * E;
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x = fmaf(q[e], e4m3_value(c.k[at + e]), x);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-    x *= a.scale * c.k_scale[block];
-    const float top = fmaxf(m, x);  // NaN scores leave m and make the sum NaN below
-    const float keep = m == top ? 1.f : expf(m - top), p = expf(x - top);
-    const float pv = p * c.v_scale[block];
-    l = l * keep + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + pv * e4m3_value(c.v[at + e]);
-    m = top;
+  launch_dependents();
+  const int teams = kWarps / a.MT, team = warp / a.MT, wt = warp % a.MT;
+  const int NS = C::kRing / teams;  // stages of a team's ring
+  auto full = [&](int s) { return smem_u32(&bars[team * NS + s]); };
+  auto empty = [&](int s) { return smem_u32(&bars[C::kStages + team * NS + s]); };
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(smem_u32(&bars[i]), 1);
+      mbar_init(smem_u32(&bars[C::kStages + i]), static_cast<uint32_t>(a.MT));
+    }
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+  // Chunks before each sequence: four sequences a thread, an inclusive scan over the warps.
+  {
+    int64_t* s_sum = reinterpret_cast<int64_t*>(smem + C::kOffSums);
+    int64_t own[4], sum = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    for (int i = 0; i < 4; ++i) {
+      const int b = 4 * tid + i;
+      int n = 0, len = 0;
+      if (b < c.B && !sequence_of(c, b, &len, &n)) n = 0;
+      own[i] = sum;
+      sum += b < c.B ? chunk_count(len, n, a.window, CK) : 0;
+    }
+    int64_t scan = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, scan, d);
+      if (lane >= d) scan += up;
+    }
+    if (lane == 31) s_sum[warp] = scan;
+    __syncthreads();
+    int64_t base = scan - sum;
+    for (int w = 0; w < warp; ++w) base += s_sum[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * tid + i <= c.B) s_first[4 * tid + i] = base + own[i];
+    if (tid == kThreads - 1 && c.B == 4 * kThreads) s_first[c.B] = base + sum;
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int b = tid; b <= c.B; b += kThreads) a.first[b] = s_first[b];
+  }
+  const int per = c.Hkv * a.NRT;  // items of a sequence
+  const int64_t total = s_first[c.B] * per;
+  const int part = static_cast<int>(blockIdx.x) * teams + team;
+  const int64_t begin = part_start(total, a.parts, part);
+  const int64_t count = part_start(total, a.parts, part + 1) - begin;
+
+  auto load_info = [&](int64_t i) {  // chunk i of the part
+    ChunkInfo ci = {-1, 0, -1, 1.f, 1.f};
+    if (i < count) {
+      const int64_t x = begin + i;
+      const int b = sequence_at(s_first, c.B, per, x);
+      const int nc = static_cast<int>(s_first[b + 1] - s_first[b]);
+      const int64_t rem = x - s_first[b] * per;
+      const int hr = static_cast<int>(rem / nc);
+      ci.item = b * per + hr;
+      ci.slot = (first_chunk(c.lens[b], a.window, CK) + static_cast<int>(rem - static_cast<int64_t>(hr) * nc)) * CK;
+      const int page = page_of(c, c.table, b, ci.slot / c.page, c.max_pages);
+      if (page >= 0) {
+        ci.plane = page * c.Hkv + hr / a.NRT;
+        ci.ks = c.k_scale[ci.plane];
+        ci.vs = c.v_scale[ci.plane];
+      }
+    }
+    return ci;
+  };
+  ChunkInfo cur = load_info(lane), nxt = load_info(32 + lane);
+  const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(team * NS) * C::kStageBytes;
+  int64_t issued = 0;
+  auto issue = [&](int64_t i, int s, bool in_next) {  // whole warp; chunk i into stage s = i % NS
+    const int plane = __shfl_sync(0xffffffffu, in_next ? nxt.plane : cur.plane, static_cast<int>(i & 31));
+    const int slot = __shfl_sync(0xffffffffu, in_next ? nxt.slot : cur.slot, static_cast<int>(i & 31));
+    if (wt == 0 && lane == 0) {
+      const uint32_t dst = ring + static_cast<uint32_t>(s) * C::kStageBytes;
+      mbar_arrive_expect_tx(full(s), C::kStageBytes);
+      // A chunk whose page is out of range loads plane 0 and is masked.
+#pragma unroll
+      for (int x = 0; x < C::kBoxes; ++x) {
+        tma_load_3d(dst + x * C::kBoxBytes, &tm_k, full(s), 128 * x, slot % c.page, max(plane, 0));
+        tma_load_3d(dst + CK * D + x * C::kBoxBytes, &tm_v, full(s), 128 * x, slot % c.page,
+                    max(plane, 0));
+      }
+    }
+    issued = i + 1;
+  };
+  for (int i = 0; i < NS && i < count; ++i) issue(i, i, i >= 32);
+
+  const uint32_t sq = smem_u32(smem + C::kRing * C::kStageBytes) + static_cast<uint32_t>(warp) * 16 * D * 2;
+  constexpr int kSteps = D / 16;
+  uint32_t qf[D == 256 ? 1 : kSteps][4];
+  ItemState<D> st = {};
+  int item = -1, b = 0, item_first = 0, item_chunks = 0;
+  bool begins = false;
+  const int g = lane >> 2, t = lane & 3;
+  const int r0 = wt * 16 + g;  // this thread's rows of the item: r0 and r0 + 8
+
+  // Finishes the item after its chunk at `slot`.
+  auto finish = [&](int slot) {
+    const bool ends = slot / CK == item_first + item_chunks - 1;
+    const float l0 = quad_sum(st.l[0]), l1 = quad_sum(st.l[1]);
+    const int hr = item - b * per, h = hr / a.NRT, tile0 = (hr % a.NRT) * a.RT;
+    const size_t base = (static_cast<size_t>(b) * c.Hkv + h) * a.R + tile0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + 8 * e;
+      const float l = e == 0 ? l0 : l1;
+      if (tile0 + r >= a.R) continue;
+      if (begins && ends) {
+        const float inv = l == 0.f ? 0.f : st.vref / l;
+        uint16_t* out = a.o + (base + r) * D;
+#pragma unroll
+        for (int x = 0; x < (D > 128 ? 2 : 1); ++x) {
+          constexpr int kTiles = D < 128 ? 8 : 16;  // = columns of a run
+#pragma unroll
+          for (int run = 0; run < 2; ++run) {
+            uint32_t pk[kTiles / 2];
+#pragma unroll
+            for (int i = 0; i < kTiles / 2; ++i) {
+              const float y0 = st.acc[x * 16 + 2 * i][2 * e + run] * inv;
+              const float y1 = st.acc[x * 16 + 2 * i + 1][2 * e + run] * inv;
+              pk[i] = a.f16 ? Elem<true>::pack(y0, y1) : Elem<false>::pack(y0, y1);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(out + 128 * x + kTiles * (2 * t + run));
+#pragma unroll
+            for (int i = 0; i < kTiles / 8; ++i)
+              dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          }
+        }
+        if (t == 0) a.lse[base + r] = l == 0.f ? SWA_NEG_INF : (st.m[e] + log2f(l)) * kLn2;
+      } else {
+        const size_t slot_row = static_cast<size_t>(partial_slot(part, begins)) * a.rows + r;
+        float* out = a.po + slot_row * D;
+#pragma unroll
+        for (int x = 0; x < (D > 128 ? 2 : 1); ++x) {
+          constexpr int kTiles = D < 128 ? 8 : 16;
+#pragma unroll
+          for (int run = 0; run < 2; ++run) {
+            float4* dst = reinterpret_cast<float4*>(out + 128 * x + kTiles * (2 * t + run));
+#pragma unroll
+            for (int i = 0; i < kTiles / 4; ++i)
+              dst[i] = make_float4(st.acc[x * 16 + 4 * i][2 * e + run] * st.vref,
+                                   st.acc[x * 16 + 4 * i + 1][2 * e + run] * st.vref,
+                                   st.acc[x * 16 + 4 * i + 2][2 * e + run] * st.vref,
+                                   st.acc[x * 16 + 4 * i + 3][2 * e + run] * st.vref);
+          }
+        }
+        if (t == 0) {
+          a.ml[slot_row * 2] = st.m[e];
+          a.ml[slot_row * 2 + 1] = l;
+        }
+      }
+    }
+  };
+
+  auto start = [&](int new_item, int slot) {
+    item = new_item;
+    b = item / per;
+    const int hr = item - b * per, h = hr / a.NRT, tile0 = (hr % a.NRT) * a.RT;
+    const int len = c.lens[b], n = c.new_lens ? c.new_lens[b] : c.T;
+    item_first = first_chunk(len, a.window, CK);
+    item_chunks = chunk_count(len, n, a.window, CK);
+    begins = slot / CK == item_first;
+    st.any_lo = visible_lo(len, a.window);
+    st.any_hi = len + n - 1;
+    st.all_lo = visible_lo(len + n - 1, a.window);
+    st.all_hi = n < c.T ? -1 : len;  // a row without a query sees nothing
+    const size_t base = (static_cast<size_t>(b) * c.Hkv + h) * a.R + tile0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + 8 * e, tq = (tile0 + r) % c.T;
+      const bool real = tile0 + r < a.R && tq < n;
+      st.lo[e] = visible_lo(len + tq, a.window);
+      st.hi[e] = real ? len + tq : -1;
+      st.m[e] = SWA_NEG_INF;
+      st.l[e] = 0.f;
+      // The row as fp16, its largest element brought to [2^14, 2^15).
+      uint2 raw[kSteps];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        raw[i] = make_uint2(0u, 0u);
+        if (real) raw[i] = __ldg(reinterpret_cast<const uint2*>(a.q + (base + r) * D + 16 * i + 4 * t));
+        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[i].x) : Elem<false>::unpack(raw[i].x);
+        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[i].y) : Elem<false>::unpack(raw[i].y);
+        top = max(max(top, __float_as_uint(fabsf(y0.x))), __float_as_uint(fabsf(y0.y)));
+        top = max(max(top, __float_as_uint(fabsf(y1.x))), __float_as_uint(fabsf(y1.y)));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(14 - exponent) as two factors, each inside fp32's range; none for zero, infinity and NaN
+      const int ex = static_cast<int>(top >> 23);
+      const int sh = ex == 255 || top == 0 ? 0 : 127 + 14 - max(ex, 1);
+      const float up0 = __uint_as_float(static_cast<uint32_t>(127 + sh / 2) << 23);
+      const float up1 = __uint_as_float(static_cast<uint32_t>(127 + sh - sh / 2) << 23);
+      st.f[e] = a.scale_log2 / up0 / up1;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[i].x) : Elem<false>::unpack(raw[i].x);
+        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[i].y) : Elem<false>::unpack(raw[i].y);
+        const uint32_t p0 = pack_f16(y0.x * up0 * up1, y0.y * up0 * up1);
+        const uint32_t p1 = pack_f16(y1.x * up0 * up1, y1.y * up0 * up1);
+        if constexpr (D == 256) {
+          st_shared_b32(sq + (i * 32 + lane) * 16 + 4 * e, p0);
+          st_shared_b32(sq + (i * 32 + lane) * 16 + 8 + 4 * e, p1);
+        } else {
+          qf[i][e] = p0;
+          qf[i][2 + e] = p1;
+        }
+      }
+    }
+    st.vref = 1.f;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.acc[i][e] = 0.f;
+    __syncwarp();
+  };
+
+  int last_slot = 0, s = 0;
+  uint32_t phase = 0;
+  int64_t done = 0;
+  bool ok = true;
+  for (int64_t i = 0; i < count; ++i) {
+    if (i > 0 && (i & 31) == 0) {
+      cur = nxt;
+      nxt = load_info(i + 32 + lane);
+    }
+    const int from = static_cast<int>(i & 31);
+    ChunkInfo ci;
+    ci.plane = __shfl_sync(0xffffffffu, cur.plane, from);
+    ci.slot = __shfl_sync(0xffffffffu, cur.slot, from);
+    ci.item = __shfl_sync(0xffffffffu, cur.item, from);
+    ci.ks = __shfl_sync(0xffffffffu, cur.ks, from);
+    ci.vs = __shfl_sync(0xffffffffu, cur.vs, from);
+    if (ci.item != item) {
+      if (item >= 0) finish(last_slot);
+      start(ci.item, ci.slot);
+    }
+    last_slot = ci.slot;
+    if (!(ok = warp_wait(full(s), phase, &abort_flag, c.err))) break;
+    const uint32_t sk = ring + static_cast<uint32_t>(s) * C::kStageBytes;
+    float* sc = a.scores == nullptr ? nullptr
+                                    : a.scores + static_cast<size_t>(begin + i) * a.rows * CK;
+    const bool edge = ci.plane < 0 || ci.slot < st.all_lo || ci.slot + CK - 1 > st.all_hi;
+    if (edge) {
+      ItemState<D>& e = st;
+      const int lo0 = e.lo[0], lo1 = e.lo[1], any = e.any_lo;
+      if (ci.plane < 0) e.lo[0] = e.lo[1] = e.any_lo = INT_MAX;  // nothing of it is seen
+      process_chunk<D, true>(e, qf, sq, sk, ci, sc, a.rows, wt * 16);
+      e.lo[0] = lo0;
+      e.lo[1] = lo1;
+      e.any_lo = any;
+    } else {
+      process_chunk<D, false>(st, qf, sq, sk, ci, sc, a.rows, wt * 16);
+    }
+    __syncwarp();
+    done = i + 1;
+    if (a.MT > 1 && lane == 0) mbar_arrive(empty(s));
+    const int64_t ahead = i + NS;
+    if (ahead < count) {
+      if (a.MT > 1 && wt == 0 &&
+          !(ok = warp_wait(empty(s), phase, &abort_flag, c.err)))
+        break;
+      issue(ahead, s, (ahead >> 5) != (i >> 5));
+    }
+    if (++s == NS) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  if (ok) {
+    if (item >= 0) finish(last_slot);
+  } else if (wt == 0) {  // a wait ran out: this team's copies in flight land before the CTA ends
+    for (int64_t i = done; i < issued; ++i)
+      warp_drain_wait(full(static_cast<int>(i % NS)), static_cast<uint32_t>(i / NS) & 1u, c.err);
+  }
+}
+
+// Joins the partial results of items that several teams shared, and answers the rows of sequences
+// without a chunk.  Tasks are (item, row, run of 4 `lanes` columns), one block each in turn: groups of
+// `lanes` threads take the partials in turn, then the groups' sums are added in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(256) swa_cache_join_kernel(const CacheView c, const AttnDev a,
+                                                             int lanes) {
+  using C = AttnCfg<D>;
+  __shared__ float s_red[8], s_l[64];
+  __shared__ float4 s_o[256];
+  wait_predecessor();
+  launch_dependents();
+  const int tid = static_cast<int>(threadIdx.x);
+  const int per = c.Hkv * a.NRT, runs = D / 4 / lanes, groups = 256 / lanes;
+  const int64_t total = a.first[c.B] * per;
+  const int64_t tasks = static_cast<int64_t>(c.B) * per * a.rows * runs;
+  const int group = tid / lanes, sub = tid % lanes;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int run = static_cast<int>(task % runs);
+    const int64_t ir = task / runs;
+    const int row = static_cast<int>(ir % a.rows);
+    const int item = static_cast<int>(ir / a.rows);
+    const int b = item / per, hr = item % per;
+    const int h = hr / a.NRT, r = (hr % a.NRT) * a.RT + row;
+    if (r >= a.R) continue;
+    const int64_t f0 = a.first[b], nc = a.first[b + 1] - f0;
+    const size_t out_row = (static_cast<size_t>(b) * c.Hkv + h) * a.R + r;
+    uint16_t* out = a.o + out_row * D + (run * lanes + sub) * 4;
+    if (nc == 0) {
+      if (group == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
+      if (tid == 0 && run == 0) a.lse[out_row] = SWA_NEG_INF;
+      continue;
+    }
+    const int64_t x0 = f0 * per + hr * nc;
+    const int p0 = part_of(total, a.parts, x0), p1 = part_of(total, a.parts, x0 + nc - 1);
+    if (p0 == p1) continue;
+    // Row of part p's result, or -1: with fewer chunks than parts some parts hold nothing.
+    auto row_of = [&](int p) -> int64_t {
+      const int64_t from = part_start(total, a.parts, p);
+      if (from == part_start(total, a.parts, p + 1)) return -1;
+      return static_cast<int64_t>(partial_slot(p, from <= x0)) * a.rows + row;
+    };
+    float top = SWA_NEG_INF;
+    for (int p = p0 + tid; p <= p1; p += 256) {
+      const int64_t pr = row_of(p);
+      if (pr >= 0) top = fmaxf(top, a.ml[pr * 2]);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if ((tid & 31) == 0) s_red[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_red[w]);
+    const float base = top == SWA_NEG_INF ? 0.f : top;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = p0 + group; p <= p1; p += groups) {
+      const int64_t pr = row_of(p);
+      if (pr < 0) continue;
+      const float2 ml = *reinterpret_cast<const float2*>(a.ml + pr * 2);
+      const float4 y = *reinterpret_cast<const float4*>(a.po + pr * D + (run * lanes + sub) * 4);
+      const float w = ex2(ml.x - base);
+      l += w * ml.y;
+      o.x += w * y.x;
+      o.y += w * y.y;
+      o.z += w * y.z;
+      o.w += w * y.w;
+    }
+    if (sub == 0) s_l[group] = l;
+    s_o[tid] = o;
+    __syncthreads();
+    if (group == 0) {
+      l = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < groups; ++i) {
+        l += s_l[i];
+        const float4 y = s_o[i * lanes + sub];
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint2 pk;
+      if (a.f16) {
+        pk = make_uint2(Elem<true>::pack(o.x * inv, o.y * inv), Elem<true>::pack(o.z * inv, o.w * inv));
+      } else {
+        pk = make_uint2(Elem<false>::pack(o.x * inv, o.y * inv), Elem<false>::pack(o.z * inv, o.w * inv));
+      }
+      *reinterpret_cast<uint2*>(out) = pk;
+      if (tid == 0 && run == 0) a.lse[out_row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
+    }
+    __syncthreads();
+  }
+}
+
+// Adds to each cached token's weight the sum over its kv head's rows of 2^(score - lse / ln 2).  A
+// warp takes 4 chunks at a time (a lane finds one's place each), then each in turn with a lane per
+// key; one thread alone touches a weight.
+template <int D>
+__global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView c, const AttnDev a) {
+  using C = AttnCfg<D>;
+  constexpr int CK = C::CK, kSplit = 32 / CK;  // lanes that share a key
+  __shared__ int64_t s_first[kMaxSeqs + 1];
+  wait_predecessor();
+  for (int b = static_cast<int>(threadIdx.x); b <= c.B; b += 256) s_first[b] = a.first[b];
   __syncthreads();
-  float top = SWA_NEG_INF, sum = 0.f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  float f[kWarps];
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = s_l[w] == 0.f ? 0.f : (s_m[w] == top ? 1.f : expf(s_m[w] - top));
-    sum += s_l[w] * f[w];
+  const int lane = static_cast<int>(lane_id());
+  const int64_t tasks = s_first[c.B] * c.Hkv;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t y0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp_id()) * 4; y0 < tasks;
+       y0 += warps * 4) {
+    int64_t chunk = 0, stride = 0;
+    long long weight = -1;
+    int rows0 = 0;
+    if (lane < 4 && y0 + lane < tasks) {
+      const int64_t y = y0 + lane;
+      const int b = sequence_at(s_first, c.B, c.Hkv, y);
+      const int64_t f0 = s_first[b];
+      const int nc = static_cast<int>(s_first[b + 1] - f0);
+      const int64_t rem = y - f0 * c.Hkv;
+      const int h = static_cast<int>(rem / nc), cc = static_cast<int>(rem - static_cast<int64_t>(h) * nc);
+      const int slot = (first_chunk(c.lens[b], a.window, CK) + cc) * CK;
+      const int page = page_of(c, c.table, b, slot / c.page, c.max_pages);
+      if (page >= 0)
+        weight = (static_cast<long long>(page) * c.Hkv + h) * c.page + slot % c.page;
+      chunk = f0 * c.Hkv * a.NRT + static_cast<int64_t>(h) * a.NRT * nc + cc;
+      stride = nc;
+      rows0 = b * c.Hkv + h;
+    }
+    for (int j = 0; j < 4; ++j) {
+      const long long w = __shfl_sync(0xffffffffu, weight, j);
+      const int64_t x = __shfl_sync(0xffffffffu, chunk, j), nc = __shfl_sync(0xffffffffu, stride, j);
+      const int bh = __shfl_sync(0xffffffffu, rows0, j);
+      if (w < 0) continue;
+      float add = 0.f;
+      for (int rt = 0; rt < a.NRT; ++rt) {
+        const float* sc = a.scores + static_cast<size_t>(x + rt * nc) * a.rows * CK;
+        const float* lse = a.lse + static_cast<size_t>(bh) * a.R + rt * a.RT;
+        const int rows = min(a.rows, a.R - rt * a.RT);
+#pragma unroll 4
+        for (int r = lane / CK; r < rows; r += kSplit) {
+          const float z = lse[r];
+          // a row that sees nothing has scores and lse -inf, and adds nothing
+          add += ex2(sc[r * CK + lane % CK] - (z == SWA_NEG_INF ? 0.f : z * kLog2e));
+        }
+      }
+      if (kSplit == 2) add += __shfl_xor_sync(0xffffffffu, add, 16);
+      // Untouched unless something was seen: slots behind the sequence are left as they were.
+      if (lane < CK && add != 0.f) c.weight[w + lane] += add;
+    }
   }
-  for (int d = static_cast<int>(threadIdx.x); d < D; d += kWarps * 32) {
-    float acc = 0.f;
-    for (int w = 0; w < kWarps; ++w) acc += s_o[w][d] * f[w];
-    const float r = sum == 0.f ? 0.f : acc / sum;
-    static_cast<uint16_t*>(a.o)[row * D + d] =
-        static_cast<uint16_t>(Elem<F16>::pack(r, 0.f) & 0xffffu);
-  }
-  if (threadIdx.x == 0) a.lse[row] = sum == 0.f ? SWA_NEG_INF : top + logf(sum);
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(128)
-    swa_cache_weights_kernel(const CacheView c, const CacheAttnArgs a) {
-  const int h = static_cast<int>(blockIdx.y), b = static_cast<int>(blockIdx.z);
-  int len, n;
-  if (!sequence_of(c, b, &len, &n) || n == 0) return;
-  const int G = a.Hq / c.Hkv;
-  const long long at = static_cast<long long>(blockIdx.x) * 128 + threadIdx.x +
-                       max(0, len - a.window + 1) / 32 * 32;
-  if (at >= len + n) return;
-  const int s = static_cast<int>(at);
-  if (s + a.window <= len) return;  // no query sees it
-  const int page = page_of(c, c.table, b, s / c.page, c.max_pages);
-  if (page < 0) return;
-  const size_t block = static_cast<size_t>(page) * c.Hkv + h;
-  const uint8_t* key = c.k + (block * c.page + s % c.page) * D;
-  const float scale = a.scale * c.k_scale[block];
-  float add = 0.f;
-  for (int r = 0; r < G * n; ++r) {
-    const int g = r / n, t = r % n;
-    if (s > len + t || s + a.window <= len + t) continue;
-    const size_t row = (static_cast<size_t>(b) * a.Hq + h * G + g) * c.T + t;
-    float x = 0.f;
-    for (int d = 0; d < D; ++d) x = fmaf(q_value<D, F16>(a.q, row * D + d), e4m3_value(key[d]), x);
-    add += expf(x * scale - a.lse[row]);
+struct Plan {
+  int R, MT, RT, NRT, rows, parts, ck;
+  size_t off_ml, off_po, off_scores, bytes;
+};
+
+Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int accumulate) {
+  Plan p;
+  p.R = Hq / Hkv * T;
+  // A team covers as many rows as share its chunks: 16, 32 or 64.
+  p.MT = p.R <= 16 ? 1 : p.R <= 32 ? 2 : 4;
+  p.RT = 16 * p.MT;
+  p.NRT = (p.R + p.RT - 1) / p.RT;
+  p.rows = p.R < p.RT ? p.R : p.RT;
+  p.parts = sm_count() * (kWarps / p.MT);
+  p.ck = D == 256 ? AttnCfg<256>::CK : AttnCfg<128>::CK;
+  auto round = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  size_t off = round((kMaxSeqs + 1) * sizeof(int64_t));
+  p.off_ml = off;
+  off += round(static_cast<size_t>(2 * p.parts) * p.rows * 2 * sizeof(float));
+  p.off_po = off;
+  off += round(static_cast<size_t>(2 * p.parts) * p.rows * D * sizeof(float));
+  p.off_scores = off;
+  if (accumulate) {
+    const size_t chunks = static_cast<size_t>(max_pages) * page / p.ck;
+    off += static_cast<size_t>(B < kMaxSeqs ? B : kMaxSeqs) * Hkv * p.NRT * chunks * p.rows * p.ck *
+           sizeof(float);
   }
-  c.weight[block * c.page + s % c.page] += add;
+  p.bytes = round(off);
+  return p;
 }
 
-template <int D, bool F16>
-cudaError_t launch_d(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(c.T), static_cast<unsigned>(a.Hq),
-                  static_cast<unsigned>(c.B));
-  swa_cache_attn_kernel<D, F16><<<grid, kWarps * 32, 0, stream>>>(c, a);
-  if (a.accumulate) {
-    const long long most = static_cast<long long>(c.max_pages) * c.page;
-    const long long span = most < a.window + c.T + 32ll ? most : a.window + c.T + 32ll;
-    const dim3 wgrid(static_cast<unsigned>((span + 127) / 128), static_cast<unsigned>(c.Hkv),
-                     static_cast<unsigned>(c.B));
-    swa_cache_weights_kernel<D, F16><<<wgrid, 128, 0, stream>>>(c, a);
+// Launch that may begin while the kernel before it ends (it waits itself before it reads).
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, cudaStream_t stream,
+                         typename std::common_type<Args>::type... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D>
+cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream_t stream) {
+  using C = AttnCfg<D>;
+  const Plan p = plan_of(all.B, args.Hq, all.Hkv, all.T, D, all.max_pages, all.page,
+                         args.accumulate);
+  CUtensorMap tk, tv;
+  const uint64_t planes = static_cast<uint64_t>(all.pages) * all.Hkv;
+  if (!make_tmap_u8(&tk, all.k, planes, all.page, D, C::CK) ||
+      !make_tmap_u8(&tv, all.v, planes, all.page, D, C::CK))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(swa_cache_attn_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  uint8_t* ws = static_cast<uint8_t*>(args.workspace);
+  AttnDev a;
+  a.Hq = args.Hq;
+  a.G = args.Hq / all.Hkv;
+  a.R = p.R;
+  a.MT = p.MT;
+  a.RT = p.RT;
+  a.NRT = p.NRT;
+  a.rows = p.rows;
+  a.window = args.window;
+  a.parts = p.parts;
+  a.f16 = args.dtype == SWA_FP16;
+  a.scale_log2 = args.scale * kLog2e;
+  a.first = reinterpret_cast<int64_t*>(ws);
+  a.ml = reinterpret_cast<float*>(ws + p.off_ml);
+  a.po = reinterpret_cast<float*>(ws + p.off_po);
+  a.scores = args.accumulate ? reinterpret_cast<float*>(ws + p.off_scores) : nullptr;
+  for (int b0 = 0; b0 < all.B; b0 += kMaxSeqs) {
+    CacheView c = all;
+    c.B = all.B - b0 < kMaxSeqs ? all.B - b0 : kMaxSeqs;
+    c.table += static_cast<size_t>(b0) * all.max_pages;
+    c.lens += b0;
+    if (c.new_lens) c.new_lens += b0;
+    const size_t row0 = static_cast<size_t>(b0) * args.Hq * all.T;
+    a.q = static_cast<const uint16_t*>(args.q) + row0 * D;
+    a.o = static_cast<uint16_t*>(args.o) + row0 * D;
+    a.lse = args.lse + row0;
+    swa_cache_attn_kernel<D><<<p.parts / (kWarps / p.MT), kThreads, C::kSmemBytes, stream>>>(
+        tk, tv, c, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // Runs of 128 columns a warp, or of 16 when there are too few rows to fill the SMs.
+    const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv * p.NRT * p.rows;
+    const int lanes = rows * (D / 4 / (D == 64 ? 16 : 32)) >= 4 * 152 ? (D == 64 ? 16 : 32) : 4;
+    const int64_t tasks = rows * (D / 4 / lanes);
+    const unsigned grid = static_cast<unsigned>(tasks < 152 * 8 ? tasks : 152 * 8);
+    if ((e = launch_after(swa_cache_join_kernel<D>, grid, stream, c, a, lanes)) != cudaSuccess)
+      return e;
+    if (args.accumulate) {
+      // At most this many chunks of 4 warps' turns; the kernel walks what there really is.
+      const int64_t most = (static_cast<int64_t>(all.max_pages) * all.page / C::CK) * c.B * c.Hkv;
+      const int64_t blocks = (most + 31) / 32;
+      const unsigned wgrid = static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8);
+      if ((e = launch_after(swa_cache_weights_kernel<D>, wgrid, stream, c, a)) != cudaSuccess)
+        return e;
+    }
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace
 
-size_t cache_attn_workspace_bytes(int, int, int, int, int, int, int, int) { return 0; }
+size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
+                                  int accumulate) {
+  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate).bytes;
+}
 
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream) {
-  const bool f16 = a.dtype == SWA_FP16;
-  if (c.D == 64) return f16 ? launch_d<64, true>(c, a, stream) : launch_d<64, false>(c, a, stream);
-  if (c.D == 128)
-    return f16 ? launch_d<128, true>(c, a, stream) : launch_d<128, false>(c, a, stream);
-  return f16 ? launch_d<256, true>(c, a, stream) : launch_d<256, false>(c, a, stream);
+  if (c.D == 64) return launch_d<64>(c, a, stream);
+  if (c.D == 128) return launch_d<128>(c, a, stream);
+  return launch_d<256>(c, a, stream);
 }
 
 }  // namespace swa

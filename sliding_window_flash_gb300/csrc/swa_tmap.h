@@ -46,4 +46,21 @@ inline bool make_tmap_3d(CUtensorMap* map, const void* base, uint64_t bh, uint64
   return r == CUDA_SUCCESS;
 }
 
+// Tensor map over 8-bit planes [planes][rows][cols] (cols innermost, 64, 128 or 256), loaded in boxes
+// of `box_rows` rows x min(cols, 128) bytes with a swizzle as wide as the box.
+inline bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t planes, uint64_t rows,
+                         uint64_t cols, uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {cols, rows * cols};  // bytes, dims 1 and 2
+  cuuint32_t box[3] = {cols < 128 ? static_cast<cuuint32_t>(cols) : 128u, box_rows, 1u};
+  cuuint32_t estride[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                   box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   cols < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace swa
