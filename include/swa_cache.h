@@ -126,11 +126,17 @@ swa_status swa_cache_evict(const swa_cache* cache, const int* table, int max_pag
  *                   exp(scale <q_i, k_j> - lse_i).
  *   q [B, Hq, Lq, D], k [B, Hkv, Lk, D] in bf16 or fp16 (`dtype`), lse fp32 [B, Hq, Lq],
  *   w fp32 [B, Hkv, Lk], fully written; shapes, window and causal as in swa_attn_fwd_ex.
- * The N x N weights are never stored.  Bit-reproducible.
+ *   workspace : at least swa_attn_key_weights_workspace_bytes bytes (0 for many keys: it may then be
+ *               NULL), 16-byte aligned; nothing is kept there between calls.  Calls that may overlap
+ *               need workspaces of their own.
+ * The N x N weights are never stored; scores, exponentials and sums are fp32.  Bit-reproducible.
  */
+size_t swa_attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D,
+                                            int window, int causal);
 swa_status swa_attn_key_weights(const void* q, const void* k, const float* lse, float* w, int B,
                                 int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
-                                float scale, int dtype, cudaStream_t stream);
+                                float scale, int dtype, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -45,11 +45,13 @@ __all__ = [
     "swa_cache_attn_workspace_bytes",
     "swa_cache_evict",
     "swa_attn_key_weights",
+    "swa_attn_key_weights_workspace_bytes",
 ]
 
 from . import cache as _cache
-from .cache import (SwaCache, swa_attn_key_weights, swa_cache_append, swa_cache_attn,
-                    swa_cache_attn_workspace_bytes, swa_cache_evict)
+from .cache import (SwaCache, swa_attn_key_weights, swa_attn_key_weights_workspace_bytes,
+                    swa_cache_append, swa_cache_attn, swa_cache_attn_workspace_bytes,
+                    swa_cache_evict)
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libswa.so"

@@ -30,6 +30,7 @@ __all__ = [
     "swa_cache_attn_workspace_bytes",
     "swa_cache_evict",
     "swa_attn_key_weights",
+    "swa_attn_key_weights_workspace_bytes",
 ]
 
 
@@ -52,13 +53,35 @@ SIGNATURES = {
     ),
     "swa_cache_evict": (
         _c_int, [_cp, _vp, _c_int, _vp, _vp] + [_c_int] * 3 + [_vp, _vp, _c_int, _vp]),
-    "swa_attn_key_weights": (_c_int, [_vp] * 4 + [_c_int] * 8 + [_c_float, _c_int, _vp]),
+    "swa_attn_key_weights_workspace_bytes": (ctypes.c_size_t, [_c_int] * 8),
+    "swa_attn_key_weights": (
+        _c_int, [_vp] * 4 + [_c_int] * 8 + [_c_float, _c_int, _vp, ctypes.c_size_t, _vp]),
 }
 
 
+_entries = {}
+
+
+def _entry(name):
+    """The library's entry point, loaded on first use."""
+    fn = _entries.get(name)
+    if fn is None:
+        from . import load
+
+        fn = _entries[name] = getattr(load(), name)
+    return fn
+
+
 def _check(t, name, shape, dtype, device):
+    """Raises unless t is a contiguous CUDA tensor of this shape and dtype, on `device` if given."""
     import torch
 
+    try:  # a good tensor costs four attribute reads
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and \
+                (t.is_cuda if device is None else t.get_device() == device.index):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -69,8 +92,7 @@ def _check(t, name, shape, dtype, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 class SwaCache:
@@ -157,19 +179,26 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _space(workspace):
+    """(address, bytes) of a workspace tensor."""
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _run(name, device, *args):
     """Calls entry point `name` on the device's current stream, with that device current."""
     import torch
 
-    from . import SwaError, load
-
-    fn = getattr(load(), name)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        rc = _entry(name)(*args, stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = _entry(name)(*args, stream)
     if rc != 0:
+        from . import SwaError
+
         raise SwaError(rc, name)
 
 
@@ -210,10 +239,8 @@ def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) 
 
 def swa_cache_attn_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, max_pages: int,
                                    page: int, accumulate: bool = False) -> int:
-    from . import load
-
-    return int(load().swa_cache_attn_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page,
-                                                     int(bool(accumulate))))
+    return int(_entry("swa_cache_attn_workspace_bytes")(B, Hq, Hkv, T, D, max_pages, page,
+                                                        int(bool(accumulate))))
 
 
 def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional[float] = None,
@@ -228,8 +255,6 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     swa_cache_attn_workspace_bytes) is allocated here unless given.
     """
     import torch
-
-    from . import load
 
     B, width = _tables(cache, table, lens, new)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
@@ -246,15 +271,14 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
         lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
     else:
         _check(lse, "lse", (B, Hq, T), torch.float32, cache.device)
-    need = load().swa_cache_attn_workspace_bytes(B, Hq, Hkv, T, D, width, page,
-                                                 int(bool(accumulate)))
-    if workspace is None and need:
+    if workspace is None:
+        need = _entry("swa_cache_attn_workspace_bytes")(B, Hq, Hkv, T, D, width, page,
+                                                        int(bool(accumulate)))
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size())
     _run("swa_cache_attn", cache.device, cache._c(), table.data_ptr(), width, lens.data_ptr(),
          _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, _window(window),
-         1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(accumulate)), dt, *ws)
+         1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(accumulate)), dt,
+         *_space(workspace))
     return out, lse
 
 
@@ -288,15 +312,22 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
     return kept, lens_out
 
 
+def swa_attn_key_weights_workspace_bytes(B: int, Hq: int, Hkv: int, Lq: int, Lk: int, D: int,
+                                         window: int, causal: bool = True) -> int:
+    return int(_entry("swa_attn_key_weights_workspace_bytes")(B, Hq, Hkv, Lq, Lk, D,
+                                                              _window(window), int(bool(causal))))
+
+
 def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, causal: bool = True,
-                         out=None):
+                         out=None, workspace=None):
     """The attention weight every key of a prompt received: fp32 [B,Hkv,Lk], the sum over the query
     heads of its kv head and the queries that see it of exp(scale <q, k> - lse).  q [B,Hq,Lq,D] and
     k [B,Hkv,Lk,D] in bf16 or fp16, lse [B,Hq,Lq] as swa_attn_fwd returned it for the same window,
-    scale and causal."""
+    scale and causal.  The workspace (of swa_attn_key_weights_workspace_bytes) is allocated here
+    unless given."""
     import torch
 
-    for t, name in ((q, "q"), (k, "k")):
+    for t in (q, k):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError("q and k must be 4-D [B, H, L, D]")
     dt = _dtype(q, "q")
@@ -310,7 +341,12 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
         out = torch.empty((B, Hkv, Lk), dtype=torch.float32, device=dev)
     else:
         _check(out, "out", (B, Hkv, Lk), torch.float32, dev)
+    window, causal = _window(window), int(bool(causal))
+    if workspace is None:
+        need = _entry("swa_attn_key_weights_workspace_bytes")(B, Hq, Hkv, Lq, Lk, D, window, causal)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _run("swa_attn_key_weights", dev, q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(), B,
-         Hq, Hkv, Lq, Lk, D, _window(window), int(bool(causal)),
-         1.0 / math.sqrt(D) if scale is None else float(scale), dt)
+         Hq, Hkv, Lq, Lk, D, window, causal, 1.0 / math.sqrt(D) if scale is None else float(scale),
+         dt, *_space(workspace))
     return out

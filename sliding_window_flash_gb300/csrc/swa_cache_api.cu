@@ -52,6 +52,38 @@ swa::CacheView view(const swa_cache* c, const int* table, int max_pages, const i
   return v;
 }
 
+swa_status check_key_weights(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
+                             float scale) {
+  if (causal != 0 && causal != 1) return SWA_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lq < 1 || Lk < Lq || window < 1)
+    return SWA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return SWA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128 && D != 256) return SWA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hq * Lq >= kIndexLimit ||
+      static_cast<long long>(B) * Hkv * Lk >= kIndexLimit)
+    return SWA_ERR_INVALID_ARG;
+  return SWA_OK;
+}
+
+swa::Problem key_weights_problem(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window,
+                                 int causal, float scale, int f16, unsigned* err) {
+  swa::Problem pb;
+  pb.B = B;
+  pb.Hq = Hq;
+  pb.Hkv = Hkv;
+  pb.D = D;
+  const int W = window < Lk ? window : Lk;
+  pb.span.Lq = Lq;
+  pb.span.Lk = Lk;
+  pb.span.off = Lk - Lq;
+  pb.span.dmin = causal ? 0 : -(W - 1);
+  pb.span.dmax = W - 1;
+  pb.scale = scale;
+  pb.err = err;
+  pb.f16 = f16;
+  return pb;
+}
+
 }  // namespace
 
 extern "C" {
@@ -145,39 +177,32 @@ swa_status swa_cache_evict(const swa_cache* cache, const int* table, int max_pag
   return swa::launch_cache_evict(c, a, stream) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
+size_t swa_attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D,
+                                            int window, int causal) {
+  if (check_key_weights(B, Hq, Hkv, Lq, Lk, D, window, causal, 1.f) != SWA_OK) return 0;
+  return swa::key_weights_workspace_bytes(
+      key_weights_problem(B, Hq, Hkv, Lq, Lk, D, window, causal, 1.f, 0, nullptr));
+}
+
 swa_status swa_attn_key_weights(const void* q, const void* k, const float* lse, float* w, int B,
                                 int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
-                                float scale, int dtype, cudaStream_t stream) {
-  if (!q || !k || !lse || !w) return SWA_ERR_INVALID_ARG;
-  if ((causal != 0 && causal != 1) || (dtype != SWA_BF16 && dtype != SWA_FP16))
+                                float scale, int dtype, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream) {
+  if (!q || !k || !lse || !w || (dtype != SWA_BF16 && dtype != SWA_FP16))
     return SWA_ERR_INVALID_ARG;
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Lq < 1 || Lk < Lq || window < 1)
-    return SWA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return SWA_ERR_INVALID_ARG;
-  if (D != 64 && D != 128 && D != 256) return SWA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(B) * Hq * Lq >= kIndexLimit ||
-      static_cast<long long>(B) * Hkv * Lk >= kIndexLimit)
-    return SWA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 16) || !aligned(w, 16))
-    return SWA_ERR_MISALIGNED;
-  unsigned* err = nullptr;
-  swa_status st = swa::device_error_word(&err);
+  swa_status st = check_key_weights(B, Hq, Hkv, Lq, Lk, D, window, causal, scale);
   if (st != SWA_OK) return st;
-  swa::Problem pb;
-  pb.B = B;
-  pb.Hq = Hq;
-  pb.Hkv = Hkv;
-  pb.D = D;
-  const int W = window < Lk ? window : Lk;
-  pb.span.Lq = Lq;
-  pb.span.Lk = Lk;
-  pb.span.off = Lk - Lq;
-  pb.span.dmin = causal ? 0 : -(W - 1);
-  pb.span.dmax = W - 1;
-  pb.scale = scale;
-  pb.err = err;
-  pb.f16 = dtype == SWA_FP16;
-  return swa::launch_key_weights(pb, q, k, lse, w, stream) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+  swa::Problem pb = key_weights_problem(B, Hq, Hkv, Lq, Lk, D, window, causal, scale,
+                                        dtype == SWA_FP16, nullptr);
+  const size_t need = swa::key_weights_workspace_bytes(pb);
+  if (need != 0 && (!workspace || workspace_bytes < need)) return SWA_ERR_WORKSPACE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 16) || !aligned(w, 16) ||
+      !aligned(workspace, 16))
+    return SWA_ERR_MISALIGNED;
+  if ((st = swa::device_error_word(&pb.err)) != SWA_OK) return st;
+  return swa::launch_key_weights(pb, q, k, lse, w, workspace, stream) == cudaSuccess
+             ? SWA_OK
+             : SWA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -93,7 +93,8 @@ struct CacheEvictArgs {
 };
 cudaError_t launch_cache_evict(const CacheView& c, const CacheEvictArgs& a, cudaStream_t stream);
 
+size_t key_weights_workspace_bytes(const Problem& pb);
 cudaError_t launch_key_weights(const Problem& pb, const void* q, const void* k, const float* lse,
-                               float* w, cudaStream_t stream);
+                               float* w, void* workspace, cudaStream_t stream);
 
 }  // namespace swa

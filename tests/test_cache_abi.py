@@ -125,8 +125,9 @@ def test_evict_refusals(lib, kw, code):
 
 
 def _weights(lib, q=FAKE, k=FAKE, lse=FAKE, w=FAKE, B=1, Hq=4, H=2, Lq=16, Lk=20, D=64, W=4,
-             causal=1, scale=0.1, dtype=0):
-    return lib.swa_attn_key_weights(q, k, lse, w, B, Hq, H, Lq, Lk, D, W, causal, scale, dtype, None)
+             causal=1, scale=0.1, dtype=0, ws=FAKE, ws_bytes=1 << 40):
+    return lib.swa_attn_key_weights(q, k, lse, w, B, Hq, H, Lq, Lk, D, W, causal, scale, dtype, ws,
+                                    ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -137,6 +138,21 @@ def _weights(lib, q=FAKE, k=FAKE, lse=FAKE, w=FAKE, B=1, Hq=4, H=2, Lq=16, Lk=20
 ])
 def test_key_weights_refusals(lib, kw, code):
     assert _weights(lib, **kw) == code
+
+
+def test_key_weights_workspace(lib):
+    size = lib.swa_attn_key_weights_workspace_bytes
+    need = size(1, 4, 2, 600, 700, 64, 4, 1)
+    pieces = need / (2 * 700 * 4)
+    assert pieces >= 2 and need % 256 == 0
+    big = dict(Lq=600, Lk=700)
+    assert _weights(lib, ws_bytes=need - 1, **big) == 6
+    assert _weights(lib, ws=0, **big) == 6 and _weights(lib, ws=FAKE + 8, **big) == 3
+    for bad in ((0, 4, 2, 16, 20, 64, 4, 1), (1, 3, 2, 16, 20, 64, 4, 1), (1, 4, 2, 21, 20, 64, 4, 1),
+                (1, 4, 2, 16, 20, 96, 4, 1), (1, 4, 2, 16, 20, 64, 0, 1), (1, 4, 2, 16, 20, 64, 4, 2)):
+        assert size(*bad) == 0
+    # one walk per block of keys needs none
+    assert size(1, 32, 16, 1 << 20, 1 << 20, 128, 1024, 1) == 0
 
 
 def test_binding_refuses_what_is_not_on_the_gpu():
