@@ -49,11 +49,6 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
-}
-
 // 2^e for the least e in range with amax <= 448 2^e = 1.75 2^(e + 8); `bits` is amax as fp32 bits.
 __device__ __forceinline__ float scale_for(uint32_t bits) {
   int e = static_cast<int>(bits >> 23) - 127 - 8;  // subnormal amax: far below the range's end
@@ -144,9 +139,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     if (ratio == 1.f) continue;
     uint32_t* codes = reinterpret_cast<uint32_t*>((w == 0 ? c.k : c.v) + block * c.page * D);
     for (int i = static_cast<int>(threadIdx.x); i < first * D / 4; i += kAppendThreads) {
-      const uint32_t u = codes[i];
-      codes[i] = e4m3x4(e4m3_value(u & 0xffu) * ratio, e4m3_value((u >> 8) & 0xffu) * ratio,
-                        e4m3_value((u >> 16) & 0xffu) * ratio, e4m3_value(u >> 24) * ratio);
+      codes[i] = e4m3x4_times(codes[i], half2_of(ratio));
     }
   }
   for (int r = first + row0; r < last; r += kRows) {

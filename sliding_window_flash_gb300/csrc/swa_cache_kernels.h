@@ -2,6 +2,7 @@
 // their kernels, and the device helpers those kernels share.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -65,6 +66,29 @@ __device__ __forceinline__ int page_of(const CacheView& c, const int* table, int
   if (p >= 0 && p < c.pages) return p;
   raise_index_error(c);
   return -1;
+}
+
+// Four e4m3 codes times `ratio` (two equal halves), a power of two of at most 1, rounded to nearest
+// even.  fp16 holds codes exactly, and a product that it rounds (below 2^-20) is zero as a code; a
+// ratio that it rounds to zero takes every code below half the least one.
+__device__ __forceinline__ uint32_t e4m3x4_times(uint32_t codes, uint32_t ratio) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\t.reg .b32 x, y;\n\t"
+      "mov.b32 {a, b}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, b;\n\t"
+      "mul.rn.f16x2 x, x, %2;\n\t"
+      "mul.rn.f16x2 y, y, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 b, y;\n\t"
+      "mov.b32 %0, {a, b};\n\t}"
+      : "=r"(r)
+      : "r"(codes), "r"(ratio));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_of(float x) {
+  const __half2 h = __float2half2_rn(x);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 #endif  // __CUDACC__

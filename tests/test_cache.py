@@ -496,3 +496,31 @@ def test_serving_step_in_a_graph(swa):
         assert torch.equal(out, eager[i][0]) and torch.equal(lse, eager[i][1]), i
     assert torch.equal(weight, cache.weight)
     swa.swa_check_device()
+
+
+@pytest.mark.parametrize("B,H,page,longest,budget,recent", [
+    (1, 2, 64, 70000, 3000, 100),   # a cluster of eight CTAs
+    (9, 16, 32, 5000, 700, 0),      # one or two
+    (1, 1, 128, 450000, 777, 77),   # slices larger than shared memory holds
+])
+def test_evict_long(swa, B, H, page, longest, budget, recent):
+    """Long sequences against torch's stable sort: the chosen slots, and the weights moved with them."""
+    g = _gen(longest)
+    D = 64
+    width, room = -(-longest // page), -(-budget // page)
+    cache = _cache(swa, g, B * (width + room), H, D, page)
+    cache.weight.copy_(torch.round(cache.weight * 512) / 512)
+    order = _table(g, B, width + room)
+    table, dst = order[:, :width].contiguous(), order[:, width:].contiguous()
+    lens = [longest - 37 * b for b in range(B)]
+    w = cache.weight[table.long()].transpose(1, 2).reshape(B, H, -1).clone()
+    kept, out = swa.swa_cache_evict(cache, table, _ints(lens), dst, budget, recent)
+    swa.swa_check_device()
+    assert out.tolist() == [min(n, budget) for n in lens]
+    for b, n in enumerate(lens):
+        best = torch.sort(w[b, :, :n - recent], dim=-1, descending=True, stable=True).indices
+        want = torch.sort(best[:, :budget - recent], dim=-1).values
+        want = torch.cat([want, torch.arange(n - recent, n, device="cuda").expand(H, -1)], 1)
+        assert torch.equal(kept[b].long(), want)
+        moved = cache.weight[dst[b].long()].transpose(0, 1).reshape(H, -1)[:, :budget]
+        assert torch.equal(moved, torch.gather(w[b], 1, want))
