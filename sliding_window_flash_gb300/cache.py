@@ -20,6 +20,7 @@ and reported by swa_check_device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -72,16 +73,20 @@ def _entry(name):
     return fn
 
 
+def _good(t, shape, dtype, index):
+    """Whether t is a contiguous tensor of this shape and dtype on GPU `index`: the few reads that a
+    good tensor costs on every call."""
+    try:
+        return (t.dtype is dtype and t.get_device() == index and t.shape == shape and
+                t.is_contiguous())
+    except AttributeError:
+        return False
+
+
 def _check(t, name, shape, dtype, device):
     """Raises unless t is a contiguous CUDA tensor of this shape and dtype, on `device` if given."""
     import torch
 
-    try:  # a good tensor costs four attribute reads
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and \
-                (t.is_cuda if device is None else t.get_device() == device.index):
-            return
-    except AttributeError:
-        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -92,7 +97,8 @@ def _check(t, name, shape, dtype, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 class SwaCache:
@@ -101,20 +107,24 @@ class SwaCache:
     The tensors are the caller's; this object only holds and checks them.  page is 32, 64 or 128,
     D 64, 128 or 256."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "weight", "device")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "weight", "device", "shape")
 
     def __init__(self, k, v, k_scale, v_scale, weight=None):
         import torch
 
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be a 4-D tensor [pages, Hkv, page, D]")
-        dev = k.device
-        _check(k, "k", k.shape, torch.float8_e4m3fn, None)
-        _check(v, "v", k.shape, torch.float8_e4m3fn, dev)
-        _check(k_scale, "k_scale", k.shape[:2], torch.float32, dev)
-        _check(v_scale, "v_scale", k.shape[:2], torch.float32, dev)
-        if weight is not None:
-            _check(weight, "weight", k.shape[:3], torch.float32, dev)
+        dev, shape = k.device, tuple(k.shape)
+        f8, f32, index = torch.float8_e4m3fn, torch.float32, dev.index
+        if not (index is not None and _good(k, shape, f8, index) and _good(v, shape, f8, index) and
+                _good(k_scale, shape[:2], f32, index) and _good(v_scale, shape[:2], f32, index) and
+                (weight is None or _good(weight, shape[:3], f32, index))):
+            _check(k, "k", shape, f8, None)
+            _check(v, "v", shape, f8, dev)
+            _check(k_scale, "k_scale", shape[:2], f32, dev)
+            _check(v_scale, "v_scale", shape[:2], f32, dev)
+            if weight is not None:
+                _check(weight, "weight", shape[:3], f32, dev)
         put = object.__setattr__
         put(self, "k", k)
         put(self, "v", v)
@@ -122,6 +132,7 @@ class SwaCache:
         put(self, "v_scale", v_scale)
         put(self, "weight", weight)
         put(self, "device", dev)
+        put(self, "shape", shape)
 
     def __setattr__(self, name, value):
         raise AttributeError("a SwaCache's tensors are fixed; make another for other tensors")
@@ -145,29 +156,32 @@ class SwaCache:
 
     @property
     def page(self) -> int:
-        return self.k.shape[2]
+        return self.shape[2]
 
     def _c(self):
-        P, H, S, D = self.k.shape
+        P, H, S, D = self.shape
         w = self.weight
         return _CCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
                        self.v_scale.data_ptr(), None if w is None else w.data_ptr(), P, H, S, D)
 
 
 def _tables(cache, table, lens, new):
-    """(B, max_pages) after checking the int32 tables of a call."""
+    """(B, max_pages, GPU index) after checking the int32 tables of a call."""
     import torch
 
-    if not isinstance(cache, SwaCache):
+    if type(cache) is not SwaCache:
         raise TypeError("cache must be a SwaCache")
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a 2-D tensor [B, max_pages]")
-    B, width = table.shape
-    _check(table, "table", table.shape, torch.int32, cache.device)
-    _check(lens, "lens", (B,), torch.int32, cache.device)
-    if new is not None:
-        _check(new, "new", (B,), torch.int32, cache.device)
-    return B, width
+    shape, index, i32 = tuple(table.shape), cache.device.index, torch.int32
+    B = shape[:1]
+    if not (_good(table, shape, i32, index) and _good(lens, B, i32, index) and
+            (new is None or _good(new, B, i32, index))):
+        _check(table, "table", shape, i32, cache.device)
+        _check(lens, "lens", B, i32, cache.device)
+        if new is not None:
+            _check(new, "new", B, i32, cache.device)
+    return shape[0], shape[1], index
 
 
 def _window(window):
@@ -186,15 +200,15 @@ def _space(workspace):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _run(name, device, *args):
-    """Calls entry point `name` on the device's current stream, with that device current."""
+def _run(name, index, *args):
+    """Calls entry point `name` on the current stream of GPU `index`, with that GPU current."""
     import torch
 
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch.cuda.current_device():
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
         rc = _entry(name)(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = _entry(name)(*args, stream)
     if rc != 0:
         from . import SwaError
@@ -205,13 +219,15 @@ def _run(name, device, *args):
 def _dtype(t, name, fp32=False):
     import torch
 
-    code = {torch.bfloat16: 0, torch.float16: 1}.get(t.dtype)
-    if code is None and fp32 and t.dtype == torch.float32:
-        code = 2
-    if code is None:
-        raise TypeError(f"{name} must be bfloat16{', float16 or float32' if fp32 else ' or float16'},"
-                        f" got {t.dtype}")
-    return code
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return 0
+    if dt is torch.float16:
+        return 1
+    if fp32 and dt is torch.float32:
+        return 2
+    raise TypeError(f"{name} must be bfloat16{', float16 or float32' if fp32 else ' or float16'}, "
+                    f"got {dt}")
 
 
 def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) -> None:
@@ -223,24 +239,35 @@ def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) 
     """
     import torch
 
-    B, width = _tables(cache, table, lens, new)
+    B, width, index = _tables(cache, table, lens, new)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a 4-D tensor [B, Hkv, T, D]")
-    dt = _dtype(k, "k", fp32=True)
+    dt, kind = _dtype(k, "k", fp32=True), k.dtype
     T = k.shape[2]
-    shape = (B, cache.k.shape[1], T, cache.k.shape[3])
-    _check(k, "k", shape, k.dtype, cache.device)
-    _check(v, "v", shape, k.dtype, cache.device)
-    if weight is not None:
-        _check(weight, "weight", shape[:3], torch.float32, cache.device)
-    _run("swa_cache_append", cache.device, cache._c(), table.data_ptr(), width, lens.data_ptr(),
+    shape = (B, cache.shape[1], T, cache.shape[3])
+    if not (_good(k, shape, kind, index) and _good(v, shape, kind, index) and
+            (weight is None or _good(weight, shape[:3], torch.float32, index))):
+        _check(k, "k", shape, kind, cache.device)
+        _check(v, "v", shape, kind, cache.device)
+        if weight is not None:
+            _check(weight, "weight", shape[:3], torch.float32, cache.device)
+    _run("swa_cache_append", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
          _ptr(new), k.data_ptr(), v.data_ptr(), _ptr(weight), B, T, dt)
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_space(*sizes):
+    return int(_entry("swa_cache_attn_workspace_bytes")(*sizes))
+
+
+@functools.lru_cache(maxsize=256)
+def _weights_space(*sizes):
+    return int(_entry("swa_attn_key_weights_workspace_bytes")(*sizes))
 
 
 def swa_cache_attn_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, max_pages: int,
                                    page: int, accumulate: bool = False) -> int:
-    return int(_entry("swa_cache_attn_workspace_bytes")(B, Hq, Hkv, T, D, max_pages, page,
-                                                        int(bool(accumulate))))
+    return _attn_space(B, Hq, Hkv, T, D, max_pages, page, int(bool(accumulate)))
 
 
 def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional[float] = None,
@@ -256,26 +283,27 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     """
     import torch
 
-    B, width = _tables(cache, table, lens, new)
+    B, width, index = _tables(cache, table, lens, new)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a 4-D tensor [B, Hq, T, D]")
-    dt = _dtype(q, "q")
-    _, Hkv, page, D = cache.k.shape
-    Hq, T = q.shape[1], q.shape[2]
-    _check(q, "q", (B, Hq, T, D), q.dtype, cache.device)
+    dt, kind, f32 = _dtype(q, "q"), q.dtype, torch.float32
+    _, Hkv, page, D = cache.shape
+    _, Hq, T, _ = q.shape
+    shape = (B, Hq, T, D)
+    if not _good(q, shape, kind, index):
+        _check(q, "q", shape, kind, cache.device)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _check(out, "out", (B, Hq, T, D), q.dtype, cache.device)
+    elif not _good(out, shape, kind, index):
+        _check(out, "out", shape, kind, cache.device)
     if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
-    else:
-        _check(lse, "lse", (B, Hq, T), torch.float32, cache.device)
+        lse = q.new_empty(shape[:3], dtype=f32)
+    elif not _good(lse, shape[:3], f32, index):
+        _check(lse, "lse", shape[:3], f32, cache.device)
     if workspace is None:
-        need = _entry("swa_cache_attn_workspace_bytes")(B, Hq, Hkv, T, D, width, page,
-                                                        int(bool(accumulate)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
-    _run("swa_cache_attn", cache.device, cache._c(), table.data_ptr(), width, lens.data_ptr(),
+        need = _attn_space(B, Hq, Hkv, T, D, width, page, int(bool(accumulate)))
+        workspace = q.new_empty(need, dtype=torch.uint8)
+    _run("swa_cache_attn", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
          _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, _window(window),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(accumulate)), dt,
          *_space(workspace))
@@ -290,32 +318,32 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
     (kept [B,Hkv,budget] int32: their old slots, -1 behind the last; lens_out [B] int32)."""
     import torch
 
-    B, width = _tables(cache, table, lens, None)
+    B, width, index = _tables(cache, table, lens, None)
     if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
         raise ValueError("dst_table must be a 2-D tensor [B, dst_pages]")
-    _check(dst_table, "dst_table", (B, dst_table.shape[1]), torch.int32, cache.device)
-    Hkv = cache.k.shape[1]
-    shape = (B, Hkv, int(budget))
-    if int(budget) < 1:
+    budget, i32 = int(budget), torch.int32
+    if budget < 1:
         raise ValueError("budget must be at least 1")
+    room = (B, dst_table.shape[1])
+    if not _good(dst_table, room, i32, index):
+        _check(dst_table, "dst_table", room, i32, cache.device)
+    shape = (B, cache.shape[1], budget)
     if kept is None:
-        kept = torch.empty(shape, dtype=torch.int32, device=cache.device)
-    else:
-        _check(kept, "kept", shape, torch.int32, cache.device)
+        kept = table.new_empty(shape)
+    elif not _good(kept, shape, i32, index):
+        _check(kept, "kept", shape, i32, cache.device)
     if lens_out is None:
-        lens_out = torch.empty((B,), dtype=torch.int32, device=cache.device)
-    else:
-        _check(lens_out, "lens_out", (B,), torch.int32, cache.device)
-    _run("swa_cache_evict", cache.device, cache._c(), table.data_ptr(), width, lens.data_ptr(),
-         dst_table.data_ptr(), dst_table.shape[1], int(budget), int(recent), kept.data_ptr(),
-         lens_out.data_ptr(), B)
+        lens_out = torch.empty_like(lens)
+    elif not _good(lens_out, (B,), i32, index):
+        _check(lens_out, "lens_out", (B,), i32, cache.device)
+    _run("swa_cache_evict", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
+         dst_table.data_ptr(), room[1], budget, int(recent), kept.data_ptr(), lens_out.data_ptr(), B)
     return kept, lens_out
 
 
 def swa_attn_key_weights_workspace_bytes(B: int, Hq: int, Hkv: int, Lq: int, Lk: int, D: int,
                                          window: int, causal: bool = True) -> int:
-    return int(_entry("swa_attn_key_weights_workspace_bytes")(B, Hq, Hkv, Lq, Lk, D,
-                                                              _window(window), int(bool(causal))))
+    return _weights_space(B, Hq, Hkv, Lq, Lk, D, _window(window), int(bool(causal)))
 
 
 def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, causal: bool = True,
@@ -330,23 +358,26 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
     for t in (q, k):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError("q and k must be 4-D [B, H, L, D]")
-    dt = _dtype(q, "q")
+    dt, kind, f32 = _dtype(q, "q"), q.dtype, torch.float32
     B, Hq, Lq, D = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
     dev = q.device
-    _check(q, "q", q.shape, q.dtype, None)
-    _check(k, "k", (B, Hkv, Lk, D), q.dtype, dev)
-    _check(lse, "lse", (B, Hq, Lq), torch.float32, dev)
+    index = dev.index
+    if not (index is not None and _good(q, q.shape, kind, index) and
+            _good(k, (B, Hkv, Lk, D), kind, index) and _good(lse, (B, Hq, Lq), f32, index)):
+        _check(q, "q", q.shape, kind, None)
+        _check(k, "k", (B, Hkv, Lk, D), kind, dev)
+        _check(lse, "lse", (B, Hq, Lq), f32, dev)
     if out is None:
-        out = torch.empty((B, Hkv, Lk), dtype=torch.float32, device=dev)
-    else:
-        _check(out, "out", (B, Hkv, Lk), torch.float32, dev)
+        out = lse.new_empty((B, Hkv, Lk))
+    elif not _good(out, (B, Hkv, Lk), f32, index):
+        _check(out, "out", (B, Hkv, Lk), f32, dev)
     window, causal = _window(window), int(bool(causal))
     if workspace is None:
-        need = _entry("swa_attn_key_weights_workspace_bytes")(B, Hq, Hkv, Lq, Lk, D, window, causal)
+        need = _weights_space(B, Hq, Hkv, Lq, Lk, D, window, causal)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _run("swa_attn_key_weights", dev, q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(), B,
+            workspace = q.new_empty(need, dtype=torch.uint8)
+    _run("swa_attn_key_weights", index, q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(), B,
          Hq, Hkv, Lq, Lk, D, window, causal, 1.0 / math.sqrt(D) if scale is None else float(scale),
          dt, *_space(workspace))
     return out

@@ -48,7 +48,8 @@ struct AttnCfg {
   static constexpr int kQBytes = D == 256 ? kWarps * 16 * D * 2 : 0;
   static constexpr int kRing = kStages - kQBytes / kStageBytes;
   static constexpr int kOffFirst = kRing * kStageBytes + kQBytes;
-  static constexpr int kOffBar = kOffFirst + (kMaxSeqs + 1) * 8;
+  static constexpr int kOffLen = kOffFirst + (kMaxSeqs + 2) * 8;  // lengths, then new tokens
+  static constexpr int kOffBar = kOffLen + 2 * kMaxSeqs * 4;
   static constexpr int kOffSums = kOffBar + 2 * kStages * 8 + 16;  // + abort flag
   static constexpr int kSmemBytes = kOffSums + kWarps * 8;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -61,7 +62,8 @@ struct AttnDev {
   int Hq, G, R;      // query heads, per kv head, rows per kv head (G T)
   int MT, RT, NRT;   // warps of a team, rows of an item, items per kv head
   int rows;          // rows an item stores: min(RT, R)
-  int window, parts, f16;
+  int window, parts, f16, page_log2;
+  FastDiv div_t, div_nrt, div_per;  // T, NRT, items of a sequence
   float scale_log2;
   int64_t* first;    // [B + 1] chunks before each sequence
   float* ml;         // [2 parts][rows][2] partial maxima and sums
@@ -313,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!smem_base_ok(smem, c.err)) return;
   int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
+  int* s_len = reinterpret_cast<int*>(smem + C::kOffLen);
+  int* s_new = s_len + kMaxSeqs;  // 0 for a sequence that does not fit its table
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   int& abort_flag = *reinterpret_cast<int*>(bars + 2 * C::kStages);
   const int tid = static_cast<int>(threadIdx.x);
@@ -340,9 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
       const int b = 4 * tid + i;
       int n = 0, len = 0;
-      if (b < c.B && !sequence_of(c, b, &len, &n)) n = 0;
+      if (b < c.B) {
+        if (!sequence_of(c, b, &len, &n)) n = 0;
+        s_len[b] = len;
+        s_new[b] = n;
+      }
       own[i] = sum;
-      sum += b < c.B ? chunk_count(len, n, a.window, CK) : 0;
+      sum += chunk_count(len, n, a.window, CK);
     }
     int64_t scan = sum;
 #pragma unroll
@@ -364,9 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int per = c.Hkv * a.NRT;  // items of a sequence
   const int64_t total = s_first[c.B] * per;
-  const int part = static_cast<int>(blockIdx.x) * teams + team;
-  const int64_t begin = part_start(total, a.parts, part);
-  const int64_t count = part_start(total, a.parts, part + 1) - begin;
+  // Neighbouring parts go to different SMs: with few chunks every SM still gets some.
+  const int part = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  const Parts cut(total, a.parts);
+  const int64_t begin = cut.start(part), count = cut.start(part + 1) - begin;
 
   auto load_info = [&](int64_t i) {  // chunk i of the part
     ChunkInfo ci = {-1, 0, -1, 1.f, 1.f};
@@ -375,12 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = sequence_at(s_first, c.B, per, x);
       const int nc = static_cast<int>(s_first[b + 1] - s_first[b]);
       const int64_t rem = x - s_first[b] * per;
-      const int hr = static_cast<int>(rem / nc);
+      const int hr = static_cast<int>(quotient(rem, nc));
       ci.item = b * per + hr;
-      ci.slot = (first_chunk(c.lens[b], a.window, CK) + static_cast<int>(rem - static_cast<int64_t>(hr) * nc)) * CK;
-      const int page = page_of(c, c.table, b, ci.slot / c.page, c.max_pages);
+      ci.slot = (first_chunk(s_len[b], a.window, CK) +
+                 static_cast<int>(rem - static_cast<int64_t>(hr) * nc)) * CK;
+      const int page = page_of(c, c.table, b, ci.slot >> a.page_log2, c.max_pages);
       if (page >= 0) {
-        ci.plane = page * c.Hkv + hr / a.NRT;
+        ci.plane = page * c.Hkv + static_cast<int>(a.div_nrt.div(static_cast<uint32_t>(hr)));
         ci.ks = c.k_scale[ci.plane];
         ci.vs = c.v_scale[ci.plane];
       }
@@ -399,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A chunk whose page is out of range loads plane 0 and is masked.
 #pragma unroll
       for (int x = 0; x < C::kBoxes; ++x) {
-        tma_load_3d(dst + x * C::kBoxBytes, &tm_k, full(s), 128 * x, slot % c.page, max(plane, 0));
-        tma_load_3d(dst + CK * D + x * C::kBoxBytes, &tm_v, full(s), 128 * x, slot % c.page,
-                    max(plane, 0));
+        tma_load_3d(dst + x * C::kBoxBytes, &tm_k, full(s), 128 * x, slot & (c.page - 1), max(plane, 0));
+        tma_load_3d(dst + CK * D + x * C::kBoxBytes, &tm_v, full(s), 128 * x,
+                    slot & (c.page - 1), max(plane, 0));
       }
     }
     issued = i + 1;
@@ -412,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kSteps = D / 16;
   uint32_t qf[D == 256 ? 1 : kSteps][4];
   ItemState<D> st = {};
-  int item = -1, b = 0, item_first = 0, item_chunks = 0;
+  int item = -1, b = 0, tile0 = 0, item_first = 0, item_chunks = 0;
+  size_t base = 0;  // first row of the item, of all rows
   bool begins = false;
   const int g = lane >> 2, t = lane & 3;
   const int r0 = wt * 16 + g;  // this thread's rows of the item: r0 and r0 + 8
@@ -421,8 +432,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto finish = [&](int slot) {
     const bool ends = slot / CK == item_first + item_chunks - 1;
     const float l0 = quad_sum(st.l[0]), l1 = quad_sum(st.l[1]);
-    const int hr = item - b * per, h = hr / a.NRT, tile0 = (hr % a.NRT) * a.RT;
-    const size_t base = (static_cast<size_t>(b) * c.Hkv + h) * a.R + tile0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = r0 + 8 * e;
@@ -477,9 +486,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto start = [&](int new_item, int slot) {
     item = new_item;
-    b = item / per;
-    const int hr = item - b * per, h = hr / a.NRT, tile0 = (hr % a.NRT) * a.RT;
-    const int len = c.lens[b], n = c.new_lens ? c.new_lens[b] : c.T;
+    b = static_cast<int>(a.div_per.div(static_cast<uint32_t>(item)));
+    const uint32_t hr = static_cast<uint32_t>(item - b * per), h = a.div_nrt.div(hr);
+    tile0 = static_cast<int>(hr - h * a.div_nrt.d) * a.RT;
+    const int len = s_len[b], n = s_new[b];
+    base = (static_cast<size_t>(b) * c.Hkv + h) * a.R + tile0;
+    // Both rows of q are on their way before anything waits for them.
+    uint2 raw[2][kSteps];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t r = static_cast<uint32_t>(tile0 + r0 + 8 * e);
+      const int tq = static_cast<int>(a.div_t.mod(r));
+      const bool real = static_cast<int>(r) < a.R && tq < n;
+      const uint2* row = reinterpret_cast<const uint2*>(a.q + (base + r0 + 8 * e) * D) + t;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) raw[e][i] = real ? __ldg(row + 4 * i) : make_uint2(0u, 0u);
+      st.lo[e] = visible_lo(len + tq, a.window);
+      st.hi[e] = real ? len + tq : -1;
+      st.m[e] = SWA_NEG_INF;
+      st.l[e] = 0.f;
+    }
     item_first = first_chunk(len, a.window, CK);
     item_chunks = chunk_count(len, n, a.window, CK);
     begins = slot / CK == item_first;
@@ -487,41 +513,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.any_hi = len + n - 1;
     st.all_lo = visible_lo(len + n - 1, a.window);
     st.all_hi = n < c.T ? -1 : len;  // a row without a query sees nothing
-    const size_t base = (static_cast<size_t>(b) * c.Hkv + h) * a.R + tile0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = r0 + 8 * e, tq = (tile0 + r) % c.T;
-      const bool real = tile0 + r < a.R && tq < n;
-      st.lo[e] = visible_lo(len + tq, a.window);
-      st.hi[e] = real ? len + tq : -1;
-      st.m[e] = SWA_NEG_INF;
-      st.l[e] = 0.f;
-      // The row as fp16, its largest element brought to [2^14, 2^15).
-      uint2 raw[kSteps];
+      // The row as fp16, its largest element brought to [2^14, 2^15) (a row below 2^-112 less far).
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        raw[i] = make_uint2(0u, 0u);
-        if (real) raw[i] = __ldg(reinterpret_cast<const uint2*>(a.q + (base + r) * D + 16 * i + 4 * t));
-        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[i].x) : Elem<false>::unpack(raw[i].x);
-        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[i].y) : Elem<false>::unpack(raw[i].y);
+        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[e][i].x) : Elem<false>::unpack(raw[e][i].x);
+        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[e][i].y) : Elem<false>::unpack(raw[e][i].y);
         top = max(max(top, __float_as_uint(fabsf(y0.x))), __float_as_uint(fabsf(y0.y)));
         top = max(max(top, __float_as_uint(fabsf(y1.x))), __float_as_uint(fabsf(y1.y)));
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^(14 - exponent) as two factors, each inside fp32's range; none for zero, infinity and NaN
       const int ex = static_cast<int>(top >> 23);
-      const int sh = ex == 255 || top == 0 ? 0 : 127 + 14 - max(ex, 1);
-      const float up0 = __uint_as_float(static_cast<uint32_t>(127 + sh / 2) << 23);
-      const float up1 = __uint_as_float(static_cast<uint32_t>(127 + sh - sh / 2) << 23);
-      st.f[e] = a.scale_log2 / up0 / up1;
+      // 2^(14 - exponent); 1 for zero, infinity and NaN
+      const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+      st.f[e] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[i].x) : Elem<false>::unpack(raw[i].x);
-        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[i].y) : Elem<false>::unpack(raw[i].y);
-        const uint32_t p0 = pack_f16(y0.x * up0 * up1, y0.y * up0 * up1);
-        const uint32_t p1 = pack_f16(y1.x * up0 * up1, y1.y * up0 * up1);
+        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[e][i].x) : Elem<false>::unpack(raw[e][i].x);
+        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[e][i].y) : Elem<false>::unpack(raw[e][i].y);
+        const uint32_t p0 = pack_f16(y0.x * up, y0.y * up);
+        const uint32_t p1 = pack_f16(y1.x * up, y1.y * up);
         if constexpr (D == 256) {
           st_shared_b32(sq + (i * 32 + lane) * 16 + 4 * e, p0);
           st_shared_b32(sq + (i * 32 + lane) * 16 + 8 + 4 * e, p1);
@@ -599,109 +614,191 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Where an item's partial results are: parts p0 .. p1 of the list, the item's first chunk x0.  Both
+// equal: the item was finished by one team.  No chunks: nobody saw anything.
+struct ItemParts {
+  int64_t x0, chunks;
+  int p0, p1;
+};
+__device__ __forceinline__ ItemParts item_parts(const AttnDev& a, const Parts& cut, int per, int item) {
+  const int b = static_cast<int>(a.div_per.div(static_cast<uint32_t>(item)));
+  const int64_t f0 = a.first[b];
+  ItemParts ip;
+  ip.chunks = a.first[b + 1] - f0;
+  ip.x0 = f0 * per + (item - b * per) * ip.chunks;
+  ip.p0 = ip.p1 = 0;
+  if (ip.chunks > 0) {
+    ip.p0 = cut.of(ip.x0);
+    ip.p1 = cut.of(ip.x0 + ip.chunks - 1);
+  }
+  return ip;
+}
+
+// Row `r` of an item, of all rows of the call; false when the last tile of a kv head is shorter.
+__device__ __forceinline__ bool row_of_item(const AttnDev& a, int item, int r, size_t* row) {
+  const uint32_t bh = a.div_nrt.div(static_cast<uint32_t>(item));
+  const int in_head = (item - static_cast<int>(bh * a.div_nrt.d)) * a.RT + r;
+  *row = static_cast<size_t>(bh) * a.R + in_head;
+  return in_head < a.R;
+}
+
+template <int N>
+__device__ __forceinline__ void store_row(const AttnDev& a, uint16_t* out, const float (&o)[N],
+                                          float scale) {
+  uint32_t pk[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i)
+    pk[i] = a.f16 ? Elem<true>::pack(o[2 * i] * scale, o[2 * i + 1] * scale)
+                  : Elem<false>::pack(o[2 * i] * scale, o[2 * i + 1] * scale);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4*>(out) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pk[0], pk[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = pk[0];
+}
+
 // Joins the partial results of items that several teams shared, and answers the rows of sequences
-// without a chunk.  Tasks are (item, row, run of 4 `lanes` columns), one block each in turn: groups of
-// `lanes` threads take the partials in turn, then the groups' sums are added in a fixed order.
+// without a chunk: a warp a row, its lanes the row's columns.
 template <int D>
-__global__ void __launch_bounds__(256) swa_cache_join_kernel(const CacheView c, const AttnDev a,
-                                                             int lanes) {
-  using C = AttnCfg<D>;
-  __shared__ float s_red[8], s_l[64];
-  __shared__ float4 s_o[256];
+__global__ void __launch_bounds__(256) swa_cache_join_kernel(const CacheView c, const AttnDev a) {
+  constexpr int N = D / 32;
   wait_predecessor();
   launch_dependents();
-  const int tid = static_cast<int>(threadIdx.x);
-  const int per = c.Hkv * a.NRT, runs = D / 4 / lanes, groups = 256 / lanes;
+  const int lane = static_cast<int>(lane_id());
+  const int per = c.Hkv * a.NRT;
   const int64_t total = a.first[c.B] * per;
-  const int64_t tasks = static_cast<int64_t>(c.B) * per * a.rows * runs;
-  const int group = tid / lanes, sub = tid % lanes;
-  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
-    const int run = static_cast<int>(task % runs);
-    const int64_t ir = task / runs;
-    const int row = static_cast<int>(ir % a.rows);
-    const int item = static_cast<int>(ir / a.rows);
-    const int b = item / per, hr = item % per;
-    const int h = hr / a.NRT, r = (hr % a.NRT) * a.RT + row;
-    if (r >= a.R) continue;
-    const int64_t f0 = a.first[b], nc = a.first[b + 1] - f0;
-    const size_t out_row = (static_cast<size_t>(b) * c.Hkv + h) * a.R + r;
-    uint16_t* out = a.o + out_row * D + (run * lanes + sub) * 4;
-    if (nc == 0) {
-      if (group == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
-      if (tid == 0 && run == 0) a.lse[out_row] = SWA_NEG_INF;
-      continue;
-    }
-    const int64_t x0 = f0 * per + hr * nc;
-    const int p0 = part_of(total, a.parts, x0), p1 = part_of(total, a.parts, x0 + nc - 1);
-    if (p0 == p1) continue;
-    // Row of part p's result, or -1: with fewer chunks than parts some parts hold nothing.
-    auto row_of = [&](int p) -> int64_t {
-      const int64_t from = part_start(total, a.parts, p);
-      if (from == part_start(total, a.parts, p + 1)) return -1;
-      return static_cast<int64_t>(partial_slot(p, from <= x0)) * a.rows + row;
-    };
-    float top = SWA_NEG_INF;
-    for (int p = p0 + tid; p <= p1; p += 256) {
-      const int64_t pr = row_of(p);
-      if (pr >= 0) top = fmaxf(top, a.ml[pr * 2]);
-    }
+  const Parts cut(total, a.parts);
+  const uint32_t tasks = static_cast<uint32_t>(c.B) * per * a.rows;
+  for (uint32_t task = blockIdx.x * 8 + warp_id(); task < tasks; task += gridDim.x * 8) {
+    const int item = static_cast<int>(task / static_cast<uint32_t>(a.rows));
+    const int r = static_cast<int>(task - static_cast<uint32_t>(item) * a.rows);
+    size_t row;
+    if (!row_of_item(a, item, r, &row)) continue;
+    const ItemParts ip = item_parts(a, cut, per, item);
+    if (ip.chunks > 0 && ip.p0 == ip.p1) continue;
+    float o[N] = {}, l = 0.f, top = SWA_NEG_INF;
+    if (ip.chunks > 0) {
+      auto partial = [&](int p) {
+        return static_cast<size_t>(partial_slot(p, cut.start(p) <= ip.x0)) * a.rows + r;
+      };
+      for (int p = ip.p0 + lane; p <= ip.p1; p += 32) top = fmaxf(top, a.ml[partial(p) * 2]);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if ((tid & 31) == 0) s_red[tid >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_red[w]);
-    const float base = top == SWA_NEG_INF ? 0.f : top;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float base = top == SWA_NEG_INF ? 0.f : top;
+      for (int p = ip.p0; p <= ip.p1; p += 32) {
+        const int n = min(32, ip.p1 - p + 1);
+        float w = 0.f;
+        if (lane < n) {
+          const float2 ml = *reinterpret_cast<const float2*>(a.ml + partial(p + lane) * 2);
+          w = ex2(ml.x - base);
+          l += w * ml.y;
+        }
 #pragma unroll 4
-    for (int p = p0 + group; p <= p1; p += groups) {
-      const int64_t pr = row_of(p);
-      if (pr < 0) continue;
-      const float2 ml = *reinterpret_cast<const float2*>(a.ml + pr * 2);
-      const float4 y = *reinterpret_cast<const float4*>(a.po + pr * D + (run * lanes + sub) * 4);
-      const float w = ex2(ml.x - base);
-      l += w * ml.y;
-      o.x += w * y.x;
-      o.y += w * y.y;
-      o.z += w * y.z;
-      o.w += w * y.w;
-    }
-    if (sub == 0) s_l[group] = l;
-    s_o[tid] = o;
-    __syncthreads();
-    if (group == 0) {
-      l = 0.f;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < groups; ++i) {
-        l += s_l[i];
-        const float4 y = s_o[i * lanes + sub];
-        o.x += y.x;
-        o.y += y.y;
-        o.z += y.z;
-        o.w += y.w;
+        for (int j = 0; j < n; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w, j);
+          const float* y = a.po + partial(p + j) * D + lane * N;
+          float v[N];
+          if constexpr (N == 2) {
+            const float2 u = *reinterpret_cast<const float2*>(y);
+            v[0] = u.x, v[1] = u.y;
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+              const float4 u = *reinterpret_cast<const float4*>(y + i);
+              v[i] = u.x, v[i + 1] = u.y, v[i + 2] = u.z, v[i + 3] = u.w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) o[i] += wj * v[i];
+        }
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint2 pk;
-      if (a.f16) {
-        pk = make_uint2(Elem<true>::pack(o.x * inv, o.y * inv), Elem<true>::pack(o.z * inv, o.w * inv));
-      } else {
-        pk = make_uint2(Elem<false>::pack(o.x * inv, o.y * inv), Elem<false>::pack(o.z * inv, o.w * inv));
-      }
-      *reinterpret_cast<uint2*>(out) = pk;
-      if (tid == 0 && run == 0) a.lse[out_row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     }
-    __syncthreads();
+    store_row<N>(a, a.o + row * D + lane * N, o, l == 0.f ? 0.f : 1.f / l);
+    if (lane == 0) a.lse[row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
   }
 }
 
-// Adds to each cached token's weight the sum over its kv head's rows of 2^(score - lse / ln 2).  A
-// warp takes 4 chunks at a time (a lane finds one's place each), then each in turn with a lane per
-// key; one thread alone touches a weight.
+// The same with a block for 16 columns of a row, for calls with so few rows that each has very many
+// partials: 64 groups of 4 lanes take the partials in turn and meet in shared memory in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(256) swa_cache_join_few_kernel(const CacheView c, const AttnDev a) {
+  constexpr int kGroups = 64, kRuns = D / 16;
+  __shared__ float s_red[8], s_l[kGroups];
+  __shared__ float4 s_o[256];
+  wait_predecessor();
+  launch_dependents();
+  const int tid = static_cast<int>(threadIdx.x), group = tid / 4, sub = tid % 4;
+  const int per = c.Hkv * a.NRT;
+  const int64_t total = a.first[c.B] * per;
+  const Parts cut(total, a.parts);
+  const uint32_t tasks = static_cast<uint32_t>(c.B) * per * a.rows * kRuns;
+  for (uint32_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int run = static_cast<int>(task % kRuns);
+    const int item = static_cast<int>(task / kRuns / static_cast<uint32_t>(a.rows));
+    const int r = static_cast<int>(task / kRuns - static_cast<uint32_t>(item) * a.rows);
+    size_t row;
+    if (!row_of_item(a, item, r, &row)) continue;
+    const ItemParts ip = item_parts(a, cut, per, item);
+    if (ip.chunks > 0 && ip.p0 == ip.p1) continue;
+    float top = SWA_NEG_INF, l = 0.f;
+    float o[4] = {};
+    if (ip.chunks > 0) {
+      auto partial = [&](int p) {
+        return static_cast<size_t>(partial_slot(p, cut.start(p) <= ip.x0)) * a.rows + r;
+      };
+      for (int p = ip.p0 + tid; p <= ip.p1; p += 256) top = fmaxf(top, a.ml[partial(p) * 2]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      if ((tid & 31) == 0) s_red[tid >> 5] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, s_red[w]);
+      const float base = top == SWA_NEG_INF ? 0.f : top;
+#pragma unroll 4
+      for (int p = ip.p0 + group; p <= ip.p1; p += kGroups) {
+        const size_t pr = partial(p);
+        const float2 ml = *reinterpret_cast<const float2*>(a.ml + pr * 2);
+        const float4 y = *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4);
+        const float w = ex2(ml.x - base);
+        l += w * ml.y;
+        o[0] += w * y.x;
+        o[1] += w * y.y;
+        o[2] += w * y.z;
+        o[3] += w * y.w;
+      }
+      if (sub == 0) s_l[group] = l;
+      s_o[tid] = make_float4(o[0], o[1], o[2], o[3]);
+      __syncthreads();
+      if (group == 0) {
+        l = o[0] = o[1] = o[2] = o[3] = 0.f;
+        for (int i = 0; i < kGroups; ++i) {
+          l += s_l[i];
+          const float4 y = s_o[i * 4 + sub];
+          o[0] += y.x;
+          o[1] += y.y;
+          o[2] += y.z;
+          o[3] += y.w;
+        }
+      }
+      __syncthreads();  // before the next task's sums
+    }
+    if (group == 0) {
+      store_row<4>(a, a.o + row * D + run * 16 + sub * 4, o, l == 0.f ? 0.f : 1.f / l);
+      if (tid == 0 && run == 0) a.lse[row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
+    }
+  }
+}
+
+// Adds to each cached token's weight the sum over its kv head's rows of 2^(score - lse / ln 2).  The
+// lanes of a warp find the places of up to 32 chunks at once; then it takes 128 keys at a time, four a
+// lane, and one thread alone touches a weight.
 template <int D>
 __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView c, const AttnDev a) {
   using C = AttnCfg<D>;
-  constexpr int CK = C::CK, kSplit = 32 / CK;  // lanes that share a key
+  constexpr int CK = C::CK, kLanes = CK / 4, kChunks = 32 / kLanes;  // lanes of a chunk; at a time
   __shared__ int64_t s_first[kMaxSeqs + 1];
   wait_predecessor();
   for (int b = static_cast<int>(threadIdx.x); b <= c.B; b += 256) s_first[b] = a.first[b];
@@ -709,46 +806,55 @@ __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView 
   const int lane = static_cast<int>(lane_id());
   const int64_t tasks = s_first[c.B] * c.Hkv;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t y0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp_id()) * 4; y0 < tasks;
-       y0 += warps * 4) {
-    int64_t chunk = 0, stride = 0;
-    long long weight = -1;
-    int rows0 = 0;
-    if (lane < 4 && y0 + lane < tasks) {
+  // chunks of a turn: up to 32, fewer where that leaves warps without any
+  int turn = kChunks;
+  while (turn < 32 && tasks > warps * turn) turn *= 2;
+  for (int64_t y0 = (static_cast<int64_t>(blockIdx.x) * 8 + warp_id()) * turn; y0 < tasks;
+       y0 += warps * turn) {
+    int64_t chunk = 0, weight = -1;
+    int stride = 0, head = 0;
+    if (lane < turn && y0 + lane < tasks) {
       const int64_t y = y0 + lane;
       const int b = sequence_at(s_first, c.B, c.Hkv, y);
       const int64_t f0 = s_first[b];
-      const int nc = static_cast<int>(s_first[b + 1] - f0);
+      stride = static_cast<int>(s_first[b + 1] - f0);
       const int64_t rem = y - f0 * c.Hkv;
-      const int h = static_cast<int>(rem / nc), cc = static_cast<int>(rem - static_cast<int64_t>(h) * nc);
+      const int h = static_cast<int>(quotient(rem, stride));
+      const int cc = static_cast<int>(rem - static_cast<int64_t>(h) * stride);
       const int slot = (first_chunk(c.lens[b], a.window, CK) + cc) * CK;
-      const int page = page_of(c, c.table, b, slot / c.page, c.max_pages);
+      const int page = page_of(c, c.table, b, slot >> a.page_log2, c.max_pages);
       if (page >= 0)
-        weight = (static_cast<long long>(page) * c.Hkv + h) * c.page + slot % c.page;
-      chunk = f0 * c.Hkv * a.NRT + static_cast<int64_t>(h) * a.NRT * nc + cc;
-      stride = nc;
-      rows0 = b * c.Hkv + h;
+        weight = (static_cast<int64_t>(page) * c.Hkv + h) * c.page + (slot & (c.page - 1));
+      chunk = f0 * c.Hkv * a.NRT + static_cast<int64_t>(h) * a.NRT * stride + cc;
+      head = b * c.Hkv + h;
     }
-    for (int j = 0; j < 4; ++j) {
-      const long long w = __shfl_sync(0xffffffffu, weight, j);
-      const int64_t x = __shfl_sync(0xffffffffu, chunk, j), nc = __shfl_sync(0xffffffffu, stride, j);
-      const int bh = __shfl_sync(0xffffffffu, rows0, j);
-      if (w < 0) continue;
-      float add = 0.f;
+    for (int g = 0; g < turn; g += kChunks) {
+      const int from = g + lane / kLanes, key = lane % kLanes * 4;
+      const int64_t at = __shfl_sync(0xffffffffu, weight, from);
+      const int64_t x = __shfl_sync(0xffffffffu, chunk, from);
+      const int nc = __shfl_sync(0xffffffffu, stride, from);
+      const int bh = __shfl_sync(0xffffffffu, head, from);
+      if (at < 0) continue;
+      float4* w = reinterpret_cast<float4*>(c.weight + at + key);
+      const float4 old = *w;
+      float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int rt = 0; rt < a.NRT; ++rt) {
-        const float* sc = a.scores + static_cast<size_t>(x + rt * nc) * a.rows * CK;
-        const float* lse = a.lse + static_cast<size_t>(bh) * a.R + rt * a.RT;
         const int rows = min(a.rows, a.R - rt * a.RT);
+        const float* sc = a.scores + static_cast<size_t>(x + static_cast<int64_t>(rt) * nc) * a.rows * CK + key;
+        const float* lse = a.lse + static_cast<size_t>(bh) * a.R + rt * a.RT;
 #pragma unroll 4
-        for (int r = lane / CK; r < rows; r += kSplit) {
-          const float z = lse[r];
+        for (int r = 0; r < rows; ++r) {
+          const float4 s = *reinterpret_cast<const float4*>(sc + r * CK);
           // a row that sees nothing has scores and lse -inf, and adds nothing
-          add += ex2(sc[r * CK + lane % CK] - (z == SWA_NEG_INF ? 0.f : z * kLog2e));
+          const float z = lse[r] == SWA_NEG_INF ? 0.f : lse[r] * kLog2e;
+          add.x += ex2(s.x - z);
+          add.y += ex2(s.y - z);
+          add.z += ex2(s.z - z);
+          add.w += ex2(s.w - z);
         }
       }
-      if (kSplit == 2) add += __shfl_xor_sync(0xffffffffu, add, 16);
-      // Untouched unless something was seen: slots behind the sequence are left as they were.
-      if (lane < CK && add != 0.f) c.weight[w + lane] += add;
+      // Slots that nobody saw have scores -inf and keep their weight.
+      *w = make_float4(old.x + add.x, old.y + add.y, old.z + add.z, old.w + add.w);
     }
   }
 }
@@ -810,8 +916,7 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream
   if (!make_tmap_u8(&tk, all.k, planes, all.page, D, C::CK) ||
       !make_tmap_u8(&tv, all.v, planes, all.page, D, C::CK))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(swa_cache_attn_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_cache_attn_kernel<D>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(args.workspace);
   AttnDev a;
@@ -826,6 +931,10 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream
   a.parts = p.parts;
   a.f16 = args.dtype == SWA_FP16;
   a.scale_log2 = args.scale * kLog2e;
+  a.page_log2 = all.page == 32 ? 5 : all.page == 64 ? 6 : 7;
+  a.div_t = FastDiv(static_cast<uint32_t>(all.T));
+  a.div_nrt = FastDiv(static_cast<uint32_t>(p.NRT));
+  a.div_per = FastDiv(static_cast<uint32_t>(all.Hkv) * p.NRT);
   a.first = reinterpret_cast<int64_t*>(ws);
   a.ml = reinterpret_cast<float*>(ws + p.off_ml);
   a.po = reinterpret_cast<float*>(ws + p.off_po);
@@ -843,18 +952,24 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream
     swa_cache_attn_kernel<D><<<p.parts / (kWarps / p.MT), kThreads, C::kSmemBytes, stream>>>(
         tk, tv, c, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // Runs of 128 columns a warp, or of 16 when there are too few rows to fill the SMs.
+    // A warp a row, or with fewer rows than four for every SM 16 columns a block.
     const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv * p.NRT * p.rows;
-    const int lanes = rows * (D / 4 / (D == 64 ? 16 : 32)) >= 4 * 152 ? (D == 64 ? 16 : 32) : 4;
-    const int64_t tasks = rows * (D / 4 / lanes);
-    const unsigned grid = static_cast<unsigned>(tasks < 152 * 8 ? tasks : 152 * 8);
-    if ((e = launch_after(swa_cache_join_kernel<D>, grid, stream, c, a, lanes)) != cudaSuccess)
-      return e;
+    const int64_t most = 8ll * sm_count();
+    if (rows >= 4ll * sm_count()) {
+      const int64_t blocks = (rows + 7) / 8;
+      e = launch_after(swa_cache_join_kernel<D>, static_cast<unsigned>(blocks < most ? blocks : most),
+                       stream, c, a);
+    } else {
+      const int64_t blocks = rows * (D / 16);
+      e = launch_after(swa_cache_join_few_kernel<D>,
+                       static_cast<unsigned>(blocks < most ? blocks : most), stream, c, a);
+    }
+    if (e != cudaSuccess) return e;
     if (args.accumulate) {
       // At most this many chunks of 4 warps' turns; the kernel walks what there really is.
-      const int64_t most = (static_cast<int64_t>(all.max_pages) * all.page / C::CK) * c.B * c.Hkv;
-      const int64_t blocks = (most + 31) / 32;
-      const unsigned wgrid = static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8);
+      const int64_t chunks = (static_cast<int64_t>(all.max_pages) * all.page / C::CK) * c.B * c.Hkv;
+      const int64_t blocks = (chunks + 31) / 32;
+      const unsigned wgrid = static_cast<unsigned>(blocks < most ? blocks : most);
       if ((e = launch_after(swa_cache_weights_kernel<D>, wgrid, stream, c, a)) != cudaSuccess)
         return e;
     }

@@ -376,9 +376,8 @@ cudaError_t launch_cache_evict(const CacheView& c, const CacheEvictArgs& a, cuda
   const long long slice = (slots + ctas - 1) / ctas + kSelectWarps * 128;
   const int held = static_cast<int>(slice < kMaxHeld ? slice : kMaxHeld);
   const int bytes = static_cast<int>(sizeof(SelectShared)) + held * 4;
-  cudaError_t e = cudaFuncSetAttribute(
-      swa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      static_cast<int>(sizeof(SelectShared)) + kMaxHeld * 4);
+  cudaError_t e = allow_smem<swa_evict_select_kernel>(static_cast<int>(sizeof(SelectShared)) +
+                                                      kMaxHeld * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(c.Hkv * ctas), static_cast<unsigned>(c.B));

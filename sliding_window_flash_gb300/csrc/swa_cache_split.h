@@ -3,9 +3,9 @@
 //
 // The visible slots of a sequence are cut at multiples of CK slots into chunks.  All chunks of all
 // items (sequence, kv head, tile of query rows) form one list, item after item; the list is cut into
-// as many equal parts as there are teams of warps, whatever the sequences' lengths.  A team walks its
-// part from left to right: items that lie wholly inside it are finished there, and at most two, its
-// first and its last, continue in a neighbour and leave a partial result.
+// as many parts as there are teams of warps, equal within one chunk whatever the sequences' lengths.
+// A team walks its part from left to right: items that lie wholly inside it are finished there, and at
+// most two, its first and its last, continue in a neighbour and leave a partial result.
 #pragma once
 
 #include <cstdint>
@@ -18,24 +18,38 @@
 
 namespace swa {
 
-// Visible slots [lo, hi) of the n > 0 queries at slots len .. len + n - 1 under `window`, all together.
-SWA_HD int visible_lo(int len, int window) { return len >= window ? len - window + 1 : 0; }
+// First slot that a query at slot `at` sees under `window`.
+SWA_HD int visible_lo(int at, int window) { return at >= window ? at - window + 1 : 0; }
 
-// First chunk and number of chunks of a sequence (0 chunks without queries).
+// First chunk and number of chunks of a sequence (0 chunks without queries): the n queries sit at
+// slots len .. len + n - 1.
 SWA_HD int first_chunk(int len, int window, int ck) { return visible_lo(len, window) / ck; }
 SWA_HD int chunk_count(int len, int n, int window, int ck) {
   return n > 0 ? (len + n - 1) / ck - first_chunk(len, window, ck) + 1 : 0;
 }
 
-// Part i of `parts` of a list of `total` chunks starts here; parts are equal within one chunk.
-SWA_HD int64_t part_start(int64_t total, int parts, int i) { return total * i / parts; }
-
-// The part that chunk x of the list belongs to.
-SWA_HD int part_of(int64_t total, int parts, int64_t x) {
-  return static_cast<int>(((x + 1) * parts - 1) / total);
+// x / d for 0 <= x, 1 <= d, in 32 bits where they fit (a 64-bit division costs ten times as much).
+SWA_HD int64_t quotient(int64_t x, int64_t d) {
+  if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
+  return x / d;
 }
 
-// A team's two partial results: 0 continues an item begun in an earlier part, 1 begins one.
+// A list of `total` chunks in `parts` parts: the first `extra` have size + 1 chunks, the others size.
+struct Parts {
+  int64_t size;
+  int extra;
+  SWA_HD Parts(int64_t total, int parts)
+      : size(quotient(total, parts)), extra(static_cast<int>(total - size * parts)) {}
+  // First chunk of part i (parts + 1 of them: the last is the total).
+  SWA_HD int64_t start(int i) const { return size * i + (i < extra ? i : extra); }
+  // The part of chunk x < total.
+  SWA_HD int of(int64_t x) const {
+    const int64_t longer = (size + 1) * extra;
+    return static_cast<int>(x < longer ? quotient(x, size + 1) : extra + quotient(x - longer, size));
+  }
+};
+
+// A part's two partial results: 0 continues an item begun in an earlier part, 1 begins one.
 SWA_HD int partial_slot(int part, bool begins) { return 2 * part + (begins ? 1 : 0); }
 
 // Sequence that entry x of the list belongs to: the last b with first[b] * per <= x, where first[b]

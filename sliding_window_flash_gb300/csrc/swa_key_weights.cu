@@ -465,8 +465,7 @@ cudaError_t launch_d(const Problem& pb, const void* q, const void* k, const floa
       !make_tmap_3d(&tk, k, bhk, pb.span.Lk, D, kBlockN, F16))
     return cudaErrorInvalidValue;
   auto kern = swa_key_weights_kernel<D, F16>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_key_weights_kernel<D, F16>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   KwArgs a;
   a.lse = lse;

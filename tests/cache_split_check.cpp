@@ -42,15 +42,16 @@ int main() {
     const int64_t total = first[B] * per;
     if (total == 0) continue;
     std::set<int> slots;
-    CHECK(part_start(total, parts, 0) == 0 && part_start(total, parts, parts) == total);
+    const Parts cut(total, parts);
+    CHECK(cut.start(0) == 0 && cut.start(parts) == total);
     for (int i = 0; i < parts; ++i) {
-      const int64_t a = part_start(total, parts, i), z = part_start(total, parts, i + 1);
+      const int64_t a = cut.start(i), z = cut.start(i + 1);
       CHECK(z >= a && z - a <= total / parts + 1);
       int64_t last_item = -1, item_from = 0;
       for (int64_t x = a; x <= z; ++x) {
         int64_t item = -1;
         if (x < z) {
-          CHECK(part_of(total, parts, x) == i);
+          CHECK(cut.of(x) == i);
           const int b = sequence_at(first.data(), B, per, x);
           CHECK(b >= 0 && b < B && first[b] * per <= x && x < first[b + 1] * per);
           const int64_t nc = first[b + 1] - first[b];
@@ -62,8 +63,8 @@ int main() {
             const int64_t nc = first[b + 1] - first[b];
             const int64_t x0 = first[b] * per + (last_item % per) * nc;
             const bool begins = item_from == x0, ends = x == x0 + nc;
-            CHECK(begins == (part_start(total, parts, i) <= x0));
-            const int p0 = part_of(total, parts, x0), p1 = part_of(total, parts, x0 + nc - 1);
+            CHECK(begins == (cut.start(i) <= x0));
+            const int p0 = cut.of(x0), p1 = cut.of(x0 + nc - 1);
             CHECK((begins && ends) == (p0 == p1) && p0 <= i && i <= p1);
             if (!(begins && ends)) {
               const int s = partial_slot(i, begins);
@@ -81,17 +82,23 @@ int main() {
       const int64_t nc = first[b + 1] - first[b];
       if (nc == 0) continue;
       const int64_t x0 = first[b] * per + (item % per) * nc;
-      const int p0 = part_of(total, parts, x0), p1 = part_of(total, parts, x0 + nc - 1);
+      const int p0 = cut.of(x0), p1 = cut.of(x0 + nc - 1);
       if (p0 != p1)
         for (int p = p0; p <= p1; ++p) {
-          const bool holds = part_start(total, parts, p) < x0 + nc &&
-                             part_start(total, parts, p + 1) > x0 &&
-                             part_start(total, parts, p + 1) > part_start(total, parts, p);
-          CHECK(holds == (slots.count(partial_slot(p, part_start(total, parts, p) <= x0)) == 1) ||
-                !holds);
-          if (!holds) CHECK(part_start(total, parts, p) == part_start(total, parts, p + 1));
+          CHECK(cut.start(p + 1) > cut.start(p));
+          CHECK(slots.count(partial_slot(p, cut.start(p) <= x0)) == 1);
         }
     }
+  }
+  // past 32 bits
+  for (int round = 0; round < 2000; ++round) {
+    const int64_t total = (static_cast<int64_t>(rng()) << 8) + rng() % 1000 + 1;
+    const int parts = pick(1, 1300);
+    const Parts cut(total, parts);
+    const int64_t x = static_cast<int64_t>((static_cast<unsigned __int128>(total) * rng()) >> 32);
+    const int i = cut.of(x);
+    CHECK(i >= 0 && i < parts && cut.start(i) <= x && x < cut.start(i + 1));
+    CHECK(quotient(x, parts) == x / parts);
   }
   std::puts("ok");
   return 0;

@@ -29,9 +29,11 @@ def test_split_matches_brute_force(tmp_path):
 
 
 @pytest.mark.parametrize("old,new", [
-    ("len >= window ? len - window + 1 : 0", "len >= window ? len - window : 0"),
+    ("at >= window ? at - window + 1 : 0", "at >= window ? at - window : 0"),
     ("(len + n - 1) / ck", "(len + n) / ck"),
-    ("((x + 1) * parts - 1) / total", "(x * parts) / total"),
+    ("(i < extra ? i : extra)", "(i <= extra ? i : extra - 1)"),
+    ("const int64_t longer = (size + 1) * extra;", "const int64_t longer = size * extra;"),
+    ("((x | d) >> 32) == 0", "true"),
     ("if (first[mid] * per <= x)", "if (first[mid] * per < x)"),
     ("2 * part + (begins ? 1 : 0)", "part + (begins ? 1 : 0)"),
 ])
