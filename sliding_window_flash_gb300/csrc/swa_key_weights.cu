@@ -5,19 +5,28 @@
 // One product per visible pair (2 D flops) and one exponential: at D = 128 a 128 x 128 tile takes the
 // tensor core ~512 cycles and the exponential unit ~546, so both have to run all the time.  The scores
 // are taken transposed, S^T = K Q^T, which puts a key on a TMEM lane: its sum stays in the registers
-// of the threads that own the lane, and nothing is reduced across threads until the end.
-//   * A task is 256 keys (two 128-row tiles) of one (batch, kv head) with the walk over its query
-//     tiles of every query head of the group: each query tile loaded is used for two products, which
-//     halves the traffic into shared memory (30 bytes a cycle and SM at D = 128).
-//   * Persistent CTAs, one per SM, take tasks longest first, there and back again (task i of a round
-//     from the left, then from the right), so that walks of unequal length even out.  With few tasks
-//     each walk is cut into `pieces` equal parts whose sums a second kernel adds in order.
-//   * 20 warps: 16 take the exponentials (a quarter of the lanes, a key tile and half of a tile's
-//     columns each), and one each loads Q, loads K, issues the products, and keeps -lse / ln 2 of the
-//     next query tiles in shared memory.  Four score tiles in TMEM, two per key tile.
-//   * Masked tiles select; whatever a query outside the window holds does not reach the sum.  A tile's
-//     64 terms are added in fp32, tiles with a compensated sum (Kahan), so the error does not grow
-//     with the walk.
+// of the threads that own the lane, and little is reduced across threads at the end.
+//   * CTA pairs: a task is 256 keys (128 a CTA) of one (batch, kv head) with the walk over 256 queries
+//     at a time of every query head of the group.  Each CTA loads its keys and its half of the
+//     queries; rank 0 issues M = 256, N = 256 products for both.  An SM then reads 64 bytes of operands
+//     a cycle from shared memory; single CTAs with 128 x 128 products read 128, all there is.
+//     Without the exponentials the pairs take 0.173 ms where the single CTAs took 0.207, with them
+//     0.254 and 0.288 (N = 32,768, W = 1,024, 32 / 16 heads, D = 128).
+//   * Persistent pairs take tasks longest first, there and back again (task i of a round from the
+//     left, then from the right), so that walks of unequal length even out.  With few tasks each walk
+//     is cut into `pieces` equal parts whose sums a second kernel adds in order.
+//   * 20 warps a CTA: 16 take the exponentials (32 keys and 64 of a unit's 256 queries each; a part
+//     that the window hides is skipped), and one each loads Q, loads K, issues the products (rank 0)
+//     or forwards the arrival of its copies (rank 1), and keeps -lse / ln 2 of the next queries in
+//     shared memory, announced by the same barrier as their scores (0.254 ms against 0.290 with
+//     each warp fetching its own).  Two score buffers of 256 columns fill TMEM.
+//   * What bounds it: the 16 warps' chain of barrier, TMEM load, exponentials and sums, in step with
+//     one another for the wait on the same scores; products alone would take 0.135 ms.
+//   * Masked parts select; whatever a query outside the window holds does not reach the sum.  64 terms
+//     are added in fp32, then into a compensated sum (Kahan), so the error does not grow with the walk.
+#include <climits>
+#include <type_traits>
+
 #include "swa_cache_kernels.h"
 #include "swa_ptx.cuh"
 #include "swa_tmap.h"
@@ -26,11 +35,12 @@ namespace swa {
 namespace {
 
 constexpr int kTaskKeys = 256;
+constexpr int kUnitQueries = 256;
 constexpr int kEpiWarps = 16;
 constexpr int kWarpQ = kEpiWarps, kWarpK = kEpiWarps + 1, kWarpMma = kEpiWarps + 2,
               kWarpLse = kEpiWarps + 3;
 constexpr int kKwThreads = 32 * (kEpiWarps + 4);
-constexpr int kLseSlots = 3;
+constexpr int kLseSlots = 4;
 
 template <int D>
 struct KwCfg {
@@ -39,22 +49,23 @@ struct KwCfg {
   static constexpr int kPieceBytes = 128 * kCols * 2;
   static constexpr int kChunks = kCols / 64;
   static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int kTileBytes = kHalves * kPieceBytes;
   static constexpr int kKSets = D == 256 ? 1 : 2;       // tasks whose keys are held
-  static constexpr int kKPieces = kKSets * 2 * kHalves; // 4
-  static constexpr int kQStages = D == 64 ? 6 : 3;      // pieces
-  static constexpr int kOffQ = kKPieces * kPieceBytes;
+  static constexpr int kQStages = D == 64 ? 6 : 4;      // pieces
+  static constexpr int kOffQ = kKSets * kTileBytes;
   static constexpr int kOffLse = kOffQ + kQStages * kPieceBytes;
-  static constexpr int kOffRed = kOffLse + kLseSlots * 512;  // a half's sums, per key tile
-  static constexpr int kOffBar = kOffRed + 2 * 512;
+  static constexpr int kOffRed = kOffLse + kLseSlots * kUnitQueries * 4;  // three groups' sums
+  static constexpr int kOffBar = kOffRed + 3 * 512;
   static constexpr int kKFull = 0;
   static constexpr int kKEmpty = kKFull + kKSets;
   static constexpr int kQFull = kKEmpty + kKSets;
   static constexpr int kQEmpty = kQFull + kQStages;
-  static constexpr int kSFull = kQEmpty + kQStages;   // [tile][buffer]
-  static constexpr int kSEmpty = kSFull + 4;
-  static constexpr int kLFull = kSEmpty + 4;
-  static constexpr int kLEmpty = kLFull + kLseSlots;
-  static constexpr int kDrain = kLEmpty + kLseSlots;
+  static constexpr int kSFull = kQEmpty + kQStages;   // 2 buffers
+  static constexpr int kSEmpty = kSFull + 2;          // rank 0's: both CTAs' warps have read
+  static constexpr int kLEmpty = kSEmpty + 2;
+  static constexpr int kRFull = kLEmpty + kLseSlots;
+  static constexpr int kREmpty = kRFull + 1;
+  static constexpr int kDrain = kREmpty + 1;
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -63,136 +74,191 @@ struct KwCfg {
 struct KwArgs {
   const float* lse;
   float* w;        // [pieces][B Hkv][Lk] when pieces > 1, else the output
-  int BHK, Hq, Hkv, G, pieces;
-  int64_t tasks;   // key blocks x pieces x B Hkv
+  int BHK, Hq, G;
+  uint32_t tasks;  // key blocks x pieces x B Hkv
+  FastDiv div_bhk, div_pieces, div_hkv;
   Span span;
   float scale_log2;
   unsigned* err;
 };
 
-// A task's walk: units [u0, u1) of (query head, query tile) pairs, head-major.
+// A task's walk: units [u0, u1) of (query head, 256 queries) pairs, head-major; np per head.
 struct Walk {
-  int k0, bhk, piece, qb_lo, nq, u0, u1;
+  int k0, bhk, bhq0, piece, q_lo, np, u0, u1;
 };
 
+// The tasks of this pair, in order.
 struct Schedule {
-  int64_t tasks;
-  int round = 0;
-  // Index of this CTA's next task, or -1.
-  __device__ __forceinline__ int64_t next() {
-    const int64_t grid = gridDim.x;
-    const int64_t at = (round & 1) ? grid - 1 - blockIdx.x : blockIdx.x;
-    const int64_t i = round++ * grid + at;
-    if (i < tasks) return i;
-    return -1;
+  uint32_t tasks, round;
+  __device__ __forceinline__ bool over() const { return round * (gridDim.x >> 1) >= tasks; }
+  // The walk of the next task that has one; false when there is none left.
+  __device__ __forceinline__ bool next(const KwArgs& a, Walk* w) {
+    const uint32_t pairs = gridDim.x >> 1, mine = blockIdx.x >> 1;
+    while (!over()) {
+      const uint32_t task = round * pairs + ((round & 1u) ? pairs - 1u - mine : mine);
+      ++round;
+      if (task >= tasks) continue;
+      const uint32_t kbp = a.div_bhk.div(task);
+      w->bhk = static_cast<int>(task - kbp * a.div_bhk.d);
+      const uint32_t kb = a.div_pieces.div(kbp);
+      w->piece = static_cast<int>(kbp - kb * a.div_pieces.d);
+      const uint32_t batch = a.div_hkv.div(static_cast<uint32_t>(w->bhk));
+      w->bhq0 = static_cast<int>(batch) * a.Hq +
+                (w->bhk - static_cast<int>(batch * a.div_hkv.d)) * a.G;
+      w->k0 = static_cast<int>(kb) * kTaskKeys;
+      const int qb_lo = a.span.first_qblock(w->k0);
+      const int last = w->k0 + kBlockN < a.span.Lk ? w->k0 + kBlockN : w->k0;
+      w->q_lo = qb_lo * kBlockM;
+      w->np = (max(0, a.span.last_qblock(last) - qb_lo + 1) + 1) / 2;
+      // pieces are as equal as the units allow, the longer ones first
+      const uint32_t all = static_cast<uint32_t>(a.G) * w->np;
+      const uint32_t len = a.div_pieces.div(all), extra = all - len * a.div_pieces.d;
+      const uint32_t p = static_cast<uint32_t>(w->piece);
+      w->u0 = static_cast<int>(p * len + min(p, extra));
+      w->u1 = static_cast<int>(w->u0 + len + (p < extra ? 1u : 0u));
+      return true;
+    }
+    return false;
   }
-  __device__ __forceinline__ bool over() const { return round * static_cast<int64_t>(gridDim.x) >= tasks; }
 };
 
-__device__ __forceinline__ Walk walk_of(const KwArgs& a, int64_t task) {
-  Walk w;
-  const int kbp = static_cast<int>(task / a.BHK);
-  w.bhk = static_cast<int>(task - static_cast<int64_t>(kbp) * a.BHK);
-  w.piece = kbp % a.pieces;
-  w.k0 = kbp / a.pieces * kTaskKeys;
-  w.qb_lo = a.span.first_qblock(w.k0);
-  const int last = w.k0 + kBlockN < a.span.Lk ? w.k0 + kBlockN : w.k0;
-  w.nq = max(0, a.span.last_qblock(last) - w.qb_lo + 1);
-  const int64_t all = static_cast<int64_t>(a.G) * w.nq;
-  w.u0 = static_cast<int>(all * w.piece / a.pieces);
-  w.u1 = static_cast<int>(all * (w.piece + 1) / a.pieces);
-  return w;
-}
-
-// Whether key tile `tile` of the walk's block is seen by query tile qb at all.
-struct TileSpan {
-  int lo, hi;
-};
-__device__ __forceinline__ TileSpan tile_span(const KwArgs& a, int k0, int tile) {
-  const int k = k0 + tile * kBlockN;
-  TileSpan t = {0, -1};
-  if (k < a.span.Lk) {
-    t.lo = a.span.first_qblock(k);
-    t.hi = a.span.last_qblock(k);
+// A walk's position: query head of the group and first query of the unit.
+struct UnitPos {
+  int gi, pi;
+  __device__ __forceinline__ explicit UnitPos(const Walk& w)
+      : gi(w.np > 0 ? w.u0 / w.np : 0), pi(w.np > 0 ? w.u0 % w.np : 0) {}
+  __device__ __forceinline__ void advance(const Walk& w) {
+    if (++pi == w.np) {
+      pi = 0;
+      ++gi;
+    }
   }
-  return t;
+  __device__ __forceinline__ int q0(const Walk& w) const { return w.q_lo + pi * kUnitQueries; }
+};
+
+// Pair products over kCols of the contraction: each CTA holds 128 rows of A and 128 of B, K-major in
+// 64-column chunks 16 KB apart (K-step ks starts 32 bytes further inside a chunk).
+template <int kCols>
+__device__ __forceinline__ void umma2_ss_rows128(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                                 uint32_t accumulate) {
+  static_assert(kCols == 64 || kCols == 128, "columns");
+  if constexpr (kCols == 128) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 ra, rb;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, %3, %3;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 ra, %1, 2;\n\tadd.s64 rb, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 4;\n\tadd.s64 rb, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 6;\n\tadd.s64 rb, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 1024;\n\tadd.s64 rb, %2, 1024;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 1026;\n\tadd.s64 rb, %2, 1026;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 1028;\n\tadd.s64 rb, %2, 1028;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 1030;\n\tadd.s64 rb, %2, 1030;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "}" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 ra, rb;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, %3, %3;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 ra, %1, 2;\n\tadd.s64 rb, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 4;\n\tadd.s64 rb, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "add.s64 ra, %1, 6;\n\tadd.s64 rb, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, t;\n\t"
+        "}" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(accumulate)
+        : "memory");
+  }
 }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kKwThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKwThreads, 1)
     swa_key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k, const KwArgs a) {
   using C = KwCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (!smem_base_ok(smem, a.err)) return;
+  // Both CTAs of the pair always reach the cluster barriers and the collective TMEM allocation; a
+  // misaligned window only disables the work (and is reported).
+  const bool smem_ok = (smem_u32(smem) & 1023u) == 0u;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   const uint32_t sK = smem_u32(smem), sQ = smem_u32(smem + C::kOffQ);
   const uint32_t warp = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_rank();
+  const bool lead = rank == 0u;
   const Span sp = a.span;
   if (threadIdx.x == 0) {
-    abort_flag = 0;
+    abort_flag = smem_ok ? 0 : 1;
+    if (!smem_ok) atomicOr(a.err, kErrSmemLayout);
+    const uint32_t full_count = lead ? 2u : 1u;  // rank 0: own copy and rank 1's relay
     for (int i = 0; i < C::kKSets; ++i) {
-      mbar_init(bar(C::kKFull + i), 1);
+      mbar_init(bar(C::kKFull + i), full_count);
       mbar_init(bar(C::kKEmpty + i), 1);
     }
     for (int i = 0; i < C::kQStages; ++i) {
-      mbar_init(bar(C::kQFull + i), 1);
+      mbar_init(bar(C::kQFull + i), full_count);
       mbar_init(bar(C::kQEmpty + i), 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(C::kSFull + i), 1);
-      mbar_init(bar(C::kSEmpty + i), kEpiWarps / 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kSFull + i), 2);  // the product, and its queries' log-sum-exps
+      mbar_init(bar(C::kSEmpty + i), 2 * kEpiWarps);
     }
-    for (int i = 0; i < kLseSlots; ++i) {
-      mbar_init(bar(C::kLFull + i), 1);
-      mbar_init(bar(C::kLEmpty + i), kEpiWarps);
-    }
+    for (int i = 0; i < kLseSlots; ++i) mbar_init(bar(C::kLEmpty + i), kEpiWarps);
+    mbar_init(bar(C::kRFull), kEpiWarps * 3 / 4);
+    mbar_init(bar(C::kREmpty), kEpiWarps / 4);
     mbar_init(bar(C::kDrain), 1);
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Schedule sched = {a.tasks};
+  Schedule sched = {a.tasks, 0u};
 
-  if (warp == kWarpQ) {
-    // ------------------------------------------------------------------ Q pieces
+  if (!smem_ok) {
+    // nothing to do: fall through to the final barrier and the collective release
+  } else if (warp == kWarpQ) {
+    // ------------------------------------------------------------------ this CTA's half of Q
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       int s = 0;
       uint32_t phase = 1;  // of the empty barriers: the first round does not wait
       bool ok = true;
       int64_t issued = 0;
-      while (ok && !sched.over()) {
-        const int64_t task = sched.next();
-        if (task < 0) continue;
-        const Walk w = walk_of(a, task);
-        const int bhq0 = w.bhk / a.Hkv * a.Hq + w.bhk % a.Hkv * a.G;
-        int gi = w.nq > 0 ? w.u0 / w.nq : 0, qi = w.nq > 0 ? w.u0 % w.nq : 0;
-        for (int u = w.u0; ok && u < w.u1; ++u) {
+      Walk w;
+      while (ok && sched.next(a, &w)) {
+        UnitPos pos(w);
+        for (int u = w.u0; ok && u < w.u1; ++u, pos.advance(w)) {
           for (int h = 0; h < C::kHalves; ++h) {
             if (!(ok = mbar_wait(bar(C::kQEmpty + s), phase, &abort_flag, a.err))) break;
             mbar_arrive_expect_tx(bar(C::kQFull + s), C::kPieceBytes);
             for (int x = 0; x < C::kChunks; ++x)
               tma_load_3d(sQ + s * C::kPieceBytes + x * C::kChunkBytes, &tm_q, bar(C::kQFull + s),
-                          128 * h + 64 * x, (w.qb_lo + qi) * kBlockM, bhq0 + gi);
+                          128 * h + 64 * x, pos.q0(w) + kBlockM * static_cast<int>(rank),
+                          w.bhq0 + pos.gi);
             ++issued;
             if (++s == C::kQStages) {
               s = 0;
               phase ^= 1u;
             }
-          }
-          if (++qi == w.nq) {
-            qi = 0;
-            ++gi;
           }
         }
       }
@@ -202,25 +268,21 @@ __global__ void __launch_bounds__(kKwThreads, 1)
                    static_cast<uint32_t>(i / C::kQStages) & 1u, a.err);
     }
   } else if (warp == kWarpK) {
-    // ------------------------------------------------------------------ K tiles
+    // ------------------------------------------------------------------ this CTA's keys
     if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       int64_t n = 0;
-      bool ok = true;
-      while (ok && !sched.over()) {
-        const int64_t task = sched.next();
-        if (task < 0) continue;
-        const Walk w = walk_of(a, task);
+      Walk w;
+      while (sched.next(a, &w)) {
         if (w.u0 == w.u1) continue;
         const int set = static_cast<int>(n % C::kKSets);
-        if (!(ok = mbar_wait(bar(C::kKEmpty + set), (static_cast<uint32_t>(n / C::kKSets) & 1u) ^ 1u,
-                             &abort_flag, a.err)))
+        if (!mbar_wait(bar(C::kKEmpty + set), (static_cast<uint32_t>(n / C::kKSets) & 1u) ^ 1u,
+                       &abort_flag, a.err))
           break;
-        mbar_arrive_expect_tx(bar(C::kKFull + set), 2 * C::kHalves * C::kPieceBytes);
-        for (int tile = 0; tile < 2; ++tile)
-          for (int x = 0; x < C::kHalves * C::kChunks; ++x)
-            tma_load_3d(sK + ((set * 2 + tile) * C::kHalves) * C::kPieceBytes + x * C::kChunkBytes,
-                        &tm_k, bar(C::kKFull + set), 64 * x, w.k0 + tile * kBlockN, w.bhk);
+        mbar_arrive_expect_tx(bar(C::kKFull + set), C::kTileBytes);
+        for (int x = 0; x < C::kHalves * C::kChunks; ++x)
+          tma_load_3d(sK + set * C::kTileBytes + x * C::kChunkBytes, &tm_k, bar(C::kKFull + set),
+                      64 * x, w.k0 + kBlockN * static_cast<int>(rank), w.bhk);
         ++n;
       }
       for (int64_t i = n > C::kKSets ? n - C::kKSets : 0; i < n; ++i)
@@ -228,203 +290,216 @@ __global__ void __launch_bounds__(kKwThreads, 1)
                    static_cast<uint32_t>(i / C::kKSets) & 1u, a.err);
     }
   } else if (warp == kWarpMma) {
-    // ------------------------------------------------------------------ products
-    constexpr uint32_t kId = idesc_f16kind(Elem<F16>::kMmaFmt, kBlockN, kBlockM, false, false);
+    // ------------------------------------------------------------------ products / relay
+    constexpr uint32_t kId =
+        idesc_f16kind(Elem<F16>::kMmaFmt, 2 * kBlockN, kUnitQueries, false, false);
+    // Rank 1 forwards each of its copies, in the order rank 0 takes them, to rank 0's barrier.
+    auto arrived = [&](int idx, uint32_t parity) -> bool {
+      if (lead) return warp_wait_cluster(bar(idx), parity, &abort_flag, a.err);
+      if (!warp_wait(bar(idx), parity, &abort_flag, a.err)) return false;
+      if (lane == 0) mbar_arrive_cluster(mapa_rank0(bar(idx)));
+      __syncwarp();
+      return true;
+    };
     int s = 0;
-    uint32_t qphase = 0;
+    uint32_t qphase = 0, used = 0;
     int64_t n = 0;
-    uint32_t used[2] = {0, 0};  // score tiles issued for each key tile
     bool ok = true;
-    while (ok && !sched.over()) {
-      const int64_t task = sched.next();
-      if (task < 0) continue;
-      const Walk w = walk_of(a, task);
+    Walk w;
+    while (ok && sched.next(a, &w)) {
       if (w.u0 == w.u1) continue;
       const int set = static_cast<int>(n % C::kKSets);
-      const TileSpan ts0 = tile_span(a, w.k0, 0), ts1 = tile_span(a, w.k0, 1);
-      if (!(ok = warp_wait(bar(C::kKFull + set), static_cast<uint32_t>(n / C::kKSets) & 1u,
-                           &abort_flag, a.err)))
-        break;
-      int qi = w.u0 % w.nq;
+      if (!(ok = arrived(C::kKFull + set, static_cast<uint32_t>(n / C::kKSets) & 1u))) break;
       for (int u = w.u0; ok && u < w.u1; ++u) {
-        const int qb = w.qb_lo + qi;
-        const bool on[2] = {qb >= ts0.lo && qb <= ts0.hi, qb >= ts1.lo && qb <= ts1.hi};
+        const uint32_t buf = used & 1u;
+        if (lead && !(ok = warp_wait_cluster(bar(C::kSEmpty + buf), ((used >> 1) & 1u) ^ 1u,
+                                             &abort_flag, a.err)))
+          break;
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h) {
-          if (!(ok = warp_wait(bar(C::kQFull + s), qphase, &abort_flag, a.err))) break;
-#pragma unroll
-          for (int tile = 0; tile < 2; ++tile) {
-            if (!ok || !on[tile]) continue;
-            const uint32_t buf = used[tile] & 1u;
-            if (h == 0 && !(ok = warp_wait(bar(C::kSEmpty + 2 * tile + buf),
-                                           ((used[tile] >> 1) & 1u) ^ 1u, &abort_flag, a.err)))
-              continue;
+          if (!(ok = arrived(C::kQFull + s, qphase))) break;
+          if (lead) {
             tc_fence_after();
-            umma_ss_kmajor_d<C::kCols>(
-                tmem + (2 * tile + buf) * 128u,
-                smem_desc_sw128(sK + ((set * 2 + tile) * C::kHalves + h) * C::kPieceBytes, 16, 1024),
+            umma2_ss_rows128<C::kCols>(
+                tmem + buf * 256u,
+                smem_desc_sw128(sK + set * C::kTileBytes + h * C::kPieceBytes, 16, 1024),
                 smem_desc_sw128(sQ + s * C::kPieceBytes, 16, 1024), kId, h > 0 ? 1u : 0u);
-            if (h == C::kHalves - 1) {
-              umma_commit_w(bar(C::kSFull + 2 * tile + buf));
-              ++used[tile];
-            }
+            if (h == C::kHalves - 1) umma2_commit_w(bar(C::kSFull + buf));
+            umma2_commit_w(bar(C::kQEmpty + s));
           }
-          if (!ok) break;
-          umma_commit_w(bar(C::kQEmpty + s));
           if (++s == C::kQStages) {
             s = 0;
             qphase ^= 1u;
           }
         }
-        if (++qi == w.nq) qi = 0;
+        ++used;
       }
       if (!ok) break;
-      umma_commit_w(bar(C::kKEmpty + set));
+      if (lead) umma2_commit_w(bar(C::kKEmpty + set));
       ++n;
     }
-    umma_commit_w(bar(C::kDrain));
-    warp_drain_wait(bar(C::kDrain), 0, a.err);
+    if (lead) {
+      umma2_commit_w(bar(C::kDrain));
+      warp_drain_wait(bar(C::kDrain), 0, a.err);
+    }
   } else if (warp == kWarpLse) {
-    // ------------------------------------------------------------------ -lse / ln 2, a slot per query tile
+    // ------------------------------------------------------------------ -lse / ln 2, a slot per unit
+    // Slot n mod 4 holds unit n; the two S full barriers alternate, so unit n's is announced only when
+    // unit n - 2's score buffer has been handed back by everyone (its phase has then completed).
     float* s_lse = reinterpret_cast<float*>(smem + C::kOffLse);
-    int s = 0;
-    uint32_t phase = 1;
+    uint32_t n = 0;
     bool ok = true;
-    while (ok && !sched.over()) {
-      const int64_t task = sched.next();
-      if (task < 0) continue;
-      const Walk w = walk_of(a, task);
-      const int bhq0 = w.bhk / a.Hkv * a.Hq + w.bhk % a.Hkv * a.G;
-      int gi = w.nq > 0 ? w.u0 / w.nq : 0, qi = w.nq > 0 ? w.u0 % w.nq : 0;
-      for (int u = w.u0; u < w.u1; ++u) {
-        float y[4];
-        const int q0 = (w.qb_lo + qi) * kBlockM + static_cast<int>(lane);
-        const float* row = a.lse + static_cast<size_t>(bhq0 + gi) * sp.Lq;
+    Walk w;
+    while (ok && sched.next(a, &w)) {
+      UnitPos pos(w);
+      float y[8];  // the next unit's, on their way while this one's slot is waited for
+      auto fetch = [&]() {
+        const int q0 = pos.q0(w) + static_cast<int>(lane);
+        const float* row = a.lse + static_cast<size_t>(w.bhq0 + pos.gi) * sp.Lq;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // queries past the end weigh nothing
-          y[i] = q0 + 32 * i < sp.Lq ? -kLog2e * __ldg(row + q0 + 32 * i) : SWA_NEG_INF;
-        if (!(ok = warp_wait(bar(C::kLEmpty + s), phase, &abort_flag, a.err))) break;
+        for (int i = 0; i < 8; ++i)  // queries past the end weigh nothing
+          y[i] = q0 + 32 * i < sp.Lq ? __ldg(row + q0 + 32 * i) : SWA_POS_INF;
+      };
+      if (w.u0 < w.u1) fetch();
+      for (int u = w.u0; u < w.u1; ++u, ++n) {
+        const int s = static_cast<int>(n % kLseSlots);
+        if (!(ok = warp_wait(bar(C::kLEmpty + s), ((n / kLseSlots) & 1u) ^ 1u, &abort_flag, a.err)))
+          break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_lse[s * 128 + 32 * i + lane] = y[i];
+        for (int i = 0; i < 8; ++i) s_lse[s * kUnitQueries + 32 * i + lane] = -kLog2e * y[i];
+        pos.advance(w);
+        if (u + 1 < w.u1) fetch();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::kLFull + s));
-        if (++s == kLseSlots) {
-          s = 0;
-          phase ^= 1u;
-        }
-        if (++qi == w.nq) {
-          qi = 0;
-          ++gi;
-        }
+        // S full of unit n - 2 must be over before this arrival counts for unit n.
+        if (n >= 2 && !(ok = warp_wait(bar(C::kSFull + (n & 1u)), ((n >> 1) & 1u) ^ 1u, &abort_flag,
+                                       a.err)))
+          break;
+        if (lane == 0) mbar_arrive(bar(C::kSFull + (n & 1u)));
       }
     }
   } else {
     // ------------------------------------------------------------------ exponentials and sums
-    const int tile = static_cast<int>(warp >> 2) & 1, half = static_cast<int>(warp >> 3);
-    const int r = static_cast<int>((warp & 3u) * 32 + lane);  // key row of the tile
-    const uint32_t lane_base = ((warp & 3u) * 32u) << 16;
-    const float* s_lse = reinterpret_cast<const float*>(smem + C::kOffLse) + 64 * half;
-    float* s_red = reinterpret_cast<float*>(smem + C::kOffRed) + 128 * tile;
+    const int group = static_cast<int>(warp >> 2);            // 64 of a unit's 256 queries
+    const int r = static_cast<int>((warp & 3u) * 32 + lane);  // key row of the CTA's tile
+    const uint32_t col0 = tmem + (((warp & 3u) * 32u) << 16) + 64u * group;
+    const float* s_lse = reinterpret_cast<const float*>(smem + C::kOffLse) + 64 * group;
+    float* s_red = reinterpret_cast<float*>(smem + C::kOffRed);
     const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
-    int s = 0;
-    uint32_t lphase = 0, used = 0;
+    uint32_t n = 0, rphase = 0;  // units walked so far
+    Walk w;
     bool ok = true;
-    while (!sched.over()) {  // to the end even after a wait ran out: the barriers below count on it
-      const int64_t task = sched.next();
-      if (task < 0) continue;
-      const Walk w = walk_of(a, task);
-      const TileSpan ts = tile_span(a, w.k0, tile);
-      const int key = w.k0 + tile * kBlockN + r;
-      const int vis_lo = key + sp.dmin - sp.off;
-      const int vis_hi = static_cast<int>(
-          min(static_cast<long long>(key) + sp.dmax - sp.off, static_cast<long long>(sp.Lq)));
-      const int k0t = w.k0 + tile * kBlockN;
-      // A query tile at q0 needs no mask iff q_int_lo <= q0 <= q_int_hi.
-      const int q_int_lo = k0t + kBlockN - 1 + sp.dmin - sp.off;
-      const long long q_int_hi = static_cast<long long>(k0t) + sp.dmax - sp.off - (kBlockM - 1);
+    while (ok && sched.next(a, &w)) {
+      const int key = w.k0 + kBlockN * static_cast<int>(rank) + r;
+      // Queries that this key sees, that some key of the warp sees, and that every one sees.
+      const int key0 = key - static_cast<int>(lane);
+      const auto upto = [&](int k) {
+        return static_cast<int>(min(static_cast<long long>(k) + sp.dmax - sp.off,
+                                    static_cast<long long>(sp.Lq) - 1));
+      };
+      const int vis_lo = key + sp.dmin - sp.off, vis_hi = upto(key);
+      const int some_lo = key0 + sp.dmin - sp.off;
+      const int some_hi = key0 < sp.Lk ? upto(key0 + 31) : -1;
+      const int all_lo = some_lo + 31;
+      const int all_hi = static_cast<int>(
+          min(static_cast<long long>(key0) + sp.dmax - sp.off, static_cast<long long>(INT_MAX)));
       float sum = 0.f, comp = 0.f;
-      int qi = w.nq > 0 ? w.u0 % w.nq : 0;
-      for (int u = w.u0; ok && u < w.u1; ++u) {
-        const int qb = w.qb_lo + qi;
-        if (!(ok = warp_wait(bar(C::kLFull + s), lphase, &abort_flag, a.err))) break;
-        if (qb >= ts.lo && qb <= ts.hi) {
-          const uint32_t buf = used & 1u;
-          if (!(ok = warp_wait(bar(C::kSFull + 2 * tile + buf), (used >> 1) & 1u, &abort_flag,
-                               a.err)))
-            break;
-          tc_fence_after();
-          uint32_t rr[2][32];
-          const uint32_t col = tmem + lane_base + (2 * tile + buf) * 128u + 64u * half;
-          tmem_ld32(col, rr[0]);
-          tmem_ld32(col + 32u, rr[1]);
-          tmem_wait_ld_all();
-          reg_fence(rr[0]);
-          reg_fence(rr[1]);
-          warp_arrive(bar(C::kSEmpty + 2 * tile + buf));
-          ++used;
-          const float4* l4 = reinterpret_cast<const float4*>(s_lse + s * 128);
-          float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-          const int q0 = qb * kBlockM;
-          if (q0 >= q_int_lo && q0 <= q_int_hi) {
+      UnitPos pos(w);
+      for (int u = w.u0; u < w.u1; ++u, ++n) {
+        const uint32_t buf = n & 1u;
+        const int qw = pos.q0(w) + 64 * group;
+        const int slot = static_cast<int>(n % kLseSlots);
+        if (!(ok = warp_wait(bar(C::kSFull + buf), (n >> 1) & 1u, &abort_flag, a.err))) break;
+        if (qw > some_hi || qw + 63 < some_lo) {
+          warp_arrive_rank0(bar(C::kSEmpty + buf));
+          if (lane == 0) mbar_arrive(bar(C::kLEmpty + slot));
+          pos.advance(w);
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t col = col0 + buf * 256u;
+        const float4* l4 = reinterpret_cast<const float4*>(s_lse + slot * kUnitQueries);
+        uint32_t raw[32];  // 32 scores at a time: registers for more of them would spill
+        tmem_ld32(col, raw);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+        const bool late = qw < all_lo, early = qw + 63 > all_hi;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float4 l = l4[i];
-              const uint32_t* src = &rr[i >> 3][(4 * i) & 31];
-              const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])),
-                                           c2, make_float2(l.x, l.y));
-              const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(src[2]), __uint_as_float(src[3])),
-                                           c2, make_float2(l.z, l.w));
-              acc0 = __fadd2_rn(acc0, make_float2(ex2(x0.x), ex2(x0.y)));
-              acc1 = __fadd2_rn(acc1, make_float2(ex2(x1.x), ex2(x1.y)));
+        for (int c = 0; c < 2; ++c) {
+          tmem_wait_ld(raw);
+          if (c == 1) warp_arrive_rank0(bar(C::kSEmpty + buf));
+          float2 x[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 l = l4[8 * c + i];
+            x[2 * i] = __ffma2_rn(
+                make_float2(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1])), c2,
+                make_float2(l.x, l.y));
+            x[2 * i + 1] = __ffma2_rn(
+                make_float2(__uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3])), c2,
+                make_float2(l.z, l.w));
+          }
+          // At the window's edges the queries that this key does not see are masked, from either side
+          // (one branch around both: more of them keep the two halves from interleaving).
+          if (late || early) {
+            if (late) {
+              const int lo = vis_lo - qw - 32 * c;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                x[i].x = 2 * i >= lo ? x[i].x : SWA_NEG_INF;
+                x[i].y = 2 * i + 1 >= lo ? x[i].y : SWA_NEG_INF;
+              }
             }
-          } else {
-            const int base = q0 + 64 * half;
-            const int lo = vis_lo - base, hi = vis_hi - base;
+            if (early) {
+              const int hi = vis_hi - qw - 32 * c;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float4 l = l4[i];
-              const uint32_t* src = &rr[i >> 3][(4 * i) & 31];
-              const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])),
-                                           c2, make_float2(l.x, l.y));
-              const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(src[2]), __uint_as_float(src[3])),
-                                           c2, make_float2(l.z, l.w));
-              float2 p0, p1;
-              p0.x = 4 * i >= lo && 4 * i <= hi ? ex2(x0.x) : 0.f;
-              p0.y = 4 * i + 1 >= lo && 4 * i + 1 <= hi ? ex2(x0.y) : 0.f;
-              p1.x = 4 * i + 2 >= lo && 4 * i + 2 <= hi ? ex2(x1.x) : 0.f;
-              p1.y = 4 * i + 3 >= lo && 4 * i + 3 <= hi ? ex2(x1.y) : 0.f;
-              acc0 = __fadd2_rn(acc0, p0);
-              acc1 = __fadd2_rn(acc1, p1);
+              for (int i = 0; i < 16; ++i) {
+                x[i].x = 2 * i <= hi ? x[i].x : SWA_NEG_INF;
+                x[i].y = 2 * i + 1 <= hi ? x[i].y : SWA_NEG_INF;
+              }
             }
           }
-          const float2 both = __fadd2_rn(acc0, acc1);
-          const float add = __fsub_rn(__fadd_rn(both.x, both.y), comp);
-          const float next = __fadd_rn(sum, add);
-          comp = __fsub_rn(__fsub_rn(next, sum), add);
-          sum = next;
+          if (c == 0) tmem_ld32(col + 32u, raw);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            acc0 = __fadd2_rn(acc0, make_float2(ex2(x[i].x), ex2(x[i].y)));
+            acc1 = __fadd2_rn(acc1, make_float2(ex2(x[i + 1].x), ex2(x[i + 1].y)));
+          }
         }
+        const float2 both = __fadd2_rn(acc0, acc1);
+        const float add = __fadd_rn(both.x, both.y);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::kLEmpty + s));
-        if (++s == kLseSlots) {
-          s = 0;
-          lphase ^= 1u;
-        }
-        if (++qi == w.nq) qi = 0;
+        if (lane == 0) mbar_arrive(bar(C::kLEmpty + slot));
+        pos.advance(w);
+        const float term = __fsub_rn(add, comp);
+        const float next = __fadd_rn(sum, term);
+        comp = __fsub_rn(__fsub_rn(next, sum), term);
+        sum = next;
       }
-      // The two column halves of a key meet.
-      if (half == 1) s_red[r] = sum;
-      named_barrier_sync(1 + tile, 256);
-      if (half == 0 && key < sp.Lk)
-        a.w[(static_cast<size_t>(w.piece) * a.BHK + w.bhk) * sp.Lk + key] = sum + s_red[r];
-      named_barrier_sync(1 + tile, 256);
+      if (!ok) break;
+      // The four groups of a key's sum meet at the first's threads.
+      if (group != 0) {
+        if (!(ok = warp_wait(bar(C::kREmpty), rphase ^ 1u, &abort_flag, a.err))) break;
+        s_red[(group - 1) * 128 + r] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kRFull));
+      } else {
+        if (!(ok = warp_wait(bar(C::kRFull), rphase, &abort_flag, a.err))) break;
+        sum = (sum + s_red[r]) + (s_red[128 + r] + s_red[256 + r]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kREmpty));
+        if (key < sp.Lk)
+          a.w[(static_cast<size_t>(w.piece) * a.BHK + w.bhk) * sp.Lk + key] = sum;
+      }
+      rphase ^= 1u;
     }
   }
 
+  // Every cross-CTA arrival and every pair product (rank 0 waited for its drain) is complete once both
+  // CTAs are here; then the pair releases its TMEM together.
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();
   if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -442,16 +517,17 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Pieces that each walk is cut into: eight tasks for every SM even out walks of unequal length, and a
-// piece has at least one (query head, query tile) pair.
+// Pieces that each walk is cut into: eight tasks for every pair of SMs even out walks of unequal
+// length, and a piece has at least one unit.
 int pieces_of(const Problem& pb) {
   const int64_t blocks =
       static_cast<int64_t>((pb.span.Lk + kTaskKeys - 1) / kTaskKeys) * pb.B * pb.Hkv;
-  const int64_t want = (8ll * sm_count() + blocks - 1) / blocks;
+  const int64_t want = (8ll * (sm_count() / 2) + blocks - 1) / blocks;
   // queries that a block of keys can see
   const int64_t reach = static_cast<int64_t>(pb.span.dmax) - pb.span.dmin + kTaskKeys;
-  const int64_t tiles = ((reach < pb.span.Lq ? reach : pb.span.Lq) + kBlockM - 1) / kBlockM;
-  const int64_t most = tiles * (pb.Hq / pb.Hkv);
+  const int64_t units =
+      ((reach < pb.span.Lq ? reach : pb.span.Lq) + kUnitQueries - 1) / kUnitQueries;
+  const int64_t most = units * (pb.Hq / pb.Hkv);
   return static_cast<int>(want < most ? want : most);
 }
 
@@ -471,18 +547,25 @@ cudaError_t launch_d(const Problem& pb, const void* q, const void* k, const floa
   a.lse = lse;
   a.BHK = static_cast<int>(bhk);
   a.Hq = pb.Hq;
-  a.Hkv = pb.Hkv;
   a.G = pb.Hq / pb.Hkv;
-  a.pieces = pieces_of(pb);
-  a.w = a.pieces > 1 ? workspace : w;
-  a.tasks = static_cast<int64_t>((pb.span.Lk + kTaskKeys - 1) / kTaskKeys) * a.pieces * a.BHK;
+  const int pieces = pieces_of(pb);
+  a.w = pieces > 1 ? workspace : w;
+  const int64_t tasks = static_cast<int64_t>((pb.span.Lk + kTaskKeys - 1) / kTaskKeys) * pieces * a.BHK;
+  // Task indices (and rounds of them) stay below 2^31: B Hkv Lk < 2^31 keys make at most 2^23 blocks
+  // of full walks, and pieces are only cut while there are fewer tasks than that.
+  if (tasks >= (1ll << 30)) return cudaErrorInvalidValue;
+  a.tasks = static_cast<uint32_t>(tasks);
+  a.div_bhk = FastDiv(static_cast<uint32_t>(a.BHK));
+  a.div_pieces = FastDiv(static_cast<uint32_t>(pieces));
+  a.div_hkv = FastDiv(static_cast<uint32_t>(pb.Hkv));
   a.span = pb.span;
   a.scale_log2 = pb.scale * kLog2e;
   a.err = pb.err;
   const int64_t sms = sm_count();
-  const unsigned grid = static_cast<unsigned>(a.tasks < sms ? a.tasks : sms);
+  const int64_t pairs = max_pair_clusters<swa_key_weights_kernel<D, F16>>(kKwThreads, C::kSmemBytes);
+  const unsigned grid = static_cast<unsigned>(2 * (a.tasks < pairs ? a.tasks : pairs));
   kern<<<grid, kKwThreads, C::kSmemBytes, stream>>>(tq, tk, a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.pieces == 1) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || pieces == 1) return e;
   const int64_t n = static_cast<int64_t>(a.BHK) * pb.span.Lk;
   const int64_t blocks = (n + 255) / 256;
   cudaLaunchConfig_t cfg = {};
@@ -495,7 +578,7 @@ cudaError_t launch_d(const Problem& pb, const void* q, const void* k, const floa
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, swa_key_weights_join_kernel, static_cast<const float*>(workspace),
-                            w, n, a.pieces);
+                            w, n, pieces);
 }
 
 }  // namespace
