@@ -54,7 +54,7 @@ typedef struct swa_cache {
 /*
  * Append: quantises n_b new tokens of each sequence into slots lens[b] .. lens[b] + n_b - 1.
  *   table    : int32 [B, max_pages]; the entries of the pages written must name pages that no other
- *              sequence holds.
+ *              sequence holds, each once.
  *   lens     : int32 [B], tokens cached before.
  *   new_lens : int32 [B], n_b in 0..T, or NULL: n_b = T.
  *   k, v     : [B, Hkv, T, D] in `dtype` (bf16, fp16 or fp32); tokens n_b.. of a row are not read
@@ -85,14 +85,18 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  * window, and table entries behind the last token, are not read: a sliding layer's caller may reuse
  * them.
  *   accumulate : 1 -> weight of every cached token += the sum of its p over the T queries and the
- *                Hq / Hkv query heads of its kv head (needs cache->weight); 0 -> weights untouched.
+ *                Hq / Hkv query heads of its kv head (needs cache->weight; the tables must then name
+ *                each page once: two sequences that share one would add to the same weights at the
+ *                same time); 0 -> weights untouched, and pages may be shared.
  *   workspace  : at least swa_cache_attn_workspace_bytes bytes, 16-byte aligned; nothing is kept
  *                there between calls.  Calls that may overlap (other streams, graphs replayed at
  *                once) need workspaces of their own.
+ * A key that a query does not see changes nothing for it, NaN included; where some queries of a call
+ * see a token and others do not, this takes values that are finite, as append stores them.
  * Scores, softmax statistics and sums are fp32.  q is taken as fp16 operands after scaling each row
- * by a power of two (exact for bf16 and fp16 values within 2^-24 of the row's largest), codes are
- * exact in fp16, and p is rounded to fp16 as the second product's operand.  Results are
- * bit-reproducible on one GPU.
+ * by a power of two (exact for bf16 and fp16 values down to 2^-28 of the row's largest, and below
+ * that within 2^-39 of the largest), codes are exact in fp16, and p is rounded to fp16 as the second product's operand (relative 2^-11, half the
+ * step of an fp16 result).  Results are bit-reproducible on one GPU.
  */
 size_t swa_cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
                                       int page, int accumulate);
@@ -129,7 +133,8 @@ swa_status swa_cache_evict(const swa_cache* cache, const int* table, int max_pag
  *   workspace : at least swa_attn_key_weights_workspace_bytes bytes (0 for many keys: it may then be
  *               NULL), 16-byte aligned; nothing is kept there between calls.  Calls that may overlap
  *               need workspaces of their own.
- * The N x N weights are never stored; scores, exponentials and sums are fp32.  Bit-reproducible.
+ * B Hkv ceil(Lk / 256) must stay below 2^30.  The N x N weights are never stored; scores, exponentials
+ * and sums are fp32.  Bit-reproducible on one GPU.
  */
 size_t swa_attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D,
                                             int window, int causal);

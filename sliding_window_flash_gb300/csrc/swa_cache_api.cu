@@ -60,7 +60,8 @@ swa_status check_key_weights(int B, int Hq, int Hkv, int Lq, int Lk, int D, int 
   if (!(scale > 0.f) || !std::isfinite(scale)) return SWA_ERR_INVALID_ARG;
   if (D != 64 && D != 128 && D != 256) return SWA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * Hq * Lq >= kIndexLimit ||
-      static_cast<long long>(B) * Hkv * Lk >= kIndexLimit)
+      static_cast<long long>(B) * Hkv * Lk >= kIndexLimit ||
+      static_cast<long long>(B) * Hkv * ((static_cast<long long>(Lk) + 255) / 256) >= kIndexLimit / 2)
     return SWA_ERR_INVALID_ARG;
   return SWA_OK;
 }

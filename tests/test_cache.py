@@ -153,6 +153,10 @@ ATTN = [
     (5, 4, 4, 128, 64, 1, [0, 31, 4000, 32, 95], 10000, None, torch.bfloat16, True),
     (40, 2, 1, 64, 32, 1, [3 * i for i in range(40)], 50, None, torch.float16, True),
     (1, 2, 1, 128, 64, 1, [20000], 30000, None, torch.bfloat16, True),
+    # so many rows that a warp joins each
+    (4, 64, 16, 128, 64, 4, [900, 350, 0, 620], 2000, None, torch.bfloat16, True),
+    (4, 32, 16, 256, 128, 5, [300, 350, 128, 620], 200, [5, 0, 3, 1], torch.float16, True),
+    (9, 40, 20, 64, 32, 2, [100 + 61 * i for i in range(9)], 500, None, torch.bfloat16, True),
 ]
 
 
@@ -524,3 +528,196 @@ def test_evict_long(swa, B, H, page, longest, budget, recent):
         assert torch.equal(kept[b].long(), want)
         moved = cache.weight[dst[b].long()].transpose(0, 1).reshape(H, -1)[:, :budget]
         assert torch.equal(moved, torch.gather(w[b], 1, want))
+
+
+# ---- further corners ---------------------------------------------------------------------------
+
+def test_append_fp16_ends(swa):
+    """fp16's largest and subnormal numbers, alone and beside older tokens of a far larger scale,
+    where the new codes vanish or the old ones do."""
+    g = _gen(61)
+    D, page = 64, 32
+    cache = swa.SwaCache.empty(6, 1, D, page)
+    table = _ints([[4, 0, 2, 5, 1, 3]])
+    pool = ref.pool_of(cache)
+
+    def put(lens, k, v):
+        ref.append(pool, table, lens, k, v)
+        swa.swa_cache_append(cache, table, _ints(lens), k, v)
+        swa.swa_check_device()
+        _same_pool(cache, pool)
+
+    def rand(n, scale, dtype):
+        x = torch.randn((1, 1, n, D), generator=g, device="cuda") * scale
+        return x.to(dtype)
+
+    put([0], rand(5, 1e4, torch.float16).clamp(-65504, 65504), rand(5, 2.0**-22, torch.float16))
+    put([5], rand(5, 2.0**-20, torch.float16), rand(5, 1.0, torch.float16))
+    put([10], rand(5, 1e9, torch.bfloat16), rand(5, 1e-12, torch.bfloat16))
+    put([15], rand(5, 1.0, torch.float16), rand(5, 6e4, torch.float16).clamp(-65504, 65504))
+    put([20], rand(5, 60.0, torch.bfloat16), rand(5, 1e13, torch.bfloat16))
+    put([25], rand(60, 2.0**-14, torch.float16), rand(60, 1e-3, torch.float16))
+    put([85], rand(20, 1e-20, torch.float32), rand(20, 1e-30, torch.float32))
+    edge = torch.tensor([448.0 * 2**-10, 2.0**-24, 3 * 2.0**-24, 2.0**-14, 2.0**-19, 2.0**-20, 0.0, -0.0])
+    e = edge.repeat(D // 8).view(1, 1, 1, D).cuda()
+    put([105], e.half(), -e.half())
+
+
+def test_attn_many_sequences(swa):
+    """More sequences than one launch takes."""
+    g = _gen(62)
+    B, width, page, D = 2100, 2, 32, 64
+    cache = _cache(swa, g, B * width, 1, D, page)
+    table = _table(g, B, width)
+    lens = [(7 * i) % 60 for i in range(B)]
+    q = torch.randn((B, 2, 1, D), generator=g, device="cuda").bfloat16()
+    pool = ref.pool_of(cache)
+    o, lse, to, tl, tw = ref.attn(pool, table, lens, q, 40, accumulate=True)
+    go, gl = swa.swa_cache_attn(q, cache, table, _ints(lens), 40, accumulate=True)
+    swa.swa_check_device()
+    _near(go, o, to, "o")
+    _near(gl, lse, tl, "lse")
+    _near(cache.weight, pool["weight"], tw, "weight")
+
+
+def test_offsets_past_32_bits(swa):
+    """A pool of more than 2^32 bytes: the last pages, through append, attention and eviction."""
+    g = _gen(63)
+    pages, H, page, D = 34000, 16, 64, 128  # 4.46e9 bytes of keys
+    cache = swa.SwaCache.empty(pages, H, D, page)
+    last = pages - 8
+    table = _ints([[last + 3, last, last + 5], [7, last + 1, 9]])
+    dst = _ints([[last + 2, last + 7], [last + 4, 1]])
+    T = 150
+    k = torch.randn((2, H, T, D), generator=g, device="cuda").bfloat16()
+    v = torch.randn((2, H, T, D), generator=g, device="cuda").bfloat16()
+    w = torch.rand((2, H, T), generator=g, device="cuda")
+    swa.swa_cache_append(cache, table, _ints([0, 0]), k, v, weight=w)
+    small = swa.SwaCache.empty(8, H, D, page)
+    stable, sdst = _ints([[0, 1, 2], [3, 4, 5]]), _ints([[6, 7], [6, 7]])
+    swa.swa_cache_append(small, stable, _ints([0, 0]), k, v, weight=w)
+    q = torch.randn((2, 2 * H, 1, D), generator=g, device="cuda").bfloat16()
+    lens = _ints([149, 149])
+    a = swa.swa_cache_attn(q, cache, table, lens, 1000, accumulate=True)
+    b = swa.swa_cache_attn(q, small, stable, lens, 1000, accumulate=True)
+    swa.swa_check_device()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    kept, _ = swa.swa_cache_evict(cache, table, _ints([150, 150]), dst, 100, 10)
+    skept, _ = swa.swa_cache_evict(small, stable[:1], _ints([150]), sdst[:1], 100, 10)
+    swa.swa_check_device()
+    assert torch.equal(kept[:1], skept)
+    for i in range(2):
+        rows = 64 if i == 0 else 36
+        for x, y in ((cache.k, small.k), (cache.v, small.v)):
+            assert torch.equal(x[int(dst[0, i])].view(torch.uint8)[:, :rows],
+                               y[int(sdst[0, i])].view(torch.uint8)[:, :rows])
+
+
+def test_calls_on_two_streams(swa):
+    """Two sequences' steps on two streams at once, each with buffers of its own, equal the same steps
+    one after the other."""
+    g = _gen(64)
+    H, D, page, n = 4, 128, 64, 12
+
+    def state(seed):
+        gg = _gen(seed)
+        c = _cache(swa, gg, 64, H, D, page)
+        return c, _table(gg, 1, 60), _ints([1500 + seed])
+
+    ks = torch.randn((2, n, 1, H, 1, D), generator=g, device="cuda").bfloat16()
+    qs = torch.randn((2, n, 1, 3 * H, 1, D), generator=g, device="cuda").half()
+
+    def step(st, i, j):
+        c, table, lens = st
+        swa.swa_cache_append(c, table, lens, ks[j, i], ks[j, i])
+        r = swa.swa_cache_attn(qs[j, i], c, table, lens, 1 << 20, accumulate=True)
+        lens += 1
+        return r
+
+    want = []
+    for j in range(2):
+        st = state(j)
+        want.append([step(st, i, j) for i in range(n)] + [st[0].weight.clone()])
+    states = [state(0), state(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for i in range(n):
+        for j in range(2):
+            with torch.cuda.stream(streams[j]):
+                got[j].append(step(states[j], i, j))
+    torch.cuda.synchronize()
+    swa.swa_check_device()
+    for j in range(2):
+        for a, b in zip(got[j], want[j]):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        assert torch.equal(states[j][0].weight, want[j][-1])
+
+
+def test_evict_and_weights_in_a_graph(swa):
+    """A captured prompt (forward, key weights, append) and eviction replayed on other inputs."""
+    g = _gen(65)
+    N, Hq, H, D, page, budget = 500, 4, 2, 64, 32, 100
+    cache = swa.SwaCache.empty(40, H, D, page)
+    table = torch.arange(16, dtype=torch.int32, device="cuda").view(1, 16)
+    dst = torch.arange(20, 24, dtype=torch.int32, device="cuda").view(1, 4)
+    zero, full = _ints([0]), _ints([N])
+
+    def draw():
+        return [torch.randn((1, h, N, D), generator=g, device="cuda").bfloat16() for h in (Hq, H, H)]
+
+    def run(q, k, v):
+        _, lse = swa.swa_attn_fwd(q, k, v, 128)
+        w = swa.swa_attn_key_weights(q, k, lse, 128)
+        swa.swa_cache_append(cache, table, zero, k, v, weight=w)
+        kept, lens = swa.swa_cache_evict(cache, table, full, dst, budget, 16)
+        return w, kept, lens
+
+    a, b = draw(), draw()
+    want = []
+    for x in (a, b):
+        r = run(*x)
+        want.append([t.clone() for t in r] + [cache.k.view(torch.uint8).clone()])
+    held = [t.clone() for t in a]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(*held)
+    for x, y in ((a, want[0]), (b, want[1])):
+        for h, t in zip(held, x):
+            h.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, r in zip(out, y):
+            assert torch.equal(p, r)
+        assert torch.equal(cache.k.view(torch.uint8), y[-1])
+    swa.swa_check_device()
+
+
+@pytest.mark.parametrize("B,Hq,H,L,D,window", [
+    (1, 16, 2, 5000, 128, 700), (1, 8, 8, 3000, 256, 3000), (3, 4, 4, 2049, 64, 100),
+    (1, 32, 16, 9000, 128, 1024),
+])
+def test_key_weights_long(swa, B, Hq, H, L, D, window):
+    """Many tasks a pair, full and cut walks, against 64-bit sums on the GPU."""
+    g = _gen(L)
+    q = torch.randn((B, Hq, L, D), generator=g, device="cuda").bfloat16()
+    k = torch.randn((B, H, L, D), generator=g, device="cuda").bfloat16()
+    lse = torch.empty((B, Hq, L), device="cuda")
+    want = torch.zeros((B, H, L), dtype=torch.float64, device="cuda")
+    for b in range(B):
+        for h in range(Hq):
+            for i in range(0, L, 1024):
+                z, lo = min(L, i + 1024), max(0, i - window + 1)
+                x = q[b, h, i:z].double() @ k[b, h // (Hq // H), lo:z].double().T / math.sqrt(D)
+                d = torch.arange(i, z, device="cuda")[:, None] - torch.arange(lo, z, device="cuda")
+                x = x.masked_fill((d < 0) | (d >= window), -math.inf)
+                lse[b, h, i:z] = torch.logsumexp(x, -1).float()
+                want[b, h // (Hq // H), lo:z] += torch.exp(x - lse[b, h, i:z, None].double()).sum(0)
+    got = swa.swa_attn_key_weights(q, k, lse, window)
+    swa.swa_check_device()
+    # a score is an fp32 sum of D products and a scaling, so off by at most (D + 8) 2^-24 of
+    # scale |q| |k| (Cauchy-Schwarz); lse's product with log2(e), the exponential and the sum of the
+    # weights (compensated) add a few 2^-21
+    es = (D + 8) * 2.0**-24 / math.sqrt(D) * float(q.float().norm(dim=-1).max() *
+                                                   k.float().norm(dim=-1).max())
+    assert ((got.double() - want).abs() <= (2 * es + 2.0**-18) * want + 1e-30).all()
