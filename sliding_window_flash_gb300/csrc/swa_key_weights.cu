@@ -24,7 +24,6 @@
 //     one another for the wait on the same scores; products alone would take 0.135 ms.
 //   * Masked parts select; whatever a query outside the window holds does not reach the sum.  64 terms
 //     are added in fp32, then into a compensated sum (Kahan), so the error does not grow with the walk.
-#include <climits>
 #include <type_traits>
 
 #include "swa_cache_kernels.h"
@@ -390,18 +389,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKwThreads, 1)
     bool ok = true;
     while (ok && sched.next(a, &w)) {
       const int key = w.k0 + kBlockN * static_cast<int>(rank) + r;
-      // Queries that this key sees, that some key of the warp sees, and that every one sees.
+      // This lane's key sees queries vis_lo .. vis_hi; some key of the warp sees vis_lo - lane ..
+      // vis_hi - lane + 31, every one vis_lo - lane + 31 .. vis_hi - lane.
+      const int vis_lo = key + sp.dmin - sp.off;
+      // (vis_hi - lane is cut off behind the last query, the same for the whole warp.)
       const int key0 = key - static_cast<int>(lane);
-      const auto upto = [&](int k) {
-        return static_cast<int>(min(static_cast<long long>(k) + sp.dmax - sp.off,
-                                    static_cast<long long>(sp.Lq) - 1));
-      };
-      const int vis_lo = key + sp.dmin - sp.off, vis_hi = upto(key);
-      const int some_lo = key0 + sp.dmin - sp.off;
-      const int some_hi = key0 < sp.Lk ? upto(key0 + 31) : -1;
-      const int all_lo = some_lo + 31;
-      const int all_hi = static_cast<int>(
-          min(static_cast<long long>(key0) + sp.dmax - sp.off, static_cast<long long>(INT_MAX)));
+      const int vis_hi = static_cast<int>(lane) +
+                         (key0 < sp.Lk
+                              ? static_cast<int>(min(static_cast<long long>(key0) + sp.dmax - sp.off,
+                                                     static_cast<long long>(sp.Lq) + 63))
+                              : -64);  // a warp without keys: everything is skipped
       float sum = 0.f, comp = 0.f;
       UnitPos pos(w);
       for (int u = w.u0; u < w.u1; ++u, ++n) {
@@ -409,7 +406,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKwThreads, 1)
         const int qw = pos.q0(w) + 64 * group;
         const int slot = static_cast<int>(n % kLseSlots);
         if (!(ok = warp_wait(bar(C::kSFull + buf), (n >> 1) & 1u, &abort_flag, a.err))) break;
-        if (qw > some_hi || qw + 63 < some_lo) {
+        const int rel_lo = vis_lo - qw, rel_hi = vis_hi - qw;
+        if (rel_hi - static_cast<int>(lane) + 31 < 0 || rel_lo - static_cast<int>(lane) > 63) {
           warp_arrive_rank0(bar(C::kSEmpty + buf));
           if (lane == 0) mbar_arrive(bar(C::kLEmpty + slot));
           pos.advance(w);
@@ -421,7 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKwThreads, 1)
         uint32_t raw[32];  // 32 scores at a time: registers for more of them would spill
         tmem_ld32(col, raw);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        const bool late = qw < all_lo, early = qw + 63 > all_hi;
+        const bool late = rel_lo - static_cast<int>(lane) + 31 > 0;
+        const bool early = rel_hi - static_cast<int>(lane) < 63;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           tmem_wait_ld(raw);
@@ -441,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKwThreads, 1)
           // (one branch around both: more of them keep the two halves from interleaving).
           if (late || early) {
             if (late) {
-              const int lo = vis_lo - qw - 32 * c;
+              const int lo = rel_lo - 32 * c;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 x[i].x = 2 * i >= lo ? x[i].x : SWA_NEG_INF;
@@ -449,7 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKwThreads, 1)
               }
             }
             if (early) {
-              const int hi = vis_hi - qw - 32 * c;
+              const int hi = rel_hi - 32 * c;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 x[i].x = 2 * i <= hi ? x[i].x : SWA_NEG_INF;
