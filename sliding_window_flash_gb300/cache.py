@@ -60,6 +60,21 @@ SIGNATURES = {
 }
 
 
+class _Torch:
+    """torch's names that every call needs, looked up once (the package imports torch lazily)."""
+
+    def __getattr__(self, name):
+        import torch
+
+        self.__dict__.update(
+            f8=torch.float8_e4m3fn, f32=torch.float32, i32=torch.int32, u8=torch.uint8,
+            kinds={torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}, Tensor=torch.Tensor,
+            empty_like=torch.empty_like, stream=torch._C._cuda_getCurrentRawStream,
+            current_device=torch.cuda.current_device)
+        return self.__dict__[name]
+
+
+_t = _Torch()
 _entries = {}
 
 
@@ -101,6 +116,9 @@ def _check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+_put = object.__setattr__
+
+
 class SwaCache:
     """A pool of cache pages: k, v float8_e4m3fn [pages, Hkv, page, D], their scales k_scale, v_scale
     fp32 [pages, Hkv], and weight fp32 [pages, Hkv, page] (None for a cache never evicted from).
@@ -110,12 +128,10 @@ class SwaCache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "weight", "device", "shape")
 
     def __init__(self, k, v, k_scale, v_scale, weight=None):
-        import torch
-
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        if not isinstance(k, _t.Tensor) or k.dim() != 4:
             raise ValueError("k must be a 4-D tensor [pages, Hkv, page, D]")
         dev, shape = k.device, tuple(k.shape)
-        f8, f32, index = torch.float8_e4m3fn, torch.float32, dev.index
+        f8, f32, index = _t.f8, _t.f32, dev.index
         if not (index is not None and _good(k, shape, f8, index) and _good(v, shape, f8, index) and
                 _good(k_scale, shape[:2], f32, index) and _good(v_scale, shape[:2], f32, index) and
                 (weight is None or _good(weight, shape[:3], f32, index))):
@@ -125,7 +141,7 @@ class SwaCache:
             _check(v_scale, "v_scale", shape[:2], f32, dev)
             if weight is not None:
                 _check(weight, "weight", shape[:3], f32, dev)
-        put = object.__setattr__
+        put = _put
         put(self, "k", k)
         put(self, "v", v)
         put(self, "k_scale", k_scale)
@@ -167,13 +183,11 @@ class SwaCache:
 
 def _tables(cache, table, lens, new):
     """(B, max_pages, GPU index) after checking the int32 tables of a call."""
-    import torch
-
     if type(cache) is not SwaCache:
         raise TypeError("cache must be a SwaCache")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+    if not isinstance(table, _t.Tensor) or table.dim() != 2:
         raise ValueError("table must be a 2-D tensor [B, max_pages]")
-    shape, index, i32 = tuple(table.shape), cache.device.index, torch.int32
+    shape, index, i32 = tuple(table.shape), cache.device.index, _t.i32
     B = shape[:1]
     if not (_good(table, shape, i32, index) and _good(lens, B, i32, index) and
             (new is None or _good(new, B, i32, index))):
@@ -202,12 +216,12 @@ def _space(workspace):
 
 def _run(name, index, *args):
     """Calls entry point `name` on the current stream of GPU `index`, with that GPU current."""
-    import torch
-
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch.cuda.current_device():
+    stream = _t.stream(index)
+    if index == _t.current_device():
         rc = _entry(name)(*args, stream)
     else:
+        import torch
+
         with torch.cuda.device(index):
             rc = _entry(name)(*args, stream)
     if rc != 0:
@@ -217,17 +231,11 @@ def _run(name, index, *args):
 
 
 def _dtype(t, name, fp32=False):
-    import torch
-
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return 0
-    if dt is torch.float16:
-        return 1
-    if fp32 and dt is torch.float32:
-        return 2
+    code = _t.kinds.get(t.dtype, 3)
+    if code < 2 or fp32 and code == 2:
+        return code
     raise TypeError(f"{name} must be bfloat16{', float16 or float32' if fp32 else ' or float16'}, "
-                    f"got {dt}")
+                    f"got {t.dtype}")
 
 
 def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) -> None:
@@ -237,20 +245,18 @@ def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) 
     None: all T) go to slots lens[b], lens[b] + 1, ...  weight [B, Hkv, T] fp32: the accumulated
     attention weights they start with (None: zero).  The pages written must belong to one sequence.
     """
-    import torch
-
     B, width, index = _tables(cache, table, lens, new)
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+    if not isinstance(k, _t.Tensor) or k.dim() != 4:
         raise ValueError("k must be a 4-D tensor [B, Hkv, T, D]")
     dt, kind = _dtype(k, "k", fp32=True), k.dtype
     T = k.shape[2]
     shape = (B, cache.shape[1], T, cache.shape[3])
     if not (_good(k, shape, kind, index) and _good(v, shape, kind, index) and
-            (weight is None or _good(weight, shape[:3], torch.float32, index))):
+            (weight is None or _good(weight, shape[:3], _t.f32, index))):
         _check(k, "k", shape, kind, cache.device)
         _check(v, "v", shape, kind, cache.device)
         if weight is not None:
-            _check(weight, "weight", shape[:3], torch.float32, cache.device)
+            _check(weight, "weight", shape[:3], _t.f32, cache.device)
     _run("swa_cache_append", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
          _ptr(new), k.data_ptr(), v.data_ptr(), _ptr(weight), B, T, dt)
 
@@ -281,19 +287,17 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     adds to cache.weight what each cached token received.  The workspace (of
     swa_cache_attn_workspace_bytes) is allocated here unless given.
     """
-    import torch
-
     B, width, index = _tables(cache, table, lens, new)
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+    if not isinstance(q, _t.Tensor) or q.dim() != 4:
         raise ValueError("q must be a 4-D tensor [B, Hq, T, D]")
-    dt, kind, f32 = _dtype(q, "q"), q.dtype, torch.float32
+    dt, kind, f32 = _dtype(q, "q"), q.dtype, _t.f32
     _, Hkv, page, D = cache.shape
     _, Hq, T, _ = q.shape
     shape = (B, Hq, T, D)
     if not _good(q, shape, kind, index):
         _check(q, "q", shape, kind, cache.device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _t.empty_like(q)
     elif not _good(out, shape, kind, index):
         _check(out, "out", shape, kind, cache.device)
     if lse is None:
@@ -302,7 +306,7 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
         _check(lse, "lse", shape[:3], f32, cache.device)
     if workspace is None:
         need = _attn_space(B, Hq, Hkv, T, D, width, page, int(bool(accumulate)))
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = q.new_empty(need, dtype=_t.u8)
     _run("swa_cache_attn", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
          _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, _window(window),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(accumulate)), dt,
@@ -316,12 +320,10 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
     of the others those with the largest accumulated weight (equal: the earlier).  The survivors are
     written in order to the pages of dst_table [B, dst_pages], which must be none of table's; returns
     (kept [B,Hkv,budget] int32: their old slots, -1 behind the last; lens_out [B] int32)."""
-    import torch
-
     B, width, index = _tables(cache, table, lens, None)
-    if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
+    if not isinstance(dst_table, _t.Tensor) or dst_table.dim() != 2:
         raise ValueError("dst_table must be a 2-D tensor [B, dst_pages]")
-    budget, i32 = int(budget), torch.int32
+    budget, i32 = int(budget), _t.i32
     if budget < 1:
         raise ValueError("budget must be at least 1")
     room = (B, dst_table.shape[1])
@@ -333,7 +335,7 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
     elif not _good(kept, shape, i32, index):
         _check(kept, "kept", shape, i32, cache.device)
     if lens_out is None:
-        lens_out = torch.empty_like(lens)
+        lens_out = _t.empty_like(lens)
     elif not _good(lens_out, (B,), i32, index):
         _check(lens_out, "lens_out", (B,), i32, cache.device)
     _run("swa_cache_evict", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
@@ -353,12 +355,10 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
     k [B,Hkv,Lk,D] in bf16 or fp16, lse [B,Hq,Lq] as swa_attn_fwd returned it for the same window,
     scale and causal.  The workspace (of swa_attn_key_weights_workspace_bytes) is allocated here
     unless given."""
-    import torch
-
     for t in (q, k):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        if not isinstance(t, _t.Tensor) or t.dim() != 4:
             raise ValueError("q and k must be 4-D [B, H, L, D]")
-    dt, kind, f32 = _dtype(q, "q"), q.dtype, torch.float32
+    dt, kind, f32 = _dtype(q, "q"), q.dtype, _t.f32
     B, Hq, Lq, D = q.shape
     Hkv, Lk = k.shape[1], k.shape[2]
     dev = q.device
@@ -376,7 +376,7 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
     if workspace is None:
         need = _weights_space(B, Hq, Hkv, Lq, Lk, D, window, causal)
         if need:
-            workspace = q.new_empty(need, dtype=torch.uint8)
+            workspace = q.new_empty(need, dtype=_t.u8)
     _run("swa_attn_key_weights", index, q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(), B,
          Hq, Hkv, Lq, Lk, D, window, causal, 1.0 / math.sqrt(D) if scale is None else float(scale),
          dt, *_space(workspace))
