@@ -17,7 +17,8 @@
  * token) is row s % page of page table[b][s / page].  `lens` holds how many tokens each sequence
  * had cached before the step's new tokens, in every call of the step; the caller adds the new
  * tokens to it afterwards.  The table, lens and new_lens are read on the device, so a captured step
- * replays with whatever they hold then.
+ * replays with whatever they hold then.  max_pages * page < 2^30, pages * Hkv < 2^31, B * Hkv < 2^31,
+ * and B and Hkv at most 65535.
  *
  * What the device reads is checked there: a page number outside the pool, a sequence longer than
  * its table or a negative length is not followed; the call skips that page or sequence (attention
@@ -112,10 +113,10 @@ swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_page
  * They are written to slots 0, 1, .. of the pages of dst_table, with their weights; the pages of
  * `table` are only read, so they may be shared, and the caller frees them.
  *   dst_table : int32 [B, dst_pages] with dst_pages * page >= budget; its pages must not occur in
- *               `table`, nor twice.
+ *               `table`, nor twice (dst_table == table is refused).
  *   budget    : >= 1;  0 <= recent <= budget.
  *   kept      : int32 [B, Hkv, budget], the surviving slots in order, -1 behind the last.
- *   lens_out  : int32 [B], min(lens[b], budget).
+ *   lens_out  : int32 [B], min(lens[b], budget); may be lens.
  * A destination block's scale is the largest of its tokens' old scales; slots behind the last
  * survivor are left as they were.  Window rules count cached tokens, so under a window evicted
  * tokens no longer count.  Needs cache->weight.

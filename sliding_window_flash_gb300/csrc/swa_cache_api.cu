@@ -10,6 +10,7 @@ namespace {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 constexpr long long kIndexLimit = 1ll << 31;
+constexpr long long kSlotLimit = 1ll << 30;  // of a sequence's table
 
 // The checks every cache call makes of the cache, its table and lengths.
 swa_status check_cache(const swa_cache* c, const int* table, int max_pages, const int* lens, int B) {
@@ -18,8 +19,9 @@ swa_status check_cache(const swa_cache* c, const int* table, int max_pages, cons
   if (c->pages < 1 || c->Hkv < 1 || max_pages < 1 || B < 1) return SWA_ERR_INVALID_ARG;
   if (c->page != 32 && c->page != 64 && c->page != 128) return SWA_ERR_UNSUPPORTED;
   if (c->D != 64 && c->D != 128 && c->D != 256) return SWA_ERR_UNSUPPORTED;
-  // Slots, blocks (page, head) and table entries in 31 bits; element offsets are 64-bit.
-  if (static_cast<long long>(max_pages) * c->page >= kIndexLimit ||
+  // Slots in 30 bits (the kernels add to them), blocks (page, head) and table entries in 31; element
+  // offsets are 64-bit.
+  if (static_cast<long long>(max_pages) * c->page >= kSlotLimit ||
       static_cast<long long>(c->pages) * c->Hkv >= kIndexLimit ||
       static_cast<long long>(B) * c->Hkv >= kIndexLimit || B > 65535 || c->Hkv > 65535)
     return SWA_ERR_INVALID_ARG;
@@ -111,7 +113,7 @@ size_t swa_cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int 
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > swa::kMaxCacheQueries ||
       max_pages < 1 || (D != 64 && D != 128 && D != 256) ||
       (page != 32 && page != 64 && page != 128) ||
-      static_cast<long long>(max_pages) * page >= kIndexLimit)
+      static_cast<long long>(max_pages) * page >= kSlotLimit)
     return 0;
   return swa::cache_attn_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page, accumulate);
 }
@@ -161,10 +163,11 @@ swa_status swa_cache_evict(const swa_cache* cache, const int* table, int max_pag
   if (!cache->weight || !dst_table || !kept || !lens_out) return SWA_ERR_INVALID_ARG;
   if (dst_pages < 1 || budget < 1 || recent < 0 || recent > budget ||
       static_cast<long long>(dst_pages) * cache->page < budget ||
-      static_cast<long long>(dst_pages) * cache->page >= kIndexLimit)
+      static_cast<long long>(dst_pages) * cache->page >= kSlotLimit)
     return SWA_ERR_INVALID_ARG;
   if (!aligned(dst_table, 4) || !aligned(kept, 4) || !aligned(lens_out, 4))
     return SWA_ERR_MISALIGNED;
+  if (dst_table == table) return SWA_ERR_INVALID_ARG;  // the pages read would be written
   unsigned* err = nullptr;
   if ((st = swa::device_error_word(&err)) != SWA_OK) return st;
   const swa::CacheView c = view(cache, table, max_pages, lens, nullptr, B, 0, err);

@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kKeep && kDtype == SWA_FP32 ? 512 : D * 4,
   int len, n;
   if (!sequence_of(c, b, &len, &n) || n == 0) return;
   const int blk = len / c.page + static_cast<int>(blockIdx.x);
+  if (blk >= c.max_pages) return;  // behind the table, where slots may pass 31 bits
   const int slot0 = blk * c.page;
   const int first = max(len, slot0) - slot0;      // first new row of the block
   const int last = min(len + n - slot0, c.page);  // one past the last
@@ -267,7 +268,7 @@ template <int D>
 cudaError_t launch_d(const CacheView& c, const void* k, const void* v, const float* weight,
                      int dtype, cudaStream_t stream) {
   // T tokens touch at most this many pages of a sequence.
-  const dim3 grid(static_cast<unsigned>((c.T + c.page - 2) / c.page + 1),
+  const dim3 grid((static_cast<unsigned>(c.T) + c.page - 2) / c.page + 1,
                   static_cast<unsigned>(c.Hkv), static_cast<unsigned>(c.B));
   const unsigned threads = static_cast<unsigned>(c.page * D / (8 * kHeld));
   if (dtype == SWA_BF16)

@@ -82,7 +82,6 @@ __global__ void __launch_bounds__(kSelectThreads, 2)
   int len, n;
   if (!sequence_of(c, b, &len, &n)) len = 0;
   const int m = min(len, a.budget);
-  if (h == 0 && rank == 0 && tid == 0) a.lens_out[b] = m;
   const int me = rank * kSelectThreads + tid, all = ctas * kSelectThreads;
   for (int i = m + me; i < a.budget; i += all) kept[i] = -1;
   // Where nothing is chosen the whole cluster leaves: the same for all of its CTAs.
@@ -284,14 +283,20 @@ __global__ void __launch_bounds__(kMoveThreads + kLookThreads, 4)
   const int tid = static_cast<int>(threadIdx.x);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // Task t is destination page t % pages of head (t / pages) % Hkv of a sequence.
-  auto look = [&](int64_t t, MoveBlock& m) {
+  auto look = [&](int64_t t, MoveBlock& to_do) {
     const int i = tid - kMoveThreads;
     const int64_t bh = t / pages;
     const int j = static_cast<int>(t - bh * pages);
     const int b = static_cast<int>(bh / c.Hkv), h = static_cast<int>(bh - static_cast<int64_t>(b) * c.Hkv);
-    const int rows = min(c.page, min(a.lens_out[b], a.budget) - j * c.page);
+    // lens_out may be lens: cutting a length twice is cutting it once, so it does not matter whether
+    // another block has written it yet.
+    int len, n;
+    if (!sequence_of(c, b, &len, &n)) len = 0;
+    const int m = min(len, a.budget);
+    if (h == 0 && j == 0 && i == 0) a.lens_out[b] = m;
+    const int rows = min(c.page, m - j * c.page);
     const int to = rows > 0 ? page_of(c, a.dst_table, b, j, a.dst_pages) : -1;
-    if (i == 0) m.block = to < 0 ? -1 : static_cast<long long>(to) * c.Hkv + h;
+    if (i == 0) to_do.block = to < 0 ? -1 : static_cast<long long>(to) * c.Hkv + h;
     long long row = -1;
     float ks = 0.f, vs = 0.f;
     if (i < rows && to >= 0) {
@@ -305,9 +310,9 @@ __global__ void __launch_bounds__(kMoveThreads + kLookThreads, 4)
         c.weight[(static_cast<size_t>(to) * c.Hkv + h) * c.page + i] = c.weight[row];
       }
     }
-    m.row[i] = row;
-    m.scale[0][i] = ks;
-    m.scale[1][i] = vs;
+    to_do.row[i] = row;
+    to_do.scale[0][i] = ks;
+    to_do.scale[1][i] = vs;
   };
   if (tid >= kMoveThreads && blockIdx.x < tasks) look(blockIdx.x, s_block[0]);
   __syncthreads();

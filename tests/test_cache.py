@@ -340,6 +340,25 @@ def test_evict_bad_pages_and_lengths(swa):
             assert int(out[1]) == 0 and (kept[1] == -1).all()
 
 
+def test_evict_lengths_in_place(swa):
+    """lens_out may be lens: blocks that start after others have cut a length cut the same tokens."""
+    g = _gen(22)
+    B, H, D, page, budget, recent = 16, 8, 64, 32, 500, 40
+    lens = [0, 1, 499, 500, 501, 900] + [600 + 17 * b for b in range(10)]
+    width, room = -(-max(lens) // page), -(-budget // page)
+    cache = _cache(swa, g, B * (width + room), H, D, page, spread=6)
+    order = _table(g, B, width + room)
+    table, dst = order[:, :width].contiguous(), order[:, width:].contiguous()
+    pool = ref.pool_of(cache)
+    kept, out = ref.evict(pool, table, lens, dst, budget, recent)
+    held = _ints(lens)
+    gk, go = swa.swa_cache_evict(cache, table, held, dst, budget, recent, lens_out=held)
+    swa.swa_check_device()
+    assert go is held and torch.equal(held.cpu(), out)
+    assert torch.equal(gk.cpu(), kept)
+    _same_pool(cache, pool)
+
+
 # ---- key weights -------------------------------------------------------------------------------
 
 def _ref_lse(q, k, window, causal):

@@ -124,6 +124,17 @@ def test_evict_refusals(lib, kw, code):
     assert _evict(lib, **kw) == code
 
 
+def test_evict_refuses_its_own_table_as_destination(lib):
+    assert _evict(lib, dst=FAKE, table=FAKE) == 1
+
+
+@pytest.mark.parametrize("call", [_append, _attn, _evict], ids=["append", "attn", "evict"])
+def test_slots_stay_below_thirty_bits(lib, call):
+    assert call(lib, width=1 << 24) == 1
+    assert lib.swa_cache_attn_workspace_bytes(2, 4, 2, 1, 128, 1 << 24, 64, 0) == 0
+    assert lib.swa_cache_attn_workspace_bytes(2, 4, 2, 1, 128, (1 << 24) - 1, 64, 0) > 0
+
+
 def _weights(lib, q=FAKE, k=FAKE, lse=FAKE, w=FAKE, B=1, Hq=4, H=2, Lq=16, Lk=20, D=64, W=4,
              causal=1, scale=0.1, dtype=0, ws=FAKE, ws_bytes=1 << 40):
     return lib.swa_attn_key_weights(q, k, lse, w, B, Hq, H, Lq, Lk, D, W, causal, scale, dtype, ws,
