@@ -10,18 +10,20 @@
 //     at a time of every query head of the group.  Each CTA loads its keys and its half of the
 //     queries; rank 0 issues M = 256, N = 256 products for both.  An SM then reads 64 bytes of operands
 //     a cycle from shared memory; single CTAs with 128 x 128 products read 128, all there is.
-//     Without the exponentials the pairs take 0.173 ms where the single CTAs took 0.207, with them
-//     0.254 and 0.288 (N = 32,768, W = 1,024, 32 / 16 heads, D = 128).
+//     Products alone take the pairs 0.169 ms and single CTAs 0.207, the whole 0.235 and 0.288 or more
+//     (N = 32,768, W = 1,024, 32 / 16 heads, D = 128).  Units of 128 queries in four buffers, in turn
+//     for two groups of warps, take 0.282: their products alone take 0.200.
 //   * Persistent pairs take tasks longest first, there and back again (task i of a round from the
 //     left, then from the right), so that walks of unequal length even out.  With few tasks each walk
 //     is cut into `pieces` equal parts whose sums a second kernel adds in order.
 //   * 20 warps a CTA: 16 take the exponentials (32 keys and 64 of a unit's 256 queries each; a part
 //     that the window hides is skipped), and one each loads Q, loads K, issues the products (rank 0)
 //     or forwards the arrival of its copies (rank 1), and keeps -lse / ln 2 of the next queries in
-//     shared memory, announced by the same barrier as their scores (0.254 ms against 0.290 with
-//     each warp fetching its own).  Two score buffers of 256 columns fill TMEM.
-//   * What bounds it: the 16 warps' chain of barrier, TMEM load, exponentials and sums, in step with
-//     one another for the wait on the same scores; products alone would take 0.135 ms.
+//     shared memory, announced by the same barrier as their scores (0.036 ms less than with each
+//     warp fetching its own).  Two score buffers of 256 columns fill TMEM.
+//   * What bounds it: the instructions of the 16 exponential warps, in step with one another for the
+//     wait on the same scores.  Of the time over the products', reading the scores from TMEM is 0.006 ms,
+//     the log-sum-exps from shared memory 0.016, masks 0.009, exponentials 0.04.
 //   * Masked parts select; whatever a query outside the window holds does not reach the sum.  64 terms
 //     are added in fp32, then into a compensated sum (Kahan), so the error does not grow with the walk.
 #include <type_traits>
@@ -416,55 +418,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKwThreads, 1)
         tc_fence_after();
         const uint32_t col = col0 + buf * 256u;
         const float4* l4 = reinterpret_cast<const float4*>(s_lse + slot * kUnitQueries);
-        uint32_t raw[32];  // 32 scores at a time: registers for more of them would spill
-        tmem_ld32(col, raw);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        const bool late = rel_lo - static_cast<int>(lane) + 31 > 0;
-        const bool early = rel_hi - static_cast<int>(lane) < 63;
+        // Sum of the part's exponentials.  At the window's edges (at_edge) the queries that this key does
+        // not see are masked.  Two copies: a branch around the masks alone keeps the two halves of a part
+        // without any from interleaving (0.254 and 0.202 ms where this takes 0.235 and 0.195), and
+        // comparing with one bound at a time takes 0.254 here too.
+        auto part = [&](auto at_edge) -> float {
+          constexpr bool kEdge = decltype(at_edge)::value;
+          uint32_t raw[32];  // 32 scores at a time: registers for more of them would spill
+          tmem_ld32(col, raw);
+          float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          tmem_wait_ld(raw);
-          if (c == 1) warp_arrive_rank0(bar(C::kSEmpty + buf));
-          float2 x[16];
+          for (int c = 0; c < 2; ++c) {
+            tmem_wait_ld(raw);
+            if (c == 1) warp_arrive_rank0(bar(C::kSEmpty + buf));
+            float2 x[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 l = l4[8 * c + i];
-            x[2 * i] = __ffma2_rn(
-                make_float2(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1])), c2,
-                make_float2(l.x, l.y));
-            x[2 * i + 1] = __ffma2_rn(
-                make_float2(__uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3])), c2,
-                make_float2(l.z, l.w));
-          }
-          // At the window's edges the queries that this key does not see are masked, from either side
-          // (one branch around both: more of them keep the two halves from interleaving).
-          if (late || early) {
-            if (late) {
-              const int lo = rel_lo - 32 * c;
+            for (int i = 0; i < 8; ++i) {
+              const float4 l = l4[8 * c + i];
+              x[2 * i] = __ffma2_rn(
+                  make_float2(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1])), c2,
+                  make_float2(l.x, l.y));
+              x[2 * i + 1] = __ffma2_rn(
+                  make_float2(__uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3])), c2,
+                  make_float2(l.z, l.w));
+            }
+            if constexpr (kEdge) {
+              // lo <= i <= hi as one unsigned comparison; a part that is not skipped has lo <= hi
+              const uint32_t lo = static_cast<uint32_t>(rel_lo - 32 * c);
+              const uint32_t n = static_cast<uint32_t>(rel_hi - rel_lo);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                x[i].x = 2 * i >= lo ? x[i].x : SWA_NEG_INF;
-                x[i].y = 2 * i + 1 >= lo ? x[i].y : SWA_NEG_INF;
+                x[i].x = 2u * i - lo <= n ? x[i].x : SWA_NEG_INF;
+                x[i].y = 2u * i + 1u - lo <= n ? x[i].y : SWA_NEG_INF;
               }
             }
-            if (early) {
-              const int hi = rel_hi - 32 * c;
+            if (c == 0) tmem_ld32(col + 32u, raw);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                x[i].x = 2 * i <= hi ? x[i].x : SWA_NEG_INF;
-                x[i].y = 2 * i + 1 <= hi ? x[i].y : SWA_NEG_INF;
-              }
+            for (int i = 0; i < 16; i += 2) {
+              acc0 = __fadd2_rn(acc0, make_float2(ex2(x[i].x), ex2(x[i].y)));
+              acc1 = __fadd2_rn(acc1, make_float2(ex2(x[i + 1].x), ex2(x[i + 1].y)));
             }
           }
-          if (c == 0) tmem_ld32(col + 32u, raw);
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            acc0 = __fadd2_rn(acc0, make_float2(ex2(x[i].x), ex2(x[i].y)));
-            acc1 = __fadd2_rn(acc1, make_float2(ex2(x[i + 1].x), ex2(x[i + 1].y)));
-          }
-        }
-        const float2 both = __fadd2_rn(acc0, acc1);
-        const float add = __fadd_rn(both.x, both.y);
+          const float2 both = __fadd2_rn(acc0, acc1);
+          return __fadd_rn(both.x, both.y);
+        };
+        const bool edge = rel_lo - static_cast<int>(lane) + 31 > 0 || rel_hi - static_cast<int>(lane) < 63;
+        const float add = edge ? part(std::true_type{}) : part(std::false_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kLEmpty + slot));
         pos.advance(w);
