@@ -80,7 +80,7 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  * them first).  Query t of sequence b sits at slot lens[b] + t and sees slots s with
  * 0 <= lens[b] + t - s < window, for t < n_b (new_lens; NULL: n_b = T):
  *     x = scale <q, k_s>,  lse = ln sum exp(x),  p = exp(x - lse),  o = sum p v_s.
- *   q, o  : [B, Hq, T, D], bf16 or fp16 (`dtype`); Hq % Hkv == 0; 1 <= T <= 64.
+ *   q, o  : [B, Hq, T, D], bf16 or fp16 (`dtype`); Hq % Hkv == 0; 1 <= T <= 64; o may be q.
  *   lse   : fp32 [B, Hq, T].
  * Rows t >= n_b, and rows of skipped sequences, get o = 0, lse = -inf.  Pages wholly before every
  * window, and table entries behind the last token, are not read: a sliding layer's caller may reuse

@@ -740,3 +740,116 @@ def test_key_weights_long(swa, B, Hq, H, L, D, window):
     es = (D + 8) * 2.0**-24 / math.sqrt(D) * float(q.float().norm(dim=-1).max() *
                                                    k.float().norm(dim=-1).max())
     assert ((got.double() - want).abs() <= (2 * es + 2.0**-18) * want + 1e-30).all()
+
+
+# ---- arguments ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("H_q,H,D,T,lens,dtype", [
+    (4, 2, 64, 3, [90, 700], torch.float16),
+    (8, 2, 128, 1, [2000, 31], torch.bfloat16),
+    (6, 1, 256, 9, [400, 0], torch.bfloat16),
+])
+@pytest.mark.parametrize("scale", [0.5, 1e-3])
+def test_attn_scale_and_output_over_q(swa, H_q, H, D, T, lens, dtype, scale):
+    """A scale of the caller's, buffers of the caller's, and o written over q."""
+    g = _gen(D + T)
+    page, B, window = 32, len(lens), 300
+    width = -(-(max(lens) + T) // page)
+    cache = _cache(swa, g, B * width, H, D, page, spread=3)
+    table = _table(g, B, width)
+    q = torch.randn((B, H_q, T, D), generator=g, device="cuda").to(dtype)
+    o, lse, to, tl, _ = ref.attn(ref.pool_of(cache), table, lens, q, window, scale=scale)
+    lse_out = torch.full((B, H_q, T), math.nan, device="cuda")
+    need = swa.swa_cache_attn_workspace_bytes(B, H_q, H, T, D, width, page)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    go, gl = swa.swa_cache_attn(q, cache, table, _ints(lens), window, scale=scale, out=q,
+                                lse=lse_out, workspace=ws)
+    swa.swa_check_device()
+    assert go is q and gl is lse_out
+    _near(go, o, to, "o")
+    _near(gl, lse, tl, "lse")
+
+
+@pytest.mark.parametrize("scale", [0.5, 1e-3])
+def test_key_weights_scale(swa, scale):
+    g = _gen(71)
+    q = torch.randn((1, 4, 200, 64), generator=g, device="cuda").to(torch.bfloat16)
+    k = torch.randn((1, 2, 333, 64), generator=g, device="cuda").to(torch.bfloat16)
+    x = q.double().cpu() @ k.double().cpu().repeat_interleave(2, 1).transpose(-1, -2) * scale
+    d = torch.arange(200)[:, None] + 133 - torch.arange(333)
+    lse = torch.logsumexp(x.masked_fill((d < 0) | (d >= 90), -math.inf), -1).float().cuda()
+    w, tol = ref.key_weights(q, k, lse, 90, scale=scale)
+    need = swa.swa_attn_key_weights_workspace_bytes(1, 4, 2, 200, 333, 64, 90)
+    ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")
+    got = swa.swa_attn_key_weights(q, k, lse, 90, scale=scale, workspace=ws)
+    swa.swa_check_device()
+    _near(got, w, tol, "weights")
+
+
+def test_binding_refusals(swa):
+    """Tensors of a wrong kind, shape, type or layout raise before anything is launched."""
+    cache = swa.SwaCache.empty(8, 2, 64, page=32)
+    k = torch.zeros((2, 2, 4, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((2, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    table, lens = _ints([[0, 1], [2, 3]]), _ints([5, 6])
+    dst = _ints([[4], [5]])
+    append, attn, evict = swa.swa_cache_append, swa.swa_cache_attn, swa.swa_cache_evict
+    weights = swa.swa_attn_key_weights
+    wrong = (TypeError, ValueError)
+    with pytest.raises(wrong):
+        swa.SwaCache(cache.k, cache.v, cache.k_scale.double(), cache.v_scale)
+    with pytest.raises(wrong):
+        swa.SwaCache(cache.k, cache.v[:7], cache.k_scale, cache.v_scale)
+    with pytest.raises(wrong):
+        swa.SwaCache(cache.k, cache.v, cache.k_scale, cache.v_scale, cache.weight[..., ::2])
+    with pytest.raises(AttributeError):
+        cache.k = cache.v
+    for t, n in ((table.long(), lens), (table, lens.long()), (table[0], lens), (table, lens[:1]),
+                 (table.cpu(), lens), (table.t(), lens)):
+        for call in (lambda: append(cache, t, n, k, k), lambda: attn(q, cache, t, n, 9),
+                     lambda: evict(cache, t, n, dst, 20, 2)):
+            with pytest.raises(wrong):
+                call()
+    for bad in (k.double(), k[:1], k[:, :1], k[..., :32], k.transpose(1, 2), k.cpu()):
+        with pytest.raises(wrong):
+            append(cache, table, lens, bad, k)
+        with pytest.raises(wrong):
+            append(cache, table, lens, k, bad)
+    with pytest.raises(wrong):
+        append(cache, table, lens, k, k.half())
+    with pytest.raises(wrong):
+        append(cache, table, lens, k, k, weight=torch.zeros((2, 2, 3), device="cuda"))
+    with pytest.raises(wrong):
+        append(cache, table, lens, k, k, new=_ints([1]))
+    for bad in (q.float(), q[:1], q[..., :32], q.cpu(), q.expand(2, 4, 3, 64)):
+        with pytest.raises(wrong):
+            attn(bad, cache, table, lens, 9)
+    for kw in (dict(out=q.half()), dict(out=q[:, :2]), dict(lse=torch.zeros((2, 4), device="cuda")),
+               dict(new=lens.float())):
+        with pytest.raises(wrong):
+            attn(q, cache, table, lens, 9, **kw)
+    for kw in (dict(window=0), dict(window=9, scale=-1.0),
+               dict(window=9, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(swa.SwaError):
+            attn(q, cache, table, lens, **kw)
+    with pytest.raises(wrong):
+        evict(cache, table, lens, dst[0], 20, 2)
+    with pytest.raises(wrong):
+        evict(cache, table, lens, dst, 20, 2, kept=torch.zeros((2, 2, 19), dtype=torch.int32, device="cuda"))
+    with pytest.raises(wrong):
+        evict(cache, table, lens, dst, 0, 0)
+    for budget, recent in ((20, 21), (33, 2)):
+        with pytest.raises(swa.SwaError):
+            evict(cache, table, lens, dst, budget, recent)
+    with pytest.raises(swa.SwaError):
+        evict(cache, table, lens, table, 20, 2)
+    lse = torch.zeros((2, 4, 1), device="cuda")
+    for args in ((q, k[:1], lse), (q, k, lse[..., 0]), (q, k.half(), lse), (q, k, lse.double()),
+                 (q, k.cpu(), lse)):
+        with pytest.raises(wrong):
+            weights(*args, 9)
+    with pytest.raises(swa.SwaError):
+        weights(q, k, lse, 0)
+    torch.cuda.synchronize()
+    swa.swa_check_device()
+    assert (ref.pool_of(cache)["k"] == 0).all()

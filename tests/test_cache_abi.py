@@ -190,3 +190,39 @@ def test_struct_matches_the_header():
     names = re.findall(r"(?:void\*|float\*|int) (\w+);", body)
     assert names == [n for n, _ in swa_cache_mod._CCache._fields_]
     assert ctypes.sizeof(swa_cache_mod._CCache) == 5 * 8 + 4 * 4
+
+
+def test_calls_run_on_the_caches_gpu(monkeypatch):
+    """A call makes the tensors' GPU current, takes that GPU's stream, and leaves the current one."""
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.was
+
+    class Names:
+        stream = staticmethod(lambda index: 1000 + index)
+        current_device = staticmethod(lambda: now[0])
+
+    monkeypatch.setattr(swa_cache_mod, "_t", Names)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    rc = [0]
+
+    def entry(*args):
+        seen.append((now[0], args))
+        return rc[0]
+
+    monkeypatch.setitem(swa_cache_mod._entries, "swa_cache_append", entry)
+    swa_cache_mod._run("swa_cache_append", 0, 7)
+    swa_cache_mod._run("swa_cache_append", 3, 8)
+    assert seen == [(0, (7, 1000)), (3, (8, 1003))] and now[0] == 0
+    rc[0] = 1
+    with pytest.raises(swa.SwaError):
+        swa_cache_mod._run("swa_cache_append", 3, 8)
+    assert now[0] == 0
