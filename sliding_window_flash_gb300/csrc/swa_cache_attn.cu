@@ -24,9 +24,10 @@
 //
 // Measured in a CUDA graph, D = 128 unless said: 8 sequences of up to 128K tokens, 16 kv heads: 600 us,
 // 6.8 TB/s.  64 ragged sequences to 16K with accumulation: 203 us, the walk about 175 of it (5.8 TB/s;
-// the last teams end some 15 us after most), the join 8, the weights 20.  A window of 1024 for one
-// sequence, 16 heads: 11 us, the latency of two kernels.  12 sequences, 5 tokens, D = 256, window
-// 1024: 31 us; a part is only ten chunks, so partial results are half the traffic there.
+// the last teams end some 15 us after most), the join 8, the weights 20.  A window of 1024: 11 us for
+// one sequence with 16 heads, the latency of two kernels; 18.6 us for 16 sequences with 8 heads.  12
+// sequences, 5 tokens, D = 256, window 1024: 31 us; a part is only ten chunks, so partial results are
+// half the traffic there.
 #include <climits>
 #include <type_traits>
 
@@ -735,6 +736,60 @@ __global__ void __launch_bounds__(256) swa_cache_join_kernel(const CacheView c, 
   }
 }
 
+// The same with a warp for 16 columns of a row: 8 groups of 4 lanes take the partials in turn.
+template <int D>
+__global__ void __launch_bounds__(256) swa_cache_join_part_kernel(const CacheView c, const AttnDev a) {
+  constexpr uint32_t kRuns = D / 16;
+  wait_predecessor();
+  launch_dependents();
+  const int lane = static_cast<int>(lane_id()), group = lane / 4, sub = lane % 4;
+  const int per = c.Hkv * a.NRT;
+  const Parts cut(a.first[c.B] * per, a.parts);
+  const uint32_t tasks = static_cast<uint32_t>(c.B) * per * a.rows * kRuns;
+  for (uint32_t task = blockIdx.x * 8 + warp_id(); task < tasks; task += gridDim.x * 8) {
+    const int run = static_cast<int>(task % kRuns);
+    const int item = static_cast<int>(task / kRuns / static_cast<uint32_t>(a.rows));
+    const int r = static_cast<int>(task / kRuns - static_cast<uint32_t>(item) * a.rows);
+    size_t row;
+    if (!row_of_item(a, item, r, &row)) continue;
+    const ItemParts ip = item_parts(a, cut, per, item);
+    if (ip.chunks > 0 && ip.p0 == ip.p1) continue;
+    float top = SWA_NEG_INF, l = 0.f;
+    float o[4] = {};
+    if (ip.chunks > 0) {
+      auto partial = [&](int p) {
+        return static_cast<size_t>(partial_slot(p, cut.start(p) <= ip.x0)) * a.rows + r;
+      };
+      for (int p = ip.p0 + lane; p <= ip.p1; p += 32) top = fmaxf(top, a.ml[partial(p) * 2]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float base = top == SWA_NEG_INF ? 0.f : top;
+#pragma unroll 4
+      for (int p = ip.p0 + group; p <= ip.p1; p += 8) {
+        const size_t pr = partial(p);
+        const float2 ml = *reinterpret_cast<const float2*>(a.ml + pr * 2);
+        const float4 y = *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4);
+        const float w = ex2(ml.x - base);
+        l += w * ml.y;
+        o[0] += w * y.x;
+        o[1] += w * y.y;
+        o[2] += w * y.z;
+        o[3] += w * y.w;
+      }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], d);
+      }
+    }
+    if (group == 0) {
+      store_row<4>(a, a.o + row * D + run * 16 + sub * 4, o, l == 0.f ? 0.f : 1.f / l);
+      if (lane == 0 && run == 0) a.lse[row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
+    }
+  }
+}
+
 // The same with a block for 16 columns of a row, for calls with so few rows that each has very many
 // partials: 64 groups of 4 lanes take the partials in turn and meet in shared memory in a fixed order.
 template <int D>
@@ -964,18 +1019,22 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream
     swa_cache_attn_kernel<D><<<p.parts / (kWarps / p.MT), kThreads, C::kSmemBytes, stream>>>(
         tk, tv, c, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // A warp a row, or with fewer rows than four for every SM 16 columns a block.
-    const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv * p.NRT * p.rows;
+    // A warp a row where that fills the SMs; else a warp 16 columns of a row; and a block for them where
+    // even those are few.  (us of the whole call, a window of 1024, 32 / 8 heads, D = 128, as a row / a
+    // warp / a block: 1 sequence - / 12.6 / 11.2, 4 sequences 20.2 / 14 / 15.1, 16 sequences 21 / 18.6 /
+    // 32.8, 32 sequences 23.6 / 24.6 / -; one of 30,000 tokens at D = 256: - / 48 / 37.)
+    const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv * p.NRT * p.rows, runs = rows * (D / 16);
     const int64_t most = 8ll * sm_count();
-    if (rows >= 4ll * sm_count()) {
-      const int64_t blocks = (rows + 7) / 8;
-      e = launch_after(swa_cache_join_kernel<D>, static_cast<unsigned>(blocks < most ? blocks : most),
-                       stream, c, a);
-    } else {
-      const int64_t blocks = rows * (D / 16);
-      e = launch_after(swa_cache_join_few_kernel<D>,
-                       static_cast<unsigned>(blocks < most ? blocks : most), stream, c, a);
+    auto join = swa_cache_join_kernel<D>;
+    int64_t blocks = (rows + 7) / 8;
+    if (runs <= 4ll * sm_count()) {
+      join = swa_cache_join_few_kernel<D>;
+      blocks = runs;
+    } else if (rows < 6ll * sm_count()) {
+      join = swa_cache_join_part_kernel<D>;
+      blocks = (runs + 7) / 8;
     }
+    e = launch_after(join, static_cast<unsigned>(blocks < most ? blocks : most), stream, c, a);
     if (e != cudaSuccess) return e;
     if (args.accumulate) {
       // At most this many chunks of 4 warps' turns; the kernel walks what there really is.

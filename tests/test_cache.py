@@ -157,6 +157,10 @@ ATTN = [
     (4, 64, 16, 128, 64, 4, [900, 350, 0, 620], 2000, None, torch.bfloat16, True),
     (4, 32, 16, 256, 128, 5, [300, 350, 128, 620], 200, [5, 0, 3, 1], torch.float16, True),
     (9, 40, 20, 64, 32, 2, [100 + 61 * i for i in range(9)], 500, None, torch.bfloat16, True),
+    (8, 64, 16, 64, 32, 2, [100 + 97 * i for i in range(8)], 300, None, torch.float16, True),
+    (8, 32, 16, 256, 64, 4, [90 + 53 * i for i in range(8)], 200, None, torch.bfloat16, False),
+    # a warp joins 16 columns of a row
+    (6, 16, 4, 128, 64, 2, [700, 0, 31, 1200, 64, 333], 800, [2, 1, 0, 2, 1, 2], torch.bfloat16, True),
 ]
 
 
