@@ -8,7 +8,7 @@
 //   * The list of all chunks (32 keys, 16 at D = 256: 8 KB of keys and values at D >= 128) of all
 //     items is cut into equal parts, one per team (swa_cache_split.h), so ragged lengths and few
 //     heads fill the SMs alike.  One CTA of 8 warps per SM; a team is MT warps with 16 query rows
-//     each (MT = 1, 2, 4), which share its ring of chunks in shared memory.
+//     each, in long walks of many rows 32 (MT = 1, 2, 4), which share its ring in shared memory.
 //   * Chunks arrive by TMA, swizzled; 192 KB of ring keep 128 KB in flight per SM.  A lane looks up
 //     the pages and scales of one of the next 32 chunks, so the walk never waits for a table.
 //   * Codes become fp16 exactly (cvt.f16x2.e4m3x2).  S = Q K^T takes keys by ldmatrix, whose 8 x 16
@@ -43,7 +43,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSeqs = 1024;  // sequences per launch; more run as several launches
 
-template <int D>
+// kTiles: tiles of 16 query rows of a warp.
+template <int D, int kTiles = 1>
 struct AttnCfg {
   static constexpr int CK = D == 256 ? 16 : 32;          // keys of a chunk
   static constexpr int kCols = D < 128 ? D : 128;        // columns of a TMA box
@@ -51,8 +52,10 @@ struct AttnCfg {
   static constexpr int kBoxBytes = CK * kCols;
   static constexpr int kStageBytes = 2 * CK * D;         // keys, then values
   static constexpr int kStages = 192 * 1024 / kStageBytes;  // of the CTA, shared out to its teams
-  // D = 256 keeps its Q fragments in shared memory (64 KB), in place of 8 stages.
-  static constexpr int kQBytes = D == 256 ? kWarps * 16 * D * 2 : 0;
+  // Q fragments of 16 x 256 or 32 x 128 elements are kept in shared memory (64 KB), in place of a third
+  // of the stages.
+  static constexpr bool kQShared = D * kTiles >= 256;
+  static constexpr int kQBytes = kQShared ? kWarps * 16 * kTiles * D * 2 : 0;
   static constexpr int kRing = kStages - kQBytes / kStageBytes;
   static constexpr int kOffFirst = kRing * kStageBytes + kQBytes;
   static constexpr int kOffLen = kOffFirst + (kMaxSeqs + 2) * 8;  // lengths, then new tokens
@@ -144,131 +147,153 @@ struct ChunkInfo {
 };
 
 // The walk's state for one item.
-template <int D>
+template <int D, int kTiles>
 struct ItemState {
-  float acc[D / 8][4];  // o in units of vref; tile i of half x: columns 128 x + 16 n + i
-  float m[2], l[2];     // rows g, g + 8: running maximum (base 2) and this lane's part of the sum
+  struct Tile {
+    float acc[D / 8][4];  // o in units of vref; n-tile i of half x: columns 128 x + 16 n + i
+    float m[2], l[2];     // rows g, g + 8: running maximum (base 2) and this lane's part of the sum
+    float f[2];           // score factors of the two rows without the block's scale
+    int lo[2], hi[2];     // slots the two rows see, inclusive
+  } tile[kTiles];
   float vref;
-  float f[2];           // score factors of the two rows without the block's scale
-  int lo[2], hi[2];     // slots the two rows see, inclusive
   int any_lo, any_hi;   // slots any row sees
   int all_lo, all_hi;   // slots every real row sees
 };
 
-template <int D, bool kEdge>
-__device__ __forceinline__ void process_chunk(ItemState<D>& st, const uint32_t (*qf)[4],
+template <int D, int kTiles, bool kEdge>
+__device__ __forceinline__ void process_chunk(ItemState<D, kTiles>& st, const uint32_t (*qf)[4],
                                               uint32_t sq, uint32_t sk, const ChunkInfo& ci,
                                               float* scores, int rows, int row0) {
-  using C = AttnCfg<D>;
-  constexpr int CK = C::CK;
+  using C = AttnCfg<D, kTiles>;
+  constexpr int CK = C::CK, kSteps = D / 16;
   const uint32_t lane = lane_id(), g = lane >> 2, t = lane & 3u;
-  float s[CK / 8][4];
+  float s[kTiles][CK / 8][4];
 #pragma unroll
-  for (int j = 0; j < CK / 8; ++j)
+  for (int y = 0; y < kTiles; ++y)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[j][i] = 0.f;
+    for (int j = 0; j < CK / 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[y][j][i] = 0.f;
 #pragma unroll
   for (int x = 0; x < C::kBoxes; ++x) {
 #pragma unroll
     for (int cq = 0; cq < C::kCols / 64; ++cq) {
-      uint32_t qa[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int step = x * 8 + cq * 4 + i;
-        if constexpr (D == 256) {
-          lds_words<4>(sq + (step * 32 + lane) * 16, qa[i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) qa[i][e] = qf[step][e];
-        }
-      }
+      uint32_t key[CK / 8][4];  // codes of 8 keys, 4 steps of the contraction
 #pragma unroll
       for (int j = 0; j < CK / 8; ++j) {
         const uint32_t row = 8 * j + (lane & 7u);
         const uint32_t unit = (4 * cq + (lane >> 3)) ^ swizzle_of(C::kCols, row);
-        uint32_t r[4];
-        ldmatrix_x4(sk + x * C::kBoxBytes + row * C::kCols + (unit << 4), r);
+        ldmatrix_x4(sk + x * C::kBoxBytes + row * C::kCols + (unit << 4), key[j]);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {
+        const int step = x * 8 + cq * 4 + i;
+        uint32_t qa[kTiles][4];
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y) {
+          if constexpr (C::kQShared) {
+            lds_words<4>(sq + ((y * kSteps + step) * 32 + lane) * 16, qa[y]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qa[y][e] = qf[y * kSteps + step][e];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < CK / 8; ++j) {
           uint32_t b0, b1;
-          e4m3x4_to_f16(r[i], b0, b1);
-          mma16816(s[j], qa[i], b0, b1);
+          e4m3x4_to_f16(key[j][i], b0, b1);
+#pragma unroll
+          for (int y = 0; y < kTiles; ++y) mma16816(s[y][j], qa[y], b0, b1);
         }
       }
     }
   }
   // scores in base 2
-  const float f0 = st.f[0] * ci.ks, f1 = st.f[1] * ci.ks;
-  float mx0 = SWA_NEG_INF, mx1 = SWA_NEG_INF;
+  float mx[kTiles][2];
+  bool moves = !(ci.vs >= st.vref && ci.vs <= 64.f * st.vref);
 #pragma unroll
-  for (int j = 0; j < CK / 8; ++j) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s[j][i] *= f0;
-      s[j][2 + i] *= f1;
-      if (kEdge) {
-        const int slot = ci.slot + 8 * j + 2 * static_cast<int>(t) + i;
-        s[j][i] = slot >= st.lo[0] && slot <= st.hi[0] ? s[j][i] : SWA_NEG_INF;
-        s[j][2 + i] = slot >= st.lo[1] && slot <= st.hi[1] ? s[j][2 + i] : SWA_NEG_INF;
-      }
-      mx0 = fmaxf(mx0, s[j][i]);
-      mx1 = fmaxf(mx1, s[j][2 + i]);
-    }
-  }
-  if (scores != nullptr) {
+  for (int y = 0; y < kTiles; ++y) {
+    auto& tl = st.tile[y];
+    const float f0 = tl.f[0] * ci.ks, f1 = tl.f[1] * ci.ks;
+    float mx0 = SWA_NEG_INF, mx1 = SWA_NEG_INF;
 #pragma unroll
     for (int j = 0; j < CK / 8; ++j) {
-      const int r0 = row0 + static_cast<int>(g);
-      if (r0 < rows)
-        *reinterpret_cast<float2*>(scores + r0 * CK + 8 * j + 2 * t) = make_float2(s[j][0], s[j][1]);
-      if (r0 + 8 < rows)
-        *reinterpret_cast<float2*>(scores + (r0 + 8) * CK + 8 * j + 2 * t) =
-            make_float2(s[j][2], s[j][3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[y][j][i] *= f0;
+        s[y][j][2 + i] *= f1;
+        if (kEdge) {
+          const int slot = ci.slot + 8 * j + 2 * static_cast<int>(t) + i;
+          s[y][j][i] = slot >= tl.lo[0] && slot <= tl.hi[0] ? s[y][j][i] : SWA_NEG_INF;
+          s[y][j][2 + i] = slot >= tl.lo[1] && slot <= tl.hi[1] ? s[y][j][2 + i] : SWA_NEG_INF;
+        }
+        mx0 = fmaxf(mx0, s[y][j][i]);
+        mx1 = fmaxf(mx1, s[y][j][2 + i]);
+      }
     }
+    if (scores != nullptr) {
+#pragma unroll
+      for (int j = 0; j < CK / 8; ++j) {
+        const int r0 = row0 + 16 * y + static_cast<int>(g);
+        if (r0 < rows)
+          *reinterpret_cast<float2*>(scores + r0 * CK + 8 * j + 2 * t) =
+              make_float2(s[y][j][0], s[y][j][1]);
+        if (r0 + 8 < rows)
+          *reinterpret_cast<float2*>(scores + (r0 + 8) * CK + 8 * j + 2 * t) =
+              make_float2(s[y][j][2], s[y][j][3]);
+      }
+    }
+    mx[y][0] = quad_max(mx0);
+    mx[y][1] = quad_max(mx1);
+    moves = moves || mx[y][0] > tl.m[0] + 4.f || mx[y][1] > tl.m[1] + 4.f;
   }
-  mx0 = quad_max(mx0);
-  mx1 = quad_max(mx1);
   // The maximum and the value reference move only when a probability could reach 2^4, or a scale
   // leaves [vref, 64 vref]: p vs / vref then stays within fp16 and above its subnormals as far as
   // p itself is.
-  const bool moves = mx0 > st.m[0] + 4.f || mx1 > st.m[1] + 4.f ||
-                     !(ci.vs >= st.vref && ci.vs <= 64.f * st.vref);
   if (__any_sync(0xffffffffu, moves)) {
-    const float n0 = fmaxf(st.m[0], mx0), n1 = fmaxf(st.m[1], mx1);
     const float nref = ci.vs >= st.vref && ci.vs <= 64.f * st.vref ? st.vref : ci.vs * 0.125f;
-    const float a0 = st.m[0] == SWA_NEG_INF ? 0.f : ex2(st.m[0] - n0);
-    const float a1 = st.m[1] == SWA_NEG_INF ? 0.f : ex2(st.m[1] - n1);
     const float u = nref == st.vref ? 1.f : st.vref / nref;
-    // A sum that is NaN stays so (0 * NaN); before the first visible key everything is zero.
-    st.l[0] *= a0;
-    st.l[1] *= a1;
-    const float w0 = a0 * u, w1 = a1 * u;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      st.acc[i][0] *= w0;
-      st.acc[i][1] *= w0;
-      st.acc[i][2] *= w1;
-      st.acc[i][3] *= w1;
+    for (int y = 0; y < kTiles; ++y) {
+      auto& tl = st.tile[y];
+      const float n0 = fmaxf(tl.m[0], mx[y][0]), n1 = fmaxf(tl.m[1], mx[y][1]);
+      const float a0 = tl.m[0] == SWA_NEG_INF ? 0.f : ex2(tl.m[0] - n0);
+      const float a1 = tl.m[1] == SWA_NEG_INF ? 0.f : ex2(tl.m[1] - n1);
+      // A sum that is NaN stays so (0 * NaN); before the first visible key everything is zero.
+      tl.l[0] *= a0;
+      tl.l[1] *= a1;
+      const float w0 = a0 * u, w1 = a1 * u;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        tl.acc[i][0] *= w0;
+        tl.acc[i][1] *= w0;
+        tl.acc[i][2] *= w1;
+        tl.acc[i][3] *= w1;
+      }
+      tl.m[0] = n0;
+      tl.m[1] = n1;
     }
-    st.m[0] = n0;
-    st.m[1] = n1;
     st.vref = nref;
   }
-  const float b0 = st.m[0] == SWA_NEG_INF ? 0.f : st.m[0];
-  const float b1 = st.m[1] == SWA_NEG_INF ? 0.f : st.m[1];
   const float ratio = ci.vs / st.vref;
-  uint32_t pa[CK / 16][4];
+  uint32_t pa[kTiles][CK / 16][4];
 #pragma unroll
-  for (int j = 0; j < CK / 8; ++j) {
-    float p[4];
-    p[0] = ex2(s[j][0] - b0);
-    p[1] = ex2(s[j][1] - b0);
-    p[2] = ex2(s[j][2] - b1);
-    p[3] = ex2(s[j][3] - b1);
-    st.l[0] += p[0] + p[1];
-    st.l[1] += p[2] + p[3];
-    pa[j / 2][2 * (j & 1)] = pack_f16(p[0] * ratio, p[1] * ratio);
-    pa[j / 2][2 * (j & 1) + 1] = pack_f16(p[2] * ratio, p[3] * ratio);
+  for (int y = 0; y < kTiles; ++y) {
+    auto& tl = st.tile[y];
+    const float b0 = tl.m[0] == SWA_NEG_INF ? 0.f : tl.m[0];
+    const float b1 = tl.m[1] == SWA_NEG_INF ? 0.f : tl.m[1];
+#pragma unroll
+    for (int j = 0; j < CK / 8; ++j) {
+      float p[4];
+      p[0] = ex2(s[y][j][0] - b0);
+      p[1] = ex2(s[y][j][1] - b0);
+      p[2] = ex2(s[y][j][2] - b1);
+      p[3] = ex2(s[y][j][3] - b1);
+      tl.l[0] += p[0] + p[1];
+      tl.l[1] += p[2] + p[3];
+      pa[y][j / 2][2 * (j & 1)] = pack_f16(p[0] * ratio, p[1] * ratio);
+      pa[y][j / 2][2 * (j & 1) + 1] = pack_f16(p[2] * ratio, p[3] * ratio);
+    }
   }
   // o += P V
   const uint32_t sv = sk + CK * D;
@@ -303,21 +328,24 @@ __device__ __forceinline__ void process_chunk(ItemState<D>& st, const uint32_t (
         e4m3x4_to_f16(__byte_perm(v[2][w], v[3][w], 0x5140), c0, c1);
         e4m3x4_to_f16(__byte_perm(v[2][w], v[3][w], 0x7362), c2, c3);
         const int tile = x * (D > 128 ? 16 : 0) + 4 * w;
-        mma16816(st.acc[tile], pa[i], a0, c0);
-        mma16816(st.acc[tile + 1], pa[i], a1, c1);
-        mma16816(st.acc[tile + 2], pa[i], a2, c2);
-        mma16816(st.acc[tile + 3], pa[i], a3, c3);
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y) {
+          mma16816(st.tile[y].acc[tile], pa[y][i], a0, c0);
+          mma16816(st.tile[y].acc[tile + 1], pa[y][i], a1, c1);
+          mma16816(st.tile[y].acc[tile + 2], pa[y][i], a2, c2);
+          mma16816(st.tile[y].acc[tile + 3], pa[y][i], a3, c3);
+        }
       }
     }
   }
 }
 
-template <int D>
+template <int D, int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
     swa_cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const CacheView c,
                           const AttnDev a) {
-  using C = AttnCfg<D>;
+  using C = AttnCfg<D, kTiles>;
   constexpr int CK = C::CK;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!smem_base_ok(smem, c.err)) return;
@@ -433,66 +461,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   for (int i = 0; i < NS && i < count; ++i) issue(i, i, i >= 32);
 
-  const uint32_t sq = smem_u32(smem + C::kRing * C::kStageBytes) + static_cast<uint32_t>(warp) * 16 * D * 2;
+  const uint32_t sq = smem_u32(smem + C::kRing * C::kStageBytes) + static_cast<uint32_t>(warp) * 16 * kTiles * D * 2;
   constexpr int kSteps = D / 16;
-  uint32_t qf[D == 256 ? 1 : kSteps][4];
-  ItemState<D> st = {};
+  uint32_t qf[C::kQShared ? 1 : kTiles * kSteps][4];
+  ItemState<D, kTiles> st = {};
   int item = -1, b = 0, tile0 = 0, item_first = 0, item_chunks = 0;
   size_t base = 0;  // first row of the item, of all rows
   bool begins = false;
   const int g = lane >> 2, t = lane & 3;
-  const int r0 = wt * 16 + g;  // this thread's rows of the item: r0 and r0 + 8
+  const int r0 = wt * 16 * kTiles + g;  // this thread's rows of the item: r0, r0 + 8, r0 + 16, ..
 
   // Finishes the item after its chunk at `slot`.
   auto finish = [&](int slot) {
     const bool ends = slot / CK == item_first + item_chunks - 1;
-    const float l0 = quad_sum(st.l[0]), l1 = quad_sum(st.l[1]);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = r0 + 8 * e;
-      const float l = e == 0 ? l0 : l1;
+    for (int ye = 0; ye < 2 * kTiles; ++ye) {
+      const int e = ye & 1, r = r0 + 8 * ye;
+      const auto& tl = st.tile[ye >> 1];
+      const float l = quad_sum(tl.l[e]);
       if (tile0 + r >= a.R) continue;
       if (begins && ends) {
         const float inv = l == 0.f ? 0.f : st.vref / l;
         uint16_t* out = a.o + (base + r) * D;
 #pragma unroll
         for (int x = 0; x < (D > 128 ? 2 : 1); ++x) {
-          constexpr int kTiles = D < 128 ? 8 : 16;  // = columns of a run
+          constexpr int kRun = D < 128 ? 8 : 16;  // = columns of a run
 #pragma unroll
           for (int run = 0; run < 2; ++run) {
-            uint32_t pk[kTiles / 2];
+            uint32_t pk[kRun / 2];
 #pragma unroll
-            for (int i = 0; i < kTiles / 2; ++i) {
-              const float y0 = st.acc[x * 16 + 2 * i][2 * e + run] * inv;
-              const float y1 = st.acc[x * 16 + 2 * i + 1][2 * e + run] * inv;
+            for (int i = 0; i < kRun / 2; ++i) {
+              const float y0 = tl.acc[x * 16 + 2 * i][2 * e + run] * inv;
+              const float y1 = tl.acc[x * 16 + 2 * i + 1][2 * e + run] * inv;
               pk[i] = a.f16 ? Elem<true>::pack(y0, y1) : Elem<false>::pack(y0, y1);
             }
-            uint4* dst = reinterpret_cast<uint4*>(out + 128 * x + kTiles * (2 * t + run));
+            uint4* dst = reinterpret_cast<uint4*>(out + 128 * x + kRun * (2 * t + run));
 #pragma unroll
-            for (int i = 0; i < kTiles / 8; ++i)
+            for (int i = 0; i < kRun / 8; ++i)
               dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
           }
         }
-        if (t == 0) a.lse[base + r] = l == 0.f ? SWA_NEG_INF : (st.m[e] + log2f(l)) * kLn2;
+        if (t == 0) a.lse[base + r] = l == 0.f ? SWA_NEG_INF : (tl.m[e] + log2f(l)) * kLn2;
       } else {
         const size_t slot_row = static_cast<size_t>(partial_slot(part, begins)) * a.rows + r;
         float* out = a.po + slot_row * D;
 #pragma unroll
         for (int x = 0; x < (D > 128 ? 2 : 1); ++x) {
-          constexpr int kTiles = D < 128 ? 8 : 16;
+          constexpr int kRun = D < 128 ? 8 : 16;
 #pragma unroll
           for (int run = 0; run < 2; ++run) {
-            float4* dst = reinterpret_cast<float4*>(out + 128 * x + kTiles * (2 * t + run));
+            float4* dst = reinterpret_cast<float4*>(out + 128 * x + kRun * (2 * t + run));
 #pragma unroll
-            for (int i = 0; i < kTiles / 4; ++i)
-              dst[i] = make_float4(st.acc[x * 16 + 4 * i][2 * e + run] * st.vref,
-                                   st.acc[x * 16 + 4 * i + 1][2 * e + run] * st.vref,
-                                   st.acc[x * 16 + 4 * i + 2][2 * e + run] * st.vref,
-                                   st.acc[x * 16 + 4 * i + 3][2 * e + run] * st.vref);
+            for (int i = 0; i < kRun / 4; ++i)
+              dst[i] = make_float4(tl.acc[x * 16 + 4 * i][2 * e + run] * st.vref,
+                                   tl.acc[x * 16 + 4 * i + 1][2 * e + run] * st.vref,
+                                   tl.acc[x * 16 + 4 * i + 2][2 * e + run] * st.vref,
+                                   tl.acc[x * 16 + 4 * i + 3][2 * e + run] * st.vref);
           }
         }
         if (t == 0) {
-          a.ml[slot_row * 2] = st.m[e];
+          a.ml[slot_row * 2] = tl.m[e];
           a.ml[slot_row * 2 + 1] = l;
         }
       }
@@ -507,19 +535,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int len = s_len[b], n = s_new[b];
     base = (static_cast<size_t>(b) * c.Hkv + h) * a.R + tile0;
     // Both rows of q are on their way before anything waits for them.
-    uint2 raw[2][kSteps];
+    uint2 raw[2 * kTiles][kSteps];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 2 * kTiles; ++e) {
       const uint32_t r = static_cast<uint32_t>(tile0 + r0 + 8 * e);
       const int tq = static_cast<int>(a.div_t.mod(r));
       const bool real = static_cast<int>(r) < a.R && tq < n;
       const uint2* row = reinterpret_cast<const uint2*>(a.q + (base + r0 + 8 * e) * D) + t;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) raw[e][i] = real ? __ldg(row + 4 * i) : make_uint2(0u, 0u);
-      st.lo[e] = visible_lo(len + tq, a.window);
-      st.hi[e] = real ? len + tq : -1;
-      st.m[e] = SWA_NEG_INF;
-      st.l[e] = 0.f;
+      auto& tl = st.tile[e >> 1];
+      tl.lo[e & 1] = visible_lo(len + tq, a.window);
+      tl.hi[e & 1] = real ? len + tq : -1;
+      tl.m[e & 1] = SWA_NEG_INF;
+      tl.l[e & 1] = 0.f;
     }
     item_first = first_chunk(len, a.window, CK);
     item_chunks = chunk_count(len, n, a.window, CK);
@@ -529,13 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.all_lo = visible_lo(len + n - 1, a.window);
     st.all_hi = n < c.T ? -1 : len;  // a row without a query sees nothing
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int ye = 0; ye < 2 * kTiles; ++ye) {
+      const int y = ye >> 1, e = ye & 1;
       // The row as fp16, its largest element brought to [2^14, 2^15) (a row below 2^-112 less far).
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[e][i].x) : Elem<false>::unpack(raw[e][i].x);
-        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[e][i].y) : Elem<false>::unpack(raw[e][i].y);
+        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[ye][i].x) : Elem<false>::unpack(raw[ye][i].x);
+        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[ye][i].y) : Elem<false>::unpack(raw[ye][i].y);
         top = max(max(top, __float_as_uint(fabsf(y0.x))), __float_as_uint(fabsf(y0.y)));
         top = max(max(top, __float_as_uint(fabsf(y1.x))), __float_as_uint(fabsf(y1.y)));
       }
@@ -545,27 +575,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 2^(14 - exponent); 1 for zero, infinity and NaN
       const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-      st.f[e] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      st.tile[y].f[e] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[e][i].x) : Elem<false>::unpack(raw[e][i].x);
-        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[e][i].y) : Elem<false>::unpack(raw[e][i].y);
+        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[ye][i].x) : Elem<false>::unpack(raw[ye][i].x);
+        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[ye][i].y) : Elem<false>::unpack(raw[ye][i].y);
         const uint32_t p0 = pack_f16(y0.x * up, y0.y * up);
         const uint32_t p1 = pack_f16(y1.x * up, y1.y * up);
-        if constexpr (D == 256) {
-          st_shared_b32(sq + (i * 32 + lane) * 16 + 4 * e, p0);
-          st_shared_b32(sq + (i * 32 + lane) * 16 + 8 + 4 * e, p1);
+        if constexpr (C::kQShared) {
+          const uint32_t to = sq + ((y * kSteps + i) * 32 + lane) * 16 + 4 * e;
+          st_shared_b32(to, p0);
+          st_shared_b32(to + 8, p1);
         } else {
-          qf[i][e] = p0;
-          qf[i][2 + e] = p1;
+          qf[y * kSteps + i][e] = p0;
+          qf[y * kSteps + i][2 + e] = p1;
         }
       }
     }
     st.vref = 1.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int y = 0; y < kTiles; ++y)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) st.acc[i][e] = 0.f;
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.tile[y].acc[i][e] = 0.f;
     __syncwarp();
   };
 
@@ -596,15 +629,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     : a.scores + static_cast<size_t>(begin + i) * a.rows * CK;
     const bool edge = ci.plane < 0 || ci.slot < st.all_lo || ci.slot + CK - 1 > st.all_hi;
     if (edge) {
-      ItemState<D>& e = st;
-      const int lo0 = e.lo[0], lo1 = e.lo[1], any = e.any_lo;
-      if (ci.plane < 0) e.lo[0] = e.lo[1] = e.any_lo = INT_MAX;  // nothing of it is seen
-      process_chunk<D, true>(e, qf, sq, sk, ci, sc, a.rows, wt * 16);
-      e.lo[0] = lo0;
-      e.lo[1] = lo1;
+      ItemState<D, kTiles>& e = st;
+      int lo[2 * kTiles];
+      const int any = e.any_lo;
+#pragma unroll
+      for (int y = 0; y < 2 * kTiles; ++y) {
+        lo[y] = e.tile[y >> 1].lo[y & 1];
+        if (ci.plane < 0) e.tile[y >> 1].lo[y & 1] = INT_MAX;  // nothing of it is seen
+      }
+      if (ci.plane < 0) e.any_lo = INT_MAX;
+      process_chunk<D, kTiles, true>(e, qf, sq, sk, ci, sc, a.rows, wt * 16 * kTiles);
+#pragma unroll
+      for (int y = 0; y < 2 * kTiles; ++y) e.tile[y >> 1].lo[y & 1] = lo[y];
       e.any_lo = any;
     } else {
-      process_chunk<D, false>(st, qf, sq, sk, ci, sc, a.rows, wt * 16);
+      process_chunk<D, kTiles, false>(st, qf, sq, sk, ci, sc, a.rows, wt * 16 * kTiles);
     }
     __syncwarp();
     done = i + 1;
@@ -929,26 +968,43 @@ __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView 
 }
 
 struct Plan {
-  int R, MT, RT, NRT, rows, parts, ck;
+  int R, tiles, MT, RT, NRT, rows, parts, ck;
   size_t off_ml, off_po, off_scores, bytes;
 };
 
-Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int accumulate) {
+// The workspace's layout is the same for every window.
+Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int accumulate, int window) {
   Plan p;
   p.R = Hq / Hkv * T;
+  p.ck = D == 256 ? AttnCfg<256>::CK : AttnCfg<128>::CK;
   // A team covers as many rows as share its chunks: 16, 32 or 64.
   p.MT = p.R <= 16 ? 1 : p.R <= 32 ? 2 : 4;
   p.RT = 16 * p.MT;
   p.NRT = (p.R + p.RT - 1) / p.RT;
   p.rows = p.R < p.RT ? p.R : p.RT;
+  p.tiles = 1;
+  size_t parts = static_cast<size_t>(sm_count()) * (kWarps / p.MT);
+  if (p.R > 16 && D < 256) {
+    // Two tiles a warp halve the conversions of a chunk's codes, and twice as many chunks are in work;
+    // but twice as many parts have twice the partial results.  So long walks take them, by the most that
+    // the table and the window allow (32 / 8 heads, T = 8, D = 128, 64 sequences of 4,000: 146 us and 174
+    // with one; under a window of 1024, 16 sequences: 34 and 26).
+    parts *= 2;
+    const int64_t slots = static_cast<int64_t>(max_pages) * page;
+    const int64_t span = window + T - 1 < slots ? window + T - 1 : slots;
+    const int64_t chunks = (span + p.ck - 2) / p.ck + 1;  // of an item, at most
+    if (static_cast<int64_t>(B) * Hkv * p.NRT * chunks >= 32 * static_cast<int64_t>(parts)) {
+      p.tiles = 2;
+      p.MT /= 2;
+    }
+  }
   p.parts = sm_count() * (kWarps / p.MT);
-  p.ck = D == 256 ? AttnCfg<256>::CK : AttnCfg<128>::CK;
   auto round = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   size_t off = round((kMaxSeqs + 1) * sizeof(int64_t));
   p.off_ml = off;
-  off += round(static_cast<size_t>(2 * p.parts) * p.rows * 2 * sizeof(float));
+  off += round(2 * parts * p.rows * 2 * sizeof(float));
   p.off_po = off;
-  off += round(static_cast<size_t>(2 * p.parts) * p.rows * D * sizeof(float));
+  off += round(2 * parts * p.rows * D * sizeof(float));
   p.off_scores = off;
   if (accumulate) {
     const size_t chunks = static_cast<size_t>(max_pages) * page / p.ck;
@@ -975,17 +1031,16 @@ cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D>
-cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream_t stream) {
-  using C = AttnCfg<D>;
-  const Plan p = plan_of(all.B, args.Hq, all.Hkv, all.T, D, all.max_pages, all.page,
-                         args.accumulate);
+template <int D, int kTiles>
+cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan& p,
+                     cudaStream_t stream) {
+  using C = AttnCfg<D, kTiles>;
   CUtensorMap tk, tv;
   const uint64_t planes = static_cast<uint64_t>(all.pages) * all.Hkv;
   if (!make_tmap_u8(&tk, all.k, planes, all.page, D, C::CK) ||
       !make_tmap_u8(&tv, all.v, planes, all.page, D, C::CK))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<swa_cache_attn_kernel<D>>(C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_cache_attn_kernel<D, kTiles>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(args.workspace);
   AttnDev a;
@@ -1016,8 +1071,8 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream
     a.q = static_cast<const uint16_t*>(args.q) + row0 * D;
     a.o = static_cast<uint16_t*>(args.o) + row0 * D;
     a.lse = args.lse + row0;
-    swa_cache_attn_kernel<D><<<p.parts / (kWarps / p.MT), kThreads, C::kSmemBytes, stream>>>(
-        tk, tv, c, a);
+    swa_cache_attn_kernel<D, kTiles>
+        <<<p.parts / (kWarps / p.MT), kThreads, C::kSmemBytes, stream>>>(tk, tv, c, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // A warp a row where that fills the SMs; else a warp 16 columns of a row; and a block for them where
     // even those are few.  (us of the whole call, a window of 1024, 32 / 8 heads, D = 128, as a row / a
@@ -1052,13 +1107,16 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, cudaStream
 
 size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
                                   int accumulate) {
-  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate).bytes;
+  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate, 1).bytes;
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream) {
-  if (c.D == 64) return launch_d<64>(c, a, stream);
-  if (c.D == 128) return launch_d<128>(c, a, stream);
-  return launch_d<256>(c, a, stream);
+  const Plan p = plan_of(c.B, a.Hq, c.Hkv, c.T, c.D, c.max_pages, c.page, a.accumulate, a.window);
+  if (c.D == 64)
+    return p.tiles == 2 ? launch_d<64, 2>(c, a, p, stream) : launch_d<64, 1>(c, a, p, stream);
+  if (c.D == 128)
+    return p.tiles == 2 ? launch_d<128, 2>(c, a, p, stream) : launch_d<128, 1>(c, a, p, stream);
+  return launch_d<256, 1>(c, a, p, stream);
 }
 
 }  // namespace swa

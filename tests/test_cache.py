@@ -193,6 +193,41 @@ def test_attn(swa, B, H_q, H, D, page, T, lens, window, new, dtype, acc):
     assert torch.equal(go, go2) and torch.equal(gl, gl2) and torch.equal(w, cache.weight)
 
 
+@pytest.mark.parametrize("B,H_q,H,D,page,T,lens,window,new,dtype,acc,longest", [
+    (2, 8, 1, 128, 64, 5, [2000, 65], 1 << 20, None, torch.bfloat16, True, 700000),
+    (3, 14, 2, 128, 32, 3, [900, 0, 33], 1 << 20, [3, 0, 2], torch.float16, True, 300000),
+    (2, 24, 3, 64, 128, 3, [1500, 127], 1 << 20, None, torch.bfloat16, True, 250000),
+    (2, 7, 1, 64, 64, 9, [31, 1100], 400000, [9, 4], torch.float16, False, 500000),
+    (1, 8, 4, 64, 32, 64, [300], 1 << 20, None, torch.bfloat16, True, 200000),
+    (40, 112, 16, 64, 32, 5, [1300, 1024] + [11 * b for b in range(38)], 1000, None, torch.float16,
+     False, 1536),
+    (40, 42, 14, 128, 32, 12, [1400, 90] + [7 * b for b in range(38)], 1200,
+     [12 - b % 4 for b in range(40)], torch.bfloat16, True, 1536),
+])
+def test_attn_long_tables(swa, B, H_q, H, D, page, T, lens, window, new, dtype, acc, longest):
+    """Many rows under a table (and window) for long sequences, whatever their lengths are: a warp has two
+    tiles of rows.  What the table holds behind the last token is no page."""
+    g = _gen(D + B)
+    width = -(-(max(lens) + T) // page)
+    cache = _cache(swa, g, B * width, H, D, page, spread=4)
+    table = torch.full((B, longest // page), -1, dtype=torch.int32, device="cuda")
+    table[:, :width] = _table(g, B, width)
+    for b in range(B):
+        table[b, -(-(lens[b] + (T if new is None else new[b])) // page):] = -1
+    q = torch.randn((B, H_q, T, D), generator=g, device="cuda").to(dtype)
+    pool = ref.pool_of(cache)
+    o, lse, to, tl, tw = ref.attn(pool, table, lens, q, window, new=new, accumulate=acc)
+    go, gl = swa.swa_cache_attn(q, cache, table, _ints(lens), window, new=_ints(new),
+                                accumulate=acc)
+    swa.swa_check_device()
+    _near(go, o, to, "o")
+    _near(gl, lse, tl, "lse")
+    if acc:
+        _near(cache.weight, pool["weight"], tw, "weight")
+    again = swa.swa_cache_attn(q, cache, table, _ints(lens), window, new=_ints(new))
+    assert torch.equal(go, again[0]) and torch.equal(gl, again[1])
+
+
 def test_attn_reads_nothing_outside_the_window(swa):
     """Table entries of pages wholly before the window, or behind the last token, may name no page
     at all, and NaN tokens outside a query's range change nothing for it."""
