@@ -409,8 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t total = s_first[c.B] * per;
   // Neighbouring parts go to different SMs: with few chunks every SM still gets some.
   const int part = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-  const Parts cut(total, a.parts);
-  const int64_t begin = cut.start(part), count = cut.start(part + 1) - begin;
+  const Parts cut(total, used_parts(total, a.parts, a.rows * D));
+  const int64_t begin = part < cut.parts ? cut.start(part) : total;
+  const int64_t count = part < cut.parts ? cut.start(part + 1) - begin : 0;
 
   auto load_info = [&](int64_t i) {  // chunk i of the part
     ChunkInfo ci = {-1, 0, -1, 1.f, 1.f};
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(256) swa_cache_join_kernel(const CacheView c, 
   const int lane = static_cast<int>(lane_id());
   const int per = c.Hkv * a.NRT;
   const int64_t total = a.first[c.B] * per;
-  const Parts cut(total, a.parts);
+  const Parts cut(total, used_parts(total, a.parts, a.rows * D));
   const uint32_t tasks = static_cast<uint32_t>(c.B) * per * a.rows;
   for (uint32_t task = blockIdx.x * 8 + warp_id(); task < tasks; task += gridDim.x * 8) {
     const int item = static_cast<int>(task / static_cast<uint32_t>(a.rows));
@@ -783,7 +784,8 @@ __global__ void __launch_bounds__(256) swa_cache_join_part_kernel(const CacheVie
   launch_dependents();
   const int lane = static_cast<int>(lane_id()), group = lane / 4, sub = lane % 4;
   const int per = c.Hkv * a.NRT;
-  const Parts cut(a.first[c.B] * per, a.parts);
+  const int64_t total = a.first[c.B] * per;
+  const Parts cut(total, used_parts(total, a.parts, a.rows * D));
   const uint32_t tasks = static_cast<uint32_t>(c.B) * per * a.rows * kRuns;
   for (uint32_t task = blockIdx.x * 8 + warp_id(); task < tasks; task += gridDim.x * 8) {
     const int run = static_cast<int>(task % kRuns);
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(256) swa_cache_join_few_kernel(const CacheView
   const int tid = static_cast<int>(threadIdx.x), group = tid / 4, sub = tid % 4;
   const int per = c.Hkv * a.NRT;
   const int64_t total = a.first[c.B] * per;
-  const Parts cut(total, a.parts);
+  const Parts cut(total, used_parts(total, a.parts, a.rows * D));
   const uint32_t tasks = static_cast<uint32_t>(c.B) * per * a.rows * kRuns;
   for (uint32_t task = blockIdx.x; task < tasks; task += gridDim.x) {
     const int run = static_cast<int>(task % kRuns);

@@ -3,11 +3,13 @@
 //
 // The visible slots of a sequence are cut at multiples of CK slots into chunks.  All chunks of all
 // items (sequence, kv head, tile of query rows) form one list, item after item; the list is cut into
-// as many parts as there are teams of warps, equal within one chunk whatever the sequences' lengths.
+// as many parts as there are teams of warps, or fewer where their partial results would be more than
+// they are worth, equal within one chunk whatever the sequences' lengths.
 // A team walks its part from left to right: items that lie wholly inside it are finished there, and at
 // most two, its first and its last, continue in a neighbour and leave a partial result.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 #ifdef __CUDACC__
@@ -37,9 +39,9 @@ SWA_HD int64_t quotient(int64_t x, int64_t d) {
 // A list of `total` chunks in `parts` parts: the first `extra` have size + 1 chunks, the others size.
 struct Parts {
   int64_t size;
-  int extra;
-  SWA_HD Parts(int64_t total, int parts)
-      : size(quotient(total, parts)), extra(static_cast<int>(total - size * parts)) {}
+  int parts, extra;
+  SWA_HD Parts(int64_t total, int n)
+      : size(quotient(total, n)), parts(n), extra(static_cast<int>(total - size * n)) {}
   // First chunk of part i (parts + 1 of them: the last is the total).
   SWA_HD int64_t start(int i) const { return size * i + (i < extra ? i : extra); }
   // The part of chunk x < total.
@@ -48,6 +50,17 @@ struct Parts {
     return static_cast<int>(x < longer ? quotient(x, size + 1) : extra + quotient(x - longer, size));
   }
 };
+
+// How many of `parts` parts a list of `total` chunks is cut into, when a part's partial result has `size`
+// floats.  Parts of n chunks take about n us, and 8 size total / n bytes of partial results, written and
+// read at 3 TB/s; the sum is least at n^2 = 8 size total / 3 MB.  n is rounded down.  (One kv head, 24
+// rows, D = 256, 14,000 tokens: 21 us, 30 with all parts; 64 rows: 33 and 47.)
+SWA_HD int used_parts(int64_t total, int parts, int size) {
+  const int64_t n = static_cast<int64_t>(
+      sqrtf(static_cast<float>(total) * (static_cast<float>(size) * (1.f / 375000.f))));
+  const int64_t used = n > 1 ? quotient(total + n - 1, n) : total;
+  return used >= parts ? parts : used < 1 ? 1 : static_cast<int>(used);
+}
 
 // A part's two partial results: 0 continues an item begun in an earlier part, 1 begins one.
 SWA_HD int partial_slot(int part, bool begins) { return 2 * part + (begins ? 1 : 0); }

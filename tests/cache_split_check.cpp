@@ -23,7 +23,7 @@ int main() {
   std::mt19937 rng(7);
   auto pick = [&](int lo, int hi) { return lo + static_cast<int>(rng() % (hi - lo + 1)); };
   for (int round = 0; round < 3000; ++round) {
-    const int B = pick(1, 9), per = pick(1, 5), parts = pick(1, 40), ck = pick(0, 1) ? 32 : 16;
+    const int B = pick(1, 9), per = pick(1, 5), most = pick(1, 40), ck = pick(0, 1) ? 32 : 16;
     const int window = pick(0, 2) ? pick(1, 300) : 1 << 30;
     std::vector<int64_t> first(B + 1, 0);
     std::vector<int> len(B), n(B);
@@ -40,6 +40,11 @@ int main() {
       first[b + 1] = first[b] + nc;
     }
     const int64_t total = first[B] * per;
+    const int size = pick(0, 1) ? pick(1, 4000) : pick(4000, 2000000);
+    const int parts = used_parts(total, most, size);
+    CHECK(parts >= 1 && parts <= most && parts <= (total > 0 ? total : 1));
+    CHECK(used_parts(total, most, 1) == (total >= most ? most : total > 0 ? total : 1));
+    CHECK(used_parts(total, most, size + 1000) <= parts);
     if (total == 0) continue;
     std::set<int> slots;
     const Parts cut(total, parts);
@@ -99,6 +104,7 @@ int main() {
     const int i = cut.of(x);
     CHECK(i >= 0 && i < parts && cut.start(i) <= x && x < cut.start(i + 1));
     CHECK(quotient(x, parts) == x / parts);
+    CHECK(used_parts(total, parts, 16384) == parts);
   }
   std::puts("ok");
   return 0;
