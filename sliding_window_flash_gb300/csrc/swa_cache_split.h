@@ -56,9 +56,12 @@ struct Parts {
 // read at 3 TB/s; the sum is least at n^2 = 8 size total / 3 MB.  n is rounded down.  (One kv head, 24
 // rows, D = 256, 14,000 tokens: 21 us, 30 with all parts; 64 rows: 33 and 47.)
 SWA_HD int used_parts(int64_t total, int parts, int size) {
-  const int64_t n = static_cast<int64_t>(
-      sqrtf(static_cast<float>(total) * (static_cast<float>(size) * (1.f / 375000.f))));
-  const int64_t used = n > 1 ? quotient(total + n - 1, n) : total;
+  int64_t used = total;
+  if (total * size >= 4 * 375000ll) {  // n is at least 2
+    const int64_t n = static_cast<int64_t>(
+        sqrtf(static_cast<float>(total) * (static_cast<float>(size) * (1.f / 375000.f))));
+    used = n > 1 ? quotient(total + n - 1, n) : total;
+  }
   return used >= parts ? parts : used < 1 ? 1 : static_cast<int>(used);
 }
 

@@ -35,7 +35,7 @@ def test_split_matches_brute_force(tmp_path):
     ("const int64_t longer = (size + 1) * extra;", "const int64_t longer = size * extra;"),
     ("((x | d) >> 32) == 0", "true"),
     ("if (first[mid] * per <= x)", "if (first[mid] * per < x)"),
-    ("n > 1 ? quotient(total + n - 1, n) : total", "n > 1 ? quotient(total, n) : 2 * total"),
+    ("used = n > 1 ? quotient(total + n - 1, n) : total;", "used = total + n;"),
     ("used < 1 ? 1 :", "false ? 1 :"),
     ("2 * part + (begins ? 1 : 0)", "part + (begins ? 1 : 0)"),
 ])
