@@ -373,11 +373,15 @@ __global__ void __launch_bounds__(kMoveThreads + kLookThreads, 4)
 }  // namespace
 
 cudaError_t launch_cache_evict(const CacheView& c, const CacheEvictArgs& a, cudaStream_t stream) {
-  // CTAs of a cluster: as many as the SMs hold at once, with at least 2048 slots each.
+  // CTAs of a cluster: as many as there are SMs for, with at least 2048 slots each; two for each SM where
+  // they have 12,288 (8 sequences of 32,768 tokens, 8 heads: 45 us, 50 otherwise; 16 of 8,192: 24, or 27
+  // with two for each SM there too).
   const long long slots = static_cast<long long>(c.max_pages) * c.page;
   const long long heads = static_cast<long long>(c.B) * c.Hkv;
   int ctas = 1;
-  while (ctas < kMaxCluster && heads * ctas * 2 <= sm_count() && slots > 2048ll * ctas) ctas *= 2;
+  while (ctas < kMaxCluster && ((heads * ctas * 2 <= sm_count() && slots > 2048ll * ctas) ||
+                                (heads * ctas <= sm_count() && slots > 12288ll * ctas)))
+    ctas *= 2;
   const long long slice = (slots + ctas - 1) / ctas + kSelectWarps * 128;
   const int held = static_cast<int>(slice < kMaxHeld ? slice : kMaxHeld);
   const int bytes = static_cast<int>(sizeof(SelectShared)) + held * 4;
