@@ -20,6 +20,9 @@
  * replays with whatever they hold then.  max_pages * page < 2^30, pages * Hkv < 2^31, B * Hkv < 2^31,
  * and B and Hkv at most 65535.
  *
+ * Alignment: 16 bytes for codes, k, v, q, o, the cache's weight and workspaces; 4 bytes (an element) for
+ * scales, lse, the weights of append and key_weights, tables and lengths.
+ *
  * What the device reads is checked there: a page number outside the pool, a sequence longer than
  * its table or a negative length is not followed; the call skips that page or sequence (attention
  * treats its tokens as unseen) and sets the device error word: swa_check_device returns

@@ -25,9 +25,9 @@ swa_status check_cache(const swa_cache* c, const int* table, int max_pages, cons
       static_cast<long long>(c->pages) * c->Hkv >= kIndexLimit ||
       static_cast<long long>(B) * c->Hkv >= kIndexLimit || B > 65535 || c->Hkv > 65535)
     return SWA_ERR_INVALID_ARG;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) ||
-      !aligned(c->v_scale, 16) || !aligned(c->weight, 16) || !aligned(table, 4) ||
-      !aligned(lens, 4))
+  // What is read an element at a time needs an element's alignment only, here and in the calls below.
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+      !aligned(c->v_scale, 4) || !aligned(c->weight, 16) || !aligned(table, 4) || !aligned(lens, 4))
     return SWA_ERR_MISALIGNED;
   return SWA_OK;
 }
@@ -99,7 +99,7 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
   if (!k || !v || T < 1 || dtype < SWA_BF16 || dtype > SWA_FP32) return SWA_ERR_INVALID_ARG;
   if (weight && !cache->weight) return SWA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * cache->Hkv * T >= kIndexLimit) return SWA_ERR_INVALID_ARG;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(weight, 16) || !aligned(new_lens, 4))
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(weight, 4) || !aligned(new_lens, 4))
     return SWA_ERR_MISALIGNED;
   unsigned* err = nullptr;
   if ((st = swa::device_error_word(&err)) != SWA_OK) return st;
@@ -134,7 +134,7 @@ swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_page
   const size_t need = swa_cache_attn_workspace_bytes(B, Hq, cache->Hkv, T, cache->D, max_pages,
                                                      cache->page, accumulate);
   if (need != 0 && (!workspace || workspace_bytes < need)) return SWA_ERR_WORKSPACE;
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16) ||
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(new_lens, 4))
     return SWA_ERR_MISALIGNED;
   unsigned* err = nullptr;
@@ -200,7 +200,7 @@ swa_status swa_attn_key_weights(const void* q, const void* k, const float* lse, 
                                         dtype == SWA_FP16, nullptr);
   const size_t need = swa::key_weights_workspace_bytes(pb);
   if (need != 0 && (!workspace || workspace_bytes < need)) return SWA_ERR_WORKSPACE;
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 16) || !aligned(w, 16) ||
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 4) || !aligned(w, 4) ||
       !aligned(workspace, 16))
     return SWA_ERR_MISALIGNED;
   if ((st = swa::device_error_word(&pb.err)) != SWA_OK) return st;

@@ -892,3 +892,35 @@ def test_binding_refusals(swa):
     torch.cuda.synchronize()
     swa.swa_check_device()
     assert (ref.pool_of(cache)["k"] == 0).all()
+
+
+def test_elements_need_only_their_own_alignment(swa):
+    """Scales, lse and weights that begin one element behind a 16-byte boundary give the same bits."""
+    g = _gen(81)
+    B, H_q, H, D, page, T = 2, 4, 2, 64, 32, 3
+    cache = _cache(swa, g, 8, H, D, page, spread=3)
+    table, lens = _table(g, B, 4), _ints([70, 33])
+    q = torch.randn((B, H_q, T, D), generator=g, device="cuda").to(torch.bfloat16)
+    k = torch.randn((B, H, T, D), generator=g, device="cuda").to(torch.bfloat16)
+
+    def off(x):
+        y = torch.zeros(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape)
+        return y.copy_(x)
+
+    odd = swa.SwaCache(cache.k.view(torch.uint8).clone().view(torch.float8_e4m3fn),
+                       cache.v.view(torch.uint8).clone().view(torch.float8_e4m3fn),
+                       off(cache.k_scale), off(cache.v_scale), cache.weight.clone())
+    given = torch.rand((B, H, T), generator=g, device="cuda")
+    out = []
+    for c, move in ((cache, lambda x: x), (odd, off)):
+        swa.swa_cache_append(c, move(table), move(lens), k, k, weight=move(given))
+        lse = move(torch.zeros((B, H_q, T), device="cuda"))
+        o, _ = swa.swa_cache_attn(q, c, move(table), move(lens), 50, accumulate=True, lse=lse)
+        w = swa.swa_attn_key_weights(q, k, move(lse), 2, out=move(torch.zeros((B, H, T), device="cuda")))
+        spare = [p for p in range(8) if p not in table[:, :3].flatten().tolist()]
+        dst = _ints([[spare[0]], [spare[1]]])
+        kept, m = swa.swa_cache_evict(c, move(table[:, :3].contiguous()), move(lens), move(dst), 30, 4)
+        swa.swa_check_device()
+        out.append((o, lse, w, kept, m, *ref.pool_of(c).values()))
+    for x, y in zip(*out):
+        assert torch.equal(torch.nan_to_num(x, nan=1e9), torch.nan_to_num(y, nan=1e9))

@@ -39,8 +39,8 @@ def _c(k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, w=FAKE, pages=9, H=2, page=64, D=128):
 CACHE_FAULTS = [
     (dict(k=0), 1), (dict(v=0), 1), (dict(ks=0), 1), (dict(vs=0), 1), (dict(pages=0), 1),
     (dict(H=0), 1), (dict(page=16), 2), (dict(page=48), 2), (dict(page=256), 2), (dict(D=96), 2),
-    (dict(D=512), 2), (dict(k=FAKE + 8), 3), (dict(v=FAKE + 4), 3), (dict(ks=FAKE + 4), 3),
-    (dict(vs=FAKE + 8), 3), (dict(w=FAKE + 4), 3), (dict(pages=1 << 30, H=2), 1),
+    (dict(D=512), 2), (dict(k=FAKE + 8), 3), (dict(v=FAKE + 4), 3), (dict(ks=FAKE + 2), 3),
+    (dict(vs=FAKE + 1), 3), (dict(w=FAKE + 4), 3), (dict(pages=1 << 30, H=2), 1),
 ]
 
 
@@ -77,7 +77,7 @@ def test_bad_tables(lib, call):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(k=0), 1), (dict(v=0), 1), (dict(T=0), 1), (dict(dtype=3), 1), (dict(dtype=-1), 1),
-    (dict(k=FAKE + 8), 3), (dict(v=FAKE + 8), 3), (dict(w=FAKE + 4), 3), (dict(new=FAKE + 2), 3),
+    (dict(k=FAKE + 8), 3), (dict(v=FAKE + 8), 3), (dict(w=FAKE + 2), 3), (dict(new=FAKE + 2), 3),
     (dict(B=1 << 15, T=1 << 16), 1),
 ])
 def test_append_refusals(lib, kw, code):
@@ -94,7 +94,7 @@ def test_weights_need_a_cache_that_holds_them(lib):
     (dict(q=0), 1), (dict(o=0), 1), (dict(lse=0), 1), (dict(Hq=0), 1), (dict(Hq=3), 1),
     (dict(W=0), 1), (dict(T=0), 1), (dict(T=65), 1), (dict(scale=0.0), 1),
     (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(acc=2), 1),
-    (dict(dtype=2), 1), (dict(q=FAKE + 8), 3), (dict(o=FAKE + 8), 3), (dict(lse=FAKE + 4), 3),
+    (dict(dtype=2), 1), (dict(q=FAKE + 8), 3), (dict(o=FAKE + 8), 3), (dict(lse=FAKE + 2), 3),
     (dict(new=FAKE + 2), 3),
 ])
 def test_attn_refusals(lib, kw, code):
@@ -145,7 +145,8 @@ def _weights(lib, q=FAKE, k=FAKE, lse=FAKE, w=FAKE, B=1, Hq=4, H=2, Lq=16, Lk=20
     (dict(q=0), 1), (dict(k=0), 1), (dict(lse=0), 1), (dict(w=0), 1), (dict(B=0), 1),
     (dict(Hq=3), 1), (dict(Lq=0), 1), (dict(Lq=21), 1), (dict(W=0), 1), (dict(causal=2), 1),
     (dict(scale=-1.0), 1), (dict(dtype=2), 1), (dict(D=96), 2), (dict(q=FAKE + 8), 3),
-    (dict(w=FAKE + 4), 3), (dict(B=1 << 16, Lq=1 << 14, Lk=1 << 14), 1),
+    (dict(w=FAKE + 2), 3), (dict(lse=FAKE + 1), 3), (dict(k=FAKE + 8), 3),
+    (dict(B=1 << 16, Lq=1 << 14, Lk=1 << 14), 1),
 ])
 def test_key_weights_refusals(lib, kw, code):
     assert _weights(lib, **kw) == code
