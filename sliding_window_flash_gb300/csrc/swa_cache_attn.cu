@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   for (int i = 0; i < NS && i < count; ++i) issue(i, i, i >= 32);
 
-  const uint32_t sq = smem_u32(smem + C::kRing * C::kStageBytes) + static_cast<uint32_t>(warp) * 16 * kTiles * D * 2;
+  const uint32_t sq = smem_u32(smem + C::kRing * C::kStageBytes) +
+                      static_cast<uint32_t>(warp) * 16 * kTiles * D * 2;
   constexpr int kSteps = D / 16;
   uint32_t qf[C::kQShared ? 1 : kTiles * kSteps][4];
   ItemState<D, kTiles> st = {};
@@ -950,7 +951,8 @@ __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView 
       float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int rt = 0; rt < a.NRT; ++rt) {
         const int rows = min(a.rows, a.R - rt * a.RT);
-        const float* sc = a.scores + static_cast<size_t>(x + static_cast<int64_t>(rt) * nc) * a.rows * CK + key;
+        const float* sc =
+            a.scores + static_cast<size_t>(x + static_cast<int64_t>(rt) * nc) * a.rows * CK + key;
         const float* lse = a.lse + static_cast<size_t>(bh) * a.R + rt * a.RT;
 #pragma unroll 4
         for (int r = 0; r < rows; ++r) {
