@@ -71,7 +71,7 @@ class _Torch:
             f8=torch.float8_e4m3fn, f32=torch.float32, i32=torch.int32, u8=torch.uint8,
             kinds={torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}, Tensor=torch.Tensor,
             empty=torch.empty, empty_like=torch.empty_like, stream=torch._C._cuda_getCurrentRawStream,
-            current_device=torch.cuda.current_device)
+            current_device=torch._C._cuda_getDevice)
         return self.__dict__[name]
 
 
@@ -126,30 +126,26 @@ class SwaCache:
     The tensors are the caller's; this object only holds and checks them.  page is 32, 64 or 128,
     D 64, 128 or 256."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "weight", "device", "shape")
+    __slots__ = ("held",)
+    k, v, k_scale, v_scale, weight, device, shape = (
+        property(lambda self, i=i: self.held[i]) for i in range(7))
 
     def __init__(self, k, v, k_scale, v_scale, weight=None):
-        if not isinstance(k, _t.Tensor) or k.dim() != 4:
+        t = _t
+        if not isinstance(k, t.Tensor) or k.dim() != 4:
             raise ValueError("k must be a 4-D tensor [pages, Hkv, page, D]")
         dev, shape = k.device, tuple(k.shape)
-        f8, f32, index = _t.f8, _t.f32, dev.index
+        f8, f32, index, blocks = t.f8, t.f32, dev.index, shape[:2]
         if not (index is not None and _good(k, shape, f8, index) and _good(v, shape, f8, index) and
-                _good(k_scale, shape[:2], f32, index) and _good(v_scale, shape[:2], f32, index) and
+                _good(k_scale, blocks, f32, index) and _good(v_scale, blocks, f32, index) and
                 (weight is None or _good(weight, shape[:3], f32, index))):
             _check(k, "k", shape, f8, None)
             _check(v, "v", shape, f8, dev)
-            _check(k_scale, "k_scale", shape[:2], f32, dev)
-            _check(v_scale, "v_scale", shape[:2], f32, dev)
+            _check(k_scale, "k_scale", blocks, f32, dev)
+            _check(v_scale, "v_scale", blocks, f32, dev)
             if weight is not None:
                 _check(weight, "weight", shape[:3], f32, dev)
-        put = _put
-        put(self, "k", k)
-        put(self, "v", v)
-        put(self, "k_scale", k_scale)
-        put(self, "v_scale", v_scale)
-        put(self, "weight", weight)
-        put(self, "device", dev)
-        put(self, "shape", shape)
+        _put(self, "held", (k, v, k_scale, v_scale, weight, dev, shape))
 
     def __setattr__(self, name, value):
         raise AttributeError("a SwaCache's tensors are fixed; make another for other tensors")
@@ -176,10 +172,9 @@ class SwaCache:
         return self.shape[2]
 
     def _c(self):
-        P, H, S, D = self.shape
-        w = self.weight
-        return _CCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                       self.v_scale.data_ptr(), None if w is None else w.data_ptr(), P, H, S, D)
+        k, v, ks, vs, w, _, shape = self.held
+        return _CCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                       None if w is None else w.data_ptr(), *shape)
 
 
 def _tables(cache, table, lens, new):
