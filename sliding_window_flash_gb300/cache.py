@@ -181,16 +181,17 @@ def _tables(cache, table, lens, new):
     """(B, max_pages, GPU index) after checking the int32 tables of a call."""
     if type(cache) is not SwaCache:
         raise TypeError("cache must be a SwaCache")
-    if not isinstance(table, _t.Tensor) or table.dim() != 2:
+    t, dev = _t, cache.held[5]
+    if not isinstance(table, t.Tensor) or table.dim() != 2:
         raise ValueError("table must be a 2-D tensor [B, max_pages]")
-    shape, index, i32 = tuple(table.shape), cache.device.index, _t.i32
+    shape, index, i32 = tuple(table.shape), dev.index, t.i32
     B = shape[:1]
     if not (_good(table, shape, i32, index) and _good(lens, B, i32, index) and
             (new is None or _good(new, B, i32, index))):
-        _check(table, "table", shape, i32, cache.device)
-        _check(lens, "lens", B, i32, cache.device)
+        _check(table, "table", shape, i32, dev)
+        _check(lens, "lens", B, i32, dev)
         if new is not None:
-            _check(new, "new", B, i32, cache.device)
+            _check(new, "new", B, i32, dev)
     return shape[0], shape[1], index
 
 
@@ -284,25 +285,25 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     swa_cache_attn_workspace_bytes) is allocated here unless given.
     """
     B, width, index = _tables(cache, table, lens, new)
+    dev, (_, Hkv, page, D) = cache.held[5:]
     if not isinstance(q, _t.Tensor) or q.dim() != 4:
         raise ValueError("q must be a 4-D tensor [B, Hq, T, D]")
     dt, kind, f32 = _dtype(q, "q"), q.dtype, _t.f32
-    _, Hkv, page, D = cache.shape
     _, Hq, T, _ = q.shape
     shape = (B, Hq, T, D)
     if not _good(q, shape, kind, index):
-        _check(q, "q", shape, kind, cache.device)
+        _check(q, "q", shape, kind, dev)
     if out is None:
         out = _t.empty_like(q)
     elif not _good(out, shape, kind, index):
-        _check(out, "out", shape, kind, cache.device)
+        _check(out, "out", shape, kind, dev)
     if lse is None:
-        lse = _t.empty(shape[:3], dtype=f32, device=cache.device)
+        lse = _t.empty(shape[:3], dtype=f32, device=dev)
     elif not _good(lse, shape[:3], f32, index):
-        _check(lse, "lse", shape[:3], f32, cache.device)
+        _check(lse, "lse", shape[:3], f32, dev)
     if workspace is None:
         need = _attn_space(B, Hq, Hkv, T, D, width, page, int(bool(accumulate)))
-        workspace = _t.empty(need, dtype=_t.u8, device=cache.device)
+        workspace = _t.empty(need, dtype=_t.u8, device=dev)
     _run("swa_cache_attn", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
          _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, _window(window),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(accumulate)), dt,
