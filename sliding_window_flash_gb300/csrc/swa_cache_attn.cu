@@ -26,8 +26,8 @@
 // 6.8 TB/s.  64 ragged sequences to 16K with accumulation: 203 us, the walk about 175 of it (5.8 TB/s;
 // the last teams end some 15 us after most), the join 8, the weights 20.  A window of 1024: 11 us for
 // one sequence with 16 heads, the latency of two kernels; 18.6 us for 16 sequences with 8 heads.  12
-// sequences, 5 tokens, D = 256, window 1024: 31 us; a part is only ten chunks, so partial results are
-// half the traffic there.
+// sequences, 5 tokens, D = 256, window 1024: 31 us; a part is only ten chunks there, and its partial
+// results, written and read, add 40 % to the cache's bytes.
 #include <climits>
 #include <type_traits>
 
