@@ -959,10 +959,11 @@ __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView 
           const float4 s = *reinterpret_cast<const float4*>(sc + r * CK);
           // a row that sees nothing has scores and lse -inf, and adds nothing
           const float z = lse[r] == SWA_NEG_INF ? 0.f : lse[r] * kLog2e;
-          add.x += ex2(s.x - z);
-          add.y += ex2(s.y - z);
-          add.z += ex2(s.z - z);
-          add.w += ex2(s.w - z);
+          // nor does a row to a slot that it does not see, when its lse is NaN (-inf - NaN is NaN)
+          add.x += s.x == SWA_NEG_INF ? 0.f : ex2(s.x - z);
+          add.y += s.y == SWA_NEG_INF ? 0.f : ex2(s.y - z);
+          add.z += s.z == SWA_NEG_INF ? 0.f : ex2(s.z - z);
+          add.w += s.w == SWA_NEG_INF ? 0.f : ex2(s.w - z);
         }
       }
       // Slots that nobody saw have scores -inf and keep their weight.
