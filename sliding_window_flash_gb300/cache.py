@@ -204,10 +204,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _space(workspace):
-    """(address, bytes) of a workspace tensor."""
-    if workspace is None:
-        return None, 0
+def _space(workspace, device):
+    """(address, bytes) of a caller's workspace: all of its bytes are there, on `device`."""
+    if not isinstance(workspace, _t.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -304,10 +308,13 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     if workspace is None:
         need = _attn_space(B, Hq, Hkv, T, D, width, page, int(bool(accumulate)))
         workspace = _t.empty(need, dtype=_t.u8, device=dev)
+        space = workspace.data_ptr(), need
+    else:
+        space = _space(workspace, dev)
     _run("swa_cache_attn", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
          _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, _window(window),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(accumulate)), dt,
-         *_space(workspace))
+         *space)
     return out, lse
 
 
@@ -371,11 +378,15 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
     elif not _good(out, (B, Hkv, Lk), f32, index):
         _check(out, "out", (B, Hkv, Lk), f32, dev)
     window, causal = _window(window), int(bool(causal))
-    if workspace is None:
+    space = None, 0
+    if workspace is not None:
+        space = _space(workspace, dev)
+    else:
         need = _weights_space(B, Hq, Hkv, Lq, Lk, D, window, causal)
         if need:
             workspace = _t.empty(need, dtype=_t.u8, device=dev)
+            space = workspace.data_ptr(), need
     _run("swa_attn_key_weights", index, q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(), B,
          Hq, Hkv, Lq, Lk, D, window, causal, 1.0 / math.sqrt(D) if scale is None else float(scale),
-         dt, *_space(workspace))
+         dt, *space)
     return out

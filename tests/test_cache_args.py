@@ -1,0 +1,81 @@
+"""What the cache calls refuse before anything is launched, shown on the CPU (the launch is replaced by
+a recorder), and the same refusals on the GPU."""
+import pytest
+import torch
+
+import sliding_window_flash_gb300 as swa
+from sliding_window_flash_gb300 import cache as mod
+
+CPU = torch.device("cpu")
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Calls take CPU tensors for GPU ones and are recorded instead of launched."""
+    seen = []
+    monkeypatch.setattr(mod, "_check", lambda *a, **k: None)
+    monkeypatch.setattr(mod, "_good", lambda *a, **k: True)
+    monkeypatch.setattr(mod, "_run", lambda name, index, *args: seen.append((name, args)))
+    monkeypatch.setattr(mod, "_attn_space", lambda *a: 4096)
+    monkeypatch.setattr(mod, "_weights_space", lambda *a: 4096)
+    return seen
+
+
+def _cpu_cache(pages=4, H=2, page=32, D=64):
+    k = torch.zeros((pages, H, page, D), dtype=torch.uint8).view(torch.float8_e4m3fn)
+    s, w = torch.ones((pages, H)), torch.zeros((pages, H, page))
+    c = object.__new__(swa.SwaCache)
+    mod._put(c, "held", (k, k, s, s, w, CPU, tuple(k.shape)))
+    return c
+
+
+def _attn(**kw):
+    q = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16)
+    table, lens = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    return swa.swa_cache_attn(q, _cpu_cache(), table, lens, kw.pop("window", 9), **kw)
+
+
+def _weights(**kw):
+    q = torch.zeros((1, 4, 8, 64), dtype=torch.bfloat16)
+    return swa.swa_attn_key_weights(q, q[:, :2], torch.zeros((1, 4, 8)), kw.pop("window", 9), **kw)
+
+
+# ---- workspaces --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("call", [_attn, _weights], ids=["attn", "weights"])
+def test_workspace_is_a_whole_tensor_on_the_gpu(calls, call):
+    """An expanded tensor holds less than its shape says; another device's memory is not the kernels'."""
+    u8 = torch.uint8
+    for bad in (torch.empty(1, dtype=u8).expand(1 << 20), torch.empty((64, 64), dtype=u8).t(),
+                torch.empty(8192, dtype=u8)[::2], torch.empty(8192, dtype=u8, device="meta"),
+                bytearray(8192), 8192):
+        with pytest.raises((TypeError, ValueError), match="workspace"):
+            call(workspace=bad)
+    assert calls == []
+    good = torch.empty((4, 4096), dtype=torch.int16)
+    call(workspace=good)
+    call()
+    (_, given), (_, own) = calls
+    assert (good.data_ptr(), 32768) == tuple(a for a in given if a in (good.data_ptr(), 32768))
+    assert 4096 in own
+
+
+@pytest.mark.gpu
+def test_workspace_refusals_on_the_gpu(swa):
+    cache = swa.SwaCache.empty(4, 2, 64, page=32)
+    q = torch.zeros((1, 4, 1, 64), dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((1, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lse = torch.zeros((1, 4, 8), device="cuda")
+    n = 1 << 26
+    wrong = (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(n))
+    for bad in wrong:
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_cache_attn(q, cache, table, lens, 9, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_attn_key_weights(q.expand(1, 4, 8, 64).contiguous(), k, lse, 9, workspace=bad)
+    fine = torch.empty((2, n // 2), dtype=torch.uint8, device="cuda")
+    swa.swa_cache_attn(q, cache, table, lens, 9, workspace=fine)
+    swa.swa_attn_key_weights(q.expand(1, 4, 8, 64).contiguous(), k, lse, 9, workspace=fine)
+    swa.swa_check_device()
