@@ -205,7 +205,7 @@ def _f32_workspace(workspace, B, Hq, Hkv, Lq, Lk, D, device):
     n = swa_attn_f32_workspace_bytes(B, Hq, Hkv, Lq, Lk, D)
     if workspace is None:
         workspace = torch.empty(n, dtype=torch.uint8, device=device)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return _cache._space(workspace, device)
 
 
 def swa_attn_fwd(q, k, v, window: int, scale: Optional[float] = None, out=None, lse=None,
@@ -301,7 +301,7 @@ def swa_attn_bwd(q, k, v, o, do, lse, window: int, scale: Optional[float] = None
         ws_bytes = int(lib.swa_attn_bwd_workspace_bytes(B, Hq, Lq, D))
     if workspace is None:
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws = _cache._space(workspace, q.device)
     if fused:
         name = "swa_attn_bwd_fused"
         rc = lib.swa_attn_bwd_fused(*ptrs, B, Hq, Hkv, Lq, Lk, D, int(window), int(bool(causal)),
@@ -386,7 +386,7 @@ def _fused_phases(q, k, v, o, do, lse, window, scale, dq, dk, dv, workspace, bet
     n = int(lib.swa_attn_bwd_fused_workspace_bytes(B, Hq, N, D))
     if workspace is None:
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws = _cache._space(workspace, q.device)
     st = _stream_handle(q.device)
     mark = between or (lambda i: None)
     mark(0)
@@ -433,7 +433,9 @@ def swa_attn_fwd_bwd_host(q, k, v, do, window: int, scale: Optional[float] = Non
     import torch
 
     lib = load()
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    dev = torch.device("cuda" if device is None else device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
     B, Hq, Hkv, N, Lk, D = _dims(q, k)
     dt = q.dtype
     if dt != torch.bfloat16:
@@ -451,11 +453,10 @@ def swa_attn_fwd_bwd_host(q, k, v, do, window: int, scale: Optional[float] = Non
     n = swa_attn_host_workspace_bytes(B, Hq, Hkv, N, D, U)
     if workspace is None:
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    ws = _cache._space(workspace, dev)
     ptrs = [t.data_ptr() for t in (q, k, v, do)] + [t.data_ptr() for t in outs]
     rc = lib.swa_attn_fwd_bwd_host(*ptrs, B, Hq, Hkv, N, D, int(window), _scale(scale, D), U,
-                                   workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(),
-                                   _stream_handle(dev))
+                                   *ws, _stream_handle(dev))
     if rc != 0:
         raise SwaError(rc, "swa_attn_fwd_bwd_host")
     return tuple(outs)
