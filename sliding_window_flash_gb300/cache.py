@@ -195,9 +195,10 @@ def _tables(cache, table, lens, new):
     return shape[0], shape[1], index
 
 
-def _window(window):
-    """A window as the C int it becomes: one past every slot means the same however large."""
-    return min(int(window), 2**31 - 1)
+def _int32(x):
+    """The C int nearest to x: what an int does not hold must not wrap to another number.  A window past
+    every slot means the same however large; what else is out of range is refused."""
+    return max(-2**31, min(int(x), 2**31 - 1))
 
 
 def _ptr(t):
@@ -312,7 +313,7 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     else:
         space = _space(workspace, dev)
     _run("swa_cache_attn", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
-         _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, _window(window),
+         _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, _int32(window),
          1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(accumulate)), dt,
          *space)
     return out, lse
@@ -329,8 +330,8 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
     if not isinstance(dst_table, _t.Tensor) or dst_table.dim() != 2:
         raise ValueError("dst_table must be a 2-D tensor [B, dst_pages]")
     budget, i32 = int(budget), _t.i32
-    if budget < 1:
-        raise ValueError("budget must be at least 1")
+    if not 1 <= budget < 2**30:  # slots of a table
+        raise ValueError("budget must be at least 1 and below 2^30")
     room = (B, dst_table.shape[1])
     if not _good(dst_table, room, i32, index):
         _check(dst_table, "dst_table", room, i32, cache.device)
@@ -344,13 +345,13 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
     elif not _good(lens_out, (B,), i32, index):
         _check(lens_out, "lens_out", (B,), i32, cache.device)
     _run("swa_cache_evict", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
-         dst_table.data_ptr(), room[1], budget, int(recent), kept.data_ptr(), lens_out.data_ptr(), B)
+         dst_table.data_ptr(), room[1], budget, _int32(recent), kept.data_ptr(), lens_out.data_ptr(), B)
     return kept, lens_out
 
 
 def swa_attn_key_weights_workspace_bytes(B: int, Hq: int, Hkv: int, Lq: int, Lk: int, D: int,
                                          window: int, causal: bool = True) -> int:
-    return _weights_space(B, Hq, Hkv, Lq, Lk, D, _window(window), int(bool(causal)))
+    return _weights_space(B, Hq, Hkv, Lq, Lk, D, _int32(window), int(bool(causal)))
 
 
 def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, causal: bool = True,
@@ -377,7 +378,7 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
         out = _t.empty((B, Hkv, Lk), dtype=f32, device=dev)
     elif not _good(out, (B, Hkv, Lk), f32, index):
         _check(out, "out", (B, Hkv, Lk), f32, dev)
-    window, causal = _window(window), int(bool(causal))
+    window, causal = _int32(window), int(bool(causal))
     space = None, 0
     if workspace is not None:
         space = _space(workspace, dev)

@@ -1,5 +1,7 @@
 """What the cache calls refuse before anything is launched, shown on the CPU (the launch is replaced by
 a recorder), and the same refusals on the GPU."""
+import ctypes
+
 import pytest
 import torch
 
@@ -79,3 +81,48 @@ def test_workspace_refusals_on_the_gpu(swa):
     swa.swa_cache_attn(q, cache, table, lens, 9, workspace=fine)
     swa.swa_attn_key_weights(q.expand(1, 4, 8, 64).contiguous(), k, lse, 9, workspace=fine)
     swa.swa_check_device()
+
+
+# ---- numbers that a C int does not hold --------------------------------------------------------
+
+def _passed(calls, value_at):
+    """What the last call's C function sees of argument `value_at`."""
+    return ctypes.c_int(calls[-1][1][value_at]).value
+
+
+@pytest.mark.parametrize("window", [2**32 + 5, 2**31, 2**40, 10**30])
+def test_windows_past_an_int_see_everything(calls, window):
+    _attn(window=window)
+    assert _passed(calls, 11) == 2**31 - 1
+    _weights(window=window)
+    assert _passed(calls, 10) == 2**31 - 1
+
+
+@pytest.mark.parametrize("window", [-2**32 + 5, -2**31 - 1, -10**30, 0, -1])
+def test_windows_below_one_stay_below_one(calls, window):
+    _attn(window=window)
+    assert _passed(calls, 11) < 1
+    _weights(window=window)
+    assert _passed(calls, 10) < 1
+
+
+def _evict(budget, recent):
+    table, lens = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    return swa.swa_cache_evict(_cpu_cache(), table, lens, torch.zeros((1, 2), dtype=torch.int32), budget,
+                               recent)
+
+
+def test_evict_numbers_past_an_int(calls):
+    for recent in (2**32, 2**32 + 3, 2**31, 10**30):
+        _evict(20, recent)
+        assert _passed(calls, 6) == 20 and _passed(calls, 7) > 20
+    for recent in (-2**32, -2**32 + 3, -2**31 - 1, -1):
+        _evict(20, recent)
+        assert _passed(calls, 7) < 0
+    _evict(20, 3)
+    assert _passed(calls, 7) == 3
+    done = len(calls)
+    for budget in (2**32 + 20, 2**31, 2**30, -2**32 + 20, 0):
+        with pytest.raises(ValueError, match="budget"):
+            _evict(budget, 3)
+    assert len(calls) == done
