@@ -95,6 +95,7 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  *   workspace  : at least swa_cache_attn_workspace_bytes bytes, 16-byte aligned; nothing is kept
  *                there between calls.  Calls that may overlap (other streams, graphs replayed at
  *                once) need workspaces of their own.
+ *                The size holds for the GPU that is current when it is asked for.
  * A key that a query does not see changes nothing for it, NaN included; where some queries of a call
  * see a token and others do not, this takes values that are finite, as append stores them.
  * Scores, softmax statistics and sums are fp32.  q is taken as fp16 operands after scaling each row
@@ -137,7 +138,8 @@ swa_status swa_cache_evict(const swa_cache* cache, const int* table, int max_pag
  *   w fp32 [B, Hkv, Lk], fully written; shapes, window and causal as in swa_attn_fwd_ex.
  *   workspace : at least swa_attn_key_weights_workspace_bytes bytes (0 for many keys: it may then be
  *               NULL), 16-byte aligned; nothing is kept there between calls.  Calls that may overlap
- *               need workspaces of their own.
+ *               need workspaces of their own.  The size holds for the GPU that is current when it is
+ *               asked for.
  * B Hkv ceil(Lk / 256) must stay below 2^30.  The N x N weights are never stored; scores, exponentials
  * and sums are fp32.  Bit-reproducible on one GPU.
  */

@@ -216,16 +216,19 @@ def _space(workspace, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _on(index, name, *args):
+    """Calls entry point `name` with GPU `index` current."""
+    if index == _t.current_device():
+        return _entry(name)(*args)
+    import torch
+
+    with torch.cuda.device(index):
+        return _entry(name)(*args)
+
+
 def _run(name, index, *args):
     """Calls entry point `name` on the current stream of GPU `index`, with that GPU current."""
-    stream = _t.stream(index)
-    if index == _t.current_device():
-        rc = _entry(name)(*args, stream)
-    else:
-        import torch
-
-        with torch.cuda.device(index):
-            rc = _entry(name)(*args, stream)
+    rc = _on(index, name, *args, _t.stream(index))
     if rc != 0:
         from . import SwaError
 
@@ -263,19 +266,22 @@ def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) 
          _ptr(new), k.data_ptr(), v.data_ptr(), _ptr(weight), B, T, dt)
 
 
+# A workspace's size follows the number of the GPU's SMs, so it is asked for, and kept, for that GPU.
 @functools.lru_cache(maxsize=256)
-def _attn_space(*sizes):
-    return int(_entry("swa_cache_attn_workspace_bytes")(*sizes))
+def _attn_space(index, *sizes):
+    return int(_on(index, "swa_cache_attn_workspace_bytes", *sizes))
 
 
 @functools.lru_cache(maxsize=256)
-def _weights_space(*sizes):
-    return int(_entry("swa_attn_key_weights_workspace_bytes")(*sizes))
+def _weights_space(index, *sizes):
+    return int(_on(index, "swa_attn_key_weights_workspace_bytes", *sizes))
 
 
 def swa_cache_attn_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, max_pages: int,
                                    page: int, accumulate: bool = False) -> int:
-    return _attn_space(B, Hq, Hkv, T, D, max_pages, page, int(bool(accumulate)))
+    """Bytes of swa_cache_attn's workspace on the current GPU."""
+    return int(_entry("swa_cache_attn_workspace_bytes")(B, Hq, Hkv, T, D, max_pages, page,
+                                                        int(bool(accumulate))))
 
 
 def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional[float] = None,
@@ -307,7 +313,7 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     elif not _good(lse, shape[:3], f32, index):
         _check(lse, "lse", shape[:3], f32, dev)
     if workspace is None:
-        need = _attn_space(B, Hq, Hkv, T, D, width, page, int(bool(accumulate)))
+        need = _attn_space(index, B, Hq, Hkv, T, D, width, page, int(bool(accumulate)))
         workspace = _t.empty(need, dtype=_t.u8, device=dev)
         space = workspace.data_ptr(), need
     else:
@@ -351,7 +357,9 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
 
 def swa_attn_key_weights_workspace_bytes(B: int, Hq: int, Hkv: int, Lq: int, Lk: int, D: int,
                                          window: int, causal: bool = True) -> int:
-    return _weights_space(B, Hq, Hkv, Lq, Lk, D, _int32(window), int(bool(causal)))
+    """Bytes of swa_attn_key_weights' workspace on the current GPU."""
+    return int(_entry("swa_attn_key_weights_workspace_bytes")(B, Hq, Hkv, Lq, Lk, D, _int32(window),
+                                                              int(bool(causal))))
 
 
 def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, causal: bool = True,
@@ -383,7 +391,7 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
     if workspace is not None:
         space = _space(workspace, dev)
     else:
-        need = _weights_space(B, Hq, Hkv, Lq, Lk, D, window, causal)
+        need = _weights_space(index, B, Hq, Hkv, Lq, Lk, D, window, causal)
         if need:
             workspace = _t.empty(need, dtype=_t.u8, device=dev)
             space = workspace.data_ptr(), need

@@ -126,3 +126,52 @@ def test_evict_numbers_past_an_int(calls):
         with pytest.raises(ValueError, match="budget"):
             _evict(budget, 3)
     assert len(calls) == done
+
+
+# ---- a workspace's size belongs to a GPU -------------------------------------------------------
+
+def test_workspace_sizes_are_the_tensors_gpus(calls, monkeypatch):
+    """GPUs may differ in SMs: a size is asked for with the tensors' GPU current, and not handed on."""
+    monkeypatch.undo()
+    assert mod._t.f32 is torch.float32  # the names are loaded
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.index
+
+        def __exit__(self, *_):
+            now[0] = self.was
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(mod._t, "current_device", lambda: now[0])
+    monkeypatch.setattr(mod, "_check", lambda *a, **k: None)
+    monkeypatch.setattr(mod, "_good", lambda *a, **k: True)
+    monkeypatch.setattr(mod, "_run", lambda name, index, *args: seen.append(args))
+    for name in ("swa_cache_attn_workspace_bytes", "swa_attn_key_weights_workspace_bytes"):
+        monkeypatch.setitem(mod._entries, name, lambda *sizes: 1000 + now[0] + sizes[0])
+    sizes = getattr(mod._attn_space, "cache_clear", None), getattr(mod._weights_space, "cache_clear", None)
+    try:
+        for index in (0, 3, 0, 5):
+            monkeypatch.setattr(mod, "_tables", lambda *a: (1, 4, index))
+            _attn()
+            assert seen[-1][-1] == 1001 + index and now[0] == 0
+        now[0] = 5
+        _attn()
+        assert seen[-1][-1] == 1006
+        monkeypatch.setattr(mod, "_tables", lambda *a: (1, 4, 0))
+        _attn()
+        assert seen[-1][-1] == 1001 and now[0] == 5
+        assert mod._weights_space(3, 1, 4) == 1004 and mod._weights_space(5, 1, 4) == 1006
+        assert now[0] == 5
+        # the public forms answer for the current GPU
+        assert swa.swa_cache_attn_workspace_bytes(1, 4, 2, 1, 64, 4, 32) == 1006
+        now[0] = 2
+        assert swa.swa_cache_attn_workspace_bytes(1, 4, 2, 1, 64, 4, 32) == 1003
+        assert swa.swa_attn_key_weights_workspace_bytes(1, 4, 2, 8, 8, 64, 4) == 1003
+    finally:
+        for clear in filter(None, sizes):
+            clear()
