@@ -95,7 +95,8 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  *   workspace  : at least swa_cache_attn_workspace_bytes bytes, 16-byte aligned; nothing is kept
  *                there between calls.  Calls that may overlap (other streams, graphs replayed at
  *                once) need workspaces of their own.
- *                The size holds for the GPU that is current when it is asked for.
+ *                The size holds for the GPU that is current when it is asked for; 0 for sizes that
+ *                the call refuses.
  * A key that a query does not see changes nothing for it, NaN included; where some queries of a call
  * see a token and others do not, this takes values that are finite, as append stores them.
  * Scores, softmax statistics and sums are fp32.  q is taken as fp16 operands after scaling each row

@@ -12,6 +12,16 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 constexpr long long kIndexLimit = 1ll << 31;
 constexpr long long kSlotLimit = 1ll << 30;  // of a sequence's table
 
+// Slots in 30 bits (the kernels add to them), blocks (page, head) and table entries in 31; element
+// offsets are 64-bit.
+bool sizes_fit(int B, int Hkv, int max_pages, int page) {
+  return static_cast<long long>(max_pages) * page < kSlotLimit &&
+         static_cast<long long>(B) * Hkv < kIndexLimit && B <= 65535 && Hkv <= 65535;
+}
+
+// Query rows of an attention call in 31 bits (B <= 65535, T <= 64: no overflow here).
+bool rows_fit(int B, int Hq, int T) { return static_cast<long long>(B) * Hq * T < kIndexLimit; }
+
 // The checks every cache call makes of the cache, its table and lengths.
 swa_status check_cache(const swa_cache* c, const int* table, int max_pages, const int* lens, int B) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !table || !lens)
@@ -19,11 +29,8 @@ swa_status check_cache(const swa_cache* c, const int* table, int max_pages, cons
   if (c->pages < 1 || c->Hkv < 1 || max_pages < 1 || B < 1) return SWA_ERR_INVALID_ARG;
   if (c->page != 32 && c->page != 64 && c->page != 128) return SWA_ERR_UNSUPPORTED;
   if (c->D != 64 && c->D != 128 && c->D != 256) return SWA_ERR_UNSUPPORTED;
-  // Slots in 30 bits (the kernels add to them), blocks (page, head) and table entries in 31; element
-  // offsets are 64-bit.
-  if (static_cast<long long>(max_pages) * c->page >= kSlotLimit ||
-      static_cast<long long>(c->pages) * c->Hkv >= kIndexLimit ||
-      static_cast<long long>(B) * c->Hkv >= kIndexLimit || B > 65535 || c->Hkv > 65535)
+  if (static_cast<long long>(c->pages) * c->Hkv >= kIndexLimit ||
+      !sizes_fit(B, c->Hkv, max_pages, c->page))
     return SWA_ERR_INVALID_ARG;
   // What is read an element at a time needs an element's alignment only, here and in the calls below.
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
@@ -113,7 +120,7 @@ size_t swa_cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int 
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > swa::kMaxCacheQueries ||
       max_pages < 1 || (D != 64 && D != 128 && D != 256) ||
       (page != 32 && page != 64 && page != 128) ||
-      static_cast<long long>(max_pages) * page >= kSlotLimit)
+      !sizes_fit(B, Hkv, max_pages, page) || !rows_fit(B, Hq, T))
     return 0;
   return swa::cache_attn_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page, accumulate);
 }
@@ -130,7 +137,7 @@ swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_page
       (dtype != SWA_BF16 && dtype != SWA_FP16))
     return SWA_ERR_INVALID_ARG;
   if (accumulate && !cache->weight) return SWA_ERR_INVALID_ARG;
-  if (static_cast<long long>(B) * Hq * T >= kIndexLimit) return SWA_ERR_INVALID_ARG;
+  if (!rows_fit(B, Hq, T)) return SWA_ERR_INVALID_ARG;
   const size_t need = swa_cache_attn_workspace_bytes(B, Hq, cache->Hkv, T, cache->D, max_pages,
                                                      cache->page, accumulate);
   if (need != 0 && (!workspace || workspace_bytes < need)) return SWA_ERR_WORKSPACE;

@@ -175,3 +175,28 @@ def test_workspace_sizes_are_the_tensors_gpus(calls, monkeypatch):
     finally:
         for clear in filter(None, sizes):
             clear()
+
+
+# ---- sizes that the call refuses ---------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+
+    from sliding_window_flash_gb300 import build
+
+    if not os.path.exists(swa.library_path()):
+        build.build()
+    return swa.load()
+
+
+@pytest.mark.parametrize("sizes", [
+    (1, 2**31 - 1, 1, 64, 64, 4, 64), (1, 2**31 - 1, 1, 2, 64, 4, 64), (65536, 4, 2, 1, 64, 4, 64),
+    (2**31 - 1, 2**31 - 1, 2**31 - 1, 1, 64, 4, 64), (1, 70000, 70000, 1, 64, 4, 64),
+    (40000, 60000, 60000, 1, 64, 4, 64), (65535, 64, 1, 512, 64, 4, 64), (1000, 40000, 4, 64, 64, 4, 64),
+])
+def test_size_of_refused_calls_is_zero(lib, sizes):
+    for acc in (0, 1):
+        assert lib.swa_cache_attn_workspace_bytes(*sizes, acc) == 0
+    largest = lib.swa_cache_attn_workspace_bytes(1024, 65535, 1, 31, 64, 2**24 - 1, 32, 1)
+    assert 0 < largest < 2**63  # counted without wrapping
