@@ -92,9 +92,12 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  *                Hq / Hkv query heads of its kv head (needs cache->weight; the tables must then name
  *                each page once: two sequences that share one would add to the same weights at the
  *                same time); 0 -> weights untouched, and pages may be shared.
- *   workspace  : at least swa_cache_attn_workspace_bytes bytes, 16-byte aligned; nothing is kept
- *                there between calls.  Calls that may overlap (other streams, graphs replayed at
- *                once) need workspaces of their own.
+ *   workspace  : at least swa_cache_attn_window_workspace_bytes bytes for this window, 16-byte
+ *                aligned (swa_cache_attn_workspace_bytes is enough for any); nothing is kept there
+ *                between calls.  Calls that may overlap (other streams, graphs replayed at once)
+ *                need workspaces of their own.  Accumulating takes 4 bytes for each row (T Hq) and
+ *                slot that a sequence can see, min(max_pages page, window + T + 62), of up to 1024
+ *                sequences, in units of 2 MB; up to twice that where a kv head has more than 64 rows.
  *                The size holds for the GPU that is current when it is asked for; 0 for sizes that
  *                the call refuses.
  * A key that a query does not see changes nothing for it, NaN included; where some queries of a call
@@ -107,6 +110,8 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  */
 size_t swa_cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
                                       int page, int accumulate);
+size_t swa_cache_attn_window_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
+                                             int page, int window, int accumulate);
 swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_pages,
                           const int* lens, const int* new_lens, const void* q, void* o, float* lse,
                           int B, int Hq, int T, int window, float scale, int accumulate, int dtype,

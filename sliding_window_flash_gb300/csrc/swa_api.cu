@@ -396,7 +396,7 @@ swa_status swa_selftest_wait_timeout(cudaStream_t stream) {
   return swa::launch_wait_timeout_selftest(err, stream) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
-int swa_version(void) { return 101; }
+int swa_version(void) { return 102; }
 
 }  // extern "C"
 

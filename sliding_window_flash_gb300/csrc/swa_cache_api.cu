@@ -1,5 +1,6 @@
 // swa_cache_api.cu — the C ABI of include/swa_cache.h: argument checks and launches of the cache
 // calls and of the key weights.
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -21,6 +22,12 @@ bool sizes_fit(int B, int Hkv, int max_pages, int page) {
 
 // Query rows of an attention call in 31 bits (B <= 65535, T <= 64: no overflow here).
 bool rows_fit(int B, int Hq, int T) { return static_cast<long long>(B) * Hq * T < kIndexLimit; }
+
+// A window reaching past every slot changes nothing; clamping keeps the offsets in range.
+int slots_seen(int window, int max_pages, int page) {
+  const int slots = max_pages * page;
+  return window < slots ? window : slots;
+}
 
 // The checks every cache call makes of the cache, its table and lengths.
 swa_status check_cache(const swa_cache* c, const int* table, int max_pages, const int* lens, int B) {
@@ -115,14 +122,20 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
                                                                                  : SWA_ERR_CUDA;
 }
 
-size_t swa_cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
-                                      int page, int accumulate) {
+size_t swa_cache_attn_window_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
+                                             int page, int window, int accumulate) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > swa::kMaxCacheQueries ||
-      max_pages < 1 || (D != 64 && D != 128 && D != 256) ||
+      max_pages < 1 || window < 1 || (D != 64 && D != 128 && D != 256) ||
       (page != 32 && page != 64 && page != 128) ||
       !sizes_fit(B, Hkv, max_pages, page) || !rows_fit(B, Hq, T))
     return 0;
-  return swa::cache_attn_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page, accumulate);
+  return swa::cache_attn_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page,
+                                         slots_seen(window, max_pages, page), accumulate);
+}
+
+size_t swa_cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
+                                      int page, int accumulate) {
+  return swa_cache_attn_window_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page, INT_MAX, accumulate);
 }
 
 swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_pages,
@@ -138,8 +151,8 @@ swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_page
     return SWA_ERR_INVALID_ARG;
   if (accumulate && !cache->weight) return SWA_ERR_INVALID_ARG;
   if (!rows_fit(B, Hq, T)) return SWA_ERR_INVALID_ARG;
-  const size_t need = swa_cache_attn_workspace_bytes(B, Hq, cache->Hkv, T, cache->D, max_pages,
-                                                     cache->page, accumulate);
+  const size_t need = swa_cache_attn_window_workspace_bytes(B, Hq, cache->Hkv, T, cache->D, max_pages,
+                                                            cache->page, window, accumulate);
   if (need != 0 && (!workspace || workspace_bytes < need)) return SWA_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(new_lens, 4))
@@ -152,9 +165,7 @@ swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_page
   a.o = o;
   a.lse = lse;
   a.Hq = Hq;
-  // A window reaching past every slot changes nothing; clamping keeps the offsets in range.
-  const int slots = max_pages * cache->page;
-  a.window = window < slots ? window : slots;
+  a.window = slots_seen(window, max_pages, cache->page);
   a.scale = scale;
   a.accumulate = accumulate;
   a.dtype = dtype;

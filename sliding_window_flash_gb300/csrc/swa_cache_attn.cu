@@ -977,7 +977,12 @@ struct Plan {
   size_t off_ml, off_po, off_scores, bytes;
 };
 
-// The workspace's layout is the same for every window.
+// Scores take whole units of this size, so that small tables have one size for every window (torch's
+// allocator cuts large blocks into such units in any case).
+constexpr size_t kScoreUnit = 2 << 20;
+
+// The workspace's layout is the same for every window; the scores, at its end, are fewer under a smaller
+// one.
 Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int accumulate, int window) {
   Plan p;
   p.R = Hq / Hkv * T;
@@ -987,6 +992,8 @@ Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int 
   p.RT = 16 * p.MT;
   p.NRT = (p.R + p.RT - 1) / p.RT;
   p.rows = p.R < p.RT ? p.R : p.RT;
+  const int64_t slots = static_cast<int64_t>(max_pages) * page;
+  const int64_t chunks = most_chunks(T, window, slots, p.ck);  // of an item
   p.tiles = 1;
   size_t parts = static_cast<size_t>(sm_count()) * (kWarps / p.MT);
   if (p.R > 16 && D < 256) {
@@ -995,9 +1002,6 @@ Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int 
     // the table and the window allow (32 / 8 heads, T = 8, D = 128, 64 sequences of 4,000: 146 us and 174
     // with one; under a window of 1024, 16 sequences: 34 and 26).
     parts *= 2;
-    const int64_t slots = static_cast<int64_t>(max_pages) * page;
-    const int64_t span = window + T - 1 < slots ? window + T - 1 : slots;
-    const int64_t chunks = (span + p.ck - 2) / p.ck + 1;  // of an item, at most
     if (static_cast<int64_t>(B) * Hkv * p.NRT * chunks >= 32 * static_cast<int64_t>(parts)) {
       p.tiles = 2;
       p.MT /= 2;
@@ -1012,9 +1016,13 @@ Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int 
   off += round(2 * parts * p.rows * D * sizeof(float));
   p.off_scores = off;
   if (accumulate) {
-    const size_t chunks = static_cast<size_t>(max_pages) * page / p.ck;
-    off += static_cast<size_t>(B < kMaxSeqs ? B : kMaxSeqs) * Hkv * p.NRT * chunks * p.rows * p.ck *
-           sizeof(float);
+    // The scores of all chunks that can be seen, in whole units, and no more than the table has (64
+    // sequences, 32 / 8 heads, 131,072 slots, a window of 1024: 10 MB, 1.07 GB for the table).
+    const size_t chunk = static_cast<size_t>(B < kMaxSeqs ? B : kMaxSeqs) * Hkv * p.NRT * p.rows * p.ck *
+                         sizeof(float);
+    const size_t table = chunk * (slots / p.ck);
+    const size_t seen = (chunk * chunks + kScoreUnit - 1) / kScoreUnit * kScoreUnit;
+    off += seen < table ? seen : table;
   }
   p.bytes = round(off);
   return p;
@@ -1111,8 +1119,8 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
-                                  int accumulate) {
-  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate, 1).bytes;
+                                  int window, int accumulate) {
+  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate, window).bytes;
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream) {

@@ -120,7 +120,7 @@ struct CacheAttnArgs {
   void* workspace;
 };
 size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
-                                  int accumulate);
+                                  int window, int accumulate);
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream);
 
 struct CacheEvictArgs {

@@ -30,6 +30,13 @@ SWA_HD int chunk_count(int len, int n, int window, int ck) {
   return n > 0 ? (len + n - 1) / ck - first_chunk(len, window, ck) + 1 : 0;
 }
 
+// Most chunks that T queries can see under `window` in a table of `slots`: of window + T - 1 consecutive
+// slots, wherever they begin.
+SWA_HD int64_t most_chunks(int T, int window, int64_t slots, int ck) {
+  const int64_t span = static_cast<int64_t>(window) + T - 1;
+  return ((span < slots ? span : slots) + ck - 2) / ck + 1;
+}
+
 // x / d for 0 <= x, 1 <= d, in 32 bits where they fit (a 64-bit division costs ten times as much).
 SWA_HD int64_t quotient(int64_t x, int64_t d) {
   if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);

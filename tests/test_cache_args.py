@@ -151,7 +151,7 @@ def test_workspace_sizes_are_the_tensors_gpus(calls, monkeypatch):
     monkeypatch.setattr(mod, "_check", lambda *a, **k: None)
     monkeypatch.setattr(mod, "_good", lambda *a, **k: True)
     monkeypatch.setattr(mod, "_run", lambda name, index, *args: seen.append(args))
-    for name in ("swa_cache_attn_workspace_bytes", "swa_attn_key_weights_workspace_bytes"):
+    for name in filter(lambda n: n.endswith("workspace_bytes"), mod.SIGNATURES):
         monkeypatch.setitem(mod._entries, name, lambda *sizes: 1000 + now[0] + sizes[0])
     sizes = getattr(mod._attn_space, "cache_clear", None), getattr(mod._weights_space, "cache_clear", None)
     try:
