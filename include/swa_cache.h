@@ -128,6 +128,11 @@ swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_page
  *   budget    : >= 1;  0 <= recent <= budget.
  *   kept      : int32 [B, Hkv, budget], the surviving slots in order, -1 behind the last.
  *   lens_out  : int32 [B], min(lens[b], budget); may be lens.
+ * A sequence that is skipped (its length negative or longer than its table) keeps nothing: kept -1,
+ * lens_out 0, no page written.  Whoever goes on with lens_out has dropped it, so swa_check_device, or
+ * the lengths, come first where they can be wrong.  Tokens on a skipped page of `table` count as the
+ * lightest; those that stay all the same are in kept, and their destination slots are left as they were,
+ * like every slot of a skipped page of dst_table.
  * A destination block's scale is the largest of its tokens' old scales; slots behind the last
  * survivor are left as they were.  Window rules count cached tokens, so under a window evicted
  * tokens no longer count.  Needs cache->weight.

@@ -335,7 +335,7 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
     of the others those with the largest accumulated weight (equal: the earlier).  The survivors are
     written in order to the pages of dst_table [B, dst_pages], which must be none of table's; returns
     (kept [B,Hkv,budget] int32: their old slots, -1 behind the last; lens_out [B] int32, which may be
-    given as lens itself)."""
+    given as lens itself).  A sequence whose length is out of range keeps nothing: lens_out 0."""
     B, width, index = _tables(cache, table, lens, None)
     if not isinstance(dst_table, _t.Tensor) or dst_table.dim() != 2:
         raise ValueError("dst_table must be a 2-D tensor [B, dst_pages]")
