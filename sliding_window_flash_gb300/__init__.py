@@ -434,6 +434,8 @@ def swa_attn_fwd_bwd_host(q, k, v, do, window: int, scale: Optional[float] = Non
 
     lib = load()
     dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {dev}")
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     B, Hq, Hkv, N, Lk, D = _dims(q, k)

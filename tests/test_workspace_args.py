@@ -87,6 +87,15 @@ def test_host_pipeline_workspace(lib, monkeypatch, device):
     assert lib.calls == []
 
 
+@pytest.mark.parametrize("device", ["cpu", torch.device("cpu"), "meta"])
+def test_host_pipeline_runs_on_a_gpu_only(lib, monkeypatch, device):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    q, k, lse = _tensors(torch.bfloat16)
+    with pytest.raises(ValueError, match="device"):
+        swa.swa_attn_fwd_bwd_host(q, k, k, q, 4, outs=(q, lse, q, k, k), device=device)
+    assert lib.calls == []
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("device", [None, "cuda", 0])
 def test_host_pipeline_takes_its_gpus_workspace(swa, device):
