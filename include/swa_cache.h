@@ -106,7 +106,8 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  * by a power of two (exact for bf16 and fp16 values down to 2^-28 of the row's largest, and below
  * that within 2^-39 of the largest), codes are exact in fp16, and p is rounded to fp16 as the second
  * product's operand (relative 2^-11, half the step of an fp16 result).  The same call on one GPU gives the
- * same bits (another max_pages may divide the work otherwise).
+ * same bits (another max_pages may divide the work otherwise).  Accumulated weights are exp(x - lse) of
+ * both in fp32: beside the score's own error, relative to within |x| 2^-22.
  */
 size_t swa_cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
                                       int page, int accumulate);

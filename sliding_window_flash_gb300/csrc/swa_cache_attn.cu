@@ -1000,7 +1000,8 @@ Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int 
     // Two tiles a warp halve the conversions of a chunk's codes, and twice as many chunks are in work;
     // but twice as many parts have twice the partial results.  So long walks take them, by the most that
     // the table and the window allow (32 / 8 heads, T = 8, D = 128, 64 sequences of 4,000: 146 us and 174
-    // with one; under a window of 1024, 16 sequences: 34 and 26).
+    // with one; under a window of 1024, 16 sequences: 34 and 26).  Lengths are the device's alone, so
+    // short contexts under a wide table take them too, to their loss (16 sequences of 1,000: 48 us and 35).
     parts *= 2;
     if (static_cast<int64_t>(B) * Hkv * p.NRT * chunks >= 32 * static_cast<int64_t>(parts)) {
       p.tiles = 2;
