@@ -102,6 +102,7 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
  *                the call refuses.
  * A key that a query does not see changes nothing for it, NaN included; where some queries of a call
  * see a token and others do not, this takes values that are finite, as append stores them.
+ * A query with an element that is NaN or infinite gets o, lse and the weights that it adds as NaN.
  * Scores, softmax statistics and sums are fp32.  q is taken as fp16 operands after scaling each row
  * by a power of two (exact for bf16 and fp16 values down to 2^-28 of the row's largest, and below
  * that within 2^-39 of the largest), codes are exact in fp16, and p is rounded to fp16 as the second

@@ -577,7 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 2^(14 - exponent); 1 for zero, infinity and NaN
       const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-      st.tile[y].f[e] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      // Scores of an infinite query are infinite, and exp(x - lse) of them NaN: all NaN from here on, since
+      // a row whose scores were all -inf would look like one that sees nothing.
+      st.tile[y].f[e] = ex == 255 ? __uint_as_float(0x7fffffffu)
+                                  : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const float2 y0 = a.f16 ? Elem<true>::unpack(raw[ye][i].x) : Elem<false>::unpack(raw[ye][i].x);
