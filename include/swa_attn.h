@@ -58,6 +58,11 @@ typedef enum {
                                    out of range and skipped it (reported by swa_check_device)    */
 } swa_status;
 
+/* Element types of the calls that take a `dtype`. */
+#define SWA_BF16 0
+#define SWA_FP16 1
+#define SWA_FP32 2
+
 /*
  * Forward.  Writes o [B,Hq,N,D] bf16 and lse [B,Hq,N] fp32.
  *   q, k, v : inputs (device, bf16, layout above); not modified.
@@ -168,6 +173,36 @@ swa_status swa_attn_bwd_f32(const float* q, const float* k, const float* v, cons
                             int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
                             float scale, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream);
+
+/*
+ * Attention sinks: the general forms above with the first `sinks` keys visible to every query behind
+ * them.  With d = i + Lk - Lq - j, query i sees key j iff
+ *     d >= 0 (causal = 0: d > -window)  and  (d < window or j < sinks),
+ * so the window's near side is unchanged and its far side never passes the sinks.  sinks >= 0; 0, or a
+ * window that reaches every key, gives the general forms' results; sinks > Lk means Lk.
+ *   dtype     : SWA_BF16, SWA_FP16 or SWA_FP32, of q, k, v, o, dO, dq, dk, dv (fp32: bf16 operands and
+ *               the corrected lse, as in the fp32 forms).
+ *   workspace : at least swa_attn_sinks_workspace_bytes bytes (backward: 0 or 1, which call; 0 bytes for
+ *               a 16-bit forward, whose workspace may be NULL), 16-byte aligned; nothing is kept there
+ *               between calls, and calls that may overlap need workspaces of their own.  The size holds
+ *               for the GPU that is current when it is asked for; 0 for arguments that the calls refuse.
+ * As in the general forms a NaN in k or v reaches the query tiles (128 rows) whose window touches its
+ * block of 128 keys; blocks of sinks before the window hold the sinks alone, whatever lies beside them.
+ * A sink's dk and dv sum over every query behind it: the walk over the queries runs in parts, whose fp32
+ * sums are added in a fixed order (bit-reproducible on one GPU).  The backward is launched as Delta, dK/dV
+ * (D = 256: dK, dV), the joining of the sinks' rows, dQ.  Other arguments, checks and errors as in the general and fp32 forms.
+ */
+size_t swa_attn_sinks_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window,
+                                      int sinks, int causal, int dtype, int backward);
+swa_status swa_attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                              int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks,
+                              int causal, float scale, int dtype, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+swa_status swa_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
+                              const void* dO, const float* lse, void* dq, void* dk, void* dv,
+                              int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks,
+                              int causal, float scale, int dtype, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Forward and backward of one layer whose tensors live in host memory: q, k, v, dO in and

@@ -50,11 +50,6 @@ typedef struct swa_cache {
     int D;          /* 64, 128 or 256                                                         */
 } swa_cache;
 
-/* Element types of the calls below. */
-#define SWA_BF16 0
-#define SWA_FP16 1
-#define SWA_FP32 2
-
 /*
  * Append: quantises n_b new tokens of each sequence into slots lens[b] .. lens[b] + n_b - 1.
  *   table    : int32 [B, max_pages]; the entries of the pages written must name pages that no other

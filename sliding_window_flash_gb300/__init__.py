@@ -20,6 +20,7 @@ D in {64, 128, 256}; Hq % Hkv == 0; Lq <= Lk (the queries are the last Lq key po
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -33,6 +34,7 @@ __all__ = [
     "swa_attn_bwd_workspace_bytes",
     "swa_attn_bwd_fused_workspace_bytes",
     "swa_attn_f32_workspace_bytes",
+    "swa_attn_sinks_workspace_bytes",
     "swa_attn_fwd_bwd_host",
     "swa_attn_host_workspace_bytes",
     "swa_attn_bwd_phases",
@@ -92,6 +94,15 @@ SIGNATURES = {
     "swa_attn_fwd_f32": (_c_int, [_vp] * 5 + [_c_int] * 8 + [_c_float, _vp, ctypes.c_size_t, _vp]),
     "swa_attn_bwd_f32": (_c_int, [_vp] * 9 + [_c_int] * 8 + [_c_float, _vp, ctypes.c_size_t, _vp]),
     "swa_attn_host_workspace_bytes": (ctypes.c_size_t, [_c_int] * 6),
+    "swa_attn_sinks_workspace_bytes": (ctypes.c_size_t, [_c_int] * 11),
+    "swa_attn_fwd_sinks": (
+        _c_int,
+        [_vp] * 5 + [_c_int] * 9 + [_c_float, _c_int, _vp, ctypes.c_size_t, _vp],
+    ),
+    "swa_attn_bwd_sinks": (
+        _c_int,
+        [_vp] * 9 + [_c_int] * 9 + [_c_float, _c_int, _vp, ctypes.c_size_t, _vp],
+    ),
     "swa_attn_fwd_bwd_host": (
         _c_int,
         [_vp] * 9 + [_c_int] * 6 + [_c_float, _c_int, _vp, ctypes.c_size_t, _vp],
@@ -208,17 +219,63 @@ def _f32_workspace(workspace, B, Hq, Hkv, Lq, Lk, D, device):
     return _cache._space(workspace, device)
 
 
+def swa_attn_sinks_workspace_bytes(B: int, Hq: int, Hkv: int, Lq: int, Lk: int, D: int, window: int,
+                                   sinks: int, causal: bool = True, dtype=None,
+                                   backward: bool = False) -> int:
+    """Bytes of the workspace of swa_attn_fwd (backward=True: swa_attn_bwd) with sinks, for tensors of
+    this dtype (None: 16-bit), on the current GPU."""
+    import torch
+
+    return int(load().swa_attn_sinks_workspace_bytes(
+        B, Hq, Hkv, Lq, Lk, D, _cache._int32(window), _sinks(sinks), int(bool(causal)),
+        2 if dtype == torch.float32 else 0, int(bool(backward))))
+
+
+def _sinks(sinks):
+    """`sinks` as a C int; more than an int holds are more than any sequence has."""
+    sinks = int(sinks)
+    if sinks < 0:
+        raise ValueError(f"sinks must not be negative, got {sinks}")
+    return _cache._int32(sinks)
+
+
+# A workspace's size follows the number of the GPU's SMs, so it is asked for, and kept, for that GPU.
+@functools.lru_cache(maxsize=256)
+def _sinks_space(index, *sizes):
+    return int(_cache._on(index, "swa_attn_sinks_workspace_bytes", *sizes))
+
+
+def _run_sinks(name, tensors, sizes, window, sinks, causal, scale, dt, workspace):
+    """Calls an entry point for sinks on the current stream of the tensors' GPU."""
+    import torch
+
+    device = tensors[0].device
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"a tensor is on {t.device}, expected {device}")
+    window, causal, kind = _cache._int32(window), int(bool(causal)), _cache._t.kinds[dt]
+    if workspace is None:
+        need = _sinks_space(device.index, *sizes, window, sinks, causal, kind,
+                            int(name == "swa_attn_bwd_sinks"))
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    space = _cache._space(workspace, device)
+    _cache._run(name, device.index, *(t.data_ptr() for t in tensors), *sizes, window, sinks, causal,
+                _scale(scale, sizes[-1]), kind, *space)
+
+
 def swa_attn_fwd(q, k, v, window: int, scale: Optional[float] = None, out=None, lse=None,
-                 causal: bool = True, workspace=None):
+                 causal: bool = True, workspace=None, sinks: int = 0):
     """Forward: returns (o [B,Hq,Lq,D] in q's dtype (bf16, fp16 or fp32), lse [B,Hq,Lq] fp32).
 
     q [B,Hq,Lq,D], k and v [B,Hkv,Lk,D] with Lq <= Lk: the queries are the last Lq positions of the
-    keys.  causal=False selects the two-sided window |pos - j| < window.  fp32 calls use a device
-    workspace of swa_attn_f32_workspace_bytes (allocated here unless given).
+    keys.  causal=False selects the two-sided window |pos - j| < window.  The first `sinks` keys stay
+    visible to every query behind them.  fp32 calls use a device workspace of
+    swa_attn_f32_workspace_bytes, or of swa_attn_sinks_workspace_bytes (allocated here unless given).
     """
     import torch
 
     lib = load()
+    sinks = _sinks(sinks)
     B, Hq, Hkv, Lq, Lk, D = _dims(q, k)
     dt = _elem_dtype(q)
     _check_tensor(q, "q", (B, Hq, Lq, D), dt)
@@ -230,6 +287,10 @@ def swa_attn_fwd(q, k, v, window: int, scale: Optional[float] = None, out=None, 
         lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
     _check_tensor(out, "out", (B, Hq, Lq, D), dt)
     _check_tensor(lse, "lse", (B, Hq, Lq), torch.float32)
+    if sinks:
+        _run_sinks("swa_attn_fwd_sinks", (q, k, v, out, lse), (B, Hq, Hkv, Lq, Lk, D), window, sinks,
+                   causal, scale, dt, workspace)
+        return out, lse
     ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr())
     f16 = dt == torch.float16
     st = _stream_handle(q.device)
@@ -260,18 +321,22 @@ def swa_attn_bwd_fused_workspace_bytes(B: int, Hq: int, Lq: int, D: int) -> int:
 
 def swa_attn_bwd(q, k, v, o, do, lse, window: int, scale: Optional[float] = None,
                  dq=None, dk=None, dv=None, workspace=None, causal: bool = True,
-                 fused: bool = False) -> Tuple:
+                 fused: bool = False, sinks: int = 0) -> Tuple:
     """Backward of sum(do * o): returns (dq, dk, dv) in q's dtype (bf16, fp16 or fp32), dk/dv
-    summed over each kv group.  Shapes, window and workspace as in swa_attn_fwd.
+    summed over each kv group.  Shapes, window and sinks as in swa_attn_fwd.
 
     bf16 / fp16: ``fused=False`` (default) runs the split, bit-reproducible swa_attn_bwd /
     swa_attn_bwd_ex (workspace of swa_attn_bwd_workspace_bytes), the faster path on GB300;
     ``fused=True`` runs swa_attn_bwd_fused (one kernel for dK, dV and dQ; workspace of
     swa_attn_bwd_fused_workspace_bytes; dQ's fp32 additions run in a varying order).  fp32 tensors
-    always take the split path."""
+    and calls with sinks (workspace of swa_attn_sinks_workspace_bytes) always take the split path;
+    fused=True with sinks is refused."""
     import torch
 
     lib = load()
+    sinks = _sinks(sinks)
+    if sinks and fused:
+        raise ValueError("the fused backward has no sinks")
     B, Hq, Hkv, Lq, Lk, D = _dims(q, k)
     dt = _elem_dtype(q)
     for t, name, hs, L in ((q, "q", Hq, Lq), (k, "k", Hkv, Lk), (v, "v", Hkv, Lk), (o, "o", Hq, Lq),
@@ -283,6 +348,10 @@ def swa_attn_bwd(q, k, v, o, do, lse, window: int, scale: Optional[float] = None
     dv = torch.empty_like(v) if dv is None else dv
     for t, name, hs, L in ((dq, "dq", Hq, Lq), (dk, "dk", Hkv, Lk), (dv, "dv", Hkv, Lk)):
         _check_tensor(t, name, (B, hs, L, D), dt)
+    if sinks:
+        _run_sinks("swa_attn_bwd_sinks", (q, k, v, o, do, lse, dq, dk, dv),
+                   (B, Hq, Hkv, Lq, Lk, D), window, sinks, causal, scale, dt, workspace)
+        return dq, dk, dv
     ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
     f16 = dt == torch.float16
@@ -479,22 +548,23 @@ def _make_autograd():
     import torch
 
     class SlidingWindowAttention(torch.autograd.Function):
-        """o = attention(q, k, v) under a sliding window (causal unless causal=False); saves only
-        (o, lse) for the backward."""
+        """o = attention(q, k, v) under a sliding window (causal unless causal=False), with the first
+        `sinks` keys visible to every query behind them; saves only (o, lse) for the backward."""
 
         @staticmethod
-        def forward(ctx, q, k, v, window: int, scale: Optional[float] = None, causal: bool = True):
-            o, lse = swa_attn_fwd(q, k, v, window, scale, causal=causal)
+        def forward(ctx, q, k, v, window: int, scale: Optional[float] = None, causal: bool = True,
+                    sinks: int = 0):
+            o, lse = swa_attn_fwd(q, k, v, window, scale, causal=causal, sinks=sinks)
             ctx.save_for_backward(q, k, v, o, lse)
-            ctx.window, ctx.scale, ctx.causal = window, scale, causal
+            ctx.window, ctx.scale, ctx.causal, ctx.sinks = window, scale, causal, sinks
             return o
 
         @staticmethod
         def backward(ctx, do):
             q, k, v, o, lse = ctx.saved_tensors
             dq, dk, dv = swa_attn_bwd(q, k, v, o, do.contiguous(), lse, ctx.window, ctx.scale,
-                                      causal=ctx.causal)
-            return dq, dk, dv, None, None, None
+                                      causal=ctx.causal, sinks=ctx.sinks)
+            return dq, dk, dv, None, None, None, None
 
     return SlidingWindowAttention
 

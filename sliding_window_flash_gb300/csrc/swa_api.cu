@@ -81,9 +81,10 @@ swa_status check_sizes(int B, int Hq, int Hkv, int N, int D, int window, float s
   return check_shape(B, Hq, Hkv, N, N, D, window, scale);
 }
 
-// Lq query rows as the last Lq positions of Lk keys; causal: 0 <= pos - j < W, else |pos - j| < W.
+// Lq query rows as the last Lq positions of Lk keys; causal: 0 <= pos - j < W, else |pos - j| < W; the
+// first `sinks` keys stay visible when pos - j >= W.
 swa::Problem make_problem_ex(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
-                             float scale, unsigned* err, int f16) {
+                             float scale, unsigned* err, int f16, int sinks = 0) {
   swa::Problem pb;
   pb.B = B;
   pb.Hq = Hq;
@@ -99,6 +100,7 @@ swa::Problem make_problem_ex(int B, int Hq, int Hkv, int Lq, int Lk, int D, int 
   pb.scale = scale;
   pb.err = err;
   pb.f16 = f16;
+  pb.sinks = W == Lk ? 0 : sinks < Lk ? sinks : Lk;
   return pb;
 }
 
@@ -111,7 +113,7 @@ swa::Problem make_problem(int B, int Hq, int Hkv, int N, int D, int window, floa
 // or not.
 swa_status fwd_impl(int f16, const void* q, const void* k, const void* v, void* o, float* lse,
                     int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
-                    float scale, cudaStream_t stream) {
+                    float scale, cudaStream_t stream, int sinks = 0) {
   if (!q || !k || !v || !o || !lse) return SWA_ERR_INVALID_ARG;
   if ((causal != 0 && causal != 1) || (f16 != 0 && f16 != 1)) return SWA_ERR_INVALID_ARG;
   swa_status st = check_shape(B, Hq, Hkv, Lq, Lk, D, window, scale);
@@ -120,7 +122,8 @@ swa_status fwd_impl(int f16, const void* q, const void* k, const void* v, void* 
     return SWA_ERR_MISALIGNED;
   unsigned* err = nullptr;
   if ((st = current_device(&err)) != SWA_OK) return st;
-  const swa::Problem pb = make_problem_ex(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, err, f16);
+  const swa::Problem pb =
+      make_problem_ex(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, err, f16, sinks);
   if (swa::launch_fwd(pb, q, k, v, o, lse, stream) != cudaSuccess) return SWA_ERR_CUDA;
   return SWA_OK;
 }
@@ -128,20 +131,22 @@ swa_status fwd_impl(int f16, const void* q, const void* k, const void* v, void* 
 swa_status bwd_impl(int f16, const void* q, const void* k, const void* v, const void* o,
                     const void* dO, const float* lse, void* dq, void* dk, void* dv, int B, int Hq,
                     int Hkv, int Lq, int Lk, int D, int window, int causal, float scale,
-                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+                    void* workspace, size_t workspace_bytes, cudaStream_t stream, int sinks = 0) {
   if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv) return SWA_ERR_INVALID_ARG;
   if ((causal != 0 && causal != 1) || (f16 != 0 && f16 != 1)) return SWA_ERR_INVALID_ARG;
   swa_status st = check_shape(B, Hq, Hkv, Lq, Lk, D, window, scale);
   if (st != SWA_OK) return st;
-  if (!workspace || workspace_bytes < swa_attn_bwd_workspace_bytes(B, Hq, Lq, D))
+  swa::Problem pb =
+      make_problem_ex(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, nullptr, f16, sinks);
+  const size_t delta_bytes = swa_attn_bwd_workspace_bytes(B, Hq, Lq, D);
+  if (!workspace || workspace_bytes < delta_bytes + swa::sink_part_bytes(pb))
     return SWA_ERR_WORKSPACE;
   const void* ptrs[] = {q, k, v, o, dO, lse, dq, dk, dv, workspace};
   for (const void* p : ptrs)
     if (!aligned16(p)) return SWA_ERR_MISALIGNED;
-  unsigned* err = nullptr;
-  if ((st = current_device(&err)) != SWA_OK) return st;
-  const swa::Problem pb = make_problem_ex(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, err, f16);
+  if ((st = current_device(&pb.err)) != SWA_OK) return st;
   float* delta = static_cast<float*>(workspace);
+  pb.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + delta_bytes);
   if (swa::launch_bwd_delta(pb, o, dO, delta, stream) != cudaSuccess) return SWA_ERR_CUDA;
   if (swa::launch_bwd_dkdv(pb, q, k, v, dO, lse, delta, dk, dv, stream) != cudaSuccess)
     return SWA_ERR_CUDA;
@@ -441,21 +446,21 @@ F32Layout f32_layout(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
 
 swa_status f32_prologue(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
                         float scale, const void* workspace, size_t workspace_bytes,
-                        std::initializer_list<const void*> ptrs, swa::Problem* pb) {
+                        std::initializer_list<const void*> ptrs, swa::Problem* pb, int sinks,
+                        bool backward) {
   for (const void* p : ptrs)
     if (!p) return SWA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return SWA_ERR_INVALID_ARG;
   swa_status st = check_shape(B, Hq, Hkv, Lq, Lk, D, window, scale);
   if (st != SWA_OK) return st;
-  if (!workspace || workspace_bytes < f32_layout(B, Hq, Hkv, Lq, Lk, D).total)
-    return SWA_ERR_WORKSPACE;
+  *pb = make_problem_ex(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, nullptr, 0, sinks);
+  const size_t need = f32_layout(B, Hq, Hkv, Lq, Lk, D).total +
+                      (backward ? swa::sink_part_bytes(*pb) : 0);
+  if (!workspace || workspace_bytes < need) return SWA_ERR_WORKSPACE;
   for (const void* p : ptrs)
     if (!aligned16(p)) return SWA_ERR_MISALIGNED;
   if (!aligned16(workspace)) return SWA_ERR_MISALIGNED;
-  unsigned* err = nullptr;
-  if ((st = current_device(&err)) != SWA_OK) return st;
-  *pb = make_problem_ex(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, err, 0);
-  return SWA_OK;
+  return current_device(&pb->err);
 }
 
 // q, k, v rounded to bf16; with `split`, also the bf16 residuals of q and k.
@@ -475,23 +480,12 @@ swa::RoundJob round_qkv(const float* q, const float* k, const float* v, uint8_t*
   return j;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t swa_attn_f32_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lk < Lq || (D != 64 && D != 128 && D != 256))
-    return 0;
-  return f32_layout(B, Hq, Hkv, Lq, Lk, D).total;
-}
-
-swa_status swa_attn_fwd_f32(const float* q, const float* k, const float* v, float* o, float* lse,
-                            int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
-                            float scale, void* workspace, size_t workspace_bytes,
-                            cudaStream_t stream) {
+swa_status fwd_f32_impl(const float* q, const float* k, const float* v, float* o, float* lse, int B,
+                        int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks, int causal,
+                        float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   swa::Problem pb;
   swa_status st = f32_prologue(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, workspace,
-                               workspace_bytes, {q, k, v, o, lse}, &pb);
+                               workspace_bytes, {q, k, v, o, lse}, &pb, sinks, false);
   if (st != SWA_OK) return st;
   const F32Layout L = f32_layout(B, Hq, Hkv, Lq, Lk, D);
   auto* ws = static_cast<uint8_t*>(workspace);
@@ -516,18 +510,18 @@ swa_status swa_attn_fwd_f32(const float* q, const float* k, const float* v, floa
   return swa::launch_widen_bf16(w, stream) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
-swa_status swa_attn_bwd_f32(const float* q, const float* k, const float* v, const float* o,
-                            const float* dO, const float* lse, float* dq, float* dk, float* dv,
-                            int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
-                            float scale, void* workspace, size_t workspace_bytes,
-                            cudaStream_t stream) {
+swa_status bwd_f32_impl(const float* q, const float* k, const float* v, const float* o,
+                        const float* dO, const float* lse, float* dq, float* dk, float* dv, int B,
+                        int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks, int causal,
+                        float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   swa::Problem pb;
   swa_status st = f32_prologue(B, Hq, Hkv, Lq, Lk, D, window, causal, scale, workspace,
-                               workspace_bytes, {q, k, v, o, dO, lse, dq, dk, dv}, &pb);
+                               workspace_bytes, {q, k, v, o, dO, lse, dq, dk, dv}, &pb, sinks, true);
   if (st != SWA_OK) return st;
   const F32Layout L = f32_layout(B, Hq, Hkv, Lq, Lk, D);
   auto* ws = static_cast<uint8_t*>(workspace);
   float* delta = reinterpret_cast<float*>(ws + L.delta);
+  pb.sink_part = reinterpret_cast<float*>(ws + L.total);
   if (swa::launch_round_bf16(round_qkv(q, k, v, ws, L), stream) != cudaSuccess) return SWA_ERR_CUDA;
   if (swa::launch_delta_f32(pb, o, dO, delta, ws + L.a16, stream) != cudaSuccess)
     return SWA_ERR_CUDA;
@@ -545,6 +539,78 @@ swa_status swa_attn_bwd_f32(const float* q, const float* k, const float* v, cons
   w.end[1] = L.q_units + L.k_units;
   w.end[2] = w.end[3] = L.q_units + 2 * L.k_units;
   return swa::launch_widen_bf16(w, stream) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t swa_attn_f32_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lk < Lq || (D != 64 && D != 128 && D != 256))
+    return 0;
+  return f32_layout(B, Hq, Hkv, Lq, Lk, D).total;
+}
+
+swa_status swa_attn_fwd_f32(const float* q, const float* k, const float* v, float* o, float* lse,
+                            int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
+                            float scale, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  return fwd_f32_impl(q, k, v, o, lse, B, Hq, Hkv, Lq, Lk, D, window, 0, causal, scale, workspace,
+                      workspace_bytes, stream);
+}
+
+swa_status swa_attn_bwd_f32(const float* q, const float* k, const float* v, const float* o,
+                            const float* dO, const float* lse, float* dq, float* dk, float* dv,
+                            int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
+                            float scale, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  return bwd_f32_impl(q, k, v, o, dO, lse, dq, dk, dv, B, Hq, Hkv, Lq, Lk, D, window, 0, causal,
+                      scale, workspace, workspace_bytes, stream);
+}
+
+// ---- Sinks: any of the three element types.
+
+size_t swa_attn_sinks_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window,
+                                      int sinks, int causal, int dtype, int backward) {
+  if (check_shape(B, Hq, Hkv, Lq, Lk, D, window, 1.f) != SWA_OK || sinks < 0 ||
+      (causal != 0 && causal != 1) || (backward != 0 && backward != 1) || dtype < SWA_BF16 ||
+      dtype > SWA_FP32)
+    return 0;
+  const size_t base = dtype == SWA_FP32 ? f32_layout(B, Hq, Hkv, Lq, Lk, D).total
+                      : backward        ? swa_attn_bwd_workspace_bytes(B, Hq, Lq, D)
+                                        : 0;
+  if (!backward) return base;
+  return base + swa::sink_part_bytes(
+                    make_problem_ex(B, Hq, Hkv, Lq, Lk, D, window, causal, 1.f, nullptr, 0, sinks));
+}
+
+swa_status swa_attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                              int B, int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks,
+                              int causal, float scale, int dtype, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  if (sinks < 0 || dtype < SWA_BF16 || dtype > SWA_FP32) return SWA_ERR_INVALID_ARG;
+  if (dtype == SWA_FP32)
+    return fwd_f32_impl(static_cast<const float*>(q), static_cast<const float*>(k),
+                        static_cast<const float*>(v), static_cast<float*>(o), lse, B, Hq, Hkv, Lq,
+                        Lk, D, window, sinks, causal, scale, workspace, workspace_bytes, stream);
+  return fwd_impl(dtype, q, k, v, o, lse, B, Hq, Hkv, Lq, Lk, D, window, causal, scale, stream,
+                  sinks);
+}
+
+swa_status swa_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
+                              const void* dO, const float* lse, void* dq, void* dk, void* dv, int B,
+                              int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks,
+                              int causal, float scale, int dtype, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  if (sinks < 0 || dtype < SWA_BF16 || dtype > SWA_FP32) return SWA_ERR_INVALID_ARG;
+  if (dtype == SWA_FP32)
+    return bwd_f32_impl(static_cast<const float*>(q), static_cast<const float*>(k),
+                        static_cast<const float*>(v), static_cast<const float*>(o),
+                        static_cast<const float*>(dO), lse, static_cast<float*>(dq),
+                        static_cast<float*>(dk), static_cast<float*>(dv), B, Hq, Hkv, Lq, Lk, D,
+                        window, sinks, causal, scale, workspace, workspace_bytes, stream);
+  return bwd_impl(dtype, q, k, v, o, dO, lse, dq, dk, dv, B, Hq, Hkv, Lq, Lk, D, window, causal,
+                  scale, workspace, workspace_bytes, stream, sinks);
 }
 
 }  // extern "C"

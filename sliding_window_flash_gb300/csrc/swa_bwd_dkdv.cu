@@ -19,6 +19,8 @@
 // S^T is computed while it exponentiates; once dP^T has landed and been read, P^T and dS^T go
 // back to TMEM as bf16 pairs over the dP^T columns (each half of a row: P^T over the first 32 of
 // its 64 columns, dS^T over the last 32) and are the A operands of dV += P^T dO and dK += dS^T Q.
+// With sinks (kSinks) the first CTAs of the grid each walk a part of all query tiles behind a block of
+// sinks and leave fp32 sums of its rows (SinkPlan); a second kernel joins them.
 // TMEM columns: [0,128) S^T, [128,256) dP^T / P^T + dS^T, [256, 256+D) dK, [256+D, 256+2D) dV.
 #include "swa_kernels.h"
 #include "swa_ptx.cuh"
@@ -72,11 +74,13 @@ struct DkdvArgs {
   uint16_t* dv;
   int BHK, Hq, Hkv, G, nkb;
   Span span;
+  int sinks, sink_ctas, splits;
+  float* part;
   float scale, scale_log2;
   unsigned* err;
 };
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 __global__ void __launch_bounds__(352, 1)
     swa_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_do,
@@ -99,17 +103,31 @@ __global__ void __launch_bounds__(352, 1)
   const uint32_t sDO0 = smem_u32(smem + C::kOffDO);
 
   // Key blocks with the longest walks (lowest index under a full causal window) go first.
-  const int kb = static_cast<int>(blockIdx.x) / a.BHK;
-  const int bhk = static_cast<int>(blockIdx.x) % a.BHK;
+  int block = static_cast<int>(blockIdx.x), split = 0;
+  Span sp = a.span;  // window geometry, held in registers
+  bool sink = false;  // this CTA takes a part of a sinks' walk
+  if constexpr (kSinks) {
+    sink = block < a.sink_ctas;
+    if (sink) {
+      sp.dmax = sp.Lk - 1;
+      split = block % a.splits;
+      block /= a.splits;
+    } else {
+      block -= a.sink_ctas;
+    }
+  }
+  const int kb = block / a.BHK;
+  const int bhk = block % a.BHK;
   const int b = bhk / a.Hkv, hk = bhk % a.Hkv;
   const int k0 = kb * kBlockN;
-  const Span sp = a.span;  // window geometry, held in registers
+  if constexpr (kSinks)
+    if (!sink && k0 + kBlockN <= a.sinks) return;  // the join writes all of these rows
   const int qb_lo = sp.first_qblock(k0);
   const int qb_hi = sp.last_qblock(k0);
   // No query sees this key block when the queries are a short suffix of the keys: then nq <= 0,
   // nothing is computed and dK = dV = 0 is written.
   const int nq = qb_hi >= qb_lo ? qb_hi - qb_lo + 1 : 0;
-  const int T = a.G * nq;  // (query head, query block) tiles of the walk
+  int T = a.G * nq;  // (query head, query block) tiles of the walk
   // A query tile q0 needs no mask iff q_int_lo <= q0 <= q_int_hi (Span::interior for this key
   // block, solved for q0 once).
   const int q_int_lo = k0 + kBlockN - 1 + sp.dmin - sp.off;
@@ -122,6 +140,15 @@ __global__ void __launch_bounds__(352, 1)
   struct WalkPos {
     int qi = 0, gi = 0;
   };
+  WalkPos start;
+  if constexpr (kSinks) {
+    if (sink && T > 0) {
+      const int t0 = static_cast<int>(static_cast<long long>(T) * split / a.splits);
+      T = static_cast<int>(static_cast<long long>(T) * (split + 1) / a.splits) - t0;
+      start.gi = t0 / nq;
+      start.qi = t0 - start.gi * nq;
+    }
+  }
   auto advance = [&](WalkPos& w) {
     if (++w.qi == nq) {
       w.qi = 0;
@@ -135,6 +162,15 @@ __global__ void __launch_bounds__(352, 1)
   if (T == 0) {
     // No query sees this key block: its dK and dV rows are zero.  Written straight from the
     // threads, before any barrier, tensor memory or copy is set up.
+    if constexpr (kSinks) {
+      if (sink) {  // more parts than tiles: this one's sums are zero
+        const int rows = min(kBlockN, a.sinks - k0);
+        for (int which = 0; which < 2; ++which)
+          for (int i = static_cast<int>(threadIdx.x); i < rows * D; i += C::kThreads)
+            a.part[sink_part_offset(split, a.BHK, bhk, which, a.sinks, k0, D) + i] = 0.f;
+        return;
+      }
+    }
     zero_key_rows(a.dk, a.dv, bhk, k0, sp.Lk, D);
     return;
   }
@@ -181,7 +217,7 @@ __global__ void __launch_bounds__(352, 1)
         tma_load_3d(sK + h * C::kChunkBytes, &tm_k, bar(C::kKVFull), 64 * h, k0, bhk);
       int last_q[C::kQStages];
       for (int s = 0; s < C::kQStages; ++s) last_q[s] = -1;
-      WalkPos wp;
+      WalkPos wp = start;
       for (int t = 0; t < T; ++t, advance(wp)) {
         const int sq = t % C::kQStages, nqs = t / C::kQStages;
         if (t >= C::kQStages && !mbar_wait(bar(C::kQEmpty + sq), (nqs - 1) & 1, &abort_flag, a.err))
@@ -207,7 +243,7 @@ __global__ void __launch_bounds__(352, 1)
         tma_load_3d(sV + h * C::kChunkBytes, &tm_v, bar(C::kKVFull), 64 * h, k0, bhk);
       int last_do[C::kDOStages];
       for (int s = 0; s < C::kDOStages; ++s) last_do[s] = -1;
-      WalkPos wp;
+      WalkPos wp = start;
       for (int t = 0; t < T; ++t, advance(wp)) {
         const int sd = t % C::kDOStages, nds = t / C::kDOStages;
         if (t >= C::kDOStages &&
@@ -310,7 +346,7 @@ __global__ void __launch_bounds__(352, 1)
         nxt = h == 0 ? SWA_POS_INF : 0.f;
       }
     };
-    WalkPos wcur, wnext;  // tiles t and t + 1
+    WalkPos wcur = start, wnext = start;  // tiles t and t + 1
     advance(wnext);
     if (T > 0) fetch_row(wcur);
     bool ok = true;
@@ -412,8 +448,30 @@ __global__ void __launch_bounds__(352, 1)
       tmem_wait_st();
       warp_arrive(bar(C::kPFull));
     }
-    if (ok && warp_wait(bar(C::kDone), 0, &abort_flag, a.err)) {
-      tc_fence_after();
+    ok = ok && warp_wait(bar(C::kDone), 0, &abort_flag, a.err);
+    if (ok) tc_fence_after();
+    if constexpr (kSinks) {
+      if (ok && sink) {  // the part's sums, unscaled, in fp32
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          float* dst = a.part + sink_part_offset(split, a.BHK, bhk, which, a.sinks, key, D) + D / 2 * h;
+#pragma unroll
+          for (int c0 = 0; c0 < D / 2; c0 += 32) {
+            uint32_t rr[32];
+            tmem_ld32(tmem + lane_base + (which == 0 ? C::kColDK : C::kColDV) + D / 2 * h + c0, rr);
+            tmem_wait_ld(rr);
+            if (key < a.sinks) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(dst + c0 + i) =
+                    make_uint4(rr[i], rr[i + 1], rr[i + 2], rr[i + 3]);
+            }
+          }
+        }
+        ok = false;  // nothing else to write
+      }
+    }
+    if (ok) {
       // dK * scale and dV -> bf16, staged in the two Q slots (free: every MMA has completed) and
       // written with tensor stores, one per 64-column chunk (rows past Lk are not written).
       constexpr int kHalf = D / 2;
@@ -466,7 +524,7 @@ __global__ void __launch_bounds__(352, 1)
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 cudaError_t launch_dkdv_d(const Problem& pb, const void* q, const void* k, const void* v,
                           const void* dO, const float* lse, const float* delta, void* dk, void* dv,
                           cudaStream_t stream) {
@@ -480,7 +538,7 @@ cudaError_t launch_dkdv_d(const Problem& pb, const void* q, const void* k, const
       !make_tmap_3d(&tdk, dk, bhk, pb.span.Lk, D, kBlockN, F16) ||
       !make_tmap_3d(&tdv, dv, bhk, pb.span.Lk, D, kBlockN, F16))
     return cudaErrorInvalidValue;
-  auto kern = swa_dkdv_kernel<D, F16>;
+  auto kern = swa_dkdv_kernel<D, F16, kSinks>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -498,23 +556,43 @@ cudaError_t launch_dkdv_d(const Problem& pb, const void* q, const void* k, const
   a.scale = pb.scale;
   a.scale_log2 = pb.scale * kLog2e;
   a.err = pb.err;
-  const unsigned grid = static_cast<unsigned>(a.nkb) * static_cast<unsigned>(a.BHK);
+  a.sinks = pb.sinks;
+  a.part = pb.sink_part;
+  a.splits = 1;
+  a.sink_ctas = 0;
+  if (kSinks) {
+    const SinkPlan p = sink_plan(pb);
+    a.splits = p.splits;
+    a.sink_ctas = p.blocks * a.BHK * p.splits;
+  }
+  const unsigned grid =
+      static_cast<unsigned>(a.nkb) * static_cast<unsigned>(a.BHK) + static_cast<unsigned>(a.sink_ctas);
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk, tv, tdk, tdv, a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e != cudaSuccess || !kSinks ? e : launch_sink_join(pb, a.splits, dk, dv, stream);
 }
 
+}  // namespace
+
+namespace {
+template <int D>
+cudaError_t launch_dkdv_any(const Problem& pb, const void* q, const void* k, const void* v,
+                            const void* dO, const float* lse, const float* delta, void* dk,
+                            void* dv, cudaStream_t stream) {
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_dkdv_d<D, true, true>(pb, q, k, v, dO, lse, delta, dk, dv, stream)
+                  : launch_dkdv_d<D, false, true>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
+  return pb.f16 ? launch_dkdv_d<D, true, false>(pb, q, k, v, dO, lse, delta, dk, dv, stream)
+                : launch_dkdv_d<D, false, false>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
+}
 }  // namespace
 
 cudaError_t launch_bwd_dkdv(const Problem& pb, const void* q, const void* k, const void* v,
                             const void* dO, const float* lse, const float* delta, void* dk,
                             void* dv, cudaStream_t stream) {
   if (pb.D == 256) return launch_dkdv_d256(pb, q, k, v, dO, lse, delta, dk, dv, stream);
-  if (pb.D == 64)
-    return pb.f16 ? launch_dkdv_d<64, true>(pb, q, k, v, dO, lse, delta, dk, dv, stream)
-                  : launch_dkdv_d<64, false>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
-  if (pb.D == 128)
-    return pb.f16 ? launch_dkdv_d<128, true>(pb, q, k, v, dO, lse, delta, dk, dv, stream)
-                  : launch_dkdv_d<128, false>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
+  if (pb.D == 64) return launch_dkdv_any<64>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
+  if (pb.D == 128) return launch_dkdv_any<128>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -72,18 +72,21 @@ struct DqArgs {
   uint16_t* dq;  // bf16 or fp16 elements
   int BH, Hq, Hkv, G, nqb, ntiles;
   Span span;
+  int sinks;
   float scale, scale_log2;
   unsigned* err;
   FastDiv divBH, divHq, divG;  // tile index decomposition
 };
 
-struct DqTile {
-  int bh, bhk, q0, kb_lo, nkv;
+template <bool kSinks>
+struct DqTile : KeyWalk<kSinks> {
+  int bh, bhk, q0;
 };
 
 // Tile t: heaviest query blocks first (the causal case gives later blocks more key blocks).
-__device__ __forceinline__ DqTile dq_tile(int t, const DqArgs& a, const Span sp) {
-  DqTile f;
+template <bool kSinks>
+__device__ __forceinline__ DqTile<kSinks> dq_tile(int t, const DqArgs& a, const Span sp) {
+  DqTile<kSinks> f;
   const uint32_t tq = a.divBH.div(static_cast<uint32_t>(t));
   const int qb = a.nqb - 1 - static_cast<int>(tq);
   f.bh = t - static_cast<int>(tq) * a.BH;
@@ -91,16 +94,16 @@ __device__ __forceinline__ DqTile dq_tile(int t, const DqArgs& a, const Span sp)
   f.bhk = static_cast<int>(b) * a.Hkv +
           static_cast<int>(a.divG.div(static_cast<uint32_t>(f.bh) - b * static_cast<uint32_t>(a.Hq)));
   f.q0 = qb * kBlockM;
-  f.kb_lo = sp.first_kblock(f.q0);
-  f.nkv = sp.last_kblock(f.q0) - f.kb_lo + 1;
+  f.set(sp, a.sinks, f.q0);
   return f;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 __global__ void __launch_bounds__(352, 1)
     swa_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const DqArgs a) {
+                  const __grid_constant__ CUtensorMap tm_ks,  // K and V up to the last sink
+                  const __grid_constant__ CUtensorMap tm_vs, const DqArgs a) {
   using C = DqCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(352, 1)
       int g = 0;  // key blocks loaded so far by this CTA
       bool ok = true;
       for (int t = blockIdx.x, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-        const DqTile f = dq_tile(t, a, sp);
+        const DqTile<kSinks> f = dq_tile<kSinks>(t, a, sp);
         // Q / dO of the previous tile are free once its last dP has been computed.
         if (it >= 1 && !mbar_wait(bar(C::kQDEmpty), (it - 1) & 1, &abort_flag, a.err)) break;
         mbar_arrive_expect_tx(bar(C::kQDFull), 2 * C::kTileBytes);
@@ -171,7 +174,8 @@ __global__ void __launch_bounds__(352, 1)
         }
         last_qd = it;
         for (int j = 0; j < f.nkv; ++j, ++g) {
-          const int k0 = (f.kb_lo + j) * kBlockN;
+          const int k0 = f.k0(j);
+          const CUtensorMap* map = f.is_far(j) ? &tm_ks : &tm_k;
           const int sk = g % C::kKStages, nk = g / C::kKStages;
           if (g >= C::kKStages &&
               !(ok = mbar_wait(bar(C::kKEmpty + sk), (nk - 1) & 1, &abort_flag, a.err)))
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(352, 1)
           const uint32_t sK = sK0 + sk * C::kTileBytes;
           mbar_arrive_expect_tx(bar(C::kKFull + sk), C::kTileBytes);
           for (int h = 0; h < C::kChunks; ++h)
-            tma_load_3d(sK + h * C::kChunkBytes, &tm_k, bar(C::kKFull + sk), 64 * h, k0, f.bhk);
+            tma_load_3d(sK + h * C::kChunkBytes, map, bar(C::kKFull + sk), 64 * h, k0, f.bhk);
           last_k[sk] = g;
         }
       }
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(352, 1)
       int g = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < a.ntiles; t += tile_step) {
-        const DqTile f = dq_tile(t, a, sp);
+        const DqTile<kSinks> f = dq_tile<kSinks>(t, a, sp);
         for (int j = 0; j < f.nkv; ++j, ++g) {
           const int sv = g % C::kVStages, nv = g / C::kVStages;
           if (g >= C::kVStages &&
@@ -205,8 +209,8 @@ __global__ void __launch_bounds__(352, 1)
           const uint32_t sV = sV0 + sv * C::kTileBytes;
           mbar_arrive_expect_tx(bar(C::kVFull + sv), C::kTileBytes);
           for (int h = 0; h < C::kChunks; ++h)
-            tma_load_3d(sV + h * C::kChunkBytes, &tm_v, bar(C::kVFull + sv), 64 * h,
-                        (f.kb_lo + j) * kBlockN, f.bhk);
+            tma_load_3d(sV + h * C::kChunkBytes, f.is_far(j) ? &tm_vs : &tm_v, bar(C::kVFull + sv),
+                        64 * h, f.k0(j), f.bhk);
           last_v[sv] = g;
         }
       }
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(352, 1)
     int g = 0;  // key blocks issued so far by this CTA
     bool ok = true;
     for (int t = blockIdx.x, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const DqTile f = dq_tile(t, a, sp);
+      const DqTile<kSinks> f = dq_tile<kSinks>(t, a, sp);
       const int n = f.nkv;
       ok = warp_wait(bar(C::kQDFull), it & 1, &abort_flag, a.err);
       if (ok) ok = issue_s(g);
@@ -288,9 +292,9 @@ __global__ void __launch_bounds__(352, 1)
                       C::kDQEmpty - C::kSFull == dqc::DqBar::kDQEmpty && C::kColS == dqc::kColS &&
                       C::kColDP == dqc::kColDP && C::kColDQ == dqc::kColDQ,
                   "dQ compute layout");
-    dqc::dq_compute<D, F16, false>(a, sp, tmem, bar(C::kSFull), &abort_flag,
-                                   static_cast<int>(blockIdx.x), tile_step,
-                                   [&](int t) { return dq_tile(t, a, sp); });
+    dqc::dq_compute<D, F16, false, kSinks>(a, sp, tmem, bar(C::kSFull), &abort_flag,
+                                           static_cast<int>(blockIdx.x), tile_step,
+                                           [&](int t) { return dq_tile<kSinks>(t, a, sp); });
   }
 
   tc_fence_before();
@@ -301,19 +305,21 @@ __global__ void __launch_bounds__(352, 1)
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 cudaError_t launch_dq_d(const Problem& pb, const void* q, const void* k, const void* v,
                         const void* dO, const float* lse, const float* delta, void* dq,
                         cudaStream_t stream) {
   using C = DqCfg<D>;
-  CUtensorMap tq, tdo, tk, tv;
+  CUtensorMap tq, tdo, tk, tv, tks, tvs;
   const uint64_t bhq = static_cast<uint64_t>(pb.B) * pb.Hq, bhk = static_cast<uint64_t>(pb.B) * pb.Hkv;
   if (!make_tmap_3d(&tq, q, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&tdo, dO, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&tk, k, bhk, pb.span.Lk, D, kBlockN, F16) ||
-      !make_tmap_3d(&tv, v, bhk, pb.span.Lk, D, kBlockN, F16))
+      !make_tmap_3d(&tv, v, bhk, pb.span.Lk, D, kBlockN, F16) ||
+      !make_tmap_3d(&tks, k, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks) ||
+      !make_tmap_3d(&tvs, v, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_dq_kernel<D, F16>;
+  auto kern = swa_dq_kernel<D, F16, kSinks>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -326,6 +332,7 @@ cudaError_t launch_dq_d(const Problem& pb, const void* q, const void* k, const v
   a.Hkv = pb.Hkv;
   a.G = pb.Hq / pb.Hkv;
   a.span = pb.span;
+  a.sinks = pb.sinks;
   a.nqb = (pb.span.Lq + kBlockM - 1) / kBlockM;
   a.ntiles = a.nqb * a.BH;
   a.scale = pb.scale;
@@ -335,10 +342,23 @@ cudaError_t launch_dq_d(const Problem& pb, const void* q, const void* k, const v
   a.divHq = FastDiv(static_cast<uint32_t>(a.Hq));
   a.divG = FastDiv(static_cast<uint32_t>(a.G));
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk, tv, a);
+  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk, tv, tks, tvs, a);
   return cudaGetLastError();
 }
 
+}  // namespace
+
+namespace {
+template <int D>
+cudaError_t launch_dq_any(const Problem& pb, const void* q, const void* k, const void* v,
+                          const void* dO, const float* lse, const float* delta, void* dq,
+                          cudaStream_t stream) {
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_dq_d<D, true, true>(pb, q, k, v, dO, lse, delta, dq, stream)
+                  : launch_dq_d<D, false, true>(pb, q, k, v, dO, lse, delta, dq, stream);
+  return pb.f16 ? launch_dq_d<D, true, false>(pb, q, k, v, dO, lse, delta, dq, stream)
+                : launch_dq_d<D, false, false>(pb, q, k, v, dO, lse, delta, dq, stream);
+}
 }  // namespace
 
 cudaError_t launch_bwd_dq(const Problem& pb, const void* q, const void* k, const void* v,
@@ -346,12 +366,8 @@ cudaError_t launch_bwd_dq(const Problem& pb, const void* q, const void* k, const
                           cudaStream_t stream) {
   if (pb.D == 256) return launch_dq_d256(pb, q, k, v, dO, lse, delta, dq, stream);
   if (dq_pair_applies(pb)) return launch_dq_pair(pb, q, k, v, dO, lse, delta, dq, stream);
-  if (pb.D == 64)
-    return pb.f16 ? launch_dq_d<64, true>(pb, q, k, v, dO, lse, delta, dq, stream)
-                  : launch_dq_d<64, false>(pb, q, k, v, dO, lse, delta, dq, stream);
-  if (pb.D == 128)
-    return pb.f16 ? launch_dq_d<128, true>(pb, q, k, v, dO, lse, delta, dq, stream)
-                  : launch_dq_d<128, false>(pb, q, k, v, dO, lse, delta, dq, stream);
+  if (pb.D == 64) return launch_dq_any<64>(pb, q, k, v, dO, lse, delta, dq, stream);
+  if (pb.D == 128) return launch_dq_any<128>(pb, q, k, v, dO, lse, delta, dq, stream);
   return cudaErrorInvalidValue;
 }
 

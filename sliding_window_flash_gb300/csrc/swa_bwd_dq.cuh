@@ -28,10 +28,9 @@ constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 384;
 // Runs the compute warps (warps 0-7: two threads per query row, warp w on TMEM lanes 32 (w % 4)..
 // and columns [64 h, 64 h + 64), h = w / 4) over the CTA's tiles tile0, tile0 + tile_step, ..
 // < a.ntiles.  `bars` is the address of the first barrier of DqBar; `a` supplies lse, delta, dq,
-// scale, scale_log2, err and ntiles; tile_of(t) the tile's plane bh, first query q0, first key block
-// kb_lo and block count nkv.  With kPair the S-read, dS-written and dQ-read handshakes go to rank
+// scale, scale_log2, err, ntiles and sinks; tile_of(t) the tile's plane bh, first query q0 and KeyWalk.  With kPair the S-read, dS-written and dQ-read handshakes go to rank
 // 0 of the CTA pair (whose MMA warp issues for both SMs).
-template <int D, bool F16, bool kPair, typename Args, typename TileOf>
+template <int D, bool F16, bool kPair, bool kSinks, typename Args, typename TileOf>
 __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32_t tmem,
                                            uint32_t bars, volatile int* abort_flag, int tile0,
                                            int tile_step, TileOf tile_of) {
@@ -112,7 +111,7 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
     fetch_rows(t + tile_step);
     for (int j = 0; j < f.nkv; ++j) {
       const int gg = g + j;
-      const int k0 = (f.kb_lo + j) * kBlockN;
+      const int k0 = f.k0(j);
       if (!(ok = warp_wait(bar(DqBar::kSFull), gg & 1, abort_flag, a.err))) break;
       tc_fence_after();
       float p[64];
@@ -137,8 +136,10 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
         const int rel = row + sp.off - k0 - 64 * static_cast<int>(h);
         const int lo = rel - sp.dmax;
         const int hi = min(rel - sp.dmin, sp.Lk - 1 - k0 - 64 * static_cast<int>(h));
+        const int sk = a.sinks - k0 - 64 * static_cast<int>(h);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c <= hi) ? p[c] : SWA_NEG_INF;
+        for (int c = 0; c < 64; ++c)
+          p[c] = column_visible<kSinks>(c, lo, hi, sk) ? p[c] : SWA_NEG_INF;
       }
       // P = 2^(scale log2(e) S - LSE log2(e)), two scores per packed FFMA.
       {

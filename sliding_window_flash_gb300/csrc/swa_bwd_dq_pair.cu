@@ -80,19 +80,22 @@ struct DqPairArgs {
   int BHKP;  // B * Hkv * G / 2: head pairs per query block
   int Hq, Hkv, G, nqb, ntiles;
   Span span;
+  int sinks;
   float scale, scale_log2;
   unsigned* err;
   FastDiv divBHKP, divGP, divHkv;  // tile index decomposition (divGP: G / 2)
 };
 
-struct DqPairTile {
-  int bh, bhk, q0, kb_lo, nkv;
+template <bool kSinks>
+struct DqPairTile : KeyWalk<kSinks> {
+  int bh, bhk, q0;
 };
 
 // Pair tile t (heaviest query blocks first); rank r takes query head 2 p + r of the kv group.
-__device__ __forceinline__ DqPairTile dq_pair_tile(int t, const DqPairArgs& a, const Span sp,
-                                                   uint32_t rank) {
-  DqPairTile f;
+template <bool kSinks>
+__device__ __forceinline__ DqPairTile<kSinks> dq_pair_tile(int t, const DqPairArgs& a, const Span sp,
+                                                           uint32_t rank) {
+  DqPairTile<kSinks> f;
   const uint32_t tq = a.divBHKP.div(static_cast<uint32_t>(t));
   const int qb = a.nqb - 1 - static_cast<int>(tq);
   const uint32_t rem = static_cast<uint32_t>(t) - tq * static_cast<uint32_t>(a.BHKP);
@@ -102,19 +105,20 @@ __device__ __forceinline__ DqPairTile dq_pair_tile(int t, const DqPairArgs& a, c
   const int hk = f.bhk - b * a.Hkv;
   f.bh = b * a.Hq + hk * a.G + 2 * gp + static_cast<int>(rank);
   f.q0 = qb * kBlockM;
-  f.kb_lo = sp.first_kblock(f.q0);
-  f.nkv = sp.last_kblock(f.q0) - f.kb_lo + 1;
+  f.set(sp, a.sinks, f.q0);
   return f;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     swa_dq_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ CUtensorMap tm_k64,   // K, 64-row boxes
                        const __grid_constant__ CUtensorMap tm_k128,  // K, 128-row boxes
                        const __grid_constant__ CUtensorMap tm_v64,   // V, 64-row boxes
-                       const DqPairArgs a) {
+                       const __grid_constant__ CUtensorMap tm_k64s,  // the same up to the last sink
+                       const __grid_constant__ CUtensorMap tm_k128s,
+                       const __grid_constant__ CUtensorMap tm_v64s, const DqPairArgs a) {
   using C = DqPairCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -188,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
       int g = 0;
       bool ok = true;
       for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-        const DqPairTile f = dq_pair_tile(t, a, sp, rank);
+        const DqPairTile<kSinks> f = dq_pair_tile<kSinks>(t, a, sp, rank);
         // Q / dO of the previous tile are free once its last dP has been computed.
         if (it >= 1 && !mbar_wait(bar(C::kQDEmpty), (it - 1) & 1, &abort_flag, a.err)) break;
         mbar_arrive_expect_tx(bar(C::kQDFull), 2 * C::kTileBytes);
@@ -198,17 +202,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
         }
         last_qd = it;
         for (int j = 0; j < f.nkv; ++j, ++g) {
-          const int k0 = (f.kb_lo + j) * kBlockN;
+          const int k0 = f.k0(j);
+          const bool far = f.is_far(j);
           const int sk = g % C::kKStages, nk = g / C::kKStages;
           if (g >= C::kKStages &&
               !(ok = mbar_wait(bar(C::kKEmpty + sk), (nk - 1) & 1, &abort_flag, a.err)))
             break;
           mbar_arrive_expect_tx(bar(C::kKFull + sk), C::kKStageBytes);
           for (int h = 0; h < C::kChunks; ++h)
-            tma_load_3d(sKS(sk) + h * C::kHalfChunkBytes, &tm_k64, bar(C::kKFull + sk), 64 * h,
-                        k0 + C::kHalfRows * static_cast<int>(rank), f.bhk);
-          tma_load_3d(sKQ(sk), &tm_k128, bar(C::kKFull + sk), 64 * static_cast<int>(rank), k0,
-                      f.bhk);
+            tma_load_3d(sKS(sk) + h * C::kHalfChunkBytes, far ? &tm_k64s : &tm_k64,
+                        bar(C::kKFull + sk), 64 * h, k0 + C::kHalfRows * static_cast<int>(rank),
+                        f.bhk);
+          tma_load_3d(sKQ(sk), far ? &tm_k128s : &tm_k128, bar(C::kKFull + sk),
+                      64 * static_cast<int>(rank), k0, f.bhk);
           last_k[sk] = g;
         }
       }
@@ -225,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
       int g = 0;
       bool ok = true;
       for (int t = tile0; ok && t < a.ntiles; t += tile_step) {
-        const DqPairTile f = dq_pair_tile(t, a, sp, rank);
+        const DqPairTile<kSinks> f = dq_pair_tile<kSinks>(t, a, sp, rank);
         for (int j = 0; j < f.nkv; ++j, ++g) {
           const int sv = g % C::kVStages, nv = g / C::kVStages;
           if (g >= C::kVStages &&
@@ -234,8 +240,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
           const uint32_t sV = sV0 + sv * C::kHalfBytes;
           mbar_arrive_expect_tx(bar(C::kVFull + sv), C::kHalfBytes);
           for (int h = 0; h < C::kChunks; ++h)
-            tma_load_3d(sV + h * C::kHalfChunkBytes, &tm_v64, bar(C::kVFull + sv), 64 * h,
-                        (f.kb_lo + j) * kBlockN + C::kHalfRows * static_cast<int>(rank), f.bhk);
+            tma_load_3d(sV + h * C::kHalfChunkBytes, f.is_far(j) ? &tm_v64s : &tm_v64,
+                        bar(C::kVFull + sv), 64 * h,
+                        f.k0(j) + C::kHalfRows * static_cast<int>(rank), f.bhk);
           last_v[sv] = g;
         }
       }
@@ -288,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     int g = 0;
     bool ok = true;
     for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const DqPairTile f = dq_pair_tile(t, a, sp, rank);
+      const DqPairTile<kSinks> f = dq_pair_tile<kSinks>(t, a, sp, rank);
       const int n = f.nkv;
       ok = warp_wait_cluster(bar(C::kQDFull), it & 1, &abort_flag, a.err);
       if (ok) ok = issue_s(g);
@@ -323,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     int g = 0;
     bool ok = true;
     for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const DqPairTile f = dq_pair_tile(t, a, sp, rank);
+      const DqPairTile<kSinks> f = dq_pair_tile<kSinks>(t, a, sp, rank);
       ok = relay(C::kQDFull, it & 1);
       for (int j = 0; ok && j < f.nkv; ++j) ok = relay_kv(g + j);
       g += f.nkv;
@@ -337,8 +344,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
                       C::kDQEmpty - C::kSFull == dqc::DqBar::kDQEmpty && C::kColS == dqc::kColS &&
                       C::kColDP == dqc::kColDP && C::kColDQ == dqc::kColDQ,
                   "dQ compute layout");
-    dqc::dq_compute<D, F16, true>(a, sp, tmem, bar(C::kSFull), &abort_flag, tile0, tile_step,
-                                  [&](int t) { return dq_pair_tile(t, a, sp, rank); });
+    dqc::dq_compute<D, F16, true, kSinks>(
+        a, sp, tmem, bar(C::kSFull), &abort_flag, tile0, tile_step,
+        [&](int t) { return dq_pair_tile<kSinks>(t, a, sp, rank); });
   }
 
   // Every cross-CTA arrival and every pair MMA (rank 0 waited for its drain) is complete once both
@@ -351,20 +359,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 cudaError_t launch_dq_pair_d(const Problem& pb, const void* q, const void* k, const void* v,
                              const void* dO, const float* lse, const float* delta, void* dq,
                              cudaStream_t stream) {
   using C = DqPairCfg<D>;
-  CUtensorMap tq, tdo, tk64, tk128, tv64;
+  CUtensorMap tq, tdo, tk64, tk128, tv64, tk64s, tk128s, tv64s;
   const uint64_t bhq = static_cast<uint64_t>(pb.B) * pb.Hq, bhk = static_cast<uint64_t>(pb.B) * pb.Hkv;
   if (!make_tmap_3d(&tq, q, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&tdo, dO, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&tk64, k, bhk, pb.span.Lk, D, C::kHalfRows, F16) ||
       !make_tmap_3d(&tk128, k, bhk, pb.span.Lk, D, kBlockN, F16) ||
-      !make_tmap_3d(&tv64, v, bhk, pb.span.Lk, D, C::kHalfRows, F16))
+      !make_tmap_3d(&tv64, v, bhk, pb.span.Lk, D, C::kHalfRows, F16) ||
+      !make_tmap_3d(&tk64s, k, bhk, pb.span.Lk, D, C::kHalfRows, F16, pb.sinks) ||
+      !make_tmap_3d(&tk128s, k, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks) ||
+      !make_tmap_3d(&tv64s, v, bhk, pb.span.Lk, D, C::kHalfRows, F16, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_dq_pair_kernel<D, F16>;
+  auto kern = swa_dq_pair_kernel<D, F16, kSinks>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -377,6 +388,7 @@ cudaError_t launch_dq_pair_d(const Problem& pb, const void* q, const void* k, co
   a.Hq = pb.Hq;
   a.Hkv = pb.Hkv;
   a.span = pb.span;
+  a.sinks = pb.sinks;
   a.nqb = (pb.span.Lq + kBlockM - 1) / kBlockM;
   a.ntiles = a.nqb * a.BHKP;
   a.scale = pb.scale;
@@ -385,9 +397,11 @@ cudaError_t launch_dq_pair_d(const Problem& pb, const void* q, const void* k, co
   a.divBHKP = FastDiv(static_cast<uint32_t>(a.BHKP));
   a.divGP = FastDiv(static_cast<uint32_t>(a.G / 2));
   a.divHkv = FastDiv(static_cast<uint32_t>(a.Hkv));
-  const int clusters = max_pair_clusters<swa_dq_pair_kernel<D, F16>>(C::kThreads, C::kSmemBytes);
+  const int clusters =
+      max_pair_clusters<swa_dq_pair_kernel<D, F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
-  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk64, tk128, tv64, a);
+  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk64, tk128, tv64, tk64s,
+                                                              tk128s, tv64s, a);
   return cudaGetLastError();
 }
 
@@ -402,8 +416,11 @@ cudaError_t launch_dq_pair(const Problem& pb, const void* q, const void* k, cons
                            const void* dO, const float* lse, const float* delta, void* dq,
                            cudaStream_t stream) {
   if (!dq_pair_applies(pb)) return cudaErrorInvalidValue;
-  return pb.f16 ? launch_dq_pair_d<128, true>(pb, q, k, v, dO, lse, delta, dq, stream)
-                : launch_dq_pair_d<128, false>(pb, q, k, v, dO, lse, delta, dq, stream);
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_dq_pair_d<128, true, true>(pb, q, k, v, dO, lse, delta, dq, stream)
+                  : launch_dq_pair_d<128, false, true>(pb, q, k, v, dO, lse, delta, dq, stream);
+  return pb.f16 ? launch_dq_pair_d<128, true, false>(pb, q, k, v, dO, lse, delta, dq, stream)
+                : launch_dq_pair_d<128, false, false>(pb, q, k, v, dO, lse, delta, dq, stream);
 }
 
 }  // namespace swa

@@ -76,23 +76,25 @@ struct Args256 {
   int BH, Hq, Hkv, G;    // B * Hq, heads, G = Hq / Hkv
   int nqb, ntiles;       // query blocks per head, B * Hq * nqb
   Span span;
+  int sinks;
   float scale, scale_log2;  // softmax scale, scale * log2(e)
   unsigned* err;
 };
 
-struct QTile {
-  int bh, bhk, q0, kb_lo, nkv;
+template <bool kSinks>
+struct QTile : KeyWalk<kSinks> {
+  int bh, bhk, q0;
 };
 
 // Query tile t: heaviest query blocks first (a causal window gives later blocks more key blocks).
-__device__ __forceinline__ QTile qtile(int t, const Args256& a, const Span& sp) {
-  QTile f;
+template <bool kSinks>
+__device__ __forceinline__ QTile<kSinks> qtile(int t, const Args256& a, const Span& sp) {
+  QTile<kSinks> f;
   const int qb = a.nqb - 1 - t / a.BH;
   f.bh = t % a.BH;
   f.bhk = (f.bh / a.Hq) * a.Hkv + (f.bh % a.Hq) / a.G;
   f.q0 = qb * kBlockM;
-  f.kb_lo = sp.first_kblock(f.q0);
-  f.nkv = sp.last_kblock(f.q0) - f.kb_lo + 1;
+  f.set(sp, a.sinks, f.q0);
   return f;
 }
 
@@ -131,12 +133,14 @@ struct F256 {
   static constexpr int kThreads = 384;
 };
 
-template <bool F16>
+template <bool F16, bool kSinks>
 __global__ void __launch_bounds__(384, 1)
     swa_fwd256_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ CUtensorMap tm_o, const Args256 a) {
+                      const __grid_constant__ CUtensorMap tm_o,
+                      const __grid_constant__ CUtensorMap tm_ks,  // K and V up to the last sink
+                      const __grid_constant__ CUtensorMap tm_vs, const Args256 a) {
   using C = F256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -198,11 +202,12 @@ __global__ void __launch_bounds__(384, 1)
         }
       };
       for (int t = blockIdx.x; ok && t < a.ntiles; t += tile_step) {
-        const QTile f = qtile(t, a, sp);
-        put_block(&tm_k, f.kb_lo * kBlockN, f.bhk);
+        const QTile<kSinks> f = qtile<kSinks>(t, a, sp);
+        auto put_k = [&](int j) { put_block(f.is_far(j) ? &tm_ks : &tm_k, f.k0(j), f.bhk); };
+        put_k(0);
         for (int j = 0; j < f.nkv; ++j) {
-          if (j + 1 < f.nkv) put_block(&tm_k, (f.kb_lo + j + 1) * kBlockN, f.bhk);
-          put_block(&tm_v, (f.kb_lo + j) * kBlockN, f.bhk);
+          if (j + 1 < f.nkv) put_k(j + 1);
+          put_block(f.is_far(j) ? &tm_vs : &tm_v, f.k0(j), f.bhk);
         }
       }
     }
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------ Q loads, O stores
     auto load_q = [&](int t) {
-      const QTile f = qtile(t, a, sp);
+      const QTile<kSinks> f = qtile<kSinks>(t, a, sp);
       mbar_arrive_expect_tx(bar(C::kQFull), kFullBytes);
       for (int c = 0; c < 4; ++c)
         tma_load_3d(sQ + c * kChunk, &tm_q, bar(C::kQFull), 64 * c, f.q0, f.bh);
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int t = blockIdx.x, it = 0; t < a.ntiles; t += tile_step, ++it) {
       if (!warp_wait(bar(C::kOutFull), it & 1, &abort_flag, a.err)) break;
       if (lane == 0) {
-        const QTile f = qtile(t, a, sp);
+        const QTile<kSinks> f = qtile<kSinks>(t, a, sp);
         for (int c = 0; c < 4; ++c) tma_store_3d(&tm_o, sQ + c * kChunk, 64 * c, f.q0, f.bh);
         bulk_commit_group();
         bulk_wait_group_read0();  // the Q buffer may be refilled once the store has read it
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(384, 1)
     int g = 0;  // key blocks issued so far by this CTA
     bool ok = true;
     for (int t = blockIdx.x, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const QTile f = qtile(t, a, sp);
+      const QTile<kSinks> f = qtile<kSinks>(t, a, sp);
       ok = warp_wait(bar(C::kQFull), it & 1, &abort_flag, a.err);
       if (ok) ok = issue_s(g);
       for (int j = 0; ok && j < f.nkv; ++j) {
@@ -299,9 +304,9 @@ __global__ void __launch_bounds__(384, 1)
                       C::kOutFull - C::kSFull == d256::FwdBar::kOutFull,
                   "softmax barrier layout");
     const d256::FwdSoftmax cx{tmem + C::kColS, sQ,        s_red,      bar(C::kSFull),
-                              &abort_flag,     a.err,     a.scale_log2, a.lse_out};
-    d256::fwd_softmax<F16, false>(cx, sp, static_cast<int>(blockIdx.x), tile_step, a.ntiles,
-                                  [&](int t) { return qtile(t, a, sp); });
+                              &abort_flag,     a.err,     a.scale_log2, a.lse_out, a.sinks};
+    d256::fwd_softmax<F16, false, kSinks>(cx, sp, static_cast<int>(blockIdx.x), tile_step, a.ntiles,
+                                          [&](int t) { return qtile<kSinks>(t, a, sp); });
   }
 
   tc_fence_before();
@@ -350,12 +355,14 @@ struct Q256 {
   static constexpr int kThreads = 384;
 };
 
-template <bool F16>
+template <bool F16, bool kSinks>
 __global__ void __launch_bounds__(384, 1)
     swa_dq256_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const Args256 a) {
+                     const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_ks,  // K and V up to the last sink
+                     const __grid_constant__ CUtensorMap tm_vs, const Args256 a) {
   using C = Q256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -416,13 +423,15 @@ __global__ void __launch_bounds__(384, 1)
         }
       };
       for (int t = blockIdx.x; ok && t < a.ntiles; t += tile_step) {
-        const QTile f = qtile(t, a, sp);
-        put_block(&tm_k, f.kb_lo * kBlockN, f.bhk);
-        put_block(&tm_v, f.kb_lo * kBlockN, f.bhk);
+        const QTile<kSinks> f = qtile<kSinks>(t, a, sp);
+        auto put_k = [&](int j) { put_block(f.is_far(j) ? &tm_ks : &tm_k, f.k0(j), f.bhk); };
+        auto put_v = [&](int j) { put_block(f.is_far(j) ? &tm_vs : &tm_v, f.k0(j), f.bhk); };
+        put_k(0);
+        put_v(0);
         for (int j = 0; j < f.nkv; ++j) {
-          if (j + 1 < f.nkv) put_block(&tm_k, (f.kb_lo + j + 1) * kBlockN, f.bhk);
-          put_block(&tm_k, (f.kb_lo + j) * kBlockN, f.bhk);
-          if (j + 1 < f.nkv) put_block(&tm_v, (f.kb_lo + j + 1) * kBlockN, f.bhk);
+          if (j + 1 < f.nkv) put_k(j + 1);
+          put_k(j);
+          if (j + 1 < f.nkv) put_v(j + 1);
         }
       }
     }
@@ -434,7 +443,7 @@ __global__ void __launch_bounds__(384, 1)
       tma_prefetch_desc(&tm_do);
       int last = -1;
       for (int t = blockIdx.x, it = 0; t < a.ntiles; t += tile_step, ++it) {
-        const QTile f = qtile(t, a, sp);
+        const QTile<kSinks> f = qtile<kSinks>(t, a, sp);
         // Q / dO of the previous tile are free once its last S and dP have completed.
         if (it >= 1 && !mbar_wait(bar(C::kQDEmpty), (it - 1) & 1, &abort_flag, a.err)) break;
         mbar_arrive_expect_tx(bar(C::kQDFull), 2 * kFullBytes);
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(384, 1)
     int g = 0;  // key blocks issued so far by this CTA
     bool ok = true;
     for (int t = blockIdx.x, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const QTile f = qtile(t, a, sp);
+      const QTile<kSinks> f = qtile<kSinks>(t, a, sp);
       const int n = f.nkv;
       ok = warp_wait(bar(C::kQDFull), it & 1, &abort_flag, a.err);
       if (ok) ok = issue_s(g);
@@ -517,9 +526,9 @@ __global__ void __launch_bounds__(384, 1)
                       C::kDQEmpty - C::kSFull == d256::DqBar::kDQEmpty && C::kColDP == 128 &&
                       C::kColDQ == 256,
                   "dQ compute layout");
-    d256::dq_compute<F16, false>(a, sp, tmem + C::kColS, bar(C::kSFull), &abort_flag,
-                                 static_cast<int>(blockIdx.x), tile_step,
-                                 [&](int t) { return qtile(t, a, sp); });
+    d256::dq_compute<F16, false, kSinks>(a, sp, tmem + C::kColS, bar(C::kSFull), &abort_flag,
+                                         static_cast<int>(blockIdx.x), tile_step,
+                                         [&](int t) { return qtile<kSinks>(t, a, sp); });
   }
 
   tc_fence_before();
@@ -547,6 +556,7 @@ Args256 make_args(const Problem& pb, const float* lse, const float* delta, void*
   a.nqb = (pb.span.Lq + kBlockM - 1) / kBlockM;
   a.ntiles = a.nqb * a.BH;
   a.span = pb.span;
+  a.sinks = pb.sinks;
   a.scale = pb.scale;
   a.scale_log2 = pb.scale * kLog2e;
   a.err = pb.err;
@@ -557,8 +567,9 @@ Args256 make_args(const Problem& pb, const float* lse, const float* delta, void*
 bool qmap(CUtensorMap* m, const void* p, const Problem& pb) {
   return make_tmap_3d(m, p, static_cast<uint64_t>(pb.B) * pb.Hq, pb.span.Lq, kD, kBlockM, pb.f16);
 }
-bool kmap(CUtensorMap* m, const void* p, const Problem& pb) {
-  return make_tmap_3d(m, p, static_cast<uint64_t>(pb.B) * pb.Hkv, pb.span.Lk, kD, kBlockN, pb.f16);
+bool kmap(CUtensorMap* m, const void* p, const Problem& pb, int seen = 0) {
+  return make_tmap_3d(m, p, static_cast<uint64_t>(pb.B) * pb.Hkv, pb.span.Lk, kD, kBlockN, pb.f16,
+                      seen);
 }
 
 template <typename Kern>
@@ -566,33 +577,35 @@ cudaError_t set_smem(Kern kern, int bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <bool F16>
+template <bool F16, bool kSinks>
 cudaError_t fwd256(const Problem& pb, const void* q, const void* k, const void* v, void* o,
                    float* lse, cudaStream_t stream) {
-  CUtensorMap tq, tk, tv, to;
-  if (!qmap(&tq, q, pb) || !qmap(&to, o, pb) || !kmap(&tk, k, pb) || !kmap(&tv, v, pb))
+  CUtensorMap tq, tk, tv, to, tks, tvs;
+  if (!qmap(&tq, q, pb) || !qmap(&to, o, pb) || !kmap(&tk, k, pb) || !kmap(&tv, v, pb) ||
+      !kmap(&tks, k, pb, pb.sinks) || !kmap(&tvs, v, pb, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_fwd256_kernel<F16>;
+  auto kern = swa_fwd256_kernel<F16, kSinks>;
   cudaError_t e = set_smem(kern, F256::kSmemBytes);
   if (e != cudaSuccess) return e;
   const Args256 a = make_args(pb, nullptr, nullptr, nullptr, lse);
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
-  kern<<<grid, F256::kThreads, F256::kSmemBytes, stream>>>(tq, tk, tv, to, a);
+  kern<<<grid, F256::kThreads, F256::kSmemBytes, stream>>>(tq, tk, tv, to, tks, tvs, a);
   return cudaGetLastError();
 }
 
-template <bool F16>
+template <bool F16, bool kSinks>
 cudaError_t dq256(const Problem& pb, const void* q, const void* k, const void* v, const void* dO,
                   const float* lse, const float* delta, void* dq, cudaStream_t stream) {
-  CUtensorMap tq, tdo, tk, tv;
-  if (!qmap(&tq, q, pb) || !qmap(&tdo, dO, pb) || !kmap(&tk, k, pb) || !kmap(&tv, v, pb))
+  CUtensorMap tq, tdo, tk, tv, tks, tvs;
+  if (!qmap(&tq, q, pb) || !qmap(&tdo, dO, pb) || !kmap(&tk, k, pb) || !kmap(&tv, v, pb) ||
+      !kmap(&tks, k, pb, pb.sinks) || !kmap(&tvs, v, pb, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_dq256_kernel<F16>;
+  auto kern = swa_dq256_kernel<F16, kSinks>;
   cudaError_t e = set_smem(kern, Q256::kSmemBytes);
   if (e != cudaSuccess) return e;
   const Args256 a = make_args(pb, lse, delta, dq);
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
-  kern<<<grid, Q256::kThreads, Q256::kSmemBytes, stream>>>(tq, tdo, tk, tv, a);
+  kern<<<grid, Q256::kThreads, Q256::kSmemBytes, stream>>>(tq, tdo, tk, tv, tks, tvs, a);
   return cudaGetLastError();
 }
 
@@ -601,16 +614,22 @@ cudaError_t dq256(const Problem& pb, const void* q, const void* k, const void* v
 cudaError_t launch_fwd_d256(const Problem& pb, const void* q, const void* k, const void* v,
                             void* o, float* lse, cudaStream_t stream) {
   if (fwd256_pair_applies(pb)) return launch_fwd256_pair(pb, q, k, v, o, lse, stream);
-  return pb.f16 ? fwd256<true>(pb, q, k, v, o, lse, stream)
-                : fwd256<false>(pb, q, k, v, o, lse, stream);
+  if (pb.sinks > 0)
+    return pb.f16 ? fwd256<true, true>(pb, q, k, v, o, lse, stream)
+                  : fwd256<false, true>(pb, q, k, v, o, lse, stream);
+  return pb.f16 ? fwd256<true, false>(pb, q, k, v, o, lse, stream)
+                : fwd256<false, false>(pb, q, k, v, o, lse, stream);
 }
 
 cudaError_t launch_dq_d256(const Problem& pb, const void* q, const void* k, const void* v,
                            const void* dO, const float* lse, const float* delta, void* dq,
                            cudaStream_t stream) {
   if (dq256_pair_applies(pb)) return launch_dq256_pair(pb, q, k, v, dO, lse, delta, dq, stream);
-  return pb.f16 ? dq256<true>(pb, q, k, v, dO, lse, delta, dq, stream)
-                : dq256<false>(pb, q, k, v, dO, lse, delta, dq, stream);
+  if (pb.sinks > 0)
+    return pb.f16 ? dq256<true, true>(pb, q, k, v, dO, lse, delta, dq, stream)
+                  : dq256<false, true>(pb, q, k, v, dO, lse, delta, dq, stream);
+  return pb.f16 ? dq256<true, false>(pb, q, k, v, dO, lse, delta, dq, stream)
+                : dq256<false, false>(pb, q, k, v, dO, lse, delta, dq, stream);
 }
 
 cudaError_t launch_dkdv_d256(const Problem& pb, const void* q, const void* k, const void* v,

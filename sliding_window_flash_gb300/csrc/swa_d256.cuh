@@ -33,10 +33,12 @@ __device__ __forceinline__ void drain_ring(const int (&last)[kSlots], int* s_las
   }
 }
 
-// Column mask of one half-row of scores: keeps columns [lo, hi] of 64, sets the rest to `fill`.
-__device__ __forceinline__ void mask64(float (&x)[64], int lo, int hi, float fill) {
+// Column mask of one half-row of scores: keeps columns [lo, hi] of 64 (with kSinks also those below
+// `sk` up to hi), sets the rest to `fill`.
+template <bool kSinks = false>
+__device__ __forceinline__ void mask64(float (&x)[64], int lo, int hi, float fill, int sk = 0) {
 #pragma unroll
-  for (int c = 0; c < 64; ++c) x[c] = (c >= lo && c <= hi) ? x[c] : fill;
+  for (int c = 0; c < 64; ++c) x[c] = column_visible<kSinks>(c, lo, hi, sk) ? x[c] : fill;
 }
 
 // P^T = 2^(scale log2(e) S^T - LSE log2(e)) for this thread's 64 query columns, from the S^T
@@ -159,6 +161,7 @@ struct FwdSoftmax {
   unsigned* err;
   float scale_log2;
   float* lse;
+  int sinks;
 };
 struct FwdBar {
   static constexpr int kSFull = 0;    // 2: S of block g landed in buffer g & 1
@@ -170,10 +173,9 @@ struct FwdBar {
 };
 
 // Runs the softmax warps over the CTA's tiles tile0, tile0 + tile_step, .. < ntiles, with the
-// addresses in cx; tile_of(t) gives the tile's plane bh, first query q0, first key block kb_lo and
-// block count nkv.  With kPair the P-written and O-read handshakes go to rank 0 of the CTA pair
+// addresses in cx; tile_of(t) gives the tile's plane bh, first query q0 and KeyWalk.  With kPair the P-written and O-read handshakes go to rank 0 of the CTA pair
 // (whose MMA warp issues for both SMs).
-template <bool F16, bool kPair, typename TileOf>
+template <bool F16, bool kPair, bool kSinks, typename TileOf>
 __device__ __forceinline__ void fwd_softmax(const FwdSoftmax& cx, const Span& sp, int tile0,
                                             int tile_step, int ntiles, TileOf tile_of) {
   const uint32_t warp = warp_id(), lane = lane_id();
@@ -214,7 +216,7 @@ __device__ __forceinline__ void fwd_softmax(const FwdSoftmax& cx, const Span& sp
     float l = 0.f;              // partial row sum over this thread's half of the columns
     for (int j = 0; j < f.nkv; ++j) {
       const int gg = g + j;
-      const int k0 = (f.kb_lo + j) * kBlockN;
+      const int k0 = f.k0(j);
       const int sb = gg & 1;
       if (!(ok = warp_wait(bar(FwdBar::kSFull + sb), (gg >> 1) & 1, cx.abort_flag, cx.err))) break;
       tc_fence_after();
@@ -233,8 +235,9 @@ __device__ __forceinline__ void fwd_softmax(const FwdSoftmax& cx, const Span& sp
       if (!sp.interior(q0, k0)) {
         // Columns c (keys k0 + 64h + c) visible to row `row`, and inside the key sequence.
         const int rel = row + sp.off - k0 - 64 * static_cast<int>(h);
-        mask64(x, rel - sp.dmax, min(rel - sp.dmin, sp.Lk - 1 - k0 - 64 * static_cast<int>(h)),
-               SWA_NEG_INF);
+        mask64<kSinks>(x, rel - sp.dmax,
+                       min(rel - sp.dmin, sp.Lk - 1 - k0 - 64 * static_cast<int>(h)), SWA_NEG_INF,
+                       cx.sinks - k0 - 64 * static_cast<int>(h));
       }
       uint32_t pk[32];
       auto exponentiate = [&](float m) -> float {
@@ -363,9 +366,9 @@ struct DqBar {
 
 // Runs the compute warps over the CTA's tiles tile0, tile0 + tile_step, .. < a.ntiles.  TMEM: S at
 // tmem + 0, dP / dS at + 128, dQ at + 256; `bars` is the address of the first of the six
-// consecutive barriers of DqBar.  `a` supplies lse, delta, dq, scale, scale_log2, err and ntiles;
-// tile_of(t) the tile's plane bh, first query q0, first key block kb_lo and block count nkv.
-template <bool F16, bool kPair, typename Args, typename TileOf>
+// consecutive barriers of DqBar.  `a` supplies lse, delta, dq, scale, scale_log2, err, ntiles and
+// sinks; tile_of(t) the tile's plane bh, first query q0 and KeyWalk.
+template <bool F16, bool kPair, bool kSinks, typename Args, typename TileOf>
 __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32_t tmem,
                                            uint32_t bars, volatile int* abort_flag, int tile0,
                                            int tile_step, TileOf tile_of) {
@@ -412,7 +415,7 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
     fetch_rows(t + tile_step);
     for (int j = 0; j < f.nkv; ++j) {
       const int gg = g + j;
-      const int k0 = (f.kb_lo + j) * kBlockN;
+      const int k0 = f.k0(j);
       if (!(ok = warp_wait(bar(DqBar::kSFull), gg & 1, abort_flag, a.err))) break;
       tc_fence_after();
       float p[64];
@@ -429,8 +432,9 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
       arrive(bar(DqBar::kSEmpty));
       if (!sp.interior(q0, k0)) {
         const int rel = row + sp.off - k0 - 64 * static_cast<int>(h);
-        mask64(p, rel - sp.dmax, min(rel - sp.dmin, sp.Lk - 1 - k0 - 64 * static_cast<int>(h)),
-               SWA_NEG_INF);
+        mask64<kSinks>(p, rel - sp.dmax,
+                       min(rel - sp.dmin, sp.Lk - 1 - k0 - 64 * static_cast<int>(h)), SWA_NEG_INF,
+                       a.sinks - k0 - 64 * static_cast<int>(h));
       }
       {
         const float2 scale2 = make_float2(sl2, sl2), neg_l2 = make_float2(-lse2, -lse2);

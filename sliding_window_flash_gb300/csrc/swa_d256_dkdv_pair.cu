@@ -15,6 +15,9 @@
 // Each SM thus moves half the query-side bytes the single-CTA kernels move per query block, and
 // its MMAs read half their B operand from shared memory.
 //
+// With sinks (kSinks) the first clusters of the grid each walk a part of all query tiles behind two
+// blocks of sinks and leave fp32 sums of their rows (SinkPlan); a second kernel joins them.
+//
 // Warp roles (352 threads per CTA): warps 0-7 compute (as swa_d256.cu: warp w owns key rows
 // 32 (w % 4).. and query columns [64 h, 64 h + 64), h = w / 4; the arrivals that let rank 0 issue
 // an MMA reading their output go to rank 0's barriers, 16 arrivals); warps 8 and 10 load this
@@ -49,21 +52,41 @@ struct PairArgs {
   uint16_t* dv;
   int Hq, Hkv, G, BHK;  // BHK = B * Hkv
   Span span;
+  int sinks, sink_pairs, splits;
+  float* part;
   float scale, scale_log2;
   unsigned* err;
 };
 
 // The pair's walk: G query heads x the union [qb_lo, qb_lo + nq) of the two key blocks' query
-// blocks; tile t = g nq + (query block - qb_lo).  Own-block fields describe this CTA's keys.
+// blocks; tile t = g nq + (query block - qb_lo), from t0 on, T of them.  Own-block fields describe this
+// CTA's keys.
 struct PairWalk {
-  int bhk, b, hk, k0, qb_lo, nq, T;
+  int bhk, b, hk, k0, qb_lo, nq, t0, T;
+  int dmax;                  // the window's far side for these keys
+  bool sink;                 // a part of a walk over sinks
+  int split;
   bool valid;                // this CTA's key block starts inside the key sequence
   int q_int_lo, q_int_hi;    // query tiles q0 in [q_int_lo, q_int_hi] need no mask for own keys
 };
 
-__device__ __forceinline__ PairWalk pair_walk(const PairArgs& a, const Span& sp, uint32_t rank) {
+template <bool kSinks>
+__device__ __forceinline__ PairWalk pair_walk(const PairArgs& a, Span sp, uint32_t rank) {
   PairWalk w;
-  const int c = static_cast<int>(blockIdx.x >> 1);
+  int c = static_cast<int>(blockIdx.x >> 1);
+  w.sink = false;
+  w.split = 0;
+  if constexpr (kSinks) {
+    w.sink = c < a.sink_pairs;
+    if (w.sink) {
+      sp.dmax = sp.Lk - 1;
+      w.split = c % a.splits;
+      c /= a.splits;
+    } else {
+      c -= a.sink_pairs;
+    }
+  }
+  w.dmax = sp.dmax;
   const int kp = c / a.BHK;
   w.bhk = c - kp * a.BHK;
   w.b = w.bhk / a.Hkv;
@@ -81,7 +104,14 @@ __device__ __forceinline__ PairWalk pair_walk(const PairArgs& a, const Span& sp,
   }
   w.qb_lo = lo;
   w.nq = any ? hi - lo + 1 : 0;
+  w.t0 = 0;
   w.T = a.G * w.nq;
+  if constexpr (kSinks) {
+    if (w.sink) {
+      w.t0 = static_cast<int>(static_cast<long long>(w.T) * w.split / a.splits);
+      w.T = static_cast<int>(static_cast<long long>(w.T) * (w.split + 1) / a.splits) - w.t0;
+    }
+  }
   w.k0 = (2 * kp + static_cast<int>(rank)) * kBlockN;
   w.valid = w.k0 < sp.Lk;
   w.q_int_lo = w.k0 + kBlockN - 1 + sp.dmin - sp.off;
@@ -93,10 +123,44 @@ __device__ __forceinline__ PairWalk pair_walk(const PairArgs& a, const Span& sp,
 
 // Query position and (batch, query head) plane of walk tile t.
 __device__ __forceinline__ int pw_q0(const PairWalk& w, int t) {
-  return (w.qb_lo + t % w.nq) * kBlockM;
+  return (w.qb_lo + (w.t0 + t) % w.nq) * kBlockM;
 }
 __device__ __forceinline__ int pw_bhq(const PairWalk& w, const PairArgs& a, int t) {
-  return w.b * a.Hq + w.hk * a.G + t / w.nq;
+  return w.b * a.Hq + w.hk * a.G + (w.t0 + t) / w.nq;
+}
+
+// What a cluster without tiles has to write for its keys (`which`: 0 dK, 1 dV): zeros, in a sinks'
+// part (more parts than tiles) or in the gradient.
+template <bool kSinks>
+__device__ __forceinline__ void zero_keys(const PairArgs& a, const PairWalk& w, const Span& sp,
+                                          int which) {
+  if constexpr (kSinks) {
+    if (w.sink) {
+      const int n = min(kBlockN, a.sinks - w.k0) * kD;
+      for (int i = static_cast<int>(threadIdx.x); i < n; i += static_cast<int>(blockDim.x))
+        a.part[sink_part_offset(w.split, a.BHK, w.bhk, which, a.sinks, w.k0, kD) + i] = 0.f;
+      return;
+    }
+  }
+  zero_key_rows(which == 0 ? a.dk : a.dv, nullptr, w.bhk, w.k0, sp.Lk, kD);
+}
+
+// The fp32 sums of a sinks' part: this thread's half of row `key` of the accumulator.
+__device__ __forceinline__ void sink_epilogue(const PairArgs& a, const PairWalk& w, uint32_t acc,
+                                              int key, uint32_t h, int which) {
+  float* dst = a.part + sink_part_offset(w.split, a.BHK, w.bhk, which, a.sinks, key, kD) + 128 * h;
+#pragma unroll
+  for (int c4 = 0; c4 < 4; ++c4) {
+    uint32_t rr[32];
+    tmem_ld32(acc + 128u * h + 32u * c4, rr);
+    tmem_wait_ld(rr);
+    if (key < a.sinks) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<uint4*>(dst + 32 * c4 + i) =
+            make_uint4(rr[i], rr[i + 1], rr[i + 2], rr[i + 3]);
+    }
+  }
 }
 
 // Ring item kinds: query half of Q (B of S^T), query half of dO (B of dP^T), head-dim half of
@@ -146,7 +210,7 @@ struct VP {
   static constexpr int kThreads = 352;
 };
 
-template <bool F16>
+template <bool F16, bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     swa_dv256_pair_kernel(const __grid_constant__ CUtensorMap tm_q64,
                           const __grid_constant__ CUtensorMap tm_do128,
@@ -158,9 +222,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   const Span sp = a.span;
   const uint32_t rank = cluster_rank();
   const bool lead = rank == 0u;
-  const PairWalk w = pair_walk(a, sp, rank);
+  const PairWalk w = pair_walk<kSinks>(a, sp, rank);
+  if constexpr (kSinks)  // the join writes all rows of both blocks (both CTAs return here)
+    if (!w.sink && w.k0 - kBlockN * static_cast<int>(rank) + 2 * kBlockN <= a.sinks) return;
   if (w.T == 0) {  // neither key block is seen by any query (both CTAs return here)
-    zero_key_rows(a.dv, nullptr, w.bhk, w.k0, sp.Lk, kD);
+    zero_keys<kSinks>(a, w, sp, 1);
     return;
   }
   const bool smem_ok = (smem_u32(smem) & 1023u) == 0u;
@@ -302,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     const int r = static_cast<int>(threadIdx.x & 127);  // key row within the block = TMEM lane
     const uint32_t h = warp >> 2;
     const int key = w.k0 + r;
-    const int vis_lo = key + sp.dmin - sp.off, vis_hi = key + sp.dmax - sp.off;
+    const int vis_lo = key + sp.dmin - sp.off, vis_hi = key + w.dmax - sp.off;
     const uint32_t lane_base = ((warp & 3u) * 32u) << 16;
     float nxt = 0.f;  // LSE of query q0(t) + r, fetched a tile ahead (h = 0 threads)
     auto fetch_row = [&](int t) {
@@ -337,7 +403,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     if (ok && warp_wait(bar(C::kDone), 0, &abort_flag, a.err) && w.valid) {
       tc_fence_after();
       // dV -> 16-bit, staged in the K buffer (every MMA of the pair has completed).
-      key_epilogue<F16>(tmem + lane_base + C::kColAcc, sK, r, h, 1.f, false, bar(C::kOutFull),
+      if (kSinks && w.sink)
+        sink_epilogue(a, w, tmem + lane_base + C::kColAcc, key, h, 1);
+      else
+        key_epilogue<F16>(tmem + lane_base + C::kColAcc, sK, r, h, 1.f, false, bar(C::kOutFull),
                         &tm_dv, w.k0, w.bhk, &abort_flag, a.err);
     }
   }
@@ -384,7 +453,7 @@ struct KP {
   static constexpr int kThreads = 352;
 };
 
-template <bool F16>
+template <bool F16, bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     swa_dk256_pair_kernel(const __grid_constant__ CUtensorMap tm_q64,
                           const __grid_constant__ CUtensorMap tm_do64,
@@ -398,9 +467,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   const Span sp = a.span;
   const uint32_t rank = cluster_rank();
   const bool lead = rank == 0u;
-  const PairWalk w = pair_walk(a, sp, rank);
+  const PairWalk w = pair_walk<kSinks>(a, sp, rank);
+  if constexpr (kSinks)  // the join writes all rows of both blocks (both CTAs return here)
+    if (!w.sink && w.k0 - kBlockN * static_cast<int>(rank) + 2 * kBlockN <= a.sinks) return;
   if (w.T == 0) {  // neither key block is seen by any query (both CTAs return here)
-    zero_key_rows(a.dk, nullptr, w.bhk, w.k0, sp.Lk, kD);
+    zero_keys<kSinks>(a, w, sp, 0);
     return;
   }
   const bool smem_ok = (smem_u32(smem) & 1023u) == 0u;
@@ -556,7 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     const int r = static_cast<int>(threadIdx.x & 127);
     const uint32_t h = warp >> 2;
     const int key = w.k0 + r;
-    const int vis_lo = key + sp.dmin - sp.off, vis_hi = key + sp.dmax - sp.off;
+    const int vis_lo = key + sp.dmin - sp.off, vis_hi = key + w.dmax - sp.off;
     const uint32_t lane_base = ((warp & 3u) * 32u) << 16;
     // h = 0 threads fetch LSE, h = 1 threads Delta, of query q0(t) + r, a tile ahead.
     float nxt = 0.f;
@@ -599,7 +670,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     if (ok && warp_wait(bar(C::kDone), 0, &abort_flag, a.err) && w.valid) {
       tc_fence_after();
       // dK * scale -> 16-bit, staged in the K buffer (every MMA of the pair has completed).
-      key_epilogue<F16>(tmem + lane_base + C::kColAcc, sK, r, h, a.scale, false, bar(C::kOutFull),
+      if (kSinks && w.sink)
+        sink_epilogue(a, w, tmem + lane_base + C::kColAcc, key, h, 0);
+      else
+        key_epilogue<F16>(tmem + lane_base + C::kColAcc, sK, r, h, a.scale, false, bar(C::kOutFull),
                         &tm_dk, w.k0, w.bhk, &abort_flag, a.err);
     }
   }
@@ -612,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   }
 }
 
-template <bool F16>
+template <bool F16, bool kSinks>
 cudaError_t launch_t(const Problem& pb, const void* q, const void* k, const void* v,
                      const void* dO, const float* lse, const float* delta, void* dk, void* dv,
                      cudaStream_t stream) {
@@ -643,18 +717,29 @@ cudaError_t launch_t(const Problem& pb, const void* q, const void* k, const void
   a.scale_log2 = pb.scale * kLog2e;
   a.err = pb.err;
   const int nkb = (Lk + kBlockN - 1) / kBlockN;
-  const unsigned grid = 2u * static_cast<unsigned>((nkb + 1) / 2) * static_cast<unsigned>(a.BHK);
-  auto kk = swa_dk256_pair_kernel<F16>;
+  a.sinks = pb.sinks;
+  a.part = pb.sink_part;
+  a.splits = 1;
+  a.sink_pairs = 0;
+  if (kSinks) {
+    const SinkPlan p = sink_plan(pb);
+    a.splits = p.splits;
+    a.sink_pairs = p.blocks * a.BHK * p.splits;
+  }
+  const unsigned grid = 2u * (static_cast<unsigned>((nkb + 1) / 2) * static_cast<unsigned>(a.BHK) +
+                              static_cast<unsigned>(a.sink_pairs));
+  auto kk = swa_dk256_pair_kernel<F16, kSinks>;
   cudaError_t e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        KP::kSmemBytes);
   if (e != cudaSuccess) return e;
   kk<<<grid, KP::kThreads, KP::kSmemBytes, stream>>>(tq64, tdo64, tq128, tk, tv, tdk, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  auto kv = swa_dv256_pair_kernel<F16>;
+  auto kv = swa_dv256_pair_kernel<F16, kSinks>;
   e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, VP::kSmemBytes);
   if (e != cudaSuccess) return e;
   kv<<<grid, VP::kThreads, VP::kSmemBytes, stream>>>(tq64, tdo128, tk, tdv, a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e != cudaSuccess || !kSinks ? e : launch_sink_join(pb, a.splits, dk, dv, stream);
 }
 
 }  // namespace
@@ -665,8 +750,11 @@ cudaError_t launch_dkdv256_pair(const Problem& pb, const void* q, const void* k,
                                 const void* dO, const float* lse, const float* delta, void* dk,
                                 void* dv, cudaStream_t stream) {
   if (!dkdv256_pair_applies(pb)) return cudaErrorInvalidValue;
-  return pb.f16 ? launch_t<true>(pb, q, k, v, dO, lse, delta, dk, dv, stream)
-                : launch_t<false>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_t<true, true>(pb, q, k, v, dO, lse, delta, dk, dv, stream)
+                  : launch_t<false, true>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
+  return pb.f16 ? launch_t<true, false>(pb, q, k, v, dO, lse, delta, dk, dv, stream)
+                : launch_t<false, false>(pb, q, k, v, dO, lse, delta, dk, dv, stream);
 }
 
 }  // namespace swa

@@ -71,19 +71,22 @@ struct DqP256Args {
   int BHKP;  // B * Hkv * G / 2: head pairs per query block
   int Hq, Hkv, G, nqb, ntiles;
   Span span;
+  int sinks;
   float scale, scale_log2;
   unsigned* err;
   FastDiv divBHKP, divGP, divHkv;  // tile index decomposition (divGP: G / 2)
 };
 
-struct DqP256Tile {
-  int bh, bhk, q0, kb_lo, nkv;
+template <bool kSinks>
+struct DqP256Tile : KeyWalk<kSinks> {
+  int bh, bhk, q0;
 };
 
 // Pair tile t (heaviest query blocks first); rank r takes query head 2 p + r of the kv group.
-__device__ __forceinline__ DqP256Tile dqp256_tile(int t, const DqP256Args& a, const Span sp,
-                                                  uint32_t rank) {
-  DqP256Tile f;
+template <bool kSinks>
+__device__ __forceinline__ DqP256Tile<kSinks> dqp256_tile(int t, const DqP256Args& a, const Span sp,
+                                                          uint32_t rank) {
+  DqP256Tile<kSinks> f;
   const uint32_t tq = a.divBHKP.div(static_cast<uint32_t>(t));
   const int qb = a.nqb - 1 - static_cast<int>(tq);
   const uint32_t rem = static_cast<uint32_t>(t) - tq * static_cast<uint32_t>(a.BHKP);
@@ -93,22 +96,23 @@ __device__ __forceinline__ DqP256Tile dqp256_tile(int t, const DqP256Args& a, co
   const int hk = f.bhk - b * a.Hkv;
   f.bh = b * a.Hq + hk * a.G + 2 * gp + static_cast<int>(rank);
   f.q0 = qb * kBlockM;
-  f.kb_lo = sp.first_kblock(f.q0);
-  f.nkv = sp.last_kblock(f.q0) - f.kb_lo + 1;
+  f.set(sp, a.sinks, f.q0);
   return f;
 }
 
 // Ring item kinds: key half of K or V (four 64 x 64 boxes), head-dim half of K (two 128 x 64).
 enum ItemKind : int { kKH = 0, kVH = 1, kKC = 2 };
 
-template <bool F16>
+template <bool F16, bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     swa_dq256_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_do,
                           const __grid_constant__ CUtensorMap tm_k64,   // K, 64-row boxes
                           const __grid_constant__ CUtensorMap tm_v64,   // V, 64-row boxes
                           const __grid_constant__ CUtensorMap tm_k128,  // K, 128-row boxes
-                          const DqP256Args a) {
+                          const __grid_constant__ CUtensorMap tm_k64s,  // the same up to the last
+                          const __grid_constant__ CUtensorMap tm_v64s,  // sink
+                          const __grid_constant__ CUtensorMap tm_k128s, const DqP256Args a) {
   using C = DqP256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -162,20 +166,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Walks this CTA's ring items in consumption order: on_item(index, kind, key block start,
-  // kv plane); on_tile(tile iteration) before each tile's first item.
+  // Walks this CTA's ring items in consumption order: on_item(index, kind, key block start, kv
+  // plane, block of far sinks); on_tile(tile iteration) before each tile's first item.
   auto walk_items = [&](auto&& on_tile, auto&& on_item) -> bool {
     int i = 0;
     for (int t = tile0, it = 0; t < a.ntiles; t += tile_step, ++it) {
-      const DqP256Tile f = dqp256_tile(t, a, sp, rank);
+      const DqP256Tile<kSinks> f = dqp256_tile<kSinks>(t, a, sp, rank);
       if (!on_tile(it)) return false;
-      const int kb = f.kb_lo * kBlockN;
-      if (!on_item(i++, kKH, kb, f.bhk) || !on_item(i++, kVH, kb, f.bhk)) return false;
+      auto item = [&](int kind, int j) { return on_item(i++, kind, f.k0(j), f.bhk, f.is_far(j)); };
+      if (!item(kKH, 0) || !item(kVH, 0)) return false;
       for (int j = 0; j < f.nkv; ++j) {
-        const int k0 = (f.kb_lo + j) * kBlockN;
-        if (j + 1 < f.nkv && !on_item(i++, kKH, k0 + kBlockN, f.bhk)) return false;
-        if (!on_item(i++, kKC, k0, f.bhk)) return false;
-        if (j + 1 < f.nkv && !on_item(i++, kVH, k0 + kBlockN, f.bhk)) return false;
+        if (j + 1 < f.nkv && !item(kKH, j + 1)) return false;
+        if (!item(kKC, j)) return false;
+        if (j + 1 < f.nkv && !item(kVH, j + 1)) return false;
       }
     }
     return true;
@@ -193,7 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       tma_prefetch_desc(&tm_v64);
       tma_prefetch_desc(&tm_k128);
       walk_items([&](int) { return true; },
-                 [&](int i, int kind, int k0, int bhk) -> bool {
+                 [&](int i, int kind, int k0, int bhk, bool far) -> bool {
                    if ((i & 1) != p) return true;
                    if (i >= C::kSlots &&
                        !mbar_wait(empty(i), ((i / C::kSlots) - 1) & 1, &abort_flag, a.err))
@@ -202,10 +205,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                    mbar_arrive_expect_tx(full(i), C::kItemBytes);
                    if (kind == kKC) {
                      for (int c = 0; c < 2; ++c)
-                       tma_load_3d(dst + c * C::kChunk, &tm_k128, full(i),
+                       tma_load_3d(dst + c * C::kChunk, far ? &tm_k128s : &tm_k128, full(i),
                                    128 * static_cast<int>(rank) + 64 * c, k0, bhk);
                    } else {
-                     const CUtensorMap* m = kind == kKH ? &tm_k64 : &tm_v64;
+                     const CUtensorMap* m = kind == kKH ? (far ? &tm_k64s : &tm_k64)
+                                                        : (far ? &tm_v64s : &tm_v64);
                      for (int c = 0; c < 4; ++c)
                        tma_load_3d(dst + c * C::kHalfChunk, m, full(i), 64 * c,
                                    k0 + C::kHalfRows * static_cast<int>(rank), bhk);
@@ -222,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       tma_prefetch_desc(&tm_do);
       int last = -1;
       for (int t = tile0, it = 0; t < a.ntiles; t += tile_step, ++it) {
-        const DqP256Tile f = dqp256_tile(t, a, sp, rank);
+        const DqP256Tile<kSinks> f = dqp256_tile<kSinks>(t, a, sp, rank);
         // Q / dO of the previous tile are free once its last S and dP have completed.
         if (it >= 1 && !mbar_wait(bar(C::kQDEmpty), (it - 1) & 1, &abort_flag, a.err)) break;
         mbar_arrive_expect_tx(bar(C::kQDFull), 2 * C::kTileBytes);
@@ -281,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     int g = 0;  // key blocks issued so far by this CTA
     bool ok = true;
     for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const DqP256Tile f = dqp256_tile(t, a, sp, rank);
+      const DqP256Tile<kSinks> f = dqp256_tile<kSinks>(t, a, sp, rank);
       const int n = f.nkv;
       ok = warp_wait_cluster(bar(C::kQDFull), it & 1, &abort_flag, a.err);
       if (ok) ok = issue_s(g);
@@ -307,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       return true;
     };
     walk_items([&](int it) { return relay(bar(C::kQDFull), static_cast<uint32_t>(it & 1)); },
-               [&](int i, int, int, int) { return relay(full(i), parity(i)); });
+               [&](int i, int, int, int, bool) { return relay(full(i), parity(i)); });
   } else {
     // ------------------------------------------------------------ compute (warps 0-7)
     static_assert(C::kSEmpty - C::kSFull == d256::DqBar::kSEmpty &&
@@ -317,8 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                       C::kDQEmpty - C::kSFull == d256::DqBar::kDQEmpty && C::kColDP == 128 &&
                       C::kColDQ == 256,
                   "dQ compute layout");
-    d256::dq_compute<F16, true>(a, sp, tmem + C::kColS, bar(C::kSFull), &abort_flag, tile0,
-                                tile_step, [&](int t) { return dqp256_tile(t, a, sp, rank); });
+    d256::dq_compute<F16, true, kSinks>(
+        a, sp, tmem + C::kColS, bar(C::kSFull), &abort_flag, tile0, tile_step,
+        [&](int t) { return dqp256_tile<kSinks>(t, a, sp, rank); });
   }
 
   // Every cross-CTA arrival and every pair MMA (rank 0 waited for its drain) is complete once both
@@ -331,20 +336,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   }
 }
 
-template <bool F16>
+template <bool F16, bool kSinks>
 cudaError_t launch_dq256_pair_t(const Problem& pb, const void* q, const void* k, const void* v,
                                 const void* dO, const float* lse, const float* delta, void* dq,
                                 cudaStream_t stream) {
   using C = DqP256;
-  CUtensorMap tq, tdo, tk64, tv64, tk128;
+  CUtensorMap tq, tdo, tk64, tv64, tk128, tk64s, tv64s, tk128s;
   const uint64_t bhq = static_cast<uint64_t>(pb.B) * pb.Hq, bhk = static_cast<uint64_t>(pb.B) * pb.Hkv;
   if (!make_tmap_3d(&tq, q, bhq, pb.span.Lq, C::kD, kBlockM, F16) ||
       !make_tmap_3d(&tdo, dO, bhq, pb.span.Lq, C::kD, kBlockM, F16) ||
       !make_tmap_3d(&tk64, k, bhk, pb.span.Lk, C::kD, C::kHalfRows, F16) ||
       !make_tmap_3d(&tv64, v, bhk, pb.span.Lk, C::kD, C::kHalfRows, F16) ||
-      !make_tmap_3d(&tk128, k, bhk, pb.span.Lk, C::kD, kBlockN, F16))
+      !make_tmap_3d(&tk128, k, bhk, pb.span.Lk, C::kD, kBlockN, F16) ||
+      !make_tmap_3d(&tk64s, k, bhk, pb.span.Lk, C::kD, C::kHalfRows, F16, pb.sinks) ||
+      !make_tmap_3d(&tv64s, v, bhk, pb.span.Lk, C::kD, C::kHalfRows, F16, pb.sinks) ||
+      !make_tmap_3d(&tk128s, k, bhk, pb.span.Lk, C::kD, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_dq256_pair_kernel<F16>;
+  auto kern = swa_dq256_pair_kernel<F16, kSinks>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -357,6 +365,7 @@ cudaError_t launch_dq256_pair_t(const Problem& pb, const void* q, const void* k,
   a.Hq = pb.Hq;
   a.Hkv = pb.Hkv;
   a.span = pb.span;
+  a.sinks = pb.sinks;
   a.nqb = (pb.span.Lq + kBlockM - 1) / kBlockM;
   a.ntiles = a.nqb * a.BHKP;
   a.scale = pb.scale;
@@ -365,9 +374,11 @@ cudaError_t launch_dq256_pair_t(const Problem& pb, const void* q, const void* k,
   a.divBHKP = FastDiv(static_cast<uint32_t>(a.BHKP));
   a.divGP = FastDiv(static_cast<uint32_t>(a.G / 2));
   a.divHkv = FastDiv(static_cast<uint32_t>(a.Hkv));
-  const int clusters = max_pair_clusters<swa_dq256_pair_kernel<F16>>(C::kThreads, C::kSmemBytes);
+  const int clusters =
+      max_pair_clusters<swa_dq256_pair_kernel<F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
-  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk64, tv64, tk128, a);
+  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk64, tv64, tk128,
+                                                              tk64s, tv64s, tk128s, a);
   return cudaGetLastError();
 }
 
@@ -381,8 +392,11 @@ cudaError_t launch_dq256_pair(const Problem& pb, const void* q, const void* k, c
                               const void* dO, const float* lse, const float* delta, void* dq,
                               cudaStream_t stream) {
   if (!dq256_pair_applies(pb)) return cudaErrorInvalidValue;
-  return pb.f16 ? launch_dq256_pair_t<true>(pb, q, k, v, dO, lse, delta, dq, stream)
-                : launch_dq256_pair_t<false>(pb, q, k, v, dO, lse, delta, dq, stream);
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_dq256_pair_t<true, true>(pb, q, k, v, dO, lse, delta, dq, stream)
+                  : launch_dq256_pair_t<false, true>(pb, q, k, v, dO, lse, delta, dq, stream);
+  return pb.f16 ? launch_dq256_pair_t<true, false>(pb, q, k, v, dO, lse, delta, dq, stream)
+                : launch_dq256_pair_t<false, false>(pb, q, k, v, dO, lse, delta, dq, stream);
 }
 
 }  // namespace swa

@@ -67,19 +67,22 @@ struct FwdP256Args {
   int BHKP;  // B * Hkv * G / 2: head pairs per query block
   int Hq, Hkv, G, nqb, ntiles;
   Span span;
+  int sinks;
   float scale_log2;
   unsigned* err;
   FastDiv divBHKP, divGP, divHkv;  // tile index decomposition (divGP: G / 2)
 };
 
-struct FwdP256Tile {
-  int bh, bhk, q0, kb_lo, nkv;
+template <bool kSinks>
+struct FwdP256Tile : KeyWalk<kSinks> {
+  int bh, bhk, q0;
 };
 
 // Pair tile t (heaviest query blocks first); rank r takes query head 2 p + r of the kv group.
-__device__ __forceinline__ FwdP256Tile fwdp256_tile(int t, const FwdP256Args& a, const Span sp,
-                                                    uint32_t rank) {
-  FwdP256Tile f;
+template <bool kSinks>
+__device__ __forceinline__ FwdP256Tile<kSinks> fwdp256_tile(int t, const FwdP256Args& a,
+                                                            const Span sp, uint32_t rank) {
+  FwdP256Tile<kSinks> f;
   const uint32_t tq = a.divBHKP.div(static_cast<uint32_t>(t));
   const int qb = a.nqb - 1 - static_cast<int>(tq);
   const uint32_t rem = static_cast<uint32_t>(t) - tq * static_cast<uint32_t>(a.BHKP);
@@ -89,17 +92,18 @@ __device__ __forceinline__ FwdP256Tile fwdp256_tile(int t, const FwdP256Args& a,
   const int hk = f.bhk - b * a.Hkv;
   f.bh = b * a.Hq + hk * a.G + 2 * gp + static_cast<int>(rank);
   f.q0 = qb * kBlockM;
-  f.kb_lo = sp.first_kblock(f.q0);
-  f.nkv = sp.last_kblock(f.q0) - f.kb_lo + 1;
+  f.set(sp, a.sinks, f.q0);
   return f;
 }
 
-template <bool F16>
+template <bool F16, bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     swa_fwd256_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k64,   // K, 64-row boxes
                            const __grid_constant__ CUtensorMap tm_v128,  // V, 128-row boxes
-                           const __grid_constant__ CUtensorMap tm_o, const FwdP256Args a) {
+                           const __grid_constant__ CUtensorMap tm_o,
+                           const __grid_constant__ CUtensorMap tm_k64s,  // up to the last sink
+                           const __grid_constant__ CUtensorMap tm_v128s, const FwdP256Args a) {
   using C = FwdP256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -154,18 +158,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // This CTA's ring items in consumption order: on_item(index, is V, key block start, kv plane);
-  // on_tile(tile iteration) before each tile's first item.
+  // This CTA's ring items in consumption order: on_item(index, is V, key block start, kv plane, block
+  // of far sinks); on_tile(tile iteration) before each tile's first item.
   auto walk_items = [&](auto&& on_tile, auto&& on_item) -> bool {
     int i = 0;
     for (int t = tile0, it = 0; t < a.ntiles; t += tile_step, ++it) {
-      const FwdP256Tile f = fwdp256_tile(t, a, sp, rank);
+      const FwdP256Tile<kSinks> f = fwdp256_tile<kSinks>(t, a, sp, rank);
       if (!on_tile(it)) return false;
-      if (!on_item(i++, false, f.kb_lo * kBlockN, f.bhk)) return false;
+      auto item = [&](bool is_v, int j) { return on_item(i++, is_v, f.k0(j), f.bhk, f.is_far(j)); };
+      if (!item(false, 0)) return false;
       for (int j = 0; j < f.nkv; ++j) {
-        const int k0 = (f.kb_lo + j) * kBlockN;
-        if (j + 1 < f.nkv && !on_item(i++, false, k0 + kBlockN, f.bhk)) return false;
-        if (!on_item(i++, true, k0, f.bhk)) return false;
+        if (j + 1 < f.nkv && !item(false, j + 1)) return false;
+        if (!item(true, j)) return false;
       }
     }
     return true;
@@ -182,7 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       tma_prefetch_desc(&tm_k64);
       tma_prefetch_desc(&tm_v128);
       walk_items([&](int) { return true; },
-                 [&](int i, bool is_v, int k0, int bhk) -> bool {
+                 [&](int i, bool is_v, int k0, int bhk, bool far) -> bool {
                    if ((i & 1) != p) return true;
                    if (i >= C::kSlots &&
                        !mbar_wait(empty(i), ((i / C::kSlots) - 1) & 1, &abort_flag, a.err))
@@ -191,12 +195,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                    mbar_arrive_expect_tx(full(i), C::kItemBytes);
                    if (is_v) {
                      for (int c = 0; c < 2; ++c)
-                       tma_load_3d(dst + c * C::kChunk, &tm_v128, full(i),
+                       tma_load_3d(dst + c * C::kChunk, far ? &tm_v128s : &tm_v128, full(i),
                                    128 * static_cast<int>(rank) + 64 * c, k0, bhk);
                    } else {
                      for (int c = 0; c < 4; ++c)
-                       tma_load_3d(dst + c * C::kHalfChunk, &tm_k64, full(i), 64 * c,
-                                   k0 + C::kHalfRows * static_cast<int>(rank), bhk);
+                       tma_load_3d(dst + c * C::kHalfChunk, far ? &tm_k64s : &tm_k64, full(i),
+                                   64 * c, k0 + C::kHalfRows * static_cast<int>(rank), bhk);
                    }
                    last[i % C::kSlots] = i;
                    return true;
@@ -206,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------ Q loads, O stores
     auto load_q = [&](int t) {
-      const FwdP256Tile f = fwdp256_tile(t, a, sp, rank);
+      const FwdP256Tile<kSinks> f = fwdp256_tile<kSinks>(t, a, sp, rank);
       mbar_arrive_expect_tx(bar(C::kQFull), C::kTileBytes);
       for (int c = 0; c < 4; ++c)
         tma_load_3d(sQ + c * C::kChunk, &tm_q, bar(C::kQFull), 64 * c, f.q0, f.bh);
@@ -223,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     for (int t = tile0, it = 0; t < a.ntiles; t += tile_step, ++it) {
       if (!warp_wait(bar(C::kOutFull), it & 1, &abort_flag, a.err)) break;
       if (lane == 0) {
-        const FwdP256Tile f = fwdp256_tile(t, a, sp, rank);
+        const FwdP256Tile<kSinks> f = fwdp256_tile<kSinks>(t, a, sp, rank);
         for (int c = 0; c < 4; ++c) tma_store_3d(&tm_o, sQ + c * C::kChunk, 64 * c, f.q0, f.bh);
         bulk_commit_group();
         bulk_wait_group_read0();  // the Q buffer may be refilled once the store has read it
@@ -272,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     int g = 0;
     bool ok = true;
     for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const FwdP256Tile f = fwdp256_tile(t, a, sp, rank);
+      const FwdP256Tile<kSinks> f = fwdp256_tile<kSinks>(t, a, sp, rank);
       ok = warp_wait_cluster(bar(C::kQFull), it & 1, &abort_flag, a.err);
       if (ok) ok = issue_s(g);
       for (int j = 0; ok && j < f.nkv; ++j) {
@@ -295,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       return true;
     };
     walk_items([&](int it) { return relay(bar(C::kQFull), static_cast<uint32_t>(it & 1)); },
-               [&](int i, bool, int, int) { return relay(full(i), parity(i)); });
+               [&](int i, bool, int, int, bool) { return relay(full(i), parity(i)); });
   } else {
     // ------------------------------------------------------------ softmax (warps 0-7)
     static_assert(C::kPFull - C::kSFull == d256::FwdBar::kPFull &&
@@ -305,9 +309,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                       C::kOutFull - C::kSFull == d256::FwdBar::kOutFull,
                   "softmax barrier layout");
     const d256::FwdSoftmax cx{tmem + C::kColS, sQ,        s_red,      bar(C::kSFull),
-                              &abort_flag,     a.err,     a.scale_log2, a.lse};
-    d256::fwd_softmax<F16, true>(cx, sp, tile0, tile_step, a.ntiles,
-                                 [&](int t) { return fwdp256_tile(t, a, sp, rank); });
+                              &abort_flag,     a.err,     a.scale_log2, a.lse, a.sinks};
+    d256::fwd_softmax<F16, true, kSinks>(
+        cx, sp, tile0, tile_step, a.ntiles,
+        [&](int t) { return fwdp256_tile<kSinks>(t, a, sp, rank); });
   }
 
   // Every cross-CTA arrival and every pair MMA (rank 0 waited for its drain) is complete once both
@@ -320,18 +325,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   }
 }
 
-template <bool F16>
+template <bool F16, bool kSinks>
 cudaError_t launch_fwd256_pair_t(const Problem& pb, const void* q, const void* k, const void* v,
                                  void* o, float* lse, cudaStream_t stream) {
   using C = FwdP256;
-  CUtensorMap tq, to, tk64, tv128;
+  CUtensorMap tq, to, tk64, tv128, tk64s, tv128s;
   const uint64_t bhq = static_cast<uint64_t>(pb.B) * pb.Hq, bhk = static_cast<uint64_t>(pb.B) * pb.Hkv;
   if (!make_tmap_3d(&tq, q, bhq, pb.span.Lq, C::kD, kBlockM, F16) ||
       !make_tmap_3d(&to, o, bhq, pb.span.Lq, C::kD, kBlockM, F16) ||
       !make_tmap_3d(&tk64, k, bhk, pb.span.Lk, C::kD, C::kHalfRows, F16) ||
-      !make_tmap_3d(&tv128, v, bhk, pb.span.Lk, C::kD, kBlockN, F16))
+      !make_tmap_3d(&tv128, v, bhk, pb.span.Lk, C::kD, kBlockN, F16) ||
+      !make_tmap_3d(&tk64s, k, bhk, pb.span.Lk, C::kD, C::kHalfRows, F16, pb.sinks) ||
+      !make_tmap_3d(&tv128s, v, bhk, pb.span.Lk, C::kD, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_fwd256_pair_kernel<F16>;
+  auto kern = swa_fwd256_pair_kernel<F16, kSinks>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -342,6 +349,7 @@ cudaError_t launch_fwd256_pair_t(const Problem& pb, const void* q, const void* k
   a.Hq = pb.Hq;
   a.Hkv = pb.Hkv;
   a.span = pb.span;
+  a.sinks = pb.sinks;
   a.nqb = (pb.span.Lq + kBlockM - 1) / kBlockM;
   a.ntiles = a.nqb * a.BHKP;
   a.scale_log2 = pb.scale * kLog2e;
@@ -349,9 +357,11 @@ cudaError_t launch_fwd256_pair_t(const Problem& pb, const void* q, const void* k
   a.divBHKP = FastDiv(static_cast<uint32_t>(a.BHKP));
   a.divGP = FastDiv(static_cast<uint32_t>(a.G / 2));
   a.divHkv = FastDiv(static_cast<uint32_t>(a.Hkv));
-  const int clusters = max_pair_clusters<swa_fwd256_pair_kernel<F16>>(C::kThreads, C::kSmemBytes);
+  const int clusters =
+      max_pair_clusters<swa_fwd256_pair_kernel<F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
-  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tk64, tv128, to, a);
+  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tk64, tv128, to, tk64s,
+                                                              tv128s, a);
   return cudaGetLastError();
 }
 
@@ -364,8 +374,11 @@ bool fwd256_pair_applies(const Problem& pb) {
 cudaError_t launch_fwd256_pair(const Problem& pb, const void* q, const void* k, const void* v,
                                void* o, float* lse, cudaStream_t stream) {
   if (!fwd256_pair_applies(pb)) return cudaErrorInvalidValue;
-  return pb.f16 ? launch_fwd256_pair_t<true>(pb, q, k, v, o, lse, stream)
-                : launch_fwd256_pair_t<false>(pb, q, k, v, o, lse, stream);
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_fwd256_pair_t<true, true>(pb, q, k, v, o, lse, stream)
+                  : launch_fwd256_pair_t<false, true>(pb, q, k, v, o, lse, stream);
+  return pb.f16 ? launch_fwd256_pair_t<true, false>(pb, q, k, v, o, lse, stream)
+                : launch_fwd256_pair_t<false, false>(pb, q, k, v, o, lse, stream);
 }
 
 }  // namespace swa

@@ -105,18 +105,21 @@ struct FwdArgs {
   int BH;  // B * Hq
   int Hq, Hkv, G, nqb, ntiles;
   Span span;
+  int sinks;
   float scale_log2;  // scale * log2(e)
   unsigned* err;
   FastDiv divBH, divHq, divG;  // tile index decomposition
 };
 
-struct FwdTile {
-  int bh, bhk, q0, kb_lo, nkv;
+template <bool kSinks>
+struct FwdTile : KeyWalk<kSinks> {
+  int bh, bhk, q0;
 };
 
 // Tile t: heaviest query blocks first (the causal case gives later blocks more key blocks).
-__device__ __forceinline__ FwdTile fwd_tile(int t, const FwdArgs& a, const Span sp) {
-  FwdTile f;
+template <bool kSinks>
+__device__ __forceinline__ FwdTile<kSinks> fwd_tile(int t, const FwdArgs& a, const Span sp) {
+  FwdTile<kSinks> f;
   const uint32_t tq = a.divBH.div(static_cast<uint32_t>(t));
   const int qb = a.nqb - 1 - static_cast<int>(tq);
   f.bh = t - static_cast<int>(tq) * a.BH;
@@ -124,16 +127,16 @@ __device__ __forceinline__ FwdTile fwd_tile(int t, const FwdArgs& a, const Span 
   f.bhk = static_cast<int>(b) * a.Hkv +
           static_cast<int>(a.divG.div(static_cast<uint32_t>(f.bh) - b * static_cast<uint32_t>(a.Hq)));
   f.q0 = qb * kBlockM;
-  f.kb_lo = sp.first_kblock(f.q0);
-  f.nkv = sp.last_kblock(f.q0) - f.kb_lo + 1;
+  f.set(sp, a.sinks, f.q0);
   return f;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 __global__ void __launch_bounds__(384, 1)
     swa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                   const FwdArgs a) {
+                   const __grid_constant__ CUtensorMap tm_ks,  // K and V up to the last sink
+                   const __grid_constant__ CUtensorMap tm_vs, const FwdArgs a) {
   using C = FwdCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(384, 1)
       int g = 0;  // key blocks loaded so far by this CTA
       bool ok = true;
       for (int t = blockIdx.x, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-        const FwdTile f = fwd_tile(t, a, sp);
+        const FwdTile<kSinks> f = fwd_tile<kSinks>(t, a, sp);
         const int qbuf = it & 1;
         // The Q buffer was last the staging tile of tile it - 2's output.
         if (it >= 2 && !mbar_wait(bar(C::kQEmpty + qbuf), ((it - 2) >> 1) & 1, &abort_flag, a.err))
@@ -206,7 +209,8 @@ __global__ void __launch_bounds__(384, 1)
           tma_load_3d(sQ + h * C::kChunkBytes, &tm_q, bar(C::kQFull + qbuf), 64 * h, f.q0, f.bh);
         last_q[qbuf] = it;
         for (int j = 0; j < f.nkv; ++j, ++g) {
-          const int k0 = (f.kb_lo + j) * kBlockN;
+          const int k0 = f.k0(j);
+          const CUtensorMap* map = f.is_far(j) ? &tm_ks : &tm_k;
           const int sk = g % C::kKStages, nk = g / C::kKStages;
           if (g >= C::kKStages &&
               !(ok = mbar_wait(bar(C::kKEmpty + sk), (nk - 1) & 1, &abort_flag, a.err)))
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(384, 1)
           const uint32_t sK = sK0 + sk * C::kTileBytes;
           mbar_arrive_expect_tx(bar(C::kKFull + sk), C::kTileBytes);
           for (int h = 0; h < C::kChunks; ++h)
-            tma_load_3d(sK + h * C::kChunkBytes, &tm_k, bar(C::kKFull + sk), 64 * h, k0, f.bhk);
+            tma_load_3d(sK + h * C::kChunkBytes, map, bar(C::kKFull + sk), 64 * h, k0, f.bhk);
           last_k[sk] = g;
         }
       }
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(384, 1)
       int g = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < a.ntiles; t += tile_step) {
-        const FwdTile f = fwd_tile(t, a, sp);
+        const FwdTile<kSinks> f = fwd_tile<kSinks>(t, a, sp);
         for (int j = 0; j < f.nkv; ++j, ++g) {
           const int sv = g % C::kVStages, nv = g / C::kVStages;
           if (g >= C::kVStages &&
@@ -242,8 +246,8 @@ __global__ void __launch_bounds__(384, 1)
           const uint32_t sV = sV0 + sv * C::kTileBytes;
           mbar_arrive_expect_tx(bar(C::kVFull + sv), C::kTileBytes);
           for (int h = 0; h < C::kChunks; ++h)
-            tma_load_3d(sV + h * C::kChunkBytes, &tm_v, bar(C::kVFull + sv), 64 * h,
-                        (f.kb_lo + j) * kBlockN, f.bhk);
+            tma_load_3d(sV + h * C::kChunkBytes, f.is_far(j) ? &tm_vs : &tm_v, bar(C::kVFull + sv),
+                        64 * h, f.k0(j), f.bhk);
           last_v[sv] = g;
         }
       }
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(384, 1)
     // every P V of the tile two before it has been: its Q buffer is that tile's output staging
     // area, refilled after the store.
     int s_t = static_cast<int>(blockIdx.x), s_it = 0, s_j = 0, s_g = 0;
-    FwdTile s_f = fwd_tile(s_t < a.ntiles ? s_t : 0, a, sp);
+    FwdTile<kSinks> s_f = fwd_tile<kSinks>(s_t < a.ntiles ? s_t : 0, a, sp);
     auto issue_next_s = [&]() -> bool {
       if (s_t >= a.ntiles) return true;
       if (s_j == 0 &&
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(384, 1)
         s_j = 0;
         s_t += tile_step;
         ++s_it;
-        if (s_t < a.ntiles) s_f = fwd_tile(s_t, a, sp);
+        if (s_t < a.ntiles) s_f = fwd_tile<kSinks>(s_t, a, sp);
       }
       return true;
     };
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = fill_s(C::kSBufs, 0);
     int g = 0;  // key blocks whose P V has been issued
     for (int t = blockIdx.x, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const FwdTile f = fwd_tile(t, a, sp);
+      const FwdTile<kSinks> f = fwd_tile<kSinks>(t, a, sp);
       for (int j = 0; ok && j < f.nkv; ++j) {
         // The first P V of a tile overwrites O: the previous tile's epilogue must have read it.
         if (j == 0 && it > 0) ok = warp_wait(bar(C::kOEmpty), (it - 1) & 1, &abort_flag, a.err);
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------------ output stores
     for (int t = blockIdx.x, it = 0; t < a.ntiles; t += tile_step, ++it) {
-      const FwdTile f = fwd_tile(t, a, sp);
+      const FwdTile<kSinks> f = fwd_tile<kSinks>(t, a, sp);
       const int b = it & 1;
       if (!warp_wait(bar(C::kOutFull + b), (it >> 1) & 1, &abort_flag, a.err)) break;
       if (lane == 0) {
@@ -370,14 +374,14 @@ __global__ void __launch_bounds__(384, 1)
     int g = 0;  // key blocks consumed so far by this CTA
     bool ok = true;
     for (int t = blockIdx.x, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const FwdTile f = fwd_tile(t, a, sp);
+      const FwdTile<kSinks> f = fwd_tile<kSinks>(t, a, sp);
       const int q0 = f.q0;
       const int row = q0 + r;
       float m_ref = SWA_NEG_INF;  // reference max (log2 domain) that P and l are taken against
       float l = 0.f;              // partial row sum over this thread's half of the columns
       for (int j = 0; j < f.nkv; ++j) {
         const int gg = g + j;
-        const int k0 = (f.kb_lo + j) * kBlockN;
+        const int k0 = f.k0(j);
         const int sb = gg % C::kSBufs;
         if (!(ok = warp_wait(bar(C::kSFull + sb), (gg / C::kSBufs) & 1, &abort_flag, a.err))) break;
         tc_fence_after();
@@ -398,8 +402,10 @@ __global__ void __launch_bounds__(384, 1)
           const int rel = row + sp.off - k0 - 64 * static_cast<int>(h);
           const int lo = rel - sp.dmax;
           const int hi = min(rel - sp.dmin, sp.Lk - 1 - k0 - 64 * static_cast<int>(h));
+          const int sk = a.sinks - k0 - 64 * static_cast<int>(h);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = (c >= lo && c <= hi) ? x[c] : SWA_NEG_INF;
+          for (int c = 0; c < 64; ++c)
+            x[c] = column_visible<kSinks>(c, lo, hi, sk) ? x[c] : SWA_NEG_INF;
         }
         // p = 2^(scale log2(e) S - m) for this half, two scores per step: one packed FFMA, two
         // MUFU.EX2, one packed FADD into the row sum and one bf16 pack.  Returns the half's sum.
@@ -545,18 +551,20 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 cudaError_t launch_fwd_d(const Problem& pb, const void* q, const void* k, const void* v, void* o,
                          float* lse, cudaStream_t stream) {
   using C = FwdCfg<D>;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv, to, tks, tvs;
   const uint64_t bhq = static_cast<uint64_t>(pb.B) * pb.Hq, bhk = static_cast<uint64_t>(pb.B) * pb.Hkv;
   if (!make_tmap_3d(&tq, q, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&to, o, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&tk, k, bhk, pb.span.Lk, D, kBlockN, F16) ||
-      !make_tmap_3d(&tv, v, bhk, pb.span.Lk, D, kBlockN, F16))
+      !make_tmap_3d(&tv, v, bhk, pb.span.Lk, D, kBlockN, F16) ||
+      !make_tmap_3d(&tks, k, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks) ||
+      !make_tmap_3d(&tvs, v, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_fwd_kernel<D, F16>;
+  auto kern = swa_fwd_kernel<D, F16, kSinks>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -567,6 +575,7 @@ cudaError_t launch_fwd_d(const Problem& pb, const void* q, const void* k, const 
   a.Hkv = pb.Hkv;
   a.G = pb.Hq / pb.Hkv;
   a.span = pb.span;
+  a.sinks = pb.sinks;
   a.nqb = (pb.span.Lq + kBlockM - 1) / kBlockM;
   a.ntiles = a.nqb * a.BH;
   a.scale_log2 = pb.scale * kLog2e;
@@ -575,22 +584,30 @@ cudaError_t launch_fwd_d(const Problem& pb, const void* q, const void* k, const 
   a.divHq = FastDiv(static_cast<uint32_t>(a.Hq));
   a.divG = FastDiv(static_cast<uint32_t>(a.G));
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, a);
+  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, tks, tvs, a);
   return cudaGetLastError();
 }
 
+}  // namespace
+
+namespace {
+template <int D>
+cudaError_t launch_fwd_any(const Problem& pb, const void* q, const void* k, const void* v, void* o,
+                           float* lse, cudaStream_t stream) {
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_fwd_d<D, true, true>(pb, q, k, v, o, lse, stream)
+                  : launch_fwd_d<D, false, true>(pb, q, k, v, o, lse, stream);
+  return pb.f16 ? launch_fwd_d<D, true, false>(pb, q, k, v, o, lse, stream)
+                : launch_fwd_d<D, false, false>(pb, q, k, v, o, lse, stream);
+}
 }  // namespace
 
 cudaError_t launch_fwd(const Problem& pb, const void* q, const void* k, const void* v, void* o,
                        float* lse, cudaStream_t stream) {
   if (pb.D == 256) return launch_fwd_d256(pb, q, k, v, o, lse, stream);
   if (fwd_pair_applies(pb)) return launch_fwd_pair(pb, q, k, v, o, lse, stream);
-  if (pb.D == 64)
-    return pb.f16 ? launch_fwd_d<64, true>(pb, q, k, v, o, lse, stream)
-                  : launch_fwd_d<64, false>(pb, q, k, v, o, lse, stream);
-  if (pb.D == 128)
-    return pb.f16 ? launch_fwd_d<128, true>(pb, q, k, v, o, lse, stream)
-                  : launch_fwd_d<128, false>(pb, q, k, v, o, lse, stream);
+  if (pb.D == 64) return launch_fwd_any<64>(pb, q, k, v, o, lse, stream);
+  if (pb.D == 128) return launch_fwd_any<128>(pb, q, k, v, o, lse, stream);
   return cudaErrorInvalidValue;
 }
 

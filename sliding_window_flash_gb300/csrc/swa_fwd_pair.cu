@@ -83,19 +83,22 @@ struct FwdPairArgs {
   int BHKP;  // B * Hkv * G / 2: head pairs per query block
   int Hq, Hkv, G, nqb, ntiles;
   Span span;
+  int sinks;
   float scale_log2;
   unsigned* err;
   FastDiv divBHKP, divGP, divHkv;  // tile index decomposition (divGP: G / 2)
 };
 
-struct PairTile {
-  int bh, bhk, q0, kb_lo, nkv;
+template <bool kSinks>
+struct PairTile : KeyWalk<kSinks> {
+  int bh, bhk, q0;
 };
 
 // Pair tile t (heaviest query blocks first); rank r takes query head 2 p + r of the kv group.
-__device__ __forceinline__ PairTile fwd_pair_tile(int t, const FwdPairArgs& a, const Span sp,
-                                                  uint32_t rank) {
-  PairTile f;
+template <bool kSinks>
+__device__ __forceinline__ PairTile<kSinks> fwd_pair_tile(int t, const FwdPairArgs& a, const Span sp,
+                                                          uint32_t rank) {
+  PairTile<kSinks> f;
   const uint32_t tq = a.divBHKP.div(static_cast<uint32_t>(t));
   const int qb = a.nqb - 1 - static_cast<int>(tq);
   const uint32_t rem = static_cast<uint32_t>(t) - tq * static_cast<uint32_t>(a.BHKP);
@@ -105,17 +108,18 @@ __device__ __forceinline__ PairTile fwd_pair_tile(int t, const FwdPairArgs& a, c
   const int hk = f.bhk - b * a.Hkv;
   f.bh = b * a.Hq + hk * a.G + 2 * gp + static_cast<int>(rank);
   f.q0 = qb * kBlockM;
-  f.kb_lo = sp.first_kblock(f.q0);
-  f.nkv = sp.last_kblock(f.q0) - f.kb_lo + 1;
+  f.set(sp, a.sinks, f.q0);
   return f;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     swa_fwd_pair_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
-                        const __grid_constant__ CUtensorMap tm_o, const FwdPairArgs a) {
+                        const __grid_constant__ CUtensorMap tm_o,
+                        const __grid_constant__ CUtensorMap tm_ks,  // K and V up to the last sink
+                        const __grid_constant__ CUtensorMap tm_vs, const FwdPairArgs a) {
   using C = FwdPairCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
@@ -178,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   // on_s(g, tile index, first block of its tile) and on_pv(g, tile index, block within the tile).
   auto walk = [&](auto&& on_s, auto&& on_pv) -> bool {
     int s_t = tile0, s_it = 0, s_j = 0, s_g = 0;
-    PairTile s_f = fwd_pair_tile(s_t < a.ntiles ? s_t : 0, a, sp, rank);
+    PairTile<kSinks> s_f = fwd_pair_tile<kSinks>(s_t < a.ntiles ? s_t : 0, a, sp, rank);
     auto fill_s = [&](int s_limit, int tiles_done) -> bool {
       while (s_t < a.ntiles && s_g < s_limit && s_it < tiles_done + 2) {
         if (!on_s(s_g, s_it, s_j == 0)) return false;
@@ -187,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           s_j = 0;
           s_t += tile_step;
           ++s_it;
-          if (s_t < a.ntiles) s_f = fwd_pair_tile(s_t, a, sp, rank);
+          if (s_t < a.ntiles) s_f = fwd_pair_tile<kSinks>(s_t, a, sp, rank);
         }
       }
       return true;
@@ -195,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     bool ok = fill_s(C::kSBufs, 0);
     int g = 0;
     for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const PairTile f = fwd_pair_tile(t, a, sp, rank);
+      const PairTile<kSinks> f = fwd_pair_tile<kSinks>(t, a, sp, rank);
       for (int j = 0; ok && j < f.nkv; ++j) {
         ok = on_pv(g + j, it, j);
         if (ok) ok = fill_s(g + j + 1 + C::kSBufs, it + (j + 1 == f.nkv ? 1 : 0));
@@ -218,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       int g = 0;
       bool ok = true;
       for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-        const PairTile f = fwd_pair_tile(t, a, sp, rank);
+        const PairTile<kSinks> f = fwd_pair_tile<kSinks>(t, a, sp, rank);
         const int qbuf = it & 1;
         if (it >= 2 && !mbar_wait(bar(C::kQEmpty + qbuf), ((it - 2) >> 1) & 1, &abort_flag, a.err))
           break;
@@ -228,7 +232,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           tma_load_3d(sQ + h * C::kChunkBytes, &tm_q, bar(C::kQFull + qbuf), 64 * h, f.q0, f.bh);
         last_q[qbuf] = it;
         for (int j = 0; j < f.nkv; ++j, ++g) {
-          const int k0 = (f.kb_lo + j) * kBlockN + C::kKHalfRows * static_cast<int>(rank);
+          const int k0 = f.k0(j) + C::kKHalfRows * static_cast<int>(rank);
+          const CUtensorMap* map = f.is_far(j) ? &tm_ks : &tm_k;
           const int sk = g % C::kKStages, nk = g / C::kKStages;
           if (g >= C::kKStages &&
               !(ok = mbar_wait(bar(C::kKEmpty + sk), (nk - 1) & 1, &abort_flag, a.err)))
@@ -236,7 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           const uint32_t sK = sK0 + sk * C::kKHalfBytes;
           mbar_arrive_expect_tx(bar(C::kKFull + sk), C::kKHalfBytes);
           for (int h = 0; h < C::kChunks; ++h)
-            tma_load_3d(sK + h * C::kKChunkBytes, &tm_k, bar(C::kKFull + sk), 64 * h, k0, f.bhk);
+            tma_load_3d(sK + h * C::kKChunkBytes, map, bar(C::kKFull + sk), 64 * h, k0, f.bhk);
           last_k[sk] = g;
         }
       }
@@ -254,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       int g = 0;
       bool ok = true;
       for (int t = tile0; ok && t < a.ntiles; t += tile_step) {
-        const PairTile f = fwd_pair_tile(t, a, sp, rank);
+        const PairTile<kSinks> f = fwd_pair_tile<kSinks>(t, a, sp, rank);
         for (int j = 0; j < f.nkv; ++j, ++g) {
           const int sv = g % C::kVStages, nv = g / C::kVStages;
           if (g >= C::kVStages &&
@@ -262,8 +267,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             break;
           const uint32_t sV = sV0 + sv * C::kVHalfBytes;
           mbar_arrive_expect_tx(bar(C::kVFull + sv), C::kVHalfBytes);
-          tma_load_3d(sV, &tm_v, bar(C::kVFull + sv), 64 * static_cast<int>(rank),
-                      (f.kb_lo + j) * kBlockN, f.bhk);
+          tma_load_3d(sV, f.is_far(j) ? &tm_vs : &tm_v, bar(C::kVFull + sv),
+                      64 * static_cast<int>(rank), f.k0(j), f.bhk);
           last_v[sv] = g;
         }
       }
@@ -331,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------------ output stores
     for (int t = tile0, it = 0; t < a.ntiles; t += tile_step, ++it) {
-      const PairTile f = fwd_pair_tile(t, a, sp, rank);
+      const PairTile<kSinks> f = fwd_pair_tile<kSinks>(t, a, sp, rank);
       const int b = it & 1;
       if (!warp_wait(bar(C::kOutFull + b), (it >> 1) & 1, &abort_flag, a.err)) break;
       if (lane == 0) {
@@ -367,14 +372,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     int g = 0;
     bool ok = true;
     for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
-      const PairTile f = fwd_pair_tile(t, a, sp, rank);
+      const PairTile<kSinks> f = fwd_pair_tile<kSinks>(t, a, sp, rank);
       const int q0 = f.q0;
       const int row0 = q0 + r0, row1 = row0 + 8;
       float m0 = SWA_NEG_INF, m1 = SWA_NEG_INF;  // reference max (log2 domain) of rows R0, R1
       float l0 = 0.f, l1 = 0.f;                  // partial sums over this thread's columns
       for (int j = 0; j < f.nkv; ++j) {
         const int gg = g + j;
-        const int k0 = (f.kb_lo + j) * kBlockN;
+        const int k0 = f.k0(j);
         const int sb = gg % C::kSBufs;
         if (!(ok = warp_wait(bar(C::kSFull + sb), (gg / C::kSBufs) & 1, &abort_flag, a.err))) break;
         tc_fence_after();
@@ -396,10 +401,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           const int rel0 = row0 + sp.off - k0 - 2 * kq, rel1 = rel0 + 8;
           const int lo0 = rel0 - sp.dmax, hi0 = min(rel0 - sp.dmin, sp.Lk - 1 - k0 - 2 * kq);
           const int lo1 = rel1 - sp.dmax, hi1 = min(rel1 - sp.dmin, sp.Lk - 1 - k0 - 2 * kq);
+          const int sk = a.sinks - k0 - 2 * kq;
 #pragma unroll
           for (int i = 0; i < 64; ++i) {
             const int c = 8 * (i >> 2) + (i & 1);
-            const bool vis = (i & 2) ? (c >= lo1 && c <= hi1) : (c >= lo0 && c <= hi0);
+            const bool vis = (i & 2) ? column_visible<kSinks>(c, lo1, hi1, sk)
+                                     : column_visible<kSinks>(c, lo0, hi0, sk);
             x[i] = vis ? x[i] : SWA_NEG_INF;
           }
         }
@@ -550,18 +557,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool kSinks>
 cudaError_t launch_fwd_pair_d(const Problem& pb, const void* q, const void* k, const void* v,
                               void* o, float* lse, cudaStream_t stream) {
   using C = FwdPairCfg<D>;
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv, to, tks, tvs;
   const uint64_t bhq = static_cast<uint64_t>(pb.B) * pb.Hq, bhk = static_cast<uint64_t>(pb.B) * pb.Hkv;
   if (!make_tmap_3d(&tq, q, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&to, o, bhq, pb.span.Lq, D, kBlockM, F16) ||
       !make_tmap_3d(&tk, k, bhk, pb.span.Lk, D, C::kKHalfRows, F16) ||
-      !make_tmap_3d(&tv, v, bhk, pb.span.Lk, D, kBlockN, F16))
+      !make_tmap_3d(&tv, v, bhk, pb.span.Lk, D, kBlockN, F16) ||
+      !make_tmap_3d(&tks, k, bhk, pb.span.Lk, D, C::kKHalfRows, F16, pb.sinks) ||
+      !make_tmap_3d(&tvs, v, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
-  auto kern = swa_fwd_pair_kernel<D, F16>;
+  auto kern = swa_fwd_pair_kernel<D, F16, kSinks>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -572,6 +581,7 @@ cudaError_t launch_fwd_pair_d(const Problem& pb, const void* q, const void* k, c
   a.Hq = pb.Hq;
   a.Hkv = pb.Hkv;
   a.span = pb.span;
+  a.sinks = pb.sinks;
   a.nqb = (pb.span.Lq + kBlockM - 1) / kBlockM;
   a.ntiles = a.nqb * a.BHKP;
   a.scale_log2 = pb.scale * kLog2e;
@@ -579,9 +589,10 @@ cudaError_t launch_fwd_pair_d(const Problem& pb, const void* q, const void* k, c
   a.divBHKP = FastDiv(static_cast<uint32_t>(a.BHKP));
   a.divGP = FastDiv(static_cast<uint32_t>(a.G / 2));
   a.divHkv = FastDiv(static_cast<uint32_t>(a.Hkv));
-  const int clusters = max_pair_clusters<swa_fwd_pair_kernel<D, F16>>(C::kThreads, C::kSmemBytes);
+  const int clusters =
+      max_pair_clusters<swa_fwd_pair_kernel<D, F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
-  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, a);
+  kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, tks, tvs, a);
   return cudaGetLastError();
 }
 
@@ -595,8 +606,11 @@ bool fwd_pair_applies(const Problem& pb) {
 cudaError_t launch_fwd_pair(const Problem& pb, const void* q, const void* k, const void* v,
                             void* o, float* lse, cudaStream_t stream) {
   if (!fwd_pair_applies(pb)) return cudaErrorInvalidValue;
-  return pb.f16 ? launch_fwd_pair_d<128, true>(pb, q, k, v, o, lse, stream)
-                : launch_fwd_pair_d<128, false>(pb, q, k, v, o, lse, stream);
+  if (pb.sinks > 0)
+    return pb.f16 ? launch_fwd_pair_d<128, true, true>(pb, q, k, v, o, lse, stream)
+                  : launch_fwd_pair_d<128, false, true>(pb, q, k, v, o, lse, stream);
+  return pb.f16 ? launch_fwd_pair_d<128, true, false>(pb, q, k, v, o, lse, stream)
+                : launch_fwd_pair_d<128, false, false>(pb, q, k, v, o, lse, stream);
 }
 
 }  // namespace swa

@@ -56,6 +56,38 @@ struct Span {
   }
 };
 
+// The key blocks that the query tile at q0 visits, in order: with kSinks first the blocks of the
+// sequence's first `sinks` keys that lie before the window's (its far sinks, all of them visible to
+// every query of the tile), then the window's blocks.  Far blocks are loaded through tensor maps that
+// end behind the last sink, so what the other keys of a far block hold reads as zero.
+template <bool kSinks>
+struct KeyWalk {
+  int kb_lo, nkv;  // first block of the window; blocks in all
+  int far;         // far blocks
+  __host__ __device__ void set(const Span& sp, int sinks, int q0) {
+    kb_lo = sp.first_kblock(q0);
+    far = 0;
+    if constexpr (kSinks) {
+      far = (sinks + kBlockN - 1) / kBlockN;
+      if (far > kb_lo) far = kb_lo;
+    }
+    nkv = sp.last_kblock(q0) - kb_lo + 1 + far;
+  }
+  // First key of block j, and whether it is a far one.
+  __host__ __device__ int k0(int j) const {
+    if constexpr (kSinks) return (j < far ? j : kb_lo + j - far) * kBlockN;
+    return (kb_lo + j) * kBlockN;
+  }
+  __host__ __device__ bool is_far(int j) const { return kSinks && j < far; }
+};
+
+// Columns c of 64 or 128 keys visible to a row: [lo, hi], and with kSinks those below `sk` up to hi.
+template <bool kSinks>
+__host__ __device__ __forceinline__ bool column_visible(int c, int lo, int hi, int sk) {
+  if constexpr (kSinks) return (c >= lo || c < sk) && c <= hi;
+  return c >= lo && c <= hi;
+}
+
 // Shape and window of one call.  Query tensors (q, o, dO, dq) are contiguous [B, Hq, Lq, D], key
 // tensors (k, v, dk, dv) [B, Hkv, Lk, D], LSE and Delta [B, Hq, Lq].
 struct Problem {
@@ -64,7 +96,39 @@ struct Problem {
   float scale;    // softmax scale
   unsigned* err;  // per-device error word (bounded-wait timeouts)
   int f16 = 0;    // element type of every tensor but LSE / Delta: 0 = bf16, 1 = fp16
+  int sinks = 0;  // first keys that stay visible behind the window; 0 when the window hides none
+  float* sink_part = nullptr;  // backward: sink_part_bytes of workspace
 };
+
+// dK and dV of the sinks.  A sink is seen by every query behind it, where another key is seen by a
+// window of them, so the walk over the query tiles of a sinks' key block is cut into `splits` parts;
+// their fp32 sums are joined in order (launch_sink_join), which replaces the first `sinks` rows of dK and
+// dV.  The parts go first in the launch that walks the windows' key blocks.  A part is at most half of
+// an SM's share of that launch's tiles, so that the windows' walks fill up what the parts leave.
+// `width`: key blocks that a CTA (1) or a pair of them (2) takes.
+struct SinkPlan {
+  int blocks, splits;  // of `width` key blocks; parts of each one's walk
+};
+inline SinkPlan sink_plan(const Problem& pb, int width, int units) {
+  const long long G = pb.Hq / pb.Hkv, heads = static_cast<long long>(pb.B) * pb.Hkv;
+  const long long span = static_cast<long long>(width) * kBlockN;
+  const long long walk = G * ((pb.span.Lq + kBlockM - 1) / kBlockM);  // at most, of a sinks' block
+  const long long seen = pb.span.dmax - pb.span.dmin + span;
+  const long long near = G * ((seen < pb.span.Lq ? seen : pb.span.Lq) / kBlockM + 1);
+  SinkPlan p;
+  p.blocks = static_cast<int>((pb.sinks + span - 1) / span);
+  const long long all = heads * (p.blocks * walk + (pb.span.Lk + span - 1) / span * near);
+  long long part = all / (2 * units);
+  if (part < 4) part = 4;
+  p.splits = static_cast<int>((walk + part - 1) / part);
+  return p;
+}
+// Where a part's sums lie: [splits][B Hkv][dK, dV][sinks][D] fp32.
+__host__ __device__ inline size_t sink_part_offset(int split, int heads, int bhk, int which,
+                                                   int sinks, int row, int D) {
+  return (((static_cast<size_t>(split) * heads + bhk) * 2 + which) * sinks + row) *
+         static_cast<size_t>(D);
+}
 
 // Division by a divisor fixed for a launch, without a divide instruction: for 0 <= n < 2^31 and
 // 1 <= d < 2^31, n / d = (umulhi(n, m) + n) >> s with s = ceil(log2 d) and
@@ -134,6 +198,15 @@ int max_pair_clusters(int threads, int smem) {
   return cached[dev];
 }
 
+inline SinkPlan sink_plan(const Problem& pb) {
+  return pb.D == 256 ? sink_plan(pb, 2, sm_count() / 2) : sink_plan(pb, 1, sm_count());
+}
+inline size_t sink_part_bytes(const Problem& pb) {
+  if (pb.sinks == 0) return 0;
+  return sink_part_offset(sink_plan(pb).splits, pb.B * pb.Hkv, 0, 0, pb.sinks, 0, pb.D) *
+         sizeof(float);
+}
+
 // Launchers (each returns the launch's cudaError_t).
 cudaError_t launch_fwd(const Problem& pb, const void* q, const void* k, const void* v, void* o,
                        float* lse, cudaStream_t stream);
@@ -156,6 +229,9 @@ bool dq_pair_applies(const Problem& pb);
 cudaError_t launch_dq_pair(const Problem& pb, const void* q, const void* k, const void* v,
                            const void* dO, const float* lse, const float* delta, void* dq,
                            cudaStream_t stream);
+
+// dK and dV rows of the sinks from the parts' sums (swa_bwd_sinks.cu).
+cudaError_t launch_sink_join(const Problem& pb, int splits, void* dk, void* dv, cudaStream_t stream);
 
 // Fused backward (swa_bwd_fused.cu): dK, dV and the dQ partials of every (key block, query tile)
 // pair in one kernel.  dQ accumulates in fp32, tile-major: block (bhq, qb) holds query rows
