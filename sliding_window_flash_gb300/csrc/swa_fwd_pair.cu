@@ -441,8 +441,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         bool redo = true;
         if (__all_sync(0xffffffffu, m0 != SWA_NEG_INF && m1 != SWA_NEG_INF)) {
           exponentiate(m0, m1);
-          redo = __any_sync(0xffffffffu,
-                            !(row_sum(b0) <= kFastSumLimit) || !(row_sum(b1) <= kFastSumLimit));
+          // Both sums before either is judged: every lane has to take part in their shuffles.
+          const float sum0 = row_sum(b0), sum1 = row_sum(b1);
+          redo = __any_sync(0xffffffffu, !(sum0 <= kFastSumLimit) || !(sum1 <= kFastSumLimit));
         }
         bool resc = false;
         float f0 = 1.f, f1 = 1.f;  // rescale factors of rows R0, R1
