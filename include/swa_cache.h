@@ -115,6 +115,20 @@ swa_status swa_cache_attn(const swa_cache* cache, const int* table, int max_page
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The same with sinks: query t of sequence b also sees the slots s < sinks behind the window, up to its
+ * own slot.  sinks >= 0; 0, or a window that hides nothing, is swa_cache_attn.  Pages wholly between the
+ * sinks and every window are not read.  The workspace is at least swa_cache_attn_sinks_workspace_bytes
+ * bytes; accumulating takes its 4 bytes for the sinks' slots too.
+ */
+size_t swa_cache_attn_sinks_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
+                                            int page, int window, int sinks, int accumulate);
+swa_status swa_cache_attn_sinks(const swa_cache* cache, const int* table, int max_pages,
+                                const int* lens, const int* new_lens, const void* q, void* o,
+                                float* lse, int B, int Hq, int T, int window, int sinks, float scale,
+                                int accumulate, int dtype, void* workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/*
  * Eviction: cuts each sequence and kv head to min(lens[b], budget) tokens.  When lens[b] > budget
  * the last `recent` slots stay, and of the others the budget - recent with the largest accumulated
  * weight (equal weights: the lower slot; NaN above every number); the survivors keep their order.

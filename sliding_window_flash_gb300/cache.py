@@ -53,6 +53,12 @@ SIGNATURES = {
         [_cp, _vp, _c_int] + [_vp] * 5 + [_c_int] * 4 + [_c_float] + [_c_int] * 2 +
         [_vp, ctypes.c_size_t, _vp],
     ),
+    "swa_cache_attn_sinks_workspace_bytes": (ctypes.c_size_t, [_c_int] * 10),
+    "swa_cache_attn_sinks": (
+        _c_int,
+        [_cp, _vp, _c_int] + [_vp] * 5 + [_c_int] * 5 + [_c_float] + [_c_int] * 2 +
+        [_vp, ctypes.c_size_t, _vp],
+    ),
     "swa_cache_evict": (
         _c_int, [_cp, _vp, _c_int, _vp, _vp] + [_c_int] * 3 + [_vp, _vp, _c_int, _vp]),
     "swa_attn_key_weights_workspace_bytes": (ctypes.c_size_t, [_c_int] * 8),
@@ -270,7 +276,7 @@ def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) 
 # A workspace's size follows the number of the GPU's SMs, so it is asked for, and kept, for that GPU.
 @functools.lru_cache(maxsize=256)
 def _attn_space(index, *sizes):
-    return int(_on(index, "swa_cache_attn_window_workspace_bytes", *sizes))
+    return int(_on(index, "swa_cache_attn_sinks_workspace_bytes", *sizes))
 
 
 @functools.lru_cache(maxsize=256)
@@ -280,24 +286,28 @@ def _weights_space(index, *sizes):
 
 def swa_cache_attn_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, max_pages: int,
                                    page: int, accumulate: bool = False,
-                                   window: Optional[int] = None) -> int:
+                                   window: Optional[int] = None, sinks: int = 0) -> int:
     """Bytes of swa_cache_attn's workspace on the current GPU, for this window or (None) for any."""
     sizes, acc = (B, Hq, Hkv, T, D, max_pages, page), int(bool(accumulate))
-    if window is None:
+    if window is None:  # the whole table, sinks included
         return int(_entry("swa_cache_attn_workspace_bytes")(*sizes, acc))
-    return int(_entry("swa_cache_attn_window_workspace_bytes")(*sizes, _int32(window), acc))
+    if not sinks:
+        return int(_entry("swa_cache_attn_window_workspace_bytes")(*sizes, _int32(window), acc))
+    return int(_entry("swa_cache_attn_sinks_workspace_bytes")(*sizes, _int32(window), _int32(sinks), acc))
 
 
 def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional[float] = None,
-                   new=None, accumulate: bool = False, out=None, lse=None, workspace=None):
+                   new=None, accumulate: bool = False, out=None, lse=None, workspace=None,
+                   sinks: int = 0):
     """Attention of the newest tokens over their cache: returns (o [B,Hq,T,D] in q's dtype, lse
     [B,Hq,T] fp32).
 
     q [B,Hq,T,D] bf16 or fp16, T <= 64: query t of sequence b sits at slot lens[b] + t (append its
-    key and value first) and sees the window's slots up to its own.  new (int32 [B], or None) says
+    key and value first) and sees the window's slots up to its own, and behind the window the first
+    `sinks` slots.  new (int32 [B], or None) says
     how many of the T tokens are real; the rows of the others get o = 0, lse = -inf.  accumulate
     adds to cache.weight what each cached token received.  The workspace (of
-    swa_cache_attn_workspace_bytes, for this window or any) is allocated here unless given.
+    swa_cache_attn_workspace_bytes, for this window and sinks or any) is allocated here unless given.
     """
     B, width, index = _tables(cache, table, lens, new)
     dev, (_, Hkv, page, D) = cache.held[5:]
@@ -316,16 +326,20 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
         lse = _t.empty(shape[:3], dtype=f32, device=dev)
     elif not _good(lse, shape[:3], f32, index):
         _check(lse, "lse", shape[:3], f32, dev)
-    window, accumulate = _int32(window), int(bool(accumulate))
+    window, sinks, accumulate = _int32(window), _int32(sinks), int(bool(accumulate))
     if workspace is None:
-        need = _attn_space(index, B, Hq, Hkv, T, D, width, page, window, accumulate)
+        need = _attn_space(index, B, Hq, Hkv, T, D, width, page, window, sinks, accumulate)
         workspace = _t.empty(need, dtype=_t.u8, device=dev)
         space = workspace.data_ptr(), need
     else:
         space = _space(workspace, dev)
-    _run("swa_cache_attn", index, cache._c(), table.data_ptr(), width, lens.data_ptr(),
-         _ptr(new), q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, T, window,
-         1.0 / math.sqrt(D) if scale is None else float(scale), accumulate, dt, *space)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    args = (cache._c(), table.data_ptr(), width, lens.data_ptr(), _ptr(new), q.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), B, Hq, T, window)
+    if sinks:
+        _run("swa_cache_attn_sinks", index, *args, sinks, scale, accumulate, dt, *space)
+    else:
+        _run("swa_cache_attn", index, *args, scale, accumulate, dt, *space)
     return out, lse
 
 

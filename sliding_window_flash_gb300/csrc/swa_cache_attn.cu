@@ -72,7 +72,9 @@ struct AttnDev {
   int R;             // query rows per kv head: G T
   int MT, RT, NRT;   // warps of a team, rows of an item, items per kv head
   int rows;          // rows an item stores: min(RT, R)
-  int window, parts, f16, page_log2;
+  Reach reach;       // window, sinks, and the first slot of the walk
+  int parts, f16, page_log2;
+  int whole;         // 0, or where items that one team finished leave a partial result all the same
   FastDiv div_t, div_nrt, div_per;  // T, NRT, items of a sequence
   float scale_log2;
   int64_t* first;    // [B + 1] chunks before each sequence
@@ -156,6 +158,7 @@ struct ItemState {
     int lo[2], hi[2];     // slots the two rows see, inclusive
   } tile[kTiles];
   float vref;
+  int sinks;            // slots below are seen whatever the window's first
   int any_lo, any_hi;   // slots any row sees
   int all_lo, all_hi;   // slots every real row sees
 };
@@ -224,8 +227,10 @@ __device__ __forceinline__ void process_chunk(ItemState<D, kTiles>& st, const ui
         s[y][j][2 + i] *= f1;
         if (kEdge) {
           const int slot = ci.slot + 8 * j + 2 * static_cast<int>(t) + i;
-          s[y][j][i] = slot >= tl.lo[0] && slot <= tl.hi[0] ? s[y][j][i] : SWA_NEG_INF;
-          s[y][j][2 + i] = slot >= tl.lo[1] && slot <= tl.hi[1] ? s[y][j][2 + i] : SWA_NEG_INF;
+          const bool sunk = slot < st.sinks;
+          s[y][j][i] = (sunk || slot >= tl.lo[0]) && slot <= tl.hi[0] ? s[y][j][i] : SWA_NEG_INF;
+          s[y][j][2 + i] =
+              (sunk || slot >= tl.lo[1]) && slot <= tl.hi[1] ? s[y][j][2 + i] : SWA_NEG_INF;
         }
         mx0 = fmaxf(mx0, s[y][j][i]);
         mx1 = fmaxf(mx1, s[y][j][2 + i]);
@@ -314,7 +319,7 @@ __device__ __forceinline__ void process_chunk(ItemState<D, kTiles>& st, const ui
         lds_words<W>(sv + x * C::kBoxBytes + at, v[e]);
         if (kEdge) {
           const int slot = ci.slot + static_cast<int>(row);
-          if (slot < st.any_lo || slot > st.any_hi) {
+          if ((slot < st.any_lo && slot >= st.sinks) || slot > st.any_hi) {
 #pragma unroll
             for (int w = 0; w < W; ++w) v[e][w] = 0u;
           }
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_new[b] = n;
       }
       own[i] = sum;
-      sum += chunk_count(len, n, a.window, CK);
+      sum += ChunkWalk(len, n, a.reach, CK).count;
     }
     int64_t scan = sum;
 #pragma unroll
@@ -422,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t rem = x - s_first[b] * per;
       const int hr = static_cast<int>(quotient(rem, nc));
       ci.item = b * per + hr;
-      ci.slot = (first_chunk(s_len[b], a.window, CK) +
-                 static_cast<int>(rem - static_cast<int64_t>(hr) * nc)) * CK;
+      ci.slot = ChunkWalk(s_len[b], 1, a.reach, CK)
+                    .at(static_cast<int>(rem - static_cast<int64_t>(hr) * nc)) * CK;
       const int page = page_of(c, c.table, b, ci.slot >> a.page_log2, c.max_pages);
       if (page >= 0) {
         ci.plane = page * c.Hkv + static_cast<int>(a.div_nrt.div(static_cast<uint32_t>(hr)));
@@ -467,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kSteps = D / 16;
   uint32_t qf[C::kQShared ? 1 : kTiles * kSteps][4];
   ItemState<D, kTiles> st = {};
-  int item = -1, b = 0, tile0 = 0, item_first = 0, item_chunks = 0;
+  int item = -1, b = 0, tile0 = 0, item_last = 0;
   size_t base = 0;  // first row of the item, of all rows
   bool begins = false;
   const int g = lane >> 2, t = lane & 3;
@@ -475,14 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Finishes the item after its chunk at `slot`.
   auto finish = [&](int slot) {
-    const bool ends = slot / CK == item_first + item_chunks - 1;
+    const bool ends = slot / CK == item_last;
 #pragma unroll
     for (int ye = 0; ye < 2 * kTiles; ++ye) {
       const int e = ye & 1, r = r0 + 8 * ye;
       const auto& tl = st.tile[ye >> 1];
       const float l = quad_sum(tl.l[e]);
       if (tile0 + r >= a.R) continue;
-      if (begins && ends) {
+      if (begins && ends && a.whole == 0) {
         const float inv = l == 0.f ? 0.f : st.vref / l;
         uint16_t* out = a.o + (base + r) * D;
 #pragma unroll
@@ -505,7 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (t == 0) a.lse[base + r] = l == 0.f ? SWA_NEG_INF : (tl.m[e] + log2f(l)) * kLn2;
       } else {
-        const size_t slot_row = static_cast<size_t>(partial_slot(part, begins)) * a.rows + r;
+        const int at = begins && ends ? a.whole + item : partial_slot(part, begins);
+        const size_t slot_row = static_cast<size_t>(at) * a.rows + r;
         float* out = a.po + slot_row * D;
 #pragma unroll
         for (int x = 0; x < (D > 128 ? 2 : 1); ++x) {
@@ -547,17 +553,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) raw[e][i] = real ? __ldg(row + 4 * i) : make_uint2(0u, 0u);
       auto& tl = st.tile[e >> 1];
-      tl.lo[e & 1] = visible_lo(len + tq, a.window);
+      tl.lo[e & 1] = visible_lo(len + tq, a.reach.window);
       tl.hi[e & 1] = real ? len + tq : -1;
       tl.m[e & 1] = SWA_NEG_INF;
       tl.l[e & 1] = 0.f;
     }
-    item_first = first_chunk(len, a.window, CK);
-    item_chunks = chunk_count(len, n, a.window, CK);
-    begins = slot / CK == item_first;
-    st.any_lo = visible_lo(len, a.window);
+    const ChunkWalk walk(len, n, a.reach, CK);
+    item_last = walk.last();
+    begins = slot / CK == walk.at(0);
+    st.sinks = a.reach.sinks;
+    st.any_lo = visible_lo(len, a.reach.window);
     st.any_hi = len + n - 1;
-    st.all_lo = visible_lo(len + n - 1, a.window);
+    st.all_lo = visible_lo(len + n - 1, a.reach.window);
     st.all_hi = n < c.T ? -1 : len;  // a row without a query sees nothing
 #pragma unroll
     for (int ye = 0; ye < 2 * kTiles; ++ye) {
@@ -632,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sk = ring + static_cast<uint32_t>(s) * C::kStageBytes;
     float* sc = a.scores == nullptr ? nullptr
                                     : a.scores + static_cast<size_t>(begin + i) * a.rows * CK;
-    const bool edge = ci.plane < 0 || ci.slot < st.all_lo || ci.slot + CK - 1 > st.all_hi;
+    const bool edge = ci.plane < 0 || (ci.slot < st.all_lo && ci.slot + CK > st.sinks) ||
+                      ci.slot + CK - 1 > st.all_hi;
     if (edge) {
       ItemState<D, kTiles>& e = st;
       int lo[2 * kTiles];
@@ -642,11 +650,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         lo[y] = e.tile[y >> 1].lo[y & 1];
         if (ci.plane < 0) e.tile[y >> 1].lo[y & 1] = INT_MAX;  // nothing of it is seen
       }
-      if (ci.plane < 0) e.any_lo = INT_MAX;
+      if (ci.plane < 0) {
+        e.any_lo = INT_MAX;
+        e.sinks = 0;
+      }
       process_chunk<D, kTiles, true>(e, qf, sq, sk, ci, sc, a.rows, wt * 16 * kTiles);
 #pragma unroll
       for (int y = 0; y < 2 * kTiles; ++y) e.tile[y >> 1].lo[y & 1] = lo[y];
       e.any_lo = any;
+      e.sinks = a.reach.sinks;
     } else {
       process_chunk<D, kTiles, false>(st, qf, sq, sk, ci, sc, a.rows, wt * 16 * kTiles);
     }
@@ -935,7 +947,7 @@ __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView 
       const int64_t rem = y - f0 * c.Hkv;
       const int h = static_cast<int>(quotient(rem, stride));
       const int cc = static_cast<int>(rem - static_cast<int64_t>(h) * stride);
-      const int slot = (first_chunk(c.lens[b], a.window, CK) + cc) * CK;
+      const int slot = ChunkWalk(c.lens[b], 1, a.reach, CK).at(cc) * CK;
       const int page = page_of(c, c.table, b, slot >> a.page_log2, c.max_pages);
       if (page >= 0)
         weight = (static_cast<int64_t>(page) * c.Hkv + h) * c.page + (slot & (c.page - 1));
@@ -986,7 +998,7 @@ constexpr size_t kScoreUnit = 2 << 20;
 
 // The workspace's layout is the same for every window; the scores, at its end, are fewer under a smaller
 // one.
-Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int accumulate, int window) {
+Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int accumulate, Reach reach) {
   Plan p;
   p.R = Hq / Hkv * T;
   p.ck = D == 256 ? AttnCfg<256>::CK : AttnCfg<128>::CK;
@@ -996,7 +1008,9 @@ Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int 
   p.NRT = (p.R + p.RT - 1) / p.RT;
   p.rows = p.R < p.RT ? p.R : p.RT;
   const int64_t slots = static_cast<int64_t>(max_pages) * page;
-  const int64_t chunks = most_chunks(T, window, slots, p.ck);  // of an item
+  const int64_t chunks = reach.sinks == 0 && reach.base == 0  // of an item
+                             ? most_chunks(T, reach.window, slots, p.ck)
+                             : most_chunks(T, reach, slots, p.ck);
   p.tiles = 1;
   size_t parts = static_cast<size_t>(sm_count()) * (kWarps / p.MT);
   if (p.R > 16 && D < 256) {
@@ -1048,6 +1062,8 @@ cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+Reach args_reach(const CacheAttnArgs& args) { return {args.window, args.sinks, 0}; }
+
 template <int D, int kTiles>
 cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan& p,
                      cudaStream_t stream) {
@@ -1066,7 +1082,8 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
   a.RT = p.RT;
   a.NRT = p.NRT;
   a.rows = p.rows;
-  a.window = args.window;
+  a.reach = args_reach(args);
+  a.whole = 0;
   a.parts = p.parts;
   a.f16 = args.dtype == SWA_FP16;
   a.scale_log2 = args.scale * kLog2e;
@@ -1123,12 +1140,13 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
-                                  int window, int accumulate) {
-  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate, window).bytes;
+                                  int window, int sinks, int accumulate) {
+  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate, {window, sinks, 0}).bytes;
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream) {
-  const Plan p = plan_of(c.B, a.Hq, c.Hkv, c.T, c.D, c.max_pages, c.page, a.accumulate, a.window);
+  const Plan p =
+      plan_of(c.B, a.Hq, c.Hkv, c.T, c.D, c.max_pages, c.page, a.accumulate, args_reach(a));
   if (c.D == 64)
     return p.tiles == 2 ? launch_d<64, 2>(c, a, p, stream) : launch_d<64, 1>(c, a, p, stream);
   if (c.D == 128)

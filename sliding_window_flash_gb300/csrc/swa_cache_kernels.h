@@ -114,13 +114,13 @@ struct CacheAttnArgs {
   const void* q;
   void* o;
   float* lse;
-  int Hq, window;
+  int Hq, window, sinks;
   float scale;
   int accumulate, dtype;
   void* workspace;
 };
 size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
-                                  int window, int accumulate);
+                                  int window, int sinks, int accumulate);
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream);
 
 struct CacheEvictArgs {

@@ -1,7 +1,8 @@
 // swa_cache_split.h — how the attention over the paged cache divides its work, in functions that the
 // host, the kernels and the CPU tests share.
 //
-// The visible slots of a sequence are cut at multiples of CK slots into chunks.  All chunks of all
+// The visible slots of a sequence (with sinks also those of its first slots that lie before the
+// window) are cut at multiples of CK slots into chunks.  All chunks of all
 // items (sequence, kv head, tile of query rows) form one list, item after item; the list is cut into
 // as many parts as there are teams of warps, or fewer where their partial results would be more than
 // they are worth, equal within one chunk whatever the sequences' lengths.
@@ -35,6 +36,37 @@ SWA_HD int chunk_count(int len, int n, int window, int ck) {
 SWA_HD int64_t most_chunks(int T, int window, int64_t slots, int ck) {
   const int64_t span = static_cast<int64_t>(window) + T - 1;
   return ((span < slots ? span : slots) + ck - 2) / ck + 1;
+}
+
+// Which slots a walk is about: those that the window or the sinks show, from slot `base` (a multiple
+// of CK) on.
+struct Reach {
+  int window, sinks, base;
+};
+
+// A sequence's chunks in order: `far` chunks from `far0` on, of sinks before the window, then the
+// window's from `first` on; `count` in all.
+struct ChunkWalk {
+  int far0, far, first, count;
+  SWA_HD ChunkWalk(int len, int n, Reach r, int ck) {
+    const int base = r.base / ck, stop = (r.sinks + ck - 1) / ck, wide = first_chunk(len, r.window, ck);
+    first = wide > base ? wide : base;
+    far0 = base;
+    far = (stop < first ? stop : first) - base;
+    if (far < 0) far = 0;
+    const int end = len + n;
+    count = n > 0 && end > r.base ? (end - 1) / ck - first + 1 + far : 0;
+  }
+  // Chunk i, and the last one.
+  SWA_HD int at(int i) const { return i < far ? far0 + i : first + (i - far); }
+  SWA_HD int last() const { return at(count - 1); }
+};
+
+// Most chunks of a walk in a table of `slots`.
+SWA_HD int64_t most_chunks(int T, Reach r, int64_t slots, int ck) {
+  const int64_t near = most_chunks(T, r.window, slots, ck), far = (static_cast<int64_t>(r.sinks) + ck - 1) / ck;
+  const int64_t all = (slots - r.base) / ck;
+  return near + far < all ? near + far : all;
 }
 
 // x / d for 0 <= x, 1 <= d, in 32 bits where they fit (a 64-bit division costs ten times as much).
