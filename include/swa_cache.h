@@ -129,6 +129,29 @@ swa_status swa_cache_attn_sinks(const swa_cache* cache, const int* table, int ma
                                 cudaStream_t stream);
 
 /*
+ * The same for a batch whose sequences begin with the same text: the first `shared` entries of every
+ * table are the same pages (0 <= shared <= max_pages), and their slots are walked once for the rows of all
+ * sequences, by the first table's entries, instead of once for each.  Lengths count from slot 0 as ever; the
+ * result is that of swa_cache_attn_sinks up to rounding, for any lengths, sequences shorter than the shared
+ * pages among them.
+ *   accumulate : has to be 0 with shared > 0 (the weights of shared pages would be added to by all
+ *                sequences at once); (Hq / Hkv) T <= 65536 then.
+ *   workspace  : at least swa_cache_attn_shared_workspace_bytes bytes, on the terms of swa_cache_attn's.
+ * Where the pages that one product takes together (128 slots; 64 at D = 256) have value scales that
+ * differ by more than 2^8, a value keeps an absolute error of 2^-25 of the largest of these scales.
+ * Scores, statistics and sums are fp32, p is rounded to fp16 as in swa_cache_attn.  The same call on one GPU
+ * gives the same bits.
+ */
+size_t swa_cache_attn_shared_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
+                                             int page, int window, int sinks, int shared,
+                                             int accumulate);
+swa_status swa_cache_attn_shared(const swa_cache* cache, const int* table, int max_pages,
+                                 const int* lens, const int* new_lens, const void* q, void* o,
+                                 float* lse, int B, int Hq, int T, int window, int sinks, int shared,
+                                 float scale, int accumulate, int dtype, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Eviction: cuts each sequence and kv head to min(lens[b], budget) tokens.  When lens[b] > budget
  * the last `recent` slots stay, and of the others the budget - recent with the largest accumulated
  * weight (equal weights: the lower slot; NaN above every number); the survivors keep their order.

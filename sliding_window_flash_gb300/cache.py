@@ -59,6 +59,12 @@ SIGNATURES = {
         [_cp, _vp, _c_int] + [_vp] * 5 + [_c_int] * 5 + [_c_float] + [_c_int] * 2 +
         [_vp, ctypes.c_size_t, _vp],
     ),
+    "swa_cache_attn_shared_workspace_bytes": (ctypes.c_size_t, [_c_int] * 11),
+    "swa_cache_attn_shared": (
+        _c_int,
+        [_cp, _vp, _c_int] + [_vp] * 5 + [_c_int] * 6 + [_c_float] + [_c_int] * 2 +
+        [_vp, ctypes.c_size_t, _vp],
+    ),
     "swa_cache_evict": (
         _c_int, [_cp, _vp, _c_int, _vp, _vp] + [_c_int] * 3 + [_vp, _vp, _c_int, _vp]),
     "swa_attn_key_weights_workspace_bytes": (ctypes.c_size_t, [_c_int] * 8),
@@ -276,7 +282,7 @@ def swa_cache_append(cache: SwaCache, table, lens, k, v, new=None, weight=None) 
 # A workspace's size follows the number of the GPU's SMs, so it is asked for, and kept, for that GPU.
 @functools.lru_cache(maxsize=256)
 def _attn_space(index, *sizes):
-    return int(_on(index, "swa_cache_attn_sinks_workspace_bytes", *sizes))
+    return int(_on(index, "swa_cache_attn_shared_workspace_bytes", *sizes))
 
 
 @functools.lru_cache(maxsize=256)
@@ -286,9 +292,13 @@ def _weights_space(index, *sizes):
 
 def swa_cache_attn_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, max_pages: int,
                                    page: int, accumulate: bool = False,
-                                   window: Optional[int] = None, sinks: int = 0) -> int:
+                                   window: Optional[int] = None, sinks: int = 0,
+                                   shared: int = 0) -> int:
     """Bytes of swa_cache_attn's workspace on the current GPU, for this window or (None) for any."""
     sizes, acc = (B, Hq, Hkv, T, D, max_pages, page), int(bool(accumulate))
+    if shared:
+        return int(_entry("swa_cache_attn_shared_workspace_bytes")(
+            *sizes, 2**31 - 1 if window is None else _int32(window), _int32(sinks), _int32(shared), acc))
     if window is None:  # the whole table, sinks included
         return int(_entry("swa_cache_attn_workspace_bytes")(*sizes, acc))
     if not sinks:
@@ -298,7 +308,7 @@ def swa_cache_attn_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, ma
 
 def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional[float] = None,
                    new=None, accumulate: bool = False, out=None, lse=None, workspace=None,
-                   sinks: int = 0):
+                   sinks: int = 0, shared: int = 0):
     """Attention of the newest tokens over their cache: returns (o [B,Hq,T,D] in q's dtype, lse
     [B,Hq,T] fp32).
 
@@ -306,8 +316,10 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     key and value first) and sees the window's slots up to its own, and behind the window the first
     `sinks` slots.  new (int32 [B], or None) says
     how many of the T tokens are real; the rows of the others get o = 0, lse = -inf.  accumulate
-    adds to cache.weight what each cached token received.  The workspace (of
-    swa_cache_attn_workspace_bytes, for this window and sinks or any) is allocated here unless given.
+    adds to cache.weight what each cached token received.  shared says that the first `shared` entries
+    of all tables are the same pages: their slots are walked once for all sequences (without
+    accumulate).  The workspace (of swa_cache_attn_workspace_bytes, for this window, sinks and shared;
+    without shared also for any window) is allocated here unless given.
     """
     B, width, index = _tables(cache, table, lens, new)
     dev, (_, Hkv, page, D) = cache.held[5:]
@@ -326,9 +338,10 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
         lse = _t.empty(shape[:3], dtype=f32, device=dev)
     elif not _good(lse, shape[:3], f32, index):
         _check(lse, "lse", shape[:3], f32, dev)
-    window, sinks, accumulate = _int32(window), _int32(sinks), int(bool(accumulate))
+    window, accumulate = _int32(window), int(bool(accumulate))
+    sinks, shared = sinks and _int32(sinks), shared and _int32(shared)
     if workspace is None:
-        need = _attn_space(index, B, Hq, Hkv, T, D, width, page, window, sinks, accumulate)
+        need = _attn_space(index, B, Hq, Hkv, T, D, width, page, window, sinks, shared, accumulate)
         workspace = _t.empty(need, dtype=_t.u8, device=dev)
         space = workspace.data_ptr(), need
     else:
@@ -336,7 +349,9 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     args = (cache._c(), table.data_ptr(), width, lens.data_ptr(), _ptr(new), q.data_ptr(),
             out.data_ptr(), lse.data_ptr(), B, Hq, T, window)
-    if sinks:
+    if shared:
+        _run("swa_cache_attn_shared", index, *args, sinks, shared, scale, accumulate, dt, *space)
+    elif sinks:
         _run("swa_cache_attn_sinks", index, *args, sinks, scale, accumulate, dt, *space)
     else:
         _run("swa_cache_attn", index, *args, scale, accumulate, dt, *space)

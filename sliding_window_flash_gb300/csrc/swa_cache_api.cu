@@ -35,6 +35,12 @@ int sinks_seen(int window, int sinks, int max_pages, int page) {
   return window >= slots ? 0 : sinks < slots ? sinks : slots;
 }
 
+// Query rows of a sequence and kv head that a call with a shared prefix takes.
+constexpr int kSharedRows = 65536;
+
+// Slots that are walked once for all sequences: a single sequence shares them with nobody.
+int prefix_slots(int B, int shared, int page) { return B > 1 ? shared * page : 0; }
+
 // The checks every cache call makes of the cache, its table and lengths.
 swa_status check_cache(const swa_cache* c, const int* table, int max_pages, const int* lens, int B) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !table || !lens)
@@ -128,16 +134,25 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
                                                                                  : SWA_ERR_CUDA;
 }
 
-size_t swa_cache_attn_sinks_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
-                                            int page, int window, int sinks, int accumulate) {
-  if (sinks < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > swa::kMaxCacheQueries ||
+size_t swa_cache_attn_shared_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
+                                             int page, int window, int sinks, int shared,
+                                             int accumulate) {
+  if (sinks < 0 || shared < 0 || shared > max_pages || (shared > 0 && accumulate) || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > swa::kMaxCacheQueries ||
       max_pages < 1 || window < 1 || (D != 64 && D != 128 && D != 256) ||
       (page != 32 && page != 64 && page != 128) ||
-      !sizes_fit(B, Hkv, max_pages, page) || !rows_fit(B, Hq, T))
+      !sizes_fit(B, Hkv, max_pages, page) || !rows_fit(B, Hq, T) ||
+      (shared > 0 && Hq / Hkv * T > kSharedRows))
     return 0;
   return swa::cache_attn_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page,
                                          slots_seen(window, max_pages, page),
-                                         sinks_seen(window, sinks, max_pages, page), accumulate);
+                                         sinks_seen(window, sinks, max_pages, page),
+                                         prefix_slots(B, shared, page), accumulate);
+}
+
+size_t swa_cache_attn_sinks_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
+                                            int page, int window, int sinks, int accumulate) {
+  return swa_cache_attn_shared_workspace_bytes(B, Hq, Hkv, T, D, max_pages, page, window, sinks, 0,
+                                               accumulate);
 }
 
 size_t swa_cache_attn_window_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
@@ -163,6 +178,15 @@ swa_status swa_cache_attn_sinks(const swa_cache* cache, const int* table, int ma
                                 float* lse, int B, int Hq, int T, int window, int sinks, float scale,
                                 int accumulate, int dtype, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream) {
+  return swa_cache_attn_shared(cache, table, max_pages, lens, new_lens, q, o, lse, B, Hq, T, window,
+                               sinks, 0, scale, accumulate, dtype, workspace, workspace_bytes, stream);
+}
+
+swa_status swa_cache_attn_shared(const swa_cache* cache, const int* table, int max_pages,
+                                 const int* lens, const int* new_lens, const void* q, void* o,
+                                 float* lse, int B, int Hq, int T, int window, int sinks, int shared,
+                                 float scale, int accumulate, int dtype, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
   swa_status st = check_cache(cache, table, max_pages, lens, B);
   if (st != SWA_OK) return st;
   if (!q || !o || !lse || Hq < 1 || Hq % cache->Hkv != 0 || window < 1) return SWA_ERR_INVALID_ARG;
@@ -172,8 +196,11 @@ swa_status swa_cache_attn_sinks(const swa_cache* cache, const int* table, int ma
     return SWA_ERR_INVALID_ARG;
   if (accumulate && !cache->weight) return SWA_ERR_INVALID_ARG;
   if (sinks < 0 || !rows_fit(B, Hq, T)) return SWA_ERR_INVALID_ARG;
-  const size_t need = swa_cache_attn_sinks_workspace_bytes(
-      B, Hq, cache->Hkv, T, cache->D, max_pages, cache->page, window, sinks, accumulate);
+  if (shared < 0 || shared > max_pages || (shared > 0 && accumulate) ||
+      (shared > 0 && Hq / cache->Hkv * T > kSharedRows))
+    return SWA_ERR_INVALID_ARG;
+  const size_t need = swa_cache_attn_shared_workspace_bytes(
+      B, Hq, cache->Hkv, T, cache->D, max_pages, cache->page, window, sinks, shared, accumulate);
   if (need != 0 && (!workspace || workspace_bytes < need)) return SWA_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
       !aligned(new_lens, 4))
@@ -188,6 +215,7 @@ swa_status swa_cache_attn_sinks(const swa_cache* cache, const int* table, int ma
   a.Hq = Hq;
   a.window = slots_seen(window, max_pages, cache->page);
   a.sinks = sinks_seen(window, sinks, max_pages, cache->page);
+  a.base = prefix_slots(B, shared, cache->page);
   a.scale = scale;
   a.accumulate = accumulate;
   a.dtype = dtype;

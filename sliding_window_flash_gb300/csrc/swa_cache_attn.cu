@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "swa_cache_kernels.h"
+#include "swa_cache_prefix.h"
 #include "swa_cache_split.h"
 #include "swa_ptx.cuh"
 #include "swa_tmap.h"
@@ -918,6 +919,91 @@ __global__ void __launch_bounds__(256) swa_cache_join_few_kernel(const CacheView
   }
 }
 
+// With a shared prefix: joins what the parts of the prefix's items and the parts of a sequence's own slots
+// left for a row.  A warp for 16 columns of a row: 8 groups of 4 lanes take the partials in turn.
+template <int D>
+__global__ void __launch_bounds__(256)
+    swa_cache_join_shared_kernel(const CacheView c, const AttnDev a, const PrefixDev p) {
+  constexpr uint32_t kRuns = D / 16;
+  wait_predecessor();
+  launch_dependents();
+  const int lane = static_cast<int>(lane_id()), group = lane / 4, sub = lane % 4;
+  const int per = c.Hkv * a.NRT;
+  const int64_t total = a.first[c.B] * per, ptotal = p.first[p.tiles] * c.Hkv;
+  const Parts cut(total, used_parts(total, a.parts, a.rows * D));
+  const Parts pcut(ptotal, used_parts(ptotal, p.parts, p.stored * D));
+  const int64_t tasks = static_cast<int64_t>(c.B) * c.Hkv * a.R * kRuns;
+  for (int64_t task = blockIdx.x * 8 + warp_id(); task < tasks; task += gridDim.x * 8) {
+    const int run = static_cast<int>(task % kRuns);
+    const uint32_t row = static_cast<uint32_t>(task / kRuns), bh = p.div_r.div(row),
+                   b = p.div_hkv.div(bh);
+    const int r = static_cast<int>(row - bh * p.div_r.d), h = static_cast<int>(bh - b * p.div_hkv.d);
+    float top = SWA_NEG_INF, l = 0.f;
+    float o[4] = {};
+    int len, n;
+    if (sequence_of(c, static_cast<int>(b), &len, &n) &&
+        static_cast<int>(a.div_t.mod(static_cast<uint32_t>(r))) < n) {
+      // the sequence's own slots
+      const int rt = r / a.RT, item = static_cast<int>(bh) * a.NRT + rt;
+      const ItemParts ip = item_parts(a, cut, per, item);
+      const int own = ip.chunks > 0 ? ip.p1 - ip.p0 + 1 : 0;
+      // the prefix
+      const int rho = static_cast<int>(b) * a.R + r, j = rho / kPrefixRows;
+      const int64_t f0 = p.first[j], chunks = p.first[j + 1] - f0;
+      const int64_t x0 = f0 * c.Hkv + h * chunks;
+      const int q0 = chunks > 0 ? pcut.of(x0) : 0;
+      const int q1 = chunks > 0 ? pcut.of(x0 + chunks - 1) : -1;
+      const int all = own + q1 - q0 + 1;
+      auto source = [&](int k, const float** ml) -> const float* {
+        if (k < own) {
+          const int part = ip.p0 + k;
+          const int at = own == 1 ? a.whole + item : partial_slot(part, cut.start(part) <= ip.x0);
+          const size_t to = static_cast<size_t>(at) * a.rows + (r - rt * a.RT);
+          *ml = a.ml + to * 2;
+          return a.po + to * D;
+        }
+        const int part = q0 + k - own;
+        const int at = q0 == q1 ? 2 * p.parts + j * c.Hkv + h
+                                : partial_slot(part, pcut.start(part) <= x0);
+        const size_t to = static_cast<size_t>(at) * p.stored + (rho - j * kPrefixRows);
+        *ml = p.ml + to * 2;
+        return p.po + to * D;
+      };
+      const float* ml;
+      for (int k = lane; k < all; k += 32) {
+        source(k, &ml);
+        top = fmaxf(top, ml[0]);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float base = top == SWA_NEG_INF ? 0.f : top;
+      for (int k = group; k < all; k += 8) {
+        const float* y = source(k, &ml);
+        const float2 s = *reinterpret_cast<const float2*>(ml);
+        if (s.x == SWA_NEG_INF && s.y == 0.f) continue;  // the row saw nothing there
+        const float4 v = *reinterpret_cast<const float4*>(y + run * 16 + sub * 4);
+        const float w = ex2(s.x - base);
+        l += w * s.y;
+        o[0] += w * v.x;
+        o[1] += w * v.y;
+        o[2] += w * v.z;
+        o[3] += w * v.w;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], d);
+      }
+    }
+    if (group == 0) {
+      store_row<4>(a, a.o + static_cast<size_t>(row) * D + run * 16 + sub * 4, o, l == 0.f ? 0.f : 1.f / l);
+      if (lane == 0 && run == 0) a.lse[row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
+    }
+  }
+}
+
 // Adds to each cached token's weight the sum over its kv head's rows of 2^(score - lse / ln 2).  The
 // lanes of a warp find the places of up to 32 chunks at once; then it takes 128 keys at a time, four a
 // lane, and one thread alone touches a weight.
@@ -989,7 +1075,10 @@ __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView 
 
 struct Plan {
   int R, tiles, MT, RT, NRT, rows, parts, ck;
+  int group;  // sequences per launch
   size_t off_ml, off_po, off_scores, bytes;
+  size_t off_prefix;  // with a shared prefix: the workspace of its walk
+  PrefixPlan prefix;
 };
 
 // Scores take whole units of this size, so that small tables have one size for every window (torch's
@@ -1028,10 +1117,22 @@ Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int 
   p.parts = sm_count() * (kWarps / p.MT);
   auto round = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   size_t off = round((kMaxSeqs + 1) * sizeof(int64_t));
+  // partial results: two a part, and with a shared prefix one for every item that one team finishes
+  size_t held = 2 * parts;
+  p.group = kMaxSeqs;
+  if (reach.base > 0) {
+    p.group = prefix_group(kMaxSeqs, p.R);
+    held += static_cast<size_t>(B < p.group ? B : p.group) * Hkv * p.NRT;
+  }
   p.off_ml = off;
-  off += round(2 * parts * p.rows * 2 * sizeof(float));
+  off += round(held * p.rows * 2 * sizeof(float));
   p.off_po = off;
-  off += round(2 * parts * p.rows * D * sizeof(float));
+  off += round(held * p.rows * D * sizeof(float));
+  p.off_prefix = off;
+  if (reach.base > 0) {
+    p.prefix = prefix_plan(B < p.group ? B : p.group, Hkv, p.R, D, reach.base);
+    off += round(p.prefix.bytes);
+  }
   p.off_scores = off;
   if (accumulate) {
     // The scores of all chunks that can be seen, in whole units, and no more than the table has (64
@@ -1062,7 +1163,7 @@ cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-Reach args_reach(const CacheAttnArgs& args) { return {args.window, args.sinks, 0}; }
+Reach args_reach(const CacheAttnArgs& args) { return {args.window, args.sinks, args.base}; }
 
 template <int D, int kTiles>
 cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan& p,
@@ -1083,7 +1184,7 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
   a.NRT = p.NRT;
   a.rows = p.rows;
   a.reach = args_reach(args);
-  a.whole = 0;
+  a.whole = args.base > 0 ? 2 * p.parts : 0;
   a.parts = p.parts;
   a.f16 = args.dtype == SWA_FP16;
   a.scale_log2 = args.scale * kLog2e;
@@ -1095,9 +1196,27 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
   a.ml = reinterpret_cast<float*>(ws + p.off_ml);
   a.po = reinterpret_cast<float*>(ws + p.off_po);
   a.scores = args.accumulate ? reinterpret_cast<float*>(ws + p.off_scores) : nullptr;
-  for (int b0 = 0; b0 < all.B; b0 += kMaxSeqs) {
+  PrefixDev pd;
+  if (args.base > 0) {
+    pd.table = all.table;
+    pd.R = p.R;
+    pd.reach = a.reach;
+    pd.f16 = a.f16;
+    pd.page_log2 = a.page_log2;
+    pd.parts = p.prefix.parts;
+    pd.stored = p.prefix.stored;
+    pd.div_t = a.div_t;
+    pd.div_r = FastDiv(static_cast<uint32_t>(p.R));
+    pd.div_hkv = FastDiv(static_cast<uint32_t>(all.Hkv));
+    pd.scale_log2 = a.scale_log2;
+    uint8_t* pws = ws + p.off_prefix;
+    pd.first = reinterpret_cast<int64_t*>(pws);
+    pd.ml = reinterpret_cast<float*>(pws + p.prefix.off_ml);
+    pd.po = reinterpret_cast<float*>(pws + p.prefix.off_po);
+  }
+  for (int b0 = 0; b0 < all.B; b0 += p.group) {
     CacheView c = all;
-    c.B = all.B - b0 < kMaxSeqs ? all.B - b0 : kMaxSeqs;
+    c.B = all.B - b0 < p.group ? all.B - b0 : p.group;
     c.table += static_cast<size_t>(b0) * all.max_pages;
     c.lens += b0;
     if (c.new_lens) c.new_lens += b0;
@@ -1108,6 +1227,18 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
     swa_cache_attn_kernel<D, kTiles>
         <<<p.parts / (kWarps / p.MT), kThreads, C::kSmemBytes, stream>>>(tk, tv, c, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (args.base > 0) {
+      pd.q = a.q;
+      pd.rows = c.B * p.R;
+      pd.tiles = (pd.rows + kPrefixRows - 1) / kPrefixRows;
+      if ((e = launch_cache_prefix(c, pd, stream)) != cudaSuccess) return e;
+      const int64_t need = (static_cast<int64_t>(c.B) * c.Hkv * p.R * (D / 16) + 7) / 8;
+      const int64_t limit = 8ll * sm_count();
+      e = launch_after(swa_cache_join_shared_kernel<D>,
+                       static_cast<unsigned>(need < limit ? need : limit), stream, c, a, pd);
+      if (e != cudaSuccess) return e;
+      continue;
+    }
     // A warp a row where that fills the SMs; else a warp 16 columns of a row; and a block for them where
     // even those are few.  (us of the whole call, a window of 1024, 32 / 8 heads, D = 128, as a row / a
     // warp / a block: 1 sequence - / 12.6 / 11.2, 4 sequences 20.2 / 14 / 15.1, 16 sequences 21 / 18.6 /
@@ -1140,8 +1271,8 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
-                                  int window, int sinks, int accumulate) {
-  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate, {window, sinks, 0}).bytes;
+                                  int window, int sinks, int base, int accumulate) {
+  return plan_of(B, Hq, Hkv, T, D, max_pages, page, accumulate, {window, sinks, base}).bytes;
 }
 
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream) {

@@ -115,12 +115,13 @@ struct CacheAttnArgs {
   void* o;
   float* lse;
   int Hq, window, sinks;
+  int base;  // slots of the shared prefix
   float scale;
   int accumulate, dtype;
   void* workspace;
 };
 size_t cache_attn_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages, int page,
-                                  int window, int sinks, int accumulate);
+                                  int window, int sinks, int base, int accumulate);
 cudaError_t launch_cache_attn(const CacheView& c, const CacheAttnArgs& a, cudaStream_t stream);
 
 struct CacheEvictArgs {

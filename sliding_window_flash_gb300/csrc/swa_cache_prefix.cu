@@ -1,0 +1,716 @@
+// swa_cache_prefix.cu — attention of a batch over the prefix whose pages all its sequences share: the
+// prefix is walked once for the rows of all sequences instead of once for each sequence.
+//
+// The B G T query rows of a kv head meet the same keys, so this is a product of matrices again: 4 D
+// flops for each row and slot against 2 D bytes a slot, which the memory bounds up to some 150 rows and
+// the tensor cores beyond.  A CTA takes 128 rows of a kv head and a part of their chunks (128 keys, 64 at
+// D = 256), on tcgen05:
+//   * 4 warps turn codes into fp16 operands: a chunk's codes are read from global memory a chunk ahead into
+//     registers, converted (exact, cvt.f16x2.e4m3x2) and stored in the swizzled layouts of the tensor core,
+//     keys K-major, values MN-major, which is how tokens lie anyway.
+//   * One warp issues S = Q K^T two chunks ahead of O += P V; P goes back to TMEM as the A operand.
+//   * 8 warps are the softmax, two threads a row, against a running maximum that moves only when a block's
+//     sum calls for it.
+// q is taken as fp16 after scaling each row by a power of two, as in swa_cache_attn.cu.  Keys carry their
+// block's scale into the scores' factor; values carry theirs relative to a reference that stays within
+// 2^6 of the chunk's largest, so that o is rarely rescaled.
+// Parts leave fp32 partial results; swa_cache_attn.cu joins them with those of the slots behind the prefix.
+#include <climits>
+
+#include "swa_cache_prefix.h"
+#include "swa_ptx.cuh"
+
+namespace swa {
+namespace {
+
+constexpr float kRescaleThreshold = 8.0f;  // the maximum moves past 2^8
+constexpr float kFastSumLimit = 4096.0f;   // a chunk's one-pass sum stands up to 2^12
+
+template <int D>
+struct PrefixCfg {
+  static constexpr int KT = D == 256 ? 64 : 128;  // keys of a chunk
+  static constexpr int kGroups = KT / 32;         // of 32 keys, each inside one page
+  static constexpr int kQBytes = kPrefixRows * D * 2;
+  static constexpr int kQChunk = kPrefixRows * 128;
+  static constexpr int kKVBytes = KT * D * 2;
+  static constexpr int kKVChunk = KT * 128;
+  static constexpr int kKStages = D == 256 ? 2 : 3;
+  static constexpr int kVStages = 2;
+  static constexpr int kOffK = kQBytes;
+  static constexpr int kOffV = kOffK + kKStages * kKVBytes;
+  static constexpr int kOffFirst = kOffV + kVStages * kKVBytes;
+  static constexpr int kOffRange = kOffFirst + (kPrefixTiles + 2) * 8;
+  static constexpr int kOffRed = kOffRange + kPrefixTiles * 16;  // [2 slots][2 halves][128] fp32
+  static constexpr int kOffBar = kOffRed + 2 * 2 * kPrefixRows * 4;
+  static constexpr int kQFull = 0;
+  static constexpr int kKFull = 1;
+  static constexpr int kKEmpty = kKFull + kKStages;
+  static constexpr int kVFull = kKEmpty + kKStages;
+  static constexpr int kVEmpty = kVFull + kVStages;
+  static constexpr int kSFull = kVEmpty + kVStages;  // 2
+  static constexpr int kPFull = kSFull + 2;          // 2
+  static constexpr int kPVDone = kPFull + 2;         // 2
+  static constexpr int kXch = kPVDone + 2;           // [4 lane quarters][2 slots]
+  static constexpr int kOEmpty = kXch + 8;
+  static constexpr int kDrain = kOEmpty + 1;
+  static constexpr int kNumBars = kDrain + 1;
+  static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;  // + TMEM address and abort flag
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  // TMEM: two S buffers, O, two P buffers of packed pairs
+  static constexpr uint32_t kColS = 0, kColO = 2 * KT, kColP = 2 * KT + D;
+  static_assert(kColP + KT <= 512, "tensor memory");
+  static constexpr int kSoftmaxWarps = 8, kConvertWarps = 4, kMmaWarp = 12;
+  static constexpr int kThreads = 32 * 13;
+};
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+
+// Codes 0, 1 (low half) and 2, 3 (high half) of a word as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The prefix slots that the rows of a tile see: the lowest length and the highest end of its sequences that
+// have queries, and the same the other way round (what all of them see).
+struct TileRange {
+  int len_min, end_max, len_max_q, end_min;  // len_max_q: the last query's slot of the longest
+};
+
+// The chunks of a tile in order, as ChunkWalk.
+struct TileWalk {
+  int far, first, count;
+  __device__ TileWalk(const TileRange& t, const Reach& r, int ck) {
+    const int end = min(t.end_max, r.base);  // slots from here on nobody sees
+    const int last = end > 0 ? (end - 1) / ck : -1;
+    first = visible_lo(t.len_min, r.window) / ck;
+    far = min(min((r.sinks + ck - 1) / ck, first), last + 1);
+    count = far + max(0, last - first + 1);
+  }
+  __device__ int at(int i) const { return i < far ? i : first + (i - far); }
+};
+
+// What a lane holds about 32 keys: lane l those of group l % 4 of chunk l / 4 of the next eight.
+struct GroupInfo {
+  int plane;   // page * Hkv + head, or -1: nothing to be seen there
+  int item, slot;  // of the chunk
+  float ks, vs;
+  float vmax;  // largest value scale of the chunk's groups, 0 without any
+  bool whole;  // every group of the chunk has a plane
+};
+
+template <int D>
+__global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
+    swa_cache_prefix_kernel(const CacheView c, const PrefixDev a) {
+  using C = PrefixCfg<D>;
+  constexpr int KT = C::KT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!smem_base_ok(smem, c.err)) return;
+  int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
+  TileRange* s_range = reinterpret_cast<TileRange*>(smem + C::kOffRange);
+  float* s_red = reinterpret_cast<float*>(smem + C::kOffRed);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  const uint32_t sQ = smem_u32(smem), sK0 = smem_u32(smem + C::kOffK), sV0 = smem_u32(smem + C::kOffV);
+  const uint32_t warp = warp_id(), lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(bar(C::kQFull), C::kSoftmaxWarps);
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(bar(C::kKFull + s), C::kConvertWarps);
+      mbar_init(bar(C::kKEmpty + s), 1);
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(bar(C::kVFull + s), C::kConvertWarps);
+      mbar_init(bar(C::kVEmpty + s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(C::kSFull + b), 1);
+      mbar_init(bar(C::kPFull + b), C::kSoftmaxWarps);
+      mbar_init(bar(C::kPVDone + b), 1);
+    }
+    for (int x = 0; x < 8; ++x) mbar_init(bar(C::kXch + x), 2);  // the two warps of a lane quarter
+    mbar_init(bar(C::kOEmpty), C::kSoftmaxWarps);
+    mbar_init(bar(C::kDrain), 1);
+    fence_barrier_init();
+  }
+  // What each tile's rows see: a warp a tile, its lanes the tile's sequences.
+  for (int j = static_cast<int>(warp); j < a.tiles; j += C::kThreads / 32) {
+    const int b0 = static_cast<int>(a.div_r.div(static_cast<uint32_t>(j) * kPrefixRows));
+    const int last = min(a.rows, (j + 1) * kPrefixRows) - 1;
+    const int b1 = static_cast<int>(a.div_r.div(static_cast<uint32_t>(last)));
+    int len_min = INT_MAX, end_max = 0, q_max = 0, end_min = INT_MAX;
+    for (int b = b0 + static_cast<int>(lane); b <= b1; b += 32) {
+      int len, n;
+      if (!sequence_of(c, b, &len, &n) || n == 0) continue;
+      len_min = min(len_min, len);
+      end_max = max(end_max, len + n);
+      q_max = max(q_max, len + n - 1);
+      end_min = min(end_min, len + 1);
+    }
+    len_min = __reduce_min_sync(0xffffffffu, len_min);
+    end_max = __reduce_max_sync(0xffffffffu, end_max);
+    q_max = __reduce_max_sync(0xffffffffu, q_max);
+    end_min = __reduce_min_sync(0xffffffffu, end_min);
+    if (lane == 0) s_range[j] = TileRange{end_max > 0 ? len_min : 0, end_max, q_max, end_min};
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  if (warp == 0) {  // chunks before each tile
+    int64_t sum = 0;
+    for (int j0 = 0; j0 <= a.tiles; j0 += 32) {
+      const int j = j0 + static_cast<int>(lane);
+      const int64_t own = j < a.tiles ? TileWalk(s_range[j], a.reach, KT).count : 0;
+      int64_t scan = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, scan, d);
+        if (static_cast<int>(lane) >= d) scan += up;
+      }
+      if (j <= a.tiles) s_first[j] = sum + scan - own;
+      sum += __shfl_sync(0xffffffffu, scan, 31);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (blockIdx.x == 0)
+    for (int j = static_cast<int>(threadIdx.x); j <= a.tiles; j += C::kThreads) a.first[j] = s_first[j];
+
+  const int64_t total = s_first[a.tiles] * c.Hkv;
+  const Parts cut(total, used_parts(total, a.parts, a.stored * D));
+  const int part = static_cast<int>(blockIdx.x);
+  const int64_t begin = part < cut.parts ? cut.start(part) : total;
+  const int count = part < cut.parts ? static_cast<int>(cut.start(part + 1) - begin) : 0;
+
+  // Chunk i of the part, one of its groups.
+  auto load_info = [&](int i, int group) {
+    GroupInfo gi = {-1, -1, 0, 1.f, 0.f, 0.f, false};
+    if (i < count && group < C::kGroups) {
+      const int64_t x = begin + i;
+      const int j = sequence_at(s_first, a.tiles, c.Hkv, x);
+      const int64_t nc = s_first[j + 1] - s_first[j], rem = x - s_first[j] * c.Hkv;
+      const int h = static_cast<int>(quotient(rem, nc));
+      gi.item = j * c.Hkv + h;
+      gi.slot = TileWalk(s_range[j], a.reach, KT).at(static_cast<int>(rem - h * nc)) * KT;
+      const int slot = gi.slot + 32 * group;
+      if (slot < a.reach.base) {
+        const int page = page_of(c, a.table, 0, slot >> a.page_log2, c.max_pages);
+        if (page >= 0) {
+          gi.plane = page * c.Hkv + h;
+          gi.ks = c.k_scale[gi.plane];
+          gi.vs = c.v_scale[gi.plane];
+        }
+      }
+    }
+    const unsigned quad = 0xfu << (lane & 28u);
+    gi.whole = (__ballot_sync(0xffffffffu, gi.plane >= 0) & quad) ==
+               (quad & (C::kGroups == 4 ? 0xffffffffu : 0x33333333u));
+    gi.vmax = fmaxf(gi.vs, __shfl_xor_sync(0xffffffffu, gi.vs, 1));
+    gi.vmax = fmaxf(gi.vmax, __shfl_xor_sync(0xffffffffu, gi.vmax, 2));
+    return gi;
+  };
+  // The value reference after a chunk: an item's first chunk sets it, a chunk whose scales leave the range
+  // moves it.  Both the converting and the softmax warps follow it.
+  auto next_ref = [](float vref, float vmax, bool starts) {
+    if (vmax == 0.f) return starts ? 1.f : vref;
+    return !starts && vmax <= 64.f * vref && vmax >= vref * 0.015625f ? vref : vmax;
+  };
+
+  if (warp >= C::kSoftmaxWarps && warp < C::kMmaWarp) {
+    // ------------------------------------------------------------------ codes to operands
+    constexpr int kUnitsRow = D / 16;  // 16 codes each
+    constexpr int kThr = 32 * C::kConvertWarps, kRowsPass = kThr / kUnitsRow;
+    constexpr int kPasses = KT / kRowsPass;  // units of a thread in a tile of keys or values
+    static_assert(32 % kRowsPass == 0 || kRowsPass == 32, "a pass lies within a group");
+    const int tid = static_cast<int>(threadIdx.x) - 32 * C::kSoftmaxWarps;
+    const int row0 = tid / kUnitsRow, cu = tid % kUnitsRow;
+    // Two 16-byte units of the operand; the order keeps eight neighbouring lanes on different banks.
+    const uint32_t odd = D > 64 ? (cu >> 2) & 1 : 0;
+    const uint32_t chunk_off = static_cast<uint32_t>(cu >> 2) * C::kKVChunk, u0 = 2u * (cu & 3);
+    GroupInfo cur = load_info(static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
+    GroupInfo nxt = load_info(8 + static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
+    uint4 kc[kPasses], vc[kPasses];
+    auto fetch = [&](const uint8_t* pool, uint4 (&to)[kPasses], int i, bool in_next) {
+      int plane[C::kGroups];
+#pragma unroll
+      for (int g = 0; g < C::kGroups; ++g)
+        plane[g] = __shfl_sync(0xffffffffu, in_next ? nxt.plane : cur.plane, 4 * (i & 7) + g);
+      const int slot = __shfl_sync(0xffffffffu, in_next ? nxt.slot : cur.slot, 4 * (i & 7));
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int row = row0 + p * kRowsPass;
+        const int pl = plane[p * kRowsPass / 32];
+        const int in_page = (slot + row) & (c.page - 1);
+        to[p] = make_uint4(0u, 0u, 0u, 0u);
+        if (pl >= 0)
+          to[p] = __ldg(reinterpret_cast<const uint4*>(
+                            pool + (static_cast<size_t>(pl) * c.page + in_page) * D) + cu);
+      }
+    };
+    // 16 codes as fp16, times `ratio`, into the row of a tile
+    auto put = [&](uint32_t tile, int row, uint4 w, uint32_t ratio, bool scaled) {
+      uint32_t y[8];
+      e4m3x4_to_f16(w.x, y[0], y[1]);
+      e4m3x4_to_f16(w.y, y[2], y[3]);
+      e4m3x4_to_f16(w.z, y[4], y[5]);
+      e4m3x4_to_f16(w.w, y[6], y[7]);
+      if (scaled) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = mul_f16x2(y[i], ratio);
+      }
+      const uint32_t base = tile + chunk_off, ur = static_cast<uint32_t>(row);
+      const uint32_t a0 = base + sw128_offset(ur, u0), a1 = base + sw128_offset(ur, u0 + 1);
+      if (odd) {
+        st_shared_v4(a1, y[4], y[5], y[6], y[7]);
+        st_shared_v4(a0, y[0], y[1], y[2], y[3]);
+      } else {
+        st_shared_v4(a0, y[0], y[1], y[2], y[3]);
+        st_shared_v4(a1, y[4], y[5], y[6], y[7]);
+      }
+    };
+    auto hand_over = [&](uint32_t full) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+    };
+    if (count > 0) {
+      fetch(c.k, kc, 0, false);
+      fetch(c.v, vc, 0, false);
+    }
+    float vref = 1.f;
+    int item = -1;
+    for (int i = 0; i < count; ++i) {
+      const int from = 4 * (i & 7);
+      const int it = __shfl_sync(0xffffffffu, cur.item, from);
+      const int slot = __shfl_sync(0xffffffffu, cur.slot, from);
+      vref = next_ref(vref, __shfl_sync(0xffffffffu, cur.vmax, from), it != item);
+      item = it;
+      uint32_t ratio[C::kGroups];
+#pragma unroll
+      for (int g = 0; g < C::kGroups; ++g)
+        ratio[g] = half2_of(__shfl_sync(0xffffffffu, cur.vs, from + g) / vref);
+      const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(it)))];
+      const int lo = visible_lo(range.len_min, a.reach.window), end = min(range.end_max, a.reach.base);
+      const bool next_in_nxt = (i & 7) == 7;
+
+      const int sk = i % C::kKStages, sv = i % C::kVStages;
+      if (i >= C::kKStages &&
+          !warp_wait(bar(C::kKEmpty + sk), (i / C::kKStages - 1) & 1, &abort_flag, c.err))
+        break;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) put(sK0 + sk * C::kKVBytes, row0 + p * kRowsPass, kc[p], 0u, false);
+      hand_over(bar(C::kKFull + sk));
+      if (i + 1 < count) fetch(c.k, kc, i + 1, next_in_nxt);
+      if (i >= C::kVStages &&
+          !warp_wait(bar(C::kVEmpty + sv), (i / C::kVStages - 1) & 1, &abort_flag, c.err))
+        break;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int row = row0 + p * kRowsPass, s = slot + row;
+        // what nobody sees must not meet a probability of zero as infinity or NaN
+        if (s >= end || (s < lo && s >= a.reach.sinks)) vc[p] = make_uint4(0u, 0u, 0u, 0u);
+        put(sV0 + sv * C::kKVBytes, row, vc[p], ratio[p * kRowsPass / 32], true);
+      }
+      hand_over(bar(C::kVFull + sv));
+      if (i + 1 < count) fetch(c.v, vc, i + 1, next_in_nxt);
+      if (next_in_nxt) {
+        cur = nxt;
+        nxt = load_info(i + 9 + static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
+      }
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdS = idesc_f16kind(0u, kPrefixRows, KT, false, false);
+    constexpr uint32_t kIdO = idesc_f16kind(0u, kPrefixRows, D, false, true);
+    auto issue_s = [&](int g) -> bool {  // S_g = Q K_g^T into buffer g & 1, whose P_{g-2} has been written
+      const int s = g % C::kKStages;
+      if (!warp_wait(bar(C::kKFull + s), (g / C::kKStages) & 1, &abort_flag, c.err)) return false;
+      tc_fence_after();
+      const uint64_t da = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t db = smem_desc_sw128(sK0 + s * C::kKVBytes, 16, 1024);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        umma_ss(tmem + C::kColS + KT * (g & 1), da + (ks / 4) * (C::kQChunk >> 4) + 2 * (ks % 4),
+                db + (ks / 4) * (C::kKVChunk >> 4) + 2 * (ks % 4), kIdS, ks > 0);
+      umma_commit_w(bar(C::kSFull + (g & 1)));
+      umma_commit_w(bar(C::kKEmpty + s));
+      return true;
+    };
+    auto issue_pv = [&](int g, bool first) -> bool {  // O (+)= P_g V_g
+      const int s = g % C::kVStages;
+      if (!warp_wait(bar(C::kPFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err)) return false;
+      if (!warp_wait(bar(C::kVFull + s), (g / C::kVStages) & 1, &abort_flag, c.err)) return false;
+      tc_fence_after();
+      const uint64_t db = smem_desc_sw128(sV0 + s * C::kKVBytes, C::kKVChunk, 1024);
+#pragma unroll
+      for (int ks = 0; ks < KT / 16; ++ks)
+        umma_ts(tmem + C::kColO, tmem + C::kColP + KT / 2 * (g & 1) + 8 * ks, db + 128 * ks, kIdO,
+                !first || ks > 0);
+      umma_commit_w(bar(C::kPVDone + (g & 1)));
+      umma_commit_w(bar(C::kVEmpty + s));
+      return true;
+    };
+    bool ok = true;
+    int seg = 0;
+    for (int g = 0; ok && g < count; ++seg) {
+      // the chunks of one item
+      const int64_t x = begin + g;
+      const int j = sequence_at(s_first, a.tiles, c.Hkv, x);
+      const int64_t nc = s_first[j + 1] - s_first[j], rem = x - s_first[j] * c.Hkv;
+      const int64_t left = nc - (rem - quotient(rem, nc) * nc);
+      const int n = left < count - g ? static_cast<int>(left) : count - g;
+      ok = warp_wait(bar(C::kQFull), seg & 1, &abort_flag, c.err);
+      if (ok) ok = issue_s(g);
+      if (ok && n > 1) ok = issue_s(g + 1);
+      for (int i = 0; ok && i < n; ++i) {
+        // an item's first P V overwrites O, which the epilogue of the one before has read
+        if (i == 0 && seg > 0) ok = warp_wait(bar(C::kOEmpty), (seg - 1) & 1, &abort_flag, c.err);
+        if (ok) ok = issue_pv(g + i, i == 0);
+        if (ok && i + 2 < n) ok = issue_s(g + i + 2);
+      }
+      g += n;
+    }
+    umma_commit_w(bar(C::kDrain));
+    warp_drain_wait(bar(C::kDrain), 0, c.err);
+  } else if (warp < C::kSoftmaxWarps) {
+    // ------------------------------------------------------------------ softmax
+    constexpr int kHalfK = KT / 2, kHalfD = D / 2, kOwn = kHalfK / 32;  // groups of this thread's columns
+    const int r = static_cast<int>(threadIdx.x & 127);  // row of the tile = TMEM lane
+    const uint32_t h = warp >> 2;                          // half of the columns
+    const uint32_t quarter = warp & 3u, lane_base = (quarter * 32u) << 16;
+    int xn = 0;
+    // Swaps a value with the thread that has the other half of the row (slot xn & 1 was last used two
+    // exchanges ago, and the partner passed the one in between only after reading it).
+    auto exchange = [&](float v, float* other) -> bool {
+      float* red = s_red + (xn & 1) * 2 * kPrefixRows;
+      red[h * kPrefixRows + r] = v;
+      __syncwarp();
+      const uint32_t xb = bar(C::kXch + quarter * 2 + (xn & 1));
+      if (lane == 0) mbar_arrive(xb);
+      if (!warp_wait(xb, (xn >> 1) & 1, &abort_flag, c.err)) return false;
+      *other = red[(h ^ 1u) * kPrefixRows + r];
+      ++xn;
+      return true;
+    };
+    GroupInfo cur = load_info(static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
+    int item = -1, seg = 0, lo = 0, hi = INT_MAX, all_lo = 0, all_hi = -1;
+    bool real = false, begins = false, ok = true;
+    float f = 0.f, vref = 1.f, m_ref = SWA_NEG_INF, l = 0.f;
+
+    // Loads this thread's half of its row of q, scaled, into the Q tile.
+    auto start = [&](int new_item, int slot) -> bool {
+      item = new_item;
+      const int j = static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)));
+      const int head = item - j * c.Hkv;
+      const TileRange range = s_range[j];
+      begins = slot == TileWalk(range, a.reach, KT).at(0) * KT;
+      all_lo = visible_lo(range.len_max_q, a.reach.window);
+      all_hi = min(range.end_min, a.reach.base) - 1;
+      const int rho = j * kPrefixRows + r;
+      real = false;
+      lo = 0;
+      hi = INT_MAX;  // rows that stand for nothing need no mask
+      const uint16_t* row = a.q;
+      if (rho < a.rows) {
+        const int b = static_cast<int>(a.div_r.div(static_cast<uint32_t>(rho)));
+        const int in_seq = rho - b * a.R, t = static_cast<int>(a.div_t.mod(static_cast<uint32_t>(in_seq)));
+        int len, n;
+        real = sequence_of(c, b, &len, &n) && t < n;
+        if (real) {
+          lo = visible_lo(len + t, a.reach.window);
+          hi = min(len + t, a.reach.base - 1);
+          row += ((static_cast<size_t>(b) * c.Hkv + head) * a.R + in_seq) * D + kHalfD * h;
+        }
+      }
+      uint4 raw[kHalfD / 8];
+#pragma unroll
+      for (int i = 0; i < kHalfD / 8; ++i)
+        raw[i] = real ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0u, 0u, 0u, 0u);
+      uint32_t top = 0;
+      auto pair_of = [&](uint32_t w) { return a.f16 ? Elem<true>::unpack(w) : Elem<false>::unpack(w); };
+#pragma unroll
+      for (int i = 0; i < kHalfD / 8; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = pair_of(w[e]);
+          top = max(top, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y))));
+        }
+      }
+      float other;
+      if (!exchange(__uint_as_float(top), &other)) return false;
+      top = max(top, __float_as_uint(other));
+      const int ex = static_cast<int>(top >> 23);
+      // 2^(14 - exponent); 1 for zero, infinity and NaN
+      const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+      // a row that is not finite has scores that are all NaN
+      f = ex == 255 ? __uint_as_float(0x7fffffffu)
+                    : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+#pragma unroll
+      for (int i = 0; i < kHalfD / 8; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 z = pair_of(w[e]);
+          y[e] = Elem<true>::pack(z.x * up, z.y * up);
+        }
+        const uint32_t col = kHalfD * h + 8u * i;
+        st_shared_v4(sQ + (col >> 6) * C::kQChunk +
+                         sw128_offset(static_cast<uint32_t>(r), (col & 63u) >> 3),
+                     y[0], y[1], y[2], y[3]);
+      }
+      m_ref = SWA_NEG_INF;
+      l = 0.f;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kQFull));
+      return true;
+    };
+
+    // The item's partial result after its chunk g at `slot`.
+    auto finish = [&](int g, int slot) -> bool {
+      float l_other;
+      if (!exchange(l, &l_other)) return false;
+      if (!warp_wait(bar(C::kPVDone + (g & 1)), (g >> 1) & 1, &abort_flag, c.err)) return false;
+      tc_fence_after();
+      const int j = static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)));
+      const TileWalk walk(s_range[j], a.reach, KT);
+      const bool ends = slot == walk.at(walk.count - 1) * KT;
+      const int at = begins && ends ? 2 * a.parts + item : partial_slot(part, begins);
+      const size_t to = static_cast<size_t>(at) * a.stored + r;
+      float* out = a.po + to * D + kHalfD * h;
+#pragma unroll
+      for (int c0 = 0; c0 < kHalfD; c0 += 32) {
+        uint32_t rr[32];
+        tmem_ld32(tmem + lane_base + C::kColO + kHalfD * h + c0, rr);
+        tmem_wait_ld(rr);
+        if (real) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(out + c0 + i) =
+                make_float4(__uint_as_float(rr[i]) * vref, __uint_as_float(rr[i + 1]) * vref,
+                            __uint_as_float(rr[i + 2]) * vref, __uint_as_float(rr[i + 3]) * vref);
+        }
+      }
+      warp_arrive(bar(C::kOEmpty));
+      if (real && h == 0)
+        *reinterpret_cast<float2*>(a.ml + to * 2) = make_float2(m_ref, l + l_other);
+      return true;
+    };
+
+    int last_slot = 0;
+    for (int g = 0; g < count; ++g) {
+      if (g > 0 && (g & 7) == 0) cur = load_info(g + static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
+      const int from = 4 * (g & 7);
+      const int it = __shfl_sync(0xffffffffu, cur.item, from);
+      const int slot = __shfl_sync(0xffffffffu, cur.slot, from);
+      const float vmax = __shfl_sync(0xffffffffu, cur.vmax, from);
+      const bool whole = __shfl_sync(0xffffffffu, cur.whole, from);
+      float ks[kOwn];
+      int plane[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        ks[i] = __shfl_sync(0xffffffffu, cur.ks, from + kOwn * static_cast<int>(h) + i);
+        plane[i] = __shfl_sync(0xffffffffu, cur.plane, from + kOwn * static_cast<int>(h) + i);
+      }
+      const bool starts = it != item;
+      if (starts) {
+        if (item >= 0 && !(ok = finish(g - 1, last_slot))) break;
+        if (!(ok = start(it, slot))) break;
+        ++seg;
+      }
+      last_slot = slot;
+      const float was = vref;
+      vref = next_ref(vref, vmax, starts);
+      float fk[kOwn];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        fk[i] = f * ks[i];
+        fk[i] = fk[i] < 1e-37f ? 1e-37f : fk[i];  // a masked score times zero would be NaN
+      }
+      if (!(ok = warp_wait(bar(C::kSFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err))) break;
+      tc_fence_after();
+      float x[kHalfK];
+#pragma unroll
+      for (int c0 = 0; c0 < kHalfK; c0 += 32) {
+        uint32_t rr[32];
+        tmem_ld32(tmem + lane_base + C::kColS + KT * (g & 1) + kHalfK * h + c0, rr);
+        tmem_wait_ld(rr);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[c0 + i] = __uint_as_float(rr[i]);
+      }
+      if (!whole || (slot < all_lo && slot + KT > a.reach.sinks) || slot + KT - 1 > all_hi) {
+        const int s0 = slot + kHalfK * static_cast<int>(h);
+        const int clo = lo - s0, chi = hi - s0, csink = a.reach.sinks - s0;
+#pragma unroll
+        for (int i = 0; i < kHalfK; ++i) {
+          const bool see = (i >= clo || i < csink) && i <= chi && plane[i / 32] >= 0;
+          x[i] = see ? x[i] : SWA_NEG_INF;
+        }
+      }
+      uint32_t pk[kHalfK / 2];
+      auto exponentiate = [&](float m) -> float {
+        const float2 neg_m2 = make_float2(-m, -m);
+        float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                        make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < kHalfK / 2; ++i) {
+          const float s = fk[2 * i / 32];
+          const float2 t = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(s, s), neg_m2);
+          const float2 e = make_float2(ex2(t.x), ex2(t.y));
+          rs[i & 3] = __fadd2_rn(rs[i & 3], e);
+          pk[i] = Elem<true>::pack(e.x, e.y);
+        }
+        return ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y));
+      };
+      // One pass against the reference maximum; redone exactly on an item's first chunk or when a row's sum
+      // exceeds 2^12 (the two halves of a row decide alike).
+      bool redo = true;
+      float bsum = 0.f;
+      if (__all_sync(0xffffffffu, m_ref != SWA_NEG_INF)) {
+        bsum = exponentiate(m_ref);
+        float other;
+        if (!(ok = exchange(bsum, &other))) break;
+        redo = __any_sync(0xffffffffu, !(bsum + other <= kFastSumLimit));
+      }
+      float factor = starts ? 1.f : was / vref;
+      bool resc = factor != 1.f;
+      if (redo) {
+        float mx = SWA_NEG_INF;
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+          float m4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = x[32 * o + i];
+#pragma unroll
+          for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[32 * o + i]);
+          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * fk[o]);
+        }
+        float mx_other;
+        if (!(ok = exchange(mx, &mx_other))) break;
+        const float m_new = fmaxf(m_ref, fmaxf(mx, mx_other));
+        if (m_new > m_ref + kRescaleThreshold) {
+          const float down = ex2(m_ref - m_new);  // 0 when m_ref is -inf
+          factor *= down;
+          l *= down;
+          m_ref = m_new;
+          resc = true;
+        }
+        bsum = exponentiate(m_ref == SWA_NEG_INF ? 0.f : m_ref);
+      }
+      l += bsum;
+      // P buffer g & 1 was last read by P V of chunk g - 2
+      if (g >= 2 && !(ok = warp_wait(bar(C::kPVDone + (g & 1)), ((g - 2) >> 1) & 1, &abort_flag, c.err)))
+        break;
+      if (!starts && __any_sync(0xffffffffu, resc)) {
+        if (!(ok = warp_wait(bar(C::kPVDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1, &abort_flag, c.err)))
+          break;
+        tc_fence_after();
+#pragma unroll
+        for (int c0 = 0; c0 < kHalfD; c0 += 32) {
+          const uint32_t oc = tmem + lane_base + C::kColO + kHalfD * h + c0;
+          uint32_t rr[32];
+          tmem_ld32(oc, rr);
+          tmem_wait_ld(rr);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * factor);
+          tmem_st32(oc, rr);
+        }
+      } else {
+        tc_fence_after();
+      }
+      const uint32_t pc = tmem + lane_base + C::kColP + KT / 2 * (g & 1) + kHalfK / 2 * h;
+      if constexpr (kHalfK == 64)
+        tmem_st32(pc, pk);
+      else
+        tmem_st16(pc, pk);
+      tmem_wait_st();
+      warp_arrive(bar(C::kPFull + (g & 1)));
+    }
+    if (ok && item >= 0) finish(count - 1, last_slot);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_prefix_d(const CacheView& c, const PrefixDev& a, cudaStream_t stream) {
+  using C = PrefixCfg<D>;
+  cudaError_t e = allow_smem<swa_cache_prefix_kernel<D>>(C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  swa_cache_prefix_kernel<D>
+      <<<static_cast<unsigned>(a.parts), C::kThreads, C::kSmemBytes, stream>>>(c, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+PrefixPlan prefix_plan(int B, int Hkv, int R, int D, int base) {
+  PrefixPlan p;
+  const long long rows = static_cast<long long>(B) * R;
+  p.tiles = static_cast<int>((rows + kPrefixRows - 1) / kPrefixRows);
+  p.stored = static_cast<int>(rows < kPrefixRows ? rows : kPrefixRows);
+  const int64_t items = static_cast<int64_t>(p.tiles) * Hkv, ck = prefix_chunk(D);
+  const int64_t chunks = items * ((base + ck - 1) / ck), sms = sm_count();
+  // As many parts as SMs, or the least multiple with a part for every item.
+  const int64_t most = sms * ((items + sms - 1) / sms);
+  p.parts = static_cast<int>(chunks < most ? chunks : most);
+  const size_t slots = (2 * static_cast<size_t>(p.parts) + items) * p.stored;
+  auto round = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  size_t off = round((kPrefixTiles + 1) * sizeof(int64_t));
+  p.off_ml = off;
+  off += round(slots * 2 * sizeof(float));
+  p.off_po = off;
+  off += round(slots * D * sizeof(float));
+  p.bytes = off;
+  return p;
+}
+
+cudaError_t launch_cache_prefix(const CacheView& c, const PrefixDev& a, cudaStream_t stream) {
+  if (c.D == 64) return launch_prefix_d<64>(c, a, stream);
+  if (c.D == 128) return launch_prefix_d<128>(c, a, stream);
+  return launch_prefix_d<256>(c, a, stream);
+}
+
+}  // namespace swa

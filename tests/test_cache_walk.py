@@ -50,3 +50,33 @@ def test_workspace_sizes():
     assert size(*args, window=100, sinks=2**40, accumulate=True) <= wide
     assert size(*args, window=2**40, sinks=9, accumulate=True) == wide
     assert size(*args, window=100, sinks=-1) == 0
+
+
+def test_shared_workspaces_and_refusals():
+    size = swa.swa_cache_attn_workspace_bytes
+    args = (3, 8, 2, 2, 128, 500, 64)
+    assert size(*args, shared=100) > size(*args)
+    assert size(*args, window=100, shared=0) == size(*args, window=100)
+    assert size(1, *args[1:], shared=100) == size(1, *args[1:])     # nobody to share with
+    assert size(*args, shared=501) == 0 and size(*args, shared=-1) == 0
+    assert size(*args, shared=1, accumulate=True) == 0
+    assert size(2, 2, 1, 64, 64, 8, 64, shared=1) > 0
+    assert size(2, 2050, 1, 64, 64, 8, 64, shared=1) == 0           # too many rows to a kv head
+
+
+def call(**kw):
+    from sliding_window_flash_gb300.cache import _CCache
+    a = dict(B=2, Hq=2, Hkv=1, T=1, window=10, sinks=0, shared=1, scale=0.1, acc=0, dtype=0, max_pages=4,
+             size=1 << 30)
+    a.update(kw)
+    c = _CCache(16, 16, 16, 16, 16, 8, a["Hkv"], 32, 64)
+    return swa.load().swa_cache_attn_shared(c, 16, a["max_pages"], 16, None, 16, 16, 16, a["B"], a["Hq"],
+                                            a["T"], a["window"], a["sinks"], a["shared"], a["scale"],
+                                            a["acc"], a["dtype"], 16, a["size"], None)
+
+
+@pytest.mark.parametrize("kw,code", [(dict(shared=-1), 1), (dict(shared=5), 1), (dict(acc=1), 1),
+                                     (dict(sinks=-1), 1), (dict(sinks=-1, shared=0), 1),
+                                     (dict(Hq=1025, T=64), 1), (dict(size=100), 6)], ids=str)
+def test_bad_arguments(kw, code):
+    assert call(**kw) == code
