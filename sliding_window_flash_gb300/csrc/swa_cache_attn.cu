@@ -920,14 +920,16 @@ __global__ void __launch_bounds__(256) swa_cache_join_few_kernel(const CacheView
 }
 
 // With a shared prefix: joins what the parts of the prefix's items and the parts of a sequence's own slots
-// left for a row.  A warp for 16 columns of a row: 8 groups of 4 lanes take the partials in turn.
-template <int D>
+// left for a row.  A warp for kCols columns of a row: a lane looks up a partial's place, then groups of
+// kCols / 4 lanes take the partials in turn.
+template <int D, int kCols>
 __global__ void __launch_bounds__(256)
     swa_cache_join_shared_kernel(const CacheView c, const AttnDev a, const PrefixDev p) {
-  constexpr uint32_t kRuns = D / 16;
+  constexpr uint32_t kRuns = D / kCols;
+  constexpr int kSub = kCols / 4, kGroups = 32 / kSub;
   wait_predecessor();
   launch_dependents();
-  const int lane = static_cast<int>(lane_id()), group = lane / 4, sub = lane % 4;
+  const int lane = static_cast<int>(lane_id()), group = lane / kSub, sub = lane % kSub;
   const int per = c.Hkv * a.NRT;
   const int64_t total = a.first[c.B] * per, ptotal = p.first[p.tiles] * c.Hkv;
   const Parts cut(total, used_parts(total, a.parts, a.rows * D));
@@ -954,51 +956,65 @@ __global__ void __launch_bounds__(256)
       const int q0 = chunks > 0 ? pcut.of(x0) : 0;
       const int q1 = chunks > 0 ? pcut.of(x0 + chunks - 1) : -1;
       const int all = own + q1 - q0 + 1;
-      auto source = [&](int k, const float** ml) -> const float* {
+      for (int k0 = 0; k0 < all; k0 += 32) {  // partials in runs of 32, lane k the place of k0 + k
+        const int k = k0 + lane;
+        const float* y = nullptr;
+        float2 s = make_float2(SWA_NEG_INF, 0.f);
         if (k < own) {
           const int part = ip.p0 + k;
-          const int at = own == 1 ? a.whole + item : partial_slot(part, cut.start(part) <= ip.x0);
+          const int at = own == 1 ? a.whole + item : partial_slot(part, k == 0);
           const size_t to = static_cast<size_t>(at) * a.rows + (r - rt * a.RT);
-          *ml = a.ml + to * 2;
-          return a.po + to * D;
+          s = *reinterpret_cast<const float2*>(a.ml + to * 2);
+          y = a.po + to * D;
+        } else if (k < all) {
+          const int part = q0 + k - own;
+          const int at = q0 == q1 ? 2 * p.parts + j * c.Hkv + h : partial_slot(part, part == q0);
+          const size_t to = static_cast<size_t>(at) * p.stored + (rho - j * kPrefixRows);
+          s = *reinterpret_cast<const float2*>(p.ml + to * 2);
+          y = p.po + to * D;
         }
-        const int part = q0 + k - own;
-        const int at = q0 == q1 ? 2 * p.parts + j * c.Hkv + h
-                                : partial_slot(part, pcut.start(part) <= x0);
-        const size_t to = static_cast<size_t>(at) * p.stored + (rho - j * kPrefixRows);
-        *ml = p.ml + to * 2;
-        return p.po + to * D;
-      };
-      const float* ml;
-      for (int k = lane; k < all; k += 32) {
-        source(k, &ml);
-        top = fmaxf(top, ml[0]);
+        if (s.x == SWA_NEG_INF && s.y == 0.f) y = nullptr;  // the row saw nothing there
+        float most = s.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        if (most > top) {  // what came before was against a lower maximum
+          const float down = ex2(top - most);
+          l *= down;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] *= down;
+          top = most;
+        }
+        const float w = y == nullptr ? 0.f : ex2(s.x - (top == SWA_NEG_INF ? 0.f : top));
+        const float lw = y == nullptr ? 0.f : w * s.y;
+        const int n = min(32, all - k0);
+#pragma unroll 4
+        for (int i = 0; i < n; i += kGroups) {
+          const int from = i + group;
+          const float* src = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(y), from & 31));
+          const float wk = __shfl_sync(0xffffffffu, w, from & 31);
+          const float lk = __shfl_sync(0xffffffffu, lw, from & 31);
+          if (from < n && src != nullptr) {
+            const float4 v = *reinterpret_cast<const float4*>(src + run * kCols + sub * 4);
+            l += lk;
+            o[0] += wk * v.x;
+            o[1] += wk * v.y;
+            o[2] += wk * v.z;
+            o[3] += wk * v.w;
+          }
+        }
+        __syncwarp();
       }
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float base = top == SWA_NEG_INF ? 0.f : top;
-      for (int k = group; k < all; k += 8) {
-        const float* y = source(k, &ml);
-        const float2 s = *reinterpret_cast<const float2*>(ml);
-        if (s.x == SWA_NEG_INF && s.y == 0.f) continue;  // the row saw nothing there
-        const float4 v = *reinterpret_cast<const float4*>(y + run * 16 + sub * 4);
-        const float w = ex2(s.x - base);
-        l += w * s.y;
-        o[0] += w * v.x;
-        o[1] += w * v.y;
-        o[2] += w * v.z;
-        o[3] += w * v.w;
-      }
-      __syncwarp();
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
+      for (int d = kSub; d < 32; d <<= 1) {
         l += __shfl_xor_sync(0xffffffffu, l, d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], d);
       }
     }
     if (group == 0) {
-      store_row<4>(a, a.o + static_cast<size_t>(row) * D + run * 16 + sub * 4, o, l == 0.f ? 0.f : 1.f / l);
+      store_row<4>(a, a.o + static_cast<size_t>(row) * D + run * kCols + sub * 4, o,
+                   l == 0.f ? 0.f : 1.f / l);
       if (lane == 0 && run == 0) a.lse[row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
     }
   }
@@ -1232,10 +1248,13 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
       pd.rows = c.B * p.R;
       pd.tiles = (pd.rows + kPrefixRows - 1) / kPrefixRows;
       if ((e = launch_cache_prefix(c, pd, stream)) != cudaSuccess) return e;
-      const int64_t need = (static_cast<int64_t>(c.B) * c.Hkv * p.R * (D / 16) + 7) / 8;
-      const int64_t limit = 8ll * sm_count();
-      e = launch_after(swa_cache_join_shared_kernel<D>,
-                       static_cast<unsigned>(need < limit ? need : limit), stream, c, a, pd);
+      // A warp a row (at D = 256 half of one) where that fills the SMs, else a warp 16 columns of a row.
+      const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv * p.R, limit = 8ll * sm_count();
+      constexpr int kWide = D < 128 ? D : 128;
+      const bool wide = rows * (D / kWide) >= 4ll * sm_count();
+      const int64_t need = (rows * (D / (wide ? kWide : 16)) + 7) / 8;
+      auto join = wide ? swa_cache_join_shared_kernel<D, kWide> : swa_cache_join_shared_kernel<D, 16>;
+      e = launch_after(join, static_cast<unsigned>(need < limit ? need : limit), stream, c, a, pd);
       if (e != cudaSuccess) return e;
       continue;
     }

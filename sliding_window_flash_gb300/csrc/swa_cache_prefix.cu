@@ -5,17 +5,22 @@
 // flops for each row and slot against 2 D bytes a slot, which the memory bounds up to some 150 rows and
 // the tensor cores beyond.  A CTA takes 128 rows of a kv head and a part of their chunks (128 keys, 64 at
 // D = 256), on tcgen05:
-//   * 4 warps turn codes into fp16 operands: a chunk's codes are read from global memory a chunk ahead into
-//     registers, converted (exact, cvt.f16x2.e4m3x2) and stored in the swizzled layouts of the tensor core,
-//     keys K-major, values MN-major, which is how tokens lie anyway.
-//   * One warp issues S = Q K^T two chunks ahead of O += P V; P goes back to TMEM as the A operand.
+//   * 4 warps turn keys and 4 values into fp16 operands: codes are read from global memory two chunks ahead
+//     into registers, converted (exact, cvt.f16x2.e4m3x2) and stored in the swizzled layouts of the tensor
+//     core, keys K-major, values MN-major, which is how tokens lie anyway.
+//   * The first key warp issues S = Q K^T, as soon as the scores two chunks before have become P; the first
+//     value warp issues O += P V, with P as the A operand in TMEM.  16 warps have 128 registers each.
 //   * 8 warps are the softmax, two threads a row, against a running maximum that moves only when a block's
 //     sum calls for it.
+//   * Where 128 chunks lie, their pages and their scales, is looked up by all threads at once and kept in
+//     shared memory, which leaves the loops few registers to hold: what spills would miss the little L1
+//     that operands of 200 KB leave.
 // q is taken as fp16 after scaling each row by a power of two, as in swa_cache_attn.cu.  Keys carry their
-// block's scale into the scores' factor; values carry theirs relative to a reference that stays within
-// 2^6 of the chunk's largest, so that o is rarely rescaled.
+// block's scale into the scores' factor; values are scaled by theirs relative to the largest of the item's
+// chunks, exactly while a scale is at least 2^-15 of it (a code is a multiple of 2^-9, an fp16 value of 2^-24).
 // Parts leave fp32 partial results; swa_cache_attn.cu joins them with those of the slots behind the prefix.
 #include <climits>
+#include <type_traits>
 
 #include "swa_cache_prefix.h"
 #include "swa_ptx.cuh"
@@ -29,6 +34,7 @@ constexpr float kFastSumLimit = 4096.0f;   // a chunk's one-pass sum stands up t
 template <int D>
 struct PrefixCfg {
   static constexpr int KT = D == 256 ? 64 : 128;  // keys of a chunk
+  static constexpr int kBlock = 128;              // chunks that are looked up together
   static constexpr int kGroups = KT / 32;         // of 32 keys, each inside one page
   static constexpr int kQBytes = kPrefixRows * D * 2;
   static constexpr int kQChunk = kPrefixRows * 128;
@@ -40,7 +46,9 @@ struct PrefixCfg {
   static constexpr int kOffV = kOffK + kKStages * kKVBytes;
   static constexpr int kOffFirst = kOffV + kVStages * kKVBytes;
   static constexpr int kOffRange = kOffFirst + (kPrefixTiles + 2) * 8;
-  static constexpr int kOffRed = kOffRange + kPrefixTiles * 16;  // [2 slots][2 halves][128] fp32
+  static constexpr int kOffRec = kOffRange + kPrefixTiles * 16;  // what is known about kBlock chunks
+  static constexpr int kOffMax = kOffRec + kBlock * 64;          // largest value scales of their items
+  static constexpr int kOffRed = kOffMax + kBlock * 4;           // [2 slots][2 halves][128] fp32
   static constexpr int kOffBar = kOffRed + 2 * 2 * kPrefixRows * 4;
   static constexpr int kQFull = 0;
   static constexpr int kKFull = 1;
@@ -52,15 +60,17 @@ struct PrefixCfg {
   static constexpr int kPVDone = kPFull + 2;         // 2
   static constexpr int kXch = kPVDone + 2;           // [4 lane quarters][2 slots]
   static constexpr int kOEmpty = kXch + 8;
-  static constexpr int kDrain = kOEmpty + 1;
-  static constexpr int kNumBars = kDrain + 1;
+  static constexpr int kDrain = kOEmpty + 1;         // 2: of the S and of the P V products
+  static constexpr int kNumBars = kDrain + 2;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;  // + TMEM address and abort flag
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   // TMEM: two S buffers, O, two P buffers of packed pairs
   static constexpr uint32_t kColS = 0, kColO = 2 * KT, kColP = 2 * KT + D;
   static_assert(kColP + KT <= 512, "tensor memory");
-  static constexpr int kSoftmaxWarps = 8, kConvertWarps = 4, kMmaWarp = 12;
-  static constexpr int kThreads = 32 * 13;
+  // Warps 0-7 softmax, 8-11 keys, 12-15 values.
+  static constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+  static constexpr int kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + kConvertWarps;
+  static constexpr int kThreads = 32 * (kValueWarp + kConvertWarps);
 };
 
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -116,14 +126,23 @@ struct TileWalk {
   __device__ int at(int i) const { return i < far ? i : first + (i - far); }
 };
 
-// What a lane holds about 32 keys: lane l those of group l % 4 of chunk l / 4 of the next eight.
-struct GroupInfo {
-  int plane;   // page * Hkv + head, or -1: nothing to be seen there
-  int item, slot;  // of the chunk
-  float ks, vs;
-  float vmax;  // largest value scale of the chunk's groups, 0 without any
-  bool whole;  // every group of the chunk has a plane
+// What is known about a chunk: its item and first slot, the index in its block of its item's first chunk
+// there, and for each group of 32 keys the plane (page * Hkv + head, or -1: nothing to be seen) and scales.
+struct ChunkRec {
+  int item, slot, origin;
+  int whole;  // every group has a plane
+  int plane[4];
+  float ks[4], vs[4];
 };
+static_assert(sizeof(ChunkRec) == 64, "kOffRec");
+
+__device__ __forceinline__ uint4 load_codes(const uint4* p) {  // read once: not for the L1
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 template <int D>
 __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
@@ -160,7 +179,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     }
     for (int x = 0; x < 8; ++x) mbar_init(bar(C::kXch + x), 2);  // the two warps of a lane quarter
     mbar_init(bar(C::kOEmpty), C::kSoftmaxWarps);
-    mbar_init(bar(C::kDrain), 1);
+    mbar_init(bar(C::kDrain + 0), 1);
+    mbar_init(bar(C::kDrain + 1), 1);
     fence_barrier_init();
   }
   // What each tile's rows see: a warp a tile, its lanes the tile's sequences.
@@ -183,7 +203,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     end_min = __reduce_min_sync(0xffffffffu, end_min);
     if (lane == 0) s_range[j] = TileRange{end_max > 0 ? len_min : 0, end_max, q_max, end_min};
   }
-  if (warp == C::kMmaWarp) {
+  if (warp == C::kKeyWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -216,149 +236,88 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   const int64_t begin = part < cut.parts ? cut.start(part) : total;
   const int count = part < cut.parts ? static_cast<int>(cut.start(part + 1) - begin) : 0;
 
-  // Chunk i of the part, one of its groups.
-  auto load_info = [&](int i, int group) {
-    GroupInfo gi = {-1, -1, 0, 1.f, 0.f, 0.f, false};
-    if (i < count && group < C::kGroups) {
+  ChunkRec* s_rec = reinterpret_cast<ChunkRec*>(smem + C::kOffRec);
+  unsigned* s_max = reinterpret_cast<unsigned*>(smem + C::kOffMax);
+  // Looks up the part's chunks from i0 on, a thread a group of 32 keys.  Every thread of the CTA comes here
+  // for every block, whatever became of its work on the one before.
+  auto look_up = [&](int i0) {
+    __syncthreads();  // the block before has been read
+    const int rec = static_cast<int>(threadIdx.x) / 4, group = static_cast<int>(threadIdx.x) & 3;
+    const int i = i0 + rec;
+    if (group == 0) s_max[rec] = 0u;
+    __syncthreads();
+    int plane = -1;
+    if (i < count) {
       const int64_t x = begin + i;
       const int j = sequence_at(s_first, a.tiles, c.Hkv, x);
       const int64_t nc = s_first[j + 1] - s_first[j], rem = x - s_first[j] * c.Hkv;
-      const int h = static_cast<int>(quotient(rem, nc));
-      gi.item = j * c.Hkv + h;
-      gi.slot = TileWalk(s_range[j], a.reach, KT).at(static_cast<int>(rem - h * nc)) * KT;
-      const int slot = gi.slot + 32 * group;
-      if (slot < a.reach.base) {
+      const int h = static_cast<int>(quotient(rem, nc)), cc = static_cast<int>(rem - h * nc);
+      const int slot0 = TileWalk(s_range[j], a.reach, KT).at(cc) * KT, slot = slot0 + 32 * group;
+      const int origin = max(rec - cc, 0);
+      float ks = 1.f, vs = 0.f;
+      if (group < C::kGroups && slot < a.reach.base) {
         const int page = page_of(c, a.table, 0, slot >> a.page_log2, c.max_pages);
         if (page >= 0) {
-          gi.plane = page * c.Hkv + h;
-          gi.ks = c.k_scale[gi.plane];
-          gi.vs = c.v_scale[gi.plane];
+          plane = page * c.Hkv + h;
+          ks = c.k_scale[plane];
+          vs = c.v_scale[plane];
+          atomicMax(&s_max[origin], __float_as_uint(vs));
         }
       }
+      ChunkRec& to = s_rec[rec];
+      to.plane[group] = plane;
+      to.ks[group] = ks;
+      to.vs[group] = vs;
+      if (group == 0) {
+        to.item = j * c.Hkv + h;
+        to.slot = slot0;
+        to.origin = origin;
+      }
     }
-    const unsigned quad = 0xfu << (lane & 28u);
-    gi.whole = (__ballot_sync(0xffffffffu, gi.plane >= 0) & quad) ==
-               (quad & (C::kGroups == 4 ? 0xffffffffu : 0x33333333u));
-    gi.vmax = fmaxf(gi.vs, __shfl_xor_sync(0xffffffffu, gi.vs, 1));
-    gi.vmax = fmaxf(gi.vmax, __shfl_xor_sync(0xffffffffu, gi.vmax, 2));
-    return gi;
+    const unsigned there = __ballot_sync(0xffffffffu, plane >= 0) >> (lane & 28u);
+    constexpr unsigned kAll = (1u << C::kGroups) - 1u;
+    if (i < count && group == 0) s_rec[rec].whole = (there & kAll) == kAll;
+    __syncthreads();
   };
-  // The value reference after a chunk: an item's first chunk sets it, a chunk whose scales leave the range
-  // moves it.  Both the converting and the softmax warps follow it.
-  auto next_ref = [](float vref, float vmax, bool starts) {
-    if (vmax == 0.f) return starts ? 1.f : vref;
-    return !starts && vmax <= 64.f * vref && vmax >= vref * 0.015625f ? vref : vmax;
+  // The value reference: the largest scale of the item's chunks so far, a block of chunks at a time.
+  auto reference = [&](const ChunkRec& rec, float vref, bool starts) {
+    const float top = __uint_as_float(s_max[rec.origin]);
+    return starts ? (top > 0.f ? top : 1.f) : fmaxf(vref, top);
   };
 
-  if (warp >= C::kSoftmaxWarps && warp < C::kMmaWarp) {
-    // ------------------------------------------------------------------ codes to operands
+  if (warp >= C::kKeyWarp) {
+    // ------------------------------------------------------------------ codes to operands, products
+    // Four warps take the keys, four the values; a thread has the codes of the next two chunks on their way.
     constexpr int kUnitsRow = D / 16;  // 16 codes each
     constexpr int kThr = 32 * C::kConvertWarps, kRowsPass = kThr / kUnitsRow;
-    constexpr int kPasses = KT / kRowsPass;  // units of a thread in a tile of keys or values
-    static_assert(32 % kRowsPass == 0 || kRowsPass == 32, "a pass lies within a group");
-    const int tid = static_cast<int>(threadIdx.x) - 32 * C::kSoftmaxWarps;
-    const int row0 = tid / kUnitsRow, cu = tid % kUnitsRow;
-    // Two 16-byte units of the operand; the order keeps eight neighbouring lanes on different banks.
-    const uint32_t odd = D > 64 ? (cu >> 2) & 1 : 0;
-    const uint32_t chunk_off = static_cast<uint32_t>(cu >> 2) * C::kKVChunk, u0 = 2u * (cu & 3);
-    GroupInfo cur = load_info(static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
-    GroupInfo nxt = load_info(8 + static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
-    uint4 kc[kPasses], vc[kPasses];
-    auto fetch = [&](const uint8_t* pool, uint4 (&to)[kPasses], int i, bool in_next) {
-      int plane[C::kGroups];
+    constexpr int kPasses = KT / kRowsPass;  // units of a thread in a tile
+    static_assert(32 % kRowsPass == 0, "a pass lies within a group");
+    const int tid = static_cast<int>(threadIdx.x & (kThr - 1)), cu = tid % kUnitsRow;
+    // Neighbouring 64-column pieces of a row go to the same banks: every other one is taken a row on.
+    const int row0 = (tid / kUnitsRow) ^ ((cu >> 2) & 1);
+    const uint32_t piece = static_cast<uint32_t>(cu >> 2) * C::kKVChunk, unit = 2u * (cu & 3);
+    auto fetch = [&](const uint8_t* pool, uint4 (&to)[kPasses], int i) {
+      const ChunkRec& rec = s_rec[i];
 #pragma unroll
-      for (int g = 0; g < C::kGroups; ++g)
-        plane[g] = __shfl_sync(0xffffffffu, in_next ? nxt.plane : cur.plane, 4 * (i & 7) + g);
-      const int slot = __shfl_sync(0xffffffffu, in_next ? nxt.slot : cur.slot, 4 * (i & 7));
+      for (int g = 0; g < C::kGroups; ++g) {
+        const int pl = rec.plane[g];
+        const uint4* src = reinterpret_cast<const uint4*>(
+                               pool + (static_cast<size_t>(max(pl, 0)) * c.page +
+                                       ((rec.slot + 32 * g) & (c.page - 1)) + row0) * D) + cu;
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int row = row0 + p * kRowsPass;
-        const int pl = plane[p * kRowsPass / 32];
-        const int in_page = (slot + row) & (c.page - 1);
-        to[p] = make_uint4(0u, 0u, 0u, 0u);
-        if (pl >= 0)
-          to[p] = __ldg(reinterpret_cast<const uint4*>(
-                            pool + (static_cast<size_t>(pl) * c.page + in_page) * D) + cu);
+        for (int p = 0; p < 32 / kRowsPass; ++p)
+          to[g * (32 / kRowsPass) + p] =
+              pl >= 0 ? load_codes(src + p * kRowsPass * kUnitsRow) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
-    // 16 codes as fp16, times `ratio`, into the row of a tile
-    auto put = [&](uint32_t tile, int row, uint4 w, uint32_t ratio, bool scaled) {
-      uint32_t y[8];
-      e4m3x4_to_f16(w.x, y[0], y[1]);
-      e4m3x4_to_f16(w.y, y[2], y[3]);
-      e4m3x4_to_f16(w.z, y[4], y[5]);
-      e4m3x4_to_f16(w.w, y[6], y[7]);
-      if (scaled) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = mul_f16x2(y[i], ratio);
-      }
-      const uint32_t base = tile + chunk_off, ur = static_cast<uint32_t>(row);
-      const uint32_t a0 = base + sw128_offset(ur, u0), a1 = base + sw128_offset(ur, u0 + 1);
-      if (odd) {
-        st_shared_v4(a1, y[4], y[5], y[6], y[7]);
-        st_shared_v4(a0, y[0], y[1], y[2], y[3]);
-      } else {
-        st_shared_v4(a0, y[0], y[1], y[2], y[3]);
-        st_shared_v4(a1, y[4], y[5], y[6], y[7]);
-      }
-    };
-    auto hand_over = [&](uint32_t full) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full);
-    };
-    if (count > 0) {
-      fetch(c.k, kc, 0, false);
-      fetch(c.v, vc, 0, false);
-    }
-    float vref = 1.f;
-    int item = -1;
-    for (int i = 0; i < count; ++i) {
-      const int from = 4 * (i & 7);
-      const int it = __shfl_sync(0xffffffffu, cur.item, from);
-      const int slot = __shfl_sync(0xffffffffu, cur.slot, from);
-      vref = next_ref(vref, __shfl_sync(0xffffffffu, cur.vmax, from), it != item);
-      item = it;
-      uint32_t ratio[C::kGroups];
-#pragma unroll
-      for (int g = 0; g < C::kGroups; ++g)
-        ratio[g] = half2_of(__shfl_sync(0xffffffffu, cur.vs, from + g) / vref);
-      const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(it)))];
-      const int lo = visible_lo(range.len_min, a.reach.window), end = min(range.end_max, a.reach.base);
-      const bool next_in_nxt = (i & 7) == 7;
-
-      const int sk = i % C::kKStages, sv = i % C::kVStages;
-      if (i >= C::kKStages &&
-          !warp_wait(bar(C::kKEmpty + sk), (i / C::kKStages - 1) & 1, &abort_flag, c.err))
-        break;
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) put(sK0 + sk * C::kKVBytes, row0 + p * kRowsPass, kc[p], 0u, false);
-      hand_over(bar(C::kKFull + sk));
-      if (i + 1 < count) fetch(c.k, kc, i + 1, next_in_nxt);
-      if (i >= C::kVStages &&
-          !warp_wait(bar(C::kVEmpty + sv), (i / C::kVStages - 1) & 1, &abort_flag, c.err))
-        break;
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int row = row0 + p * kRowsPass, s = slot + row;
-        // what nobody sees must not meet a probability of zero as infinity or NaN
-        if (s >= end || (s < lo && s >= a.reach.sinks)) vc[p] = make_uint4(0u, 0u, 0u, 0u);
-        put(sV0 + sv * C::kKVBytes, row, vc[p], ratio[p * kRowsPass / 32], true);
-      }
-      hand_over(bar(C::kVFull + sv));
-      if (i + 1 < count) fetch(c.v, vc, i + 1, next_in_nxt);
-      if (next_in_nxt) {
-        cur = nxt;
-        nxt = load_info(i + 9 + static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
-      }
-    }
-  } else if (warp == C::kMmaWarp) {
-    // ------------------------------------------------------------------ MMA issuer
     constexpr uint32_t kIdS = idesc_f16kind(0u, kPrefixRows, KT, false, false);
     constexpr uint32_t kIdO = idesc_f16kind(0u, kPrefixRows, D, false, true);
-    auto issue_s = [&](int g) -> bool {  // S_g = Q K_g^T into buffer g & 1, whose P_{g-2} has been written
-      const int s = g % C::kKStages;
-      if (!warp_wait(bar(C::kKFull + s), (g / C::kKStages) & 1, &abort_flag, c.err)) return false;
+    // S_g = Q K_g^T into buffer g & 1, once its scores before have become P.
+    auto issue_s = [&](int g, int s, uint32_t landed, bool starts, int seg) -> bool {
+      if (starts && !warp_wait(bar(C::kQFull), seg & 1, &abort_flag, c.err)) return false;
+      if (!warp_wait(bar(C::kKFull + s), landed, &abort_flag, c.err)) return false;
+      if (g >= 2 && !warp_wait(bar(C::kPFull + (g & 1)), ((g - 2) >> 1) & 1, &abort_flag, c.err))
+        return false;
       tc_fence_after();
       const uint64_t da = smem_desc_sw128(sQ, 16, 1024);
       const uint64_t db = smem_desc_sw128(sK0 + s * C::kKVBytes, 16, 1024);
@@ -370,43 +329,112 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       umma_commit_w(bar(C::kKEmpty + s));
       return true;
     };
-    auto issue_pv = [&](int g, bool first) -> bool {  // O (+)= P_g V_g
-      const int s = g % C::kVStages;
+    // O (+)= P_g V_g; an item's first overwrites O, which the epilogue of the one before has read.
+    auto issue_pv = [&](int g, int s, uint32_t landed, bool starts, int seg) -> bool {
+      if (starts && seg > 0 && !warp_wait(bar(C::kOEmpty), (seg - 1) & 1, &abort_flag, c.err))
+        return false;
+      if (!warp_wait(bar(C::kVFull + s), landed, &abort_flag, c.err)) return false;
       if (!warp_wait(bar(C::kPFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err)) return false;
-      if (!warp_wait(bar(C::kVFull + s), (g / C::kVStages) & 1, &abort_flag, c.err)) return false;
       tc_fence_after();
       const uint64_t db = smem_desc_sw128(sV0 + s * C::kKVBytes, C::kKVChunk, 1024);
 #pragma unroll
       for (int ks = 0; ks < KT / 16; ++ks)
         umma_ts(tmem + C::kColO, tmem + C::kColP + KT / 2 * (g & 1) + 8 * ks, db + 128 * ks, kIdO,
-                !first || ks > 0);
+                !starts || ks > 0);
       umma_commit_w(bar(C::kPVDone + (g & 1)));
       umma_commit_w(bar(C::kVEmpty + s));
       return true;
     };
-    bool ok = true;
-    int seg = 0;
-    for (int g = 0; ok && g < count; ++seg) {
-      // the chunks of one item
-      const int64_t x = begin + g;
-      const int j = sequence_at(s_first, a.tiles, c.Hkv, x);
-      const int64_t nc = s_first[j + 1] - s_first[j], rem = x - s_first[j] * c.Hkv;
-      const int64_t left = nc - (rem - quotient(rem, nc) * nc);
-      const int n = left < count - g ? static_cast<int>(left) : count - g;
-      ok = warp_wait(bar(C::kQFull), seg & 1, &abort_flag, c.err);
-      if (ok) ok = issue_s(g);
-      if (ok && n > 1) ok = issue_s(g + 1);
-      for (int i = 0; ok && i < n; ++i) {
-        // an item's first P V overwrites O, which the epilogue of the one before has read
-        if (i == 0 && seg > 0) ok = warp_wait(bar(C::kOEmpty), (seg - 1) & 1, &abort_flag, c.err);
-        if (ok) ok = issue_pv(g + i, i == 0);
-        if (ok && i + 2 < n) ok = issue_s(g + i + 2);
+    int item = -1, seg = -1, stage = 0;
+    uint32_t phase = 1;  // the first round of stages is free
+    float vref = 1.f;
+    auto walk = [&](auto kind) {
+      constexpr bool kValues = decltype(kind)::value;
+      const uint8_t* pool = kValues ? c.v : c.k;
+      // 16 codes as fp16, values times `ratio`, into a row of a tile
+      auto put = [&](uint32_t tile, int row, uint4 w, uint32_t ratio) {
+        uint32_t y[8];
+        e4m3x4_to_f16(w.x, y[0], y[1]);
+        e4m3x4_to_f16(w.y, y[2], y[3]);
+        e4m3x4_to_f16(w.z, y[4], y[5]);
+        e4m3x4_to_f16(w.w, y[6], y[7]);
+        if constexpr (kValues) {
+  #pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = mul_f16x2(y[i], ratio);
+        }
+        const uint32_t to = tile + piece, ur = static_cast<uint32_t>(row);
+        st_shared_v4(to + sw128_offset(ur, unit), y[0], y[1], y[2], y[3]);
+        st_shared_v4(to + sw128_offset(ur, unit + 1), y[4], y[5], y[6], y[7]);
+      };
+      // Chunk g, record i of its block, of `n`: its codes become the operand, and those of the chunk two on are
+      // sent for.
+      auto step = [&](int g, int i, int n, uint4 (&codes)[kPasses]) -> bool {
+        const ChunkRec& rec = s_rec[i];
+        const bool starts = rec.item != item;
+        if (starts) ++seg;
+        item = rec.item;
+        uint32_t ratio[C::kGroups] = {};
+        if constexpr (kValues) {
+          vref = reference(rec, vref, starts);
+  #pragma unroll
+          for (int o = 0; o < C::kGroups; ++o) ratio[o] = half2_of(rec.vs[o] / vref);
+          const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)))];
+          const int lo = visible_lo(range.len_min, a.reach.window), end = min(range.end_max, a.reach.base);
+          // what nobody sees must not meet a probability of zero as infinity or NaN
+          if (rec.slot + KT > end || (rec.slot < lo && rec.slot + KT > a.reach.sinks)) {
+  #pragma unroll
+            for (int p = 0; p < kPasses; ++p) {
+              const int s = rec.slot + row0 + p * kRowsPass;
+              if (s >= end || (s < lo && s >= a.reach.sinks)) codes[p] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+        constexpr int kStages = kValues ? C::kVStages : C::kKStages;
+        constexpr int kFull = kValues ? C::kVFull : C::kKFull, kEmpty = kValues ? C::kVEmpty : C::kKEmpty;
+        if (!warp_wait(bar(kEmpty + stage), phase, &abort_flag, c.err)) return false;
+        const uint32_t tile = (kValues ? sV0 : sK0) + static_cast<uint32_t>(stage) * C::kKVBytes;
+  #pragma unroll
+        for (int p = 0; p < kPasses; ++p)
+          put(tile, row0 + p * kRowsPass, codes[p], ratio[p * kRowsPass / 32]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kFull + stage));
+        const int s = stage;
+        const uint32_t landed = phase ^ 1u;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (i + 2 < n) fetch(kValues ? c.v : c.k, codes, i + 2);
+        if (warp == (kValues ? C::kValueWarp : C::kKeyWarp))
+          return kValues ? issue_pv(g, s, landed, starts, seg) : issue_s(g, s, landed, starts, seg);
+        return true;
+      };
+      bool ok = true;
+      for (int i0 = 0; i0 < count; i0 += C::kBlock) {
+        look_up(i0);
+        const int n = min(C::kBlock, count - i0);
+        uint4 even[kPasses], odds[kPasses];
+        if (ok) {
+          fetch(pool, even, 0);
+          if (n > 1) fetch(pool, odds, 1);
+        }
+        for (int i = 0; ok && i < n; i += 2) {
+          ok = step(i0 + i, i, n, even);
+          if (ok && i + 1 < n) ok = step(i0 + i + 1, i + 1, n, odds);
+        }
       }
-      g += n;
+    };
+    const bool values = warp >= C::kValueWarp;
+    if (values)
+      walk(std::true_type{});
+    else
+      walk(std::false_type{});
+    if (warp == C::kKeyWarp || warp == C::kValueWarp) {  // nothing issued is left running
+      umma_commit_w(bar(C::kDrain + values));
+      warp_drain_wait(bar(C::kDrain + values), 0, c.err);
     }
-    umma_commit_w(bar(C::kDrain));
-    warp_drain_wait(bar(C::kDrain), 0, c.err);
-  } else if (warp < C::kSoftmaxWarps) {
+  } else {
     // ------------------------------------------------------------------ softmax
     constexpr int kHalfK = KT / 2, kHalfD = D / 2, kOwn = kHalfK / 32;  // groups of this thread's columns
     const int r = static_cast<int>(threadIdx.x & 127);  // row of the tile = TMEM lane
@@ -426,8 +454,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       ++xn;
       return true;
     };
-    GroupInfo cur = load_info(static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
-    int item = -1, seg = 0, lo = 0, hi = INT_MAX, all_lo = 0, all_hi = -1;
+    int item = -1, lo = 0, hi = INT_MAX, all_lo = 0, all_hi = -1;
     bool real = false, begins = false, ok = true;
     float f = 0.f, vref = 1.f, m_ref = SWA_NEG_INF, l = 0.f;
 
@@ -515,7 +542,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       const int at = begins && ends ? 2 * a.parts + item : partial_slot(part, begins);
       const size_t to = static_cast<size_t>(at) * a.stored + r;
       float* out = a.po + to * D + kHalfD * h;
-#pragma unroll
+#pragma unroll 1
       for (int c0 = 0; c0 < kHalfD; c0 += 32) {
         uint32_t rr[32];
         tmem_ld32(tmem + lane_base + C::kColO + kHalfD * h + c0, rr);
@@ -535,67 +562,60 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     };
 
     int last_slot = 0;
-    for (int g = 0; g < count; ++g) {
-      if (g > 0 && (g & 7) == 0) cur = load_info(g + static_cast<int>(lane >> 2), static_cast<int>(lane & 3));
-      const int from = 4 * (g & 7);
-      const int it = __shfl_sync(0xffffffffu, cur.item, from);
-      const int slot = __shfl_sync(0xffffffffu, cur.slot, from);
-      const float vmax = __shfl_sync(0xffffffffu, cur.vmax, from);
-      const bool whole = __shfl_sync(0xffffffffu, cur.whole, from);
-      float ks[kOwn];
-      int plane[kOwn];
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        ks[i] = __shfl_sync(0xffffffffu, cur.ks, from + kOwn * static_cast<int>(h) + i);
-        plane[i] = __shfl_sync(0xffffffffu, cur.plane, from + kOwn * static_cast<int>(h) + i);
-      }
-      const bool starts = it != item;
+    for (int i0 = 0; i0 < count; i0 += C::kBlock) {
+    look_up(i0);
+    for (int g = i0; ok && g < min(count, i0 + C::kBlock); ++g) {
+      const ChunkRec& rec = s_rec[g - i0];
+      const int slot = rec.slot;
+      const bool starts = rec.item != item;
       if (starts) {
         if (item >= 0 && !(ok = finish(g - 1, last_slot))) break;
-        if (!(ok = start(it, slot))) break;
-        ++seg;
+        if (!(ok = start(rec.item, slot))) break;
       }
       last_slot = slot;
       const float was = vref;
-      vref = next_ref(vref, vmax, starts);
+      vref = reference(rec, vref, starts);
       float fk[kOwn];
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        fk[i] = f * ks[i];
+        fk[i] = f * rec.ks[kOwn * h + i];
         fk[i] = fk[i] < 1e-37f ? 1e-37f : fk[i];  // a masked score times zero would be NaN
       }
       if (!(ok = warp_wait(bar(C::kSFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err))) break;
       tc_fence_after();
-      float x[kHalfK];
-#pragma unroll
-      for (int c0 = 0; c0 < kHalfK; c0 += 32) {
+      // 32 of this thread's scores of the chunk.  They are read from TMEM for each pass: held in registers
+      // all together they would spill, and what spills misses the little L1 that is left.
+      const bool edge = !rec.whole || (slot < all_lo && slot + KT > a.reach.sinks) || slot + KT - 1 > all_hi;
+      auto scores = [&](int o, float (&x)[32]) {
         uint32_t rr[32];
-        tmem_ld32(tmem + lane_base + C::kColS + KT * (g & 1) + kHalfK * h + c0, rr);
+        tmem_ld32(tmem + lane_base + C::kColS + KT * (g & 1) + kHalfK * h + 32u * o, rr);
         tmem_wait_ld(rr);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[c0 + i] = __uint_as_float(rr[i]);
-      }
-      if (!whole || (slot < all_lo && slot + KT > a.reach.sinks) || slot + KT - 1 > all_hi) {
-        const int s0 = slot + kHalfK * static_cast<int>(h);
-        const int clo = lo - s0, chi = hi - s0, csink = a.reach.sinks - s0;
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(rr[i]);
+        if (edge) {
+          const int s0 = slot + kHalfK * static_cast<int>(h) + 32 * o;
+          const int clo = lo - s0, chi = rec.plane[kOwn * h + o] >= 0 ? hi - s0 : -1, csink = a.reach.sinks - s0;
 #pragma unroll
-        for (int i = 0; i < kHalfK; ++i) {
-          const bool see = (i >= clo || i < csink) && i <= chi && plane[i / 32] >= 0;
-          x[i] = see ? x[i] : SWA_NEG_INF;
+          for (int i = 0; i < 32; ++i) x[i] = (i >= clo || i < csink) && i <= chi ? x[i] : SWA_NEG_INF;
         }
-      }
+      };
       uint32_t pk[kHalfK / 2];
       auto exponentiate = [&](float m) -> float {
         const float2 neg_m2 = make_float2(-m, -m);
         float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int i = 0; i < kHalfK / 2; ++i) {
-          const float s = fk[2 * i / 32];
-          const float2 t = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(s, s), neg_m2);
-          const float2 e = make_float2(ex2(t.x), ex2(t.y));
-          rs[i & 3] = __fadd2_rn(rs[i & 3], e);
-          pk[i] = Elem<true>::pack(e.x, e.y);
+        for (int o = 0; o < kOwn; ++o) {
+          float x[32];
+          scores(o, x);
+          const float2 s2 = make_float2(fk[o], fk[o]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 t = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), s2, neg_m2);
+            const float2 e = make_float2(ex2(t.x), ex2(t.y));
+            rs[i & 3] = __fadd2_rn(rs[i & 3], e);
+            pk[16 * o + i] = Elem<true>::pack(e.x, e.y);
+          }
         }
         return ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y));
       };
@@ -615,11 +635,12 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         float mx = SWA_NEG_INF;
 #pragma unroll
         for (int o = 0; o < kOwn; ++o) {
-          float m4[4];
+          float x[32], m4[4];
+          scores(o, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = x[32 * o + i];
+          for (int i = 0; i < 4; ++i) m4[i] = x[i];
 #pragma unroll
-          for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[32 * o + i]);
+          for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
           mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * fk[o]);
         }
         float mx_other;
@@ -642,7 +663,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         if (!(ok = warp_wait(bar(C::kPVDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1, &abort_flag, c.err)))
           break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < kHalfD; c0 += 32) {
           const uint32_t oc = tmem + lane_base + C::kColO + kHalfD * h + c0;
           uint32_t rr[32];
@@ -663,12 +684,13 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       tmem_wait_st();
       warp_arrive(bar(C::kPFull + (g & 1)));
     }
+    }
     if (ok && item >= 0) finish(count - 1, last_slot);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kMmaWarp) {
+  if (warp == C::kKeyWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
