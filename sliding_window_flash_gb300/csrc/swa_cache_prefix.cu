@@ -5,13 +5,12 @@
 // flops for each row and slot against 2 D bytes a slot, which the memory bounds up to some 150 rows and
 // the tensor cores beyond.  A CTA takes 128 rows of a kv head and a part of their chunks (128 keys, 64 at
 // D = 256), on tcgen05:
-//   * 4 warps turn keys and 4 values into fp16 operands: codes are read from global memory two chunks ahead
+//   * 2 warps turn keys and 4 values into fp16 operands: codes are read from global memory a chunk ahead
 //     into registers, converted (exact, cvt.f16x2.e4m3x2) and stored in the swizzled layouts of the tensor
 //     core, keys K-major, values MN-major, which is how tokens lie anyway.
-//   * The first key warp issues S = Q K^T, as soon as the scores two chunks before have become P; the first
-//     value warp issues O += P V, with P as the A operand in TMEM.  16 warps have 128 registers each.
-//   * 8 warps are the softmax, two threads a row, against a running maximum that moves only when a block's
-//     sum calls for it.
+//   * One warp issues S = Q K^T two chunks ahead of O += P V; P goes back to TMEM as the A operand.
+//   * 8 warps are the softmax, 16 whole rows each (four threads a row), against a running maximum that moves
+//     only when a chunk's sum calls for it.
 //   * Where 128 chunks lie, their pages and their scales, is looked up by all threads at once and kept in
 //     shared memory, which leaves the loops few registers to hold: what spills would miss the little L1
 //     that operands of 200 KB leave.
@@ -48,8 +47,8 @@ struct PrefixCfg {
   static constexpr int kOffRange = kOffFirst + (kPrefixTiles + 2) * 8;
   static constexpr int kOffRec = kOffRange + kPrefixTiles * 16;  // what is known about kBlock chunks
   static constexpr int kOffMax = kOffRec + kBlock * 64;          // largest value scales of their items
-  static constexpr int kOffRed = kOffMax + kBlock * 4;           // [2 slots][2 halves][128] fp32
-  static constexpr int kOffBar = kOffRed + 2 * 2 * kPrefixRows * 4;
+  static constexpr int kOffSeen = kOffMax + kBlock * 4;          // the slots that each row sees
+  static constexpr int kOffBar = kOffSeen + kPrefixRows * 8;
   static constexpr int kQFull = 0;
   static constexpr int kKFull = 1;
   static constexpr int kKEmpty = kKFull + kKStages;
@@ -58,19 +57,20 @@ struct PrefixCfg {
   static constexpr int kSFull = kVEmpty + kVStages;  // 2
   static constexpr int kPFull = kSFull + 2;          // 2
   static constexpr int kPVDone = kPFull + 2;         // 2
-  static constexpr int kXch = kPVDone + 2;           // [4 lane quarters][2 slots]
-  static constexpr int kOEmpty = kXch + 8;
-  static constexpr int kDrain = kOEmpty + 1;         // 2: of the S and of the P V products
-  static constexpr int kNumBars = kDrain + 2;
+  static constexpr int kOEmpty = kPVDone + 2;
+  static constexpr int kDrain = kOEmpty + 1;
+  static constexpr int kNumBars = kDrain + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;  // + TMEM address and abort flag
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   // TMEM: two S buffers, O, two P buffers of packed pairs
   static constexpr uint32_t kColS = 0, kColO = 2 * KT, kColP = 2 * KT + D;
   static_assert(kColP + KT <= 512, "tensor memory");
-  // Warps 0-7 softmax, 8-11 keys, 12-15 values.
-  static constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
-  static constexpr int kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + kConvertWarps;
-  static constexpr int kThreads = 32 * (kValueWarp + kConvertWarps);
+  // Warps 0-7 softmax, 8 and 9 keys, 10-13 values, 14 products: more than 16 would have fewer than 128
+  // registers each, and spill.
+  static constexpr int kSoftmaxWarps = 8, kKeyWarps = 2, kValueWarps = 4;
+  static constexpr int kKeyWarp = kSoftmaxWarps, kValueWarp = kKeyWarp + kKeyWarps;
+  static constexpr int kMmaWarp = kValueWarp + kValueWarps;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
 };
 
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -153,7 +153,6 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   if (!smem_base_ok(smem, c.err)) return;
   int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
   TileRange* s_range = reinterpret_cast<TileRange*>(smem + C::kOffRange);
-  float* s_red = reinterpret_cast<float*>(smem + C::kOffRed);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
@@ -165,11 +164,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     abort_flag = 0;
     mbar_init(bar(C::kQFull), C::kSoftmaxWarps);
     for (int s = 0; s < C::kKStages; ++s) {
-      mbar_init(bar(C::kKFull + s), C::kConvertWarps);
+      mbar_init(bar(C::kKFull + s), C::kKeyWarps);
       mbar_init(bar(C::kKEmpty + s), 1);
     }
     for (int s = 0; s < C::kVStages; ++s) {
-      mbar_init(bar(C::kVFull + s), C::kConvertWarps);
+      mbar_init(bar(C::kVFull + s), C::kValueWarps);
       mbar_init(bar(C::kVEmpty + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -177,10 +176,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       mbar_init(bar(C::kPFull + b), C::kSoftmaxWarps);
       mbar_init(bar(C::kPVDone + b), 1);
     }
-    for (int x = 0; x < 8; ++x) mbar_init(bar(C::kXch + x), 2);  // the two warps of a lane quarter
     mbar_init(bar(C::kOEmpty), C::kSoftmaxWarps);
-    mbar_init(bar(C::kDrain + 0), 1);
-    mbar_init(bar(C::kDrain + 1), 1);
+    mbar_init(bar(C::kDrain), 1);
     fence_barrier_init();
   }
   // What each tile's rows see: a warp a tile, its lanes the tile's sequences.
@@ -203,7 +200,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     end_min = __reduce_min_sync(0xffffffffu, end_min);
     if (lane == 0) s_range[j] = TileRange{end_max > 0 ? len_min : 0, end_max, q_max, end_min};
   }
-  if (warp == C::kKeyWarp) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -242,41 +239,42 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   // for every block, whatever became of its work on the one before.
   auto look_up = [&](int i0) {
     __syncthreads();  // the block before has been read
-    const int rec = static_cast<int>(threadIdx.x) / 4, group = static_cast<int>(threadIdx.x) & 3;
-    const int i = i0 + rec;
-    if (group == 0) s_max[rec] = 0u;
+    for (int i = static_cast<int>(threadIdx.x); i < C::kBlock; i += C::kThreads) s_max[i] = 0u;
     __syncthreads();
-    int plane = -1;
-    if (i < count) {
-      const int64_t x = begin + i;
-      const int j = sequence_at(s_first, a.tiles, c.Hkv, x);
-      const int64_t nc = s_first[j + 1] - s_first[j], rem = x - s_first[j] * c.Hkv;
-      const int h = static_cast<int>(quotient(rem, nc)), cc = static_cast<int>(rem - h * nc);
-      const int slot0 = TileWalk(s_range[j], a.reach, KT).at(cc) * KT, slot = slot0 + 32 * group;
-      const int origin = max(rec - cc, 0);
-      float ks = 1.f, vs = 0.f;
-      if (group < C::kGroups && slot < a.reach.base) {
-        const int page = page_of(c, a.table, 0, slot >> a.page_log2, c.max_pages);
-        if (page >= 0) {
-          plane = page * c.Hkv + h;
-          ks = c.k_scale[plane];
-          vs = c.v_scale[plane];
-          atomicMax(&s_max[origin], __float_as_uint(vs));
+    for (int at = static_cast<int>(threadIdx.x); at < 4 * C::kBlock; at += C::kThreads) {  // whole warps
+      const int rec = at / 4, group = at & 3, i = i0 + rec;
+      int plane = -1;
+      if (i < count) {
+        const int64_t x = begin + i;
+        const int j = sequence_at(s_first, a.tiles, c.Hkv, x);
+        const int64_t nc = s_first[j + 1] - s_first[j], rem = x - s_first[j] * c.Hkv;
+        const int h = static_cast<int>(quotient(rem, nc)), cc = static_cast<int>(rem - h * nc);
+        const int slot0 = TileWalk(s_range[j], a.reach, KT).at(cc) * KT, slot = slot0 + 32 * group;
+        const int origin = max(rec - cc, 0);
+        float ks = 1.f, vs = 0.f;
+        if (group < C::kGroups && slot < a.reach.base) {
+          const int page = page_of(c, a.table, 0, slot >> a.page_log2, c.max_pages);
+          if (page >= 0) {
+            plane = page * c.Hkv + h;
+            ks = c.k_scale[plane];
+            vs = c.v_scale[plane];
+            atomicMax(&s_max[origin], __float_as_uint(vs));
+          }
+        }
+        ChunkRec& to = s_rec[rec];
+        to.plane[group] = plane;
+        to.ks[group] = ks;
+        to.vs[group] = vs;
+        if (group == 0) {
+          to.item = j * c.Hkv + h;
+          to.slot = slot0;
+          to.origin = origin;
         }
       }
-      ChunkRec& to = s_rec[rec];
-      to.plane[group] = plane;
-      to.ks[group] = ks;
-      to.vs[group] = vs;
-      if (group == 0) {
-        to.item = j * c.Hkv + h;
-        to.slot = slot0;
-        to.origin = origin;
-      }
+      const unsigned there = __ballot_sync(0xffffffffu, plane >= 0) >> (lane & 28u);
+      constexpr unsigned kAll = (1u << C::kGroups) - 1u;
+      if (i < count && group == 0) s_rec[rec].whole = (there & kAll) == kAll;
     }
-    const unsigned there = __ballot_sync(0xffffffffu, plane >= 0) >> (lane & 28u);
-    constexpr unsigned kAll = (1u << C::kGroups) - 1u;
-    if (i < count && group == 0) s_rec[rec].whole = (there & kAll) == kAll;
     __syncthreads();
   };
   // The value reference: the largest scale of the item's chunks so far, a block of chunks at a time.
@@ -285,72 +283,37 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     return starts ? (top > 0.f ? top : 1.f) : fmaxf(vref, top);
   };
 
-  if (warp >= C::kKeyWarp) {
-    // ------------------------------------------------------------------ codes to operands, products
-    // Four warps take the keys, four the values; a thread has the codes of the next two chunks on their way.
-    constexpr int kUnitsRow = D / 16;  // 16 codes each
-    constexpr int kThr = 32 * C::kConvertWarps, kRowsPass = kThr / kUnitsRow;
-    constexpr int kPasses = KT / kRowsPass;  // units of a thread in a tile
-    static_assert(32 % kRowsPass == 0, "a pass lies within a group");
-    const int tid = static_cast<int>(threadIdx.x & (kThr - 1)), cu = tid % kUnitsRow;
-    // Neighbouring 64-column pieces of a row go to the same banks: every other one is taken a row on.
-    const int row0 = (tid / kUnitsRow) ^ ((cu >> 2) & 1);
-    const uint32_t piece = static_cast<uint32_t>(cu >> 2) * C::kKVChunk, unit = 2u * (cu & 3);
-    auto fetch = [&](const uint8_t* pool, uint4 (&to)[kPasses], int i) {
-      const ChunkRec& rec = s_rec[i];
-#pragma unroll
-      for (int g = 0; g < C::kGroups; ++g) {
-        const int pl = rec.plane[g];
-        const uint4* src = reinterpret_cast<const uint4*>(
-                               pool + (static_cast<size_t>(max(pl, 0)) * c.page +
-                                       ((rec.slot + 32 * g) & (c.page - 1)) + row0) * D) + cu;
-#pragma unroll
-        for (int p = 0; p < 32 / kRowsPass; ++p)
-          to[g * (32 / kRowsPass) + p] =
-              pl >= 0 ? load_codes(src + p * kRowsPass * kUnitsRow) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    constexpr uint32_t kIdS = idesc_f16kind(0u, kPrefixRows, KT, false, false);
-    constexpr uint32_t kIdO = idesc_f16kind(0u, kPrefixRows, D, false, true);
-    // S_g = Q K_g^T into buffer g & 1, once its scores before have become P.
-    auto issue_s = [&](int g, int s, uint32_t landed, bool starts, int seg) -> bool {
-      if (starts && !warp_wait(bar(C::kQFull), seg & 1, &abort_flag, c.err)) return false;
-      if (!warp_wait(bar(C::kKFull + s), landed, &abort_flag, c.err)) return false;
-      if (g >= 2 && !warp_wait(bar(C::kPFull + (g & 1)), ((g - 2) >> 1) & 1, &abort_flag, c.err))
-        return false;
-      tc_fence_after();
-      const uint64_t da = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t db = smem_desc_sw128(sK0 + s * C::kKVBytes, 16, 1024);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        umma_ss(tmem + C::kColS + KT * (g & 1), da + (ks / 4) * (C::kQChunk >> 4) + 2 * (ks % 4),
-                db + (ks / 4) * (C::kKVChunk >> 4) + 2 * (ks % 4), kIdS, ks > 0);
-      umma_commit_w(bar(C::kSFull + (g & 1)));
-      umma_commit_w(bar(C::kKEmpty + s));
-      return true;
-    };
-    // O (+)= P_g V_g; an item's first overwrites O, which the epilogue of the one before has read.
-    auto issue_pv = [&](int g, int s, uint32_t landed, bool starts, int seg) -> bool {
-      if (starts && seg > 0 && !warp_wait(bar(C::kOEmpty), (seg - 1) & 1, &abort_flag, c.err))
-        return false;
-      if (!warp_wait(bar(C::kVFull + s), landed, &abort_flag, c.err)) return false;
-      if (!warp_wait(bar(C::kPFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err)) return false;
-      tc_fence_after();
-      const uint64_t db = smem_desc_sw128(sV0 + s * C::kKVBytes, C::kKVChunk, 1024);
-#pragma unroll
-      for (int ks = 0; ks < KT / 16; ++ks)
-        umma_ts(tmem + C::kColO, tmem + C::kColP + KT / 2 * (g & 1) + 8 * ks, db + 128 * ks, kIdO,
-                !starts || ks > 0);
-      umma_commit_w(bar(C::kPVDone + (g & 1)));
-      umma_commit_w(bar(C::kVEmpty + s));
-      return true;
-    };
-    int item = -1, seg = -1, stage = 0;
+  if (warp >= C::kKeyWarp && warp < C::kMmaWarp) {
+    // ------------------------------------------------------------------ codes to operands
+    // A thread has the codes of the next chunk on their way while it converts this one's.
+    int item = -1, stage = 0;
     uint32_t phase = 1;  // the first round of stages is free
     float vref = 1.f;
     auto walk = [&](auto kind) {
       constexpr bool kValues = decltype(kind)::value;
       const uint8_t* pool = kValues ? c.v : c.k;
+      constexpr int kUnitsRow = D / 16;  // 16 codes each
+      constexpr int kThr = 32 * (kValues ? C::kValueWarps : C::kKeyWarps), kRowsPass = kThr / kUnitsRow;
+      constexpr int kPasses = KT / kRowsPass;  // units of a thread in a tile
+      static_assert(32 % kRowsPass == 0, "a pass lies within a group");
+      const int tid = static_cast<int>(threadIdx.x) - 32 * (kValues ? C::kValueWarp : C::kKeyWarp), cu = tid % kUnitsRow;
+      // Neighbouring 64-column pieces of a row go to the same banks: every other one is taken a row on.
+      const int row0 = (tid / kUnitsRow) ^ ((cu >> 2) & 1);
+      const uint32_t piece = static_cast<uint32_t>(cu >> 2) * C::kKVChunk, unit = 2u * (cu & 3);
+      auto fetch = [&](uint4 (&to)[kPasses], int i) {
+        const ChunkRec& rec = s_rec[i];
+  #pragma unroll
+        for (int g = 0; g < C::kGroups; ++g) {
+          const int pl = rec.plane[g];
+          const uint4* src = reinterpret_cast<const uint4*>(
+                                 pool + (static_cast<size_t>(max(pl, 0)) * c.page +
+                                         ((rec.slot + 32 * g) & (c.page - 1)) + row0) * D) + cu;
+  #pragma unroll
+          for (int p = 0; p < 32 / kRowsPass; ++p)
+            to[g * (32 / kRowsPass) + p] =
+                pl >= 0 ? load_codes(src + p * kRowsPass * kUnitsRow) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
       // 16 codes as fp16, values times `ratio`, into a row of a tile
       auto put = [&](uint32_t tile, int row, uint4 w, uint32_t ratio) {
         uint32_t y[8];
@@ -366,12 +329,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         st_shared_v4(to + sw128_offset(ur, unit), y[0], y[1], y[2], y[3]);
         st_shared_v4(to + sw128_offset(ur, unit + 1), y[4], y[5], y[6], y[7]);
       };
-      // Chunk g, record i of its block, of `n`: its codes become the operand, and those of the chunk two on are
+      // Chunk g, record i of its block, of `n`: its codes become the operand, and those of the next one are
       // sent for.
       auto step = [&](int g, int i, int n, uint4 (&codes)[kPasses]) -> bool {
         const ChunkRec& rec = s_rec[i];
         const bool starts = rec.item != item;
-        if (starts) ++seg;
         item = rec.item;
         uint32_t ratio[C::kGroups] = {};
         if constexpr (kValues) {
@@ -399,29 +361,23 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kFull + stage));
-        const int s = stage;
-        const uint32_t landed = phase ^ 1u;
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
         }
-        if (i + 2 < n) fetch(kValues ? c.v : c.k, codes, i + 2);
-        if (warp == (kValues ? C::kValueWarp : C::kKeyWarp))
-          return kValues ? issue_pv(g, s, landed, starts, seg) : issue_s(g, s, landed, starts, seg);
+        if (i + 1 < n) fetch(codes, i + 1);
         return true;
       };
       bool ok = true;
       for (int i0 = 0; i0 < count; i0 += C::kBlock) {
         look_up(i0);
         const int n = min(C::kBlock, count - i0);
-        uint4 even[kPasses], odds[kPasses];
+        uint4 even[kPasses];
         if (ok) {
-          fetch(pool, even, 0);
-          if (n > 1) fetch(pool, odds, 1);
+          fetch(even, 0);
         }
-        for (int i = 0; ok && i < n; i += 2) {
+        for (int i = 0; ok && i < n; ++i) {
           ok = step(i0 + i, i, n, even);
-          if (ok && i + 1 < n) ok = step(i0 + i + 1, i + 1, n, odds);
         }
       }
     };
@@ -430,267 +386,338 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       walk(std::true_type{});
     else
       walk(std::false_type{});
-    if (warp == C::kKeyWarp || warp == C::kValueWarp) {  // nothing issued is left running
-      umma_commit_w(bar(C::kDrain + values));
-      warp_drain_wait(bar(C::kDrain + values), 0, c.err);
-    }
-  } else {
-    // ------------------------------------------------------------------ softmax
-    constexpr int kHalfK = KT / 2, kHalfD = D / 2, kOwn = kHalfK / 32;  // groups of this thread's columns
-    const int r = static_cast<int>(threadIdx.x & 127);  // row of the tile = TMEM lane
-    const uint32_t h = warp >> 2;                          // half of the columns
-    const uint32_t quarter = warp & 3u, lane_base = (quarter * 32u) << 16;
-    int xn = 0;
-    // Swaps a value with the thread that has the other half of the row (slot xn & 1 was last used two
-    // exchanges ago, and the partner passed the one in between only after reading it).
-    auto exchange = [&](float v, float* other) -> bool {
-      float* red = s_red + (xn & 1) * 2 * kPrefixRows;
-      red[h * kPrefixRows + r] = v;
-      __syncwarp();
-      const uint32_t xb = bar(C::kXch + quarter * 2 + (xn & 1));
-      if (lane == 0) mbar_arrive(xb);
-      if (!warp_wait(xb, (xn >> 1) & 1, &abort_flag, c.err)) return false;
-      *other = red[(h ^ 1u) * kPrefixRows + r];
-      ++xn;
+  } else if (warp == C::kMmaWarp) {
+    // ------------------------------------------------------------------ products
+    constexpr uint32_t kIdS = idesc_f16kind(0u, kPrefixRows, KT, false, false);
+    constexpr uint32_t kIdO = idesc_f16kind(0u, kPrefixRows, D, false, true);
+    // S_g = Q K_g^T into buffer g & 1, whose scores before have become P.
+    auto issue_s = [&](int g) -> bool {
+      const int s = g % C::kKStages;
+      if (!warp_wait(bar(C::kKFull + s), (g / C::kKStages) & 1, &abort_flag, c.err)) return false;
+      tc_fence_after();
+      const uint64_t da = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t db = smem_desc_sw128(sK0 + s * C::kKVBytes, 16, 1024);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        umma_ss(tmem + C::kColS + KT * (g & 1), da + (ks / 4) * (C::kQChunk >> 4) + 2 * (ks % 4),
+                db + (ks / 4) * (C::kKVChunk >> 4) + 2 * (ks % 4), kIdS, ks > 0);
+      umma_commit_w(bar(C::kSFull + (g & 1)));
+      umma_commit_w(bar(C::kKEmpty + s));
       return true;
     };
-    int item = -1, lo = 0, hi = INT_MAX, all_lo = 0, all_hi = -1;
-    bool real = false, begins = false, ok = true;
-    float f = 0.f, vref = 1.f, m_ref = SWA_NEG_INF, l = 0.f;
+    auto issue_pv = [&](int g, bool first) -> bool {  // O (+)= P_g V_g
+      const int s = g % C::kVStages;
+      if (!warp_wait(bar(C::kVFull + s), (g / C::kVStages) & 1, &abort_flag, c.err)) return false;
+      if (!warp_wait(bar(C::kPFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err)) return false;
+      tc_fence_after();
+      const uint64_t db = smem_desc_sw128(sV0 + s * C::kKVBytes, C::kKVChunk, 1024);
+#pragma unroll
+      for (int ks = 0; ks < KT / 16; ++ks)
+        umma_ts(tmem + C::kColO, tmem + C::kColP + KT / 2 * (g & 1) + 8 * ks, db + 128 * ks, kIdO,
+                !first || ks > 0);
+      umma_commit_w(bar(C::kPVDone + (g & 1)));
+      umma_commit_w(bar(C::kVEmpty + s));
+      return true;
+    };
+    // S runs up to two chunks ahead, within an item: the next one's Q takes the place of this one's.
+    bool ok = true;
+    int item = -1, seg = -1, ahead = 0;  // chunks whose S has been issued
+    for (int i0 = 0; i0 < count; i0 += C::kBlock) {
+      look_up(i0);
+      const int end = min(count, i0 + C::kBlock);
+      for (int g = i0; ok && g < end; ++g) {
+        const int it = s_rec[g - i0].item;
+        const bool starts = it != item;
+        if (starts) {
+          ++seg;
+          item = it;
+          ok = warp_wait(bar(C::kQFull), seg & 1, &abort_flag, c.err);
+        }
+        while (ok && ahead < min(end, g + 2) && s_rec[ahead - i0].item == it) ok = issue_s(ahead++);
+        // an item's first P V overwrites O, which the epilogue of the one before has read
+        if (ok && starts && seg > 0) ok = warp_wait(bar(C::kOEmpty), (seg - 1) & 1, &abort_flag, c.err);
+        if (ok) ok = issue_pv(g, starts);
+      }
+    }
+    umma_commit_w(bar(C::kDrain));  // nothing issued is left running
+    warp_drain_wait(bar(C::kDrain), 0, c.err);
+  } else {
+    // ------------------------------------------------------------------ softmax
+    // Thread t of warp w has rows R0 = 32 (w % 4) + 16 (w / 4) + t / 4 and R1 = R0 + 8, and of every 8 columns
+    // the columns 2 kq, 2 kq + 1 (kq = t % 4): the 16x256b shape of TMEM.  Four threads have a row.
+    constexpr int kHalves = KT / 64;  // 64 columns at a time
+    const uint32_t lane0 = 32u * (warp & 3u) + 16u * (warp >> 2), lane_base = lane0 << 16;
+    const int r0 = static_cast<int>(lane0 + (lane >> 2)), kq = static_cast<int>(lane & 3u);
+    auto row_max = [](float v) {
+      v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+      return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+    };
+    auto row_sum = [](float v) {
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      return v + __shfl_xor_sync(0xffffffffu, v, 2);
+    };
+    int2* s_seen = reinterpret_cast<int2*>(smem + C::kOffSeen);
+    int item = -1;
+    bool begins = false, ok = true;
+    float f[2], m[2], l[2], vref = 1.f;
 
-    // Loads this thread's half of its row of q, scaled, into the Q tile.
-    auto start = [&](int new_item, int slot) -> bool {
+    // Loads this thread's quarters of its rows of q, scaled, into the Q tile.
+    auto start = [&](int new_item, int slot) {
       item = new_item;
       const int j = static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)));
       const int head = item - j * c.Hkv;
       const TileRange range = s_range[j];
       begins = slot == TileWalk(range, a.reach, KT).at(0) * KT;
-      all_lo = visible_lo(range.len_max_q, a.reach.window);
-      all_hi = min(range.end_min, a.reach.base) - 1;
-      const int rho = j * kPrefixRows + r;
-      real = false;
-      lo = 0;
-      hi = INT_MAX;  // rows that stand for nothing need no mask
-      const uint16_t* row = a.q;
-      if (rho < a.rows) {
-        const int b = static_cast<int>(a.div_r.div(static_cast<uint32_t>(rho)));
-        const int in_seq = rho - b * a.R, t = static_cast<int>(a.div_t.mod(static_cast<uint32_t>(in_seq)));
-        int len, n;
-        real = sequence_of(c, b, &len, &n) && t < n;
-        if (real) {
-          lo = visible_lo(len + t, a.reach.window);
-          hi = min(len + t, a.reach.base - 1);
-          row += ((static_cast<size_t>(b) * c.Hkv + head) * a.R + in_seq) * D + kHalfD * h;
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + 8 * e, rho = j * kPrefixRows + r;
+        bool is = false;
+        int2 seen = make_int2(0, INT_MAX);  // rows that stand for nothing need no mask
+        const uint16_t* row = a.q;
+        if (rho < a.rows) {
+          const int b = static_cast<int>(a.div_r.div(static_cast<uint32_t>(rho)));
+          const int in_seq = rho - b * a.R, t = static_cast<int>(a.div_t.mod(static_cast<uint32_t>(in_seq)));
+          int len, n;
+          is = sequence_of(c, b, &len, &n) && t < n;
+          if (is) {
+            seen = make_int2(visible_lo(len + t, a.reach.window), min(len + t, a.reach.base - 1));
+            row += ((static_cast<size_t>(b) * c.Hkv + head) * a.R + in_seq) * D;
+          }
         }
-      }
-      uint4 raw[kHalfD / 8];
+        uint4 raw[D / 32];
 #pragma unroll
-      for (int i = 0; i < kHalfD / 8; ++i)
-        raw[i] = real ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t top = 0;
-      auto pair_of = [&](uint32_t w) { return a.f16 ? Elem<true>::unpack(w) : Elem<false>::unpack(w); };
+        for (int i = 0; i < D / 32; ++i)
+          raw[i] = is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
+        auto pair_of = [&](uint32_t w) { return a.f16 ? Elem<true>::unpack(w) : Elem<false>::unpack(w); };
+        uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < kHalfD / 8; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 y = pair_of(w[e]);
-          top = max(top, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y))));
+          for (int z = 0; z < 4; ++z) {
+            const float2 y = pair_of(w[z]);
+            top = max(top, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y))));
+          }
         }
-      }
-      float other;
-      if (!exchange(__uint_as_float(top), &other)) return false;
-      top = max(top, __float_as_uint(other));
-      const int ex = static_cast<int>(top >> 23);
-      // 2^(14 - exponent); 1 for zero, infinity and NaN
-      const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-      // a row that is not finite has scores that are all NaN
-      f = ex == 255 ? __uint_as_float(0x7fffffffu)
-                    : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = static_cast<int>(top >> 23);
+        // 2^(14 - exponent); 1 for zero, infinity and NaN
+        const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+        // a row that is not finite has scores that are all NaN
+        const float fs = ex == 255 ? __uint_as_float(0x7fffffffu)
+                                   : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
-      for (int i = 0; i < kHalfD / 8; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t y[4];
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 z = pair_of(w[e]);
-          y[e] = Elem<true>::pack(z.x * up, z.y * up);
+          for (int z = 0; z < 4; ++z) {
+            const float2 v = pair_of(w[z]);
+            y[z] = Elem<true>::pack(v.x * up, v.y * up);
+          }
+          const uint32_t unit = 4u * i + static_cast<uint32_t>(kq);
+          st_shared_v4(sQ + (unit >> 3) * C::kQChunk + sw128_offset(static_cast<uint32_t>(r), unit & 7u),
+                       y[0], y[1], y[2], y[3]);
         }
-        const uint32_t col = kHalfD * h + 8u * i;
-        st_shared_v4(sQ + (col >> 6) * C::kQChunk +
-                         sw128_offset(static_cast<uint32_t>(r), (col & 63u) >> 3),
-                     y[0], y[1], y[2], y[3]);
+        if (kq == 0) s_seen[r] = seen;
+        if (e == 0)
+          f[0] = fs;
+        else
+          f[1] = fs;
       }
-      m_ref = SWA_NEG_INF;
-      l = 0.f;
+      m[0] = m[1] = SWA_NEG_INF;
+      l[0] = l[1] = 0.f;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::kQFull));
-      return true;
     };
 
     // The item's partial result after its chunk g at `slot`.
     auto finish = [&](int g, int slot) -> bool {
-      float l_other;
-      if (!exchange(l, &l_other)) return false;
+      const float sum0 = row_sum(l[0]), sum1 = row_sum(l[1]);
       if (!warp_wait(bar(C::kPVDone + (g & 1)), (g >> 1) & 1, &abort_flag, c.err)) return false;
       tc_fence_after();
       const int j = static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)));
       const TileWalk walk(s_range[j], a.reach, KT);
       const bool ends = slot == walk.at(walk.count - 1) * KT;
       const int at = begins && ends ? 2 * a.parts + item : partial_slot(part, begins);
-      const size_t to = static_cast<size_t>(at) * a.stored + r;
-      float* out = a.po + to * D + kHalfD * h;
+      const size_t to = static_cast<size_t>(at) * a.stored + r0;
+      const bool real[2] = {s_seen[r0].y != INT_MAX, s_seen[r0 + 8].y != INT_MAX};
 #pragma unroll 1
-      for (int c0 = 0; c0 < kHalfD; c0 += 32) {
+      for (int c0 = 0; c0 < D; c0 += 64) {
         uint32_t rr[32];
-        tmem_ld32(tmem + lane_base + C::kColO + kHalfD * h + c0, rr);
+        tmem_ld16x256_x8(tmem + lane_base + C::kColO + c0, rr);
         tmem_wait_ld(rr);
-        if (real) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(out + c0 + i) =
-                make_float4(__uint_as_float(rr[i]) * vref, __uint_as_float(rr[i + 1]) * vref,
-                            __uint_as_float(rr[i + 2]) * vref, __uint_as_float(rr[i + 3]) * vref);
+        for (int e = 0; e < 2; ++e) {
+          if (real[e]) {
+            float* out = a.po + (to + 8 * e) * D + c0 + 2 * kq;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float2*>(out + 8 * i) =
+                  make_float2(__uint_as_float(rr[4 * i + 2 * e]) * vref,
+                              __uint_as_float(rr[4 * i + 2 * e + 1]) * vref);
+          }
         }
       }
       warp_arrive(bar(C::kOEmpty));
-      if (real && h == 0)
-        *reinterpret_cast<float2*>(a.ml + to * 2) = make_float2(m_ref, l + l_other);
+      if (kq == 0) {
+        if (real[0]) *reinterpret_cast<float2*>(a.ml + to * 2) = make_float2(m[0], sum0);
+        if (real[1]) *reinterpret_cast<float2*>(a.ml + (to + 8) * 2) = make_float2(m[1], sum1);
+      }
       return true;
     };
 
     int last_slot = 0;
     for (int i0 = 0; i0 < count; i0 += C::kBlock) {
-    look_up(i0);
-    for (int g = i0; ok && g < min(count, i0 + C::kBlock); ++g) {
-      const ChunkRec& rec = s_rec[g - i0];
-      const int slot = rec.slot;
-      const bool starts = rec.item != item;
-      if (starts) {
-        if (item >= 0 && !(ok = finish(g - 1, last_slot))) break;
-        if (!(ok = start(rec.item, slot))) break;
-      }
-      last_slot = slot;
-      const float was = vref;
-      vref = reference(rec, vref, starts);
-      float fk[kOwn];
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        fk[i] = f * rec.ks[kOwn * h + i];
-        fk[i] = fk[i] < 1e-37f ? 1e-37f : fk[i];  // a masked score times zero would be NaN
-      }
-      if (!(ok = warp_wait(bar(C::kSFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err))) break;
-      tc_fence_after();
-      // 32 of this thread's scores of the chunk.  They are read from TMEM for each pass: held in registers
-      // all together they would spill, and what spills misses the little L1 that is left.
-      const bool edge = !rec.whole || (slot < all_lo && slot + KT > a.reach.sinks) || slot + KT - 1 > all_hi;
-      auto scores = [&](int o, float (&x)[32]) {
-        uint32_t rr[32];
-        tmem_ld32(tmem + lane_base + C::kColS + KT * (g & 1) + kHalfK * h + 32u * o, rr);
-        tmem_wait_ld(rr);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(rr[i]);
-        if (edge) {
-          const int s0 = slot + kHalfK * static_cast<int>(h) + 32 * o;
-          const int clo = lo - s0, chi = rec.plane[kOwn * h + o] >= 0 ? hi - s0 : -1, csink = a.reach.sinks - s0;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = (i >= clo || i < csink) && i <= chi ? x[i] : SWA_NEG_INF;
+      look_up(i0);
+      for (int g = i0; ok && g < min(count, i0 + C::kBlock); ++g) {
+        const ChunkRec& rec = s_rec[g - i0];
+        const int slot = rec.slot;
+        const bool starts = rec.item != item;
+        if (starts) {
+          if (item >= 0 && !(ok = finish(g - 1, last_slot))) break;
+          start(rec.item, slot);
         }
-      };
-      uint32_t pk[kHalfK / 2];
-      auto exponentiate = [&](float m) -> float {
-        const float2 neg_m2 = make_float2(-m, -m);
-        float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                        make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int o = 0; o < kOwn; ++o) {
-          float x[32];
-          scores(o, x);
-          const float2 s2 = make_float2(fk[o], fk[o]);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 t = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), s2, neg_m2);
-            const float2 e = make_float2(ex2(t.x), ex2(t.y));
-            rs[i & 3] = __fadd2_rn(rs[i & 3], e);
-            pk[16 * o + i] = Elem<true>::pack(e.x, e.y);
-          }
-        }
-        return ((rs[0].x + rs[0].y) + (rs[1].x + rs[1].y)) + ((rs[2].x + rs[2].y) + (rs[3].x + rs[3].y));
-      };
-      // One pass against the reference maximum; redone exactly on an item's first chunk or when a row's sum
-      // exceeds 2^12 (the two halves of a row decide alike).
-      bool redo = true;
-      float bsum = 0.f;
-      if (__all_sync(0xffffffffu, m_ref != SWA_NEG_INF)) {
-        bsum = exponentiate(m_ref);
-        float other;
-        if (!(ok = exchange(bsum, &other))) break;
-        redo = __any_sync(0xffffffffu, !(bsum + other <= kFastSumLimit));
-      }
-      float factor = starts ? 1.f : was / vref;
-      bool resc = factor != 1.f;
-      if (redo) {
-        float mx = SWA_NEG_INF;
-#pragma unroll
-        for (int o = 0; o < kOwn; ++o) {
-          float x[32], m4[4];
-          scores(o, x);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = x[i];
-#pragma unroll
-          for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
-          mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * fk[o]);
-        }
-        float mx_other;
-        if (!(ok = exchange(mx, &mx_other))) break;
-        const float m_new = fmaxf(m_ref, fmaxf(mx, mx_other));
-        if (m_new > m_ref + kRescaleThreshold) {
-          const float down = ex2(m_ref - m_new);  // 0 when m_ref is -inf
-          factor *= down;
-          l *= down;
-          m_ref = m_new;
-          resc = true;
-        }
-        bsum = exponentiate(m_ref == SWA_NEG_INF ? 0.f : m_ref);
-      }
-      l += bsum;
-      // P buffer g & 1 was last read by P V of chunk g - 2
-      if (g >= 2 && !(ok = warp_wait(bar(C::kPVDone + (g & 1)), ((g - 2) >> 1) & 1, &abort_flag, c.err)))
-        break;
-      if (!starts && __any_sync(0xffffffffu, resc)) {
-        if (!(ok = warp_wait(bar(C::kPVDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1, &abort_flag, c.err)))
+        last_slot = slot;
+        const float was = vref;
+        vref = reference(rec, vref, starts);
+        const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(rec.item)))];
+        const bool edge = !rec.whole || slot + KT > min(range.end_min, a.reach.base) ||
+                          (slot < visible_lo(range.len_max_q, a.reach.window) && slot + KT > a.reach.sinks);
+        if (!(ok = warp_wait(bar(C::kSFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err))) break;
+        // P buffer g & 1 was last read by P V of chunk g - 2
+        if (g >= 2 && !(ok = warp_wait(bar(C::kPVDone + (g & 1)), ((g - 2) >> 1) & 1, &abort_flag, c.err)))
           break;
         tc_fence_after();
-#pragma unroll 1
-        for (int c0 = 0; c0 < kHalfD; c0 += 32) {
-          const uint32_t oc = tmem + lane_base + C::kColO + kHalfD * h + c0;
+        const uint32_t s_addr = tmem + lane_base + C::kColS + KT * (g & 1);
+        // 64 columns of this thread's rows: x[4 i], x[4 i + 1] of R0 and x[4 i + 2], x[4 i + 3] of R1.  They
+        // are read from TMEM for each pass: held all together they would spill.
+        auto scores = [&](int half, float (&x)[32]) {
           uint32_t rr[32];
-          tmem_ld32(oc, rr);
+          tmem_ld16x256_x8(s_addr + 64u * half, rr);
           tmem_wait_ld(rr);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * factor);
-          tmem_st32(oc, rr);
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(rr[i]);
+          if (edge) {
+            const int2 seen[2] = {s_seen[r0], s_seen[r0 + 8]};
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {  // groups of 32 columns
+              const int s0 = slot + 64 * half + 32 * o + 2 * kq, csink = a.reach.sinks - s0;
+              const bool there = rec.plane[2 * half + o] >= 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int clo = seen[e].x - s0, chi = there ? seen[e].y - s0 : -1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int z = 0; z < 2; ++z) {
+                    float& y = x[16 * o + 4 * i + 2 * e + z];
+                    const int at = 8 * i + z;
+                    y = (at >= clo || at < csink) && at <= chi ? y : SWA_NEG_INF;
+                  }
+              }
+            }
+          }
+        };
+        // a masked score times zero would be NaN
+        auto factor_of = [&](int e, int o) {
+          const float y = f[e] * rec.ks[o];
+          return y < 1e-37f ? 1e-37f : y;
+        };
+        // One pass against the reference maxima; redone exactly on an item's first chunk or when a row's sum
+        // exceeds 2^12.
+        float fac[2] = {1.f, 1.f}, sum[2];
+        if (!starts && was != vref) fac[0] = fac[1] = was / vref;
+        bool exact = !__all_sync(0xffffffffu, m[0] != SWA_NEG_INF && m[1] != SWA_NEG_INF);
+        for (;;) {
+          if (exact) {
+            float mx[2] = {SWA_NEG_INF, SWA_NEG_INF};
+#pragma unroll 1
+            for (int half = 0; half < kHalves; ++half) {
+              float x[32];
+              scores(half, x);
+#pragma unroll
+              for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float top = fmaxf(x[16 * o + 2 * e], x[16 * o + 2 * e + 1]);
+#pragma unroll
+                  for (int i = 1; i < 4; ++i)
+                    top = fmaxf(top, fmaxf(x[16 * o + 4 * i + 2 * e], x[16 * o + 4 * i + 2 * e + 1]));
+                  mx[e] = fmaxf(mx[e], top * factor_of(e, 2 * half + o));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float now = fmaxf(m[e], row_max(mx[e]));
+              if (now > m[e] + kRescaleThreshold) {
+                const float down = ex2(m[e] - now);  // 0 when m is -inf
+                fac[e] *= down;
+                l[e] *= down;
+                m[e] = now;
+              }
+            }
+          }
+          const float at0 = m[0] == SWA_NEG_INF ? 0.f : m[0], at1 = m[1] == SWA_NEG_INF ? 0.f : m[1];
+          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half) {
+            float x[32];
+            scores(half, x);
+            uint32_t pk[16];  // pk[2 i] of R0, pk[2 i + 1] of R1: packed column 4 i + kq
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float g0 = factor_of(0, 2 * half + i / 4), g1 = factor_of(1, 2 * half + i / 4);
+              const float2 t0 = __ffma2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(g0, g0),
+                                           make_float2(-at0, -at0));
+              const float2 t1 = __ffma2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(g1, g1),
+                                           make_float2(-at1, -at1));
+              const float2 e0 = make_float2(ex2(t0.x), ex2(t0.y)), e1 = make_float2(ex2(t1.x), ex2(t1.y));
+              s0 = __fadd2_rn(s0, e0);
+              s1 = __fadd2_rn(s1, e1);
+              pk[2 * i] = Elem<true>::pack(e0.x, e0.y);
+              pk[2 * i + 1] = Elem<true>::pack(e1.x, e1.y);
+            }
+            tmem_st16x128_x8(tmem + lane_base + C::kColP + KT / 2 * (g & 1) + 32u * half, pk);
+          }
+          sum[0] = s0.x + s0.y;
+          sum[1] = s1.x + s1.y;
+          if (exact) break;
+          const float all0 = row_sum(sum[0]), all1 = row_sum(sum[1]);
+          if (!__any_sync(0xffffffffu, !(all0 <= kFastSumLimit) || !(all1 <= kFastSumLimit))) break;
+          exact = true;
         }
-      } else {
-        tc_fence_after();
+        l[0] += sum[0];
+        l[1] += sum[1];
+        if (!starts && __any_sync(0xffffffffu, fac[0] != 1.f || fac[1] != 1.f)) {
+          if (!(ok = warp_wait(bar(C::kPVDone + ((g - 1) & 1)), ((g - 1) >> 1) & 1, &abort_flag, c.err)))
+            break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 64) {
+            const uint32_t oc = tmem + lane_base + C::kColO + c0;
+            uint32_t rr[32];
+            tmem_ld16x256_x8(oc, rr);
+            tmem_wait_ld(rr);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              rr[i] = __float_as_uint(__uint_as_float(rr[i]) * ((i & 2) ? fac[1] : fac[0]));
+            tmem_st16x256_x8(oc, rr);
+          }
+        }
+        tmem_wait_st();
+        warp_arrive(bar(C::kPFull + (g & 1)));
       }
-      const uint32_t pc = tmem + lane_base + C::kColP + KT / 2 * (g & 1) + kHalfK / 2 * h;
-      if constexpr (kHalfK == 64)
-        tmem_st32(pc, pk);
-      else
-        tmem_st16(pc, pk);
-      tmem_wait_st();
-      warp_arrive(bar(C::kPFull + (g & 1)));
-    }
     }
     if (ok && item >= 0) finish(count - 1, last_slot);
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kKeyWarp) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -507,6 +507,15 @@ __device__ __forceinline__ void tmem_st16x128_x16(uint32_t taddr, const uint32_t
       : "memory");
 }
 
+// The same with 8 groups of 4 columns.
+__device__ __forceinline__ void tmem_st16x128_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      SWA_W8(0), SWA_W8(8)
+      : "memory");
+}
+
 // 32 lanes x 16 columns.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
