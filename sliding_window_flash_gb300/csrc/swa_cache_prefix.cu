@@ -130,7 +130,7 @@ struct TileWalk {
 // there, and for each group of 32 keys the plane (page * Hkv + head, or -1: nothing to be seen) and scales.
 struct ChunkRec {
   int item, slot, origin;
-  int whole;  // every group has a plane
+  int edge;  // some row of the tile does not see some of it
   int plane[4];
   float ks[4], vs[4];
 };
@@ -273,11 +273,18 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       }
       const unsigned there = __ballot_sync(0xffffffffu, plane >= 0) >> (lane & 28u);
       constexpr unsigned kAll = (1u << C::kGroups) - 1u;
-      if (i < count && group == 0) s_rec[rec].whole = (there & kAll) == kAll;
+      if (i < count && group == 0) {
+        ChunkRec& to = s_rec[rec];
+        const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(to.item)))];
+        to.edge = (there & kAll) != kAll || to.slot + KT > min(range.end_min, a.reach.base) ||
+                  (to.slot < visible_lo(range.len_max_q, a.reach.window) &&
+                   to.slot + KT > a.reach.sinks);
+      }
     }
     __syncthreads();
   };
-  // The value reference: the largest scale of the item's chunks so far, a block of chunks at a time.
+  // The value reference: the largest scale of the item's chunks so far, a block of chunks at a time; it moves
+  // where an item or a block begins.
   auto reference = [&](const ChunkRec& rec, float vref, bool starts) {
     const float top = __uint_as_float(s_max[rec.origin]);
     return starts ? (top > 0.f ? top : 1.f) : fmaxf(vref, top);
@@ -289,6 +296,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     int item = -1, stage = 0;
     uint32_t phase = 1;  // the first round of stages is free
     float vref = 1.f;
+    int lo = 0, end = 0;  // slots that some row of the tile sees
     auto walk = [&](auto kind) {
       constexpr bool kValues = decltype(kind)::value;
       const uint8_t* pool = kValues ? c.v : c.k;
@@ -337,11 +345,15 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         item = rec.item;
         uint32_t ratio[C::kGroups] = {};
         if constexpr (kValues) {
-          vref = reference(rec, vref, starts);
-  #pragma unroll
-          for (int o = 0; o < C::kGroups; ++o) ratio[o] = half2_of(rec.vs[o] / vref);
-          const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)))];
-          const int lo = visible_lo(range.len_min, a.reach.window), end = min(range.end_max, a.reach.base);
+          if (starts || i == 0) {
+            vref = reference(rec, vref, starts);
+            const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)))];
+            lo = visible_lo(range.len_min, a.reach.window);
+            end = min(range.end_max, a.reach.base);
+          }
+          const float inv = 1.f / vref;
+#pragma unroll
+          for (int o = 0; o < C::kGroups; ++o) ratio[o] = half2_of(rec.vs[o] * inv);
           // what nobody sees must not meet a probability of zero as infinity or NaN
           if (rec.slot + KT > end || (rec.slot < lo && rec.slot + KT > a.reach.sinks)) {
   #pragma unroll
@@ -468,7 +480,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       const int head = item - j * c.Hkv;
       const TileRange range = s_range[j];
       begins = slot == TileWalk(range, a.reach, KT).at(0) * KT;
-#pragma unroll 1
+      uint4 raw[2][D / 32];
+#pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = r0 + 8 * e, rho = j * kPrefixRows + r;
         bool is = false;
@@ -484,15 +497,19 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             row += ((static_cast<size_t>(b) * c.Hkv + head) * a.R + in_seq) * D;
           }
         }
-        uint4 raw[D / 32];
+        if (kq == 0) s_seen[r] = seen;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          raw[i] = is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
-        auto pair_of = [&](uint32_t w) { return a.f16 ? Elem<true>::unpack(w) : Elem<false>::unpack(w); };
+          raw[e][i] =
+              is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      auto pair_of = [&](uint32_t w) { return a.f16 ? Elem<true>::unpack(w) : Elem<false>::unpack(w); };
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          const uint32_t w[4] = {raw[e][i].x, raw[e][i].y, raw[e][i].z, raw[e][i].w};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const float2 y = pair_of(w[z]);
@@ -506,11 +523,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
         // a row that is not finite has scores that are all NaN
-        const float fs = ex == 255 ? __uint_as_float(0x7fffffffu)
-                                   : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+        f[e] = ex == 255 ? __uint_as_float(0x7fffffffu)
+                         : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          const uint32_t w[4] = {raw[e][i].x, raw[e][i].y, raw[e][i].z, raw[e][i].w};
           uint32_t y[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
@@ -518,14 +535,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
             y[z] = Elem<true>::pack(v.x * up, v.y * up);
           }
           const uint32_t unit = 4u * i + static_cast<uint32_t>(kq);
-          st_shared_v4(sQ + (unit >> 3) * C::kQChunk + sw128_offset(static_cast<uint32_t>(r), unit & 7u),
+          st_shared_v4(sQ + (unit >> 3) * C::kQChunk +
+                           sw128_offset(static_cast<uint32_t>(r0 + 8 * e), unit & 7u),
                        y[0], y[1], y[2], y[3]);
         }
-        if (kq == 0) s_seen[r] = seen;
-        if (e == 0)
-          f[0] = fs;
-        else
-          f[1] = fs;
       }
       m[0] = m[1] = SWA_NEG_INF;
       l[0] = l[1] = 0.f;
@@ -582,11 +595,12 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           start(rec.item, slot);
         }
         last_slot = slot;
-        const float was = vref;
-        vref = reference(rec, vref, starts);
-        const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(rec.item)))];
-        const bool edge = !rec.whole || slot + KT > min(range.end_min, a.reach.base) ||
-                          (slot < visible_lo(range.len_max_q, a.reach.window) && slot + KT > a.reach.sinks);
+        float fac[2] = {1.f, 1.f};  // of o and the sums so far
+        if (starts || g == i0) {
+          const float was = vref;
+          vref = reference(rec, vref, starts);
+          if (!starts) fac[0] = fac[1] = was / vref;
+        }
         if (!(ok = warp_wait(bar(C::kSFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err))) break;
         // P buffer g & 1 was last read by P V of chunk g - 2
         if (g >= 2 && !(ok = warp_wait(bar(C::kPVDone + (g & 1)), ((g - 2) >> 1) & 1, &abort_flag, c.err)))
@@ -594,15 +608,26 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + C::kColS + KT * (g & 1);
         // 64 columns of this thread's rows: x[4 i], x[4 i + 1] of R0 and x[4 i + 2], x[4 i + 3] of R1.  They
-        // are read from TMEM for each pass: held all together they would spill.
-        auto scores = [&](int half, float (&x)[32]) {
-          uint32_t rr[32];
-          tmem_ld16x256_x8(s_addr + 64u * half, rr);
-          tmem_wait_ld(rr);
+        // are read from TMEM for each pass.
+        auto scores = [&](float (&x)[kHalves][32]) {
+          uint32_t rr[kHalves][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(rr[i]);
-          if (edge) {
-            const int2 seen[2] = {s_seen[r0], s_seen[r0 + 8]};
+          for (int half = 0; half < kHalves; ++half) tmem_ld16x256_x8(s_addr + 64u * half, rr[half]);
+          tmem_wait_ld_all();
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half) {
+            reg_fence(rr[half]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[half][i] = __uint_as_float(rr[half][i]);
+          }
+        };
+        if (rec.edge) {  // what a row does not see becomes -inf, in TMEM: the passes need no mask of their own
+          const int2 seen[2] = {s_seen[r0], s_seen[r0 + 8]};
+#pragma unroll 1
+          for (int half = 0; half < kHalves; ++half) {
+            uint32_t rr[32];
+            tmem_ld16x256_x8(s_addr + 64u * half, rr);
+            tmem_wait_ld(rr);
 #pragma unroll
             for (int o = 0; o < 2; ++o) {  // groups of 32 columns
               const int s0 = slot + 64 * half + 32 * o + 2 * kq, csink = a.reach.sinks - s0;
@@ -614,23 +639,24 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                   for (int z = 0; z < 2; ++z) {
-                    float& y = x[16 * o + 4 * i + 2 * e + z];
+                    uint32_t& y = rr[16 * o + 4 * i + 2 * e + z];
                     const int at = 8 * i + z;
-                    y = (at >= clo || at < csink) && at <= chi ? y : SWA_NEG_INF;
+                    y = (at >= clo || at < csink) && at <= chi ? y : __float_as_uint(SWA_NEG_INF);
                   }
               }
             }
+            tmem_st16x256_x8(s_addr + 64u * half, rr);
           }
-        };
+          tmem_wait_st();
+        }
         // a masked score times zero would be NaN
         auto factor_of = [&](int e, int o) {
           const float y = f[e] * rec.ks[o];
           return y < 1e-37f ? 1e-37f : y;
         };
-        // One pass against the reference maxima; redone exactly on an item's first chunk or when a row's sum
-        // exceeds 2^12.
-        float fac[2] = {1.f, 1.f}, sum[2];
-        if (!starts && was != vref) fac[0] = fac[1] = was / vref;
+        // One pass against the reference maxima; redone exactly on an item's first chunk or when a thread's
+        // part of a row's sum exceeds 2^12.
+        float sum[2];
         bool exact = !__all_sync(0xffffffffu, m[0] != SWA_NEG_INF && m[1] != SWA_NEG_INF);
         for (;;) {
           if (exact) {
@@ -638,7 +664,13 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
 #pragma unroll 1
             for (int half = 0; half < kHalves; ++half) {
               float x[32];
-              scores(half, x);
+              {
+                uint32_t rr[32];
+                tmem_ld16x256_x8(s_addr + 64u * half, rr);
+                tmem_wait_ld(rr);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(rr[i]);
+              }
 #pragma unroll
               for (int o = 0; o < 2; ++o)
 #pragma unroll
@@ -663,10 +695,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           }
           const float at0 = m[0] == SWA_NEG_INF ? 0.f : m[0], at1 = m[1] == SWA_NEG_INF ? 0.f : m[1];
           float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+          float y[kHalves][32];
+          scores(y);
 #pragma unroll
           for (int half = 0; half < kHalves; ++half) {
-            float x[32];
-            scores(half, x);
+            const float (&x)[32] = y[half];
             uint32_t pk[16];  // pk[2 i] of R0, pk[2 i + 1] of R1: packed column 4 i + kq
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -686,8 +719,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           sum[0] = s0.x + s0.y;
           sum[1] = s1.x + s1.y;
           if (exact) break;
-          const float all0 = row_sum(sum[0]), all1 = row_sum(sum[1]);
-          if (!__any_sync(0xffffffffu, !(all0 <= kFastSumLimit) || !(all1 <= kFastSumLimit))) break;
+          if (!__any_sync(0xffffffffu, !(sum[0] <= kFastSumLimit) || !(sum[1] <= kFastSumLimit))) break;
           exact = true;
         }
         l[0] += sum[0];
