@@ -245,22 +245,57 @@ def _sinks_space(index, *sizes):
     return int(_cache._on(index, "swa_attn_sinks_workspace_bytes", *sizes))
 
 
-def _run_sinks(name, tensors, sizes, window, sinks, causal, scale, dt, workspace):
-    """Calls an entry point for sinks on the current stream of the tensors' GPU."""
-    import torch
-
-    device = tensors[0].device
-    for t in tensors:
-        if t.device != device:
-            raise ValueError(f"a tensor is on {t.device}, expected {device}")
-    window, causal, kind = _cache._int32(window), int(bool(causal)), _cache._t.kinds[dt]
+def _run_sinks(name, tensors, f32, sizes, window, sinks, causal, scale, workspace):
+    """Calls an entry point for sinks on the current stream of the tensors' GPU: `tensors` as (tensor, name,
+    shape) in the element type of the first, `f32` (their index, name, shape) the log-sum-exp among them."""
+    t = _cache._t
+    first = tensors[0][0]
+    device, dt = first.device, _elem_dtype(first)
+    index, kind = device.index, t.kinds[dt]
+    for i, (x, label, shape) in enumerate(tensors):
+        want = t.f32 if i == f32 else dt
+        if index is None or not _cache._good(x, shape, want, index):
+            _check_tensor(x, label, shape, want)
+            if x.device != device:
+                raise ValueError(f"{label} is on {x.device}, expected {device}")
+    window, causal = _cache._int32(window), int(bool(causal))
     if workspace is None:
-        need = _sinks_space(device.index, *sizes, window, sinks, causal, kind,
-                            int(name == "swa_attn_bwd_sinks"))
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    space = _cache._space(workspace, device)
-    _cache._run(name, device.index, *(t.data_ptr() for t in tensors), *sizes, window, sinks, causal,
+        need = _sinks_space(index, *sizes, window, sinks, causal, kind, int(name == "swa_attn_bwd_sinks"))
+        if need:
+            workspace = t.empty(need, dtype=t.u8, device=device)
+            space = workspace.data_ptr(), need
+        else:
+            space = None, 0
+    else:
+        space = _cache._space(workspace, device)
+    _cache._run(name, index, *[x.data_ptr() for x, _, _ in tensors], *sizes, window, sinks, causal,
                 _scale(scale, sizes[-1]), kind, *space)
+
+
+def _fwd_sinks(q, k, v, window, scale, out, lse, causal, workspace, sinks):
+    B, Hq, Hkv, Lq, Lk, D = sizes = _dims(q, k)
+    t, rows, keys = _cache._t, (B, Hq, Lq, D), (B, Hkv, Lk, D)
+    if out is None:
+        out = t.empty_like(q)
+    if lse is None:
+        lse = t.empty((B, Hq, Lq), dtype=t.f32, device=q.device)
+    _run_sinks("swa_attn_fwd_sinks", ((q, "q", rows), (k, "k", keys), (v, "v", keys), (out, "out", rows),
+                                      (lse, "lse", rows[:3])), 4, sizes, window, sinks, causal, scale,
+               workspace)
+    return out, lse
+
+
+def _bwd_sinks(q, k, v, o, do, lse, window, scale, dq, dk, dv, workspace, causal, sinks):
+    B, Hq, Hkv, Lq, Lk, D = sizes = _dims(q, k)
+    t, rows, keys = _cache._t, (B, Hq, Lq, D), (B, Hkv, Lk, D)
+    dq = t.empty_like(q) if dq is None else dq
+    dk = t.empty_like(k) if dk is None else dk
+    dv = t.empty_like(v) if dv is None else dv
+    _run_sinks("swa_attn_bwd_sinks", ((q, "q", rows), (k, "k", keys), (v, "v", keys), (o, "o", rows),
+                                      (do, "do", rows), (lse, "lse", rows[:3]), (dq, "dq", rows),
+                                      (dk, "dk", keys), (dv, "dv", keys)), 5, sizes, window, sinks, causal,
+               scale, workspace)
+    return dq, dk, dv
 
 
 def swa_attn_fwd(q, k, v, window: int, scale: Optional[float] = None, out=None, lse=None,
@@ -272,10 +307,11 @@ def swa_attn_fwd(q, k, v, window: int, scale: Optional[float] = None, out=None, 
     visible to every query behind them.  fp32 calls use a device workspace of
     swa_attn_f32_workspace_bytes, or of swa_attn_sinks_workspace_bytes (allocated here unless given).
     """
+    if sinks:
+        return _fwd_sinks(q, k, v, window, scale, out, lse, causal, workspace, _sinks(sinks))
     import torch
 
     lib = load()
-    sinks = _sinks(sinks)
     B, Hq, Hkv, Lq, Lk, D = _dims(q, k)
     dt = _elem_dtype(q)
     _check_tensor(q, "q", (B, Hq, Lq, D), dt)
@@ -287,10 +323,6 @@ def swa_attn_fwd(q, k, v, window: int, scale: Optional[float] = None, out=None, 
         lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
     _check_tensor(out, "out", (B, Hq, Lq, D), dt)
     _check_tensor(lse, "lse", (B, Hq, Lq), torch.float32)
-    if sinks:
-        _run_sinks("swa_attn_fwd_sinks", (q, k, v, out, lse), (B, Hq, Hkv, Lq, Lk, D), window, sinks,
-                   causal, scale, dt, workspace)
-        return out, lse
     ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr())
     f16 = dt == torch.float16
     st = _stream_handle(q.device)
@@ -331,12 +363,13 @@ def swa_attn_bwd(q, k, v, o, do, lse, window: int, scale: Optional[float] = None
     swa_attn_bwd_fused_workspace_bytes; dQ's fp32 additions run in a varying order).  fp32 tensors
     and calls with sinks (workspace of swa_attn_sinks_workspace_bytes) always take the split path;
     fused=True with sinks is refused."""
+    if sinks:
+        if fused:
+            raise ValueError("the fused backward has no sinks")
+        return _bwd_sinks(q, k, v, o, do, lse, window, scale, dq, dk, dv, workspace, causal, _sinks(sinks))
     import torch
 
     lib = load()
-    sinks = _sinks(sinks)
-    if sinks and fused:
-        raise ValueError("the fused backward has no sinks")
     B, Hq, Hkv, Lq, Lk, D = _dims(q, k)
     dt = _elem_dtype(q)
     for t, name, hs, L in ((q, "q", Hq, Lq), (k, "k", Hkv, Lk), (v, "v", Hkv, Lk), (o, "o", Hq, Lq),
@@ -348,10 +381,6 @@ def swa_attn_bwd(q, k, v, o, do, lse, window: int, scale: Optional[float] = None
     dv = torch.empty_like(v) if dv is None else dv
     for t, name, hs, L in ((dq, "dq", Hq, Lq), (dk, "dk", Hkv, Lk), (dv, "dv", Hkv, Lk)):
         _check_tensor(t, name, (B, hs, L, D), dt)
-    if sinks:
-        _run_sinks("swa_attn_bwd_sinks", (q, k, v, o, do, lse, dq, dk, dv),
-                   (B, Hq, Hkv, Lq, Lk, D), window, sinks, causal, scale, dt, workspace)
-        return dq, dk, dv
     ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
             dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
     f16 = dt == torch.float16

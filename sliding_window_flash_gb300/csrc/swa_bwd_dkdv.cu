@@ -539,8 +539,7 @@ cudaError_t launch_dkdv_d(const Problem& pb, const void* q, const void* k, const
       !make_tmap_3d(&tdv, dv, bhk, pb.span.Lk, D, kBlockN, F16))
     return cudaErrorInvalidValue;
   auto kern = swa_dkdv_kernel<D, F16, kSinks>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_dkdv_kernel<D, F16, kSinks>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   DkdvArgs a;
   a.lse = lse;

@@ -320,8 +320,7 @@ cudaError_t launch_dq_d(const Problem& pb, const void* q, const void* k, const v
       !make_tmap_3d(&tvs, v, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
   auto kern = swa_dq_kernel<D, F16, kSinks>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_dq_kernel<D, F16, kSinks>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   DqArgs a;
   a.lse = lse;

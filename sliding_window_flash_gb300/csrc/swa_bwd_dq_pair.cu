@@ -376,8 +376,7 @@ cudaError_t launch_dq_pair_d(const Problem& pb, const void* q, const void* k, co
       !make_tmap_3d(&tv64s, v, bhk, pb.span.Lk, D, C::kHalfRows, F16, pb.sinks))
     return cudaErrorInvalidValue;
   auto kern = swa_dq_pair_kernel<D, F16, kSinks>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_dq_pair_kernel<D, F16, kSinks>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   DqPairArgs a;
   a.lse = lse;

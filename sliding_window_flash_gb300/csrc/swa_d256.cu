@@ -572,11 +572,6 @@ bool kmap(CUtensorMap* m, const void* p, const Problem& pb, int seen = 0) {
                       seen);
 }
 
-template <typename Kern>
-cudaError_t set_smem(Kern kern, int bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <bool F16, bool kSinks>
 cudaError_t fwd256(const Problem& pb, const void* q, const void* k, const void* v, void* o,
                    float* lse, cudaStream_t stream) {
@@ -585,7 +580,7 @@ cudaError_t fwd256(const Problem& pb, const void* q, const void* k, const void* 
       !kmap(&tks, k, pb, pb.sinks) || !kmap(&tvs, v, pb, pb.sinks))
     return cudaErrorInvalidValue;
   auto kern = swa_fwd256_kernel<F16, kSinks>;
-  cudaError_t e = set_smem(kern, F256::kSmemBytes);
+  cudaError_t e = allow_smem<swa_fwd256_kernel<F16, kSinks>>(F256::kSmemBytes);
   if (e != cudaSuccess) return e;
   const Args256 a = make_args(pb, nullptr, nullptr, nullptr, lse);
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
@@ -601,7 +596,7 @@ cudaError_t dq256(const Problem& pb, const void* q, const void* k, const void* v
       !kmap(&tks, k, pb, pb.sinks) || !kmap(&tvs, v, pb, pb.sinks))
     return cudaErrorInvalidValue;
   auto kern = swa_dq256_kernel<F16, kSinks>;
-  cudaError_t e = set_smem(kern, Q256::kSmemBytes);
+  cudaError_t e = allow_smem<swa_dq256_kernel<F16, kSinks>>(Q256::kSmemBytes);
   if (e != cudaSuccess) return e;
   const Args256 a = make_args(pb, lse, delta, dq);
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();

@@ -729,13 +729,12 @@ cudaError_t launch_t(const Problem& pb, const void* q, const void* k, const void
   const unsigned grid = 2u * (static_cast<unsigned>((nkb + 1) / 2) * static_cast<unsigned>(a.BHK) +
                               static_cast<unsigned>(a.sink_pairs));
   auto kk = swa_dk256_pair_kernel<F16, kSinks>;
-  cudaError_t e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       KP::kSmemBytes);
+  cudaError_t e = allow_smem<swa_dk256_pair_kernel<F16, kSinks>>(KP::kSmemBytes);
   if (e != cudaSuccess) return e;
   kk<<<grid, KP::kThreads, KP::kSmemBytes, stream>>>(tq64, tdo64, tq128, tk, tv, tdk, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   auto kv = swa_dv256_pair_kernel<F16, kSinks>;
-  e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, VP::kSmemBytes);
+  e = allow_smem<swa_dv256_pair_kernel<F16, kSinks>>(VP::kSmemBytes);
   if (e != cudaSuccess) return e;
   kv<<<grid, VP::kThreads, VP::kSmemBytes, stream>>>(tq64, tdo128, tk, tdv, a);
   e = cudaGetLastError();

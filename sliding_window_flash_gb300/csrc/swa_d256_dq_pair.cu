@@ -353,8 +353,7 @@ cudaError_t launch_dq256_pair_t(const Problem& pb, const void* q, const void* k,
       !make_tmap_3d(&tk128s, k, bhk, pb.span.Lk, C::kD, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
   auto kern = swa_dq256_pair_kernel<F16, kSinks>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_dq256_pair_kernel<F16, kSinks>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   DqP256Args a;
   a.lse = lse;

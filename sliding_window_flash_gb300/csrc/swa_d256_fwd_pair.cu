@@ -339,8 +339,7 @@ cudaError_t launch_fwd256_pair_t(const Problem& pb, const void* q, const void* k
       !make_tmap_3d(&tv128s, v, bhk, pb.span.Lk, C::kD, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
   auto kern = swa_fwd256_pair_kernel<F16, kSinks>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_fwd256_pair_kernel<F16, kSinks>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   FwdP256Args a;
   a.lse = lse;

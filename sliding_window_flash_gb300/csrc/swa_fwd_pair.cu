@@ -572,8 +572,7 @@ cudaError_t launch_fwd_pair_d(const Problem& pb, const void* q, const void* k, c
       !make_tmap_3d(&tvs, v, bhk, pb.span.Lk, D, kBlockN, F16, pb.sinks))
     return cudaErrorInvalidValue;
   auto kern = swa_fwd_pair_kernel<D, F16, kSinks>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  cudaError_t e = allow_smem<swa_fwd_pair_kernel<D, F16, kSinks>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   FwdPairArgs a;
   a.lse = lse;

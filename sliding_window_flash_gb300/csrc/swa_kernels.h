@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -205,6 +206,19 @@ inline size_t sink_part_bytes(const Problem& pb) {
   if (pb.sinks == 0) return 0;
   return sink_part_offset(sink_plan(pb).splits, pb.B * pb.Hkv, 0, 0, pb.sinks, 0, pb.D) *
          sizeof(float);
+}
+
+// Allows kernel `Kernel` its dynamic shared memory on the current device, once for each device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 // Launchers (each returns the launch's cudaError_t).
