@@ -211,7 +211,8 @@ def _tables(cache, table, lens, new):
 def _int32(x):
     """The C int nearest to x: what an int does not hold must not wrap to another number.  A window past
     every slot means the same however large; what else is out of range is refused."""
-    return max(-2**31, min(int(x), 2**31 - 1))
+    x = int(x)
+    return x if -2**31 <= x < 2**31 else 2**31 - 1 if x > 0 else -2**31
 
 
 def _ptr(t):
