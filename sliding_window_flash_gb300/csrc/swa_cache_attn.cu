@@ -133,14 +133,6 @@ __device__ __forceinline__ uint32_t swizzle_of(int cols, uint32_t row) {
   return cols == 128 ? (row & 7u) : ((row >> 1) & 3u);
 }
 
-// Lets the next kernel of the stream be scheduled, and waits for the one before to be complete.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_predecessor() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // What a lane holds about one chunk of its team's next 32.
 struct ChunkInfo {
   int plane;  // page * Hkv + head, or -1: nothing to be seen there

@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   using C = PrefixCfg<D>;
   constexpr int KT = C::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
+  launch_dependents();
   if (!smem_base_ok(smem, c.err)) return;
   int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
   TileRange* s_range = reinterpret_cast<TileRange*>(smem + C::kOffRange);
@@ -473,14 +474,12 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     bool begins = false, ok = true;
     float f[2], m[2], l[2], vref = 1.f;
 
-    // Loads this thread's quarters of its rows of q, scaled, into the Q tile.
-    auto start = [&](int new_item, int slot) {
-      item = new_item;
-      const int j = static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)));
-      const int head = item - j * c.Hkv;
-      const TileRange range = s_range[j];
-      begins = slot == TileWalk(range, a.reach, KT).at(0) * KT;
-      uint4 raw[2][D / 32];
+    // Loads this thread's quarters of its rows of q into the Q tile, scaled.  They come there as they are, with
+    // their largest magnitude, and a loop scales them: straight code for all of it is run once and takes as
+    // long as its instructions take to be fetched (the start of an item 19,000 cycles at D = 256, 8,500 now).
+    auto start = [&](int j, int head) {
+      uint32_t top[2] = {0u, 0u};
+      uint32_t place[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = r0 + 8 * e, rho = j * kPrefixRows + r;
@@ -498,46 +497,52 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           }
         }
         if (kq == 0) s_seen[r] = seen;
+        // units kq and kq + 4 of every 64 columns
+        place[e] = sQ + sw128_offset(static_cast<uint32_t>(r), static_cast<uint32_t>(kq));
+        uint4 raw[D / 32];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          raw[e][i] =
-              is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      auto pair_of = [&](uint32_t w) { return a.f16 ? Elem<true>::unpack(w) : Elem<false>::unpack(w); };
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t top = 0;
+          raw[i] = is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          const uint32_t w[4] = {raw[e][i].x, raw[e][i].y, raw[e][i].z, raw[e][i].w};
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const float2 y = pair_of(w[z]);
-            top = max(top, max(__float_as_uint(fabsf(y.x)), __float_as_uint(fabsf(y.y))));
-          }
+          top[e] = __vmaxu2(top[e], __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
+                                             __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
+          st_shared_v4((place[e] ^ (64u * (i & 1))) + (i >> 1) * C::kQChunk, raw[i].x, raw[i].y, raw[i].z,
+                       raw[i].w);
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = static_cast<int>(top >> 23);
+      }
+      float up[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t most = max(top[e] & 0xffffu, top[e] >> 16);
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const uint32_t bits =
+            __float_as_uint(a.f16 ? Elem<true>::unpack(most).x : Elem<false>::unpack(most).x);
+        const int ex = static_cast<int>(bits >> 23);
         // 2^(14 - exponent); 1 for zero, infinity and NaN
-        const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+        const int sh = ex == 255 || bits == 0 ? 0 : min(126, 127 + 14 - ex);
+        up[e] = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
         // a row that is not finite has scores that are all NaN
         f[e] = ex == 255 ? __uint_as_float(0x7fffffffu)
                          : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+      }
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint32_t w[4] = {raw[e][i].x, raw[e][i].y, raw[e][i].z, raw[e][i].w};
-          uint32_t y[4];
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t at = (place[e] ^ (64u * (i & 1))) + (i >> 1) * C::kQChunk;
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(at)
+                       : "memory");
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const float2 v = pair_of(w[z]);
-            y[z] = Elem<true>::pack(v.x * up, v.y * up);
+            const float2 v = a.f16 ? Elem<true>::unpack(w[z]) : Elem<false>::unpack(w[z]);
+            w[z] = Elem<true>::pack(v.x * up[e], v.y * up[e]);
           }
-          const uint32_t unit = 4u * i + static_cast<uint32_t>(kq);
-          st_shared_v4(sQ + (unit >> 3) * C::kQChunk +
-                           sw128_offset(static_cast<uint32_t>(r0 + 8 * e), unit & 7u),
-                       y[0], y[1], y[2], y[3]);
+          st_shared_v4(at, w[0], w[1], w[2], w[3]);
         }
       }
       m[0] = m[1] = SWA_NEG_INF;
@@ -592,7 +597,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const bool starts = rec.item != item;
         if (starts) {
           if (item >= 0 && !(ok = finish(g - 1, last_slot))) break;
-          start(rec.item, slot);
+          item = rec.item;
+          const int j = static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)));
+          begins = slot == TileWalk(s_range[j], a.reach, KT).at(0) * KT;
+          start(j, item - j * c.Hkv);
         }
         last_slot = slot;
         float fac[2] = {1.f, 1.f};  // of o and the sums so far
@@ -602,9 +610,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           if (!starts) fac[0] = fac[1] = was / vref;
         }
         if (!(ok = warp_wait(bar(C::kSFull + (g & 1)), (g >> 1) & 1, &abort_flag, c.err))) break;
-        // P buffer g & 1 was last read by P V of chunk g - 2
-        if (g >= 2 && !(ok = warp_wait(bar(C::kPVDone + (g & 1)), ((g - 2) >> 1) & 1, &abort_flag, c.err)))
-          break;
+        // That these scores are there says too that P V of chunk g - 2, issued before them, has read the P buffer.
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + C::kColS + KT * (g & 1);
         // 64 columns of this thread's rows: x[4 i], x[4 i + 1] of R0 and x[4 i + 2], x[4 i + 3] of R1.  They
@@ -753,6 +759,9 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // This kernel may begin while the walk over the sequences' own slots ends; who waits for this one waits
+  // for both.
+  if (threadIdx.x == 0) wait_predecessor();
 }
 
 template <int D>
@@ -760,9 +769,17 @@ cudaError_t launch_prefix_d(const CacheView& c, const PrefixDev& a, cudaStream_t
   using C = PrefixCfg<D>;
   cudaError_t e = allow_smem<swa_cache_prefix_kernel<D>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  swa_cache_prefix_kernel<D>
-      <<<static_cast<unsigned>(a.parts), C::kThreads, C::kSmemBytes, stream>>>(c, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.parts));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, swa_cache_prefix_kernel<D>, c, a);
 }
 
 }  // namespace

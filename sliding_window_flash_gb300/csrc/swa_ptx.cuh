@@ -591,6 +591,14 @@ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t unit) {
 // Kernel-side helpers shared by the attention kernels
 // ------------------------------------------------------------------------------------------------
 
+// Lets the next kernel of the stream be scheduled, and waits for the one before to be complete.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 #define SWA_NEG_INF (-__int_as_float(0x7f800000))
