@@ -151,7 +151,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   constexpr int KT = C::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
   launch_dependents();
-  if (!smem_base_ok(smem, c.err)) return;
+  if (!smem_base_ok(smem, c.err)) {
+    wait_predecessor();
+    return;
+  }
   int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
   TileRange* s_range = reinterpret_cast<TileRange*>(smem + C::kOffRange);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
