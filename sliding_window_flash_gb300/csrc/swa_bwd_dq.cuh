@@ -109,7 +109,34 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
     const float lse2 = nxt_lse == SWA_POS_INF ? SWA_POS_INF : nxt_lse * kLog2e;
     const float dlt = nxt_dlt;
     fetch_rows(t + tile_step);
-    for (int j = 0; j < f.nkv; ++j) {
+    int j = 0;
+    if (kPair && f.is_narrow(0)) {  // of its 32 columns each half takes 16
+      if (!(ok = warp_wait(bar(DqBar::kSFull), g & 1, abort_flag, a.err))) break;
+      tc_fence_after();
+      uint32_t rs[16], rr[16], pk[8];
+      tmem_ld16(tmem + lane_base + kColS + 16u * h, rs);
+      tmem_wait_ld_all();
+      reg_fence(rs);
+      arrive(bar(DqBar::kSEmpty));
+      const uint32_t dp_col = tmem + lane_base + kColDP + 128u * (g & 1) + 16u * h;
+      if (!(ok = warp_wait(bar(DqBar::kDPFull + (g & 1)), (g >> 1) & 1, abort_flag, a.err))) break;
+      tc_fence_after();
+      tmem_ld16(dp_col, rr);
+      tmem_wait_ld_all();
+      reg_fence(rr);
+      const int sk = a.sinks - 16 * static_cast<int>(h);
+      auto ds = [&](int i) {
+        const float e = ex2(fmaf(__uint_as_float(rs[i]), sl2, -lse2));
+        return i < sk ? e * (__uint_as_float(rr[i]) - dlt) : 0.f;
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pk[i] = Elem<F16>::pack(ds(2 * i), ds(2 * i + 1));
+      tmem_st8(dp_col, pk);
+      tmem_wait_st();
+      arrive(bar(DqBar::kDSFull + (g & 1)));
+      j = 1;
+    }
+    for (; j < f.nkv; ++j) {
       const int gg = g + j;
       const int k0 = f.k0(j);
       if (!(ok = warp_wait(bar(DqBar::kSFull), gg & 1, abort_flag, a.err))) break;
@@ -126,7 +153,7 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
         for (int i = 0; i < 64; ++i) p[i] = __uint_as_float(rr[i >> 5][i & 31]);
       }
       arrive(bar(DqBar::kSEmpty));
-      if (j == 0 && prev_it >= 0) {  // the previous tile's epilogue (see below)
+      if (prev_it >= 0) {  // the previous tile's epilogue (see below)
         if (!(ok = epilogue(prev_it, prev_grow, prev_in))) break;
         prev_it = -1;
       }

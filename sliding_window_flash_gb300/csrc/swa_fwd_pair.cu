@@ -179,7 +179,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   // (forwarding its copies, in the same order): S for up to kSBufs key blocks ahead of P V over the
   // whole walk, across tiles, but never for a tile whose Q buffer is still the output staging area
   // of a tile with P V outstanding (S of tile i waits until every P V of tile i - 2 is issued).
-  // on_s(g, tile index, first block of its tile) and on_pv(g, tile index, block within the tile).
+  // on_s(g, tile index, first block of its tile) and on_pv(g, tile index, block within the tile,
+  // whether it is narrow).
   auto walk = [&](auto&& on_s, auto&& on_pv) -> bool {
     int s_t = tile0, s_it = 0, s_j = 0, s_g = 0;
     PairTile<kSinks> s_f = fwd_pair_tile<kSinks>(s_t < a.ntiles ? s_t : 0, a, sp, rank);
@@ -201,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     for (int t = tile0, it = 0; ok && t < a.ntiles; t += tile_step, ++it) {
       const PairTile<kSinks> f = fwd_pair_tile<kSinks>(t, a, sp, rank);
       for (int j = 0; ok && j < f.nkv; ++j) {
-        ok = on_pv(g + j, it, j);
+        ok = on_pv(g + j, it, j, f.is_narrow(j));
         if (ok) ok = fill_s(g + j + 1 + C::kSBufs, it + (j + 1 == f.nkv ? 1 : 0));
       }
       g += f.nkv;
@@ -297,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     };
     // O += P_gg V_gg with P_gg in buffer gg mod 3 (keys 16 ks .. 16 ks + 15 at packed columns
     // 8 ks .. 8 ks + 7); a tile's first P V overwrites O once both CTAs' epilogues have read it.
-    auto on_pv = [&](int gg, int it, int j) -> bool {
+    auto on_pv = [&](int gg, int it, int j, bool narrow) -> bool {
       const int s = gg % C::kVStages, n = gg / C::kVStages, pb = gg % C::kSBufs;
       if (j == 0 && it > 0 &&
           !warp_wait_cluster(bar(C::kOEmpty), (it - 1) & 1, &abort_flag, a.err))
@@ -306,9 +307,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         return false;
       if (!warp_wait_cluster(bar(C::kVFull + s), n & 1, &abort_flag, a.err)) return false;
       tc_fence_after();
-      umma2_ts_mnmajor_x8(tmem + C::kColO, tmem + C::kColS + 128u * pb,
-                                smem_desc_sw128(sV0 + s * C::kVHalfBytes, C::kVHalfBytes, 1024),
-                                kIdO, j == 0 ? 0u : 1u);
+      const uint64_t v_desc = smem_desc_sw128(sV0 + s * C::kVHalfBytes, C::kVHalfBytes, 1024);
+      if (narrow)
+        umma2_ts_mnmajor_x2(tmem + C::kColO, tmem + C::kColS + 128u * pb, 8u, v_desc, kIdO,
+                            j == 0 ? 0u : 1u);
+      else
+        umma2_ts_mnmajor_x8(tmem + C::kColO, tmem + C::kColS + 128u * pb, v_desc, kIdO,
+                            j == 0 ? 0u : 1u);
       umma2_commit_w(bar(C::kPVDone + pb));
       umma2_commit_w(bar(C::kVEmpty + s));
       return true;
@@ -329,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       if (first_of_tile && !relay(C::kQFull + (qit & 1), (qit >> 1) & 1)) return false;
       return relay(C::kKFull + gg % C::kKStages, (gg / C::kKStages) & 1);
     };
-    auto on_pv = [&](int gg, int, int) -> bool {
+    auto on_pv = [&](int gg, int, int, bool) -> bool {
       return relay(C::kVFull + gg % C::kVStages, (gg / C::kVStages) & 1);
     };
     walk(on_s, on_pv);
@@ -377,7 +382,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       const int row0 = q0 + r0, row1 = row0 + 8;
       float m0 = SWA_NEG_INF, m1 = SWA_NEG_INF;  // reference max (log2 domain) of rows R0, R1
       float l0 = 0.f, l1 = 0.f;                  // partial sums over this thread's columns
-      for (int j = 0; j < f.nkv; ++j) {
+      int j = 0;
+      if (f.is_narrow(0)) {
+        const int sb = g % C::kSBufs;
+        if (!(ok = warp_wait(bar(C::kSFull + sb), (g / C::kSBufs) & 1, &abort_flag, a.err))) break;
+        tc_fence_after();
+        const uint32_t s_addr = tmem + lane_base + C::kColS + 128u * sb;
+        // A few sinks, seen by every row that is computed, in groups 0..3 of 8 columns.  As the tile's
+        // first block they set the reference.
+        uint32_t rr[16];
+        tmem_ld16x256_x4(s_addr, rr);
+        tmem_wait_ld_all();
+        reg_fence(rr);
+        float y[16], a0 = SWA_NEG_INF, a1 = SWA_NEG_INF;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const bool vis = 8 * (i >> 2) + (i & 1) + 2 * kq < a.sinks;
+          y[i] = vis ? __uint_as_float(rr[i]) : SWA_NEG_INF;
+          if (i & 2)
+            a1 = fmaxf(a1, y[i]);
+          else
+            a0 = fmaxf(a0, y[i]);
+        }
+        a0 = row_max(a0) * sl2;
+        a1 = row_max(a1) * sl2;
+        m0 = a0;
+        m1 = a1;
+        if (a0 == SWA_NEG_INF) a0 = 0.f;
+        if (a1 == SWA_NEG_INF) a1 = 0.f;
+        uint32_t pk[8];
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const float e0 = ex2(fmaf(y[4 * jj], sl2, -a0)), e1 = ex2(fmaf(y[4 * jj + 1], sl2, -a0));
+          const float e2 = ex2(fmaf(y[4 * jj + 2], sl2, -a1)), e3 = ex2(fmaf(y[4 * jj + 3], sl2, -a1));
+          l0 += e0 + e1;
+          l1 += e2 + e3;
+          pk[2 * jj] = Elem<F16>::pack(e0, e1);
+          pk[2 * jj + 1] = Elem<F16>::pack(e2, e3);
+        }
+        tmem_st16x128_x4(s_addr, pk);
+        tmem_wait_st();
+        warp_arrive_rank0(bar(C::kPFull + sb));
+        j = 1;
+      }
+      for (; j < f.nkv; ++j) {
         const int gg = g + j;
         const int k0 = f.k0(j);
         const int sb = gg % C::kSBufs;

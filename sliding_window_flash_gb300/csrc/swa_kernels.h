@@ -61,16 +61,23 @@ struct Span {
 // sequence's first `sinks` keys that lie before the window's (its far sinks, all of them visible to
 // every query of the tile), then the window's blocks.  Far blocks are loaded through tensor maps that
 // end behind the last sink, so what the other keys of a far block hold reads as zero.
+// A far block of kNarrowSinks sinks or fewer is narrow: the pair kernels exponentiate and multiply its
+// first 32 keys only.  A few sinks are the usual case, and a whole block for them costs an eighth of the
+// call at a window of 1024.
+constexpr int kNarrowSinks = 32;
 template <bool kSinks>
 struct KeyWalk {
   int kb_lo, nkv;  // first block of the window; blocks in all
   int far;         // far blocks
+  bool narrow;     // the only far block has kNarrowSinks sinks or fewer
   __host__ __device__ void set(const Span& sp, int sinks, int q0) {
     kb_lo = sp.first_kblock(q0);
     far = 0;
+    narrow = false;
     if constexpr (kSinks) {
       far = (sinks + kBlockN - 1) / kBlockN;
       if (far > kb_lo) far = kb_lo;
+      narrow = far == 1 && sinks <= kNarrowSinks;
     }
     nkv = sp.last_kblock(q0) - kb_lo + 1 + far;
   }
@@ -80,6 +87,7 @@ struct KeyWalk {
     return (kb_lo + j) * kBlockN;
   }
   __host__ __device__ bool is_far(int j) const { return kSinks && j < far; }
+  __host__ __device__ bool is_narrow(int j) const { return kSinks && narrow && j == 0; }
 };
 
 // Columns c of 64 or 128 keys visible to a row: [lo, hi], and with kSinks those below `sk` up to hi.

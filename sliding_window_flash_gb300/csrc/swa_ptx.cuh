@@ -454,6 +454,24 @@ __device__ __forceinline__ void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[3
       : "r"(taddr));
 }
 
+// The same over 32 columns: groups j of 0..3.
+__device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : SWA_R8(0), SWA_R8(8)
+      : "r"(taddr));
+}
+
+// 32 lanes x 16 columns, thread t lane t.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : SWA_R8(0), SWA_R8(8)
+      : "r"(taddr));
+}
+
 // Waits for this thread's outstanding TMEM loads; `r` is passed through so that no use of the
 // loaded registers can be scheduled before the wait.
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
@@ -513,6 +531,22 @@ __device__ __forceinline__ void tmem_st16x128_x8(uint32_t taddr, const uint32_t 
       "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
       "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       SWA_W8(0), SWA_W8(8)
+      : "memory");
+}
+
+// The same over 4 groups of 4 columns.
+__device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      SWA_W8(0)
+      : "memory");
+}
+
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      SWA_W8(0)
       : "memory");
 }
 
@@ -861,6 +895,22 @@ __device__ __forceinline__ void umma2_ts_mnmajor_x8(uint32_t d_tmem, uint32_t a_
       "add.s32 ra, %1, 56;\n\tadd.s64 rb, %2, 896;\n\t"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ra], rb, %3, t;\n\t"
       "}" ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The first two of those MMAs (K = 32), the second one's A `step` columns behind the first's.
+__device__ __forceinline__ void umma2_ts_mnmajor_x2(uint32_t d_tmem, uint32_t a_tmem, uint32_t step,
+                                                    uint64_t b_desc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 rb;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 t, %4, %4;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %3, %4, p;\n\t"
+      "add.s64 rb, %3, 128;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%2], rb, %4, t;\n\t"
+      "}" ::"r"(d_tmem), "r"(a_tmem), "r"(a_tmem + step), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
