@@ -248,14 +248,18 @@ __global__ void __launch_bounds__(352, 1)
       return true;
     };
     // dQ += dS_gg K_gg with dS_gg in dP buffer gg & 1: keys 16 ks .. 16 ks + 15 at packed column
-    // 8 ks + 32 (ks / 4).
-    auto issue_dq = [&](int gg, bool first, bool tile_last) -> bool {
+    // 8 ks + 32 (ks / 4), of a narrow block at 16 ks.
+    auto issue_dq = [&](int gg, bool first, bool tile_last, bool narrow) -> bool {
       const int s = gg % C::kKStages, db = gg & 1;
       if (!warp_wait(bar(C::kDSFull + db), (gg >> 1) & 1, &abort_flag, a.err)) return false;
       tc_fence_after();
-      umma_ts_mnmajor_x8_split(tmem + C::kColDQ, tmem + C::kColDP + 128u * db,
-                               smem_desc_sw128(sK0 + s * C::kTileBytes, C::kChunkBytes, 1024),
-                               kIdDq, first ? 0u : 1u);
+      const uint64_t k_desc = smem_desc_sw128(sK0 + s * C::kTileBytes, C::kChunkBytes, 1024);
+      if (narrow)
+        umma_ts_mnmajor_x2(tmem + C::kColDQ, tmem + C::kColDP + 128u * db, 16u, k_desc, kIdDq,
+                           first ? 0u : 1u);
+      else
+        umma_ts_mnmajor_x8_split(tmem + C::kColDQ, tmem + C::kColDP + 128u * db, k_desc, kIdDq,
+                                 first ? 0u : 1u);
       umma_commit_w(bar(C::kKEmpty + s));
       if (tile_last) umma_commit_w(bar(C::kDQDone));
       return true;
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(352, 1)
         // have read it.
         if (ok && j == 0 && it > 0)
           ok = warp_wait(bar(C::kDQEmpty), (it - 1) & 1, &abort_flag, a.err);
-        if (ok) ok = issue_dq(g + j, j == 0, j + 1 == n);
+        if (ok) ok = issue_dq(g + j, j == 0, j + 1 == n, f.is_narrow(j));
       }
       g += n;
     }

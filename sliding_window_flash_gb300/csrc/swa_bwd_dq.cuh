@@ -110,7 +110,7 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
     const float dlt = nxt_dlt;
     fetch_rows(t + tile_step);
     int j = 0;
-    if (kPair && f.is_narrow(0)) {  // of its 32 columns each half takes 16
+    if (f.is_narrow(0)) {  // of its 32 columns each half takes 16
       if (!(ok = warp_wait(bar(DqBar::kSFull), g & 1, abort_flag, a.err))) break;
       tc_fence_after();
       uint32_t rs[16], rr[16], pk[8];

@@ -273,14 +273,18 @@ __global__ void __launch_bounds__(384, 1)
     };
     // O += P_gg V_gg.  P over S: keys 16 ks .. 16 ks + 15 at packed column 8 ks + 32 (ks / 4) of
     // buffer gg mod kSBufs (each half-row's P over the first 32 of its 64 columns); else at column
-    // 8 ks of P buffer gg & 1.
-    auto issue_pv = [&](int gg, bool first) -> bool {
+    // 8 ks of P buffer gg & 1; of a narrow block at column 16 ks of either.
+    auto issue_pv = [&](int gg, bool first, bool narrow) -> bool {
       const int s = gg % C::kVStages, n = gg / C::kVStages, pb = gg % C::kSBufs;
       if (!warp_wait(bar(C::kPFull + pb), (gg / C::kSBufs) & 1, &abort_flag, a.err)) return false;
       if (!warp_wait(bar(C::kVFull + s), n & 1, &abort_flag, a.err)) return false;
       tc_fence_after();
       const uint64_t vdesc = smem_desc_sw128(sV0 + s * C::kTileBytes, C::kChunkBytes, 1024);
-      if constexpr (C::kPOverS)
+      if (narrow)
+        umma_ts_mnmajor_x2(tmem + C::kColO,
+                           tmem + (C::kPOverS ? C::kColS + 128u * pb : C::kColP + 64u * pb), 16u,
+                           vdesc, kIdO, first ? 0u : 1u);
+      else if constexpr (C::kPOverS)
         umma_ts_mnmajor_x8_split(tmem + C::kColO, tmem + C::kColS + 128u * pb, vdesc, kIdO,
                                  first ? 0u : 1u);
       else
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(384, 1)
       for (int j = 0; ok && j < f.nkv; ++j) {
         // The first P V of a tile overwrites O: the previous tile's epilogue must have read it.
         if (j == 0 && it > 0) ok = warp_wait(bar(C::kOEmpty), (it - 1) & 1, &abort_flag, a.err);
-        if (ok) ok = issue_pv(g + j, j == 0);
+        if (ok) ok = issue_pv(g + j, j == 0, f.is_narrow(j));
         if (ok) ok = fill_s(g + j + 1 + C::kSBufs, it + (j + 1 == f.nkv ? 1 : 0));
       }
       g += f.nkv;
@@ -379,7 +383,47 @@ __global__ void __launch_bounds__(384, 1)
       const int row = q0 + r;
       float m_ref = SWA_NEG_INF;  // reference max (log2 domain) that P and l are taken against
       float l = 0.f;              // partial row sum over this thread's half of the columns
-      for (int j = 0; j < f.nkv; ++j) {
+      int j = 0;
+      if (f.is_narrow(0)) {
+        // A few sinks, seen by every row that is computed; of the 32 columns each half takes 16.  As
+        // the tile's first block they set the reference.
+        const int sb = g % C::kSBufs;
+        if (!(ok = warp_wait(bar(C::kSFull + sb), (g / C::kSBufs) & 1, &abort_flag, a.err))) break;
+        tc_fence_after();
+        uint32_t rr[16], pk[8];
+        tmem_ld16(tmem + lane_base + C::kColS + 128u * sb + 16u * h, rr);
+        tmem_wait_ld_all();
+        reg_fence(rr);
+        const int sk = a.sinks - 16 * static_cast<int>(h);
+        float y[16], mx = SWA_NEG_INF;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          y[i] = i < sk ? __uint_as_float(rr[i]) : SWA_NEG_INF;
+          mx = fmaxf(mx, y[i]);
+        }
+        float other;
+        if (!(ok = exchange(mx * sl2, &other))) break;
+        m_ref = fmaxf(mx * sl2, other);
+        const float m = m_ref == SWA_NEG_INF ? 0.f : m_ref;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e0 = ex2(fmaf(y[2 * i], sl2, -m)), e1 = ex2(fmaf(y[2 * i + 1], sl2, -m));
+          l += e0 + e1;
+          pk[i] = Elem<F16>::pack(e0, e1);
+        }
+        if constexpr (!C::kPOverS) {
+          if (g >= 2 &&
+              !(ok = warp_wait(bar(C::kPVDone + sb), ((g - 2) >> 1) & 1, &abort_flag, a.err)))
+            break;
+          tc_fence_after();
+        }
+        tmem_st8(tmem + lane_base + (C::kPOverS ? C::kColS + 128u * sb : C::kColP + 64u * sb) + 16u * h,
+                 pk);
+        tmem_wait_st();
+        warp_arrive(bar(C::kPFull + sb));
+        j = 1;
+      }
+      for (; j < f.nkv; ++j) {
         const int gg = g + j;
         const int k0 = f.k0(j);
         const int sb = gg % C::kSBufs;

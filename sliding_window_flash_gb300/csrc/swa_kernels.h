@@ -61,7 +61,7 @@ struct Span {
 // sequence's first `sinks` keys that lie before the window's (its far sinks, all of them visible to
 // every query of the tile), then the window's blocks.  Far blocks are loaded through tensor maps that
 // end behind the last sink, so what the other keys of a far block hold reads as zero.
-// A far block of kNarrowSinks sinks or fewer is narrow: the pair kernels exponentiate and multiply its
+// A far block of kNarrowSinks sinks or fewer is narrow: the kernels for D <= 128 exponentiate and multiply its
 // first 32 keys only.  A few sinks are the usual case, and a whole block for them costs an eighth of the
 // call at a window of 1024.
 constexpr int kNarrowSinks = 32;

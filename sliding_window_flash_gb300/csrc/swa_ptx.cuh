@@ -339,6 +339,22 @@ __device__ __forceinline__ void umma_ts_mnmajor_x8(uint32_t d_tmem, uint32_t a_t
       : "memory");
 }
 
+// The first two of those MMAs (K = 32), the second one's A `step` columns behind the first's.
+__device__ __forceinline__ void umma_ts_mnmajor_x2(uint32_t d_tmem, uint32_t a_tmem, uint32_t step,
+                                                   uint64_t b_desc, uint32_t idesc,
+                                                   uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 rb;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 t, %4, %4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %3, %4, p;\n\t"
+      "add.s64 rb, %3, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], rb, %4, t;\n\t"
+      "}" ::"r"(d_tmem), "r"(a_tmem), "r"(a_tmem + step), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ void umma_ts_mnmajor_x8_split(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -59,9 +59,10 @@ SHAPES = [
     Shape(1, 1, 1, 200, 600, 256, 50, 150, dtype=FP32),
     Shape(1, 1, 1, 6000, 6000, 64, 100, 2),     # a sink's walk in many parts
     Shape(1, 2, 1, 5000, 5000, 256, 200, 260),
-    # as many sinks as a narrow block holds, and one more or less, on pairs
-    *[Shape(1, 2, 1, 300, 800, D, 150, S, dtype=t) for S, t in ((16, BF16), (31, FP16), (32, BF16), (33, FP16))
-      for D in (128, 256)],
+    # as many sinks as a narrow block holds, and one more or less, on single CTAs and on pairs
+    *[Shape(1, Hq, 1, 300, 800, D, 150, S, dtype=t)
+      for S, t in ((16, BF16), (17, BF16), (31, FP16), (32, BF16), (33, FP16))
+      for Hq, D in ((1, 64), (1, 128), (2, 128), (2, 256))],
 ]
 
 
