@@ -273,6 +273,11 @@ def _run_sinks(name, tensors, f32, sizes, window, sinks, causal, scale, workspac
 
 
 def _fwd_sinks(q, k, v, window, scale, out, lse, causal, workspace, sinks):
+    done = _cache._t.fwd(q, k, v, out, lse, workspace, window, scale, causal, sinks)
+    if type(done) is tuple:
+        return done
+    if done is not None:
+        raise SwaError(done, "swa_attn_fwd_sinks")
     B, Hq, Hkv, Lq, Lk, D = sizes = _dims(q, k)
     t, rows, keys = _cache._t, (B, Hq, Lq, D), (B, Hkv, Lk, D)
     if out is None:
@@ -286,6 +291,11 @@ def _fwd_sinks(q, k, v, window, scale, out, lse, causal, workspace, sinks):
 
 
 def _bwd_sinks(q, k, v, o, do, lse, window, scale, dq, dk, dv, workspace, causal, sinks):
+    done = _cache._t.bwd(q, k, v, o, do, lse, dq, dk, dv, workspace, window, scale, causal, sinks)
+    if type(done) is tuple:
+        return done
+    if done is not None:
+        raise SwaError(done, "swa_attn_bwd_sinks")
     B, Hq, Hkv, Lq, Lk, D = sizes = _dims(q, k)
     t, rows, keys = _cache._t, (B, Hq, Lq, D), (B, Hkv, Lk, D)
     dq = t.empty_like(q) if dq is None else dq

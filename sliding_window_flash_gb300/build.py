@@ -1,19 +1,23 @@
-"""Build libswa.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked.
+"""Build libswa.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked; and beside it
+_swa_torch.so, the binding's short way to it (csrc/swa_torch.cpp, with torch's headers).
 
     python -m sliding_window_flash_gb300.build [--verbose] [--ptxas-info]
 
 Objects go to sliding_window_flash_gb300/_build/, the library to sliding_window_flash_gb300/libswa.so.
-Only nvcc and the CUDA toolkit are needed (no GPU): the build runs the same on x86_64 and aarch64.
+nvcc and the CUDA toolkit are needed, for the second a C++ compiler and torch (no GPU): the build runs
+the same on x86_64 and aarch64.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -21,6 +25,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libswa.so")
+TORCH_SRC = os.path.join(CSRC, "swa_torch.cpp")
+TORCH_PATH = os.path.join(PKG_DIR, "_swa_torch.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ARCH_FLAGS + [
@@ -58,6 +64,19 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_command(nvcc: str, out: str):
+    """The compiler's command for the binding's module: torch is found, not imported."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib = os.path.join(torch, "lib")
+    include = [INCLUDE, os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+               sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-fvisibility=hidden", *["-I" + d for d in include], TORCH_SRC, "-o", out, "-L" + lib,
+            "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
     """Compile (if needed) and return the path of libswa.so."""
     nvcc = _nvcc()
@@ -72,6 +91,9 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
         if force or ptxas_info or _stale(obj, [src] + headers):
             cmd = [nvcc] + COMMON_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append((src, cmd))
+    short = TORCH_PATH + ".tmp"
+    if force or _stale(TORCH_PATH, [TORCH_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        jobs.insert(0, (TORCH_SRC, _torch_command(nvcc, short)))
 
     def run(job):
         src, cmd = job
@@ -84,9 +106,11 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             for src, r in ex.map(run, jobs):
                 if r.returncode != 0:
-                    raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+                    raise RuntimeError(f"the compiler failed for {src}:\n{r.stdout}\n{r.stderr}")
                 if verbose or ptxas_info:
                     sys.stdout.write(r.stdout + r.stderr)
+                if src == TORCH_SRC:
+                    os.replace(short, TORCH_PATH)
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp"
         cmd = [nvcc] + ARCH_FLAGS + ["-shared", "-o", tmp] + objs

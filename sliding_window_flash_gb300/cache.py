@@ -84,8 +84,29 @@ class _Torch:
             f8=torch.float8_e4m3fn, f32=torch.float32, i32=torch.int32, u8=torch.uint8,
             kinds={torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}, Tensor=torch.Tensor,
             empty=torch.empty, empty_like=torch.empty_like, stream=torch._C._cuda_getCurrentRawStream,
-            current_device=torch._C._cuda_getDevice)
+            current_device=torch._C._cuda_getDevice, **_short_way())
         return self.__dict__[name]
+
+
+def _short_way():
+    """The calls of _swa_torch.so: each answers a call whose arguments are plainly in order, with what it
+    returns or the status of an error, and None for any other.  Without the module every call is another."""
+    try:
+        from . import _swa_torch as m
+
+        m.use(*[ctypes.cast(_entry(name), _vp).value for name in (
+            "swa_cache_attn", "swa_cache_attn_sinks", "swa_cache_attn_shared",
+            "swa_cache_attn_shared_workspace_bytes", "swa_attn_fwd_sinks", "swa_attn_bwd_sinks",
+            "swa_attn_sinks_workspace_bytes")])
+        return {"attn": m.cache_attn, "fwd": m.fwd, "bwd": m.bwd}
+    except ImportError:
+        return dict.fromkeys(("attn", "fwd", "bwd"), lambda *_: None)
+
+
+def _raise(rc, name):
+    from . import SwaError
+
+    raise SwaError(rc, name)
 
 
 _t = _Torch()
@@ -244,9 +265,7 @@ def _run(name, index, *args):
     """Calls entry point `name` on the current stream of GPU `index`, with that GPU current."""
     rc = _on(index, name, *args, _t.stream(index))
     if rc != 0:
-        from . import SwaError
-
-        raise SwaError(rc, name)
+        _raise(rc, name)
 
 
 def _dtype(t, name, fp32=False):
@@ -322,6 +341,13 @@ def swa_cache_attn(q, cache: SwaCache, table, lens, window: int, scale: Optional
     accumulate).  The workspace (of swa_cache_attn_workspace_bytes, for this window, sinks and shared;
     without shared also for any window) is allocated here unless given.
     """
+    if type(cache) is SwaCache:
+        done = _t.attn(cache.held, q, table, lens, new, out, lse, workspace, window, scale, accumulate, sinks,
+                       shared)
+        if type(done) is tuple:
+            return done
+        if done is not None:
+            _raise(done, "swa_cache_attn" + ("_shared" if shared else "_sinks" if sinks else ""))
     B, width, index = _tables(cache, table, lens, new)
     dev, (_, Hkv, page, D) = cache.held[5:]
     if not isinstance(q, _t.Tensor) or q.dim() != 4:
