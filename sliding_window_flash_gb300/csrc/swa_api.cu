@@ -152,6 +152,7 @@ swa_status bwd_impl(int f16, const void* q, const void* k, const void* v, const 
     return SWA_ERR_CUDA;
   if (swa::launch_bwd_dq(pb, q, k, v, dO, lse, delta, dq, stream) != cudaSuccess)
     return SWA_ERR_CUDA;
+  if (pb.sinks > 0 && swa::launch_sink_join(pb, dk, dv, stream) != cudaSuccess) return SWA_ERR_CUDA;
   return SWA_OK;
 }
 
@@ -530,6 +531,8 @@ swa_status bwd_f32_impl(const float* q, const float* k, const float* v, const fl
     return SWA_ERR_CUDA;
   if (swa::launch_bwd_dq(pb, ws + L.q16, ws + L.k16, ws + L.v16, ws + L.a16, lse, delta,
                          ws + L.dq16, stream) != cudaSuccess)
+    return SWA_ERR_CUDA;
+  if (pb.sinks > 0 && swa::launch_sink_join(pb, ws + L.dk16, ws + L.dv16, stream) != cudaSuccess)
     return SWA_ERR_CUDA;
   swa::WidenJob w{};
   w.src[0] = reinterpret_cast<const uint16_t*>(ws + L.dq16); w.dst[0] = dq;

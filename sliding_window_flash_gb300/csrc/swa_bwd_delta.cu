@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(256) swa_delta_kernel(const uint16_t* __restri
                                                         float* __restrict__ delta,
                                                         long long rows, float* __restrict__ dq_acc,
                                                         long long acc_floats) {
+  launch_dependents();
   constexpr int kLanesPerRow = D / 8;
   constexpr int kRowsPerWarp = 32 / kLanesPerRow;
   const int lane = static_cast<int>(threadIdx.x & 31);

@@ -91,6 +91,10 @@ __global__ void __launch_bounds__(352, 1)
   using C = DkdvCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) {  // Delta is there; dQ, which only reads what this kernel reads, may begin
+    wait_predecessor();
+    launch_dependents();
+  }
   if (!smem_base_ok(smem, a.err)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
@@ -566,9 +570,10 @@ cudaError_t launch_dkdv_d(const Problem& pb, const void* q, const void* k, const
   }
   const unsigned grid =
       static_cast<unsigned>(a.nkb) * static_cast<unsigned>(a.BHK) + static_cast<unsigned>(a.sink_ctas);
+  if (kSinks)
+    return launch_early(kern, grid, C::kThreads, C::kSmemBytes, stream, tq, tdo, tk, tv, tdk, tdv, a);
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk, tv, tdk, tdv, a);
-  e = cudaGetLastError();
-  return e != cudaSuccess || !kSinks ? e : launch_sink_join(pb, a.splits, dk, dv, stream);
+  return cudaGetLastError();
 }
 
 }  // namespace

@@ -107,7 +107,11 @@ __global__ void __launch_bounds__(352, 1)
   using C = DqCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
-  if (!smem_base_ok(smem, a.err)) return;
+  if constexpr (kSinks) launch_dependents();
+  if (!smem_base_ok(smem, a.err)) {
+    if constexpr (kSinks) wait_predecessor();
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);  // raised by a failed wait
@@ -307,6 +311,8 @@ __global__ void __launch_bounds__(352, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  if constexpr (kSinks)  // what follows may take dK and dV to be complete too
+    if (threadIdx.x == 0) wait_predecessor();
 }
 
 template <int D, bool F16, bool kSinks>
@@ -345,6 +351,9 @@ cudaError_t launch_dq_d(const Problem& pb, const void* q, const void* k, const v
   a.divHq = FastDiv(static_cast<uint32_t>(a.Hq));
   a.divG = FastDiv(static_cast<uint32_t>(a.G));
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
+  if (kSinks)
+    return launch_early(kern, static_cast<unsigned>(grid), C::kThreads, C::kSmemBytes, stream, tq, tdo, tk,
+                        tv, tks, tvs, a);
   kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk, tv, tks, tvs, a);
   return cudaGetLastError();
 }

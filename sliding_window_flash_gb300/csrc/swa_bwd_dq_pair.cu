@@ -122,6 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   using C = DqPairCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) launch_dependents();
   // Both CTAs always reach the cluster barriers and the collective TMEM allocation; a misaligned
   // window only disables the work (and is reported).
   const bool smem_ok = (smem_u32(smem) & 1023u) == 0u;
@@ -361,6 +362,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::kTmemCols);
   }
+  if constexpr (kSinks)  // what follows may take dK and dV to be complete too
+    if (threadIdx.x == 0) wait_predecessor();
 }
 
 template <int D, bool F16, bool kSinks>
@@ -403,6 +406,9 @@ cudaError_t launch_dq_pair_d(const Problem& pb, const void* q, const void* k, co
   const int clusters =
       max_pair_clusters<swa_dq_pair_kernel<D, F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
+  if (kSinks)
+    return launch_early(kern, 2u * static_cast<unsigned>(nclusters), C::kThreads, C::kSmemBytes, stream, tq,
+                        tdo, tk64, tk128, tv64, tk64s, tk128s, tv64s, a);
   kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk64, tk128, tv64, tk64s,
                                                               tk128s, tv64s, a);
   return cudaGetLastError();

@@ -12,6 +12,7 @@ template <bool F16>
 __global__ void __launch_bounds__(256)
     swa_sink_join_kernel(const float* part, uint16_t* dk, uint16_t* dv, int splits, int heads,
                          int sinks, int Lk, int D, float scale) {
+  wait_predecessor();
   const long long quads = static_cast<long long>(heads) * 2 * sinks * (D / 4);
   const size_t step = sink_part_offset(1, heads, 0, 0, sinks, 0, D);
   for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < quads;
@@ -39,16 +40,14 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-cudaError_t launch_sink_join(const Problem& pb, int splits, void* dk, void* dv,
-                             cudaStream_t stream) {
+cudaError_t launch_sink_join(const Problem& pb, void* dk, void* dv, cudaStream_t stream) {
   const int heads = pb.B * pb.Hkv;
   const long long quads = static_cast<long long>(heads) * 2 * pb.sinks * (pb.D / 4);
   const long long blocks = (quads + 255) / 256, most = 16ll * sm_count();
   auto kern = pb.f16 ? swa_sink_join_kernel<true> : swa_sink_join_kernel<false>;
-  kern<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream>>>(
-      pb.sink_part, static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv), splits, heads, pb.sinks,
-      pb.span.Lk, pb.D, pb.scale);
-  return cudaGetLastError();
+  return launch_early(kern, static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream,
+                      pb.sink_part, static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv),
+                      sink_plan(pb).splits, heads, pb.sinks, pb.span.Lk, pb.D, pb.scale);
 }
 
 }  // namespace swa

@@ -366,7 +366,11 @@ __global__ void __launch_bounds__(384, 1)
   using C = Q256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
-  if (!smem_base_ok(smem, a.err)) return;
+  if constexpr (kSinks) launch_dependents();
+  if (!smem_base_ok(smem, a.err)) {
+    if constexpr (kSinks) wait_predecessor();
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
@@ -537,6 +541,8 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if constexpr (kSinks)  // what follows may take dK and dV to be complete too
+    if (threadIdx.x == 0) wait_predecessor();
 }
 
 // ================================================================================================
@@ -600,6 +606,9 @@ cudaError_t dq256(const Problem& pb, const void* q, const void* k, const void* v
   if (e != cudaSuccess) return e;
   const Args256 a = make_args(pb, lse, delta, dq);
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
+  if (kSinks)
+    return launch_early(kern, static_cast<unsigned>(grid), Q256::kThreads, Q256::kSmemBytes, stream, tq, tdo,
+                        tk, tv, tks, tvs, a);
   kern<<<grid, Q256::kThreads, Q256::kSmemBytes, stream>>>(tq, tdo, tk, tv, tks, tvs, a);
   return cudaGetLastError();
 }

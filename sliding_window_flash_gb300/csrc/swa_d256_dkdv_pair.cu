@@ -219,6 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   using C = VP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) launch_dependents();
   const Span sp = a.span;
   const uint32_t rank = cluster_rank();
   const bool lead = rank == 0u;
@@ -419,6 +420,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+  if constexpr (kSinks)  // what follows may take dK to be complete too
+    if (threadIdx.x == 0) wait_predecessor();
 }
 
 // ================================================================================================
@@ -464,6 +467,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   using C = KP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) {  // Delta is there; dV and dQ, which only read what this kernel reads, may begin
+    wait_predecessor();
+    launch_dependents();
+  }
   const Span sp = a.span;
   const uint32_t rank = cluster_rank();
   const bool lead = rank == 0u;
@@ -731,14 +738,17 @@ cudaError_t launch_t(const Problem& pb, const void* q, const void* k, const void
   auto kk = swa_dk256_pair_kernel<F16, kSinks>;
   cudaError_t e = allow_smem<swa_dk256_pair_kernel<F16, kSinks>>(KP::kSmemBytes);
   if (e != cudaSuccess) return e;
+  auto kv = swa_dv256_pair_kernel<F16, kSinks>;
+  if ((e = allow_smem<swa_dv256_pair_kernel<F16, kSinks>>(VP::kSmemBytes)) != cudaSuccess) return e;
+  if (kSinks) {
+    e = launch_early(kk, grid, KP::kThreads, KP::kSmemBytes, stream, tq64, tdo64, tq128, tk, tv, tdk, a);
+    return e != cudaSuccess ? e : launch_early(kv, grid, VP::kThreads, VP::kSmemBytes, stream, tq64, tdo128,
+                                               tk, tdv, a);
+  }
   kk<<<grid, KP::kThreads, KP::kSmemBytes, stream>>>(tq64, tdo64, tq128, tk, tv, tdk, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  auto kv = swa_dv256_pair_kernel<F16, kSinks>;
-  e = allow_smem<swa_dv256_pair_kernel<F16, kSinks>>(VP::kSmemBytes);
-  if (e != cudaSuccess) return e;
   kv<<<grid, VP::kThreads, VP::kSmemBytes, stream>>>(tq64, tdo128, tk, tdv, a);
-  e = cudaGetLastError();
-  return e != cudaSuccess || !kSinks ? e : launch_sink_join(pb, a.splits, dk, dv, stream);
+  return cudaGetLastError();
 }
 
 }  // namespace

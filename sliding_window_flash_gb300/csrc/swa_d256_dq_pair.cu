@@ -116,6 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   using C = DqP256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) launch_dependents();
   // Both CTAs always reach the cluster barriers and the collective TMEM allocation; a misaligned
   // window only disables the work (and is reported).
   const bool smem_ok = (smem_u32(smem) & 1023u) == 0u;
@@ -334,6 +335,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+  if constexpr (kSinks)  // what follows may take dK and dV to be complete too
+    if (threadIdx.x == 0) wait_predecessor();
 }
 
 template <bool F16, bool kSinks>
@@ -376,6 +379,9 @@ cudaError_t launch_dq256_pair_t(const Problem& pb, const void* q, const void* k,
   const int clusters =
       max_pair_clusters<swa_dq256_pair_kernel<F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
+  if (kSinks)
+    return launch_early(kern, 2u * static_cast<unsigned>(nclusters), C::kThreads, C::kSmemBytes, stream, tq,
+                        tdo, tk64, tv64, tk128, tk64s, tv64s, tk128s, a);
   kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tdo, tk64, tv64, tk128,
                                                               tk64s, tv64s, tk128s, a);
   return cudaGetLastError();

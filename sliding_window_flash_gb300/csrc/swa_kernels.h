@@ -111,7 +111,7 @@ struct Problem {
 
 // dK and dV of the sinks.  A sink is seen by every query behind it, where another key is seen by a
 // window of them, so the walk over the query tiles of a sinks' key block is cut into `splits` parts;
-// their fp32 sums are joined in order (launch_sink_join), which replaces the first `sinks` rows of dK and
+// their fp32 sums are joined in order (launch_sink_join, behind dQ), which replaces the first `sinks` rows of dK and
 // dV.  The parts go first in the launch that walks the windows' key blocks.  A part is at most half of
 // an SM's share of that launch's tiles, so that the windows' walks fill up what the parts leave.
 // `width`: key blocks that a CTA (1) or a pair of them (2) takes.
@@ -229,6 +229,24 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// Launches `kern` so that it may begin before the kernel ahead of it in the stream has ended, as far as
+// that one allows it (launch_dependents) and `kern` itself waits (wait_predecessor).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t stream,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Launchers (each returns the launch's cudaError_t).
 cudaError_t launch_fwd(const Problem& pb, const void* q, const void* k, const void* v, void* o,
                        float* lse, cudaStream_t stream);
@@ -253,7 +271,7 @@ cudaError_t launch_dq_pair(const Problem& pb, const void* q, const void* k, cons
                            cudaStream_t stream);
 
 // dK and dV rows of the sinks from the parts' sums (swa_bwd_sinks.cu).
-cudaError_t launch_sink_join(const Problem& pb, int splits, void* dk, void* dv, cudaStream_t stream);
+cudaError_t launch_sink_join(const Problem& pb, void* dk, void* dv, cudaStream_t stream);
 
 // Fused backward (swa_bwd_fused.cu): dK, dV and the dQ partials of every (key block, query tile)
 // pair in one kernel.  dQ accumulates in fp32, tile-major: block (bhq, qb) holds query rows
