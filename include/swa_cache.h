@@ -137,8 +137,9 @@ swa_status swa_cache_attn_sinks(const swa_cache* cache, const int* table, int ma
  *   accumulate : has to be 0 with shared > 0 (the weights of shared pages would be added to by all
  *                sequences at once); (Hq / Hkv) T <= 65536 then.
  *   workspace  : at least swa_cache_attn_shared_workspace_bytes bytes, on the terms of swa_cache_attn's.
- * Where the pages that one product takes together (128 slots; 64 at D = 256) have value scales that
- * differ by more than 2^8, a value keeps an absolute error of 2^-25 of the largest of these scales.
+ * Values are taken relative to the largest value scale among the shared pages of their kv head (in as far
+ * as a part of the walk meets them): exactly while their own scale is at least 2^-15 of it, and below that
+ * with an absolute error of 2^-25 of it.
  * Scores, statistics and sums are fp32, p is rounded to fp16 as in swa_cache_attn.  The same call on one GPU
  * gives the same bits.
  */
@@ -194,6 +195,18 @@ swa_status swa_attn_key_weights(const void* q, const void* k, const float* lse, 
                                 int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
                                 float scale, int dtype, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream);
+
+/*
+ * The same with sinks (sinks >= 0), after swa_attn_fwd_sinks gave lse: the first `sinks` keys receive
+ * weight from every query behind them.  sinks = 0, or a window that reaches every key, is
+ * swa_attn_key_weights.
+ */
+size_t swa_attn_key_weights_sinks_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D,
+                                                  int window, int sinks, int causal);
+swa_status swa_attn_key_weights_sinks(const void* q, const void* k, const float* lse, float* w, int B,
+                                      int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks,
+                                      int causal, float scale, int dtype, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

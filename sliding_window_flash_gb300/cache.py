@@ -70,6 +70,9 @@ SIGNATURES = {
     "swa_attn_key_weights_workspace_bytes": (ctypes.c_size_t, [_c_int] * 8),
     "swa_attn_key_weights": (
         _c_int, [_vp] * 4 + [_c_int] * 8 + [_c_float, _c_int, _vp, ctypes.c_size_t, _vp]),
+    "swa_attn_key_weights_sinks_workspace_bytes": (ctypes.c_size_t, [_c_int] * 9),
+    "swa_attn_key_weights_sinks": (
+        _c_int, [_vp] * 4 + [_c_int] * 9 + [_c_float, _c_int, _vp, ctypes.c_size_t, _vp]),
 }
 
 
@@ -307,7 +310,8 @@ def _attn_space(index, *sizes):
 
 @functools.lru_cache(maxsize=256)
 def _weights_space(index, *sizes):
-    return int(_on(index, "swa_attn_key_weights_workspace_bytes", *sizes))
+    sinks = "_sinks" if len(sizes) == 9 else ""
+    return int(_on(index, f"swa_attn_key_weights{sinks}_workspace_bytes", *sizes))
 
 
 def swa_cache_attn_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, max_pages: int,
@@ -416,18 +420,21 @@ def swa_cache_evict(cache: SwaCache, table, lens, dst_table, budget: int, recent
 
 
 def swa_attn_key_weights_workspace_bytes(B: int, Hq: int, Hkv: int, Lq: int, Lk: int, D: int,
-                                         window: int, causal: bool = True) -> int:
+                                         window: int, causal: bool = True, sinks: int = 0) -> int:
     """Bytes of swa_attn_key_weights' workspace on the current GPU."""
-    return int(_entry("swa_attn_key_weights_workspace_bytes")(B, Hq, Hkv, Lq, Lk, D, _int32(window),
-                                                              int(bool(causal))))
+    sizes = B, Hq, Hkv, Lq, Lk, D, _int32(window)
+    if sinks:
+        return int(_entry("swa_attn_key_weights_sinks_workspace_bytes")(*sizes, _int32(sinks),
+                                                                        int(bool(causal))))
+    return int(_entry("swa_attn_key_weights_workspace_bytes")(*sizes, int(bool(causal))))
 
 
 def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, causal: bool = True,
-                         out=None, workspace=None):
+                         out=None, workspace=None, sinks: int = 0):
     """The attention weight every key of a prompt received: fp32 [B,Hkv,Lk], the sum over the query
     heads of its kv head and the queries that see it of exp(scale <q, k> - lse).  q [B,Hq,Lq,D] and
     k [B,Hkv,Lk,D] in bf16 or fp16, lse [B,Hq,Lq] as swa_attn_fwd returned it for the same window,
-    scale and causal.  The workspace (of swa_attn_key_weights_workspace_bytes) is allocated here
+    scale, causal and sinks.  The workspace (of swa_attn_key_weights_workspace_bytes) is allocated here
     unless given."""
     for t in (q, k):
         if not isinstance(t, _t.Tensor) or t.dim() != 4:
@@ -447,15 +454,17 @@ def swa_attn_key_weights(q, k, lse, window: int, scale: Optional[float] = None, 
     elif not _good(out, (B, Hkv, Lk), f32, index):
         _check(out, "out", (B, Hkv, Lk), f32, dev)
     window, causal = _int32(window), int(bool(causal))
+    name, reach = "swa_attn_key_weights", (window, causal)
+    if sinks:
+        name, reach = "swa_attn_key_weights_sinks", (window, _int32(sinks), causal)
     space = None, 0
     if workspace is not None:
         space = _space(workspace, dev)
     else:
-        need = _weights_space(index, B, Hq, Hkv, Lq, Lk, D, window, causal)
+        need = _weights_space(index, B, Hq, Hkv, Lq, Lk, D, *reach)
         if need:
             workspace = _t.empty(need, dtype=_t.u8, device=dev)
             space = workspace.data_ptr(), need
-    _run("swa_attn_key_weights", index, q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(), B,
-         Hq, Hkv, Lq, Lk, D, window, causal, 1.0 / math.sqrt(D) if scale is None else float(scale),
-         dt, *space)
+    _run(name, index, q.data_ptr(), k.data_ptr(), lse.data_ptr(), out.data_ptr(), B, Hq, Hkv, Lq, Lk, D,
+         *reach, 1.0 / math.sqrt(D) if scale is None else float(scale), dt, *space)
     return out

@@ -95,7 +95,7 @@ swa_status check_key_weights(int B, int Hq, int Hkv, int Lq, int Lk, int D, int 
 }
 
 swa::Problem key_weights_problem(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window,
-                                 int causal, float scale, int f16, unsigned* err) {
+                                 int sinks, int causal, float scale, int f16, unsigned* err) {
   swa::Problem pb;
   pb.B = B;
   pb.Hq = Hq;
@@ -110,6 +110,7 @@ swa::Problem key_weights_problem(int B, int Hq, int Hkv, int Lq, int Lk, int D, 
   pb.scale = scale;
   pb.err = err;
   pb.f16 = f16;
+  pb.sinks = W == Lk ? 0 : sinks < Lk ? sinks : Lk;
   return pb;
 }
 
@@ -251,20 +252,33 @@ swa_status swa_cache_evict(const swa_cache* cache, const int* table, int max_pag
 
 size_t swa_attn_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D,
                                             int window, int causal) {
-  if (check_key_weights(B, Hq, Hkv, Lq, Lk, D, window, causal, 1.f) != SWA_OK) return 0;
+  return swa_attn_key_weights_sinks_workspace_bytes(B, Hq, Hkv, Lq, Lk, D, window, 0, causal);
+}
+
+size_t swa_attn_key_weights_sinks_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D,
+                                                  int window, int sinks, int causal) {
+  if (sinks < 0 || check_key_weights(B, Hq, Hkv, Lq, Lk, D, window, causal, 1.f) != SWA_OK) return 0;
   return swa::key_weights_workspace_bytes(
-      key_weights_problem(B, Hq, Hkv, Lq, Lk, D, window, causal, 1.f, 0, nullptr));
+      key_weights_problem(B, Hq, Hkv, Lq, Lk, D, window, sinks, causal, 1.f, 0, nullptr));
 }
 
 swa_status swa_attn_key_weights(const void* q, const void* k, const float* lse, float* w, int B,
                                 int Hq, int Hkv, int Lq, int Lk, int D, int window, int causal,
                                 float scale, int dtype, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream) {
-  if (!q || !k || !lse || !w || (dtype != SWA_BF16 && dtype != SWA_FP16))
+  return swa_attn_key_weights_sinks(q, k, lse, w, B, Hq, Hkv, Lq, Lk, D, window, 0, causal, scale, dtype,
+                                    workspace, workspace_bytes, stream);
+}
+
+swa_status swa_attn_key_weights_sinks(const void* q, const void* k, const float* lse, float* w, int B,
+                                      int Hq, int Hkv, int Lq, int Lk, int D, int window, int sinks,
+                                      int causal, float scale, int dtype, void* workspace,
+                                      size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !k || !lse || !w || (dtype != SWA_BF16 && dtype != SWA_FP16) || sinks < 0)
     return SWA_ERR_INVALID_ARG;
   swa_status st = check_key_weights(B, Hq, Hkv, Lq, Lk, D, window, causal, scale);
   if (st != SWA_OK) return st;
-  swa::Problem pb = key_weights_problem(B, Hq, Hkv, Lq, Lk, D, window, causal, scale,
+  swa::Problem pb = key_weights_problem(B, Hq, Hkv, Lq, Lk, D, window, sinks, causal, scale,
                                         dtype == SWA_FP16, nullptr);
   const size_t need = swa::key_weights_workspace_bytes(pb);
   if (need != 0 && (!workspace || workspace_bytes < need)) return SWA_ERR_WORKSPACE;
