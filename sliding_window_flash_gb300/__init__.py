@@ -588,7 +588,12 @@ def _make_autograd():
 
     class SlidingWindowAttention(torch.autograd.Function):
         """o = attention(q, k, v) under a sliding window (causal unless causal=False), with the first
-        `sinks` keys visible to every query behind them; saves only (o, lse) for the backward."""
+        `sinks` keys visible to every query behind them; saves only (o, lse) for the backward.
+
+        A backward is captured into a CUDA graph only while no graph of the same leaves lives that was
+        made outside the capture: torch ties a leaf's gradient to the stream of the first graph that
+        needs it, and the captured stream must not meet that one.  Inside the capture it fails with
+        torch's error, or ends the process where the error comes up in a thread of autograd's."""
 
         @staticmethod
         def forward(ctx, q, k, v, window: int, scale: Optional[float] = None, causal: bool = True,

@@ -230,3 +230,25 @@ def test_autograd_and_given_buffers(swa):
         assert torch.equal(want[n], got[n]), n
     with pytest.raises(swa.SwaError, match="WORKSPACE"):
         step(swa, sh, x, workspace=guard[:need - 1])
+
+
+def test_autograd_captured(swa):
+    sh = Shape(1, 4, 2, 300, 300, 128, 64, 4)
+    x, y = inputs(sh, 1), inputs(sh, 2)
+    leaves = [x[n].clone().requires_grad_() for n in "qkv"]
+    eager = swa.SlidingWindowAttention.apply(*leaves, sh.W, None, True, sh.S)
+    eager.backward(x["do"])
+    del eager  # a graph made outside the capture must not live on
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = swa.SlidingWindowAttention.apply(*leaves, sh.W, None, True, sh.S)
+        grads = torch.autograd.grad(o, leaves, x["do"])
+    with torch.no_grad():
+        for t, n in zip(leaves, "qkv"):
+            t.copy_(y[n])
+    x["do"].copy_(y["do"])
+    graph.replay()
+    want = step(swa, sh, y)
+    assert torch.equal(o, want["o"])
+    for a, n in zip(grads, ("dq", "dk", "dv")):
+        assert torch.equal(a, want[n]), n
