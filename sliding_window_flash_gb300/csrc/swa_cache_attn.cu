@@ -359,30 +359,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int NS = C::kRing / teams;  // stages of a team's ring
   auto full = [&](int s) { return smem_u32(&bars[team * NS + s]); };
   auto empty = [&](int s) { return smem_u32(&bars[C::kStages + team * NS + s]); };
-  if (tid == 0) {
-    abort_flag = 0;
-    for (int i = 0; i < C::kRing; ++i) {
+  if (warp == kWarps - 1) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      abort_flag = 0;
+    }
+    for (int i = lane; i < C::kRing; i += 32) {
       mbar_init(smem_u32(&bars[i]), 1);
       mbar_init(smem_u32(&bars[C::kStages + i]), static_cast<uint32_t>(a.MT));
     }
     fence_barrier_init();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
   }
-  // Chunks before each sequence: four sequences a thread, an inclusive scan over the warps.
+  // Chunks before each sequence: a run of sequences a thread, an inclusive scan over the warps.  Loops stay
+  // rolled, here and below: what runs once takes its time by the instructions that have to be fetched.
   {
     int64_t* s_sum = reinterpret_cast<int64_t*>(smem + C::kOffSums);
-    int64_t own[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = 4 * tid + i;
+    const int each = c.B / kThreads + 1, b0 = min(tid * each, c.B + 1), b1 = min(b0 + each, c.B + 1);
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
       int n = 0, len = 0;
       if (b < c.B) {
         if (!sequence_of(c, b, &len, &n)) n = 0;
         s_len[b] = len;
         s_new[b] = n;
       }
-      own[i] = sum;
+      s_first[b] = sum;
       sum += ChunkWalk(len, n, a.reach, CK).count;
     }
     int64_t scan = sum;
@@ -394,11 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) s_sum[warp] = scan;
     __syncthreads();
     int64_t base = scan - sum;
+#pragma unroll 1
     for (int w = 0; w < warp; ++w) base += s_sum[w];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * tid + i <= c.B) s_first[4 * tid + i] = base + own[i];
-    if (tid == kThreads - 1 && c.B == 4 * kThreads) s_first[c.B] = base + sum;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) s_first[b] += base;
     __syncthreads();
     if (blockIdx.x == 0)
       for (int b = tid; b <= c.B; b += kThreads) a.first[b] = s_first[b];
