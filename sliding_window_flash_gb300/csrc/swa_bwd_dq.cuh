@@ -2,8 +2,9 @@
 // tile, and swa_bwd_dq_pair.cu, CTA pairs): per query tile, for each key block the window reaches,
 // P = exp(scale S - LSE) (window-masked) and dS = P (dP - Delta) go back over the dP columns as
 // packed pairs for dQ += dS K; each tile's dQ * scale is read out of TMEM and stored to global
-// memory straight from registers once the next tile's first S has been read ("Off NVIDIA, you fix
-// the platform yourself", Lab 28, "What did fixing it take?").
+// memory straight from registers once the next tile's first whole S has been read ("Off NVIDIA, you fix
+// the platform yourself", Lab 28, "What did fixing it take?").  With sinks a tile begins with its far blocks
+// (KeyWalk); a narrow one's 32 keys are 16 for each half of a row.
 #pragma once
 #include "swa_kernels.h"
 #include "swa_ptx.cuh"
@@ -210,7 +211,7 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
     if (!ok) break;
     g += f.nkv;
 
-    // The epilogue of this tile runs once the next tile's first S has been read (or after the
+    // The epilogue of this tile runs once the next tile's first whole S has been read (or after the
     // last tile): the MMA computes that tile's next scores while these stores drain.
     prev_it = it;
     prev_grow = grow;

@@ -27,6 +27,10 @@
 // S_g for the blocks g = b mod 3, then P_g over its first 64 columns (16-bit pairs: keys 2c and
 // 2c + 1 in column c) — and O at [384,512).  With three buffers and the deep K ring that half-tiles leave room
 // for, the S products run up to three blocks ahead of the P V products.
+//
+// With sinks (kSinks) a tile begins with its far blocks (KeyWalk), loaded through maps of their own; of a
+// narrow one 32 columns are exponentiated and two K-steps multiplied, and its maximum is the tile's first
+// reference.
 #include "swa_kernels.h"
 #include "swa_ptx.cuh"
 #include "swa_tmap.h"

@@ -62,8 +62,9 @@ struct Span {
 // every query of the tile), then the window's blocks.  Far blocks are loaded through tensor maps that
 // end behind the last sink, so what the other keys of a far block hold reads as zero.
 // A far block of kNarrowSinks sinks or fewer is narrow: the kernels for D <= 128 exponentiate and multiply its
-// first 32 keys only.  A few sinks are the usual case, and a whole block for them costs an eighth of the
-// call at a window of 1024.
+// first 32 keys only.  A few sinks are the usual case, and a window of 1024 has nine blocks.  (N 32,768,
+// D 128, 32 / 16 heads, W 1024, us without sinks / 4 / 4 as a whole block / 129: forward 481 / 502 / 545 / 622,
+// dQ 597 / 650 / 688 / 752.  At D = 256, whole blocks alone, N 8,191: forward 209 / - / 231 / 250.)
 constexpr int kNarrowSinks = 32;
 template <bool kSinks>
 struct KeyWalk {
@@ -112,7 +113,8 @@ struct Problem {
 // dK and dV of the sinks.  A sink is seen by every query behind it, where another key is seen by a
 // window of them, so the walk over the query tiles of a sinks' key block is cut into `splits` parts;
 // their fp32 sums are joined in order (launch_sink_join, behind dQ), which replaces the first `sinks` rows of dK and
-// dV.  The parts go first in the launch that walks the windows' key blocks.  A part is at most half of
+// dV.  (The same layer, dK/dV us: 806 without sinks, 903 with 4, 978 with 129; D = 256, N 8,191, dK and dV:
+// 493, 580, 582.)  The parts go first in the launch that walks the windows' key blocks.  A part is at most half of
 // an SM's share of that launch's tiles, so that the windows' walks fill up what the parts leave.
 // `width`: key blocks that a CTA (1) or a pair of them (2) takes.
 struct SinkPlan {
