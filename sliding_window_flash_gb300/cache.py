@@ -12,6 +12,10 @@ accumulated attention weight, and the weights that a prompt's keys received (inc
     lens += 1
     kept, lens = swa_cache_evict(cache, table, lens, spare, budget, recent)   # table = spare
 
+Where the model has sinks, the prompt's and the tokens' calls take the same ``sinks=``.  Where the tables
+of a batch begin with the same pages (a system prompt's), ``shared=`` says how many, and their slots are
+walked once for the batch; the rows behind are each sequence's own.
+
 ``table`` [B, max_pages] and ``lens`` [B] are int32 CUDA tensors that the kernels read on the
 device: nothing synchronises, and a captured step replays with their later contents.  Every call
 runs on the current stream of the cache's device; a page number or length out of range is skipped
