@@ -65,8 +65,11 @@ def _stale(target: str, deps) -> bool:
 
 
 def _torch_command(nvcc: str, out: str):
-    """The compiler's command for the binding's module: torch is found, not imported."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    """The compiler's command for the binding's module: torch is found, not imported.  None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
     lib = os.path.join(torch, "lib")
     include = [INCLUDE, os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
@@ -92,8 +95,9 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             cmd = [nvcc] + COMMON_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append((src, cmd))
     short = TORCH_PATH + ".tmp"
-    if force or _stale(TORCH_PATH, [TORCH_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
-        jobs.insert(0, (TORCH_SRC, _torch_command(nvcc, short)))
+    command = _torch_command(nvcc, short)
+    if command and (force or _stale(TORCH_PATH, [TORCH_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))):
+        jobs.insert(0, (TORCH_SRC, command))
 
     def run(job):
         src, cmd = job

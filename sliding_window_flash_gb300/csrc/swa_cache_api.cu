@@ -138,9 +138,9 @@ swa_status swa_cache_append(const swa_cache* cache, const int* table, int max_pa
 size_t swa_cache_attn_shared_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int max_pages,
                                              int page, int window, int sinks, int shared,
                                              int accumulate) {
-  if (sinks < 0 || shared < 0 || shared > max_pages || (shared > 0 && accumulate) || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > swa::kMaxCacheQueries ||
-      max_pages < 1 || window < 1 || (D != 64 && D != 128 && D != 256) ||
-      (page != 32 && page != 64 && page != 128) ||
+  if (sinks < 0 || shared < 0 || shared > max_pages || (shared > 0 && accumulate) || B < 1 || Hq < 1 ||
+      Hkv < 1 || Hq % Hkv != 0 || T < 1 || T > swa::kMaxCacheQueries || max_pages < 1 || window < 1 ||
+      (D != 64 && D != 128 && D != 256) || (page != 32 && page != 64 && page != 128) ||
       !sizes_fit(B, Hkv, max_pages, page) || !rows_fit(B, Hq, T) ||
       (shared > 0 && Hq / Hkv * T > kSharedRows))
     return 0;

@@ -115,10 +115,10 @@ struct Space {
   }
 };
 
-// The tensors, or the library's status where that is not SWA_OK.
+// What a call returns: made before it is launched, since a call that fails afterwards must not be taken for
+// one that has not been made.
 template <size_t N>
-PyObject* answer(int status, const Out (&outs)[N]) {
-  if (status != SWA_OK) return PyLong_FromLong(status);
+PyObject* pack(const Out (&outs)[N]) {
   PyObject* all = PyTuple_New(N);
   for (size_t i = 0; all && i < N; ++i) {
     PyObject* t = outs[i].give();
@@ -129,6 +129,12 @@ PyObject* answer(int status, const Out (&outs)[N]) {
     PyTuple_SET_ITEM(all, i, t);
   }
   return all;
+}
+// `all`, or the library's status where that is not SWA_OK.
+PyObject* answer(int status, PyObject* all) {
+  if (status == SWA_OK) return all;
+  Py_DECREF(all);
+  return PyLong_FromLong(status);
 }
 
 template <typename Body>
@@ -203,6 +209,8 @@ PyObject* cache_attn(PyObject*, PyObject* const* x, Py_ssize_t n) {
     void* op = outs[0].data();
     float* lp = static_cast<float*>(outs[1].data());
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(gpu).stream();
+    PyObject* all = pack(outs);
+    if (!all) return nullptr;
     int rc;
     Py_BEGIN_ALLOW_THREADS
     if (shared)
@@ -215,7 +223,7 @@ PyObject* cache_attn(PyObject*, PyObject* const* x, Py_ssize_t n) {
       rc = lib.attn(&c, tab, w, len, add, qp, op, lp, b, hq, t, window, scale, accumulate, kind, space.at,
                     space.bytes, stream);
     Py_END_ALLOW_THREADS
-    return answer(rc, outs);
+    return answer(rc, all);
   });
 }
 
@@ -272,12 +280,14 @@ PyObject* fwd(PyObject*, PyObject* const* x, Py_ssize_t n) {
     void* o = outs[0].data();
     float* lse = static_cast<float*>(outs[1].data());
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(y.gpu).stream();
+    PyObject* all = pack(outs);
+    if (!all) return nullptr;
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = lib.fwd(q, k, v, o, lse, y.B, y.Hq, y.Hkv, y.Lq, y.Lk, y.D, y.window, y.sinks, y.causal, y.scale,
                  y.kind, space.at, space.bytes, stream);
     Py_END_ALLOW_THREADS
-    return answer(rc, outs);
+    return answer(rc, all);
   });
 }
 
@@ -300,12 +310,14 @@ PyObject* bwd(PyObject*, PyObject* const* x, Py_ssize_t n) {
     const float* lp = static_cast<const float*>(lse->data_ptr());
     void *dq = outs[0].data(), *dk = outs[1].data(), *dv = outs[2].data();
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(y.gpu).stream();
+    PyObject* all = pack(outs);
+    if (!all) return nullptr;
     int rc;
     Py_BEGIN_ALLOW_THREADS
     rc = lib.bwd(q, k, v, op, gp, lp, dq, dk, dv, y.B, y.Hq, y.Hkv, y.Lq, y.Lk, y.D, y.window, y.sinks,
                  y.causal, y.scale, y.kind, space.at, space.bytes, stream);
     Py_END_ALLOW_THREADS
-    return answer(rc, outs);
+    return answer(rc, all);
   });
 }
 
