@@ -105,9 +105,9 @@ def _short_way():
             "swa_cache_attn", "swa_cache_attn_sinks", "swa_cache_attn_shared",
             "swa_cache_attn_shared_workspace_bytes", "swa_attn_fwd_sinks", "swa_attn_bwd_sinks",
             "swa_attn_sinks_workspace_bytes")])
-        return {"attn": m.cache_attn, "fwd": m.fwd, "bwd": m.bwd}
+        return {"pool": m.pool, "attn": m.cache_attn, "fwd": m.fwd, "bwd": m.bwd}
     except ImportError:
-        return dict.fromkeys(("attn", "fwd", "bwd"), lambda *_: None)
+        return dict.fromkeys(("pool", "attn", "fwd", "bwd"), lambda *_: None)
 
 
 def _raise(rc, name):
@@ -173,6 +173,10 @@ class SwaCache:
 
     def __init__(self, k, v, k_scale, v_scale, weight=None):
         t = _t
+        held = t.pool(k, v, k_scale, v_scale, weight)
+        if held is not None:
+            _put(self, "held", held)
+            return
         if not isinstance(k, t.Tensor) or k.dim() != 4:
             raise ValueError("k must be a 4-D tensor [pages, Hkv, page, D]")
         dev, shape = k.device, tuple(k.shape)

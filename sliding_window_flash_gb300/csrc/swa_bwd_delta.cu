@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(256) swa_delta_kernel(const uint16_t* __restri
                                                         float* __restrict__ delta,
                                                         long long rows, float* __restrict__ dq_acc,
                                                         long long acc_floats) {
+  wait_predecessor();
   launch_dependents();
   constexpr int kLanesPerRow = D / 8;
   constexpr int kRowsPerWarp = 32 / kLanesPerRow;
@@ -77,20 +78,13 @@ cudaError_t delta_impl(const Problem& pb, const void* o, const void* dO, float* 
   const dim3 grid(static_cast<unsigned>(blocks));
   const long long acc_floats =
       dq_acc != nullptr ? static_cast<long long>(dq_acc_bytes(pb.B, pb.Hq, pb.span.Lq, pb.D) / 4) : 0;
-  if (pb.D == 64 && !pb.f16)
-    swa_delta_kernel<64, false><<<grid, kThreads, 0, stream>>>(po, pd, delta, rows, dq_acc, acc_floats);
-  else if (pb.D == 64)
-    swa_delta_kernel<64, true><<<grid, kThreads, 0, stream>>>(po, pd, delta, rows, dq_acc, acc_floats);
-  else if (pb.D == 128 && !pb.f16)
-    swa_delta_kernel<128, false><<<grid, kThreads, 0, stream>>>(po, pd, delta, rows, dq_acc, acc_floats);
-  else if (pb.D == 128)
-    swa_delta_kernel<128, true><<<grid, kThreads, 0, stream>>>(po, pd, delta, rows, dq_acc, acc_floats);
-  else if (pb.D == 256 && !pb.f16 && dq_acc == nullptr)
-    swa_delta_kernel<256, false><<<grid, kThreads, 0, stream>>>(po, pd, delta, rows, nullptr, 0);
-  else if (pb.D == 256 && dq_acc == nullptr)
-    swa_delta_kernel<256, true><<<grid, kThreads, 0, stream>>>(po, pd, delta, rows, nullptr, 0);
-  else
-    return cudaErrorInvalidValue;
+  if (pb.D == 256 && dq_acc != nullptr) return cudaErrorInvalidValue;
+  auto kern = pb.D == 64    ? (pb.f16 ? swa_delta_kernel<64, true> : swa_delta_kernel<64, false>)
+              : pb.D == 128 ? (pb.f16 ? swa_delta_kernel<128, true> : swa_delta_kernel<128, false>)
+                            : (pb.f16 ? swa_delta_kernel<256, true> : swa_delta_kernel<256, false>);
+  if (pb.sinks > 0)
+    return launch_early(kern, grid.x, kThreads, 0, stream, po, pd, delta, rows, dq_acc, acc_floats);
+  kern<<<grid, kThreads, 0, stream>>>(po, pd, delta, rows, dq_acc, acc_floats);
   return cudaGetLastError();
 }
 

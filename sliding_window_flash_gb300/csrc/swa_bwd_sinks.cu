@@ -14,6 +14,7 @@ __global__ void __launch_bounds__(256)
     swa_sink_join_kernel(const float* part, uint16_t* dk, uint16_t* dv, int splits, int heads,
                          int sinks, int Lk, int D, float scale) {
   wait_predecessor();
+  launch_dependents();
   const long long quads = static_cast<long long>(heads) * 2 * sinks * (D / 4);
   const size_t step = sink_part_offset(1, heads, 0, 0, sinks, 0, D);
   for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < quads;

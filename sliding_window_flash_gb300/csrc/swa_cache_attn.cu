@@ -352,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = AttnCfg<D, kTiles>;
   constexpr int CK = C::CK;
   extern __shared__ __align__(1024) uint8_t smem[];
+  wait_predecessor();  // from here on whoever follows may take all inputs to be there
+  launch_dependents();
   if (!smem_base_ok(smem, c.err)) return;
   int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
   int* s_len = reinterpret_cast<int*>(smem + C::kOffLen);
@@ -360,7 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   int& abort_flag = *reinterpret_cast<int*>(bars + 2 * C::kStages);
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
-  launch_dependents();
   const int teams = kWarps / a.MT, team = warp / a.MT, wt = warp % a.MT;
   const int NS = C::kRing / teams;  // stages of a team's ring
   auto full = [&](int s) { return smem_u32(&bars[team * NS + s]); };
@@ -1029,6 +1030,7 @@ __global__ void __launch_bounds__(256) swa_cache_weights_kernel(const CacheView 
   constexpr int CK = C::CK, kLanes = CK / 4, kChunks = 32 / kLanes;  // lanes of a chunk; at a time
   __shared__ int64_t s_first[kMaxSeqs + 1];
   wait_predecessor();
+  launch_dependents();
   for (int b = static_cast<int>(threadIdx.x); b <= c.B; b += 256) s_first[b] = a.first[b];
   __syncthreads();
   const int lane = static_cast<int>(lane_id());
@@ -1240,9 +1242,9 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
     a.q = static_cast<const uint16_t*>(args.q) + row0 * D;
     a.o = static_cast<uint16_t*>(args.o) + row0 * D;
     a.lse = args.lse + row0;
-    swa_cache_attn_kernel<D, kTiles>
-        <<<p.parts / (kWarps / p.MT), kThreads, C::kSmemBytes, stream>>>(tk, tv, c, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_early(swa_cache_attn_kernel<D, kTiles>, static_cast<unsigned>(p.parts / (kWarps / p.MT)),
+                     kThreads, C::kSmemBytes, stream, tk, tv, c, a);
+    if (e != cudaSuccess) return e;
     if (args.base > 0) {
       pd.q = a.q;
       pd.rows = c.B * p.R;

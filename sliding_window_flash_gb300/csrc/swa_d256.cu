@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(384, 1)
   using C = F256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) wait_predecessor();  // the kernel may have been launched while the one ahead ends
   if (!smem_base_ok(smem, a.err)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kSinks) launch_dependents();  // with tensor memory in hand: who follows may want it too
 
   if (warp == 8 || warp == 11) {
     // ------------------------------------------------------------ K / V ring (even / odd items)
@@ -590,6 +592,9 @@ cudaError_t fwd256(const Problem& pb, const void* q, const void* k, const void* 
   if (e != cudaSuccess) return e;
   const Args256 a = make_args(pb, nullptr, nullptr, nullptr, lse);
   const int grid = a.ntiles < sm_count() ? a.ntiles : sm_count();
+  if (kSinks)
+    return launch_early(kern, static_cast<unsigned>(grid), F256::kThreads, F256::kSmemBytes, stream, tq, tk, tv,
+                        to, tks, tvs, a);
   kern<<<grid, F256::kThreads, F256::kSmemBytes, stream>>>(tq, tk, tv, to, tks, tvs, a);
   return cudaGetLastError();
 }

@@ -107,6 +107,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   using C = FwdP256;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) wait_predecessor();  // the kernel may have been launched while the one ahead ends
   // Both CTAs always reach the cluster barriers and the collective TMEM allocation; a misaligned
   // window only disables the work (and is reported).
   const bool smem_ok = (smem_u32(smem) & 1023u) == 0u;
@@ -157,6 +158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   cluster_sync_all();  // both CTAs' barriers are initialised before any cross-CTA arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kSinks) launch_dependents();  // with tensor memory in hand: who follows may want it too
 
   // This CTA's ring items in consumption order: on_item(index, is V, key block start, kv plane, block
   // of far sinks); on_tile(tile iteration) before each tile's first item.
@@ -359,6 +361,9 @@ cudaError_t launch_fwd256_pair_t(const Problem& pb, const void* q, const void* k
   const int clusters =
       max_pair_clusters<swa_fwd256_pair_kernel<F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
+  if (kSinks)
+    return launch_early(kern, 2u * static_cast<unsigned>(nclusters), C::kThreads, C::kSmemBytes, stream, tq,
+                        tk64, tv128, to, tk64s, tv128s, a);
   kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tk64, tv128, to, tk64s,
                                                               tv128s, a);
   return cudaGetLastError();

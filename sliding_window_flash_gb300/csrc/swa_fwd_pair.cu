@@ -127,6 +127,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   using C = FwdPairCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
+  if constexpr (kSinks) wait_predecessor();  // the kernel may have been launched while the one ahead ends
   // Both CTAs of the pair always reach the cluster barriers and the collective TMEM allocation;
   // a misaligned window only disables the work (and is reported).
   const bool smem_ok = (smem_u32(smem) & 1023u) == 0u;
@@ -178,6 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   cluster_sync_all();  // both CTAs' barriers are initialised before any cross-CTA arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kSinks) launch_dependents();  // with tensor memory in hand: who follows may want it too
 
   // The pair's MMA schedule, run by rank 0's MMA warp (issuing) and rank 1's relay warp
   // (forwarding its copies, in the same order): S for up to kSBufs key blocks ahead of P V over the
@@ -644,6 +646,9 @@ cudaError_t launch_fwd_pair_d(const Problem& pb, const void* q, const void* k, c
   const int clusters =
       max_pair_clusters<swa_fwd_pair_kernel<D, F16, kSinks>>(C::kThreads, C::kSmemBytes);
   const int nclusters = a.ntiles < clusters ? a.ntiles : clusters;
+  if (kSinks)
+    return launch_early(kern, 2u * static_cast<unsigned>(nclusters), C::kThreads, C::kSmemBytes, stream, tq,
+                        tk, tv, to, tks, tvs, a);
   kern<<<2 * nclusters, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, tks, tvs, a);
   return cudaGetLastError();
 }

@@ -1,5 +1,5 @@
-// swa_torch.cpp — the binding's short way to the library: swa_cache_attn, and swa_attn_fwd and
-// swa_attn_bwd with sinks, for arguments as they should be.
+// swa_torch.cpp — the binding's short way to the library: SwaCache and swa_cache_attn, and swa_attn_fwd
+// and swa_attn_bwd with sinks, for arguments as they should be.
 //
 // A step of one token is a few microseconds of GPU work, less than Python takes to look at a call's
 // tensors.  This module looks at them, allocates what the call returns and its workspace from torch's
@@ -145,6 +145,31 @@ PyObject* guarded(Body body) {
   }
   PyErr_Clear();
   Py_RETURN_NONE;
+}
+
+// k, v, k_scale, v_scale, weight: SwaCache.held, the tensors with their device and k's shape.
+PyObject* pool(PyObject*, PyObject* const* x, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 5) return nullptr;
+    const at::Tensor* k = tensor(x[0]);
+    if (!k || k->dim() != 4) return nullptr;
+    const at::IntArrayRef shape = k->sizes();
+    const int gpu = static_cast<int>(k->get_device());
+    if (!good(k, shape, at::kFloat8_e4m3fn, gpu) || !good(tensor(x[1]), shape, at::kFloat8_e4m3fn, gpu) ||
+        !good(tensor(x[2]), shape.slice(0, 2), at::kFloat, gpu) ||
+        !good(tensor(x[3]), shape.slice(0, 2), at::kFloat, gpu) ||
+        (x[4] != Py_None && !good(tensor(x[4]), shape.slice(0, 3), at::kFloat, gpu)))
+      return nullptr;
+    PyObject* device = PyObject_GetAttrString(x[0], "device");
+    PyObject* sizes = device ? Py_BuildValue("(LLLL)", static_cast<long long>(shape[0]),
+                                             static_cast<long long>(shape[1]), static_cast<long long>(shape[2]),
+                                             static_cast<long long>(shape[3]))
+                             : nullptr;
+    PyObject* held = sizes ? PyTuple_Pack(7, x[0], x[1], x[2], x[3], x[4], device, sizes) : nullptr;
+    Py_XDECREF(device);
+    Py_XDECREF(sizes);
+    return held;
+  });
 }
 
 // held (SwaCache.held), q, table, lens, new, out, lse, workspace, window, scale, accumulate, sinks, shared
@@ -358,6 +383,7 @@ PyCFunction fast() {
 
 PyMethodDef methods[] = {
     {"use", fast<use>(), METH_FASTCALL, nullptr},
+    {"pool", fast<pool>(), METH_FASTCALL, nullptr},
     {"cache_attn", fast<ready<cache_attn>>(), METH_FASTCALL, nullptr},
     {"fwd", fast<ready<fwd>>(), METH_FASTCALL, nullptr},
     {"bwd", fast<ready<bwd>>(), METH_FASTCALL, nullptr},

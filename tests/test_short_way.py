@@ -37,6 +37,7 @@ def test_it_is_built_and_leaves_what_is_no_cuda_tensor():
     assert mod._t.bwd(*[x] * 5, None, None, None, None, None, 4, None, True, 1) is None
     held = (x, x, x, x, None, x.device, (1, 1, 1, 64))
     assert mod._t.attn(held, x, x, x, None, None, None, None, 4, None, False, 0, 0) is None
+    assert mod._t.pool(x, x, x, x, None) is None and mod._t.pool(None) is None
     for bad in ((), (1,), (held,) * 13, (None,) * 13, (None,) * 10, (None,) * 14):
         for n in NONE:
             assert getattr(mod._t, n)(*bad) is None
@@ -95,7 +96,8 @@ def test_cache(swa, way, kw):
     name, answered = way
     kw = dict(kw)
     cache, table, lens, q = pool(weight=kw.get("accumulate", False))
-    table[1, :2] = table[0, :2]
+    if "shared" in kw:  # (never with accumulate: two sequences would add to the same weights)
+        table[1, :2] = table[0, :2]
     given = kw.pop("given", False)
     if kw.pop("new", False):
         kw["new"] = torch.tensor([3, 1], device="cuda", dtype=torch.int32)
@@ -185,3 +187,27 @@ def test_on_a_side_stream_and_captured(swa):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("weight", [False, True])
+def test_pools(swa, weight, monkeypatch):
+    a = swa.SwaCache.empty(3, 2, 64, 32, weight=weight)
+    assert mod._t.pool(*a.held[:5]) == a.held
+    monkeypatch.setitem(mod._t.__dict__, "pool", lambda *_: None)
+    b = swa.SwaCache(*a.held[:5])
+    assert [type(x) for x in a.held] == [type(x) for x in b.held]
+    assert all(x is y for x, y in zip(a.held[:5], b.held[:5])) and a.held[5:] == b.held[5:]
+    assert (a.page, a.shape, a.device) == (32, (3, 2, 32, 64), a.k.device) == (b.page, b.shape, b.device)
+
+
+@pytest.mark.gpu
+def test_pools_that_are_refused(swa):
+    k, v, ks, vs, w = swa.SwaCache.empty(3, 2, 64, 32).held[:5]
+    for args, error in (((k, v[:2], ks, vs), ValueError), ((k, v.view(torch.uint8), ks, vs), TypeError),
+                        ((k, v, ks.double(), vs), TypeError), ((k, v, ks, vs[:, :1]), ValueError),
+                        ((k, v, ks, vs, w[:, :, :16]), ValueError), ((k, v.cpu(), ks, vs), ValueError),
+                        ((k[0], v, ks, vs), ValueError), ((k.mT, v.mT, ks, vs), ValueError),
+                        ((k, v, None, vs), TypeError)):
+        with pytest.raises(error):
+            swa.SwaCache(*args)
