@@ -31,9 +31,9 @@
 // one sequence with 16 heads, the latency of two kernels; 18.6 us for 16 sequences with 8 heads.  12
 // sequences, 5 tokens, D = 256, window 1024: 31 us; a part is only ten chunks there, and its partial
 // results, written and read, add 40 % to the cache's bytes.  With sinks: 64 ragged sequences, 4 tokens, 32 /
-// 8 heads, window 4096, 68 sinks, accumulating: 155 us, the walk 104 of it (5.4 TB/s with the scores that it
-// writes), the join 9, the weights 39, of 16 rows a slot; 12 sequences, D = 256, window 1024, 4 sinks: 35 us,
-// 7 of them before the first chunk is there, 7 the join.
+// 8 heads, window 4096, 68 sinks, accumulating: 151 us, the walk 104 of it (5.4 TB/s with the scores that it
+// writes), the join 9, the weights 39, of 16 rows a slot; 12 sequences, D = 256, window 1024, 4 sinks: 32.5 us,
+// 6 of them before the first chunk is there, 7 the join.
 #include <climits>
 #include <type_traits>
 
@@ -568,43 +568,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     st.any_hi = len + n - 1;
     st.all_lo = visible_lo(len + n - 1, a.reach.window);
     st.all_hi = n < c.T ? -1 : len;  // a row without a query sees nothing
+    float up[2 * kTiles];
 #pragma unroll
     for (int ye = 0; ye < 2 * kTiles; ++ye) {
       const int y = ye >> 1, e = ye & 1;
-      // The row as fp16, its largest element brought to [2^14, 2^15) (a row below 2^-112 less far).
-      uint32_t top = 0;
+      // The row as fp16, its largest element brought to [2^14, 2^15) (a row below 2^-112 less far).  The
+      // largest magnitude is that of the bits, two elements a word.
+      uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[ye][i].x) : Elem<false>::unpack(raw[ye][i].x);
-        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[ye][i].y) : Elem<false>::unpack(raw[ye][i].y);
-        top = max(max(top, __float_as_uint(fabsf(y0.x))), __float_as_uint(fabsf(y0.y)));
-        top = max(max(top, __float_as_uint(fabsf(y1.x))), __float_as_uint(fabsf(y1.y)));
-      }
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      for (int i = 0; i < kSteps; ++i)
+        most = __vmaxu2(most, __vmaxu2(raw[ye][i].x & 0x7fff7fffu, raw[ye][i].y & 0x7fff7fffu));
+      most = max(most & 0xffffu, most >> 16);
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const uint32_t top =
+          __float_as_uint(a.f16 ? Elem<true>::unpack(most).x : Elem<false>::unpack(most).x);
       const int ex = static_cast<int>(top >> 23);
       // 2^(14 - exponent); 1 for zero, infinity and NaN
       const int sh = ex == 255 || top == 0 ? 0 : min(126, 127 + 14 - ex);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+      up[ye] = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
       // Scores of an infinite query are infinite, and exp(x - lse) of them NaN: all NaN from here on, since
       // a row whose scores were all -inf would look like one that sees nothing.
       st.tile[y].f[e] = ex == 255 ? __uint_as_float(0x7fffffffu)
                                   : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+    }
+    auto scaled = [&](uint32_t w, float by) {
+      const float2 v = a.f16 ? Elem<true>::unpack(w) : Elem<false>::unpack(w);
+      return pack_f16(v.x * by, v.y * by);
+    };
+    if constexpr (C::kQShared) {
+      // Into shared memory as they are, and scaled there by a loop: what runs once takes as long as its
+      // instructions take to be fetched.
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const float2 y0 = a.f16 ? Elem<true>::unpack(raw[ye][i].x) : Elem<false>::unpack(raw[ye][i].x);
-        const float2 y1 = a.f16 ? Elem<true>::unpack(raw[ye][i].y) : Elem<false>::unpack(raw[ye][i].y);
-        const uint32_t p0 = pack_f16(y0.x * up, y0.y * up);
-        const uint32_t p1 = pack_f16(y1.x * up, y1.y * up);
-        if constexpr (C::kQShared) {
-          const uint32_t to = sq + ((y * kSteps + i) * 32 + lane) * 16 + 4 * e;
-          st_shared_b32(to, p0);
-          st_shared_b32(to + 8, p1);
-        } else {
-          qf[y * kSteps + i][e] = p0;
-          qf[y * kSteps + i][2 + e] = p1;
+      for (int y = 0; y < kTiles; ++y) {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+          st_shared_v4(sq + ((y * kSteps + i) * 32 + lane) * 16, raw[2 * y][i].x, raw[2 * y + 1][i].x,
+                       raw[2 * y][i].y, raw[2 * y + 1][i].y);
+#pragma unroll 1
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t at = sq + ((y * kSteps + i) * 32 + lane) * 16;
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(at)
+                       : "memory");
+          st_shared_v4(at, scaled(w[0], up[2 * y]), scaled(w[1], up[2 * y + 1]), scaled(w[2], up[2 * y]),
+                       scaled(w[3], up[2 * y + 1]));
         }
       }
+    } else {
+#pragma unroll
+      for (int y = 0; y < kTiles; ++y)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            qf[y * kSteps + i][e] = scaled(raw[2 * y + e][i].x, up[2 * y + e]);
+            qf[y * kSteps + i][2 + e] = scaled(raw[2 * y + e][i].y, up[2 * y + e]);
+          }
     }
     st.vref = 1.f;
 #pragma unroll
