@@ -1272,9 +1272,10 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
       pd.rows = c.B * p.R;
       pd.tiles = (pd.rows + kPrefixRows - 1) / kPrefixRows;
       if ((e = launch_cache_prefix(c, pd, stream)) != cudaSuccess) return e;
-      // A warp a row (at D = 256 half of one) where that fills the SMs, else a warp 16 columns of a row.
+      // A warp 64 columns of a row where that fills the SMs, else 16.  (12 sequences, 5 tokens, 32 / 16 heads,
+      // D = 256, the call: 74.1 us, with 128 columns 76.5, 32 76.8; 64 sequences, 32 / 8, D = 128: 83.3, 83.5, 84.9.)
       const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv * p.R, limit = 8ll * sm_count();
-      constexpr int kWide = D < 128 ? D : 128;
+      constexpr int kWide = 64;
       const bool wide = rows * (D / kWide) >= 4ll * sm_count();
       const int64_t need = (rows * (D / (wide ? kWide : 16)) + 7) / 8;
       auto join = wide ? swa_cache_join_shared_kernel<D, kWide> : swa_cache_join_shared_kernel<D, 16>;
