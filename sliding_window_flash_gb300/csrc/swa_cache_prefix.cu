@@ -26,8 +26,10 @@
 // of instructions to fetch and waits one behind the other.  64 sequences, 32 / 8 heads, D = 128, a prefix of
 // 32,768: 50 us alone (34 GFLOP, 67 MB); 12 sequences, 5 tokens, 32 / 16 heads, D = 256, a prefix of 4,096: 31.
 // It begins while the walk over the sequences' own slots ends, and the join while it ends: 83 and 74 us in
-// all.  Tried: operands fetched register by register while they are converted (90 us), more than 16 warps
-// (96 registers each, which spill), masks in the passes instead of in TMEM (spilled).
+// all.  The first item's rows come while its chunks are looked up (the smallest calls 14.9 us in place of 15.9,
+// large ones the same).  Tried: operands fetched register by register while they are converted (90 us), more
+// than 16 warps (96 registers each, which spill), masks in the passes instead of in TMEM (spilled), the next
+// chunk's first scores read while the warp judges this one's (a few spills; 87 us).
 #include <climits>
 #include <type_traits>
 
@@ -249,13 +251,25 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
 
   ChunkRec* s_rec = reinterpret_cast<ChunkRec*>(smem + C::kOffRec);
   unsigned* s_max = reinterpret_cast<unsigned*>(smem + C::kOffMax);
-  // Looks up the part's chunks from i0 on, a thread a group of 32 keys.  Every thread of the CTA comes here
-  // for every block, whatever became of its work on the one before.
+  // Looks up the part's chunks from i0 on, a thread a group of 32 keys.  The first block is for the warps
+  // behind the softmax's, which load their first rows meanwhile and meet them at barrier 2.  Every thread of
+  // the CTA comes here for every further block, whatever became of its work on the one before.
+  constexpr int kFirstThread = 32 * C::kSoftmaxWarps;
   auto look_up = [&](int i0) {
-    __syncthreads();  // the block before has been read
-    for (int i = static_cast<int>(threadIdx.x); i < C::kBlock; i += C::kThreads) s_max[i] = 0u;
-    __syncthreads();
-    for (int at = static_cast<int>(threadIdx.x); at < 4 * C::kBlock; at += C::kThreads) {  // whole warps
+    const bool all = i0 > 0;
+    const int tid = static_cast<int>(threadIdx.x) - (all ? 0 : kFirstThread);
+    const int threads = C::kThreads - (all ? 0 : kFirstThread);
+    auto meet = [&] {
+      if (all)
+        __syncthreads();
+      else
+        named_barrier_sync(1, C::kThreads - kFirstThread);
+    };
+    if (all) __syncthreads();  // the block before has been read
+    for (int i = tid; i < C::kBlock; i += threads) s_max[i] = 0u;
+    meet();
+    const int end = min(4 * C::kBlock, (4 * (count - i0) + 31) & ~31);
+    for (int at = tid; at < end; at += threads) {  // whole warps
       const int rec = at / 4, group = at & 3, i = i0 + rec;
       int plane = -1;
       if (i < count) {
@@ -295,7 +309,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
                    to.slot + KT > a.reach.sinks);
       }
     }
-    __syncthreads();
+    meet();
   };
   // The value reference: the largest scale of the item's chunks so far, a block of chunks at a time; it moves
   // where an item or a block begins.
@@ -304,6 +318,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     return starts ? (top > 0.f ? top : 1.f) : fmaxf(vref, top);
   };
 
+  if (warp >= C::kSoftmaxWarps) {
+    look_up(0);
+    named_barrier_arrive(2, C::kThreads);
+  }
   if (warp >= C::kKeyWarp && warp < C::kMmaWarp) {
     // ------------------------------------------------------------------ codes to operands
     // A thread has the codes of the next chunk on their way while it converts this one's.
@@ -396,7 +414,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       };
       bool ok = true;
       for (int i0 = 0; i0 < count; i0 += C::kBlock) {
-        look_up(i0);
+        if (i0 > 0) look_up(i0);
         const int n = min(C::kBlock, count - i0);
         uint4 even[kPasses];
         if (ok) {
@@ -449,7 +467,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     bool ok = true;
     int item = -1, seg = -1, ahead = 0;  // chunks whose S has been issued
     for (int i0 = 0; i0 < count; i0 += C::kBlock) {
-      look_up(i0);
+      if (i0 > 0) look_up(i0);
       const int end = min(count, i0 + C::kBlock);
       for (int g = i0; ok && g < end; ++g) {
         const int it = s_rec[g - i0].item;
@@ -493,6 +511,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     auto start = [&](int j, int head) {
       uint32_t top[2] = {0u, 0u};
       uint32_t place[2];
+      uint4 raw[2][D / 32];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = r0 + 8 * e, rho = j * kPrefixRows + r;
@@ -512,16 +531,18 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         if (kq == 0) s_seen[r] = seen;
         // units kq and kq + 4 of every 64 columns
         place[e] = sQ + sw128_offset(static_cast<uint32_t>(r), static_cast<uint32_t>(kq));
-        uint4 raw[D / 32];
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          raw[i] = is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
+          raw[e][i] = is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          top[e] = __vmaxu2(top[e], __vmaxu2(__vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu),
-                                             __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu)));
-          st_shared_v4((place[e] ^ (64u * (i & 1))) + (i >> 1) * C::kQChunk, raw[i].x, raw[i].y, raw[i].z,
-                       raw[i].w);
+          const uint4 y = raw[e][i];
+          top[e] = __vmaxu2(top[e], __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu),
+                                             __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
+          st_shared_v4((place[e] ^ (64u * (i & 1))) + (i >> 1) * C::kQChunk, y.x, y.y, y.z, y.w);
         }
       }
       float up[2];
@@ -602,14 +623,23 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     };
 
     int last_slot = 0;
+    if (count > 0) {  // the part's first item, known without the look-up
+      const int j = sequence_at(s_first, a.tiles, c.Hkv, begin);
+      const int64_t nc = s_first[j + 1] - s_first[j], rem = begin - s_first[j] * c.Hkv;
+      const int head = static_cast<int>(quotient(rem, nc));
+      item = j * c.Hkv + head;
+      begins = rem == head * nc;
+      start(j, head);
+    }
+    named_barrier_sync(2, C::kThreads);
     for (int i0 = 0; i0 < count; i0 += C::kBlock) {
-      look_up(i0);
+      if (i0 > 0) look_up(i0);
       for (int g = i0; ok && g < min(count, i0 + C::kBlock); ++g) {
         const ChunkRec& rec = s_rec[g - i0];
         const int slot = rec.slot;
-        const bool starts = rec.item != item;
-        if (starts) {
-          if (item >= 0 && !(ok = finish(g - 1, last_slot))) break;
+        const bool starts = rec.item != item || g == 0;
+        if (rec.item != item) {
+          if (!(ok = finish(g - 1, last_slot))) break;
           item = rec.item;
           const int j = static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)));
           begins = slot == TileWalk(s_range[j], a.reach, KT).at(0) * KT;
@@ -763,7 +793,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         warp_arrive(bar(C::kPFull + (g & 1)));
       }
     }
-    if (ok && item >= 0) finish(count - 1, last_slot);
+    if (ok && count > 0) finish(count - 1, last_slot);
   }
 
   tc_fence_before();
