@@ -956,7 +956,7 @@ __global__ void __launch_bounds__(256)
   const int per = c.Hkv * a.NRT;
   const int64_t total = a.first[c.B] * per, ptotal = p.first[p.tiles] * c.Hkv;
   const Parts cut(total, used_parts(total, a.parts, a.rows * D));
-  const Parts pcut(ptotal, used_parts(ptotal, p.parts, p.stored * D));
+  const Parts pcut(ptotal, prefix_parts(ptotal, p.parts, p.stored, D));
   const int64_t tasks = static_cast<int64_t>(c.B) * c.Hkv * a.R * kRuns;
   for (int64_t task = blockIdx.x * 8 + warp_id(); task < tasks; task += gridDim.x * 8) {
     const int run = static_cast<int>(task % kRuns);
