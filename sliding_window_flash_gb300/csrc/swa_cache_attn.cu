@@ -944,12 +944,12 @@ __global__ void __launch_bounds__(256) swa_cache_join_few_kernel(const CacheView
 
 // With a shared prefix: joins what the parts of the prefix's items and the parts of a sequence's own slots
 // left for a row.  A warp for kCols columns of a row: a lane looks up a partial's place, then groups of
-// kCols / 4 lanes take the partials in turn.
+// lanes, 4 or 8 columns each, take the partials in turn.
 template <int D, int kCols>
 __global__ void __launch_bounds__(256)
     swa_cache_join_shared_kernel(const CacheView c, const AttnDev a, const PrefixDev p) {
   constexpr uint32_t kRuns = D / kCols;
-  constexpr int kSub = kCols / 4, kGroups = 32 / kSub;
+  constexpr int kVec = kCols < 64 ? 4 : 8, kSub = kCols / kVec, kGroups = 32 / kSub;
   wait_predecessor();
   launch_dependents();
   const int lane = static_cast<int>(lane_id()), group = lane / kSub, sub = lane % kSub;
@@ -964,7 +964,7 @@ __global__ void __launch_bounds__(256)
                    b = p.div_hkv.div(bh);
     const int r = static_cast<int>(row - bh * p.div_r.d), h = static_cast<int>(bh - b * p.div_hkv.d);
     float top = SWA_NEG_INF, l = 0.f;
-    float o[4] = {};
+    float o[kVec] = {};
     int len, n;
     if (sequence_of(c, static_cast<int>(b), &len, &n) &&
         static_cast<int>(a.div_t.mod(static_cast<uint32_t>(r))) < n) {
@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(256)
           const float down = ex2(top - most);
           l *= down;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] *= down;
+          for (int i = 0; i < kVec; ++i) o[i] *= down;
           top = most;
         }
         const float w = y == nullptr ? 0.f : ex2(s.x - (top == SWA_NEG_INF ? 0.f : top));
@@ -1018,12 +1018,15 @@ __global__ void __launch_bounds__(256)
           const float wk = __shfl_sync(0xffffffffu, w, from & 31);
           const float lk = __shfl_sync(0xffffffffu, lw, from & 31);
           if (from < n && src != nullptr) {
-            const float4 v = *reinterpret_cast<const float4*>(src + run * kCols + sub * 4);
+            float v[kVec];
+#pragma unroll
+            for (int x = 0; x < kVec; x += 4) {
+              const float4 y4 = *reinterpret_cast<const float4*>(src + run * kCols + sub * kVec + x);
+              v[x] = y4.x, v[x + 1] = y4.y, v[x + 2] = y4.z, v[x + 3] = y4.w;
+            }
             l += lk;
-            o[0] += wk * v.x;
-            o[1] += wk * v.y;
-            o[2] += wk * v.z;
-            o[3] += wk * v.w;
+#pragma unroll
+            for (int x = 0; x < kVec; ++x) o[x] += wk * v[x];
           }
         }
         __syncwarp();
@@ -1032,12 +1035,12 @@ __global__ void __launch_bounds__(256)
       for (int d = kSub; d < 32; d <<= 1) {
         l += __shfl_xor_sync(0xffffffffu, l, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], d);
+        for (int i = 0; i < kVec; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], d);
       }
     }
     if (group == 0) {
-      store_row<4>(a, a.o + static_cast<size_t>(row) * D + run * kCols + sub * 4, o,
-                   l == 0.f ? 0.f : 1.f / l);
+      store_row<kVec>(a, a.o + static_cast<size_t>(row) * D + run * kCols + sub * kVec, o,
+                      l == 0.f ? 0.f : 1.f / l);
       if (lane == 0 && run == 0) a.lse[row] = l == 0.f ? SWA_NEG_INF : (top + log2f(l)) * kLn2;
     }
   }
