@@ -32,8 +32,8 @@
 // sequences, 5 tokens, D = 256, window 1024: 31 us; a part is only ten chunks there, and its partial
 // results, written and read, add 40 % to the cache's bytes.  With sinks: 64 ragged sequences, 4 tokens, 32 /
 // 8 heads, window 4096, 68 sinks, accumulating: 151 us, the walk 104 of it (5.4 TB/s with the scores that it
-// writes), the join 9, the weights 39, of 16 rows a slot; 12 sequences, D = 256, window 1024, 4 sinks: 32.5 us,
-// 6 of them before the first chunk is there, 7 the join.
+// writes), the join 9, the weights 39, of 16 rows a slot; 12 sequences, D = 256, window 1024, 4 sinks: 31.4 us,
+// 6 of them before the first chunk is there, 6 the join.
 #include <climits>
 #include <type_traits>
 
@@ -841,21 +841,33 @@ __global__ void __launch_bounds__(256) swa_cache_join_part_kernel(const CacheVie
       auto partial = [&](int p) {
         return static_cast<size_t>(partial_slot(p, cut.start(p) <= ip.x0)) * a.rows + r;
       };
+      // The first partial of each group is on its way while the maximum is found.
+      const bool any = ip.p0 + group <= ip.p1;
+      float2 ml0 = make_float2(0.f, 0.f);
+      float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (any) {
+        const size_t pr = partial(ip.p0 + group);
+        ml0 = *reinterpret_cast<const float2*>(a.ml + pr * 2);
+        y0 = *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4);
+      }
       for (int p = ip.p0 + lane; p <= ip.p1; p += 32) top = fmaxf(top, a.ml[partial(p) * 2]);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float base = top == SWA_NEG_INF ? 0.f : top;
-#pragma unroll 4
-      for (int p = ip.p0 + group; p <= ip.p1; p += 8) {
-        const size_t pr = partial(p);
-        const float2 ml = *reinterpret_cast<const float2*>(a.ml + pr * 2);
-        const float4 y = *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4);
+      auto add = [&](float2 ml, float4 y) {
         const float w = ex2(ml.x - base);
         l += w * ml.y;
         o[0] += w * y.x;
         o[1] += w * y.y;
         o[2] += w * y.z;
         o[3] += w * y.w;
+      };
+      if (any) add(ml0, y0);
+#pragma unroll 4
+      for (int p = ip.p0 + group + 8; p <= ip.p1; p += 8) {
+        const size_t pr = partial(p);
+        add(*reinterpret_cast<const float2*>(a.ml + pr * 2),
+            *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4));
       }
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
@@ -899,6 +911,15 @@ __global__ void __launch_bounds__(256) swa_cache_join_few_kernel(const CacheView
       auto partial = [&](int p) {
         return static_cast<size_t>(partial_slot(p, cut.start(p) <= ip.x0)) * a.rows + r;
       };
+      // The first partial of each group is on its way while the maximum is found.
+      const bool any = ip.p0 + group <= ip.p1;
+      float2 ml0 = make_float2(0.f, 0.f);
+      float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (any) {
+        const size_t pr = partial(ip.p0 + group);
+        ml0 = *reinterpret_cast<const float2*>(a.ml + pr * 2);
+        y0 = *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4);
+      }
       for (int p = ip.p0 + tid; p <= ip.p1; p += 256) top = fmaxf(top, a.ml[partial(p) * 2]);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -907,23 +928,27 @@ __global__ void __launch_bounds__(256) swa_cache_join_few_kernel(const CacheView
 #pragma unroll
       for (int w = 0; w < 8; ++w) top = fmaxf(top, s_red[w]);
       const float base = top == SWA_NEG_INF ? 0.f : top;
-#pragma unroll 4
-      for (int p = ip.p0 + group; p <= ip.p1; p += kGroups) {
-        const size_t pr = partial(p);
-        const float2 ml = *reinterpret_cast<const float2*>(a.ml + pr * 2);
-        const float4 y = *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4);
+      auto add = [&](float2 ml, float4 y) {
         const float w = ex2(ml.x - base);
         l += w * ml.y;
         o[0] += w * y.x;
         o[1] += w * y.y;
         o[2] += w * y.z;
         o[3] += w * y.w;
+      };
+      if (any) add(ml0, y0);
+#pragma unroll 4
+      for (int p = ip.p0 + group + kGroups; p <= ip.p1; p += kGroups) {
+        const size_t pr = partial(p);
+        add(*reinterpret_cast<const float2*>(a.ml + pr * 2),
+            *reinterpret_cast<const float4*>(a.po + pr * D + run * 16 + sub * 4));
       }
       if (sub == 0) s_l[group] = l;
       s_o[tid] = make_float4(o[0], o[1], o[2], o[3]);
       __syncthreads();
       if (group == 0) {
         l = o[0] = o[1] = o[2] = o[3] = 0.f;
+#pragma unroll 8
         for (int i = 0; i < kGroups; ++i) {
           l += s_l[i];
           const float4 y = s_o[i * 4 + sub];

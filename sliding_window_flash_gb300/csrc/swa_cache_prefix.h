@@ -35,7 +35,7 @@ struct PrefixPlan {
 // Keys of a chunk: the tensor core's operands and two stages of them fill shared memory.
 SWA_HD int prefix_chunk(int D) { return D == 256 ? 64 : 128; }
 // Parts that the list is cut into: by used_parts' rule, whose partial results cost half here, since they are
-// still in the L2 when they are read (12 sequences, 5 tokens, D = 256, a prefix of 4,096: 71 us, 73 by the rule as
+// still in the L2 when they are read (12 sequences, 5 tokens, D = 256, a prefix of 4,096: 2 us of 73 less than by the rule as
 // it is, which leaves a quarter of the SMs without a part).
 SWA_HD int prefix_parts(int64_t total, int parts, int stored, int D) {
   return used_parts(total, parts, stored * D / 2);
