@@ -156,3 +156,23 @@ def test_inputs_of_another_stream(swa, captured):
     torch.cuda.synchronize()
     for a, b in zip(wants, got):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("sizes", [D64, D128, D256], ids=["d64", "d128", "d256"])
+def test_two_streams_at_once(swa, sizes):
+    """Layers on one stream and serving steps on another, at the same time and time and again."""
+    makes = (training, serving)
+    wants = [[t.clone() for t in make(swa, sizes, torch.cuda.synchronize)()] for make in makes]
+    streams = [torch.cuda.Stream() for _ in makes]
+    torch.cuda.synchronize()
+    gots = [[], []]
+    for _ in range(6):
+        for make, stream, got in zip(makes, streams, gots):
+            with torch.cuda.stream(stream):
+                got.append(make(swa, sizes, lambda: None)())
+    torch.cuda.synchronize()
+    swa.swa_check_device()
+    for want, runs in zip(wants, gots):
+        for got in runs:
+            for i, (a, b) in enumerate(zip(want, got)):
+                assert torch.equal(a, b), i
