@@ -125,7 +125,7 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
       tmem_ld16(dp_col, rr);
       tmem_wait_ld_all();
       reg_fence(rr);
-      const int sk = a.sinks - 16 * static_cast<int>(h);
+      const int sk = a.sinks - f.k0(0) - 16 * static_cast<int>(h);
       auto ds = [&](int i) {
         const float e = ex2(fmaf(__uint_as_float(rs[i]), sl2, -lse2));
         return i < sk ? e * (__uint_as_float(rr[i]) - dlt) : 0.f;

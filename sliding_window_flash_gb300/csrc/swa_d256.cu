@@ -265,16 +265,21 @@ __global__ void __launch_bounds__(384, 1)
       umma_commit_w(bar(C::kSFull + (gg & 1)));
       return true;
     };
-    // O[:, 128 hf ..] (+)= P_gg V_hf, P_gg packed over S buffer gg & 1 (two 32-column halves).
-    auto issue_pv = [&](int gg, bool first) -> bool {
+    // O[:, 128 hf ..] (+)= P_gg V_hf, P_gg packed over S buffer gg & 1 (two 32-column halves, of a narrow
+    // block two K-steps 16 columns apart).
+    auto issue_pv = [&](int gg, bool first, bool narrow) -> bool {
       const int pb = gg & 1;
       if (!warp_wait(bar(C::kPFull + pb), (gg >> 1) & 1, &abort_flag, a.err)) return false;
       for (int hf = 0; hf < 2; ++hf, ++i) {
         if (!warp_wait(rg.full(i), rg.parity(i), &abort_flag, a.err)) return false;
         tc_fence_after();
-        umma_ts_mnmajor_x8_split(tmem + C::kColO + 128u * hf, tmem + C::kColS + 128u * pb,
-                                 smem_desc_sw128(rg.slot(i), kChunk, 1024), kIdO,
-                                 first ? 0u : 1u);
+        const uint64_t v_desc = smem_desc_sw128(rg.slot(i), kChunk, 1024);
+        if (narrow)
+          umma_ts_mnmajor_x2(tmem + C::kColO + 128u * hf, tmem + C::kColS + 128u * pb, 16u, v_desc, kIdO,
+                             first ? 0u : 1u);
+        else
+          umma_ts_mnmajor_x8_split(tmem + C::kColO + 128u * hf, tmem + C::kColS + 128u * pb, v_desc, kIdO,
+                                   first ? 0u : 1u);
         umma_commit_w(rg.empty(i));
       }
       umma_commit_w(bar(C::kPVDone + pb));
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(384, 1)
         // The first P V of a tile overwrites O: the previous tile's epilogue must have read it.
         if (ok && j == 0 && it > 0)
           ok = warp_wait(bar(C::kOEmpty), (it - 1) & 1, &abort_flag, a.err);
-        if (ok) ok = issue_pv(g + j, j == 0);
+        if (ok) ok = issue_pv(g + j, j == 0, f.is_narrow(j));
       }
       g += f.nkv;
     }
@@ -489,14 +494,19 @@ __global__ void __launch_bounds__(384, 1)
       if (tile_last) umma_commit_w(bar(C::kQDEmpty));  // every S and dP of the tile is issued
       return true;
     };
-    auto issue_dq = [&](int gg, bool first, bool tile_last) -> bool {  // dQ += dS K_gg
+    // dQ += dS K_gg (a narrow block's dS: two K-steps 16 columns apart)
+    auto issue_dq = [&](int gg, bool first, bool tile_last, bool narrow) -> bool {
       if (!warp_wait(bar(C::kDSFull), gg & 1, &abort_flag, a.err)) return false;
       for (int hf = 0; hf < 2; ++hf, ++i) {
         if (!warp_wait(rg.full(i), rg.parity(i), &abort_flag, a.err)) return false;
         tc_fence_after();
-        umma_ts_mnmajor_x8_split(tmem + C::kColDQ + 128u * hf, tmem + C::kColDP,
-                                 smem_desc_sw128(rg.slot(i), kChunk, 1024), kIdDq,
-                                 first ? 0u : 1u);
+        const uint64_t k_desc = smem_desc_sw128(rg.slot(i), kChunk, 1024);
+        if (narrow)
+          umma_ts_mnmajor_x2(tmem + C::kColDQ + 128u * hf, tmem + C::kColDP, 16u, k_desc, kIdDq,
+                             first ? 0u : 1u);
+        else
+          umma_ts_mnmajor_x8_split(tmem + C::kColDQ + 128u * hf, tmem + C::kColDP, k_desc, kIdDq,
+                                   first ? 0u : 1u);
         umma_commit_w(rg.empty(i));
       }
       if (tile_last) umma_commit_w(bar(C::kDQDone));
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(384, 1)
         // have read it.
         if (ok && j == 0 && it > 0)
           ok = warp_wait(bar(C::kDQEmpty), (it - 1) & 1, &abort_flag, a.err);
-        if (ok) ok = issue_dq(g + j, j == 0, j + 1 == n);
+        if (ok) ok = issue_dq(g + j, j == 0, j + 1 == n, f.is_narrow(j));
         if (ok && j + 1 < n) ok = issue_dp(j + 2 == n);
       }
       g += n;

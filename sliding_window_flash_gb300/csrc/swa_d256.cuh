@@ -214,7 +214,41 @@ __device__ __forceinline__ void fwd_softmax(const FwdSoftmax& cx, const Span& sp
     const int row = q0 + r;
     float m_ref = SWA_NEG_INF;  // reference max (log2 domain) that P and l are taken against
     float l = 0.f;              // partial row sum over this thread's half of the columns
-    for (int j = 0; j < f.nkv; ++j) {
+    int j = 0;
+    if (f.is_narrow(0)) {
+      // A few sinks, seen by every row that is computed; of the 32 columns each half takes 16.  As the
+      // tile's first block they set the reference.
+      const int sb = g & 1;
+      if (!(ok = warp_wait(bar(FwdBar::kSFull + sb), (g >> 1) & 1, cx.abort_flag, cx.err))) break;
+      tc_fence_after();
+      const uint32_t s_col = cx.tmem + lane_base + 128u * sb + 16u * h;
+      uint32_t rr[16], pk[8];
+      tmem_ld16(s_col, rr);
+      tmem_wait_ld_all();
+      reg_fence(rr);
+      const int sk = cx.sinks - f.k0(0) - 16 * static_cast<int>(h);
+      float y[16], mx = SWA_NEG_INF;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        y[i] = i < sk ? __uint_as_float(rr[i]) : SWA_NEG_INF;
+        mx = fmaxf(mx, y[i]);
+      }
+      float other;
+      if (!(ok = exchange(mx * sl2, &other))) break;
+      m_ref = fmaxf(mx * sl2, other);
+      const float m = m_ref == SWA_NEG_INF ? 0.f : m_ref;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e0 = ex2(fmaf(y[2 * i], sl2, -m)), e1 = ex2(fmaf(y[2 * i + 1], sl2, -m));
+        l += e0 + e1;
+        pk[i] = Elem<F16>::pack(e0, e1);
+      }
+      tmem_st8(s_col, pk);
+      tmem_wait_st();
+      arrive(bar(FwdBar::kPFull + sb));
+      j = 1;
+    }
+    for (; j < f.nkv; ++j) {
       const int gg = g + j;
       const int k0 = f.k0(j);
       const int sb = gg & 1;
@@ -413,7 +447,34 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
     const float lse2 = nxt_lse == SWA_POS_INF ? SWA_POS_INF : nxt_lse * kLog2e;
     const float dlt = nxt_dlt;
     fetch_rows(t + tile_step);
-    for (int j = 0; j < f.nkv; ++j) {
+    int j = 0;
+    if (f.is_narrow(0)) {  // of its 32 columns each half takes 16
+      if (!(ok = warp_wait(bar(DqBar::kSFull), g & 1, abort_flag, a.err))) break;
+      tc_fence_after();
+      uint32_t rs[16], rr[16], pk[8];
+      tmem_ld16(tmem + lane_base + 16u * h, rs);
+      tmem_wait_ld_all();
+      reg_fence(rs);
+      arrive(bar(DqBar::kSEmpty));
+      const uint32_t dcol = tmem + lane_base + 128u + 16u * h;
+      if (!(ok = warp_wait(bar(DqBar::kDPFull), g & 1, abort_flag, a.err))) break;
+      tc_fence_after();
+      tmem_ld16(dcol, rr);
+      tmem_wait_ld_all();
+      reg_fence(rr);
+      const int sk = a.sinks - f.k0(0) - 16 * static_cast<int>(h);
+      auto ds = [&](int i) {
+        const float e = ex2(fmaf(__uint_as_float(rs[i]), sl2, -lse2));
+        return i < sk ? e * (__uint_as_float(rr[i]) - dlt) : 0.f;
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pk[i] = Elem<F16>::pack(ds(2 * i), ds(2 * i + 1));
+      tmem_st8(dcol, pk);
+      tmem_wait_st();
+      arrive(bar(DqBar::kDSFull));
+      j = 1;
+    }
+    for (; j < f.nkv; ++j) {
       const int gg = g + j;
       const int k0 = f.k0(j);
       if (!(ok = warp_wait(bar(DqBar::kSFull), gg & 1, abort_flag, a.err))) break;

@@ -271,13 +271,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       return true;
     };
     // dQ += dS K_gg: dS over the dP columns (keys 16 ks .. 16 ks + 15 at packed column
-    // 8 ks + 32 (ks / 4)), B = this CTA's 128 head dims of K (two 128 x 64 chunks, MN-major).
-    auto issue_dq = [&](int gg, bool first, bool tile_last) -> bool {
+    // 8 ks + 32 (ks / 4), of a narrow block at 16 ks), B = this CTA's 128 head dims of K (two 128 x 64 chunks, MN-major).
+    auto issue_dq = [&](int gg, bool first, bool tile_last, bool narrow) -> bool {
       if (!warp_wait_cluster(bar(C::kDSFull), gg & 1, &abort_flag, a.err)) return false;
       if (!warp_wait_cluster(full(i), parity(i), &abort_flag, a.err)) return false;
       tc_fence_after();
-      umma2_ts_mnmajor_x8_split(tmem + C::kColDQ, tmem + C::kColDP,
-                                smem_desc_sw128(slot(i), C::kChunk, 1024), kIdQ, first ? 0u : 1u);
+      const uint64_t k_desc = smem_desc_sw128(slot(i), C::kChunk, 1024);
+      if (narrow)
+        umma2_ts_mnmajor_x2(tmem + C::kColDQ, tmem + C::kColDP, 16u, k_desc, kIdQ, first ? 0u : 1u);
+      else
+        umma2_ts_mnmajor_x8_split(tmem + C::kColDQ, tmem + C::kColDP, k_desc, kIdQ, first ? 0u : 1u);
       umma2_commit_w(empty(i));
       ++i;
       if (tile_last) umma2_commit_w(bar(C::kDQDone));
@@ -296,7 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         // The first dQ of a tile overwrites the accumulator: both epilogues must have read it.
         if (ok && j == 0 && it > 0)
           ok = warp_wait_cluster(bar(C::kDQEmpty), (it - 1) & 1, &abort_flag, a.err);
-        if (ok) ok = issue_dq(g + j, j == 0, j + 1 == n);
+        if (ok) ok = issue_dq(g + j, j == 0, j + 1 == n, f.is_narrow(j));
         if (ok && j + 1 < n) ok = issue_dp(j + 2 == n);
       }
       g += n;

@@ -262,14 +262,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       return true;
     };
     // O (+)= P_gg V_gg: P packed over S buffer gg & 1 (keys 16 ks .. 16 ks + 15 at packed column
-    // 8 ks + 32 (ks / 4)), B = this CTA's 128 head dims of V (two 128 x 64 chunks, MN-major).
-    auto issue_pv = [&](int gg, bool first) -> bool {
+    // 8 ks + 32 (ks / 4), of a narrow block at 16 ks), B = this CTA's 128 head dims of V (two 128 x 64 chunks, MN-major).
+    auto issue_pv = [&](int gg, bool first, bool narrow) -> bool {
       const int pb = gg & 1;
       if (!warp_wait_cluster(bar(C::kPFull + pb), (gg >> 1) & 1, &abort_flag, a.err)) return false;
       if (!warp_wait_cluster(full(i), parity(i), &abort_flag, a.err)) return false;
       tc_fence_after();
-      umma2_ts_mnmajor_x8_split(tmem + C::kColO, tmem + C::kColS + 128u * pb,
-                                smem_desc_sw128(slot(i), C::kChunk, 1024), kIdO, first ? 0u : 1u);
+      const uint64_t v_desc = smem_desc_sw128(slot(i), C::kChunk, 1024);
+      if (narrow)
+        umma2_ts_mnmajor_x2(tmem + C::kColO, tmem + C::kColS + 128u * pb, 16u, v_desc, kIdO,
+                            first ? 0u : 1u);
+      else
+        umma2_ts_mnmajor_x8_split(tmem + C::kColO, tmem + C::kColS + 128u * pb, v_desc, kIdO,
+                                  first ? 0u : 1u);
       umma2_commit_w(empty(i));
       ++i;
       umma2_commit_w(bar(C::kPVDone + pb));
@@ -286,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         // The first P V of a tile overwrites O: both CTAs' epilogues must have read it.
         if (ok && j == 0 && it > 0)
           ok = warp_wait_cluster(bar(C::kOEmpty), (it - 1) & 1, &abort_flag, a.err);
-        if (ok) ok = issue_pv(g + j, j == 0);
+        if (ok) ok = issue_pv(g + j, j == 0, f.is_narrow(j));
       }
       g += f.nkv;
     }

@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld16(tmem + lane_base + C::kColS + 128u * sb + 16u * h, rr);
         tmem_wait_ld_all();
         reg_fence(rr);
-        const int sk = a.sinks - 16 * static_cast<int>(h);
+        const int sk = a.sinks - f.k0(0) - 16 * static_cast<int>(h);
         float y[16], mx = SWA_NEG_INF;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {

@@ -403,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         float y[16], a0 = SWA_NEG_INF, a1 = SWA_NEG_INF;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const bool vis = 8 * (i >> 2) + (i & 1) + 2 * kq < a.sinks;
+          const bool vis = 8 * (i >> 2) + (i & 1) + 2 * kq < a.sinks - f.k0(0);
           y[i] = vis ? __uint_as_float(rr[i]) : SWA_NEG_INF;
           if (i & 2)
             a1 = fmaxf(a1, y[i]);

@@ -61,16 +61,17 @@ struct Span {
 // sequence's first `sinks` keys that lie before the window's (its far sinks, all of them visible to
 // every query of the tile), then the window's blocks.  Far blocks are loaded through tensor maps that
 // end behind the last sink, so what the other keys of a far block hold reads as zero.
-// A far block of kNarrowSinks sinks or fewer is narrow: the kernels for D <= 128 exponentiate and multiply its
-// first 32 keys only.  A few sinks are the usual case, and a window of 1024 has nine blocks.  (N 32,768,
-// D 128, 32 / 16 heads, W 1024, us without sinks / 4 / 4 as a whole block / 129: forward 481 / 502 / 545 / 622,
-// dQ 597 / 650 / 688 / 752.  At D = 256, whole blocks alone, N 8,191: forward 209 / - / 231 / 250.)
+// The last far block is narrow where kNarrowSinks sinks or fewer reach into it: it comes first, and the kernels
+// exponentiate and multiply its first 32 keys only.  A few sinks are the usual case, and a window of 1024 has
+// nine blocks.  (W 1024, 32 / 16 heads, us without sinks / 4 / 4 as a whole block / 129 / 129 as two.  N 32,768,
+// D 128: forward 481 / 502 / 545 / 591 / 622, dQ 597 / 650 / 688 / 722 / 752; N 8,191, D 256: forward 209 / 221 /
+// 231 / 248 / 249, dQ 278 / 291 / 297 / 317 / 318.)
 constexpr int kNarrowSinks = 32;
 template <bool kSinks>
 struct KeyWalk {
   int kb_lo, nkv;  // first block of the window; blocks in all
   int far;         // far blocks
-  bool narrow;     // the only far block has kNarrowSinks sinks or fewer
+  bool narrow;     // the last far block has kNarrowSinks sinks or fewer, and comes first
   __host__ __device__ void set(const Span& sp, int sinks, int q0) {
     kb_lo = sp.first_kblock(q0);
     far = 0;
@@ -78,13 +79,16 @@ struct KeyWalk {
     if constexpr (kSinks) {
       far = (sinks + kBlockN - 1) / kBlockN;
       if (far > kb_lo) far = kb_lo;
-      narrow = far == 1 && sinks <= kNarrowSinks;
+      narrow = far > 0 && far * kBlockN >= sinks && sinks - (far - 1) * kBlockN <= kNarrowSinks;
     }
     nkv = sp.last_kblock(q0) - kb_lo + 1 + far;
   }
   // First key of block j, and whether it is a far one.
   __host__ __device__ int k0(int j) const {
-    if constexpr (kSinks) return (j < far ? j : kb_lo + j - far) * kBlockN;
+    if constexpr (kSinks) {
+      if (narrow && j < far) j = j == 0 ? far - 1 : j - 1;
+      return (j < far ? j : kb_lo + j - far) * kBlockN;
+    }
     return (kb_lo + j) * kBlockN;
   }
   __host__ __device__ bool is_far(int j) const { return kSinks && j < far; }

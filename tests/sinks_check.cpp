@@ -22,7 +22,7 @@ int main() {
   using swa::kBlockN;
   long long cases = 0;
   const int lks[] = {1, 2, 127, 128, 129, 257, 700}, lqs[] = {1, 130, 1000}, ws[] = {1, 7, 128, 129, 300};
-  const int counts[] = {1, 5, 127, 128, 129, 256, 300, 700};
+  const int counts[] = {1, 5, 32, 33, 127, 128, 129, 160, 161, 256, 300, 700};
   for (int Lk : lks)
     for (int lq : lqs)
       for (int W : ws)
@@ -42,8 +42,12 @@ int main() {
               std::vector<int> times((Lk + kBlockN - 1) / kBlockN);
               for (int j = 0, last = -1; j < walk.nkv; ++j) {
                 const int k0 = walk.k0(j);
-                if (k0 % kBlockN != 0 || k0 <= last || k0 >= Lk) return fail("order", sp, sinks, q0, j);
-                last = k0;
+                if (k0 % kBlockN != 0 || (k0 <= last && !walk.is_narrow(j - 1)) || k0 >= Lk)
+                  return fail("order", sp, sinks, q0, j);
+                // a narrow block is the last of the far ones, and holds the last sink
+                if (walk.is_narrow(j) && (j != 0 || !walk.is_far(0) || sinks <= k0 || sinks > k0 + swa::kNarrowSinks))
+                  return fail("narrow", sp, sinks, q0, j);
+                last = walk.is_narrow(j) ? -1 : k0;
                 ++times[k0 / kBlockN];
                 for (int i = q0; i < q0 + kBlockM && i < Lq; ++i) {
                   const int rel = i + sp.off - k0, lo = rel - sp.dmax;

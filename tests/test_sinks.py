@@ -63,6 +63,10 @@ SHAPES = [
     *[Shape(1, Hq, 1, 300, 800, D, 150, S, dtype=t)
       for S, t in ((16, BF16), (17, BF16), (31, FP16), (32, BF16), (33, FP16))
       for Hq, D in ((1, 64), (1, 128), (2, 128), (2, 256))],
+    # the last of several far blocks narrow, or not, with tiles that see the first of them far alone
+    *[Shape(1, Hq, 1, 700, 700, D, 130, S, dtype=t)
+      for S, t in ((129, BF16), (160, FP16), (161, BF16), (270, FP16))
+      for Hq, D in ((1, 64), (1, 128), (2, 128), (1, 256), (2, 256))],
 ]
 
 
