@@ -78,8 +78,7 @@ def test_long_prefix(swa):
 
 @pytest.mark.parametrize("D,page", [(128, 32), (64, 128), (256, 64)])
 def test_value_scales_far_apart(swa, D, page):
-    """The documented error: 2^-25 of the largest scale among the slots of one product (64 or 128), beside the
-    usual one."""
+    """The documented error: 2^-25 of the largest scale among the shared slots, beside the usual one."""
     B, shared = 3, 8 * 128 // page
     cache, table, g = setup(swa, 6, B, 1, D, page, shared, shared + 1)
     e = torch.randint(-30, 20, (cache.k.shape[0], 1), generator=g, device="cuda").float()
