@@ -133,12 +133,14 @@ swa_status swa_cache_attn_sinks(const swa_cache* cache, const int* table, int ma
  * table are the same pages (0 <= shared <= max_pages), and their slots are walked once for the rows of all
  * sequences, by the first table's entries, instead of once for each.  Lengths count from slot 0 as ever; the
  * result is that of swa_cache_attn_sinks up to rounding, for any lengths, sequences shorter than the shared
- * pages among them.
+ * pages among them.  Shared entries and pages that no sequence sees (before every window, between the sinks
+ * and the windows, behind the last token, between one sequence's last token and the others' windows) are not
+ * read.
  *   accumulate : has to be 0 with shared > 0 (the weights of shared pages would be added to by all
  *                sequences at once); (Hq / Hkv) T <= 65536 then.
  *   workspace  : at least swa_cache_attn_shared_workspace_bytes bytes, on the terms of swa_cache_attn's.
- * Values are taken relative to the largest value scale among the shared pages of their kv head (in as far
- * as a part of the walk meets them): exactly while their own scale is at least 2^-15 of it, and below that
+ * Values are taken relative to the largest value scale among the shared pages of their kv head that some
+ * sequence sees (in as far as a part of the walk meets them): exactly while their own scale is at least 2^-15 of it, and below that
  * with an absolute error of 2^-25 of it.
  * Scores, statistics and sums are fp32, p is rounded to fp16 as in swa_cache_attn.  The same call on one GPU
  * gives the same bits.

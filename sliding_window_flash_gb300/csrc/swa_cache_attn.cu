@@ -49,6 +49,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSeqs = 1024;  // sequences per launch; more run as several launches
+static_assert(kMaxSeqs <= kPrefixSeqs, "what the prefix's walk holds of each");
 
 // kTiles: tiles of 16 query rows of a warp.
 template <int D, int kTiles = 1>

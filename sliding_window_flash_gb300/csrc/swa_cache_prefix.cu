@@ -13,7 +13,9 @@
 //     only when a chunk's sum calls for it.
 //   * Where 128 chunks lie, their pages and their scales, is looked up by all threads at once and kept in
 //     shared memory, which leaves the loops few registers to hold: what spills would miss the little L1
-//     that operands of 200 KB leave.
+//     that operands of 200 KB leave.  A chunk has slots of up to four pages, and a tile rows of sequences of
+//     different lengths, so of each 32 slots it is known which some row's sequence sees: of others neither
+//     table entry nor scale is read, and their values count as zero.
 // q is taken as fp16 after scaling each row by a power of two, as in swa_cache_attn.cu.  Keys carry their
 // block's scale into the scores' factor; values are scaled by theirs relative to the largest of the item's
 // chunks, exactly while a scale is at least 2^-15 of it (a code is a multiple of 2^-9, an fp16 value of 2^-24).
@@ -58,9 +60,10 @@ struct PrefixCfg {
   static constexpr int kOffFirst = kOffV + kVStages * kKVBytes;
   static constexpr int kOffRange = kOffFirst + (kPrefixTiles + 2) * 8;
   static constexpr int kOffRec = kOffRange + kPrefixTiles * 16;  // what is known about kBlock chunks
-  static constexpr int kOffMax = kOffRec + kBlock * 64;          // largest value scales of their items
+  static constexpr int kOffMax = kOffRec + kBlock * 80;          // largest value scales of their items
   static constexpr int kOffSeen = kOffMax + kBlock * 4;          // the slots that each row sees
-  static constexpr int kOffBar = kOffSeen + kPrefixRows * 8;
+  static constexpr int kOffSeq = kOffSeen + kPrefixRows * 8;  // and each sequence
+  static constexpr int kOffBar = kOffSeq + kPrefixSeqs * 8;
   static constexpr int kQFull = 0;
   static constexpr int kKFull = 1;
   static constexpr int kKEmpty = kKFull + kKStages;
@@ -139,14 +142,26 @@ struct TileWalk {
 };
 
 // What is known about a chunk: its item and first slot, the index in its block of its item's first chunk
-// there, and for each group of 32 keys the plane (page * Hkv + head, or -1: nothing to be seen) and scales.
+// there, and for each group of 32 keys the plane (page * Hkv + head, or -1: nothing to be seen), scales, and
+// which of the keys the sequences of the tile's rows see.
 struct ChunkRec {
   int item, slot, origin;
   int edge;  // some row of the tile does not see some of it
   int plane[4];
   float ks[4], vs[4];
+  unsigned seen[4];
 };
-static_assert(sizeof(ChunkRec) == 64, "kOffRec");
+static_assert(sizeof(ChunkRec) == 80, "kOffRec");
+
+// Those of the 32 slots from `slot` on that lie in [lo, end), as bits.
+__device__ __forceinline__ unsigned slot_bits(int slot, int lo, int end) {
+  const int a = max(lo - slot, 0), z = min(end - slot, 32);
+  return a < z ? (0xffffffffu << a) & (0xffffffffu >> (32 - z)) : 0u;
+}
+// Those that a sequence sees whose queries begin to see at `lo` and end at `end`.
+__device__ __forceinline__ unsigned seen_bits(int slot, int lo, int end, int sinks) {
+  return slot_bits(slot, lo, end) | slot_bits(slot, 0, min(sinks, end));
+}
 
 __device__ __forceinline__ uint4 load_codes(const uint4* p) {  // read once: not for the L1
   uint4 v;
@@ -169,6 +184,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   }
   int64_t* s_first = reinterpret_cast<int64_t*>(smem + C::kOffFirst);
   TileRange* s_range = reinterpret_cast<TileRange*>(smem + C::kOffRange);
+  int2* s_seq = reinterpret_cast<int2*>(smem + C::kOffSeq);  // first slot seen (sinks aside), and the end
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   int& abort_flag = *reinterpret_cast<int*>(tmem_slot + 1);
@@ -204,7 +220,10 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     int len_min = INT_MAX, end_max = 0, q_max = 0, end_min = INT_MAX;
     for (int b = b0 + static_cast<int>(lane); b <= b1; b += 32) {
       int len, n;
-      if (!sequence_of(c, b, &len, &n) || n == 0) continue;
+      const bool asks = sequence_of(c, b, &len, &n) && n > 0;
+      // (a sequence of two tiles gets the same from both)
+      s_seq[b] = asks ? make_int2(visible_lo(len, a.reach.window), min(len + n, a.reach.base)) : make_int2(0, 0);
+      if (!asks) continue;
       len_min = min(len_min, len);
       end_max = max(end_max, len + n);
       q_max = max(q_max, len + n - 1);
@@ -251,6 +270,21 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
 
   ChunkRec* s_rec = reinterpret_cast<ChunkRec*>(smem + C::kOffRec);
   unsigned* s_max = reinterpret_cast<unsigned*>(smem + C::kOffMax);
+  // Which of 32 slots some sequence of tile j's rows sees.  The one whose end is the last sees all of them
+  // nearly always; where it does not (an edge, a sink, or slots between two sequences' windows), all are asked.
+  auto group_seen = [&](int j, int slot) -> unsigned {
+    const TileRange r = s_range[j];
+    const int end = min(r.end_max, a.reach.base);
+    if (slot >= end) return 0u;
+    if (slot + 32 <= end && slot >= visible_lo(r.len_max_q, a.reach.window)) return 0xffffffffu;
+    const int b0 = static_cast<int>(a.div_r.div(static_cast<uint32_t>(j) * kPrefixRows));
+    const int last = min(a.rows, (j + 1) * kPrefixRows) - 1;
+    const int b1 = static_cast<int>(a.div_r.div(static_cast<uint32_t>(last)));
+    unsigned bits = 0u;
+#pragma unroll 1
+    for (int b = b0; b <= b1; ++b) bits |= seen_bits(slot, s_seq[b].x, s_seq[b].y, a.reach.sinks);
+    return bits;
+  };
   // Looks up the part's chunks from i0 on, a thread a group of 32 keys.  The first block is for the warps
   // behind the softmax's, which load their first rows meanwhile and meet them at barrier 2.  Every thread of
   // the CTA comes here for every further block, whatever became of its work on the one before.
@@ -280,7 +314,8 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         const int slot0 = TileWalk(s_range[j], a.reach, KT).at(cc) * KT, slot = slot0 + 32 * group;
         const int origin = max(rec - cc, 0);
         float ks = 1.f, vs = 0.f;
-        if (group < C::kGroups && slot < a.reach.base) {
+        const unsigned seen = group < C::kGroups && slot < a.reach.base ? group_seen(j, slot) : 0u;
+        if (seen != 0u) {
           const int page = page_of(c, a.table, 0, slot >> a.page_log2, c.max_pages);
           if (page >= 0) {
             plane = page * c.Hkv + h;
@@ -293,6 +328,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         to.plane[group] = plane;
         to.ks[group] = ks;
         to.vs[group] = vs;
+        to.seen[group] = seen;
         if (group == 0) {
           to.item = j * c.Hkv + h;
           to.slot = slot0;
@@ -312,10 +348,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     meet();
   };
   // The value reference: the largest scale of the item's chunks so far, a block of chunks at a time; it moves
-  // where an item or a block begins.
+  // where an item or a block begins.  Where a part's first block has nothing to be seen it is the least scale.
+  constexpr float kLeastScale = 1.f / (1ll << -kScaleMinExp);
   auto reference = [&](const ChunkRec& rec, float vref, bool starts) {
     const float top = __uint_as_float(s_max[rec.origin]);
-    return starts ? (top > 0.f ? top : 1.f) : fmaxf(vref, top);
+    return fmaxf(starts ? kLeastScale : vref, top);
   };
 
   if (warp >= C::kSoftmaxWarps) {
@@ -328,7 +365,6 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     int item = -1, stage = 0;
     uint32_t phase = 1;  // the first round of stages is free
     float vref = 1.f;
-    int lo = 0, end = 0;  // slots that some row of the tile sees
     auto walk = [&](auto kind) {
       constexpr bool kValues = decltype(kind)::value;
       const uint8_t* pool = kValues ? c.v : c.k;
@@ -377,22 +413,16 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         item = rec.item;
         uint32_t ratio[C::kGroups] = {};
         if constexpr (kValues) {
-          if (starts || i == 0) {
-            vref = reference(rec, vref, starts);
-            const TileRange range = s_range[static_cast<int>(a.div_hkv.div(static_cast<uint32_t>(item)))];
-            lo = visible_lo(range.len_min, a.reach.window);
-            end = min(range.end_max, a.reach.base);
-          }
+          if (starts || i == 0) vref = reference(rec, vref, starts);
           const float inv = 1.f / vref;
 #pragma unroll
           for (int o = 0; o < C::kGroups; ++o) ratio[o] = half2_of(rec.vs[o] * inv);
           // what nobody sees must not meet a probability of zero as infinity or NaN
-          if (rec.slot + KT > end || (rec.slot < lo && rec.slot + KT > a.reach.sinks)) {
+          if (rec.edge) {
   #pragma unroll
-            for (int p = 0; p < kPasses; ++p) {
-              const int s = rec.slot + row0 + p * kRowsPass;
-              if (s >= end || (s < lo && s >= a.reach.sinks)) codes[p] = make_uint4(0u, 0u, 0u, 0u);
-            }
+            for (int p = 0; p < kPasses; ++p)
+              if ((rec.seen[p * kRowsPass / 32] >> (row0 + p * kRowsPass % 32) & 1u) == 0u)
+                codes[p] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         constexpr int kStages = kValues ? C::kVStages : C::kKStages;

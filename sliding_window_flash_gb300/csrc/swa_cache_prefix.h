@@ -9,6 +9,7 @@ namespace swa {
 
 constexpr int kPrefixRows = 128;    // query rows of a tile
 constexpr int kPrefixTiles = 512;   // tiles of rows per launch
+constexpr int kPrefixSeqs = 1024;   // and sequences
 
 // The rows that share a kv head are those of all sequences, R = G T each, one after another, in tiles of
 // kPrefixRows.  A tile and a kv head are an item; the prefix slots that any row of the tile sees are cut
