@@ -5,7 +5,8 @@ _swa_torch.so, the binding's short way to it (csrc/swa_torch.cpp, with torch's h
 
 Objects go to sliding_window_flash_gb300/_build/, the library to sliding_window_flash_gb300/libswa.so.
 nvcc and the CUDA toolkit are needed, for the second a C++ compiler and torch (no GPU): the build runs
-the same on x86_64 and aarch64.
+the same on x86_64 and aarch64.  The library does without the second: where it does not compile, the compiler's
+output goes to stderr, an older one is removed, and the binding takes the Python way.
 """
 from __future__ import annotations
 
@@ -80,6 +81,18 @@ def _torch_command(nvcc: str, out: str):
             "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
+def _put_module(made: str, r) -> None:
+    """The binding's module in its place; where the compiler failed, none, and why on stderr."""
+    if r.returncode == 0:
+        os.replace(made, TORCH_PATH)
+        return
+    for path in (made, TORCH_PATH):
+        if os.path.exists(path):
+            os.remove(path)
+    sys.stderr.write(f"no {os.path.basename(TORCH_PATH)} (calls take some microseconds more on the host): the "
+                     f"compiler failed for {TORCH_SRC}:\n{r.stdout}\n{r.stderr}\n")
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
     """Compile (if needed) and return the path of libswa.so."""
     nvcc = _nvcc()
@@ -94,27 +107,31 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
         if force or ptxas_info or _stale(obj, [src] + headers):
             cmd = [nvcc] + COMMON_FLAGS + (["-Xptxas", "-v"] if ptxas_info else []) + ["-c", src, "-o", obj]
             jobs.append((src, cmd))
-    short = TORCH_PATH + ".tmp"
+    short, short_job = TORCH_PATH + ".tmp", None
     command = _torch_command(nvcc, short)
     if command and (force or _stale(TORCH_PATH, [TORCH_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))):
-        jobs.insert(0, (TORCH_SRC, command))
+        short_job = TORCH_SRC, command
 
     def run(job):
         src, cmd = job
         if verbose:
             print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        try:
+            r = subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:  # no such compiler
+            r = subprocess.CompletedProcess(cmd, 127, "", str(e))
         return src, r
 
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            for src, r in ex.map(run, jobs):
-                if r.returncode != 0:
-                    raise RuntimeError(f"the compiler failed for {src}:\n{r.stdout}\n{r.stderr}")
-                if verbose or ptxas_info:
-                    sys.stdout.write(r.stdout + r.stderr)
-                if src == TORCH_SRC:
-                    os.replace(short, TORCH_PATH)
+    every = ([short_job] if short_job else []) + jobs
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(every), os.cpu_count() or 4))) as ex:
+        done = list(ex.map(run, every))
+    for src, r in done:
+        if src == TORCH_SRC:
+            _put_module(short, r)
+        elif r.returncode != 0:
+            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        if verbose or ptxas_info:
+            sys.stdout.write(r.stdout + r.stderr)
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + ".tmp"
         cmd = [nvcc] + ARCH_FLAGS + ["-shared", "-o", tmp] + objs
