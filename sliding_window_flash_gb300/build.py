@@ -15,6 +15,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -65,28 +66,54 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def built_for(torch_version: str) -> str:
+    """What the binding's module is compiled for: it reads torch's and Python's objects by their layouts."""
+    return f"torch {torch_version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _torch_version_file():
+    """torch/version.py of the torch that would be imported, or None."""
+    spec = importlib.util.find_spec("torch")
+    path = spec and os.path.join(spec.submodule_search_locations[0], "version.py")
+    return path if path and os.path.exists(path) else None
+
+
 def _torch_command(nvcc: str, out: str):
     """The compiler's command for the binding's module: torch is found, not imported.  None without torch."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
+    path = _torch_version_file()
+    if path is None:
         return None
-    torch = spec.submodule_search_locations[0]
+    with open(path) as f:
+        version = re.search(r"^__version__ = ['\"](.*)['\"]", f.read(), re.M)
+    torch = os.path.dirname(path)
     lib = os.path.join(torch, "lib")
     include = [INCLUDE, os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
                sysconfig.get_paths()["include"]]
     return [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
-            "-fvisibility=hidden", *["-I" + d for d in include], TORCH_SRC, "-o", out, "-L" + lib,
+            "-fvisibility=hidden", f'-DSWA_BUILT_FOR="{built_for(version.group(1) if version else "?")}"', *["-I" + d for d in include], TORCH_SRC, "-o", out, "-L" + lib,
             "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
+def _module_stale(command) -> bool:
+    """Whether the binding's module has to be compiled: its sources, or the torch that it was compiled for,
+    are newer, or the command that made it, which names torch's and Python's versions and paths, was another."""
+    deps = [TORCH_SRC, _torch_version_file()] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if _stale(TORCH_PATH, filter(None, deps)) or not os.path.exists(TORCH_PATH + ".stamp"):
+        return True
+    with open(TORCH_PATH + ".stamp") as f:
+        return f.read() != "\n".join(command)
 
 
 def _put_module(made: str, r) -> None:
     """The binding's module in its place; where the compiler failed, none, and why on stderr."""
     if r.returncode == 0:
         os.replace(made, TORCH_PATH)
+        with open(TORCH_PATH + ".stamp", "w") as f:
+            f.write("\n".join(r.args))
         return
-    for path in (made, TORCH_PATH):
+    for path in (made, TORCH_PATH, TORCH_PATH + ".stamp"):
         if os.path.exists(path):
             os.remove(path)
     sys.stderr.write(f"no {os.path.basename(TORCH_PATH)} (calls take some microseconds more on the host): the "
@@ -109,7 +136,7 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
             jobs.append((src, cmd))
     short, short_job = TORCH_PATH + ".tmp", None
     command = _torch_command(nvcc, short)
-    if command and (force or _stale(TORCH_PATH, [TORCH_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))):
+    if command and (force or _module_stale(command)):
         short_job = TORCH_SRC, command
 
     def run(job):

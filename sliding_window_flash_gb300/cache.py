@@ -97,10 +97,17 @@ class _Torch:
 
 def _short_way():
     """The calls of _swa_torch.so: each answers a call whose arguments are plainly in order, with what it
-    returns or the status of an error, and None for any other.  Without the module every call is another."""
+    returns or the status of an error, and None for any other.  Without the module every call is another, and
+    so with one that was compiled for another torch or Python: it would read their objects by old layouts."""
+    import torch
+
+    from .build import built_for
+
     try:
         from . import _swa_torch as m
 
+        if getattr(m, "built_for", None) != built_for(torch.__version__):
+            raise ImportError("_swa_torch.so was compiled for another torch or Python")
         m.use(*[ctypes.cast(_entry(name), _vp).value for name in (
             "swa_cache_attn", "swa_cache_attn_sinks", "swa_cache_attn_shared",
             "swa_cache_attn_shared_workspace_bytes", "swa_attn_fwd_sinks", "swa_attn_bwd_sinks",

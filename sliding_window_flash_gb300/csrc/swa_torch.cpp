@@ -394,4 +394,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_swa_torch", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__swa_torch() { return PyModule_Create(&module); }
+// `built_for` names the torch and the Python whose objects the module reads; the binding uses it with those
+// alone.
+PyMODINIT_FUNC PyInit__swa_torch() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", SWA_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
