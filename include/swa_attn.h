@@ -191,6 +191,8 @@ swa_status swa_attn_bwd_f32(const float* q, const float* k, const float* v, cons
  * A sink's dk and dv sum over every query behind it: the walk over the queries runs in parts, whose fp32
  * sums are added in a fixed order (bit-reproducible on one GPU).  The backward is launched as Delta, dK/dV
  * (D = 256: dK, dV), dQ, the joining of the sinks' rows; each may begin before the one ahead has ended.
+ * So dq, dk and dv of 16-bit tensors must overlap neither q, k, v, dO and lse nor one another: with sinks that
+ * the window hides from some query this is SWA_ERR_INVALID_ARG.
  * Other arguments, checks and errors as in the general and fp32 forms.
  */
 size_t swa_attn_sinks_workspace_bytes(int B, int Hq, int Hkv, int Lq, int Lk, int D, int window,

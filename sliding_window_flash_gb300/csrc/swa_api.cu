@@ -128,6 +128,26 @@ swa_status fwd_impl(int f16, const void* q, const void* k, const void* v, void* 
   return SWA_OK;
 }
 
+// With sinks dQ runs while dK/dV still reads the inputs, so a gradient written over one of them would race;
+// o is read by Delta alone, which is complete by then.
+bool gradients_apart(const swa::Problem& pb, const void* q, const void* k, const void* v, const void* dO,
+                     const float* lse, const void* dq, const void* dk, const void* dv) {
+  struct Range {
+    uintptr_t at;
+    size_t bytes;
+  };
+  const size_t rows = static_cast<size_t>(pb.B) * pb.Hq * pb.span.Lq, row = 2 * static_cast<size_t>(pb.D),
+               keys = static_cast<size_t>(pb.B) * pb.Hkv * pb.span.Lk;
+  auto range = [](const void* p, size_t bytes) { return Range{reinterpret_cast<uintptr_t>(p), bytes}; };
+  const Range r[] = {range(dq, rows * row), range(dk, keys * row), range(dv, keys * row),
+                     range(q, rows * row),  range(k, keys * row),  range(v, keys * row),
+                     range(dO, rows * row), range(lse, rows * sizeof(float))};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (r[i].at < r[j].at + r[j].bytes && r[j].at < r[i].at + r[i].bytes) return false;
+  return true;
+}
+
 swa_status bwd_impl(int f16, const void* q, const void* k, const void* v, const void* o,
                     const void* dO, const float* lse, void* dq, void* dk, void* dv, int B, int Hq,
                     int Hkv, int Lq, int Lk, int D, int window, int causal, float scale,
@@ -144,6 +164,7 @@ swa_status bwd_impl(int f16, const void* q, const void* k, const void* v, const 
   const void* ptrs[] = {q, k, v, o, dO, lse, dq, dk, dv, workspace};
   for (const void* p : ptrs)
     if (!aligned16(p)) return SWA_ERR_MISALIGNED;
+  if (pb.sinks > 0 && !gradients_apart(pb, q, k, v, dO, lse, dq, dk, dv)) return SWA_ERR_INVALID_ARG;
   if ((st = current_device(&pb.err)) != SWA_OK) return st;
   float* delta = static_cast<float*>(workspace);
   pb.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + delta_bytes);
