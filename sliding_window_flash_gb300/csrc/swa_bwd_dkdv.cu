@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(352, 1)
   using C = DkdvCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
-  if constexpr (kSinks) {  // Delta is there; dQ, which only reads what this kernel reads, may begin
+  if constexpr (kSinks) {  // Delta is there; dQ, which only reads what is there now, may begin
     wait_predecessor();
     launch_dependents();
   }

@@ -10,6 +10,9 @@
 #include "swa_attn.h"
 #include "swa_cache.h"
 #include "swa_kernels.h"
+#ifdef __CUDACC__
+#include "swa_ptx.cuh"
+#endif
 
 namespace swa {
 
@@ -46,10 +49,11 @@ __device__ __forceinline__ void raise_index_error(const CacheView& c) {
 }
 
 // Tokens cached before and new tokens of sequence b; false (and the error bit) when they do not fit
-// the table.
+// the table.  kL2: as load_global (swa_ptx.cuh).
+template <bool kL2 = false>
 __device__ __forceinline__ bool sequence_of(const CacheView& c, int b, int* len, int* n) {
-  const int l = c.lens[b];
-  const int m = c.new_lens ? c.new_lens[b] : c.T;
+  const int l = load_global<kL2>(c.lens + b);
+  const int m = c.new_lens ? load_global<kL2>(c.new_lens + b) : c.T;
   *len = l;
   *n = m;
   const bool ok = l >= 0 && m >= 0 && m <= c.T &&
@@ -60,9 +64,10 @@ __device__ __forceinline__ bool sequence_of(const CacheView& c, int b, int* len,
 
 // Page of block `i` of sequence b, or -1 (and the error bit) when the table names none; i must be
 // inside the table.
+template <bool kL2 = false>
 __device__ __forceinline__ int page_of(const CacheView& c, const int* table, int b, int i,
                                        int max_pages) {
-  const int p = table[static_cast<size_t>(b) * max_pages + i];
+  const int p = load_global<kL2>(table + static_cast<size_t>(b) * max_pages + i);
   if (p >= 0 && p < c.pages) return p;
   raise_index_error(c);
   return -1;

@@ -163,9 +163,9 @@ __device__ __forceinline__ unsigned seen_bits(int slot, int lo, int end, int sin
   return slot_bits(slot, lo, end) | slot_bits(slot, 0, min(sinks, end));
 }
 
-__device__ __forceinline__ uint4 load_codes(const uint4* p) {  // read once: not for the L1
+__device__ __forceinline__ uint4 load_codes(const uint4* p) {  // read once, and not from the L1 (load_global)
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
   using C = PrefixCfg<D>;
   constexpr int KT = C::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
-  launch_dependents();
+  launch_dependents();  // (the walk ahead waited for all that is read here before it let this kernel begin)
   if (!smem_base_ok(smem, c.err)) {
     wait_predecessor();
     return;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
     int len_min = INT_MAX, end_max = 0, q_max = 0, end_min = INT_MAX;
     for (int b = b0 + static_cast<int>(lane); b <= b1; b += 32) {
       int len, n;
-      const bool asks = sequence_of(c, b, &len, &n) && n > 0;
+      const bool asks = sequence_of<true>(c, b, &len, &n) && n > 0;
       // (a sequence of two tiles gets the same from both)
       s_seq[b] = asks ? make_int2(visible_lo(len, a.reach.window), min(len + n, a.reach.base)) : make_int2(0, 0);
       if (!asks) continue;
@@ -316,11 +316,11 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         float ks = 1.f, vs = 0.f;
         const unsigned seen = group < C::kGroups && slot < a.reach.base ? group_seen(j, slot) : 0u;
         if (seen != 0u) {
-          const int page = page_of(c, a.table, 0, slot >> a.page_log2, c.max_pages);
+          const int page = page_of<true>(c, a.table, 0, slot >> a.page_log2, c.max_pages);
           if (page >= 0) {
             plane = page * c.Hkv + h;
-            ks = c.k_scale[plane];
-            vs = c.v_scale[plane];
+            ks = load_global<true>(c.k_scale + plane);
+            vs = load_global<true>(c.v_scale + plane);
             atomicMax(&s_max[origin], __float_as_uint(vs));
           }
         }
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           const int b = static_cast<int>(a.div_r.div(static_cast<uint32_t>(rho)));
           const int in_seq = rho - b * a.R, t = static_cast<int>(a.div_t.mod(static_cast<uint32_t>(in_seq)));
           int len, n;
-          is = sequence_of(c, b, &len, &n) && t < n;
+          is = sequence_of<true>(c, b, &len, &n) && t < n;
           if (is) {
             seen = make_int2(visible_lo(len + t, a.reach.window), min(len + t, a.reach.base - 1));
             row += ((static_cast<size_t>(b) * c.Hkv + head) * a.R + in_seq) * D;
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         place[e] = sQ + sw128_offset(static_cast<uint32_t>(r), static_cast<uint32_t>(kq));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          raw[e][i] = is ? __ldg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
+          raw[e][i] = is ? __ldcg(reinterpret_cast<const uint4*>(row) + 4 * i + kq) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {

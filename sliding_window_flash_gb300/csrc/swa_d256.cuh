@@ -430,8 +430,8 @@ __device__ __forceinline__ void dq_compute(const Args& a, const Span& sp, uint32
     const int rn = fn.q0 + r;
     if (rn < sp.Lq) {
       const size_t gn = static_cast<size_t>(fn.bh) * sp.Lq + rn;
-      nxt_lse = a.lse[gn];
-      nxt_dlt = a.delta[gn];
+      nxt_lse = load_global<kSinks>(a.lse + gn);
+      nxt_dlt = load_global<kSinks>(a.delta + gn);
     } else {
       nxt_lse = SWA_POS_INF;
       nxt_dlt = 0.f;

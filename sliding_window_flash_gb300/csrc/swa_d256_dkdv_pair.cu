@@ -374,7 +374,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
     float nxt = 0.f;  // LSE of query q0(t) + r, fetched a tile ahead (h = 0 threads)
     auto fetch_row = [&](int t) {
       const int q = pw_q0(w, t) + r;
-      nxt = q < sp.Lq ? a.lse[static_cast<size_t>(pw_bhq(w, a, t)) * sp.Lq + q] : SWA_POS_INF;
+      nxt = q < sp.Lq ? load_global<kSinks>(a.lse + static_cast<size_t>(pw_bhq(w, a, t)) * sp.Lq + q)
+                      : SWA_POS_INF;
     };
     if (h == 0) fetch_row(0);
     bool ok = true;
@@ -467,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(352, 1)
   using C = KP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
-  if constexpr (kSinks) {  // Delta is there; dV and dQ, which only read what this kernel reads, may begin
+  if constexpr (kSinks) {  // Delta is there; dV and dQ, which only read what is there now, may begin
     wait_predecessor();
     launch_dependents();
   }

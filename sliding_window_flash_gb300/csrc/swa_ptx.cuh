@@ -652,6 +652,15 @@ __device__ __forceinline__ void launch_dependents() {
 __device__ __forceinline__ void wait_predecessor() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// Some kernels wait at their end instead (dQ and dV with sinks, the shared prefix): they read nothing that the
+// kernel ahead writes.  What they do read was complete when that kernel, after its own wait, let them begin,
+// so it is in the L2; but only a wait promises that no older copy is left in this SM's L1.  They read through
+// the L2 therefore: tiles by TMA, everything else with kL2 here and `.cg` loads.
+template <bool kL2, typename T>
+__device__ __forceinline__ T load_global(const T* p) {
+  if constexpr (kL2) return __ldcg(p);
+  return *p;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
