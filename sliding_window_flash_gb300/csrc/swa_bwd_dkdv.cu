@@ -59,6 +59,7 @@ struct DkdvCfg {
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;  // + TMEM address and abort flag
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(alone_on_sm(kSmemBytes), "its successor may begin before it holds tensor memory");
   static constexpr uint32_t kTmemCols = 512;
   // Once dP^T has been read, P^T and dS^T go over its columns: in each half-row's 64 columns,
   // P^T over the first 32 and dS^T over the last 32 (bf16 pairs).

@@ -66,6 +66,7 @@ struct DqPairCfg {
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;  // + TMEM address and abort flag
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(alone_on_sm(kSmemBytes), "its successor may begin before it holds tensor memory");
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 384;  // dP buffer b at kColDP + 128 b
   static constexpr int kThreads = 352;

@@ -129,6 +129,7 @@ struct F256 {
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 48;  // + TMEM address,
   // abort flag, producers' last fills
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(alone_on_sm(kSmemBytes), "its successor may begin before it holds tensor memory");
   static constexpr uint32_t kColS = 0, kColO = 256;
   static constexpr int kThreads = 384;
 };
@@ -358,6 +359,7 @@ struct Q256 {
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 48;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(alone_on_sm(kSmemBytes), "its successor may begin before it holds tensor memory");
   static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256;
   static constexpr int kThreads = 384;
 };

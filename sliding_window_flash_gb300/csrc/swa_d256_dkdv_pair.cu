@@ -206,6 +206,7 @@ struct VP {
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 48;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(alone_on_sm(kSmemBytes), "its successor may begin before it holds tensor memory");
   static constexpr uint32_t kColS = 0, kColAcc = 256;
   static constexpr int kThreads = 352;
 };
@@ -453,6 +454,7 @@ struct KP {
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 48;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(alone_on_sm(kSmemBytes), "its successor may begin before it holds tensor memory");
   static constexpr uint32_t kColS = 0, kColDP = 128, kColAcc = 256;
   static constexpr int kThreads = 352;
 };

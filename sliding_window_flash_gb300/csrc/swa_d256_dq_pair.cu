@@ -59,6 +59,7 @@ struct DqP256 {
   // + TMEM address, abort flag, and the producers' last fills ([2][kSlots] ints)
   static constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16 + 32;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(alone_on_sm(kSmemBytes), "its successor may begin before it holds tensor memory");
   static constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 256;
   static constexpr int kThreads = 384;
   static constexpr uint32_t kPairWarps = 16;

@@ -222,6 +222,12 @@ inline size_t sink_part_bytes(const Problem& pb) {
          sizeof(float);
 }
 
+// Whether two CTAs of this much dynamic shared memory never share an SM (228 KB, of which each takes 1 KB more).
+// dK/dV, dK, dV and dQ with sinks let the next of them begin before they hold their tensor memory.  All of it is
+// one CTA's, so two on an SM would wait for one another's, and pairs of CTAs that each hold one SM's half could
+// wait for ever.
+constexpr bool alone_on_sm(int smem) { return 2 * (smem + 1024) > 228 * 1024; }
+
 // Allows kernel `Kernel` its dynamic shared memory on the current device, once for each device.
 template <auto Kernel>
 cudaError_t allow_smem(int bytes) {
