@@ -115,15 +115,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Codes 0, 1 (low half) and 2, 3 (high half) of a word as two fp16 pairs.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -1216,22 +1207,6 @@ Plan plan_of(int B, int Hq, int Hkv, int T, int D, int max_pages, int page, int 
   return p;
 }
 
-// Launch that may begin while the kernel before it ends (it waits itself before it reads).
-template <typename... Args>
-cudaError_t launch_after(void (*kernel)(Args...), unsigned grid, cudaStream_t stream,
-                         typename std::common_type<Args>::type... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 Reach args_reach(const CacheAttnArgs& args) { return {args.window, args.sinks, args.base}; }
 
 template <int D, int kTiles>
@@ -1308,7 +1283,7 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
       const bool wide = rows * (D / kWide) >= 4ll * sm_count();
       const int64_t need = (rows * (D / (wide ? kWide : 16)) + 7) / 8;
       auto join = wide ? swa_cache_join_shared_kernel<D, kWide> : swa_cache_join_shared_kernel<D, 16>;
-      e = launch_after(join, static_cast<unsigned>(need < limit ? need : limit), stream, c, a, pd);
+      e = launch_early(join, static_cast<unsigned>(need < limit ? need : limit), 256, 0, stream, c, a, pd);
       if (e != cudaSuccess) return e;
       continue;
     }
@@ -1327,14 +1302,14 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
       join = swa_cache_join_part_kernel<D>;
       blocks = (runs + 7) / 8;
     }
-    e = launch_after(join, static_cast<unsigned>(blocks < most ? blocks : most), stream, c, a);
+    e = launch_early(join, static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream, c, a);
     if (e != cudaSuccess) return e;
     if (args.accumulate) {
       // At most this many chunks of 4 warps' turns; the kernel walks what there really is.
       const int64_t chunks = (static_cast<int64_t>(all.max_pages) * all.page / C::CK) * c.B * c.Hkv;
       const int64_t blocks = (chunks + 31) / 32;
       const unsigned wgrid = static_cast<unsigned>(blocks < most ? blocks : most);
-      if ((e = launch_after(swa_cache_weights_kernel<D>, wgrid, stream, c, a)) != cudaSuccess)
+      if ((e = launch_early(swa_cache_weights_kernel<D>, wgrid, 256, 0, stream, c, a)) != cudaSuccess)
         return e;
     }
   }

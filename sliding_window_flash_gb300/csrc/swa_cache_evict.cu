@@ -405,17 +405,11 @@ cudaError_t launch_cache_evict(const CacheView& c, const CacheEvictArgs& a, cuda
   // The move may be scheduled while the choice ends (it waits for it before it reads).
   const int pages = (a.budget + c.page - 1) / c.page;
   const int64_t tasks = heads * pages, most = 4ll * sm_count();
-  cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tasks < most ? tasks : most));
-  cfg.blockDim = dim3(kMoveThreads + kLookThreads);
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (c.D == 64) return cudaLaunchKernelEx(&cfg, swa_evict_move_kernel<64>, c, a, pages, tasks);
-  if (c.D == 128) return cudaLaunchKernelEx(&cfg, swa_evict_move_kernel<128>, c, a, pages, tasks);
-  return cudaLaunchKernelEx(&cfg, swa_evict_move_kernel<256>, c, a, pages, tasks);
+  auto move = c.D == 64    ? swa_evict_move_kernel<64>
+              : c.D == 128 ? swa_evict_move_kernel<128>
+                           : swa_evict_move_kernel<256>;
+  return launch_early(move, static_cast<unsigned>(tasks < most ? tasks : most), kMoveThreads + kLookThreads, 0, stream,
+                      c, a, pages, tasks);
 }
 
 }  // namespace swa

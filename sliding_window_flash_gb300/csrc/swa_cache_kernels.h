@@ -91,6 +91,15 @@ __device__ __forceinline__ uint32_t e4m3x4_times(uint32_t codes, uint32_t ratio)
       : "r"(codes), "r"(ratio));
   return r;
 }
+// Codes 0, 1 (low half) and 2, 3 (high half) of a word as two fp16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 __device__ __forceinline__ uint32_t half2_of(float x) {
   const __half2 h = __float2half2_rn(x);
   return *reinterpret_cast<const uint32_t*>(&h);

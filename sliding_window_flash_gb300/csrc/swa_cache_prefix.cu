@@ -107,15 +107,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       : "memory");
 }
 
-// Codes 0, 1 (low half) and 2, 3 (high half) of a word as two fp16 pairs.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\t"
-      "mov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -376,17 +367,18 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
       // Neighbouring 64-column pieces of a row go to the same banks: every other one is taken a row on.
       const int row0 = (tid / kUnitsRow) ^ ((cu >> 2) & 1);
       const uint32_t piece = static_cast<uint32_t>(cu >> 2) * C::kKVChunk, unit = 2u * (cu & 3);
-      auto fetch = [&](uint4 (&to)[kPasses], int i) {
+      uint4 codes[kPasses];
+      auto fetch = [&](int i) {
         const ChunkRec& rec = s_rec[i];
-  #pragma unroll
+#pragma unroll
         for (int g = 0; g < C::kGroups; ++g) {
           const int pl = rec.plane[g];
           const uint4* src = reinterpret_cast<const uint4*>(
                                  pool + (static_cast<size_t>(max(pl, 0)) * c.page +
                                          ((rec.slot + 32 * g) & (c.page - 1)) + row0) * D) + cu;
-  #pragma unroll
+#pragma unroll
           for (int p = 0; p < 32 / kRowsPass; ++p)
-            to[g * (32 / kRowsPass) + p] =
+            codes[g * (32 / kRowsPass) + p] =
                 pl >= 0 ? load_codes(src + p * kRowsPass * kUnitsRow) : make_uint4(0u, 0u, 0u, 0u);
         }
       };
@@ -398,16 +390,16 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         e4m3x4_to_f16(w.z, y[4], y[5]);
         e4m3x4_to_f16(w.w, y[6], y[7]);
         if constexpr (kValues) {
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = mul_f16x2(y[i], ratio);
         }
         const uint32_t to = tile + piece, ur = static_cast<uint32_t>(row);
         st_shared_v4(to + sw128_offset(ur, unit), y[0], y[1], y[2], y[3]);
         st_shared_v4(to + sw128_offset(ur, unit + 1), y[4], y[5], y[6], y[7]);
       };
-      // Chunk g, record i of its block, of `n`: its codes become the operand, and those of the next one are
-      // sent for.
-      auto step = [&](int g, int i, int n, uint4 (&codes)[kPasses]) -> bool {
+      // Record i of `n` of a block of chunks: its codes become the operand, and those of the next one are sent
+      // for.
+      auto step = [&](int i, int n) -> bool {
         const ChunkRec& rec = s_rec[i];
         const bool starts = rec.item != item;
         item = rec.item;
@@ -419,7 +411,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           for (int o = 0; o < C::kGroups; ++o) ratio[o] = half2_of(rec.vs[o] * inv);
           // what nobody sees must not meet a probability of zero as infinity or NaN
           if (rec.edge) {
-  #pragma unroll
+#pragma unroll
             for (int p = 0; p < kPasses; ++p)
               if ((rec.seen[p * kRowsPass / 32] >> (row0 + p * kRowsPass % 32) & 1u) == 0u)
                 codes[p] = make_uint4(0u, 0u, 0u, 0u);
@@ -429,7 +421,7 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
         constexpr int kFull = kValues ? C::kVFull : C::kKFull, kEmpty = kValues ? C::kVEmpty : C::kKEmpty;
         if (!warp_wait(bar(kEmpty + stage), phase, &abort_flag, c.err)) return false;
         const uint32_t tile = (kValues ? sV0 : sK0) + static_cast<uint32_t>(stage) * C::kKVBytes;
-  #pragma unroll
+#pragma unroll
         for (int p = 0; p < kPasses; ++p)
           put(tile, row0 + p * kRowsPass, codes[p], ratio[p * kRowsPass / 32]);
         fence_proxy_async_smem();
@@ -439,20 +431,15 @@ __global__ void __launch_bounds__(PrefixCfg<D>::kThreads, 1)
           stage = 0;
           phase ^= 1u;
         }
-        if (i + 1 < n) fetch(codes, i + 1);
+        if (i + 1 < n) fetch(i + 1);
         return true;
       };
       bool ok = true;
       for (int i0 = 0; i0 < count; i0 += C::kBlock) {
         if (i0 > 0) look_up(i0);
         const int n = min(C::kBlock, count - i0);
-        uint4 even[kPasses];
-        if (ok) {
-          fetch(even, 0);
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          ok = step(i0 + i, i, n, even);
-        }
+        if (ok) fetch(0);
+        for (int i = 0; ok && i < n; ++i) ok = step(i, n);
       }
     };
     const bool values = warp >= C::kValueWarp;
@@ -842,17 +829,8 @@ cudaError_t launch_prefix_d(const CacheView& c, const PrefixDev& a, cudaStream_t
   using C = PrefixCfg<D>;
   cudaError_t e = allow_smem<swa_cache_prefix_kernel<D>>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.parts));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, swa_cache_prefix_kernel<D>, c, a);
+  return launch_early(swa_cache_prefix_kernel<D>, static_cast<unsigned>(a.parts), C::kThreads, C::kSmemBytes,
+                      stream, c, a);
 }
 
 }  // namespace

@@ -585,17 +585,8 @@ cudaError_t launch_d(const Problem& pb, int keys, const void* q, const void* k, 
   if ((e = cudaGetLastError()) != cudaSuccess || pieces == 1) return e;
   const int64_t n = static_cast<int64_t>(a.BHK) * keys;
   const int64_t blocks = (n + 255) / 256;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < sms * 8 ? blocks : sms * 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, swa_key_weights_join_kernel, static_cast<const float*>(workspace),
-                            w, n, pieces, keys, pb.span.Lk);
+  return launch_early(swa_key_weights_join_kernel, static_cast<unsigned>(blocks < sms * 8 ? blocks : sms * 8), 256, 0,
+                      stream, static_cast<const float*>(workspace), w, n, pieces, keys, pb.span.Lk);
 }
 
 cudaError_t launch_keys(const Problem& pb, int keys, const void* q, const void* k, const float* lse,
