@@ -172,7 +172,10 @@ swa_status swa_cache_attn_shared(const swa_cache* cache, const int* table, int m
  * like every slot of a skipped page of dst_table.
  * A destination block's scale is the largest of its tokens' old scales; slots behind the last
  * survivor are left as they were.  Window rules count cached tokens, so under a window evicted
- * tokens no longer count.  Needs cache->weight.
+ * tokens no longer count.  So do sinks: in later calls the first `sinks` slots are whichever tokens
+ * survived first, and a sink that was light in one head is gone there.  Who has sinks sets their weights
+ * to infinity before: with sinks <= budget - recent they then stay, first in every head, and so do their
+ * weights.  Needs cache->weight.
  */
 swa_status swa_cache_evict(const swa_cache* cache, const int* table, int max_pages,
                            const int* lens, const int* dst_table, int dst_pages, int budget,

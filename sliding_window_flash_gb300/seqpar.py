@@ -14,7 +14,8 @@ The exchange plan is a pure function of (rank, world, L, W), so every rank deriv
 matching sends and receives.  Transfers go through batch_isend_irecv (16-bit tensors as raw int16
 words); NCCL on GPUs, gloo on the CPU.  Halo gradients are added in fp32 (or wider) and rounded
 once.  Only causal windows shard this way (a two-sided window would put the queries in the middle
-of the keys, which the kernels' bottom-right alignment does not express).
+of the keys, which the kernels' bottom-right alignment does not express), and without sinks: the
+sequence's first keys reach the ranks of the first window alone.
 
 The compute functions default to the library's kernels (swa_attn_fwd / swa_attn_bwd); `fwd_fn` /
 `bwd_fn` replace them, which is how the CPU tests drive this exchange logic with a reference.
