@@ -1276,8 +1276,10 @@ cudaError_t launch_d(const CacheView& all, const CacheAttnArgs& args, const Plan
       pd.rows = c.B * p.R;
       pd.tiles = (pd.rows + kPrefixRows - 1) / kPrefixRows;
       if ((e = launch_cache_prefix(c, pd, stream)) != cudaSuccess) return e;
-      // A warp 64 columns of a row where that fills the SMs, else 16.  (12 sequences, 5 tokens, 32 / 16 heads,
-      // D = 256, the call: 74.1 us, with 128 columns 76.5, 32 76.8; 64 sequences, 32 / 8, D = 128: 83.3, 83.5, 84.9.)
+      // A warp 64 columns of a row where that fills the SMs, else 16.  (us of the call, with 128 / 64 / 32 / 16
+      // columns.  D = 128, 32 / 8 heads: 64 sequences, a prefix of 32,768 84.7 / 83.4 / 87.1 / 92.4; 128 of 8 tokens,
+      // 2,048 133 / 150 / 191 / 273.  D = 256, 32 / 16: 12 of 5 tokens, 4,096 76.4 / 77.6 / 84.3 / 94.7; 64, 16,384
+      // 149 / 152 / 160 / 169.  D = 64, 32 / 8: 32, 8,192 - / 33.7 / 33.0 / 32.5.  2 and 8 sequences: the same.)
       const int64_t rows = static_cast<int64_t>(c.B) * c.Hkv * p.R, limit = 8ll * sm_count();
       constexpr int kWide = 64;
       const bool wide = rows * (D / kWide) >= 4ll * sm_count();

@@ -26,10 +26,10 @@
 // loop), its two products 1,024 and its operands less than that beside them; without the products or the
 // conversions the kernel takes the same time within 8 %.  A part's beginning and end, run once, take 13 us
 // of instructions to fetch and waits one behind the other.  64 sequences, 32 / 8 heads, D = 128, a prefix of
-// 32,768: 50 us alone (34 GFLOP, 67 MB); 12 sequences, 5 tokens, 32 / 16 heads, D = 256, a prefix of 4,096: 31.
-// It begins while the walk over the sequences' own slots ends, and the join while it ends: 82 and 70 us in
-// all.  The first item's rows come while its chunks are looked up (the smallest calls 14.9 us in place of 15.9,
-// large ones the same).  Tried: operands fetched register by register while they are converted (90 us), more
+// 32,768: 48-51 us alone (34 GFLOP, 67 MB); 12 sequences, 5 tokens, 32 / 16 heads, D = 256, a prefix of 4,096: 28.
+// It begins while the walk over the sequences' own slots ends, and the join while it ends: 79-80 and 71 us in
+// all.  The first item's rows come while its chunks are looked up (1 us of the smallest calls' 15 to 17, large
+// ones the same).  Tried: operands fetched register by register while they are converted (90 us), more
 // than 16 warps (96 registers each, which spill), masks in the passes instead of in TMEM (spilled), the next
 // chunk's first scores read while the warp judges this one's (a few spills; 87 us).
 #include <climits>

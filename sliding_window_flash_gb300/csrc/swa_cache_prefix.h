@@ -36,8 +36,12 @@ struct PrefixPlan {
 // Keys of a chunk: the tensor core's operands and two stages of them fill shared memory.
 SWA_HD int prefix_chunk(int D) { return D == 256 ? 64 : 128; }
 // Parts that the list is cut into: by used_parts' rule, whose partial results cost half here, since they are
-// still in the L2 when they are read (12 sequences, 5 tokens, D = 256, a prefix of 4,096: 2 us of 73 less than by the rule as
-// it is, which leaves a quarter of the SMs without a part).
+// still in the L2 when they are read.  Against the rule as it is, with fewer and longer parts, this wins as often
+// as it loses (us of the call, half / whole; sequences, tokens, kv heads, prefix).  D = 256: 12, 5, 16, 4,096 with a
+// window 70.7 / 72.7; 12, 5, 16, 2,048 45.3 / 51.2; 64, 1, 8, 4,096 60.5 / 69.4; 30, 1, 4, 2,048 33.5 / 39.0; but 64,
+// 1, 16, 4,096 125 / 108.  D = 128: 64, 1, 8, 2,048 43.1 / 44.8, but 4,096 52.2 / 43.2, and 64, 1, 4, 8,192 39.2 /
+// 35.4; 2, 1, 8, 32,768 43.4 / 43.9.  D = 64: 64, 1, 8, 2,048 35.5 / 32.8.  Within 2 % elsewhere (8 to 64 sequences,
+// prefixes of 1,024 to 32,768).
 SWA_HD int prefix_parts(int64_t total, int parts, int stored, int D) {
   return used_parts(total, parts, stored * D / 2);
 }
