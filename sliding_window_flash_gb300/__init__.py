@@ -377,7 +377,8 @@ def swa_attn_bwd(q, k, v, o, do, lse, window: int, scale: Optional[float] = None
     ``fused=True`` runs swa_attn_bwd_fused (one kernel for dK, dV and dQ; workspace of
     swa_attn_bwd_fused_workspace_bytes; dQ's fp32 additions run in a varying order).  fp32 tensors
     and calls with sinks (workspace of swa_attn_sinks_workspace_bytes) always take the split path;
-    fused=True with sinks is refused."""
+    fused=True with sinks is refused, and so are 16-bit dq, dk and dv that lie over q, k, v, do, lse or one
+    another."""
     if sinks:
         if fused:
             raise ValueError("the fused backward has no sinks")
