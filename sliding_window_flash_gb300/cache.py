@@ -85,14 +85,20 @@ class _Torch:
     Tensors are made by empty: between two launches it takes 2.7 us on a Grace core, new_empty 4.1."""
 
     def __getattr__(self, name):
+        if name in _SHORT:  # these need the library, the others do not
+            self.__dict__[name] = _short_way()[name]
+            return self.__dict__[name]
         import torch
 
         self.__dict__.update(
             f8=torch.float8_e4m3fn, f32=torch.float32, i32=torch.int32, u8=torch.uint8,
             kinds={torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}, Tensor=torch.Tensor,
             empty=torch.empty, empty_like=torch.empty_like, stream=torch._C._cuda_getCurrentRawStream,
-            current_device=torch._C._cuda_getDevice, **_short_way())
+            current_device=torch._C._cuda_getDevice)
         return self.__dict__[name]
+
+
+_SHORT = ("pool", "attn", "fwd", "bwd")
 
 
 def _short_way():
@@ -101,6 +107,7 @@ def _short_way():
     so with one that was compiled for another torch or Python: it would read their objects by old layouts."""
     import torch
 
+    from . import library_path
     from .build import built_for
 
     try:
@@ -108,13 +115,14 @@ def _short_way():
 
         if getattr(m, "built_for", None) != built_for(torch.__version__):
             raise ImportError("_swa_torch.so was compiled for another torch or Python")
-        m.use(*[ctypes.cast(_entry(name), _vp).value for name in (
+        lib = ctypes.CDLL(library_path())
+        m.use(*[ctypes.cast(getattr(lib, name), _vp).value for name in (
             "swa_cache_attn", "swa_cache_attn_sinks", "swa_cache_attn_shared",
             "swa_cache_attn_shared_workspace_bytes", "swa_attn_fwd_sinks", "swa_attn_bwd_sinks",
             "swa_attn_sinks_workspace_bytes")])
         return {"pool": m.pool, "attn": m.cache_attn, "fwd": m.fwd, "bwd": m.bwd}
-    except ImportError:
-        return dict.fromkeys(("pool", "attn", "fwd", "bwd"), lambda *_: None)
+    except (ImportError, OSError):  # no module, or no library: what is missing is said by the Python way
+        return dict.fromkeys(_SHORT, lambda *_: None)
 
 
 def _raise(rc, name):

@@ -80,6 +80,7 @@ def test_the_command_names_torch_and_python(monkeypatch, tmp_path):
 
 
 def test_a_module_for_another_torch_is_not_used(monkeypatch):
+    build.build()
     used = []
     fake = types.SimpleNamespace(use=lambda *at: used.append(at), pool=1, cache_attn=2, fwd=3, bwd=4)
     monkeypatch.setattr(swa, "_swa_torch", fake, raising=False)
@@ -92,8 +93,24 @@ def test_a_module_for_another_torch_is_not_used(monkeypatch):
     assert cache._short_way() == {"pool": 1, "attn": 2, "fwd": 3, "bwd": 4} and len(used) == 1
 
 
+def test_the_short_way_asks_nobody_else(monkeypatch, tmp_path):
+    """Torch's names need no library, and the library that is used is the one in its place, whatever stands for
+    it elsewhere."""
+    def other(*_):
+        raise RuntimeError("another library")
+
+    build.build()
+    monkeypatch.setattr(cache, "_entry", other)
+    monkeypatch.setattr(swa, "load", other)
+    names = cache._Torch()
+    assert names.f32 is torch.float32 and names.empty is torch.empty and "fwd" not in names.__dict__
+    assert names.fwd is swa._swa_torch.fwd
+    monkeypatch.setattr(swa, "library_path", lambda: str(tmp_path / "libswa.so"))
+    assert cache._Torch().fwd(1, 2, 3) is None
+
+
 def test_the_module_that_is_built_is_used():
     build.build()
-    cache._t.f32
+    fwd = cache._t.fwd
     assert swa._swa_torch.built_for == build.built_for(torch.__version__)
-    assert cache._t.fwd is swa._swa_torch.fwd
+    assert fwd is swa._swa_torch.fwd
